@@ -48,7 +48,8 @@ typedef enum {
     KDA_OK = 0,
     KDA_ERR_NULL_ARG = -1,          /* a required pointer is NULL */
     KDA_ERR_BAD_SHAPE = -2,         /* B, T, H, N inconsistent or out of range */
-    KDA_ERR_UNSUPPORTED_DIM = -3,   /* K or V is not 128 */
+    KDA_ERR_UNSUPPORTED_DIM = -3,   /* K or V is not 128 (or another size the entry point
+                                       does not take: see there) */
     KDA_ERR_MISALIGNED = -4,        /* a pointer breaks the alignment rule below */
     KDA_ERR_BAD_CU_SEQLENS = -5,    /* (device) cu_seqlens not 0..T nondecreasing */
     KDA_ERR_CUDA = -6,              /* a CUDA runtime call failed */
@@ -61,7 +62,8 @@ typedef enum {
     KDA_ERR_NOT_DEVICE_MEMORY = -13, /* a pointer is not CUDA device (or managed) memory */
     KDA_ERR_SCRATCH_LIMIT = -14,    /* kda_chunk_prefill_noalloc: the call needs more scratch
                                        than its fixed 64 MiB array holds */
-    KDA_ERR_BAD_FLAGS = -15         /* a preprocessing flag bit this library does not know */
+    KDA_ERR_BAD_FLAGS = -15,        /* a flag bit the entry point does not know */
+    KDA_ERR_BAD_PAGE_TABLE = -16    /* (device) a sequence length or page index out of range */
 } kda_status;
 
 /*
@@ -252,6 +254,183 @@ KDA_API kda_status kda_chunk_prefill_backward(const void *q, const void *k, cons
                                               const float *d_final_state, float *dq, float *dk,
                                               float *dv, float *dg, float *dbeta,
                                               float *d_initial_state, void *stream);
+
+/*
+ * kda_short_conv -- short causal convolution, one filter per channel, over a
+ * batch of sequences: what stands in front of q, k and v of a KDA layer (and
+ * of x, B and C of a state space layer). For token t of a sequence
+ *
+ *     z[t, d] = bias[d] + sum_{j < W} weight[d, j] * x[t - (W - 1) + j, d]
+ *     out     = z, or z / (1 + exp(-z)) with KDA_CONV_SILU
+ *
+ * where rows before the sequence's first token come from its history (zeros
+ * without initial_state). Sums in fp32, out rounded once to bf16.
+ *
+ *   x            device, bf16 [B*T, D], rows x_stride elements apart (so x may
+ *                be a slice of a fused projection)
+ *   weight       device, fp32 [D, W]; W = 2, 3 or 4 (others: KDA_ERR_UNSUPPORTED_DIM)
+ *   bias         device, fp32 [D] or NULL
+ *   initial_state device, bf16 [N, W-1, D] or NULL: the W-1 rows before each
+ *                sequence, the newest last
+ *   cu_seqlens, B, T, N  as for kda_chunk_prefill (contents checked on the
+ *                device: a violation makes the kernels skip all work and
+ *                kda_last_device_error() report KDA_ERR_BAD_CU_SEQLENS)
+ *   out          device, bf16 [B*T, D], rows out_stride elements apart
+ *   final_state  device, bf16 [N, W-1, D] or NULL: the last W-1 rows of
+ *                (history, sequence); not initial_state itself
+ *   D >= 1; x_stride, out_stride >= D; B*T*max(strides) < 2^40.
+ *
+ * Any D, strides and alignment to the element are taken; rows that start on
+ * 16-byte boundaries (8-byte ones next) with D a multiple of 8 (4) run
+ * fastest. No workspace.
+ */
+enum { KDA_CONV_SILU = 1, KDA_CONV_DOUT_FP32 = 2 };
+
+KDA_API kda_status kda_short_conv(const void *x, const float *weight, const float *bias,
+                                  const void *initial_state, const int32_t *cu_seqlens,
+                                  int64_t B, int64_t T, int64_t D, int64_t W, int64_t N,
+                                  int64_t x_stride, int flags, void *out, int64_t out_stride,
+                                  void *final_state, void *stream);
+
+/*
+ * kda_short_conv_step -- one new token for each of N sequences: the
+ * convolution at T = 1, the history shifted by one row.
+ *   x, out       bf16 [N, D], rows x_stride / out_stride elements apart
+ *   state_in     bf16 [N, W-1, D] or NULL (zeros)
+ *   state_out    bf16 [N, W-1, D], written; may be state_in itself, but may not
+ *                overlap it otherwise
+ * weight, bias, D, W, flags (KDA_CONV_SILU) as for kda_short_conv. N = 0 is a
+ * no-op.
+ */
+KDA_API kda_status kda_short_conv_step(const void *x, const float *weight, const float *bias,
+                                       const void *state_in, int64_t N, int64_t D, int64_t W,
+                                       int64_t x_stride, int flags, void *out,
+                                       int64_t out_stride, void *state_out, void *stream);
+
+/*
+ * kda_short_conv_backward -- gradients of kda_short_conv for a loss L with
+ * dL/d(out) = d_out and dL/d(final_state) = d_final_state:
+ *
+ *   dz = d_out, times s (1 + z (1 - s)) with s = 1 / (1 + exp(-z)) under KDA_CONV_SILU
+ *   dx[t, d]      = sum_j weight[d, j] dz[t + (W - 1) - j, d]   (within the sequence)
+ *   dweight[d, j] = sum_t dz[t, d] x[t - (W - 1) + j, d],   dbias[d] = sum_t dz[t, d]
+ *
+ * z is computed again from x. Rows of the history get d_initial_state by the
+ * same sum; d_final_state is added to the rows that final_state holds.
+ *   d_out        device [B*T, D], rows dout_stride elements apart: bf16, or fp32
+ *                with KDA_CONV_DOUT_FP32 (the gradients of
+ *                kda_chunk_prefill_backward are fp32)
+ *   d_final_state fp32 [N, W-1, D] or NULL (zeros)
+ *   dx           bf16 [B*T, D], rows dx_stride elements apart
+ *   dweight      fp32 [D, W]; dbias fp32 [D] or NULL
+ *   d_initial_state fp32 [N, W-1, D] or NULL (not written)
+ * The sums over tokens are taken in fp32 in a fixed order (the same call gives
+ * the same bits). Workspace (the stream's, as for the prefill): (W + 1) * D
+ * floats for every 256 tokens (every fewer when the call is small).
+ */
+KDA_API kda_status kda_short_conv_backward(const void *x, const float *weight, const float *bias,
+                                           const void *initial_state, const int32_t *cu_seqlens,
+                                           int64_t B, int64_t T, int64_t D, int64_t W, int64_t N,
+                                           int64_t x_stride, int flags, const void *d_out,
+                                           int64_t dout_stride, const float *d_final_state,
+                                           void *dx, int64_t dx_stride, float *dweight,
+                                           float *dbias, float *d_initial_state, void *stream);
+
+/*
+ * kda_ssm_prefill -- selective state space scan with one decay per head over a
+ * batch of sequences. With S an n x P fp32 matrix per (sequence, head) and
+ * delta = dt, or softplus(dt + dt_bias) under KDA_SSM_DT_SOFTPLUS:
+ *
+ *     S_t = exp(a delta_t) S_{t-1} + delta_t b_t x_t^T
+ *     y_t = S_t^T c_t + d x_t
+ *
+ *   x            device, bf16 [B*T, H, P], tokens x_stride elements apart
+ *   dt           device, fp32 [B*T, H], tokens dt_stride elements apart
+ *   a            device, fp32 [H]; a * delta is the log decay of a token and is
+ *                expected to be <= 0 (a positive one is computed too, as long as
+ *                the growth over any 64 tokens stays within fp32)
+ *   b, c         device, bf16 [B*T, G, n], tokens b_stride / c_stride elements
+ *                apart; head h uses group h / (H / G), H a multiple of G
+ *   d            device, fp32 [H] or NULL (0)
+ *   dt_bias      device, fp32 [H] or NULL (0); added whether or not softplus is taken
+ *   initial_state device, fp32 [N, H, n, P] or NULL (zeros)
+ *   cu_seqlens, B, T, N  as for kda_chunk_prefill
+ *   out          device, bf16 [B*T, H, P] (contiguous)
+ *   final_state  device, fp32 [N, H, n, P] or NULL (not written); may equal
+ *                initial_state
+ *   P = 64 or 128, n = 64 or 128 (others: KDA_ERR_UNSUPPORTED_DIM).
+ *
+ * Alignment: x, b, c, out and the states 16 bytes, and x_stride, b_stride,
+ * c_stride multiples of 8 elements; fp32 vectors and cu_seqlens 4 bytes.
+ * States, decays and sums are held in fp32. Workspace: the
+ * chunk offsets of a packed batch and the states at the cuts of a split
+ * sequence.
+ */
+enum { KDA_SSM_DT_SOFTPLUS = 1 };
+
+KDA_API kda_status kda_ssm_prefill(const void *x, const float *dt, const float *a, const void *b,
+                                   const void *c, const float *d, const float *dt_bias,
+                                   const float *initial_state, const int32_t *cu_seqlens,
+                                   int64_t B, int64_t T, int64_t H, int64_t P, int64_t G,
+                                   int64_t n, int64_t N, int64_t x_stride, int64_t dt_stride,
+                                   int64_t b_stride, int64_t c_stride, int flags, void *out,
+                                   float *final_state, void *stream);
+
+/*
+ * kda_ssm_step -- one new token for each of N sequences: the recurrence of
+ * kda_ssm_prefill applied once per (sequence, head).
+ *   x, dt, b, c, out  as there with one row per sequence
+ *   state_in     fp32 [N, H, n, P] or NULL (zeros)
+ *   state_out    fp32 [N, H, n, P], written; may be state_in itself (in place) but
+ *                may not overlap it otherwise
+ * Allocates nothing and uses no workspace; N = 0 is a no-op.
+ */
+KDA_API kda_status kda_ssm_step(const void *x, const float *dt, const float *a, const void *b,
+                                const void *c, const float *d, const float *dt_bias,
+                                const float *state_in, int64_t N, int64_t H, int64_t P, int64_t G,
+                                int64_t n, int64_t x_stride, int64_t dt_stride, int64_t b_stride,
+                                int64_t c_stride, int flags, void *out, float *state_out,
+                                void *stream);
+
+/*
+ * kda_paged_decode -- attention of one new token per sequence over a paged
+ * key-value cache (the full-attention layers of a hybrid model). For sequence
+ * s, query head h and its key-value head h / (Hq / Hkv), over the cached
+ * tokens j < seq_lens[s]:
+ *
+ *     out = sum_j softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
+ *
+ *   q            device, bf16 [B, Hq, D]
+ *   k_cache, v_cache device, bf16 [pages, page_size, Hkv, D], pages k_page_stride
+ *                / v_page_stride elements apart (both may be views of one cache);
+ *                inside a page the layout is contiguous
+ *   page_table   device, int32 [B, max_pages]: token j of sequence s lies in
+ *                page page_table[s, j / page_size], row j % page_size. Entries
+ *                past a sequence's last page are not read
+ *   seq_lens     device, int32 [B], the new token's own key and value included;
+ *                0 gives out = 0 and lse = -inf
+ *   out          device, bf16 [B, Hq, D]
+ *   lse          device, fp32 [B, Hq] or NULL (natural logarithm)
+ *   D = 64 or 128 (others: KDA_ERR_UNSUPPORTED_DIM); Hq a multiple of Hkv;
+ *   page_size >= 1; B <= 65536; max_pages * page_size < 2^31.
+ *
+ * A length that is negative or beyond max_pages * page_size, or a page index
+ * outside [0, pages), is reported by kda_last_device_error() as
+ * KDA_ERR_BAD_PAGE_TABLE; such a length is taken as 0 and such a page as page 0
+ * (nothing out of range is read), so the outputs of that sequence are then
+ * meaningless and those of the others are right.
+ *
+ * Alignment: q, k_cache, v_cache, out 16 bytes, page strides multiples of 8
+ * elements; int32 and fp32 arrays 4 bytes. Scores, softmax and sums in fp32;
+ * the sum over the cache is split over the SMs and joined in a fixed order (the
+ * same call gives the same bits). Workspace: partial sums of the split.
+ */
+KDA_API kda_status kda_paged_decode(const void *q, const void *k_cache, const void *v_cache,
+                                    const int32_t *page_table, const int32_t *seq_lens,
+                                    int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t pages,
+                                    int64_t page_size, int64_t max_pages, int64_t k_page_stride,
+                                    int64_t v_page_stride, float scale, void *out, float *lse,
+                                    void *stream);
 
 /* Static text for a status code (never NULL). */
 KDA_API const char *kda_status_string(kda_status status);

@@ -5,8 +5,11 @@ include/kda.h (libkda_gb300.so, built in-tree by ``build.build()``); this
 package is its thin Python binding.
 """
 from ._binding import (  # noqa: F401
+    CONV_DOUT_FP32,
+    CONV_SILU,
     PRE_GATE_LOGITS,
     PRE_NORM_QK,
+    SSM_DT_SOFTPLUS,
     STATUS,
     STATUS_CODE,
     KdaError,
@@ -23,8 +26,14 @@ from ._binding import (  # noqa: F401
     kda_chunk_prefill_noalloc,
     kda_last_device_error,
     kda_set_backward_impl,
+    kda_paged_decode,
     kda_set_recurrent_impl,
     kda_set_scan_segments,
+    kda_short_conv,
+    kda_short_conv_backward,
+    kda_short_conv_step,
+    kda_ssm_prefill,
+    kda_ssm_step,
     kda_test_stall_recurrent,
     kda_stage_timing_begin,
     kda_stage_timing_end,
@@ -32,6 +41,12 @@ from ._binding import (  # noqa: F401
     kda_workspace_bytes,
     kda_workspace_release,
     lib,
+    paged_decode,
+    short_conv,
+    short_conv_backward,
+    short_conv_step,
+    ssm_prefill,
+    ssm_step,
 )
 
 __version__ = "0.3.0"

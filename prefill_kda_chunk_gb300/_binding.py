@@ -21,10 +21,15 @@ STATUS = {
     -7: "KDA_ERR_DEVICE_TIMEOUT", -8: "KDA_ERR_NO_DEVICE_SUPPORT", -9: "KDA_ERR_ALIAS",
     -10: "KDA_ERR_GATE_RANGE", -11: "KDA_ERR_CAPTURE", -12: "KDA_ERR_WRONG_DEVICE",
     -13: "KDA_ERR_NOT_DEVICE_MEMORY", -14: "KDA_ERR_SCRATCH_LIMIT", -15: "KDA_ERR_BAD_FLAGS",
+    -16: "KDA_ERR_BAD_PAGE_TABLE",
 }
 # input preprocessing flags (include/kda.h)
 PRE_NORM_QK = 1
 PRE_GATE_LOGITS = 2
+# flags of the short convolution and of the state space scan
+CONV_SILU = 1
+CONV_DOUT_FP32 = 2
+SSM_DT_SOFTPLUS = 1
 STATUS_CODE = {v: k for k, v in STATUS.items()}
 
 _lib = None
@@ -61,6 +66,19 @@ def lib() -> ctypes.CDLL:
             L.kda_backward_workspace_bytes.argtypes = [i64] * 4 + [ctypes.c_int]
             L.kda_chunk_prefill_backward.restype = ctypes.c_int
             L.kda_chunk_prefill_backward.argtypes = [vp] * 7 + [i64] * 6 + [f32] + [vp] * 9
+            L.kda_short_conv.restype = ctypes.c_int
+            L.kda_short_conv.argtypes = [vp] * 5 + [i64] * 6 + [ctypes.c_int, vp, i64, vp, vp]
+            L.kda_short_conv_step.restype = ctypes.c_int
+            L.kda_short_conv_step.argtypes = [vp] * 4 + [i64] * 4 + [ctypes.c_int, vp, i64, vp, vp]
+            L.kda_short_conv_backward.restype = ctypes.c_int
+            L.kda_short_conv_backward.argtypes = ([vp] * 5 + [i64] * 6 + [ctypes.c_int, vp, i64, vp,
+                                                  vp, i64] + [vp] * 4)
+            L.kda_ssm_prefill.restype = ctypes.c_int
+            L.kda_ssm_prefill.argtypes = [vp] * 9 + [i64] * 11 + [ctypes.c_int, vp, vp, vp]
+            L.kda_ssm_step.restype = ctypes.c_int
+            L.kda_ssm_step.argtypes = [vp] * 8 + [i64] * 9 + [ctypes.c_int, vp, vp, vp]
+            L.kda_paged_decode.restype = ctypes.c_int
+            L.kda_paged_decode.argtypes = [vp] * 5 + [i64] * 9 + [f32, vp, vp, vp]
             L.kda_status_string.restype = ctypes.c_char_p
             L.kda_status_string.argtypes = [ctypes.c_int]
             L.kda_last_device_error.restype = ctypes.c_int
@@ -132,6 +150,53 @@ def kda_chunk_prefill_backward(q, k, v, g, beta, initial_state, cu_seqlens, B, T
     return lib().kda_chunk_prefill_backward(q, k, v, g, beta, initial_state, cu_seqlens, B, T, H,
                                             K, V, N, scale, d_out, d_final_state, dq, dk, dv, dg,
                                             dbeta, d_initial_state, stream)
+
+
+def kda_short_conv(x, weight, bias, initial_state, cu_seqlens, B, T, D, W, N, x_stride, flags,
+                   out, out_stride, final_state, stream) -> int:
+    """The short-convolution C entry point, pointers as ints (0 = NULL)."""
+    return lib().kda_short_conv(x, weight, bias, initial_state, cu_seqlens, B, T, D, W, N,
+                                x_stride, flags, out, out_stride, final_state, stream)
+
+
+def kda_short_conv_step(x, weight, bias, state_in, N, D, W, x_stride, flags, out, out_stride,
+                        state_out, stream) -> int:
+    """The single-token convolution C entry point, pointers as ints (0 = NULL)."""
+    return lib().kda_short_conv_step(x, weight, bias, state_in, N, D, W, x_stride, flags, out,
+                                     out_stride, state_out, stream)
+
+
+def kda_short_conv_backward(x, weight, bias, initial_state, cu_seqlens, B, T, D, W, N, x_stride,
+                            flags, d_out, dout_stride, d_final_state, dx, dx_stride, dweight,
+                            dbias, d_initial_state, stream) -> int:
+    """The convolution's gradient C entry point, pointers as ints (0 = NULL)."""
+    return lib().kda_short_conv_backward(x, weight, bias, initial_state, cu_seqlens, B, T, D, W,
+                                         N, x_stride, flags, d_out, dout_stride, d_final_state,
+                                         dx, dx_stride, dweight, dbias, d_initial_state, stream)
+
+
+def kda_ssm_prefill(x, dt, a, b, c, d, dt_bias, initial_state, cu_seqlens, B, T, H, P, G, n, N,
+                    x_stride, dt_stride, b_stride, c_stride, flags, out, final_state,
+                    stream) -> int:
+    """The state space scan C entry point, pointers as ints (0 = NULL)."""
+    return lib().kda_ssm_prefill(x, dt, a, b, c, d, dt_bias, initial_state, cu_seqlens, B, T, H,
+                                 P, G, n, N, x_stride, dt_stride, b_stride, c_stride, flags, out,
+                                 final_state, stream)
+
+
+def kda_ssm_step(x, dt, a, b, c, d, dt_bias, state_in, N, H, P, G, n, x_stride, dt_stride,
+                 b_stride, c_stride, flags, out, state_out, stream) -> int:
+    """The single-token scan C entry point, pointers as ints (0 = NULL)."""
+    return lib().kda_ssm_step(x, dt, a, b, c, d, dt_bias, state_in, N, H, P, G, n, x_stride,
+                              dt_stride, b_stride, c_stride, flags, out, state_out, stream)
+
+
+def kda_paged_decode(q, k_cache, v_cache, page_table, seq_lens, B, Hq, Hkv, D, pages, page_size,
+                     max_pages, k_page_stride, v_page_stride, scale, out, lse, stream) -> int:
+    """The paged decode attention C entry point, pointers as ints (0 = NULL)."""
+    return lib().kda_paged_decode(q, k_cache, v_cache, page_table, seq_lens, B, Hq, Hkv, D, pages,
+                                  page_size, max_pages, k_page_stride, v_page_stride, scale, out,
+                                  lse, stream)
 
 
 def kda_status_string(code: int) -> str:
@@ -380,6 +445,337 @@ def chunk_prefill_backward(q, k, v, g, beta, d_out, initial_state=None, cu_seqle
     if rc != 0:
         raise KdaError(rc, "kda_chunk_prefill_backward")
     return dq, dk, dv, dg, dbeta, ds0
+
+
+def _batch(t, rows_dims, cu_seqlens, name):
+    """(B, T, N) of a [T, ...] or [B, T, ...] tensor whose rows have rows_dims dims."""
+    import torch
+
+    if t.dim() == rows_dims + 2:
+        B, T = t.shape[:2]
+    elif t.dim() == rows_dims + 1:
+        B, T = 1, t.shape[0]
+    else:
+        raise ValueError(f"{name} must be [T, ...] or [B, T, ...]")
+    if cu_seqlens is None:
+        return B, T, B
+    if B != 1:
+        raise ValueError("cu_seqlens needs B == 1")
+    if cu_seqlens.dtype != torch.int32 or not cu_seqlens.is_cuda or not cu_seqlens.is_contiguous():
+        raise ValueError("cu_seqlens must be a contiguous int32 CUDA tensor")
+    return B, T, cu_seqlens.numel() - 1
+
+
+def _row_stride(t, rows_dims, name):
+    """Elements between the rows of a [T, ...] or [B, T, ...] tensor: rows are
+    contiguous inside, evenly spaced, and batches follow one another."""
+    expect = 1
+    for i in range(1, rows_dims + 1):
+        if t.shape[-i] > 1 and t.stride(-i) != expect:
+            raise ValueError(f"{name} must be contiguous within a token")
+        expect *= t.shape[-i]
+    rows = t.shape[:t.dim() - rows_dims]
+    at = t.dim() - rows_dims - 1
+    if len(rows) == 2 and rows[0] > 1 and rows[1] > 0:
+        stride = t.stride(at) if rows[1] > 1 else t.stride(at - 1)
+        if t.stride(at - 1) != rows[1] * stride:
+            raise ValueError(f"{name}: batches must follow one another at the token stride")
+    else:
+        stride = t.stride(at) if rows[-1] > 1 else expect
+    if stride < expect:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return stride
+
+
+def _need(name, t, dtype, shape, contiguous=True):
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if not t.is_cuda or (contiguous and not t.is_contiguous()):
+        raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}")
+
+
+def _conv_flags(activation):
+    if activation not in (None, "silu"):
+        raise ValueError("activation must be None or 'silu'")
+    return CONV_SILU if activation == "silu" else 0
+
+
+def _filter(x, weight, bias):
+    import torch
+
+    if weight.dim() != 2:
+        raise ValueError("weight must be [D, W]")
+    D, W = weight.shape
+    if x.dtype != torch.bfloat16 or not x.is_cuda:
+        raise ValueError("x must be a bfloat16 CUDA tensor")
+    if x.shape[-1] != D:
+        raise ValueError("x must have weight.shape[0] channels")
+    _need("weight", weight, torch.float32, (D, W))
+    if bias is not None:
+        _need("bias", bias, torch.float32, (D,))
+    return D, W
+
+
+def _current_stream(t, stream):
+    import torch
+
+    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream
+
+
+def short_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, activation="silu",
+               out=None, final_state=None, output_final_state=True, stream=None):
+    """Short causal convolution on the current CUDA device, one filter per channel.
+
+    x: bf16 [T, D] (packed or one sequence) or [B, T, D], tokens any even
+    stride apart (a slice of a fused projection); weight: fp32 [D, W], W = 2..4
+    (weight[:, W-1] meets the token itself); bias: fp32 [D] or None;
+    initial_state: bf16 [N, W-1, D], the rows before each sequence, newest
+    last, or None; cu_seqlens: int32 [N+1] on the device or None; activation:
+    "silu" or None. Returns (out, final_state): bf16 like x and the last W-1
+    rows [N, W-1, D] (None if output_final_state is False and final_state is
+    None).
+    """
+    import torch
+
+    flags = _conv_flags(activation)
+    D, W = _filter(x, weight, bias)
+    B, T, N = _batch(x, 1, cu_seqlens, "x")
+    if initial_state is not None:
+        _need("initial_state", initial_state, torch.bfloat16, (N, W - 1, D))
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _need("out", out, torch.bfloat16, x.shape, contiguous=False)
+    if final_state is not None:
+        _need("final_state", final_state, torch.bfloat16, (N, W - 1, D))
+    elif output_final_state:
+        final_state = torch.empty((N, W - 1, D), dtype=torch.bfloat16, device=x.device)
+    rc = kda_short_conv(_ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens),
+                        B, T, D, W, N, _row_stride(x, 1, "x"), flags, _ptr(out),
+                        _row_stride(out, 1, "out"), _ptr(final_state), _current_stream(x, stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_short_conv")
+    return out, final_state
+
+
+def short_conv_step(x, weight, state=None, bias=None, activation="silu", out=None, state_out=None,
+                    in_place=False, stream=None):
+    """The convolution for one new token per sequence on the current CUDA device.
+
+    x: bf16 [N, D]; state: bf16 [N, W-1, D], the last rows, newest last, or
+    None (zeros); the rest as for short_conv. Returns (out, new_state). With
+    in_place=True the new state is written over `state`.
+    """
+    import torch
+
+    flags = _conv_flags(activation)
+    if x.dim() != 2:
+        raise ValueError("x must be [N, D]")
+    D, W = _filter(x, weight, bias)
+    N = x.shape[0]
+    if state is not None:
+        _need("state", state, torch.bfloat16, (N, W - 1, D))
+    if in_place:
+        if state is None:
+            raise ValueError("in_place needs a state")
+        state_out = state
+    elif state_out is None:
+        state_out = torch.empty((N, W - 1, D), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need("state_out", state_out, torch.bfloat16, (N, W - 1, D))
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _need("out", out, torch.bfloat16, x.shape, contiguous=False)
+    rc = kda_short_conv_step(_ptr(x), _ptr(weight), _ptr(bias), _ptr(state), N, D, W,
+                             _row_stride(x, 1, "x"), flags, _ptr(out), _row_stride(out, 1, "out"),
+                             _ptr(state_out), _current_stream(x, stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_short_conv_step")
+    return out, state_out
+
+
+def short_conv_backward(x, weight, d_out, bias=None, initial_state=None, cu_seqlens=None,
+                        activation="silu", d_final_state=None, d_initial_state=True, dx=None,
+                        stream=None):
+    """Gradients of ``short_conv`` on the current CUDA device.
+
+    Inputs as for short_conv, plus d_out (bf16 or fp32, shaped like x) and
+    d_final_state (fp32 [N, W-1, D] or None = 0). Returns (dx, dweight, dbias,
+    d_initial_state): bf16 like x (written to `dx` if given, which may be
+    strided), fp32 [D, W], fp32 [D] (None without a bias) and fp32
+    [N, W-1, D] (None when asked for with False).
+    """
+    import torch
+
+    flags = _conv_flags(activation)
+    D, W = _filter(x, weight, bias)
+    B, T, N = _batch(x, 1, cu_seqlens, "x")
+    if d_out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("d_out must be bfloat16 or float32")
+    _need("d_out", d_out, d_out.dtype, x.shape, contiguous=False)
+    if d_out.dtype == torch.float32:
+        flags |= CONV_DOUT_FP32
+    if initial_state is not None:
+        _need("initial_state", initial_state, torch.bfloat16, (N, W - 1, D))
+    if d_final_state is not None:
+        _need("d_final_state", d_final_state, torch.float32, (N, W - 1, D))
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _need("dx", dx, torch.bfloat16, x.shape, contiguous=False)
+    f32 = dict(dtype=torch.float32, device=x.device)
+    dweight = torch.empty((D, W), **f32)
+    dbias = torch.empty((D,), **f32) if bias is not None else None
+    dh = torch.empty((N, W - 1, D), **f32) if d_initial_state else None
+    rc = kda_short_conv_backward(
+        _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens), B, T, D, W, N,
+        _row_stride(x, 1, "x"), flags, _ptr(d_out), _row_stride(d_out, 1, "d_out"),
+        _ptr(d_final_state), _ptr(dx), _row_stride(dx, 1, "dx"), _ptr(dweight), _ptr(dbias),
+        _ptr(dh), _current_stream(x, stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_short_conv_backward")
+    return dx, dweight, dbias, dh
+
+
+def _ssm_inputs(x, dt, a, b, c, d, dt_bias, rows):
+    """Checks the scan's inputs; returns (H, P, G, n)."""
+    import torch
+
+    H, P = x.shape[-2:]
+    G, n = b.shape[-2:]
+    _need("x", x, torch.bfloat16, (*rows, H, P), contiguous=False)
+    _need("dt", dt, torch.float32, (*rows, H), contiguous=False)
+    _need("b", b, torch.bfloat16, (*rows, G, n), contiguous=False)
+    _need("c", c, torch.bfloat16, (*rows, G, n), contiguous=False)
+    for name, t in (("a", a), ("d", d), ("dt_bias", dt_bias)):
+        if t is not None or name == "a":
+            _need(name, t, torch.float32, (H,))
+    if H % G:
+        raise ValueError("the heads must be a multiple of the groups of b and c")
+    return H, P, G, n
+
+
+def ssm_prefill(x, dt, a, b, c, d=None, dt_bias=None, initial_state=None, cu_seqlens=None,
+                dt_softplus=False, out=None, final_state=None, output_final_state=True,
+                stream=None):
+    """Selective state space scan over a batch of sequences on the current CUDA device.
+
+    S_t = exp(a delta_t) S_{t-1} + delta_t b_t x_t^T, y_t = S_t^T c_t + d x_t, with
+    delta = dt + dt_bias, through softplus if dt_softplus.
+    x: bf16 [T, H, P] (packed or one sequence) or [B, T, H, P]; dt: fp32
+    [..., H]; b, c: bf16 [..., G, n], shared by H/G heads each; tokens of x, dt,
+    b and c any even stride apart (slices of a fused projection); a: fp32 [H]
+    (negative); d, dt_bias: fp32 [H] or None; initial_state: fp32 [N, H, n, P]
+    or None; cu_seqlens: int32 [N+1] on the device or None. P and n are 64 or
+    128. Returns (out, final_state): bf16 like x (contiguous), fp32
+    [N, H, n, P] (None if output_final_state is False and final_state is None).
+    """
+    import torch
+
+    B, T, N = _batch(x, 2, cu_seqlens, "x")
+    H, P, G, n = _ssm_inputs(x, dt, a, b, c, d, dt_bias, x.shape[:-2])
+    if initial_state is not None:
+        _need("initial_state", initial_state, torch.float32, (N, H, n, P))
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _need("out", out, torch.bfloat16, x.shape)
+    if final_state is not None:
+        _need("final_state", final_state, torch.float32, (N, H, n, P))
+    elif output_final_state:
+        final_state = torch.empty((N, H, n, P), dtype=torch.float32, device=x.device)
+    rc = kda_ssm_prefill(
+        _ptr(x), _ptr(dt), _ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(dt_bias),
+        _ptr(initial_state), _ptr(cu_seqlens), B, T, H, P, G, n, N, _row_stride(x, 2, "x"),
+        _row_stride(dt, 1, "dt"), _row_stride(b, 2, "b"), _row_stride(c, 2, "c"),
+        SSM_DT_SOFTPLUS if dt_softplus else 0, _ptr(out), _ptr(final_state),
+        _current_stream(x, stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_ssm_prefill")
+    return out, final_state
+
+
+def ssm_step(x, dt, a, b, c, state=None, d=None, dt_bias=None, dt_softplus=False, out=None,
+             state_out=None, in_place=False, stream=None):
+    """The scan for one new token per sequence on the current CUDA device.
+
+    x: bf16 [N, H, P]; dt: fp32 [N, H]; b, c: bf16 [N, G, n]; state: fp32
+    [N, H, n, P] or None (zeros); the rest as for ssm_prefill. Returns
+    (out, new_state). With in_place=True the new state is written over `state`.
+    """
+    import torch
+
+    if x.dim() != 3:
+        raise ValueError("x must be [N, H, P]")
+    N = x.shape[0]
+    H, P, G, n = _ssm_inputs(x, dt, a, b, c, d, dt_bias, (N,))
+    if state is not None:
+        _need("state", state, torch.float32, (N, H, n, P))
+    if in_place:
+        if state is None:
+            raise ValueError("in_place needs a state")
+        state_out = state
+    elif state_out is None:
+        state_out = torch.empty((N, H, n, P), dtype=torch.float32, device=x.device)
+    else:
+        _need("state_out", state_out, torch.float32, (N, H, n, P))
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _need("out", out, torch.bfloat16, x.shape)
+    rc = kda_ssm_step(_ptr(x), _ptr(dt), _ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(dt_bias),
+                      _ptr(state), N, H, P, G, n, _row_stride(x, 2, "x"),
+                      _row_stride(dt, 1, "dt"), _row_stride(b, 2, "b"), _row_stride(c, 2, "c"),
+                      SSM_DT_SOFTPLUS if dt_softplus else 0, _ptr(out), _ptr(state_out),
+                      _current_stream(x, stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_ssm_step")
+    return out, state_out
+
+
+def paged_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, out=None, lse=None,
+                 stream=None):
+    """Attention of one new token per sequence over a paged cache, current CUDA device.
+
+    q: bf16 [B, Hq, D], D = 64 or 128; k_cache, v_cache: bf16
+    [pages, page_size, Hkv, D], contiguous inside a page (both may be views of
+    one cache); page_table: int32 [B, max_pages]; seq_lens: int32 [B], the new
+    token included (0: out = 0, lse = -inf); scale: 1/sqrt(D) by default.
+    Returns (out, lse): bf16 like q and fp32 [B, Hq] (natural logarithm).
+    """
+    import torch
+
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [B, Hq, D] and the caches [pages, page_size, Hkv, D]")
+    B, Hq, D = q.shape
+    pages, page_size, Hkv, _ = k_cache.shape
+    _need("q", q, torch.bfloat16, (B, Hq, D))
+    _need("k_cache", k_cache, torch.bfloat16, (pages, page_size, Hkv, D), contiguous=False)
+    _need("v_cache", v_cache, torch.bfloat16, (pages, page_size, Hkv, D), contiguous=False)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    _need("page_table", page_table, torch.int32, (B, page_table.shape[1]))
+    _need("seq_lens", seq_lens, torch.int32, (B,))
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        _need("out", out, torch.bfloat16, q.shape)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _need("lse", lse, torch.float32, (B, Hq))
+    rc = kda_paged_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
+                          B, Hq, Hkv, D, pages, page_size, page_table.shape[1],
+                          _row_stride(k_cache, 3, "k_cache"), _row_stride(v_cache, 3, "v_cache"),
+                          float(scale), _ptr(out), _ptr(lse), _current_stream(q, stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_paged_decode")
+    return out, lse
 
 
 def check_device_error(stream=None):

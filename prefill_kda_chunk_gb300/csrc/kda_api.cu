@@ -23,10 +23,15 @@ struct StreamWorkspace {
     // counters (a fused launch leaves its own counters zero and writes past
     // them; any other use of the buffer may overwrite them)
     int64_t ring_clean = 0;
+    // arrival counters of the joined kernels: zeroed when allocated, and left
+    // zero by every launch that uses them
+    void *sync = nullptr;
+    size_t sync_bytes = 0;
 };
 
 struct DeviceState {
     bool ready = false;
+    int sm_count = 0;
     int *err = nullptr;  // sticky error word (device memory, 256 B)
     std::map<cudaStream_t, StreamWorkspace> ws;
 };
@@ -212,6 +217,10 @@ kda_status init_device(int dev, DeviceState &st) {
     if (kda::configure_recurrent() != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::configure_c64() != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::configure_backward_chunk() != cudaSuccess) return KDA_ERR_CUDA;
+    if (kda::configure_ssm() != cudaSuccess) return KDA_ERR_CUDA;
+    if (kda::configure_paged() != cudaSuccess) return KDA_ERR_CUDA;
+    if (cudaDeviceGetAttribute(&st.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return KDA_ERR_CUDA;
     st.ready = true;
     return KDA_OK;
 }
@@ -235,6 +244,72 @@ int kda::pointer_device_status(const void *p, int dev) {
     return KDA_OK;
 }
 
+// Replaces *ptr by at least `need` bytes in stream order, the first `zero` of
+// them zeroed.
+static kda_status grow(void **ptr, size_t *bytes, int64_t need, int64_t zero, bool capturing,
+                       cudaStream_t stream) {
+    if (*bytes >= static_cast<size_t>(need)) return KDA_OK;
+    if (capturing) return KDA_ERR_CAPTURE;
+    if (*ptr != nullptr && cudaFreeAsync(*ptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    *ptr = nullptr;
+    *bytes = 0;
+    if (cudaMallocAsync(ptr, need, stream) != cudaSuccess) {
+        cudaGetLastError();
+        *ptr = nullptr;
+        return KDA_ERR_CUDA;
+    }
+    *bytes = need;
+    if (zero > 0 && cudaMemsetAsync(*ptr, 0, zero, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    return KDA_OK;
+}
+
+int kda::begin_call(const void *const *ptrs, int n, void *stream_, int64_t ws_bytes,
+                    int64_t sync_bytes, CallContext *ctx) {
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
+    ctx->lock = std::unique_lock<std::mutex>(g_mu);
+    DeviceState &st = g_devices[dev];
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return KDA_ERR_CUDA;
+    const bool capturing = cap != cudaStreamCaptureStatusNone;
+    if (!st.ready) {
+        if (capturing) return KDA_ERR_CAPTURE;
+        const kda_status rc = init_device(dev, st);
+        if (rc != KDA_OK) return rc;
+    }
+    if (stream != nullptr && !capturing) {
+        int sdev = -1;
+        if (cudaStreamGetDevice(stream, &sdev) != cudaSuccess) return KDA_ERR_CUDA;
+        if (sdev != dev) return KDA_ERR_WRONG_DEVICE;
+    }
+    for (int i = 0; i < n && !capturing; ++i) {   // pointer queries are not stream work
+        const kda_status rc = check_pointer_device(ptrs[i], dev);
+        if (rc != KDA_OK) return rc;
+    }
+    ctx->err = st.err;
+    ctx->sm_count = st.sm_count;
+    if (ws_bytes > 0 || sync_bytes > 0) {
+        StreamWorkspace &ws = st.ws[stream];
+        if (ws_bytes > 0) {
+            // the flag block at the start (its zeros included) belongs to the
+            // prefill's and the gradients' calls on this buffer
+            const kda_status rc = grow(&ws.ptr, &ws.bytes, 256 + ws_bytes, 256, capturing, stream);
+            if (rc != KDA_OK) return rc;
+            ws.ring_clean = 0;
+            ctx->ws = static_cast<uint8_t *>(ws.ptr) + 256;
+            ctx->call_flags = static_cast<int *>(ws.ptr);
+        }
+        if (sync_bytes > 0) {
+            const kda_status rc =
+                grow(&ws.sync, &ws.sync_bytes, sync_bytes, sync_bytes, capturing, stream);
+            if (rc != KDA_OK) return rc;
+            ctx->sync = static_cast<int *>(ws.sync);
+        }
+    }
+    return KDA_OK;
+}
+
 extern "C" {
 
 const char *kda_status_string(kda_status s) {
@@ -242,7 +317,7 @@ const char *kda_status_string(kda_status s) {
         case KDA_OK: return "ok";
         case KDA_ERR_NULL_ARG: return "a required pointer is NULL";
         case KDA_ERR_BAD_SHAPE: return "sizes are inconsistent or out of range";
-        case KDA_ERR_UNSUPPORTED_DIM: return "only K = V = 128 is supported";
+        case KDA_ERR_UNSUPPORTED_DIM: return "a size is not one the kernels support (KDA: K = V = 128)";
         case KDA_ERR_MISALIGNED: return "a pointer is not aligned as required";
         case KDA_ERR_BAD_CU_SEQLENS: return "cu_seqlens must start at 0, end at T and not decrease";
         case KDA_ERR_CUDA: return "a CUDA runtime call failed";
@@ -256,7 +331,8 @@ const char *kda_status_string(kda_status s) {
         case KDA_ERR_SCRATCH_LIMIT:
             return "the call needs more scratch than the fixed 64 MiB array of "
                    "kda_chunk_prefill_noalloc";
-        case KDA_ERR_BAD_FLAGS: return "an unknown preprocessing flag bit is set";
+        case KDA_ERR_BAD_FLAGS: return "an unknown flag bit is set";
+        case KDA_ERR_BAD_PAGE_TABLE: return "a sequence length or page index is out of range";
     }
     return "unknown status";
 }
@@ -812,6 +888,7 @@ kda_status kda_last_device_error(void *stream_) {
     if (word & kda::kErrBadCu) return KDA_ERR_BAD_CU_SEQLENS;
     if (word & kda::kErrTimeout) return KDA_ERR_DEVICE_TIMEOUT;
     if (word & kda::kErrGate) return KDA_ERR_GATE_RANGE;
+    if (word & kda::kErrPage) return KDA_ERR_BAD_PAGE_TABLE;
     return KDA_OK;
 }
 
@@ -825,6 +902,9 @@ kda_status kda_workspace_release(void) {
     for (auto &kv : it->second.ws) {
         StreamWorkspace &w = kv.second;
         if (w.ptr != nullptr && cudaFree(w.ptr) != cudaSuccess) return KDA_ERR_CUDA;
+        w.ptr = nullptr;
+        if (w.sync != nullptr && cudaFree(w.sync) != cudaSuccess) return KDA_ERR_CUDA;
+        w.sync = nullptr;
     }
     it->second.ws.clear();
     return KDA_OK;

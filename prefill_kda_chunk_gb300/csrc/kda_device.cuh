@@ -38,7 +38,7 @@ __device__ __forceinline__ float log_sigmoid(float x) {
 
 // Error bits. kErrBadCu lives in the per-call flag word and the sticky
 // per-device word; the others only in the sticky word.
-enum : int { kErrBadCu = 1, kErrTimeout = 2, kErrGate = 4 };
+enum : int { kErrBadCu = 1, kErrTimeout = 2, kErrGate = 4, kErrPage = 8 };
 
 // Bounded waits give up after this many nanoseconds of %globaltimer.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 namespace kda {
 
 // Where each sequence's tokens and chunks are. Fixed-length batches
@@ -211,6 +213,86 @@ cudaError_t launch_c64_fused(const C64Args &a, int grid, cudaStream_t stream);
 // NULL, device memory of device `dev` or managed memory; otherwise the
 // kda_status the entry point returns (not device memory / wrong device).
 int pointer_device_status(const void *p, int dev);
+
+// What an entry point works with once its arguments are checked: the device's
+// error word, the stream's workspace (ws_bytes of it; call_flags is the
+// per-call flag word in front) and its zeroed arrival counters. The lock is
+// held until the context goes out of scope, that is over the launches.
+struct CallContext {
+    std::unique_lock<std::mutex> lock;
+    int *err = nullptr;
+    int *call_flags = nullptr;
+    uint8_t *ws = nullptr;
+    int *sync = nullptr;
+    int sm_count = 0;
+};
+// The device checks of an entry point (first use, stream, pointers; NULLs are
+// skipped) and its workspace. Returns a kda_status.
+int begin_call(const void *const *ptrs, int n, void *stream, int64_t ws_bytes, int64_t sync_bytes,
+               CallContext *ctx);
+
+// Short causal convolution (kda_conv.cu). Rows of x, out, d_out and dx are
+// their own stride apart; histories are [n_seqs, W - 1, D].
+struct ConvParams {
+    const void *x;             // bf16
+    const float *weight;       // [D, W]
+    const float *bias;         // [D] or nullptr
+    const void *hist_in;       // bf16 or nullptr (zeros)
+    const int32_t *cu;         // [n_seqs + 1] or nullptr (sequences of seq_len tokens)
+    int64_t tokens, seq_len, dim, x_stride, out_stride, dout_stride;
+    int32_t n_seqs, width;
+    bool silu, dout32;
+    void *out;                 // bf16: out, or dx of the gradient
+    void *hist_out;            // bf16 or nullptr; the step: may be hist_in
+    const void *dout;          // gradient: bf16 or fp32
+    const float *dhist_out;    // gradient: [n_seqs, W - 1, D] or nullptr
+    float *dhist_in;           // gradient: [n_seqs, W - 1, D] or nullptr
+    float *partial;            // gradient: [tiles][W + 1][D]
+    float *dweight, *dbias;    // gradient: [D, W], [D] or nullptr
+    int *err;
+};
+int64_t conv_backward_tiles(int64_t tokens);
+cudaError_t launch_conv(const ConvParams &p, cudaStream_t stream);
+cudaError_t launch_conv_step(const ConvParams &p, cudaStream_t stream);
+cudaError_t launch_conv_backward(const ConvParams &p, cudaStream_t stream);
+
+// Selective state space scan (kda_ssm.cu).
+struct SsmParams {
+    const void *x;             // bf16 [tokens, H, P]
+    const float *dt;           // [tokens, H]
+    const float *a;            // [H]
+    const void *b, *c;         // bf16 [tokens, G, n]
+    const float *d, *dt_bias;  // [H] or nullptr
+    const float *s0;           // [n_seqs, H, n, P] or nullptr (zeros)
+    const int32_t *cu;         // [n_seqs + 1] or nullptr (sequences of seq_len tokens)
+    int64_t tokens, seq_len, x_stride, dt_stride, b_stride, c_stride;
+    int32_t n_seqs, heads, groups, p, n;
+    bool softplus;
+    void *out;                 // bf16 [tokens, H, P]
+    float *s_final;            // [n_seqs, H, n, P] or nullptr
+    int *err;
+};
+cudaError_t configure_ssm();
+int64_t ssm_workspace(const SsmParams &p);
+cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t stream);
+cudaError_t launch_ssm_step(const SsmParams &p, cudaStream_t stream);
+
+// Paged decode attention (kda_paged.cu).
+struct PagedParams {
+    const void *q, *k, *v;     // bf16 [B, Hq, D], pages of [page_size, Hkv, D]
+    const int32_t *table, *lens;
+    int64_t k_stride, v_stride;   // elements between pages
+    int64_t pages, max_pages;
+    int32_t batch, hq, hkv, dim, page_size;
+    float scale;
+    void *out;                 // bf16 [B, Hq, D]
+    float *lse;                // [B, Hq] or nullptr
+    int *err;
+};
+cudaError_t configure_paged();
+int64_t paged_workspace(const PagedParams &p);
+int64_t paged_sync(const PagedParams &p);
+cudaError_t launch_paged(const PagedParams &p, const CallContext &ctx, cudaStream_t stream);
 
 // The error word of the allocation-free entry point's fixed scratch array on
 // device `dev` (kda_noalloc.cu): read and cleared with a synchronous copy,
