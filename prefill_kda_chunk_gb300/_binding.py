@@ -46,6 +46,8 @@ class KdaError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load the library (once). Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -469,31 +471,37 @@ def _batch(t, rows_dims, cu_seqlens, name):
 def _row_stride(t, rows_dims, name):
     """Elements between the rows of a [T, ...] or [B, T, ...] tensor: rows are
     contiguous inside, evenly spaced, and batches follow one another."""
-    expect = 1
+    shape = t.shape
+    expect = math.prod(shape[-rows_dims:])
+    if t.is_contiguous():
+        return expect
+    strides = t.stride()
+    inner = 1
     for i in range(1, rows_dims + 1):
-        if t.shape[-i] > 1 and t.stride(-i) != expect:
+        if strides[-i] != inner and shape[-i] > 1:
             raise ValueError(f"{name} must be contiguous within a token")
-        expect *= t.shape[-i]
-    rows = t.shape[:t.dim() - rows_dims]
-    at = t.dim() - rows_dims - 1
-    if len(rows) == 2 and rows[0] > 1 and rows[1] > 0:
-        stride = t.stride(at) if rows[1] > 1 else t.stride(at - 1)
-        if t.stride(at - 1) != rows[1] * stride:
+        inner *= shape[-i]
+    at = len(shape) - rows_dims - 1
+    stride = strides[at] if shape[at] > 1 else expect
+    if at == 1 and shape[0] > 1:
+        if shape[1] == 1:
+            stride = strides[0]
+        elif strides[0] != shape[1] * stride:
             raise ValueError(f"{name}: batches must follow one another at the token stride")
-    else:
-        stride = t.stride(at) if rows[-1] > 1 else expect
     if stride < expect:
         raise ValueError(f"{name}: tokens must not overlap")
     return stride
 
 
 def _need(name, t, dtype, shape, contiguous=True):
+    if (t.dtype is dtype and t.shape == shape and t.is_cuda
+            and (not contiguous or t.is_contiguous())):
+        return
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}")
-    if not t.is_cuda or (contiguous and not t.is_contiguous()):
-        raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}CUDA tensor")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}")
+    raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}CUDA tensor")
 
 
 def _conv_flags(activation):
@@ -521,7 +529,8 @@ def _filter(x, weight, bias):
 def _current_stream(t, stream):
     import torch
 
-    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream
+    # the raw handle: torch.cuda.current_stream() builds a Stream object first
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream
 
 
 def short_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, activation="silu",
