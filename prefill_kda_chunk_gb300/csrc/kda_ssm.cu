@@ -51,11 +51,9 @@ __device__ __forceinline__ float bf16_at(const void *p, int64_t i) {
     return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
 }
 
-__device__ __forceinline__ float delta_of(const SsmParams &p, int64_t t, int h) {
-    float v = p.dt[t * p.dt_stride + h];
-    if (p.dt_bias != nullptr) v += __ldg(p.dt_bias + h);
+__device__ __forceinline__ float delta_of(float v, bool softplus) {
     // log(1 + e^v) without overflow, and exact for large negative v
-    return p.softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
+    return softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
 }
 
 // ------------------------------------------------------------- one token
@@ -76,7 +74,9 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p) {
         s_b[threadIdx.x] = bf16_at(p.b, n * p.b_stride + g * kN + threadIdx.x);
         s_c[threadIdx.x] = bf16_at(p.c, n * p.c_stride + g * kN + threadIdx.x);
     }
-    const float delta = delta_of(p, n, h), decay = expf(av * delta);
+    const float bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + h) : 0.f;
+    const float delta = delta_of(p.dt[n * p.dt_stride + h] + bias, p.softplus);
+    const float decay = expf(av * delta);
     const float x = bf16_at(p.x, n * p.x_stride + h * kP + q);
     __syncthreads();
     float y = 0.f;
@@ -100,50 +100,100 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p) {
 constexpr int kL = 128;              // tokens per chunk
 constexpr int kPS = 64;              // channels of P per unit
 constexpr int kSsmSms = 152;
-constexpr int kCompute = 256;        // threads of the eight compute warps
-constexpr int kThreads = kCompute + 64;   // and the control and scalar warps
+constexpr int kWarpsC = 16;          // compute warps
+constexpr int kCompute = 32 * kWarpsC;
+// after them one warp for the MMAs, one for the copies and two for the decays
+constexpr int kMmaWarp = kWarpsC, kCopyWarp = kMmaWarp + 1, kScalWarp = kMmaWarp + 2;
+constexpr int kThreads = 32 * (kScalWarp + 2);
+constexpr int kRing = 4;             // chunks of decays computed ahead
+constexpr int kCols = 16;            // columns of the state and of y per compute thread
 
 // Shared memory, from a 1024-byte boundary. Tiles of 128-byte rows with the
 // 16-byte granule index XOR-ed by the row's low three bits.
+constexpr int kTileBytes = 16384;                // 128 rows
 constexpr int kOffC = 0;                         // [n / 64][128 tokens][64]
-constexpr int kOffB = 32768;                     // two buffers of the same
-constexpr int kOffX = kOffB + 2 * 32768;         // two buffers of [128 tokens][64]
-constexpr int kOffW = kOffX + 2 * 16384;         // three terms of the weighted rows
-constexpr int kOffS = kOffW + 3 * 16384;         // two terms of the state, [n][64]
-constexpr int kOffSc = kOffS + 2 * 16384;        // two buffers of Scalars
+constexpr int kOffS = kOffC + 2 * kTileBytes;    // two terms of the state, [n][64]
+constexpr int kOffB = kOffS + 2 * kTileBytes;    // two buffers of [n / 64][128 tokens][64]
+constexpr int kOffX = kOffB + 4 * kTileBytes;    // two buffers of [128 tokens][64]
+constexpr int kOffW = kOffX + 2 * kTileBytes;    // three terms of the weighted rows
+constexpr int kOffSc = kOffW + 3 * kTileBytes;   // kRing buffers of Scalars
 struct Scalars {
-    float hi[kL], lo[kL];   // G_t as a sum of two floats, in units of log 2
+    float hi[kL], lo[kL];   // -G_t as a sum of two floats, in units of log 2
     float dt[kL];           // delta_t; 0 past the sequence's end
     float to_block[kL];     // 2^(G at the end of t's 32-block - G_t) delta_t
     float to_end[kL];       // 2^(G_last - G_t) delta_t
     float from[kL];         // 2^G_t
     float end_hi[4], end_lo[4];   // G at the end of each 32-block
-    float decay, pad[7];    // 2^G_last
+    float decay;            // 2^G_last
+    // where the chunk is, so that the compute warps need not walk the list
+    int valid;              // its tokens
+    int unit, seq, pos;     // head and slice; sequence; chunk of the sequence
+    int flags;              // kLast, kCut
+    int64_t row;            // its first token
 };
-constexpr int kOffBar = kOffSc + 2 * static_cast<int>(sizeof(Scalars));
+enum { kLast = 1, kCut = 2 };   // the sequence's last chunk; the run's end cuts the sequence
+constexpr int kOffBar = kOffSc + kRing * static_cast<int>(sizeof(Scalars));
 enum {   // barriers, 8 bytes each
-    kFullC, kFullBX, kScal = kFullBX + 2, kCB = kScal + 2, kCSDS, kMX, kMReady, kSReady, kWReady,
-    kDone, kDrain, kBars
+    // phases that one thread or a copy completes
+    kFullC, kFullBX, kScal = kFullBX + 2, kCB = kScal + kRing, kDS, kCS, kMX, kDrain,
+    // phases that every compute warp arrives at
+    kMReady, kSReady, kWReady, kDone, kFreeBX, kScFree = kFreeBX + 2, kBars = kScFree + kRing
 };
-constexpr int kSmem = kOffBar + 8 * kBars + 1024;
+constexpr int kOffMisc = kOffBar + 8 * kBars;    // tensor memory base, abort flag
+constexpr int kSmem = kOffMisc + 8;
 
-// Tensor memory columns.
-constexpr uint32_t kTmCB = 0, kTmM = 128, kTmY = 256, kTmCS = 320, kTmDS = 384, kTmCols = 512;
+// Tensor memory columns; the block takes all of them, so they start at 0. M
+// replaces C B^T: 16 columns (tokens s) become the 8 columns of its high terms
+// and the 8 of its low terms. The terms of S and of W X lie side by side along N,
+// so that one MMA reads C (or B) for all of them; their products are added when
+// they are read. The launch for the states works on two chunks at a time.
+constexpr uint32_t kTmCB = 0, kTmY = 128, kTmCS = 192, kTmDS = 320, kTmCols = 512;
+__device__ __forceinline__ uint32_t tm_ds(bool states, int i) {
+    return states ? 256u * (i & 1) : kTmDS;
+}
+// The weighted rows of chunk i; the launch for the states has two sets.
+__device__ __forceinline__ int off_w(bool states, int i) {
+    return states && (i & 1) != 0 ? kOffC : kOffW;
+}
 
 // ---- instruction and shared-memory descriptors (bf16, fp32 accumulate)
 constexpr uint32_t kAMajor = 1u << 15, kBMajor = 1u << 16;   // operand contiguous along M / N
 // 128-byte swizzled tiles, eight rows of 128 bytes per atom. Contiguous along
-// K: sbo = step between 8-row groups. Contiguous along M or N: sbo = step
-// between groups of 8 along K, lbo = step between blocks of 64 along M / N.
-__device__ __forceinline__ uint64_t desc128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return tc::sdesc(saddr, lbo, sbo) | (static_cast<uint64_t>(2) << 61);
+// K: the stride field is the step between 8-row groups. Contiguous along M or N:
+// it is the step between groups of 8 along K, and the leading field the one
+// between blocks of 64 along M / N. All tiles here have a stride of 1024 bytes,
+// so that descriptors differ in their lower word only.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) {
+    return ((saddr >> 4) & 0x3FFF) | (static_cast<uint32_t>(kTileBytes >> 4) << 16);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// One MMA, issued by the lane with `one` set. The whole warp runs the code around
+// it, so that descriptors stay in uniform registers (issued from a branch of a
+// single lane each MMA took 2 to 3 times as long).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc,
+                                       uint32_t one) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(acc)
+        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " mov.b64 x, {%1, %6};\n mov.b64 y, {%2, %6};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(one), "r"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc,
+                                       uint32_t one) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " mov.b64 y, {%2, %6};\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(one), "r"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t one) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+        "r"(one)
         : "memory");
 }
 
@@ -153,6 +203,13 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int
         " [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
         : "memory");
+}
+
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap *map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
 }
 
 __device__ __forceinline__ void fence_async() {
@@ -165,12 +222,61 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// (a, b) as two bf16 terms: hi + lo
-__device__ __forceinline__ uint32_t split2(float a, float b, uint32_t &lo) {
+// packed fp32 pairs: (a, b) += (x, y), (a, b) = (a, b) * (x, y) + (u, v)
+__device__ __forceinline__ void add2(float &a, float &b, float x, float y) {
+    asm("{\n .reg .b64 t, u;\n mov.b64 t, {%0, %1};\n mov.b64 u, {%2, %3};\n"
+        " add.rn.f32x2 t, t, u;\n mov.b64 {%0, %1}, t;\n}\n"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void fma2(float &a, float &b, float x, float y, float u, float v) {
+    asm("{\n .reg .b64 t, s, w;\n mov.b64 t, {%0, %1};\n mov.b64 s, {%2, %3};\n mov.b64 w, {%4, %5};\n"
+        " fma.rn.f32x2 t, t, s, w;\n mov.b64 {%0, %1}, t;\n}\n"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y), "f"(u), "f"(v));
+}
+
+// (a, b) as two bf16 terms: hi + lo; (a, b) keeps what hi leaves
+__device__ __forceinline__ uint32_t take2(float &a, float &b) {
     const uint32_t h = pack_bf16(a, b);
-    const float2 f = unpack_bf16(h);
-    lo = pack_bf16(a - f.x, b - f.y);
+    float x = __uint_as_float(h << 16), y = __uint_as_float(h & 0xffff0000u);
+    fma2(x, y, -1.f, -1.f, a, b);
+    a = x;
+    b = y;
     return h;
+}
+__device__ __forceinline__ uint32_t split2(float a, float b, uint32_t &lo) {
+    const uint32_t h = take2(a, b);
+    lo = pack_bf16(a, b);
+    return h;
+}
+
+// hi + lo += x, with the rounding error of the sum kept in lo
+struct Sum2 {
+    float hi, lo;
+    __device__ __forceinline__ void add(float xh, float xl) {
+        const float s = hi + xh, b = s - hi;
+        const float e = ((hi - (s - b)) + (xh - b)) + (lo + xl);
+        hi = s + e;
+        lo = e - (hi - s);
+    }
+};
+
+__device__ __forceinline__ void ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+// A wait of at most 2^31 clocks (about a second) for a phase of an mbarrier, in
+// few instructions: this kernel waits in some twenty places, and with longer
+// waits at each of them its loops did not fit the instruction cache (a chunk
+// then took 3 times as long).
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
+    const uint32_t t0 = static_cast<uint32_t>(clock());
+#pragma unroll 1
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+    } while (static_cast<uint32_t>(clock()) - t0 < 0x80000000u);
+    return false;
 }
 
 struct SsmMaps {
@@ -178,13 +284,13 @@ struct SsmMaps {
 };
 
 struct SsmPlan {
-    int slices;                // units per head
+    int shift;                 // a head is 1 << shift units
     int cps;                   // chunks per sequence (fixed lengths)
-    int64_t units;             // heads * slices
+    int64_t units;             // heads << shift
     const int32_t *chunk_off;  // packed: first chunk of each sequence [N + 1]
     const int *call_flags;     // packed: set by the prologue
     int64_t gran;              // chunks that stay together; 0: all of a unit's
-    float *slots;              // [G][32][256] states at the cuts
+    float *slots;              // [G][kCols][kCompute] states at the cuts
     float *saved;              // the same: initial states that a cut run starts from (in place)
     float *decay;              // [G]
     bool in_place;
@@ -283,9 +389,8 @@ __global__ void __launch_bounds__(256) ssm_hand_on_kernel(SsmParams p) {
 template <int kN, bool kStates>
 __global__ void __launch_bounds__(kThreads, 1)
 ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) {
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ uint32_t s_tmem;
-    __shared__ volatile int s_abort;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    volatile int &s_abort = *reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
     if (pl.call_flags != nullptr && (*pl.call_flags & kErrBadCu) != 0) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (!kStates && tid < kCompute) hand_on<kN>(p, tid, kCompute);
@@ -303,230 +408,280 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
     }
     const int count = static_cast<int>(q1 - q0);
 
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                ~static_cast<uintptr_t>(1023));
     const uint32_t sb = smem_u32(smem);
     const auto bar = [&](int i) { return sb + kOffBar + 8 * i; };
     Scalars *scal = reinterpret_cast<Scalars *>(smem + kOffSc);
 
     if (tid == 0) {
-        s_abort = 0;
-        for (int i : {static_cast<int>(kFullC), kFullBX + 0, kFullBX + 1, kScal + 0, kScal + 1,
-                      static_cast<int>(kCB), static_cast<int>(kCSDS), static_cast<int>(kMX),
-                      static_cast<int>(kDrain)})
-            mbar_init(bar(i), 1);
-        for (int i : {kMReady, kSReady, kWReady, kDone}) mbar_init(bar(i), kCompute);
+        s_abort = (sb & 1023) != 0;   // (the tiles' swizzle counts on it)
+        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i < kMReady ? 1 : kWarpsC);
         mbar_fence_init();
     }
     if (warp == 0) {
-        tc::alloc(smem_u32(&s_tmem), kTmCols);
+        tc::alloc(sb + kOffMisc, kTmCols);
         tc::relinquish();
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tm = s_tmem;
 
     // A bounded wait; once one has run out, all of them give up.
     auto wait = [&](int i, int phase) -> bool {
-        if (s_abort == 0 && mbar_wait(bar(i), phase & 1)) return true;
+        if (mbar_try_wait(bar(i), phase & 1)) return true;
+        if (s_abort == 0 && wait_phase(bar(i), phase & 1)) return true;
         s_abort = 1;
-        atomicOr(p.err, kErrTimeout);
         return false;
+    };
+    auto arrive = [&](int i) {   // one arrival per warp
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(i));
     };
 
     Walk w;
     w.go(p, pl, list.nc, q0);
-    const int per_group = p.heads / p.groups;
 
-    if (warp == 8) {
-        // ------------------------------------------- control: copies and MMAs
-        if (lane == 0) {
-            Walk l = w;     // the next chunk whose b and x are copied
-            int issued = 0, issued_c = 0, seen_c = 0, seen = 0;
-            auto copy_bx = [&]() {
-                const int h = l.u / pl.slices, s = issued & 1;
-                const int row = static_cast<int>(l.row());
-                mbar_arrive_expect_tx(bar(kFullBX + s), kL * 2 * (kN + kPS));
+    if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMAs
+        const uint32_t one = lane == 0;
+        // k-steps of 16: 32 bytes along a row, or 16 rows of 128 bytes
+        constexpr uint32_t kStepK = 32 >> 4, kStepMN = 2048 >> 4, kTile = kTileBytes >> 4;
+        const uint32_t C = desc_lo(sb + kOffC);
+        const uint32_t S = desc_lo(sb + kOffS);
+        auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+        // C B^T of chunk i
+        auto issue_cb = [&](int i) {
+            const uint32_t BK = desc_lo(sb + kOffB) + 2 * kTile * (i & 1);
 #pragma unroll
-                for (int k = 0; k < kN / 64; ++k)
-                    tma_2d(sb + kOffB + s * 32768 + k * 16384, &maps.b, (h / per_group) * kN + 64 * k, row,
-                           bar(kFullBX + s));
-                tma_2d(sb + kOffX + s * 16384, &maps.x, h * p.p + (l.u % pl.slices) * kPS, row,
-                       bar(kFullBX + s));
-                ++issued;
-                l.next(p, pl, list.nc);
-            };
-            auto copy_c = [&](const Walk &v) {
-                const int h = v.u / pl.slices, row = static_cast<int>(v.row());
-                mbar_arrive_expect_tx(bar(kFullC), kL * 2 * kN);
-#pragma unroll
-                for (int k = 0; k < kN / 64; ++k)
-                    tma_2d(sb + kOffC + k * 16384, &maps.c, (h / per_group) * kN + 64 * k, row, bar(kFullC));
-                ++issued_c;
-            };
-            if (!kStates) copy_c(w);
-            copy_bx();
-            if (count > 1) copy_bx();
-            for (int i = 0; i < count; ++i) {
-                const uint32_t B = sb + kOffB + (i & 1) * 32768, X = sb + kOffX + (i & 1) * 16384;
-                const uint32_t C = sb + kOffC, W = sb + kOffW, S = sb + kOffS;
-                if (!wait(kFullBX + (i & 1), i >> 1)) break;
-                ++seen;
-                if (!kStates) {
-                    if (!wait(kFullC, i)) break;
-                    ++seen_c;
-                    tc::fence_after();
-                    // C B^T
-#pragma unroll
-                    for (int k = 0; k < kN / 16; ++k) {
-                        const uint32_t o = (k >> 2) * 16384 + (k & 3) * 32;
-                        mma_ss(tm + kTmCB, desc128(C + o, 16, 1024), desc128(B + o, 16, 1024),
-                               tc::idesc(128, 128, 1), k > 0);
-                    }
-                    tc::commit(bar(kCB));
-                }
-                if (i > 0) {
-                    // the outputs of the chunk before are read, its buffers free
-                    if (!wait(kDone, i - 1)) break;
-                    if (issued < count) copy_bx();
-                }
-                if (!wait(kWReady, i)) break;
-                if (!kStates && !wait(kSReady, i)) break;
+            for (int k = 0; k < kN / 16; ++k)
+                mma_ss(kTmCB, C + (k >> 2) * kTile + (k & 3) * kStepK, BK + (k >> 2) * kTile + (k & 3) * kStepK,
+                       tc::idesc(128, 128, 1), k > 0, one);
+            commit(bar(kCB), one);
+        };
+#pragma unroll 1
+        for (int i = kStates ? 0 : -1; i < count; ++i) {
+            const int par = __shfl_sync(0xffffffffu, i & 1, 0);
+            if (i >= 0) {
+                // B^T (W X), the three terms of W X along N (for n = 64 the upper 64
+                // rows are formed from whatever lies there and are not read)
+                if (!all(wait(kWReady, i) && (!kStates || wait(kFullBX + (i & 1), i >> 1)))) break;
                 tc::fence_after();
+                const uint32_t BM = desc_lo(sb + kOffB) + 2 * kTile * par;
+                const uint32_t W = desc_lo(sb + (kStates && par != 0 ? kOffC : kOffW));
+#pragma unroll
+                for (int k = 0; k < kL / 16; ++k)
+                    mma_ss(kStates ? 256 * par : kTmDS, BM + k * kStepMN, W + k * kStepMN,
+                           tc::idesc(128, 3 * kPS, 1) | kAMajor | kBMajor, k > 0, one);
+                commit(bar(kDS), one);
                 if (!kStates) {
-                    // C S, both terms of S
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int k = 0; k < kN / 16; ++k)
-                            mma_ss(tm + kTmCS, desc128(C + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
-                                   desc128(S + t * 16384 + k * 2048, 16384, 1024),
-                                   tc::idesc(128, kPS, 1) | kBMajor, t + k > 0);
-                }
-                // B^T (W X), the three terms of W X, the smallest first (for
-                // n = 64 the upper 64 rows are formed from whatever lies there
-                // and are not read)
-#pragma unroll
-                for (int t = 2; t >= 0; --t)
-#pragma unroll
-                    for (int k = 0; k < kL / 16; ++k)
-                        mma_ss(tm + kTmDS, desc128(B + k * 2048, 16384, 1024),
-                               desc128(W + t * 16384 + k * 2048, 16384, 1024),
-                               tc::idesc(128, kPS, 1) | kAMajor | kBMajor, t < 2 || k > 0);
-                tc::commit(bar(kCSDS));
-                if (!kStates) {
-                    if (!wait(kMReady, i)) break;
+                    // C S, both terms of S along N, once the chunk before is read out
+                    if (!all(wait(kSReady, i) && (i == 0 || wait(kDone, i - 1)))) break;
                     tc::fence_after();
-                    // M X, both terms of M
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
+                    for (int k = 0; k < kN / 16; ++k)
+                        mma_ss(kTmCS, C + (k >> 2) * kTile + (k & 3) * kStepK, S + k * kStepMN,
+                               tc::idesc(128, 2 * kPS, 1) | kBMajor, k > 0, one);
+                    commit(bar(kCS), one);
+                    // M X, both terms of M along K
+                    if (!all(wait(kMReady, i))) break;
+                    tc::fence_after();
+                    const uint32_t X = desc_lo(sb + kOffX) + kTile * par;
 #pragma unroll
-                        for (int k = 0; k < kL / 16; ++k)
-                            tc::mma_bf16_ts(tm + kTmY, tm + kTmM + t * 64 + k * 8,
-                                            desc128(X + k * 2048, 16384, 1024),
-                                            tc::idesc(128, kPS, 1) | kBMajor, t + k > 0);
-                    tc::commit(bar(kMX));
-                    if (i + 1 < count) {
-                        if (!wait(kCSDS, i)) break;   // C is free
-                        w.next(p, pl, list.nc);
-                        copy_c(w);
-                    }
+                    for (int k = 0; k < kL / 8; ++k)
+                        mma_ts(kTmY, kTmCB + 8 * k, X + (k >> 1) * kStepMN, tc::idesc(128, kPS, 1) | kBMajor,
+                               k > 0, one);
+                    commit(bar(kMX), one);
                 }
             }
-            // what is still in flight after a wait that gave up: let it land
-            for (; seen < issued; ++seen) mbar_wait(bar(kFullBX + (seen & 1)), (seen >> 1) & 1);
-            for (; seen_c < issued_c; ++seen_c) mbar_wait(bar(kFullC), seen_c & 1);
-            if (s_abort != 0) {
-                tc::commit(bar(kDrain));
-                mbar_wait(bar(kDrain), 0);
+            if (!kStates && i + 1 < count) {
+                // C B^T of the next chunk, over M of this one
+                if (!all(wait(kFullBX + ((i + 1) & 1), (i + 1) >> 1) && wait(kFullC, i + 1) &&
+                         (i < 0 || wait(kMX, i))))
+                    break;
+                tc::fence_after();
+                issue_cb(__shfl_sync(0xffffffffu, i + 1, 0));
             }
         }
+        if (s_abort != 0) {   // after a wait that gave up: let what was issued end
+            commit(bar(kDrain), one);
+            wait_phase(bar(kDrain), 0);
+        }
         __syncwarp();
-    } else if (warp == 9) {
-        // --------------------------------- scalars: the decays of each chunk
-        for (int i = 0; i < count; ++i) {
-            if (i >= 2 && !wait(kDone, i - 2)) break;
-            Scalars &s = scal[i & 1];
-            const int h = w.u / pl.slices, valid = w.valid();
+    } else if (warp == kCopyWarp) {
+        // ---------------------------------------------------------- copies
+        if (lane == 0) {
+            Walk l = w, f = w;    // the next chunk whose b and x are copied; prefetched
+            int bx = 0, cc = 0, pf = 0;   // copies issued, chunks prefetched into L2
+            const int per_group = p.heads / p.groups;
+#pragma unroll 1
+            for (int i = kStates ? 0 : -1; i < count; ++i) {
+                // chunk i + 1 of c, as soon as chunk i is done with its buffer, and
+                // chunk i + 2 of b and x (the first time two of them)
+                if (!kStates && i + 1 < count) {
+                    if (i >= 0 && !wait(kCS, i)) break;
+                    const int h = w.u >> pl.shift, row = static_cast<int>(w.row());
+                    mbar_arrive_expect_tx(bar(kFullC), kL * 2 * kN);
+#pragma unroll 1
+                    for (int k = 0; k < kN / 64; ++k)
+                        tma_2d(sb + kOffC + k * kTileBytes, &maps.c, (h / per_group) * kN + 64 * k, row, bar(kFullC));
+                    ++cc;
+                    w.next(p, pl, list.nc);
+                }
+                const int upto = min(count, i + (kStates ? 2 : 3));
+#pragma unroll 1
+                while (bx < upto) {
+                    if (bx >= 2 && !wait(kFreeBX + (bx & 1), (bx >> 1) - 1)) break;
+                    const int h = l.u >> pl.shift, s = bx & 1;
+                    const int row = static_cast<int>(l.row());
+                    mbar_arrive_expect_tx(bar(kFullBX + s), kL * 2 * (kN + kPS));
+#pragma unroll 1
+                    for (int k = 0; k < kN / 64; ++k)
+                        tma_2d(sb + kOffB + (2 * s + k) * kTileBytes, &maps.b, (h / per_group) * kN + 64 * k, row,
+                               bar(kFullBX + s));
+                    tma_2d(sb + kOffX + s * kTileBytes, &maps.x, h * p.p + (l.u & pl.shift) * kPS, row,
+                           bar(kFullBX + s));
+                    ++bx;
+                    l.next(p, pl, list.nc);
+                }
+                if (bx < upto) break;
+                // a buffer is free for about half a chunk's time before its next
+                // copy is needed, less than a read from HBM takes: fetch ahead
+#pragma unroll 1
+                for (; pf < min(count, i + 6); ++pf) {
+                    if (pf >= bx) {
+                        const int h = f.u >> pl.shift, row = static_cast<int>(f.row());
+#pragma unroll 1
+                        for (int k = 0; k < kN / 64; ++k) {
+                            prefetch_2d(&maps.b, (h / per_group) * kN + 64 * k, row);
+                            if (!kStates) prefetch_2d(&maps.c, (h / per_group) * kN + 64 * k, row);
+                        }
+                        prefetch_2d(&maps.x, h * p.p + (f.u & pl.shift) * kPS, row);
+                    }
+                    f.next(p, pl, list.nc);
+                }
+            }
+            // the last copies land before the block ends (after a wait that gave
+            // up nobody else may have waited for them)
+            for (int j = bx > 2 ? bx - 2 : 0; j < bx; ++j) wait_phase(bar(kFullBX + (j & 1)), (j >> 1) & 1);
+            if (cc > 0) wait_phase(bar(kFullC), (cc - 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp >= kScalWarp) {
+        // --------- scalars: the decays of each chunk, the two warps in turn
+        float raw[4], next_raw[4] = {};
+        auto load = [&]() {   // this chunk's dt, ahead of their use
+            const int h = w.u >> pl.shift, valid = w.valid();
+            const int64_t row = w.row();
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                next_raw[j] = 4 * lane + j < valid ? __ldg(p.dt + (row + 4 * lane + j) * p.dt_stride + h) : 0.f;
+        };
+        const int first = warp - kScalWarp;
+        if (first == 1 && count > 1) w.next(p, pl, list.nc);
+        if (first < count) load();
+#pragma unroll 1
+        for (int i = first; i < count; i += 2) {
+            const int h = w.u >> pl.shift, valid = w.valid(), unit = w.u, seq = w.n, pos = w.pos;
+            const int flags = (w.last() ? kLast : 0) | (q0 + i + (w.len + kL - 1) / kL - pos > q1 ? kCut : 0);
+            const int64_t row = w.row();
             const float a2 = __ldg(p.a + h) * 1.44269504088896341f;
-            float dt[4];
-            double g[4], sum = 0.0;
+            const float bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + h) : 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = 4 * lane + j;
-                dt[j] = t < valid ? delta_of(p, w.row() + t, h) : 0.f;
-                sum += t < valid ? static_cast<double>(a2 * dt[j]) : 0.0;
-                g[j] = sum;
+            for (int j = 0; j < 4; ++j) raw[j] = next_raw[j];
+            if (i + 2 < count) {
+                w.next(p, pl, list.nc);
+                w.next(p, pl, list.nc);
+                load();
             }
-            double incl = sum;
-#pragma unroll
+            if (i >= kRing && !wait(kScFree + (i & (kRing - 1)), (i / kRing) - 1)) break;
+            Scalars &s = scal[i & (kRing - 1)];
+            // running sums over this lane's four tokens, then over the lanes
+            Sum2 sum{0.f, 0.f};
+            float dt[4], gh[4], gl[4];
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                const float v = j == 0 ? raw[0] : j == 1 ? raw[1] : j == 2 ? raw[2] : raw[3];
+                const float d = 4 * lane + j < valid ? delta_of(v + bias, p.softplus) : 0.f;
+                sum.add(a2 * d, 0.f);
+                s.dt[4 * lane + j] = d;
+                s.hi[4 * lane + j] = sum.hi;
+                s.lo[4 * lane + j] = sum.lo;
+            }
+            *reinterpret_cast<float4 *>(dt) = *reinterpret_cast<const float4 *>(s.dt + 4 * lane);
+            *reinterpret_cast<float4 *>(gh) = *reinterpret_cast<const float4 *>(s.hi + 4 * lane);
+            *reinterpret_cast<float4 *>(gl) = *reinterpret_cast<const float4 *>(s.lo + 4 * lane);
+            Sum2 incl = sum;
+#pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
-                const double v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
+                const float vh = __shfl_up_sync(0xffffffffu, incl.hi, o);
+                const float vl = __shfl_up_sync(0xffffffffu, incl.lo, o);
+                if (lane >= o) incl.add(vh, vl);
             }
-            const double before = incl - sum;
-            const double block = __shfl_sync(0xffffffffu, incl, lane | 7);
-            const double end = __shfl_sync(0xffffffffu, incl, 31);
+            float bh = __shfl_up_sync(0xffffffffu, incl.hi, 1), bl = __shfl_up_sync(0xffffffffu, incl.lo, 1);
+            if (lane == 0) bh = bl = 0.f;
+            const float kh = __shfl_sync(0xffffffffu, incl.hi, lane | 7);
+            const float kl = __shfl_sync(0xffffffffu, incl.lo, lane | 7);
+            const float eh = __shfl_sync(0xffffffffu, incl.hi, 31), el = __shfl_sync(0xffffffffu, incl.lo, 31);
+            float v[5][4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int t = 4 * lane + j;
-                const double G = before + g[j];
-                const float hi = static_cast<float>(G);
-                s.hi[t] = hi;
-                s.lo[t] = static_cast<float>(G - hi);
-                s.dt[t] = dt[j];
-                s.to_block[t] = exp2f(static_cast<float>(block - G)) * dt[j];
-                s.to_end[t] = exp2f(static_cast<float>(end - G)) * dt[j];
-                s.from[t] = exp2f(hi);
+                Sum2 G{bh, bl};
+                G.add(gh[j], gl[j]);
+                v[0][j] = -G.hi;
+                v[1][j] = -G.lo;
+                v[2][j] = ex2((kh - G.hi) + (kl - G.lo)) * dt[j];
+                v[3][j] = ex2((eh - G.hi) + (el - G.lo)) * dt[j];
+                v[4][j] = ex2(G.hi);
             }
+            float *const dst[5] = {s.hi, s.lo, s.to_block, s.to_end, s.from};
+#pragma unroll
+            for (int k = 0; k < 5; ++k)
+                *reinterpret_cast<float4 *>(dst[k] + 4 * lane) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
             if ((lane & 7) == 7) {
-                const float hi = static_cast<float>(block);
-                s.end_hi[lane >> 3] = hi;
-                s.end_lo[lane >> 3] = static_cast<float>(block - hi);
+                s.end_hi[lane >> 3] = kh;
+                s.end_lo[lane >> 3] = kl;
             }
-            if (lane == 31) s.decay = exp2f(static_cast<float>(end));
+            // (carried over all the chunks of a sequence: the more exact exponential)
+            if (lane == 31) {
+                s.decay = exp2f(eh);
+                s.valid = valid;
+                s.unit = unit;
+                s.seq = seq;
+                s.pos = pos;
+                s.flags = flags;
+                s.row = row;
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kScal + (i & 1)));
-            w.next(p, pl, list.nc);
+            if (lane == 0) mbar_arrive(bar(kScal + (i & (kRing - 1))));
         }
     } else {
         // ------------------------------------------------------------ compute
-        // rows: token (M, Y) or state row (S) 32 q + lane; columns: the half hf
-        const int q = warp & 3, hf = warp >> 2, r = 32 * q + lane;
-        const uint32_t lanes = tm + (static_cast<uint32_t>(32 * q) << 16);
-        const int srow = tid & (kL - 1), sh = tid >> 7;   // weighted rows: row and half
-        float S[32];
+        // rows: token (M, Y) or state row (S) 32 q + lane (the lanes of tensor
+        // memory that a warp reaches); columns: the cq-th quarter
+        const int q = warp & 3, cq = warp >> 2, r = 32 * q + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+        float S[kCols];
         const bool has = r < kN;
 
-        if (!kStates && hf == 0) {   // blocks above the diagonal stay zero
-            const uint32_t z[16] = {};
-            for (int b = q + 1; b < 4; ++b) {
-                tc::st16(lanes + kTmM + 16 * b, z);
-                tc::st16(lanes + kTmM + 64 + 16 * b, z);
-            }
-            tc::st_wait();
-        }
-        // this thread's 32 values in the state array
-        auto state_at = [&](const Walk &v) {
-            return ((static_cast<int64_t>(v.n) * p.heads + v.u / pl.slices) * kN + r) * p.p +
-                   (v.u % pl.slices) * kPS + 32 * hf;
+        // this thread's values in the state array
+        auto state_at = [&](const Scalars &v) {
+            return ((static_cast<int64_t>(v.seq) * p.heads + (v.unit >> pl.shift)) * kN + r) * p.p +
+                   (v.unit & pl.shift) * kPS + kCols * cq;
         };
         // ... and in the slots at the cuts
-        const int64_t slot = static_cast<int64_t>(c) * 32 * kCompute + tid;
+        const int64_t slot = static_cast<int64_t>(c) * kCols * kCompute + tid;
         // The state that enters chunk i of the run (its first, or a sequence's first).
-        auto start_state = [&](const Walk &v, int i) {
+        auto start_state = [&](const Scalars &v) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) S[j] = 0.f;
+            for (int j = 0; j < kCols; ++j) S[j] = 0.f;
             if (v.pos > 0) {
                 if (kStates) return;   // only what this part adds
                 // what the runs in front left of this sequence, the nearest first
                 const int64_t head = q0 - v.pos;
                 float f = 1.f;
                 for (int k = c - 1; k >= 0; --k) {
-                    const float *src = pl.slots + static_cast<int64_t>(k) * 32 * kCompute + tid;
+                    const float *src = pl.slots + static_cast<int64_t>(k) * kCols * kCompute + tid;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) S[j] = fmaf(src[j * kCompute], f, S[j]);
+                    for (int j = 0; j < kCols; ++j) S[j] = fmaf(src[j * kCompute], f, S[j]);
                     if (list.begin(k) <= head) break;
                     f *= pl.decay[k];
                 }
@@ -535,228 +690,257 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             if (p.s0 == nullptr) return;
             // in place, another CTA overwrites the initial state of a sequence
             // that the end of this run cuts: the first launch took a copy
-            const bool cut = q0 + i + (v.len + kL - 1) / kL > q1;
-            if (!kStates && pl.in_place && cut) {
+            if (!kStates && pl.in_place && (v.flags & kCut) != 0) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) S[j] = pl.saved[slot + j * kCompute];
+                for (int j = 0; j < kCols; ++j) S[j] = pl.saved[slot + j * kCompute];
                 return;
             }
             if (has) {
                 const float4 *src = reinterpret_cast<const float4 *>(p.s0 + state_at(v));
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < kCols / 4; ++j) {
                     const float4 f = src[j];
                     S[4 * j] = f.x; S[4 * j + 1] = f.y; S[4 * j + 2] = f.z; S[4 * j + 3] = f.w;
                 }
             }
             if (kStates && pl.in_place) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) pl.saved[slot + j * kCompute] = S[j];
+                for (int j = 0; j < kCols; ++j) pl.saved[slot + j * kCompute] = S[j];
             }
         };
         // S as two bf16 terms for C S
         auto put_state = [&]() {
-            if (!kStates && has) {
+            if (has) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 2; ++k) {
                     uint4 hi, lo;
                     hi.x = split2(S[8 * k], S[8 * k + 1], lo.x);
                     hi.y = split2(S[8 * k + 2], S[8 * k + 3], lo.y);
                     hi.z = split2(S[8 * k + 4], S[8 * k + 5], lo.z);
                     hi.w = split2(S[8 * k + 6], S[8 * k + 7], lo.w);
-                    const int at = r * 128 + (((4 * hf + k) ^ (r & 7)) << 4);
+                    const int at = r * 128 + (((2 * cq + k) ^ (r & 7)) << 4);
                     *reinterpret_cast<uint4 *>(smem + kOffS + at) = hi;
-                    *reinterpret_cast<uint4 *>(smem + kOffS + 16384 + at) = lo;
+                    *reinterpret_cast<uint4 *>(smem + kOffS + kTileBytes + at) = lo;
                 }
             }
-            fence_async();
-            mbar_arrive(bar(kSReady));
         };
-        // The weighted rows of chunk i as three bf16 terms. Rows past the end of
-        // the sequence belong to another one: they are zeroed here, as no weight
-        // of 0 makes an infinity or NaN vanish.
-        auto put_rows = [&](int i, int valid) {
-            uint8_t *X = smem + kOffX + (i & 1) * 16384, *W = smem + kOffW;
-            const float wt = scal[i & 1].to_end[srow];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int at = srow * 128 + (((4 * sh + k) ^ (srow & 7)) << 4);
+        // The weighted rows of chunk i as three bf16 terms, in 32 tasks of 32
+        // rows x 8 channels. The lower quarters of M have more blocks under the
+        // diagonal, so the upper quarters' warps take more tasks: 3, 2, 2, 1.
+        // Rows past the end of the sequence belong to another one: they are
+        // zeroed here, as no weight of 0 makes an infinity or NaN vanish.
+        const int tasks = kStates || q == 1 || q == 2 ? 2 : q == 0 ? 3 : 1;
+        const int task0 = (kStates ? 8 * q : q == 0 ? 0 : 4 + 8 * q) + cq * tasks;
+        auto put_rows = [&](int i) {
+            uint8_t *X = smem + kOffX + (i & 1) * kTileBytes, *W = smem + off_w(kStates, i);
+            const Scalars &s = scal[i & (kRing - 1)];
+            const int valid = s.valid;
+#pragma unroll 1
+            for (int k = task0; k < task0 + tasks; ++k) {
+                const int row = (k >> 3) * 32 + lane, at = row * 128 + (((k ^ row) & 7) << 4);
+                const float wt = s.to_end[row];
                 uint4 x = *reinterpret_cast<const uint4 *>(X + at);
-                if (srow >= valid) {
+                if (row >= valid) {
                     x = make_uint4(0, 0, 0, 0);
                     *reinterpret_cast<uint4 *>(X + at) = x;
 #pragma unroll
-                    for (int m = 0; m < kN / 64; ++m)
-                        *reinterpret_cast<uint4 *>(smem + kOffB + (i & 1) * 32768 + m * 16384 + at) = x;
+                    for (int z = 0; z < kN / 64; ++z)
+                        *reinterpret_cast<uint4 *>(smem + kOffB + (2 * (i & 1) + z) * kTileBytes + at) = x;
                 }
                 const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
                 uint32_t t0[4], t1[4], t2[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float2 v = unpack_bf16(xs[e]);
-                    mul2(v.x, v.y, wt, wt);
-                    t0[e] = pack_bf16(v.x, v.y);
-                    const float2 f = unpack_bf16(t0[e]);
-                    t1[e] = split2(v.x - f.x, v.y - f.y, t2[e]);
+                    float a = __uint_as_float(xs[e] << 16), b = __uint_as_float(xs[e] & 0xffff0000u);
+                    mul2(a, b, wt, wt);
+                    t0[e] = take2(a, b);
+                    t1[e] = split2(a, b, t2[e]);
                 }
                 *reinterpret_cast<uint4 *>(W + at) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
-                *reinterpret_cast<uint4 *>(W + 16384 + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-                *reinterpret_cast<uint4 *>(W + 32768 + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+                *reinterpret_cast<uint4 *>(W + kTileBytes + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                *reinterpret_cast<uint4 *>(W + 2 * kTileBytes + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
             }
             fence_async();
-            mbar_arrive(bar(kWReady));
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(kWReady));
+                if (!kStates) mbar_arrive(bar(kSReady));   // put_state's stores come before
+            }
+        };
+        auto landed = [&](int i) {
+            return wait(kScal + (i & (kRing - 1)), i / kRing) && wait(kFullBX + (i & 1), i >> 1);
         };
 
         float run_decay = 1.f;   // over this part of the sequence
-        start_state(w, 0);
-        put_state();
-        bool ok = wait(kScal, 0) && wait(kFullBX, 0);
-        if (ok) put_rows(0, w.valid());
-        for (int i = 0; ok && i < count; ++i) {
-            const Scalars &s = scal[i & 1];
-            const int valid = w.valid();
-            if (!kStates) {
-                // ---- M = (C B^T) . decay, two bf16 terms
+        bool ok = true;
+#pragma unroll 1
+        for (int i = -1; i < count; ++i) {
+            const Scalars &s = scal[i & (kRing - 1)];
+            const bool more = i + 1 < count;
+            if (kStates && more) {   // into the other set of weighted rows
+                if (!(ok = landed(i + 1))) break;
+                put_rows(i + 1);
+            }
+            if (!kStates && i >= 0) {
+                // ---- M = (C B^T) . decay, two bf16 terms: one 32-token block
                 if (!(ok = wait(kCB, i))) break;
                 tc::fence_after();
-                const float hi_r = s.hi[r], lo_r = s.lo[r];
-                for (int b = hf; b <= q; b += 2) {
-                    uint32_t v[2][16];
-                    tc::ld16(lanes + kTmCB + 32 * b, v[0]);
-                    tc::ld16(lanes + kTmCB + 32 * b + 16, v[1]);
-                    tc::ld_wait();
-                    uint32_t hi[16], lo[16];
-                    if (b < q) {
-                        const float f = ex2((hi_r - s.end_hi[b]) + (lo_r - s.end_lo[b]));
+                if (cq > q) {   // above the diagonal
+                    const uint32_t z[16] = {};
+                    tc::st16(lanes + kTmCB + 32 * cq, z);
+                    tc::st16(lanes + kTmCB + 32 * cq + 16, z);
+                } else {
+                    const float hi_r = -s.hi[r], lo_r = -s.lo[r];
+                    const float f = cq < q ? ex2((hi_r - s.end_hi[cq]) + (lo_r - s.end_lo[cq])) : 0.f;
+#pragma unroll 1
+                    for (int col = 32 * cq; col < 32 * cq + 32; col += 16) {
+                        uint32_t v[16];
+                        tc::ld16(lanes + kTmCB + col, v);
+                        tc::ld_wait();
+                        uint32_t hi[8], lo[8];
+                        if (cq < q) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const float4 e = *reinterpret_cast<const float4 *>(s.to_block + 32 * b + j);
-                            float m0 = __uint_as_float(v[j >> 4][j & 15]);
-                            float m1 = __uint_as_float(v[j >> 4][(j & 15) + 1]);
-                            float m2 = __uint_as_float(v[j >> 4][(j & 15) + 2]);
-                            float m3 = __uint_as_float(v[j >> 4][(j & 15) + 3]);
-                            mul2(m0, m1, f, f);
-                            mul2(m2, m3, f, f);
-                            mul2(m0, m1, e.x, e.y);
-                            mul2(m2, m3, e.z, e.w);
-                            hi[j / 2] = split2(m0, m1, lo[j / 2]);
-                            hi[j / 2 + 1] = split2(m2, m3, lo[j / 2 + 1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            const int t = 32 * b + j;
-                            const float4 gh = *reinterpret_cast<const float4 *>(s.hi + t);
-                            const float4 gl = *reinterpret_cast<const float4 *>(s.lo + t);
-                            const float4 d = *reinterpret_cast<const float4 *>(s.dt + t);
-                            const float ghs[4] = {gh.x, gh.y, gh.z, gh.w}, gls[4] = {gl.x, gl.y, gl.z, gl.w};
-                            const float ds[4] = {d.x, d.y, d.z, d.w};
-                            float m[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float x = __uint_as_float(v[j >> 4][(j & 15) + e]);
-                                m[e] = j + e <= lane
-                                           ? x * (ex2((hi_r - ghs[e]) + (lo_r - gls[e])) * ds[e]) : 0.f;
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 e = *reinterpret_cast<const float4 *>(s.to_block + col + j);
+                                float x[4] = {__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
+                                              __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])};
+                                mul2(x[0], x[1], f, f);
+                                mul2(x[2], x[3], f, f);
+                                mul2(x[0], x[1], e.x, e.y);
+                                mul2(x[2], x[3], e.z, e.w);
+                                hi[j / 2] = split2(x[0], x[1], lo[j / 2]);
+                                hi[j / 2 + 1] = split2(x[2], x[3], lo[j / 2 + 1]);
                             }
-                            hi[j / 2] = split2(m[0], m[1], lo[j / 2]);
-                            hi[j / 2 + 1] = split2(m[2], m[3], lo[j / 2 + 1]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                float4 a = *reinterpret_cast<const float4 *>(s.hi + col + j);
+                                float4 g = *reinterpret_cast<const float4 *>(s.lo + col + j);
+                                const float4 d = *reinterpret_cast<const float4 *>(s.dt + col + j);
+                                add2(a.x, a.y, hi_r, hi_r);
+                                add2(a.z, a.w, hi_r, hi_r);
+                                add2(g.x, g.y, lo_r, lo_r);
+                                add2(g.z, g.w, lo_r, lo_r);
+                                add2(a.x, a.y, g.x, g.y);
+                                add2(a.z, a.w, g.z, g.w);
+                                float x[4] = {ex2(a.x), ex2(a.y), ex2(a.z), ex2(a.w)};
+                                mul2(x[0], x[1], d.x, d.y);
+                                mul2(x[2], x[3], d.z, d.w);
+                                mul2(x[0], x[1], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                                mul2(x[2], x[3], __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (col + j + e > r) x[e] = 0.f;
+                                hi[j / 2] = split2(x[0], x[1], lo[j / 2]);
+                                hi[j / 2 + 1] = split2(x[2], x[3], lo[j / 2 + 1]);
+                            }
                         }
+                        tc::st8(lanes + kTmCB + col, hi);
+                        tc::st8(lanes + kTmCB + col + 8, lo);
                     }
-                    tc::st16(lanes + kTmM + 16 * b, hi);
-                    tc::st16(lanes + kTmM + 64 + 16 * b, lo);
                 }
                 tc::st_wait();
                 tc::fence_before();
-                mbar_arrive(bar(kMReady));
+                arrive(kMReady);
             }
-
-            // ---- S = 2^G_last S + B^T (W X)
-            if (!(ok = wait(kCSDS, i))) break;
-            tc::fence_after();
-            if (has) {
-                uint32_t v[2][16];
-                tc::ld16(lanes + kTmDS + 32 * hf, v[0]);
-                tc::ld16(lanes + kTmDS + 32 * hf + 16, v[1]);
-                tc::ld_wait();
+            if (i >= 0) {
+                // ---- S = 2^G_last S + B^T (W X)
+                if (!(ok = wait(kDS, i))) break;
                 const float dec = s.decay;
+                if (has) {
+                    tc::fence_after();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) S[j] = fmaf(S[j], dec, __uint_as_float(v[j >> 4][j & 15]));
-            }
-            tc::fence_before();
-            run_decay *= s.decay;
-            if (kStates) mbar_arrive(bar(kDone));
-            const bool ends = w.last();
-            if (!kStates && ends && p.s_final != nullptr && has) {
-                float4 *dst = reinterpret_cast<float4 *>(p.s_final + state_at(w));
+                    for (int k = 0; k < 2; ++k) {   // 8 columns at a time
+                        uint32_t v[3][8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    dst[j] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+                        for (int t = 0; t < 3; ++t)
+                            ld8(lanes + tm_ds(kStates, i) + kPS * t + kCols * cq + 8 * k, v[t]);
+                        tc::ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {   // the smallest term first
+                            float a = __uint_as_float(v[2][j]), b = __uint_as_float(v[2][j + 1]);
+                            add2(a, b, __uint_as_float(v[1][j]), __uint_as_float(v[1][j + 1]));
+                            add2(a, b, __uint_as_float(v[0][j]), __uint_as_float(v[0][j + 1]));
+                            fma2(S[8 * k + j], S[8 * k + j + 1], dec, dec, a, b);
+                        }
+                    }
+                    tc::fence_before();
+                }
+                run_decay *= dec;
+                if (kStates) {
+                    arrive(kFreeBX + (i & 1));
+                    arrive(kScFree + (i & (kRing - 1)));
+                }
             }
-            const Walk now = w;
-            if (i + 1 < count) {
-                w.next(p, pl, list.nc);
-                if (w.pos == 0) start_state(w, i + 1);
-                put_state();
-                if (!(ok = wait(kScal + ((i + 1) & 1), (i + 1) >> 1) &&
-                           wait(kFullBX + ((i + 1) & 1), (i + 1) >> 1)))
-                    break;
-                put_rows(i + 1, w.valid());
+            if (!kStates && i >= 0 && (s.flags & kLast) != 0 && p.s_final != nullptr && has) {
+                float4 *out = reinterpret_cast<float4 *>(p.s_final + state_at(s));
+#pragma unroll
+                for (int j = 0; j < kCols / 4; ++j)
+                    out[j] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
             }
-
-            if (!kStates) {
+            if (more && (!kStates || i < 0)) {
+                const Scalars &t = scal[(i + 1) & (kRing - 1)];
+                if (!kStates && !(ok = landed(i + 1))) break;
+                if (i < 0 || t.pos == 0) start_state(t);   // (kStates: landed above)
+                if (!kStates) {
+                    if (i >= 0 && !(ok = wait(kCS, i))) break;   // the terms of S are read
+                    put_state();
+                    put_rows(i + 1);
+                }
+            }
+            if (!kStates && i >= 0) {
                 // ---- y = 2^G (C S) + M X + d x
+                const int h = s.unit >> pl.shift;
+                const float from = s.from[r], dv = p.d != nullptr ? __ldg(p.d + h) : 0.f;
+                const bool live = r < s.valid;
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                                       ((s.row + r) * p.heads + h) * p.p +
+                                                       (s.unit & pl.shift) * kPS + kCols * cq);
                 if (!(ok = wait(kMX, i))) break;
                 tc::fence_after();
-                uint32_t y[2][16], cs[2][16];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    tc::ld16(lanes + kTmY + 32 * hf + 16 * k, y[k]);
-                    tc::ld16(lanes + kTmCS + 32 * hf + 16 * k, cs[k]);
-                }
-                tc::ld_wait();
-                tc::fence_before();
-                const int h = now.u / pl.slices;
-                const float from = s.from[r], dv = p.d != nullptr ? __ldg(p.d + h) : 0.f;
-                uint4 o[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(
-                        smem + kOffX + (i & 1) * 16384 + r * 128 + (((4 * hf + k) ^ (r & 7)) << 4));
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {   // 8 columns at a time
+                    uint32_t y[8], c0[8], c1[8];
+                    ld8(lanes + kTmY + kCols * cq + 8 * k, y);
+                    ld8(lanes + kTmCS + kCols * cq + 8 * k, c0);
+                    ld8(lanes + kTmCS + kPS + kCols * cq + 8 * k, c1);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(smem + kOffX + (i & 1) * kTileBytes + r * 128 +
+                                                                     (((2 * cq + k) ^ (r & 7)) << 4));
+                    tc::ld_wait();
                     const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
                     uint32_t os[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int j = 8 * k + 2 * e;
-                        const float2 f = unpack_bf16(xs[e]);
-                        os[e] = pack_bf16(
-                            fmaf(dv, f.x, fmaf(from, __uint_as_float(cs[j >> 4][j & 15]),
-                                               __uint_as_float(y[j >> 4][j & 15]))),
-                            fmaf(dv, f.y, fmaf(from, __uint_as_float(cs[j >> 4][(j & 15) + 1]),
-                                               __uint_as_float(y[j >> 4][(j & 15) + 1]))));
+                        float a = __uint_as_float(c0[2 * e]), b = __uint_as_float(c0[2 * e + 1]);
+                        add2(a, b, __uint_as_float(c1[2 * e]), __uint_as_float(c1[2 * e + 1]));
+                        fma2(a, b, from, from, __uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
+                        float f = __uint_as_float(xs[e] << 16), g = __uint_as_float(xs[e] & 0xffff0000u);
+                        fma2(f, g, dv, dv, a, b);
+                        os[e] = pack_bf16(f, g);
                     }
-                    o[k] = make_uint4(os[0], os[1], os[2], os[3]);
+                    if (live) dst[k] = make_uint4(os[0], os[1], os[2], os[3]);
                 }
-                mbar_arrive(bar(kDone));
-                if (r < valid) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(
-                        static_cast<__nv_bfloat16 *>(p.out) + ((now.row() + r) * p.heads + h) * p.p +
-                        (now.u % pl.slices) * kPS + 32 * hf);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) dst[k] = o[k];
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(kDone));
+                    mbar_arrive(bar(kFreeBX + (i & 1)));
+                    mbar_arrive(bar(kScFree + (i & (kRing - 1))));
                 }
             }
         }
         if (kStates && ok) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) pl.slots[slot + j * kCompute] = has ? S[j] : 0.f;
+            for (int j = 0; j < kCols; ++j) pl.slots[slot + j * kCompute] = has ? S[j] : 0.f;
             if (tid == 0) pl.decay[c] = run_decay;
         }
     }
     tc::fence_before();
     __syncthreads();
+    if (tid == 0 && s_abort != 0) atomicOr(p.err, kErrTimeout);
     if (warp == 0) {
         tc::fence_after();
-        tc::dealloc(tm, kTmCols);
+        tc::dealloc(0, kTmCols);
     }
 }
 
@@ -786,7 +970,7 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // Workspace: [chunk offsets (packed)][decays][states at the cuts][copies of
 // initial states (in place)].
-constexpr int64_t kSlotBytes = 32 * kCompute * 4;
+constexpr int64_t kSlotBytes = static_cast<int64_t>(kCols) * kCompute * 4;
 int64_t offsets_bytes(const SsmParams &p) {
     return p.cu != nullptr ? align256((static_cast<int64_t>(p.n_seqs) + 1) * 4) : 0;
 }
@@ -823,8 +1007,8 @@ cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t 
         return cudaErrorInvalidValue;
     SsmPlan pl{};
     uint8_t *ws = ctx.ws;
-    pl.slices = p.p / kPS;
-    pl.units = static_cast<int64_t>(p.heads) * pl.slices;
+    pl.shift = p.p / kPS - 1;
+    pl.units = static_cast<int64_t>(p.heads) << pl.shift;
     pl.cps = static_cast<int>((p.seq_len + kL - 1) / kL);
     pl.decay = reinterpret_cast<float *>(ws + offsets_bytes(p));
     pl.slots = reinterpret_cast<float *>(ws + offsets_bytes(p) + 1024);
