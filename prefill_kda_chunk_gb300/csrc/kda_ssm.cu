@@ -51,10 +51,34 @@ __device__ __forceinline__ float bf16_at(const void *p, int64_t i) {
     return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
 }
 
-__device__ __forceinline__ float delta_of(float v, bool softplus) {
-    // log(1 + e^v) without overflow, and exact for large negative v
-    return softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
+
+// log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| <= 1, to a few units of the
+// last place at every v (the state is linear in it). e^-|v|: the rounding error
+// of |v| log2(e) is put back to first order. log(1 + e) = 2 atanh z with
+// z = e / (2 + e) <= 1/3, whose series z (1 + z^2/3 + ... + z^16/17) ends at
+// 3^-18/19 = 1.4e-10 and keeps the relative precision of small e.
+__device__ __forceinline__ float softplus(float v) {
+    const float x = -fabsf(v), t = x * 1.44269504f;
+    const float r = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;   // log2(e) - 1.44269504f
+    const float e2 = ex2(t), e = fmaf(e2 * 0.69314718f, r, e2);
+    const float z = __fdividef(e, 2.f + e), q = z * z;
+    float s = 1.f / 17.f;
+    s = fmaf(s, q, 1.f / 15.f);
+    s = fmaf(s, q, 1.f / 13.f);
+    s = fmaf(s, q, 1.f / 11.f);
+    s = fmaf(s, q, 1.f / 9.f);
+    s = fmaf(s, q, 1.f / 7.f);
+    s = fmaf(s, q, 1.f / 5.f);
+    s = fmaf(s, q, 1.f / 3.f);
+    const float l = 2.f * fmaf(z * q, s, z);
+    return v > 0.f ? v + l : l;
+}
+__device__ __forceinline__ float delta_of(float v, bool plus) { return plus ? softplus(v) : v; }
 
 // ------------------------------------------------------------- one token
 
@@ -100,13 +124,15 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p) {
 constexpr int kL = 128;              // tokens per chunk
 constexpr int kPS = 64;              // channels of P per unit
 constexpr int kSsmSms = 152;
-constexpr int kWarpsC = 16;          // compute warps
-constexpr int kCompute = 32 * kWarpsC;
-// after them one warp for the MMAs, one for the copies and two for the decays
-constexpr int kMmaWarp = kWarpsC, kCopyWarp = kMmaWarp + 1, kScalWarp = kMmaWarp + 2;
-constexpr int kThreads = 32 * (kScalWarp + 2);
+// Warps: 0..7 form M and the outputs, 8..15 keep the state, then one for the
+// MMAs of the state, one for those of y, one for the copies and one for the decays.
+constexpr int kGroup = 8;
+constexpr int kGroupThreads = 32 * kGroup;
+constexpr int kMmaWarpS = 2 * kGroup, kMmaWarpY = kMmaWarpS + 1, kCopyWarp = kMmaWarpS + 2,
+              kScalWarp = kMmaWarpS + 3;
+constexpr int kThreads = 32 * (kScalWarp + 1);
 constexpr int kRing = 4;             // chunks of decays computed ahead
-constexpr int kCols = 16;            // columns of the state and of y per compute thread
+constexpr int kCols = 32;            // columns of the state and of y per compute thread
 
 // Shared memory, from a 1024-byte boundary. Tiles of 128-byte rows with the
 // 16-byte granule index XOR-ed by the row's low three bits.
@@ -117,7 +143,7 @@ constexpr int kOffB = kOffS + 2 * kTileBytes;    // two buffers of [n / 64][128 
 constexpr int kOffX = kOffB + 4 * kTileBytes;    // two buffers of [128 tokens][64]
 constexpr int kOffW = kOffX + 2 * kTileBytes;    // three terms of the weighted rows
 constexpr int kOffSc = kOffW + 3 * kTileBytes;   // kRing buffers of Scalars
-struct Scalars {
+struct alignas(16) Scalars {   // (read in 16-byte pieces)
     float hi[kL], lo[kL];   // -G_t as a sum of two floats, in units of log 2
     float dt[kL];           // delta_t; 0 past the sequence's end
     float to_block[kL];     // 2^(G at the end of t's 32-block - G_t) delta_t
@@ -130,26 +156,31 @@ struct Scalars {
     int unit, seq, pos;     // head and slice; sequence; chunk of the sequence
     int flags;              // kLast, kCut
     int64_t row;            // its first token
+    int xcol, gcol;         // its first column of x, and of b and c
 };
 enum { kLast = 1, kCut = 2 };   // the sequence's last chunk; the run's end cuts the sequence
 constexpr int kOffBar = kOffSc + kRing * static_cast<int>(sizeof(Scalars));
-enum {   // barriers, 8 bytes each
+enum {   // barriers, 8 bytes each; pairs and the ring by the chunk's index
     // phases that one thread or a copy completes
-    kFullC, kFullBX, kScal = kFullBX + 2, kCB = kScal + kRing, kDS, kCS, kMX, kDrain,
-    // phases that every compute warp arrives at
-    kMReady, kSReady, kWReady, kDone, kFreeBX, kScFree = kFreeBX + 2, kBars = kScFree + kRing
+    kFullC, kFullB, kFullX = kFullB + 2, kScal = kFullX + 2, kCB = kScal + kRing, kDS = kCB + 2,
+    kCS = kDS + 2, kMX = kCS + 2, kDrain = kMX + 2, kDrain2,
+    // phases that the warps of a group arrive at
+    kMReady, kSReady = kMReady + 2, kXReady, kDone = kXReady + 2,
+    // ... the state's, and in the launch for the states both
+    kWReady = kDone + 2,
+    // ... both (the launch for the states: the state's)
+    kScFree, kBars = kScFree + kRing
 };
 constexpr int kOffMisc = kOffBar + 8 * kBars;    // tensor memory base, abort flag
 constexpr int kSmem = kOffMisc + 8;
 
-// Tensor memory columns; the block takes all of them, so they start at 0. M
-// replaces C B^T: 16 columns (tokens s) become the 8 columns of its high terms
-// and the 8 of its low terms. The terms of S and of W X lie side by side along N,
-// so that one MMA reads C (or B) for all of them; their products are added when
-// they are read. The launch for the states works on two chunks at a time.
-constexpr uint32_t kTmCB = 0, kTmY = 128, kTmCS = 192, kTmDS = 320, kTmCols = 512;
+// Tensor memory columns; the block takes all of them, so they start at 0. C B^T has
+// two buffers of 128; M replaces it there: 16 columns (tokens s) become the 8 columns
+// of its high terms and the 8 of its low terms. C S has two buffers of 64. The launch
+// for the states works on two chunks at a time.
+constexpr uint32_t kTmCB = 0, kTmY = 256, kTmCS = 320, kTmDS = 448, kTmCols = 512;
 __device__ __forceinline__ uint32_t tm_ds(bool states, int i) {
-    return states ? 256u * (i & 1) : kTmDS;
+    return states ? 64u * (i & 1) : kTmDS;
 }
 // The weighted rows of chunk i; the launch for the states has two sets.
 __device__ __forceinline__ int off_w(bool states, int i) {
@@ -168,32 +199,30 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) {
     return ((saddr >> 4) & 0x3FFF) | (static_cast<uint32_t>(kTileBytes >> 4) << 16);
 }
 
-// One MMA, issued by the lane with `one` set. The whole warp runs the code around
-// it, so that descriptors stay in uniform registers (issued from a branch of a
-// single lane each MMA took 2 to 3 times as long).
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc,
-                                       uint32_t one) {
+// One MMA: D (+)= A B with both operands in shared memory, or A in tensor memory,
+// and the commit of those before it. The whole warp calls them and the instruction
+// elects a lane: descriptors then stay in uniform registers. (In a branch of one lane
+// an MMA of N = 64 took 77 cycles in a loop and 52 unrolled, this way 48 and 40.)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p, q;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " mov.b64 x, {%1, %6};\n mov.b64 y, {%2, %6};\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(one), "r"(kDescHi)
+        "{\n .reg .pred p, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc,
-                                       uint32_t one) {
+// (with A in tensor memory the elected form took 300 cycles: one lane calls this)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p, q;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-        " mov.b64 y, {%2, %6};\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(one), "r"(kDescHi)
+        "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi)
         : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar, uint32_t one) {
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
-        " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
-        "r"(one)
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
         : "memory");
 }
 
@@ -214,12 +243,6 @@ __device__ __forceinline__ void prefetch_2d(const CUtensorMap *map, int x, int y
 
 __device__ __forceinline__ void fence_async() {
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // packed fp32 pairs: (a, b) += (x, y), (a, b) = (a, b) * (x, y) + (u, v)
@@ -266,17 +289,36 @@ __device__ __forceinline__ void ld8(uint32_t taddr, uint32_t (&r)[8]) {
                  : "r"(taddr));
 }
 
+// Waits for this thread's tensor memory loads and hands on the registers of one of
+// them, so that no use (or copy) of them moves in front of the wait.
+__device__ __forceinline__ void ld_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 // A wait of at most 2^31 clocks (about a second) for a phase of an mbarrier, in
 // few instructions: this kernel waits in some twenty places, and with longer
 // waits at each of them its loops did not fit the instruction cache (a chunk
 // then took 3 times as long).
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
     const uint32_t t0 = static_cast<uint32_t>(clock());
+    bool ok;
 #pragma unroll 1
     do {
-        if (mbar_try_wait(bar, parity)) return true;
-    } while (static_cast<uint32_t>(clock()) - t0 < 0x80000000u);
-    return false;
+        // (suspended by the hardware for up to a millisecond: warps that poll would
+        // take the issue slots of those that work)
+        uint32_t r;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(r) : "r"(bar), "r"(parity), "r"(1000000u) : "memory");
+        ok = r != 0;
+    } while (!ok && static_cast<int>(static_cast<uint32_t>(clock()) - t0) >= 0);
+    return ok;
 }
 
 struct SsmMaps {
@@ -290,7 +332,7 @@ struct SsmPlan {
     const int32_t *chunk_off;  // packed: first chunk of each sequence [N + 1]
     const int *call_flags;     // packed: set by the prologue
     int64_t gran;              // chunks that stay together; 0: all of a unit's
-    float *slots;              // [G][kCols][kCompute] states at the cuts
+    float *slots;              // [G][kCols][kGroupThreads] states at the cuts
     float *saved;              // the same: initial states that a cut run starts from (in place)
     float *decay;              // [G]
     bool in_place;
@@ -392,8 +434,10 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
     extern __shared__ __align__(1024) uint8_t smem[];
     volatile int &s_abort = *reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
     if (pl.call_flags != nullptr && (*pl.call_flags & kErrBadCu) != 0) return;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (!kStates && tid < kCompute) hand_on<kN>(p, tid, kCompute);
+    // (the shuffle tells the compiler that a warp's index is uniform: without it, it
+    // guards every MMA's registers against lanes that differ, 32 instructions each)
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+    if (!kStates && tid < kGroupThreads) hand_on<kN>(p, tid, kGroupThreads);
     const List list(p, pl);
     const int c = blockIdx.x;
     if (c >= list.G) return;
@@ -414,7 +458,10 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
 
     if (tid == 0) {
         s_abort = (sb & 1023) != 0;   // (the tiles' swizzle counts on it)
-        for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i < kMReady ? 1 : kWarpsC);
+        for (int i = 0; i < kBars; ++i) 
+            mbar_init(bar(i), i == kDrain2 ? 2 : i < kMReady ? 1
+                              : i == kWReady ? (kStates ? 2 * kGroup : kGroup)
+                              : i >= kScFree ? (kStates ? kGroup : 2 * kGroup) : kGroup);
         mbar_fence_init();
     }
     if (warp == 0) {
@@ -425,12 +472,11 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
     __syncthreads();
     tc::fence_after();
 
-    // A bounded wait; once one has run out, all of them give up.
+    // A bounded wait; a role whose wait has run out stops.
     auto wait = [&](int i, int phase) -> bool {
-        if (mbar_try_wait(bar(i), phase & 1)) return true;
-        if (s_abort == 0 && wait_phase(bar(i), phase & 1)) return true;
-        s_abort = 1;
-        return false;
+        const bool ok = wait_phase(bar(i), phase & 1);
+        if (!ok) s_abort = 1;
+        return ok;
     };
     auto arrive = [&](int i) {   // one arrival per warp
         __syncwarp();
@@ -440,175 +486,237 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
     Walk w;
     w.go(p, pl, list.nc, q0);
 
-    if (warp == kMmaWarp) {
-        // ------------------------------------------------------------ MMAs
-        const uint32_t one = lane == 0;
-        // k-steps of 16: 32 bytes along a row, or 16 rows of 128 bytes
-        constexpr uint32_t kStepK = 32 >> 4, kStepMN = 2048 >> 4, kTile = kTileBytes >> 4;
-        const uint32_t C = desc_lo(sb + kOffC);
-        const uint32_t S = desc_lo(sb + kOffS);
-        auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
-        // C B^T of chunk i
-        auto issue_cb = [&](int i) {
-            const uint32_t BK = desc_lo(sb + kOffB) + 2 * kTile * (i & 1);
-#pragma unroll
-            for (int k = 0; k < kN / 16; ++k)
-                mma_ss(kTmCB, C + (k >> 2) * kTile + (k & 3) * kStepK, BK + (k >> 2) * kTile + (k & 3) * kStepK,
-                       tc::idesc(128, 128, 1), k > 0, one);
-            commit(bar(kCB), one);
-        };
+    // k-steps of 16: 32 bytes along a row, or 16 rows of 128 bytes
+    constexpr uint32_t kStepK = 32 >> 4, kStepMN = 2048 >> 4, kTile = kTileBytes >> 4;
+    // after a wait that gave up: let the MMAs that this warp issued end (C B^T and M X
+    // by two lanes of it)
+    auto drain = [&](int i) {
+        __syncwarp();
+        if (s_abort != 0) {
+            mma_commit(bar(i));
+            if (i == kDrain2 && lane == 0) tc::commit(bar(i));
+            wait_phase(bar(i), 0);
+        }
+    };
+    auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
+    // The weighted rows of chunk i as three bf16 terms, in 32 tasks of 32
+    // rows x 8 channels, Rows past the end of the sequence belong to
+    // another one: they are zeroed here, as no weight of 0 makes an infinity or NaN
+    // vanish. (With two groups each takes 16 of the tasks.)
+    auto put_rows = [&](int i, int task0, int tasks) {
+        uint8_t *X = smem + kOffX + (i & 1) * kTileBytes, *W = smem + off_w(kStates, i);
+        const Scalars &s = scal[i & (kRing - 1)];
+        const int valid = s.valid;
 #pragma unroll 1
-        for (int i = kStates ? 0 : -1; i < count; ++i) {
-            const int par = __shfl_sync(0xffffffffu, i & 1, 0);
-            if (i >= 0) {
-                // B^T (W X), the three terms of W X along N (for n = 64 the upper 64
-                // rows are formed from whatever lies there and are not read)
-                if (!all(wait(kWReady, i) && (!kStates || wait(kFullBX + (i & 1), i >> 1)))) break;
-                tc::fence_after();
-                const uint32_t BM = desc_lo(sb + kOffB) + 2 * kTile * par;
-                const uint32_t W = desc_lo(sb + (kStates && par != 0 ? kOffC : kOffW));
+        for (int k0 = task0; k0 < task0 + tasks; k0 += 2) {
+            uint4 xv[2];
+            float wts[2];
+            int ats[2];
 #pragma unroll
-                for (int k = 0; k < kL / 16; ++k)
-                    mma_ss(kStates ? 256 * par : kTmDS, BM + k * kStepMN, W + k * kStepMN,
-                           tc::idesc(128, 3 * kPS, 1) | kAMajor | kBMajor, k > 0, one);
-                commit(bar(kDS), one);
-                if (!kStates) {
-                    // C S, both terms of S along N, once the chunk before is read out
-                    if (!all(wait(kSReady, i) && (i == 0 || wait(kDone, i - 1)))) break;
-                    tc::fence_after();
+            for (int m = 0; m < 2; ++m) {   // two tasks side by side
+                const int k = k0 + m, row = (k >> 3) * 32 + lane, at = row * 128 + (((k ^ row) & 7) << 4);
+                wts[m] = s.to_end[row];
+                ats[m] = at;
+                xv[m] = *reinterpret_cast<const uint4 *>(X + at);
+                if (row >= valid) {
+                    xv[m] = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(X + at) = xv[m];
 #pragma unroll
-                    for (int k = 0; k < kN / 16; ++k)
-                        mma_ss(kTmCS, C + (k >> 2) * kTile + (k & 3) * kStepK, S + k * kStepMN,
-                               tc::idesc(128, 2 * kPS, 1) | kBMajor, k > 0, one);
-                    commit(bar(kCS), one);
-                    // M X, both terms of M along K
-                    if (!all(wait(kMReady, i))) break;
-                    tc::fence_after();
-                    const uint32_t X = desc_lo(sb + kOffX) + kTile * par;
-#pragma unroll
-                    for (int k = 0; k < kL / 8; ++k)
-                        mma_ts(kTmY, kTmCB + 8 * k, X + (k >> 1) * kStepMN, tc::idesc(128, kPS, 1) | kBMajor,
-                               k > 0, one);
-                    commit(bar(kMX), one);
+                    for (int z = 0; z < kN / 64; ++z)
+                        *reinterpret_cast<uint4 *>(smem + kOffB + (2 * (i & 1) + z) * kTileBytes + at) = xv[m];
                 }
             }
-            if (!kStates && i + 1 < count) {
-                // C B^T of the next chunk, over M of this one
-                if (!all(wait(kFullBX + ((i + 1) & 1), (i + 1) >> 1) && wait(kFullC, i + 1) &&
-                         (i < 0 || wait(kMX, i))))
-                    break;
-                tc::fence_after();
-                issue_cb(__shfl_sync(0xffffffffu, i + 1, 0));
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const uint32_t xs[4] = {xv[m].x, xv[m].y, xv[m].z, xv[m].w};
+                uint32_t t0[4], t1[4], t2[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float a = __uint_as_float(xs[e] << 16), b = __uint_as_float(xs[e] & 0xffff0000u);
+                    mul2(a, b, wts[m], wts[m]);
+                    t0[e] = take2(a, b);
+                    t1[e] = split2(a, b, t2[e]);
+                }
+                *reinterpret_cast<uint4 *>(W + ats[m]) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+                *reinterpret_cast<uint4 *>(W + kTileBytes + ats[m]) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                *reinterpret_cast<uint4 *>(W + 2 * kTileBytes + ats[m]) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
             }
         }
-        if (s_abort != 0) {   // after a wait that gave up: let what was issued end
-            commit(bar(kDrain), one);
-            wait_phase(bar(kDrain), 0);
-        }
+        fence_async();
         __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(bar(kWReady));
+            mbar_arrive(bar(kXReady + (i & 1)));
+        }
+    };
+    auto landed = [&](int i) {
+        return wait(kScal + (i & (kRing - 1)), i / kRing) && wait(kFullB + (i & 1), i >> 1) && wait(kFullX + (i & 1), i >> 1);
+    };
+    if (warp == kMmaWarpS) {
+        // ------------------------------------------- MMAs: B^T (W X) and C S
+#pragma unroll 1
+        for (int i = 0; i < count; ++i) {
+            // B^T (W X) (for n = 64 the upper 64 rows are formed from whatever lies
+            // there and are not read)
+            if (!all(wait(kFullB + (i & 1), i >> 1) && wait(kWReady, i))) break;
+            tc::fence_after();
+            const uint32_t B = desc_lo(sb + kOffB) + 2 * kTile * (i & 1);
+            const uint32_t W = desc_lo(sb + off_w(kStates, i)), D = tm_ds(kStates, i);
+#pragma unroll
+            for (int k = 0; k < 3 * kL / 16; ++k) {   // the smallest term first
+                const int j = k % (kL / 16), t = 2 - k / (kL / 16);
+                mma_ss(D, B + j * kStepMN, W + t * kTile + j * kStepMN,
+                       tc::idesc(128, kPS, 1) | kAMajor | kBMajor, k);
+            }
+            mma_commit(bar(kDS + (i & 1)));
+            if (!kStates) {
+                // C S, both terms of S, over that of two chunks before
+                if (!all(wait(kSReady, i) && wait(kFullC, i) &&
+                         (i < 2 || wait(kDone + (i & 1), (i >> 1) - 1))))
+                    break;
+                tc::fence_after();
+                const uint32_t C = desc_lo(sb + kOffC), S = desc_lo(sb + kOffS);
+#pragma unroll
+                for (int k = 0; k < kN / 8; ++k) {
+                    const int j = k % (kN / 16);
+                    mma_ss(kTmCS + 64 * (i & 1), C + (j >> 2) * kTile + (j & 3) * kStepK,
+                           S + k / (kN / 16) * kTile + j * kStepMN, tc::idesc(128, kPS, 1) | kBMajor, k);
+                }
+                mma_commit(bar(kCS + (i & 1)));
+            }
+        }
+        drain(kDrain);
+    } else if (warp == kMmaWarpY) {
+        // --------------------------------------------- MMAs: C B^T and M X
+#pragma unroll 1
+        for (int i = -1; !kStates && i < count; ++i) {
+            if (i + 1 < count) {
+                // C B^T of the next chunk, over M of the one before this
+                if (!all(wait(kFullB + ((i + 1) & 1), (i + 1) >> 1) && wait(kFullC, i + 1) &&
+                         (i < 1 || wait(kMX + ((i - 1) & 1), (i - 1) >> 1))))
+                    break;
+                tc::fence_after();
+                const uint32_t B = desc_lo(sb + kOffB) + 2 * kTile * ((i + 1) & 1), C = desc_lo(sb + kOffC);
+                const uint32_t D = kTmCB + 128 * ((i + 1) & 1);
+#pragma unroll
+                for (int k = 0; k < kN / 16; ++k)
+                    mma_ss(D, C + (k >> 2) * kTile + (k & 3) * kStepK, B + (k >> 2) * kTile + (k & 3) * kStepK,
+                           tc::idesc(128, 128, 1), k);
+                mma_commit(bar(kCB + ((i + 1) & 1)));
+            }
+            if (i < 0) continue;
+            // M X, both terms of M along K, once the chunk before is read out
+            if (!all(wait(kMReady + (i & 1), i >> 1) && wait(kFullX + (i & 1), i >> 1) &&
+                     wait(kXReady + (i & 1), i >> 1) &&
+                     (i < 1 || wait(kDone + ((i - 1) & 1), (i - 1) >> 1))))
+                break;
+            tc::fence_after();
+            if (lane == 0) {
+                const uint32_t X = desc_lo(sb + kOffX) + kTile * (i & 1), A = kTmCB + 128 * (i & 1);
+#pragma unroll
+                for (int k = 0; k < kL / 8; ++k)
+                    mma_ts(kTmY, A + 8 * k, X + (k >> 1) * kStepMN, tc::idesc(128, kPS, 1) | kBMajor, k);
+                tc::commit(bar(kMX + (i & 1)));
+            }
+            __syncwarp();
+        }
+        drain(kDrain2);
     } else if (warp == kCopyWarp) {
         // ---------------------------------------------------------- copies
         if (lane == 0) {
-            Walk l = w, f = w;    // the next chunk whose b and x are copied; prefetched
-            int bx = 0, cc = 0, pf = 0;   // copies issued, chunks prefetched into L2
-            const int per_group = p.heads / p.groups;
+            // tiles of 64 channels of chunk i; b and c have kN / 64 of them
+            auto copy = [&](int full, int off, const CUtensorMap &map, int col, int row, int n) {
+                mbar_arrive_expect_tx(bar(full), kL * 128 * n);
 #pragma unroll 1
-            for (int i = kStates ? 0 : -1; i < count; ++i) {
-                // chunk i + 1 of c, as soon as chunk i is done with its buffer, and
-                // chunk i + 2 of b and x (the first time two of them)
-                if (!kStates && i + 1 < count) {
-                    if (i >= 0 && !wait(kCS, i)) break;
-                    const int h = w.u >> pl.shift, row = static_cast<int>(w.row());
-                    mbar_arrive_expect_tx(bar(kFullC), kL * 2 * kN);
+                for (int k = 0; k < n; ++k) tma_2d(sb + off + k * kTileBytes, &map, col + 64 * k, row, bar(full));
+            };
+            int i = 0;
 #pragma unroll 1
-                    for (int k = 0; k < kN / 64; ++k)
-                        tma_2d(sb + kOffC + k * kTileBytes, &maps.c, (h / per_group) * kN + 64 * k, row, bar(kFullC));
-                    ++cc;
-                    w.next(p, pl, list.nc);
-                }
-                const int upto = min(count, i + (kStates ? 2 : 3));
-#pragma unroll 1
-                while (bx < upto) {
-                    if (bx >= 2 && !wait(kFreeBX + (bx & 1), (bx >> 1) - 1)) break;
-                    const int h = l.u >> pl.shift, s = bx & 1;
-                    const int row = static_cast<int>(l.row());
-                    mbar_arrive_expect_tx(bar(kFullBX + s), kL * 2 * (kN + kPS));
-#pragma unroll 1
-                    for (int k = 0; k < kN / 64; ++k)
-                        tma_2d(sb + kOffB + (2 * s + k) * kTileBytes, &maps.b, (h / per_group) * kN + 64 * k, row,
-                               bar(kFullBX + s));
-                    tma_2d(sb + kOffX + s * kTileBytes, &maps.x, h * p.p + (l.u & pl.shift) * kPS, row,
-                           bar(kFullBX + s));
-                    ++bx;
-                    l.next(p, pl, list.nc);
-                }
-                if (bx < upto) break;
-                // a buffer is free for about half a chunk's time before its next
-                // copy is needed, less than a read from HBM takes: fetch ahead
-#pragma unroll 1
-                for (; pf < min(count, i + 6); ++pf) {
-                    if (pf >= bx) {
-                        const int h = f.u >> pl.shift, row = static_cast<int>(f.row());
-#pragma unroll 1
-                        for (int k = 0; k < kN / 64; ++k) {
-                            prefetch_2d(&maps.b, (h / per_group) * kN + 64 * k, row);
-                            if (!kStates) prefetch_2d(&maps.c, (h / per_group) * kN + 64 * k, row);
-                        }
-                        prefetch_2d(&maps.x, h * p.p + (f.u & pl.shift) * kPS, row);
-                    }
-                    f.next(p, pl, list.nc);
+            for (; i < count; ++i) {
+                // what chunks i - 2 (b, x) and i - 1 (c) have left
+                if (!wait(kScal + (i & (kRing - 1)), i / kRing)) break;
+                const Scalars &v = scal[i & (kRing - 1)];
+                const int row = static_cast<int>(v.row), col = v.gcol, xcol = v.xcol, s = i & 1;
+                if (i > 1 && (!wait(kDS + s, (i >> 1) - 1) || (!kStates && !wait(kCB + s, (i >> 1) - 1)))) break;
+                copy(kFullB + s, kOffB + 2 * s * kTileBytes, maps.b, col, row, kN / 64);
+                if (!kStates && i > 1 && !wait(kMX + s, (i >> 1) - 1)) break;
+                copy(kFullX + s, kOffX + s * kTileBytes, maps.x, xcol, row, 1);
+                if (!kStates) {
+                    if (i > 0 && (!wait(kCS + (s ^ 1), (i - 1) >> 1) || !wait(kCB + (s ^ 1), (i - 1) >> 1))) break;
+                    copy(kFullC, kOffC, maps.c, col, row, kN / 64);
                 }
             }
-            // the last copies land before the block ends (after a wait that gave
-            // up nobody else may have waited for them)
-            for (int j = bx > 2 ? bx - 2 : 0; j < bx; ++j) wait_phase(bar(kFullBX + (j & 1)), (j >> 1) & 1);
-            if (cc > 0) wait_phase(bar(kFullC), (cc - 1) & 1);
+            // the last copies land before the block ends (after a wait that gave up
+            // nobody else may have waited for them)
+            for (int j = i > 2 ? i - 2 : 0; j < i; ++j) {
+                wait_phase(bar(kFullB + (j & 1)), (j >> 1) & 1);
+                wait_phase(bar(kFullX + (j & 1)), (j >> 1) & 1);
+            }
+            if (!kStates && i > 0) wait_phase(bar(kFullC), (i - 1) & 1);
+            if (i < count) {   // (of the chunk it gave up at)
+                wait_phase(bar(kFullB + (i & 1)), (i >> 1) & 1);
+                wait_phase(bar(kFullX + (i & 1)), (i >> 1) & 1);
+            }
         }
         __syncwarp();
-    } else if (warp >= kScalWarp) {
-        // --------- scalars: the decays of each chunk, the two warps in turn
-        float raw[4], next_raw[4] = {};
-        auto load = [&]() {   // this chunk's dt, ahead of their use
-            const int h = w.u >> pl.shift, valid = w.valid();
-            const int64_t row = w.row();
+    } else if (warp == kScalWarp) {
+        // ------------------------------------ scalars: the decays of each chunk
+        // It runs up to kRing chunks ahead of the others, so it also has the tiles
+        // fetched into L2: their buffers are free for about half a chunk's time
+        // before they are needed, less than a read from HBM takes.
+        const int per_group = p.heads / p.groups;
+        float raw[4] = {}, next_a = 0.f, next_bias = 0.f;
+        int xcol = 0, gcol = 0;
+        auto load = [&](bool ahead) {   // the next chunk's dt, ahead of their use
+            const int h = w.u >> pl.shift, valid = w.valid(), row = static_cast<int>(w.row());
+            const float *src = p.dt + (w.row() + 4 * lane) * p.dt_stride + h;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                next_raw[j] = 4 * lane + j < valid ? __ldg(p.dt + (row + 4 * lane + j) * p.dt_stride + h) : 0.f;
+            for (int j = 0; j < 4; ++j) raw[j] = 4 * lane + j < valid ? __ldg(src + j * p.dt_stride) : 0.f;
+            next_a = __ldg(p.a + h);
+            if (p.dt_bias != nullptr) next_bias = __ldg(p.dt_bias + h);
+            xcol = h * p.p + (w.u & pl.shift) * kPS;
+            gcol = h / per_group * kN;
+            if (ahead && lane < (kStates ? 2 : 3)) {   // lanes 0, 1, 2: x, b, c
+                const CUtensorMap *map = lane == 0 ? &maps.x : lane == 1 ? &maps.b : &maps.c;
+                prefetch_2d(map, lane == 0 ? xcol : gcol, row);
+                if (lane > 0 && kN == 128) prefetch_2d(map, gcol + 64, row);
+            }
         };
-        const int first = warp - kScalWarp;
-        if (first == 1 && count > 1) w.next(p, pl, list.nc);
-        if (first < count) load();
+        Sum2 sum{0.f, 0.f};
 #pragma unroll 1
-        for (int i = first; i < count; i += 2) {
-            const int h = w.u >> pl.shift, valid = w.valid(), unit = w.u, seq = w.n, pos = w.pos;
-            const int flags = (w.last() ? kLast : 0) | (q0 + i + (w.len + kL - 1) / kL - pos > q1 ? kCut : 0);
-            const int64_t row = w.row();
-            const float a2 = __ldg(p.a + h) * 1.44269504088896341f;
-            const float bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + h) : 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) raw[j] = next_raw[j];
-            if (i + 2 < count) {
-                w.next(p, pl, list.nc);
-                w.next(p, pl, list.nc);
-                load();
-            }
-            if (i >= kRing && !wait(kScFree + (i & (kRing - 1)), (i / kRing) - 1)) break;
+        for (int i = -1; i < count; ++i) {
             Scalars &s = scal[i & (kRing - 1)];
-            // running sums over this lane's four tokens, then over the lanes
-            Sum2 sum{0.f, 0.f};
-            float dt[4], gh[4], gl[4];
+            if (i >= 0) {
+                if (i >= kRing && !wait(kScFree + (i & (kRing - 1)), (i / kRing) - 1)) break;
+                const int valid = w.valid();
+                const float a2 = next_a * 1.44269504088896341f;
+                if (lane == 0) {
+                    s.valid = valid;
+                    s.unit = w.u;
+                    s.seq = w.n;
+                    s.pos = w.pos;
+                    s.flags = (w.last() ? kLast : 0) | (q0 + i + (w.len + kL - 1) / kL - w.pos > q1 ? kCut : 0);
+                    s.row = w.row();
+                    s.xcol = xcol;
+                    s.gcol = gcol;
+                }
+                // running sums over this lane's four tokens, then over the lanes
+                sum = Sum2{0.f, 0.f};
 #pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-                const float v = j == 0 ? raw[0] : j == 1 ? raw[1] : j == 2 ? raw[2] : raw[3];
-                const float d = 4 * lane + j < valid ? delta_of(v + bias, p.softplus) : 0.f;
-                sum.add(a2 * d, 0.f);
-                s.dt[4 * lane + j] = d;
-                s.hi[4 * lane + j] = sum.hi;
-                s.lo[4 * lane + j] = sum.lo;
+                for (int j = 0; j < 4; ++j) {
+                    const float d = 4 * lane + j < valid ? delta_of(raw[0] + next_bias, p.softplus) : 0.f;
+                    raw[0] = raw[1]; raw[1] = raw[2]; raw[2] = raw[3];
+                    sum.add(a2 * d, 0.f);
+                    s.dt[4 * lane + j] = d;
+                    s.hi[4 * lane + j] = sum.hi;
+                    s.lo[4 * lane + j] = sum.lo;
+                }
             }
-            *reinterpret_cast<float4 *>(dt) = *reinterpret_cast<const float4 *>(s.dt + 4 * lane);
-            *reinterpret_cast<float4 *>(gh) = *reinterpret_cast<const float4 *>(s.hi + 4 * lane);
-            *reinterpret_cast<float4 *>(gl) = *reinterpret_cast<const float4 *>(s.lo + 4 * lane);
+            if (i + 1 < count) {
+                if (i >= 0) w.next(p, pl, list.nc);
+                load(i >= 0);
+            }
+            if (i < 0) continue;
             Sum2 incl = sum;
 #pragma unroll 1
             for (int o = 1; o < 32; o <<= 1) {
@@ -621,54 +729,171 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             const float kh = __shfl_sync(0xffffffffu, incl.hi, lane | 7);
             const float kl = __shfl_sync(0xffffffffu, incl.lo, lane | 7);
             const float eh = __shfl_sync(0xffffffffu, incl.hi, 31), el = __shfl_sync(0xffffffffu, incl.lo, 31);
-            float v[5][4];
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < 4; ++j) {
+                const int t = 4 * lane + j;
+                const float dt = s.dt[t];
                 Sum2 G{bh, bl};
-                G.add(gh[j], gl[j]);
-                v[0][j] = -G.hi;
-                v[1][j] = -G.lo;
-                v[2][j] = ex2((kh - G.hi) + (kl - G.lo)) * dt[j];
-                v[3][j] = ex2((eh - G.hi) + (el - G.lo)) * dt[j];
-                v[4][j] = ex2(G.hi);
+                G.add(s.hi[t], s.lo[t]);
+                s.hi[t] = -G.hi;
+                s.lo[t] = -G.lo;
+                s.to_block[t] = ex2((kh - G.hi) + (kl - G.lo)) * dt;
+                s.to_end[t] = ex2((eh - G.hi) + (el - G.lo)) * dt;
+                s.from[t] = ex2(G.hi);
             }
-            float *const dst[5] = {s.hi, s.lo, s.to_block, s.to_end, s.from};
-#pragma unroll
-            for (int k = 0; k < 5; ++k)
-                *reinterpret_cast<float4 *>(dst[k] + 4 * lane) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
             if ((lane & 7) == 7) {
                 s.end_hi[lane >> 3] = kh;
                 s.end_lo[lane >> 3] = kl;
             }
             // (carried over all the chunks of a sequence: the more exact exponential)
-            if (lane == 31) {
-                s.decay = exp2f(eh);
-                s.valid = valid;
-                s.unit = unit;
-                s.seq = seq;
-                s.pos = pos;
-                s.flags = flags;
-                s.row = row;
-            }
+            if (lane == 31) s.decay = exp2f(eh);
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(kScal + (i & (kRing - 1))));
         }
+    } else if (warp < kGroup) {
+        // ------------------------------------------------- M and the output, row
+        // 32 q + lane (the lanes of tensor memory that a warp reaches); columns of y:
+        // the half hf
+        const int q = warp & 3, hf = warp >> 2, r = 32 * q + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+        // y = 2^G (C S) + M X of chunk i
+        auto put_out = [&](int i) -> bool {
+            const Scalars &s = scal[i & (kRing - 1)];
+            const int h = s.unit >> pl.shift;
+            const float from = s.from[r];
+            const bool live = r < s.valid;
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                                   ((s.row + r) * p.heads + h) * p.p +
+                                                   (s.unit & pl.shift) * kPS + kCols * hf);
+            if (!wait(kMX + (i & 1), i >> 1) || !wait(kCS + (i & 1), i >> 1)) return false;
+            tc::fence_after();
+#pragma unroll 2
+            for (int k = 0; k < 4; ++k) {   // 8 columns at a time
+                uint32_t y[8], cs[8];
+                ld8(lanes + kTmY + kCols * hf + 8 * k, y);
+                ld8(lanes + kTmCS + 64 * (i & 1) + kCols * hf + 8 * k, cs);
+                tc::ld_wait();
+                uint32_t os[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float a = __uint_as_float(cs[2 * e]), b = __uint_as_float(cs[2 * e + 1]);
+                    fma2(a, b, from, from, __uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
+                    os[e] = pack_bf16(a, b);
+                }
+                if (live) dst[k] = make_uint4(os[0], os[1], os[2], os[3]);
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(kDone + (i & 1)));
+                mbar_arrive(bar(kScFree + (i & (kRing - 1))));
+            }
+            return true;
+        };
+        if (kStates) {   // half of the weighted rows
+#pragma unroll 1
+            for (int i = 0; i < count; ++i) {
+                if (!landed(i) || (i > 1 && !wait(kDS + (i & 1), (i >> 1) - 1))) break;
+                put_rows(i, 16 + 2 * warp, 2);
+            }
+        }
+#pragma unroll 1
+        for (int i = 0; !kStates && i <= count; ++i) {
+            // M of chunk i, then the output of the one before, whose products are done
+            if (i < count) {
+            const Scalars &s = scal[i & (kRing - 1)];
+            // ---- M = (C B^T) . decay + d I, two bf16 terms: two 32-token blocks
+            if (!wait(kScal + (i & (kRing - 1)), i / kRing) || !wait(kCB + (i & 1), i >> 1)) break;
+            tc::fence_after();
+            const uint32_t at = lanes + kTmCB + 128 * (i & 1);
+            const float hi_r = -s.hi[r], lo_r = -s.lo[r];
+            const float dv = p.d != nullptr ? __ldg(p.d + (s.unit >> pl.shift)) : 0.f;
+            // rows of quarter 3: blocks (0, 1) and (2, 3); of quarter 2 (0, 1) and the
+            // diagonal; of the others one each; the rest, above the diagonal, is zero.
+            // 16 columns at a time, the next ones read before these are worked on.
+            const int step = q >= 2 ? 16 : 48;
+            uint32_t ahead[16] = {};
+            int next = (q >= 2 ? 64 : 32) * hf;
+            if (next >> 5 <= q) {
+                tc::ld16(at + next, ahead);
+                ld_wait16(ahead);
+            }
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                const int col = next, b = col >> 5;
+                next = col + ((k & 1) != 0 ? step : 16);
+                uint32_t v[16], hi[8], lo[8];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = ahead[j];
+                const bool more = k < 3 && next >> 5 <= q;
+                if (more) tc::ld16(at + next, ahead);
+                if (b > q) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) hi[j] = lo[j] = 0u;
+                } else {
+                    const float f = ex2((hi_r - s.end_hi[b]) + (lo_r - s.end_lo[b]));
+                    if (b < q) {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 e = *reinterpret_cast<const float4 *>(s.to_block + col + j);
+                            float x[4] = {__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
+                                          __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])};
+                            mul2(x[0], x[1], f, f);
+                            mul2(x[2], x[3], f, f);
+                            mul2(x[0], x[1], e.x, e.y);
+                            mul2(x[2], x[3], e.z, e.w);
+                            hi[j / 2] = split2(x[0], x[1], lo[j / 2]);
+                            hi[j / 2 + 1] = split2(x[2], x[3], lo[j / 2 + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            float4 a = *reinterpret_cast<const float4 *>(s.hi + col + j);
+                            float4 g = *reinterpret_cast<const float4 *>(s.lo + col + j);
+                            const float4 d = *reinterpret_cast<const float4 *>(s.dt + col + j);
+                            add2(a.x, a.y, hi_r, hi_r);
+                            add2(a.z, a.w, hi_r, hi_r);
+                            add2(g.x, g.y, lo_r, lo_r);
+                            add2(g.z, g.w, lo_r, lo_r);
+                            add2(a.x, a.y, g.x, g.y);
+                            add2(a.z, a.w, g.z, g.w);
+                            float x[4] = {ex2(a.x), ex2(a.y), ex2(a.z), ex2(a.w)};
+                            mul2(x[0], x[1], d.x, d.y);
+                            mul2(x[2], x[3], d.z, d.w);
+                            mul2(x[0], x[1], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                            mul2(x[2], x[3], __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                x[e] = col + j + e > r ? 0.f : col + j + e == r ? x[e] + dv : x[e];
+                            hi[j / 2] = split2(x[0], x[1], lo[j / 2]);
+                            hi[j / 2 + 1] = split2(x[2], x[3], lo[j / 2 + 1]);
+                        }
+                    }
+                }
+                tc::st8(at + col, hi);
+                tc::st8(at + col + 8, lo);
+                if (more) ld_wait16(ahead);
+            }
+            tc::st_wait();
+            tc::fence_before();
+            arrive(kMReady + (i & 1));
+            }
+            if (i > 0 && !put_out(i - 1)) break;
+        }
     } else {
-        // ------------------------------------------------------------ compute
-        // rows: token (M, Y) or state row (S) 32 q + lane (the lanes of tensor
-        // memory that a warp reaches); columns: the cq-th quarter
-        const int q = warp & 3, cq = warp >> 2, r = 32 * q + lane;
+        // ---------------------------------------------------------- the state
+        // row 32 q + lane of S; columns: the half hf
+        const int q = warp & 3, hf = (warp >> 2) & 1, r = 32 * q + lane, gt = tid - kGroupThreads;
         const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
         float S[kCols];
         const bool has = r < kN;
-
         // this thread's values in the state array
         auto state_at = [&](const Scalars &v) {
             return ((static_cast<int64_t>(v.seq) * p.heads + (v.unit >> pl.shift)) * kN + r) * p.p +
-                   (v.unit & pl.shift) * kPS + kCols * cq;
+                   (v.unit & pl.shift) * kPS + kCols * hf;
         };
         // ... and in the slots at the cuts
-        const int64_t slot = static_cast<int64_t>(c) * kCols * kCompute + tid;
+        const int64_t slot = static_cast<int64_t>(c) * kCols * kGroupThreads + gt;
         // The state that enters chunk i of the run (its first, or a sequence's first).
         auto start_state = [&](const Scalars &v) {
 #pragma unroll
@@ -679,9 +904,9 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 const int64_t head = q0 - v.pos;
                 float f = 1.f;
                 for (int k = c - 1; k >= 0; --k) {
-                    const float *src = pl.slots + static_cast<int64_t>(k) * kCols * kCompute + tid;
+                    const float *src = pl.slots + static_cast<int64_t>(k) * kCols * kGroupThreads + gt;
 #pragma unroll
-                    for (int j = 0; j < kCols; ++j) S[j] = fmaf(src[j * kCompute], f, S[j]);
+                    for (int j = 0; j < kCols; ++j) S[j] = fmaf(src[j * kGroupThreads], f, S[j]);
                     if (list.begin(k) <= head) break;
                     f *= pl.decay[k];
                 }
@@ -692,7 +917,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             // that the end of this run cuts: the first launch took a copy
             if (!kStates && pl.in_place && (v.flags & kCut) != 0) {
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) S[j] = pl.saved[slot + j * kCompute];
+                for (int j = 0; j < kCols; ++j) S[j] = pl.saved[slot + j * kGroupThreads];
                 return;
             }
             if (has) {
@@ -705,234 +930,78 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             }
             if (kStates && pl.in_place) {
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) pl.saved[slot + j * kCompute] = S[j];
+                for (int j = 0; j < kCols; ++j) pl.saved[slot + j * kGroupThreads] = S[j];
             }
         };
         // S as two bf16 terms for C S
         auto put_state = [&]() {
             if (has) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
+                for (int k = 0; k < 4; ++k) {
                     uint4 hi, lo;
                     hi.x = split2(S[8 * k], S[8 * k + 1], lo.x);
                     hi.y = split2(S[8 * k + 2], S[8 * k + 3], lo.y);
                     hi.z = split2(S[8 * k + 4], S[8 * k + 5], lo.z);
                     hi.w = split2(S[8 * k + 6], S[8 * k + 7], lo.w);
-                    const int at = r * 128 + (((2 * cq + k) ^ (r & 7)) << 4);
+                    const int at = r * 128 + (((4 * hf + k) ^ (r & 7)) << 4);
                     *reinterpret_cast<uint4 *>(smem + kOffS + at) = hi;
                     *reinterpret_cast<uint4 *>(smem + kOffS + kTileBytes + at) = lo;
                 }
             }
-        };
-        // The weighted rows of chunk i as three bf16 terms, in 32 tasks of 32
-        // rows x 8 channels. The lower quarters of M have more blocks under the
-        // diagonal, so the upper quarters' warps take more tasks: 3, 2, 2, 1.
-        // Rows past the end of the sequence belong to another one: they are
-        // zeroed here, as no weight of 0 makes an infinity or NaN vanish.
-        const int tasks = kStates || q == 1 || q == 2 ? 2 : q == 0 ? 3 : 1;
-        const int task0 = (kStates ? 8 * q : q == 0 ? 0 : 4 + 8 * q) + cq * tasks;
-        auto put_rows = [&](int i) {
-            uint8_t *X = smem + kOffX + (i & 1) * kTileBytes, *W = smem + off_w(kStates, i);
-            const Scalars &s = scal[i & (kRing - 1)];
-            const int valid = s.valid;
-#pragma unroll 1
-            for (int k = task0; k < task0 + tasks; ++k) {
-                const int row = (k >> 3) * 32 + lane, at = row * 128 + (((k ^ row) & 7) << 4);
-                const float wt = s.to_end[row];
-                uint4 x = *reinterpret_cast<const uint4 *>(X + at);
-                if (row >= valid) {
-                    x = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4 *>(X + at) = x;
-#pragma unroll
-                    for (int z = 0; z < kN / 64; ++z)
-                        *reinterpret_cast<uint4 *>(smem + kOffB + (2 * (i & 1) + z) * kTileBytes + at) = x;
-                }
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                uint32_t t0[4], t1[4], t2[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float a = __uint_as_float(xs[e] << 16), b = __uint_as_float(xs[e] & 0xffff0000u);
-                    mul2(a, b, wt, wt);
-                    t0[e] = take2(a, b);
-                    t1[e] = split2(a, b, t2[e]);
-                }
-                *reinterpret_cast<uint4 *>(W + at) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
-                *reinterpret_cast<uint4 *>(W + kTileBytes + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-                *reinterpret_cast<uint4 *>(W + 2 * kTileBytes + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-            }
             fence_async();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(kWReady));
-                if (!kStates) mbar_arrive(bar(kSReady));   // put_state's stores come before
-            }
-        };
-        auto landed = [&](int i) {
-            return wait(kScal + (i & (kRing - 1)), i / kRing) && wait(kFullBX + (i & 1), i >> 1);
+            arrive(kSReady);
         };
 
         float run_decay = 1.f;   // over this part of the sequence
         bool ok = true;
 #pragma unroll 1
         for (int i = -1; i < count; ++i) {
-            const Scalars &s = scal[i & (kRing - 1)];
+            const Scalars &s = scal[i & (kRing - 1)], &next = scal[(i + 1) & (kRing - 1)];
             const bool more = i + 1 < count;
             if (kStates && more) {   // into the other set of weighted rows
                 if (!(ok = landed(i + 1))) break;
-                put_rows(i + 1);
-            }
-            if (!kStates && i >= 0) {
-                // ---- M = (C B^T) . decay, two bf16 terms: one 32-token block
-                if (!(ok = wait(kCB, i))) break;
-                tc::fence_after();
-                if (cq > q) {   // above the diagonal
-                    const uint32_t z[16] = {};
-                    tc::st16(lanes + kTmCB + 32 * cq, z);
-                    tc::st16(lanes + kTmCB + 32 * cq + 16, z);
-                } else {
-                    const float hi_r = -s.hi[r], lo_r = -s.lo[r];
-                    const float f = cq < q ? ex2((hi_r - s.end_hi[cq]) + (lo_r - s.end_lo[cq])) : 0.f;
-#pragma unroll 1
-                    for (int col = 32 * cq; col < 32 * cq + 32; col += 16) {
-                        uint32_t v[16];
-                        tc::ld16(lanes + kTmCB + col, v);
-                        tc::ld_wait();
-                        uint32_t hi[8], lo[8];
-                        if (cq < q) {
-#pragma unroll
-                            for (int j = 0; j < 16; j += 4) {
-                                const float4 e = *reinterpret_cast<const float4 *>(s.to_block + col + j);
-                                float x[4] = {__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
-                                              __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])};
-                                mul2(x[0], x[1], f, f);
-                                mul2(x[2], x[3], f, f);
-                                mul2(x[0], x[1], e.x, e.y);
-                                mul2(x[2], x[3], e.z, e.w);
-                                hi[j / 2] = split2(x[0], x[1], lo[j / 2]);
-                                hi[j / 2 + 1] = split2(x[2], x[3], lo[j / 2 + 1]);
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 16; j += 4) {
-                                float4 a = *reinterpret_cast<const float4 *>(s.hi + col + j);
-                                float4 g = *reinterpret_cast<const float4 *>(s.lo + col + j);
-                                const float4 d = *reinterpret_cast<const float4 *>(s.dt + col + j);
-                                add2(a.x, a.y, hi_r, hi_r);
-                                add2(a.z, a.w, hi_r, hi_r);
-                                add2(g.x, g.y, lo_r, lo_r);
-                                add2(g.z, g.w, lo_r, lo_r);
-                                add2(a.x, a.y, g.x, g.y);
-                                add2(a.z, a.w, g.z, g.w);
-                                float x[4] = {ex2(a.x), ex2(a.y), ex2(a.z), ex2(a.w)};
-                                mul2(x[0], x[1], d.x, d.y);
-                                mul2(x[2], x[3], d.z, d.w);
-                                mul2(x[0], x[1], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                                mul2(x[2], x[3], __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (col + j + e > r) x[e] = 0.f;
-                                hi[j / 2] = split2(x[0], x[1], lo[j / 2]);
-                                hi[j / 2 + 1] = split2(x[2], x[3], lo[j / 2 + 1]);
-                            }
-                        }
-                        tc::st8(lanes + kTmCB + col, hi);
-                        tc::st8(lanes + kTmCB + col + 8, lo);
-                    }
-                }
-                tc::st_wait();
-                tc::fence_before();
-                arrive(kMReady);
+                put_rows(i + 1, 2 * (warp - kGroup), 2);
+                if (i < 0) start_state(next);
             }
             if (i >= 0) {
                 // ---- S = 2^G_last S + B^T (W X)
-                if (!(ok = wait(kDS, i))) break;
+                if (!(ok = wait(kDS + (i & 1), i >> 1))) break;
                 const float dec = s.decay;
                 if (has) {
                     tc::fence_after();
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {   // 8 columns at a time
-                        uint32_t v[3][8];
-#pragma unroll
-                        for (int t = 0; t < 3; ++t)
-                            ld8(lanes + tm_ds(kStates, i) + kPS * t + kCols * cq + 8 * k, v[t]);
+                    for (int k = 0; k < 4; ++k) {   // 8 columns at a time
+                        uint32_t v[8];
+                        ld8(lanes + tm_ds(kStates, i) + kCols * hf + 8 * k, v);
                         tc::ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 8; j += 2) {   // the smallest term first
-                            float a = __uint_as_float(v[2][j]), b = __uint_as_float(v[2][j + 1]);
-                            add2(a, b, __uint_as_float(v[1][j]), __uint_as_float(v[1][j + 1]));
-                            add2(a, b, __uint_as_float(v[0][j]), __uint_as_float(v[0][j + 1]));
-                            fma2(S[8 * k + j], S[8 * k + j + 1], dec, dec, a, b);
-                        }
+                        for (int j = 0; j < 8; j += 2)
+                            fma2(S[8 * k + j], S[8 * k + j + 1], dec, dec, __uint_as_float(v[j]),
+                                 __uint_as_float(v[j + 1]));
                     }
                     tc::fence_before();
                 }
                 run_decay *= dec;
-                if (kStates) {
-                    arrive(kFreeBX + (i & 1));
-                    arrive(kScFree + (i & (kRing - 1)));
-                }
-            }
-            if (!kStates && i >= 0 && (s.flags & kLast) != 0 && p.s_final != nullptr && has) {
-                float4 *out = reinterpret_cast<float4 *>(p.s_final + state_at(s));
+                if (!kStates && (s.flags & kLast) != 0 && p.s_final != nullptr && has) {
+                    float4 *out = reinterpret_cast<float4 *>(p.s_final + state_at(s));
 #pragma unroll
-                for (int j = 0; j < kCols / 4; ++j)
-                    out[j] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+                    for (int j = 0; j < kCols / 4; ++j)
+                        out[j] = make_float4(S[4 * j], S[4 * j + 1], S[4 * j + 2], S[4 * j + 3]);
+                }
+                arrive(kScFree + (i & (kRing - 1)));
             }
-            if (more && (!kStates || i < 0)) {
-                const Scalars &t = scal[(i + 1) & (kRing - 1)];
-                if (!kStates && !(ok = landed(i + 1))) break;
-                if (i < 0 || t.pos == 0) start_state(t);   // (kStates: landed above)
-                if (!kStates) {
-                    if (i >= 0 && !(ok = wait(kCS, i))) break;   // the terms of S are read
-                    put_state();
-                    put_rows(i + 1);
-                }
-            }
-            if (!kStates && i >= 0) {
-                // ---- y = 2^G (C S) + M X + d x
-                const int h = s.unit >> pl.shift;
-                const float from = s.from[r], dv = p.d != nullptr ? __ldg(p.d + h) : 0.f;
-                const bool live = r < s.valid;
-                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                                       ((s.row + r) * p.heads + h) * p.p +
-                                                       (s.unit & pl.shift) * kPS + kCols * cq);
-                if (!(ok = wait(kMX, i))) break;
-                tc::fence_after();
-#pragma unroll 1
-                for (int k = 0; k < 2; ++k) {   // 8 columns at a time
-                    uint32_t y[8], c0[8], c1[8];
-                    ld8(lanes + kTmY + kCols * cq + 8 * k, y);
-                    ld8(lanes + kTmCS + kCols * cq + 8 * k, c0);
-                    ld8(lanes + kTmCS + kPS + kCols * cq + 8 * k, c1);
-                    const uint4 x = *reinterpret_cast<const uint4 *>(smem + kOffX + (i & 1) * kTileBytes + r * 128 +
-                                                                     (((2 * cq + k) ^ (r & 7)) << 4));
-                    tc::ld_wait();
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t os[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float a = __uint_as_float(c0[2 * e]), b = __uint_as_float(c0[2 * e + 1]);
-                        add2(a, b, __uint_as_float(c1[2 * e]), __uint_as_float(c1[2 * e + 1]));
-                        fma2(a, b, from, from, __uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
-                        float f = __uint_as_float(xs[e] << 16), g = __uint_as_float(xs[e] & 0xffff0000u);
-                        fma2(f, g, dv, dv, a, b);
-                        os[e] = pack_bf16(f, g);
-                    }
-                    if (live) dst[k] = make_uint4(os[0], os[1], os[2], os[3]);
-                }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(kDone));
-                    mbar_arrive(bar(kFreeBX + (i & 1)));
-                    mbar_arrive(bar(kScFree + (i & (kRing - 1))));
-                }
+            if (!kStates && more) {
+                if (!(ok = landed(i + 1))) break;
+                put_rows(i + 1, 4 * (warp - kGroup), 4);   // into the rows that this chunk's product has read
+                if (i < 0 || next.pos == 0) start_state(next);
+                if (i >= 0 && !(ok = wait(kCS + (i & 1), i >> 1))) break;   // the terms of S are read
+                put_state();
             }
         }
         if (kStates && ok) {
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) pl.slots[slot + j * kCompute] = has ? S[j] : 0.f;
-            if (tid == 0) pl.decay[c] = run_decay;
+            for (int j = 0; j < kCols; ++j) pl.slots[slot + j * kGroupThreads] = has ? S[j] : 0.f;
+            if (gt == 0) pl.decay[c] = run_decay;
         }
     }
     tc::fence_before();
@@ -970,7 +1039,7 @@ int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
 // Workspace: [chunk offsets (packed)][decays][states at the cuts][copies of
 // initial states (in place)].
-constexpr int64_t kSlotBytes = static_cast<int64_t>(kCols) * kCompute * 4;
+constexpr int64_t kSlotBytes = static_cast<int64_t>(kCols) * kGroupThreads * 4;
 int64_t offsets_bytes(const SsmParams &p) {
     return p.cu != nullptr ? align256((static_cast<int64_t>(p.n_seqs) + 1) * 4) : 0;
 }
