@@ -211,11 +211,11 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint3
         "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi)
         : "memory");
 }
-// (with A in tensor memory the elected form took 300 cycles: one lane calls this)
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
     asm volatile(
-        "{\n .reg .pred p;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n mov.b64 y, {%2, %5};\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+        "{\n .reg .pred p, e;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " mov.b64 y, {%2, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
         "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi)
         : "memory");
 }
@@ -459,7 +459,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
     if (tid == 0) {
         s_abort = (sb & 1023) != 0;   // (the tiles' swizzle counts on it)
         for (int i = 0; i < kBars; ++i) 
-            mbar_init(bar(i), i == kDrain2 ? 2 : i < kMReady ? 1
+            mbar_init(bar(i), i < kMReady ? 1
                               : i == kWReady ? (kStates ? 2 * kGroup : kGroup)
                               : i >= kScFree ? (kStates ? kGroup : 2 * kGroup) : kGroup);
         mbar_fence_init();
@@ -488,13 +488,11 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
 
     // k-steps of 16: 32 bytes along a row, or 16 rows of 128 bytes
     constexpr uint32_t kStepK = 32 >> 4, kStepMN = 2048 >> 4, kTile = kTileBytes >> 4;
-    // after a wait that gave up: let the MMAs that this warp issued end (C B^T and M X
-    // by two lanes of it)
+    // after a wait that gave up: let the MMAs that this warp issued end
     auto drain = [&](int i) {
         __syncwarp();
         if (s_abort != 0) {
             mma_commit(bar(i));
-            if (i == kDrain2 && lane == 0) tc::commit(bar(i));
             wait_phase(bar(i), 0);
         }
     };
@@ -555,7 +553,8 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
     if (warp == kMmaWarpS) {
         // ------------------------------------------- MMAs: B^T (W X) and C S
 #pragma unroll 1
-        for (int i = 0; i < count; ++i) {
+        for (int j0 = 0; j0 < count; ++j0) {
+            const int i = __shfl_sync(0xffffffffu, j0, 0);   // (uniform, see above)
             // B^T (W X) (for n = 64 the upper 64 rows are formed from whatever lies
             // there and are not read)
             if (!all(wait(kFullB + (i & 1), i >> 1) && wait(kWReady, i))) break;
@@ -589,7 +588,8 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
     } else if (warp == kMmaWarpY) {
         // --------------------------------------------- MMAs: C B^T and M X
 #pragma unroll 1
-        for (int i = -1; !kStates && i < count; ++i) {
+        for (int j0 = -1; !kStates && j0 < count; ++j0) {
+            const int i = __shfl_sync(0xffffffffu, j0, 0);   // (uniform, see above)
             if (i + 1 < count) {
                 // C B^T of the next chunk, over M of the one before this
                 if (!all(wait(kFullB + ((i + 1) & 1), (i + 1) >> 1) && wait(kFullC, i + 1) &&
@@ -606,19 +606,13 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             }
             if (i < 0) continue;
             // M X, both terms of M along K, once the chunk before is read out
-            if (!all(wait(kMReady + (i & 1), i >> 1) && wait(kFullX + (i & 1), i >> 1) &&
-                     wait(kXReady + (i & 1), i >> 1) &&
-                     (i < 1 || wait(kDone + ((i - 1) & 1), (i - 1) >> 1))))
-                break;
+            if (!all(wait(kXReady + (i & 1), i >> 1) && wait(kMReady + (i & 1), i >> 1))) break;
             tc::fence_after();
-            if (lane == 0) {
-                const uint32_t X = desc_lo(sb + kOffX) + kTile * (i & 1), A = kTmCB + 128 * (i & 1);
+            const uint32_t X = desc_lo(sb + kOffX) + kTile * (i & 1), A = kTmCB + 128 * (i & 1);
 #pragma unroll
-                for (int k = 0; k < kL / 8; ++k)
-                    mma_ts(kTmY, A + 8 * k, X + (k >> 1) * kStepMN, tc::idesc(128, kPS, 1) | kBMajor, k);
-                tc::commit(bar(kMX + (i & 1)));
-            }
-            __syncwarp();
+            for (int k = 0; k < kL / 8; ++k)
+                mma_ts(kTmY, A + 8 * k, X + (k >> 1) * kStepMN, tc::idesc(128, kPS, 1) | kBMajor, k);
+            mma_commit(bar(kMX + (i & 1)));
         }
         drain(kDrain2);
     } else if (warp == kCopyWarp) {
@@ -682,7 +676,8 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 if (lane > 0 && kN == 128) prefetch_2d(map, gcol + 64, row);
             }
         };
-        Sum2 sum{0.f, 0.f};
+        Sum2 sum{0.f, 0.f}, g[4] = {};
+        float dt[4] = {};
 #pragma unroll 1
         for (int i = -1; i < count; ++i) {
             Scalars &s = scal[i & (kRing - 1)];
@@ -702,14 +697,13 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 }
                 // running sums over this lane's four tokens, then over the lanes
                 sum = Sum2{0.f, 0.f};
-#pragma unroll 1
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    dt[j] = 4 * lane + j < valid ? delta_of(raw[j] + next_bias, p.softplus) : 0.f;
+#pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float d = 4 * lane + j < valid ? delta_of(raw[0] + next_bias, p.softplus) : 0.f;
-                    raw[0] = raw[1]; raw[1] = raw[2]; raw[2] = raw[3];
-                    sum.add(a2 * d, 0.f);
-                    s.dt[4 * lane + j] = d;
-                    s.hi[4 * lane + j] = sum.hi;
-                    s.lo[4 * lane + j] = sum.lo;
+                    sum.add(a2 * dt[j], 0.f);
+                    g[j] = sum;
                 }
             }
             if (i + 1 < count) {
@@ -718,7 +712,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             }
             if (i < 0) continue;
             Sum2 incl = sum;
-#pragma unroll 1
+#pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const float vh = __shfl_up_sync(0xffffffffu, incl.hi, o);
                 const float vl = __shfl_up_sync(0xffffffffu, incl.lo, o);
@@ -729,18 +723,25 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             const float kh = __shfl_sync(0xffffffffu, incl.hi, lane | 7);
             const float kl = __shfl_sync(0xffffffffu, incl.lo, lane | 7);
             const float eh = __shfl_sync(0xffffffffu, incl.hi, 31), el = __shfl_sync(0xffffffffu, incl.lo, 31);
-#pragma unroll 1
+            float v[5][4];
+#pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int t = 4 * lane + j;
-                const float dt = s.dt[t];
                 Sum2 G{bh, bl};
-                G.add(s.hi[t], s.lo[t]);
-                s.hi[t] = -G.hi;
-                s.lo[t] = -G.lo;
-                s.to_block[t] = ex2((kh - G.hi) + (kl - G.lo)) * dt;
-                s.to_end[t] = ex2((eh - G.hi) + (el - G.lo)) * dt;
-                s.from[t] = ex2(G.hi);
+                G.add(g[j].hi, g[j].lo);
+                v[0][j] = -G.hi;
+                v[1][j] = -G.lo;
+                v[2][j] = ex2((kh - G.hi) + (kl - G.lo)) * dt[j];
+                v[3][j] = ex2((eh - G.hi) + (el - G.lo)) * dt[j];
+                v[4][j] = ex2(G.hi);
             }
+            if (!kStates) {
+                *reinterpret_cast<float4 *>(s.hi + 4 * lane) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+                *reinterpret_cast<float4 *>(s.lo + 4 * lane) = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
+                *reinterpret_cast<float4 *>(s.dt + 4 * lane) = make_float4(dt[0], dt[1], dt[2], dt[3]);
+                *reinterpret_cast<float4 *>(s.to_block + 4 * lane) = make_float4(v[2][0], v[2][1], v[2][2], v[2][3]);
+                *reinterpret_cast<float4 *>(s.from + 4 * lane) = make_float4(v[4][0], v[4][1], v[4][2], v[4][3]);
+            }
+            *reinterpret_cast<float4 *>(s.to_end + 4 * lane) = make_float4(v[3][0], v[3][1], v[3][2], v[3][3]);
             if ((lane & 7) == 7) {
                 s.end_hi[lane >> 3] = kh;
                 s.end_lo[lane >> 3] = kl;
@@ -876,9 +877,9 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             }
             tc::st_wait();
             tc::fence_before();
-            arrive(kMReady + (i & 1));
             }
             if (i > 0 && !put_out(i - 1)) break;
+            arrive(kMReady + (i & 1));   // M is there and y's columns are free
         }
     } else {
         // ---------------------------------------------------------- the state
@@ -886,7 +887,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
         const int q = warp & 3, hf = (warp >> 2) & 1, r = 32 * q + lane, gt = tid - kGroupThreads;
         const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
         float S[kCols];
-        const bool has = r < kN;
+        const bool has = 32 * q < kN;   // (of the warp's rows all or none)
         // this thread's values in the state array
         auto state_at = [&](const Scalars &v) {
             return ((static_cast<int64_t>(v.seq) * p.heads + (v.unit >> pl.shift)) * kN + r) * p.p +
