@@ -88,19 +88,63 @@ __device__ __forceinline__ void store_f32(float *dst, const float (&f)[VEC]) {
     }
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 1 / (1 + e^-z) of two values with one reciprocal: r = 1 / (a b), 1 / a = r b. The
+// exponential and the reciprocal share one unit of 16 results a clock and SM, which two
+// of each per pair would keep as busy as HBM. e^-z is held at 2^63, so that the
+// product stays finite and no channel can reach the other: below z = -43.7 the
+// result is 2^-63 instead of something smaller.
+__device__ __forceinline__ void sigmoid2(float z0, float z1, float &s0, float &s1) {
+    float e0, e1, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fminf(z0 * -1.44269504f, 63.f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fminf(z1 * -1.44269504f, 63.f)));
+    const float a = 1.f + e0, b = 1.f + e1;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
+    s0 = r * b;
+    s1 = r * a;
+}
+template <int VEC>
+__device__ __forceinline__ void sigmoids(const float (&z)[VEC], float (&s)[VEC]) {
+    if constexpr (VEC == 1) {
+        float other;
+        sigmoid2(z[0], 0.f, s[0], other);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) sigmoid2(z[i], z[i + 1], s[i], s[i + 1]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void silu(float (&z)[VEC]) {
+    float s[VEC];
+    sigmoids<VEC>(z, s);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) z[i] *= s[i];
+}
+
+// The filters of a block's 32 VEC channels, read once and kept tap by tap in shared
+// memory: read from [D, W] by each thread, their scattered sectors cost more than
+// the rows (T = D = 8192: 115 us against 57).
+template <int W, int VEC>
+struct Filters {
+    float w[W + 1][32 * VEC];   // the taps, then the bias
+    __device__ __forceinline__ void load(const ConvParams &p, int64_t d0) {
+        for (int i = threadIdx.x; i < 32 * VEC * W; i += blockDim.x) {
+            const int c = i / W;
+            w[i % W][c] = d0 + c < p.dim ? __ldg(p.weight + d0 * W + i) : 0.f;
+        }
+        for (int c = threadIdx.x; c < 32 * VEC; c += blockDim.x)
+            w[W][c] = p.bias != nullptr && d0 + c < p.dim ? __ldg(p.bias + d0 + c) : 0.f;
+        __syncthreads();
+    }
+};
 
 // The filter of a thread's channels.
 template <int W, int VEC>
 struct Filter {
     float w[W][VEC], b[VEC];
-    __device__ __forceinline__ void load(const ConvParams &p, int64_t d) {
+    __device__ __forceinline__ Filter(const Filters<W, VEC> &f, int lane) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[j][i] = __ldg(p.weight + (d + i) * W + j);
-            b[i] = p.bias != nullptr ? __ldg(p.bias + d + i) : 0.f;
-        }
+        for (int j = 0; j < W; ++j) load_f32<VEC>(f.w[j] + lane * VEC, w[j]);
+        load_f32<VEC>(f.w[W] + lane * VEC, b);
     }
 };
 
@@ -140,50 +184,69 @@ __device__ __forceinline__ void step_window(const Filter<W, VEC> &f, float (&win
     }
 }
 
-// Rows per warp: enough that the W - 1 rows read twice are few, but fewer when
-// the call is too small to fill the SMs.
-constexpr int kRun = 32;
+// Rows per warp: enough that the W - 1 rows read twice are few (9 % at 32, out of L2),
+// but fewer when the call would leave SMs without a block.
+constexpr int kRun = 32, kMinRun = 4;
+int64_t run_for(int64_t tokens, int64_t cols) {
+    const int64_t blocks = (2 * 152 + cols - 1) / cols;   // along the tokens, two per SM
+    int64_t run = (tokens + blocks * kWarps - 1) / (blocks * kWarps);
+    run = (run + kMinRun - 1) / kMinRun * kMinRun;
+    return run < kMinRun ? kMinRun : run > kRun ? kRun : run;
+}
 
 template <int W, int VEC, bool SILU>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 3)
 conv_kernel(ConvParams p, int run, int64_t col_blocks) {
+    __shared__ __align__(16) Filters<W, VEC> filters;
     const Seqs seqs{p.cu, p.seq_len, p.n_seqs};
     if (!check_cu(seqs, p.tokens, p.err)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t tile = blockIdx.x / col_blocks;
+    const int64_t tile = blockIdx.x / col_blocks, d0 = (blockIdx.x % col_blocks) * 32 * VEC;
+    filters.load(p, d0);
     const int64_t t0 = (tile * kWarps + warp) * run;
     const int64_t t1 = t0 + run < p.tokens ? t0 + run : p.tokens;
     if (t0 >= p.tokens && t0 > 0) return;
-    const int64_t d = ((blockIdx.x % col_blocks) * 32 + lane) * VEC;
+    const int64_t d = d0 + lane * VEC;
     int n = first_seq(seqs, t0);
     if (d >= p.dim) return;
-    Filter<W, VEC> f;
-    f.load(p, d);
+    const Filter<W, VEC> f(filters, lane);
     for (; n < p.n_seqs; ++n) {
         const int64_t a = seqs.start(n), b = seqs.start(n + 1);
         if (a >= t1 && t1 < p.tokens) break;
         const int64_t lo = a > t0 ? a : t0, hi = b < t1 ? b : t1;
         float win[W - 1][VEC];
         load_window<W, VEC>(p, n, a, lo, d, win);
+        using R = typename Raw<VEC>::T;
+        const uint16_t *src = static_cast<const uint16_t *>(p.x) + lo * p.x_stride + d;
+        uint16_t *dst = static_cast<uint16_t *>(p.out) + lo * p.out_stride + d;
+        auto row_out = [&](const R &raw, uint16_t *to) {
+            float row[VEC], z[VEC];
+            widen<VEC>(raw, row);
+            step_window<W, VEC>(f, win, row, z);
+            if (SILU) silu<VEC>(z);
+            *reinterpret_cast<R *>(to) = narrow<VEC>(z);
+        };
         constexpr int U = 8;   // rows in flight
-        for (int64_t t = lo; t < hi; t += U) {
-            typename Raw<VEC>::T raw[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + u < hi) raw[u] = load_row<VEC>(p.x, (t + u) * p.x_stride + d);
+        int left = static_cast<int>(hi - lo);
+#pragma unroll 1
+        for (; left >= U; left -= U) {
+            R raw[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (t + u >= hi) break;
-                float row[VEC], z[VEC];
-                widen<VEC>(raw[u], row);
-                step_window<W, VEC>(f, win, row, z);
-                if (SILU) {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) z[i] *= sigmoid(z[i]);
-                }
-                *reinterpret_cast<typename Raw<VEC>::T *>(static_cast<uint16_t *>(p.out) +
-                                                          (t + u) * p.out_stride + d) = narrow<VEC>(z);
+                raw[u] = *reinterpret_cast<const R *>(src);
+                src += p.x_stride;
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                row_out(raw[u], dst);
+                dst += p.out_stride;
+            }
+        }
+#pragma unroll 1
+        for (; left > 0; --left) {
+            row_out(*reinterpret_cast<const R *>(src), dst);
+            src += p.x_stride;
+            dst += p.out_stride;
         }
         if (b <= t1 && p.hist_out != nullptr) {
 #pragma unroll
@@ -195,41 +258,55 @@ conv_kernel(ConvParams p, int run, int64_t col_blocks) {
     }
 }
 
-// One token per sequence: a thread owns VEC channels of one sequence, reads its
-// W rows and writes one row of out and the shifted history. Every address it
+// One token per sequence: a warp takes 32 VEC channels of kStepRows sequences, reads W
+// rows of each and writes one row of out and the shifted history. Every address it
 // writes was read by the same thread before, so the history may be updated in
 // place.
+constexpr int kStepRows = 4;
 template <int W, int VEC, bool SILU>
-__global__ void __launch_bounds__(256) conv_step_kernel(ConvParams p, int64_t cols) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= p.tokens * cols) return;
-    const int64_t n = i / cols, d = (i % cols) * VEC;
-    float win[W - 1][VEC], row[VEC], z[VEC];
-    const auto raw = load_row<VEC>(p.x, n * p.x_stride + d);
-    const int64_t h = n * (W - 1) * p.dim + d;
+__global__ void __launch_bounds__(kWarps * 32) conv_step_kernel(ConvParams p, int64_t col_blocks) {
+    __shared__ __align__(16) Filters<W, VEC> filters;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t d0 = (blockIdx.x % col_blocks) * 32 * VEC, d = d0 + lane * VEC;
+    const int64_t n0 = (blockIdx.x / col_blocks) * kWarps * kStepRows + warp;
+    using R = typename Raw<VEC>::T;
+    R raw[kStepRows][W];
+    if (d < p.dim) {
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        if (p.hist_in != nullptr) {
-            widen<VEC>(load_row<VEC>(p.hist_in, h + j * p.dim), win[j]);
-        } else {
+        for (int u = 0; u < kStepRows; ++u) {
+            const int64_t n = n0 + u * kWarps;
+            if (n >= p.tokens) break;
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) win[j][k] = 0.f;
+            for (int j = 0; j < W - 1; ++j)
+                raw[u][j] = p.hist_in != nullptr
+                                ? load_row<VEC>(p.hist_in, (n * (W - 1) + j) * p.dim + d) : R{};
+            raw[u][W - 1] = load_row<VEC>(p.x, n * p.x_stride + d);
         }
     }
-    Filter<W, VEC> f;
-    f.load(p, d);
-    widen<VEC>(raw, row);
-    step_window<W, VEC>(f, win, row, z);
-    if (SILU) {
+    filters.load(p, d0);
+    if (d >= p.dim) return;
+    const Filter<W, VEC> f(filters, lane);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) z[k] *= sigmoid(z[k]);
+    for (int u = 0; u < kStepRows; ++u) {
+        const int64_t n = n0 + u * kWarps;
+        if (n >= p.tokens) break;
+        float z[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) z[i] = f.b[i];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            float row[VEC];
+            widen<VEC>(raw[u][j], row);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) z[i] = fmaf(f.w[j][i], row[i], z[i]);
+        }
+        if (SILU) silu<VEC>(z);
+        *reinterpret_cast<R *>(static_cast<uint16_t *>(p.out) + n * p.out_stride + d) = narrow<VEC>(z);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+            *reinterpret_cast<R *>(static_cast<uint16_t *>(p.hist_out) + (n * (W - 1) + j) * p.dim + d) =
+                raw[u][j + 1];
     }
-    *reinterpret_cast<typename Raw<VEC>::T *>(static_cast<uint16_t *>(p.out) + n * p.out_stride + d) =
-        narrow<VEC>(z);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-        *reinterpret_cast<typename Raw<VEC>::T *>(static_cast<uint16_t *>(p.hist_out) + h + j * p.dim) =
-            narrow<VEC>(win[j]);
 }
 
 // The gradient walks the same runs. At token t, dz_t completes dx of row
@@ -240,16 +317,18 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvParams p, int64_t co
 // conv_reduce_kernel adds the tiles in order, so the result does not depend on
 // timing.
 template <int W, int VEC, bool SILU, bool D32>
-__global__ void __launch_bounds__(kWarps * 32)
-conv_backward_kernel(ConvParams p, int64_t col_blocks) {
+__global__ void __launch_bounds__(kWarps * 32, 2)
+conv_backward_kernel(ConvParams p, int run, int64_t col_blocks) {
     __shared__ float sums[kWarps][(W + 1) * VEC * 32];
+    __shared__ __align__(16) Filters<W, VEC> filters;
     const Seqs seqs{p.cu, p.seq_len, p.n_seqs};
     if (!check_cu(seqs, p.tokens, p.err)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t tile = blockIdx.x / col_blocks;
-    const int64_t t0 = (tile * kWarps + warp) * kRun;
-    const int64_t t1 = t0 + kRun < p.tokens ? t0 + kRun : p.tokens;
+    const int64_t t0 = (tile * kWarps + warp) * run;
+    const int64_t t1 = t0 + run < p.tokens ? t0 + run : p.tokens;
     const int64_t d0 = (blockIdx.x % col_blocks) * 32 * VEC, d = d0 + lane * VEC;
+    filters.load(p, d0);
     const bool live = d < p.dim && (t0 < p.tokens || t0 == 0);
     int n = first_seq(seqs, t0);
     float dw[W][VEC], db[VEC];
@@ -260,8 +339,7 @@ conv_backward_kernel(ConvParams p, int64_t col_blocks) {
         for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
     }
     if (live) {
-        Filter<W, VEC> f;
-        f.load(p, d);
+        const Filter<W, VEC> f(filters, lane);
         for (; n < p.n_seqs; ++n) {
             const int64_t a = seqs.start(n), b = seqs.start(n + 1);
             if (a >= t1 && t1 < p.tokens) break;
@@ -285,54 +363,82 @@ conv_backward_kernel(ConvParams p, int64_t col_blocks) {
                                    v);
                 }
             };
+            using R = typename Raw<VEC>::T;
+            const uint16_t *src = static_cast<const uint16_t *>(p.x) + lo * p.x_stride + d;
+            int64_t at = lo * p.dout_stride + d;
+            auto load = [&](R &raw, float (&g)[VEC]) {
+                raw = *reinterpret_cast<const R *>(src);
+                if constexpr (D32)
+                    load_f32<VEC>(static_cast<const float *>(p.dout) + at, g);
+                else
+                    widen<VEC>(load_row<VEC>(p.dout, at), g);
+                src += p.x_stride;
+                at += p.dout_stride;
+            };
+            // token t: dz completes row t - (W - 1), which goes to `done`
+            auto token = [&](const R &raw, const float (&g)[VEC], bool own, float (&done)[VEC]) {
+                float row[VEC], z[VEC], sg[VEC];
+                widen<VEC>(raw, row);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    z[i] = f.b[i];
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) z[i] = fmaf(f.w[j][i], win[j][i], z[i]);
+                    z[i] = fmaf(f.w[W - 1][i], row[i], z[i]);
+                }
+                if (SILU) sigmoids<VEC>(z, sg);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    float dz = g[i];
+                    if (SILU) dz *= sg[i] * (1.f + z[i] * (1.f - sg[i]));
+                    done[i] = fmaf(f.w[0][i], dz, open[0][i]);
+#pragma unroll
+                    for (int j = 0; j + 1 < W - 1; ++j) open[j][i] = fmaf(f.w[j + 1][i], dz, open[j + 1][i]);
+                    open[W - 2][i] = f.w[W - 1][i] * dz;
+                    if (own) {
+                        db[i] += dz;
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j) dw[j][i] = fmaf(dz, win[j][i], dw[j][i]);
+                        dw[W - 1][i] = fmaf(dz, row[i], dw[W - 1][i]);
+                    }
+#pragma unroll
+                    for (int j = 0; j + 1 < W - 1; ++j) win[j][i] = win[j + 1][i];
+                    win[W - 2][i] = row[i];
+                }
+            };
+            int64_t t = lo;
+            // the first W - 1 tokens complete rows in front of this run: the history's
+#pragma unroll 1
+            for (; t < end && t < lo + W - 1; ++t) {
+                R raw;
+                float g[VEC], done[VEC];
+                load(raw, g);
+                token(raw, g, t < hi, done);
+                emit(t - (W - 1), done);
+            }
             constexpr int U = 4;   // rows in flight
-            for (int64_t t = lo; t < end; t += U) {
-                typename Raw<VEC>::T raw[U];
+            uint16_t *dst = static_cast<uint16_t *>(p.out) + (t - (W - 1)) * p.out_stride + d;
+#pragma unroll 1
+            for (; t + U <= hi; t += U) {
+                R raw[U];
                 float g[U][VEC];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    if (t + u < end) {
-                        raw[u] = load_row<VEC>(p.x, (t + u) * p.x_stride + d);
-                        const int64_t at = (t + u) * p.dout_stride + d;
-                        if constexpr (D32)
-                            load_f32<VEC>(static_cast<const float *>(p.dout) + at, g[u]);
-                        else
-                            widen<VEC>(load_row<VEC>(p.dout, at), g[u]);
-                    }
-                }
+                for (int u = 0; u < U; ++u) load(raw[u], g[u]);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    if (t + u >= end) break;
-                    const bool own = t + u < hi;
-                    float row[VEC], z[VEC], done[VEC];
-                    widen<VEC>(raw[u], row);
-                    float taps[W - 1][VEC];
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) taps[j][i] = win[j][i];
-                    step_window<W, VEC>(f, win, row, z);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        float dz = g[u][i];
-                        if (SILU) {
-                            const float s = sigmoid(z[i]);
-                            dz *= s * (1.f + z[i] * (1.f - s));
-                        }
-                        done[i] = fmaf(f.w[0][i], dz, open[0][i]);
-#pragma unroll
-                        for (int j = 0; j + 1 < W - 1; ++j)
-                            open[j][i] = fmaf(f.w[j + 1][i], dz, open[j + 1][i]);
-                        open[W - 2][i] = f.w[W - 1][i] * dz;
-                        if (own) {
-                            db[i] += dz;
-#pragma unroll
-                            for (int j = 0; j < W - 1; ++j) dw[j][i] = fmaf(dz, taps[j][i], dw[j][i]);
-                            dw[W - 1][i] = fmaf(dz, row[i], dw[W - 1][i]);
-                        }
-                    }
-                    emit(t + u - (W - 1), done);
+                    float done[VEC];
+                    token(raw[u], g[u], true, done);
+                    *reinterpret_cast<R *>(dst) = narrow<VEC>(done);
+                    dst += p.out_stride;
                 }
+            }
+#pragma unroll 1
+            for (; t < end; ++t) {
+                R raw;
+                float g[VEC], done[VEC];
+                load(raw, g);
+                token(raw, g, t < hi, done);
+                emit(t - (W - 1), done);
             }
             if (end == b) {   // the rows that final_state holds
 #pragma unroll
@@ -393,12 +499,14 @@ bool aligned(const void *p, int64_t stride, int64_t bytes, int64_t elem) {
 }
 
 // Channels per thread: 8 or 4 when every row of every array starts on a
-// 16- or 8-byte boundary, else 1.
-int conv_vec(const ConvParams &p) {
+// 16- or 8-byte boundary, else 1. The gradient keeps 4 W + 5 sums and rows per
+// channel in registers and takes 4 at most (T = D = 8192: 8 take 291 us).
+int conv_vec(const ConvParams &p, int most) {
     for (int v : {8, 4}) {
         const int64_t b = 2 * v;
-        if (p.dim % v == 0 && aligned(p.x, p.x_stride, b, 2) && aligned(p.out, p.out_stride, b, 2) &&
-            aligned(p.hist_in, p.dim, b, 2) && aligned(p.hist_out, p.dim, b, 2) &&
+        if (v <= most && p.dim % v == 0 && aligned(p.x, p.x_stride, b, 2) &&
+            aligned(p.out, p.out_stride, b, 2) && aligned(p.hist_in, p.dim, b, 2) &&
+            aligned(p.hist_out, p.dim, b, 2) &&
             aligned(p.dout, p.dout_stride, p.dout32 ? 16 : b, p.dout32 ? 4 : 2) &&
             aligned(p.dhist_in, p.dim, 16, 4) && aligned(p.dhist_out, p.dim, 16, 4))
             return v;
@@ -406,17 +514,17 @@ int conv_vec(const ConvParams &p) {
     return 1;
 }
 
-template <typename F>
+template <int MOST, typename F>
 cudaError_t with_shape(const ConvParams &p, F &&go) {
     auto silu = [&](auto w, auto v) {
         return p.silu ? go(w, v, std::true_type()) : go(w, v, std::false_type());
     };
     auto vec = [&](auto w) {
-        switch (conv_vec(p)) {
-            case 8: return silu(w, std::integral_constant<int, 8>());
-            case 4: return silu(w, std::integral_constant<int, 4>());
-            default: return silu(w, std::integral_constant<int, 1>());
-        }
+        const int v = conv_vec(p, MOST);
+        if constexpr (MOST == 8)
+            if (v == 8) return silu(w, std::integral_constant<int, 8>());
+        return v == 4 ? silu(w, std::integral_constant<int, 4>())
+                      : silu(w, std::integral_constant<int, 1>());
     };
     switch (p.width) {
         case 2: return vec(std::integral_constant<int, 2>());
@@ -425,48 +533,56 @@ cudaError_t with_shape(const ConvParams &p, F &&go) {
     }
 }
 
+int64_t tiles_of(int64_t tokens, int64_t run) {
+    const int64_t t = (tokens + run * kWarps - 1) / (run * kWarps);
+    return t > 0 ? t : 1;   // no tokens: the histories are still handed on
+}
+
 }  // namespace
 
 cudaError_t launch_conv(const ConvParams &p, cudaStream_t stream) {
-    return with_shape(p, [&](auto w, auto v, auto s) {
+    if (p.tokens == 0 && p.hist_out == nullptr) return cudaSuccess;
+    return with_shape<4>(p, [&](auto w, auto v, auto s) {
         constexpr int W = decltype(w)::value, VEC = decltype(v)::value;
-        const int64_t cols = (p.dim + 32 * VEC - 1) / (32 * VEC);
-        const int run = kRun;
-        int64_t tiles = (p.tokens + run * kWarps - 1) / (run * kWarps);
-        if (tiles == 0) tiles = 1;   // no tokens: the histories are still handed on
-        if (p.tokens == 0 && p.hist_out == nullptr) return cudaSuccess;
+        const int64_t cols = (p.dim + 32 * VEC - 1) / (32 * VEC), run = run_for(p.tokens, cols);
         conv_kernel<W, VEC, decltype(s)::value>
-            <<<static_cast<unsigned>(tiles * cols), kWarps * 32, 0, stream>>>(p, run, cols);
+            <<<static_cast<unsigned>(tiles_of(p.tokens, run) * cols), kWarps * 32, 0, stream>>>(
+                p, static_cast<int>(run), cols);
         return cudaGetLastError();
     });
 }
 
 cudaError_t launch_conv_step(const ConvParams &p, cudaStream_t stream) {
-    return with_shape(p, [&](auto w, auto v, auto s) {
+    return with_shape<8>(p, [&](auto w, auto v, auto s) {
         constexpr int W = decltype(w)::value, VEC = decltype(v)::value;
-        const int64_t cols = (p.dim + VEC - 1) / VEC;
+        const int64_t cols = (p.dim + 32 * VEC - 1) / (32 * VEC);
+        const int64_t rows = (p.tokens + kWarps * kStepRows - 1) / (kWarps * kStepRows);
         conv_step_kernel<W, VEC, decltype(s)::value>
-            <<<static_cast<unsigned>((p.tokens * cols + 255) / 256), 256, 0, stream>>>(p, cols);
+            <<<static_cast<unsigned>(rows * cols), kWarps * 32, 0, stream>>>(p, cols);
         return cudaGetLastError();
     });
 }
 
-int64_t conv_backward_tiles(int64_t tokens) {
-    const int64_t t = (tokens + kRun * kWarps - 1) / (kRun * kWarps);
-    return t > 0 ? t : 1;
+// Partial sums of the weights' gradients; with 4 channels per thread the runs are the
+// shortest.
+int64_t conv_backward_tiles(int64_t tokens, int64_t dim) {
+    return tiles_of(tokens, run_for(tokens, (dim + 127) / 128));
 }
 
 cudaError_t launch_conv_backward(const ConvParams &p, cudaStream_t stream) {
-    const int64_t tiles = conv_backward_tiles(p.tokens);
-    const cudaError_t e = with_shape(p, [&](auto w, auto v, auto s) {
+    int64_t tiles = 0;
+    const cudaError_t e = with_shape<4>(p, [&](auto w, auto v, auto s) {
         constexpr int W = decltype(w)::value, VEC = decltype(v)::value;
         constexpr bool S = decltype(s)::value;
-        const int64_t cols = (p.dim + 32 * VEC - 1) / (32 * VEC);
+        const int64_t cols = (p.dim + 32 * VEC - 1) / (32 * VEC), run = run_for(p.tokens, cols);
+        tiles = tiles_of(p.tokens, run);
         const unsigned grid = static_cast<unsigned>(tiles * cols);
         if (p.dout32)
-            conv_backward_kernel<W, VEC, S, true><<<grid, kWarps * 32, 0, stream>>>(p, cols);
+            conv_backward_kernel<W, VEC, S, true>
+                <<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(run), cols);
         else
-            conv_backward_kernel<W, VEC, S, false><<<grid, kWarps * 32, 0, stream>>>(p, cols);
+            conv_backward_kernel<W, VEC, S, false>
+                <<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(run), cols);
         return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;

@@ -183,7 +183,7 @@ kda_status kda_short_conv_backward(const void *x, const float *weight, const flo
     const void *ptrs[] = {x, weight, bias, initial_state, cu_seqlens, d_out, d_final_state, dx,
                           dweight, dbias, d_initial_state};
     kda::CallContext ctx;
-    const int64_t ws = kda::conv_backward_tiles(tokens) * (W + 1) * D * 4;
+    const int64_t ws = kda::conv_backward_tiles(tokens, D) * (W + 1) * D * 4;
     rc = static_cast<kda_status>(kda::begin_call(ptrs, 11, stream, ws, 0, &ctx));
     if (rc != KDA_OK) return rc;
     kda::ConvParams p{};
