@@ -217,6 +217,7 @@ kda_status init_device(int dev, DeviceState &st) {
     if (kda::configure_recurrent() != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::configure_c64() != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::configure_backward_chunk() != cudaSuccess) return KDA_ERR_CUDA;
+    if (kda::configure_conv() != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::configure_ssm() != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::configure_paged() != cudaSuccess) return KDA_ERR_CUDA;
     if (cudaDeviceGetAttribute(&st.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

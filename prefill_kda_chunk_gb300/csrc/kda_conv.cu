@@ -122,7 +122,7 @@ __device__ __forceinline__ void silu(float (&z)[VEC]) {
 
 // The filters of a block's 32 VEC channels, read once and kept tap by tap in shared
 // memory: read from [D, W] by each thread, their scattered sectors cost more than
-// the rows (T = D = 8192: 115 us against 57).
+// the rows (T = D = 8192: 115 us against 84).
 template <int W, int VEC>
 struct Filters {
     float w[W + 1][32 * VEC];   // the taps, then the bias
@@ -136,6 +136,19 @@ struct Filters {
         __syncthreads();
     }
 };
+
+// Asynchronous copy of one thread's piece of a row to its own place in shared memory.
+template <typename T>
+__device__ __forceinline__ void copy_piece(T *dst, const void *src) {
+    if constexpr (sizeof(T) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_but(int) {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
 
 // The filter of a thread's channels.
 template <int W, int VEC>
@@ -184,20 +197,37 @@ __device__ __forceinline__ void step_window(const Filter<W, VEC> &f, float (&win
     }
 }
 
-// Rows per warp: enough that the W - 1 rows read twice are few (9 % at 32, out of L2),
-// but fewer when the call would leave SMs without a block.
-constexpr int kRun = 32, kMinRun = 4;
-int64_t run_for(int64_t tokens, int64_t cols) {
-    const int64_t blocks = (2 * 152 + cols - 1) / cols;   // along the tokens, two per SM
-    int64_t run = (tokens + blocks * kWarps - 1) / (blocks * kWarps);
-    run = (run + kMinRun - 1) / kMinRun * kMinRun;
-    return run < kMinRun ? kMinRun : run > kRun ? kRun : run;
+// Rows per warp: at most `most`, and such that the blocks fill whole waves of two per
+// SM. The W - 1 rows read twice are 5 % at 64 (out of L2), and the gradient's W - 1
+// tokens worked on twice are as many, so that it takes longer runs (T = D = 8192:
+// runs of 64, 96 and 128 rows at most take 110, 103 and 99 us, the forward's 53, 53 and
+// 55).
+constexpr int kRun = 64, kBackRun = 128, kMinRun = 4, kSlots = 2 * 152;
+int64_t run_for(int64_t tokens, int64_t cols, int64_t most) {
+    int64_t run = most;
+    for (int64_t waves = 1;; ++waves) {
+        const int64_t blocks = kSlots * waves / cols > 0 ? kSlots * waves / cols : 1;   // along the tokens
+        run = (tokens + blocks * kWarps - 1) / (blocks * kWarps);
+        if (run <= most) break;
+        if (waves == 16) return most;   // (many waves: they need not be whole)
+    }
+    return run < kMinRun ? kMinRun : run;
+}
+
+constexpr int kGroup = 4, kDepth = 4;   // rows of a group, groups of the ring
+constexpr int kForwardVec = 8;
+template <int VEC>
+constexpr int ring_bytes() {
+    return VEC > 1 ? kDepth * kGroup * kWarps * 32 * 2 * VEC : 0;
 }
 
 template <int W, int VEC, bool SILU>
-__global__ void __launch_bounds__(kWarps * 32, 3)
+__global__ void __launch_bounds__(kWarps * 32, VEC == 4 ? 3 : 2)
 conv_kernel(ConvParams p, int run, int64_t col_blocks) {
+    extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(16) Filters<W, VEC> filters;
+    using R = typename Raw<VEC>::T;
+    R *ring = reinterpret_cast<R *>(smem) + threadIdx.x;
     const Seqs seqs{p.cu, p.seq_len, p.n_seqs};
     if (!check_cu(seqs, p.tokens, p.err)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -216,7 +246,6 @@ conv_kernel(ConvParams p, int run, int64_t col_blocks) {
         const int64_t lo = a > t0 ? a : t0, hi = b < t1 ? b : t1;
         float win[W - 1][VEC];
         load_window<W, VEC>(p, n, a, lo, d, win);
-        using R = typename Raw<VEC>::T;
         const uint16_t *src = static_cast<const uint16_t *>(p.x) + lo * p.x_stride + d;
         uint16_t *dst = static_cast<uint16_t *>(p.out) + lo * p.out_stride + d;
         auto row_out = [&](const R &raw, uint16_t *to) {
@@ -226,27 +255,39 @@ conv_kernel(ConvParams p, int run, int64_t col_blocks) {
             if (SILU) silu<VEC>(z);
             *reinterpret_cast<R *>(to) = narrow<VEC>(z);
         };
-        constexpr int U = 8;   // rows in flight
-        int left = static_cast<int>(hi - lo);
+        const int rows = static_cast<int>(hi - lo);
+        if constexpr (VEC > 1) {
+            // groups of kGroup rows pass through a ring in shared memory, kDepth - 1
+            // of them in flight; a thread reads only what it copied itself
+            auto fetch = [&](int r0) {
+                R *to = ring + r0 / kGroup % kDepth * kGroup * kWarps * 32;
+#pragma unroll
+                for (int u = 0; u < kGroup; ++u) {
+                    if (r0 + u < rows) copy_piece(to + u * kWarps * 32, src);
+                    src += p.x_stride;
+                }
+                cp_async_commit();
+            };
+#pragma unroll
+            for (int g = 0; g < kDepth - 1; ++g) fetch(g * kGroup);
 #pragma unroll 1
-        for (; left >= U; left -= U) {
-            R raw[U];
+            for (int r0 = 0; r0 < rows; r0 += kGroup) {
+                fetch(r0 + (kDepth - 1) * kGroup);
+                copies_but<kDepth - 1>(0);
+                const R *from = ring + r0 / kGroup % kDepth * kGroup * kWarps * 32;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                raw[u] = *reinterpret_cast<const R *>(src);
-                src += p.x_stride;
+                for (int u = 0; u < kGroup; ++u) {
+                    if (r0 + u < rows) row_out(from[u * kWarps * 32], dst);
+                    dst += p.out_stride;
+                }
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                row_out(raw[u], dst);
+        } else {
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r) {
+                row_out(*reinterpret_cast<const R *>(src), dst);
+                src += p.x_stride;
                 dst += p.out_stride;
             }
-        }
-#pragma unroll 1
-        for (; left > 0; --left) {
-            row_out(*reinterpret_cast<const R *>(src), dst);
-            src += p.x_stride;
-            dst += p.out_stride;
         }
         if (b <= t1 && p.hist_out != nullptr) {
 #pragma unroll
@@ -316,10 +357,25 @@ __global__ void __launch_bounds__(kWarps * 32) conv_step_kernel(ConvParams p, in
 // eight warps are joined in shared memory in warp order and written per tile;
 // conv_reduce_kernel adds the tiles in order, so the result does not depend on
 // timing.
+constexpr int kBackGroup = 4, kBackDepth = 3;
+template <int W, int VEC, bool D32>
+constexpr int back_bytes() {
+    const int ring = VEC > 1 ? kBackDepth * kBackGroup * kWarps * 32 * VEC * (2 + (D32 ? 4 : 2)) : 0;
+    const int sums = kWarps * (W + 1) * VEC * 32 * 4;
+    return ring > sums ? ring : sums;
+}
+
 template <int W, int VEC, bool SILU, bool D32>
 __global__ void __launch_bounds__(kWarps * 32, 2)
 conv_backward_kernel(ConvParams p, int run, int64_t col_blocks) {
-    __shared__ float sums[kWarps][(W + 1) * VEC * 32];
+    extern __shared__ __align__(16) uint8_t smem[];   // the ring, then the warps' sums
+    using R = typename Raw<VEC>::T;
+    using G1 = std::conditional_t<D32, float, uint16_t>;
+    using G = std::conditional_t<D32, std::conditional_t<VEC == 1, float, float4>, R>;
+    float(*sums)[(W + 1) * VEC * 32] = reinterpret_cast<float(*)[(W + 1) * VEC * 32]>(smem);
+    constexpr int kPieces = kBackDepth * kBackGroup * kWarps * 32;
+    G *dring = reinterpret_cast<G *>(smem) + threadIdx.x;
+    R *ring = reinterpret_cast<R *>(smem + kPieces * sizeof(G)) + threadIdx.x;
     __shared__ __align__(16) Filters<W, VEC> filters;
     const Seqs seqs{p.cu, p.seq_len, p.n_seqs};
     if (!check_cu(seqs, p.tokens, p.err)) return;
@@ -363,18 +419,8 @@ conv_backward_kernel(ConvParams p, int run, int64_t col_blocks) {
                                    v);
                 }
             };
-            using R = typename Raw<VEC>::T;
             const uint16_t *src = static_cast<const uint16_t *>(p.x) + lo * p.x_stride + d;
             int64_t at = lo * p.dout_stride + d;
-            auto load = [&](R &raw, float (&g)[VEC]) {
-                raw = *reinterpret_cast<const R *>(src);
-                if constexpr (D32)
-                    load_f32<VEC>(static_cast<const float *>(p.dout) + at, g);
-                else
-                    widen<VEC>(load_row<VEC>(p.dout, at), g);
-                src += p.x_stride;
-                at += p.dout_stride;
-            };
             // token t: dz completes row t - (W - 1), which goes to `done`
             auto token = [&](const R &raw, const float (&g)[VEC], bool own, float (&done)[VEC]) {
                 float row[VEC], z[VEC], sg[VEC];
@@ -406,39 +452,67 @@ conv_backward_kernel(ConvParams p, int run, int64_t col_blocks) {
                     win[W - 2][i] = row[i];
                 }
             };
-            int64_t t = lo;
-            // the first W - 1 tokens complete rows in front of this run: the history's
-#pragma unroll 1
-            for (; t < end && t < lo + W - 1; ++t) {
-                R raw;
-                float g[VEC], done[VEC];
-                load(raw, g);
-                token(raw, g, t < hi, done);
-                emit(t - (W - 1), done);
-            }
-            constexpr int U = 4;   // rows in flight
-            uint16_t *dst = static_cast<uint16_t *>(p.out) + (t - (W - 1)) * p.out_stride + d;
-#pragma unroll 1
-            for (; t + U <= hi; t += U) {
-                R raw[U];
-                float g[U][VEC];
+            const int rows = static_cast<int>(end - lo), own = static_cast<int>(hi - lo);
+            auto gradient = [&](const G &got, float (&g)[VEC]) {
+                if constexpr (D32) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) load(raw[u], g[u]);
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float done[VEC];
-                    token(raw[u], g[u], true, done);
-                    *reinterpret_cast<R *>(dst) = narrow<VEC>(done);
-                    dst += p.out_stride;
+                    for (int i = 0; i < VEC; ++i) g[i] = reinterpret_cast<const float *>(&got)[i];
+                } else {
+                    widen<VEC>(got, g);
                 }
-            }
-#pragma unroll 1
-            for (; t < end; ++t) {
-                R raw;
+            };
+            // row r of the run: the first W - 1 complete rows of the history or none
+            auto one = [&](int r, const R &raw, const G &got) {
                 float g[VEC], done[VEC];
-                load(raw, g);
-                token(raw, g, t < hi, done);
-                emit(t - (W - 1), done);
+                gradient(got, g);
+                token(raw, g, r < own, done);
+                emit(lo + r - (W - 1), done);
+            };
+            if constexpr (VEC > 1) {
+                // through a ring as in the forward
+                auto fetch = [&](int r0) {
+                    const int to = r0 / kBackGroup % kBackDepth * kBackGroup * kWarps * 32;
+#pragma unroll
+                    for (int u = 0; u < kBackGroup; ++u) {
+                        if (r0 + u < rows) {
+                            copy_piece(ring + to + u * kWarps * 32, src);
+                            copy_piece(dring + to + u * kWarps * 32, static_cast<const G1 *>(p.dout) + at);
+                        }
+                        src += p.x_stride;
+                        at += p.dout_stride;
+                    }
+                    cp_async_commit();
+                };
+#pragma unroll
+                for (int g = 0; g < kBackDepth - 1; ++g) fetch(g * kBackGroup);
+                uint16_t *dst = static_cast<uint16_t *>(p.out) + (lo - (W - 1)) * p.out_stride + d;
+#pragma unroll 1
+                for (int r0 = 0; r0 < rows; r0 += kBackGroup) {
+                    fetch(r0 + (kBackDepth - 1) * kBackGroup);
+                    copies_but<kBackDepth - 1>(0);
+                    const int from = r0 / kBackGroup % kBackDepth * kBackGroup * kWarps * 32;
+                    if (r0 >= W - 1 && r0 + kBackGroup <= own) {
+#pragma unroll
+                        for (int u = 0; u < kBackGroup; ++u) {
+                            float g[VEC], done[VEC];
+                            gradient(dring[from + u * kWarps * 32], g);
+                            token(ring[from + u * kWarps * 32], g, true, done);
+                            *reinterpret_cast<R *>(dst + u * p.out_stride) = narrow<VEC>(done);
+                        }
+                    } else {
+#pragma unroll 1
+                        for (int u = 0; u < kBackGroup && r0 + u < rows; ++u)
+                            one(r0 + u, ring[from + u * kWarps * 32], dring[from + u * kWarps * 32]);
+                    }
+                    dst += kBackGroup * p.out_stride;
+                }
+            } else {
+#pragma unroll 2
+                for (int r = 0; r < rows; ++r) {
+                    one(r, *reinterpret_cast<const R *>(src), static_cast<const G1 *>(p.dout)[at]);
+                    src += p.x_stride;
+                    at += p.dout_stride;
+                }
             }
             if (end == b) {   // the rows that final_state holds
 #pragma unroll
@@ -454,6 +528,7 @@ conv_backward_kernel(ConvParams p, int run, int64_t col_blocks) {
             }
         }
     }
+    __syncthreads();   // the ring is read
     float *mine = sums[warp];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
@@ -540,13 +615,43 @@ int64_t tiles_of(int64_t tokens, int64_t run) {
 
 }  // namespace
 
+cudaError_t configure_conv() {
+    auto raise = [](auto kernel, int bytes) {
+        return bytes > 0 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes)
+                         : cudaSuccess;
+    };
+    for (int width = 2; width <= 4; ++width)
+        for (int vec : {1, 4, 8})
+            for (bool silu : {false, true}) {
+                ConvParams p{};   // (no arrays: the channels alone choose the form)
+                p.width = width;
+                p.dim = vec;
+                p.silu = silu;
+                cudaError_t e = with_shape<8>(p, [&](auto w, auto v, auto s) {
+                    constexpr int W = decltype(w)::value, VEC = decltype(v)::value;
+                    return raise(conv_kernel<W, VEC, decltype(s)::value>, ring_bytes<VEC>());
+                });
+                if (e != cudaSuccess) return e;
+                e = with_shape<4>(p, [&](auto w, auto v, auto s) {
+                    constexpr int W = decltype(w)::value, VEC = decltype(v)::value;
+                    constexpr bool S = decltype(s)::value;
+                    const cudaError_t r =
+                        raise(conv_backward_kernel<W, VEC, S, true>, back_bytes<W, VEC, true>());
+                    return r != cudaSuccess
+                               ? r : raise(conv_backward_kernel<W, VEC, S, false>, back_bytes<W, VEC, false>());
+                });
+                if (e != cudaSuccess) return e;
+            }
+    return cudaSuccess;
+}
+
 cudaError_t launch_conv(const ConvParams &p, cudaStream_t stream) {
     if (p.tokens == 0 && p.hist_out == nullptr) return cudaSuccess;
-    return with_shape<4>(p, [&](auto w, auto v, auto s) {
+    return with_shape<kForwardVec>(p, [&](auto w, auto v, auto s) {
         constexpr int W = decltype(w)::value, VEC = decltype(v)::value;
-        const int64_t cols = (p.dim + 32 * VEC - 1) / (32 * VEC), run = run_for(p.tokens, cols);
+        const int64_t cols = (p.dim + 32 * VEC - 1) / (32 * VEC), run = run_for(p.tokens, cols, kRun);
         conv_kernel<W, VEC, decltype(s)::value>
-            <<<static_cast<unsigned>(tiles_of(p.tokens, run) * cols), kWarps * 32, 0, stream>>>(
+            <<<static_cast<unsigned>(tiles_of(p.tokens, run) * cols), kWarps * 32, ring_bytes<VEC>(), stream>>>(
                 p, static_cast<int>(run), cols);
         return cudaGetLastError();
     });
@@ -566,7 +671,7 @@ cudaError_t launch_conv_step(const ConvParams &p, cudaStream_t stream) {
 // Partial sums of the weights' gradients; with 4 channels per thread the runs are the
 // shortest.
 int64_t conv_backward_tiles(int64_t tokens, int64_t dim) {
-    return tiles_of(tokens, run_for(tokens, (dim + 127) / 128));
+    return tiles_of(tokens, run_for(tokens, (dim + 127) / 128, kBackRun));
 }
 
 cudaError_t launch_conv_backward(const ConvParams &p, cudaStream_t stream) {
@@ -574,15 +679,15 @@ cudaError_t launch_conv_backward(const ConvParams &p, cudaStream_t stream) {
     const cudaError_t e = with_shape<4>(p, [&](auto w, auto v, auto s) {
         constexpr int W = decltype(w)::value, VEC = decltype(v)::value;
         constexpr bool S = decltype(s)::value;
-        const int64_t cols = (p.dim + 32 * VEC - 1) / (32 * VEC), run = run_for(p.tokens, cols);
+        const int64_t cols = (p.dim + 32 * VEC - 1) / (32 * VEC), run = run_for(p.tokens, cols, kBackRun);
         tiles = tiles_of(p.tokens, run);
         const unsigned grid = static_cast<unsigned>(tiles * cols);
         if (p.dout32)
             conv_backward_kernel<W, VEC, S, true>
-                <<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(run), cols);
+                <<<grid, kWarps * 32, back_bytes<W, VEC, true>(), stream>>>(p, static_cast<int>(run), cols);
         else
             conv_backward_kernel<W, VEC, S, false>
-                <<<grid, kWarps * 32, 0, stream>>>(p, static_cast<int>(run), cols);
+                <<<grid, kWarps * 32, back_bytes<W, VEC, false>(), stream>>>(p, static_cast<int>(run), cols);
         return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;

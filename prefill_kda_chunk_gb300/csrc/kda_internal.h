@@ -251,6 +251,7 @@ struct ConvParams {
     float *dweight, *dbias;    // gradient: [D, W], [D] or nullptr
     int *err;
 };
+cudaError_t configure_conv();
 int64_t conv_backward_tiles(int64_t tokens, int64_t dim);
 cudaError_t launch_conv(const ConvParams &p, cudaStream_t stream);
 cudaError_t launch_conv_step(const ConvParams &p, cudaStream_t stream);
