@@ -63,7 +63,7 @@ struct Shape {
     static constexpr int kOut = D + 4;                       // padded floats of an output row
     static constexpr int kSmem = kPagedWarps * kWarpBytes;
     static constexpr int kSlot = kHeads * (D + 2);           // floats of one partial result
-    static_assert(kHeads * kOut * 4 <= kWarpBytes, "outputs reuse the ring");
+    static_assert(8 * kOut * 4 <= kStage, "outputs go through a slot of the ring");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -103,6 +103,38 @@ __device__ __forceinline__ int owner(int64_t u, int64_t U, int64_t G) {
     return static_cast<int>(((u + 1) * G - 1) / U);
 }
 
+// A CTA's way through its share [u, u1) of the units, piece by piece.
+struct Pieces {
+    int64_t u, u1, seq_at;   // next unit; end of the share; first unit of sequence b
+    int b;
+    // the piece: its item, and the tiles of it
+    int len, tiles, item, tile0, tile1;
+    int64_t item_at;
+
+    __device__ __forceinline__ bool next(const PagedParams &p, int items) {
+        while (u < u1) {
+            bool ignore = false;
+            len = length_of(p, b, &ignore);
+            const int64_t units = units_of(len);
+            if (u >= seq_at + units * items) {
+                seq_at += units * items;
+                ++b;
+                continue;
+            }
+            tiles = static_cast<int>(units) - kItemCost;
+            item = static_cast<int>((u - seq_at) / units);
+            item_at = seq_at + item * units;
+            const int64_t tile_at = item_at + kItemCost;
+            // the tiles among the units [u, min(u1, end of the item))
+            tile0 = static_cast<int>(u > tile_at ? u - tile_at : 0);
+            tile1 = static_cast<int>(u1 - tile_at < tiles ? u1 - tile_at : tiles);
+            u = item_at + units;
+            if (tile0 < tile1) return true;
+        }
+        return false;
+    }
+};
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kPagedWarps * 32, kPagedCtasPerSm)
 paged_kernel(PagedParams p, float *slots, int *arrived) {
@@ -110,7 +142,7 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_sum[kPagedWarps], s_off;
     __shared__ int s_first, s_last;
-    __shared__ float s_m[kPagedWarps][S::kHeads], s_l[kPagedWarps][S::kHeads];
+    __shared__ float s_m[kPagedWarps][8], s_l[kPagedWarps][8];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = p.hq / p.hkv, chunks = (group + S::kHeads - 1) / S::kHeads;
     const int items = p.hkv * chunks;   // work items of a sequence
@@ -165,39 +197,73 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
         s_off = at;
     }
     __syncthreads();
-    int b = s_first;
-    int64_t seq_at = s_off;   // first unit of sequence b
 
     uint8_t *ring = smem + warp * S::kWarpBytes;
     const uint32_t ring_u = smem_u32(ring);
     const float to_log2 = p.scale * 1.44269504088896341f;
     const int q4 = lane & 3, r8 = lane >> 2;
 
-    for (int64_t u = u0; u < u1;) {
-        bool ignore = false;
-        const int len = length_of(p, b, &ignore);
-        const int64_t units = units_of(len);
-        if (u >= seq_at + units * items) {
-            seq_at += units * items;
-            ++b;
-            continue;
+    // ---- copies: they run kStages - 1 strips ahead, across the ends of pieces. The
+    // page of this lane's token (lanes 16..31 repeat 0..15) is read a strip earlier.
+    Pieces ahead{u0, u1, s_off, s_first};
+    bool more = ahead.next(p, items);
+    int tile = ahead.tile0, page = 0;
+    auto page_of = [&] {
+        const int t = tile * kTile + warp * kStrip + (lane & 15);
+        page = more && t < ahead.len
+                   ? __ldg(p.table + static_cast<int64_t>(ahead.b) * p.max_pages + t / p.page_size)
+                   : 0;
+    };
+    int loaded = 0;   // strips
+    auto load = [&] {
+        if (more) {
+            const int tok0 = tile * kTile + warp * kStrip, t = tok0 + (lane & 15), len = ahead.len;
+            const int kv = ahead.item / chunks;
+            int pg = page;
+            if (++tile == ahead.tile1) {
+                more = ahead.next(p, items);
+                tile = ahead.tile0;
+            }
+            page_of();
+            if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.pages)) {
+                if (t < len) atomicOr(p.err, kErrPage);
+                pg = 0;
+            }
+            const int64_t in = (static_cast<int64_t>(t % p.page_size) * p.hkv + kv) * D;
+            const int64_t ka = pg * p.k_stride + in, va = pg * p.v_stride + in;
+            const uint32_t dst = ring_u + loaded % kStages * S::kStage;
+            constexpr int G16 = D / 8;             // 16-byte granules of a row
+            constexpr int R = 32 / G16;            // rows per instruction
+            const int g = lane % G16;
+#pragma unroll
+            for (int i = 0; i < kStrip / R; ++i) {
+                const int row = i * R + lane / G16;
+                const int64_t kr = __shfl_sync(0xffffffffu, ka, row);
+                const int64_t vr = __shfl_sync(0xffffffffu, va, row);
+                const uint32_t at = dst + row * S::kRow + ((g ^ (row & 7)) << 4);
+                // rows past the end are zeros: whatever the page holds there stays unread
+                const uint32_t n = tok0 + row < len ? 16 : 0;
+                cp_async16(at, static_cast<const uint16_t *>(p.k) + kr + g * 8, n);
+                cp_async16(at + kStrip * S::kRow, static_cast<const uint16_t *>(p.v) + vr + g * 8, n);
+            }
+            ++loaded;
         }
-        const int tiles = static_cast<int>(units) - kItemCost;
-        const int item = static_cast<int>((u - seq_at) / units);
-        const int64_t item_at = seq_at + item * units, tile_at = item_at + kItemCost;
-        // the tiles among the units [u, min(u1, end of the item))
-        const int tile0 = static_cast<int>(u > tile_at ? u - tile_at : 0);
-        const int tile1 = static_cast<int>(u1 - tile_at < tiles ? u1 - tile_at : tiles);
-        u = item_at + units;
-        if (tile0 >= tile1) continue;
-        const int kv = item / chunks, head0 = kv * group + (item % chunks) * S::kHeads;
-        const int heads = min(S::kHeads, group - (item % chunks) * S::kHeads);
+        cp_async_commit();
+    };
+    page_of();
+#pragma unroll 1
+    for (int s = 0; s < kStages - 1; ++s) load();
 
+    Pieces w{u0, u1, s_off, s_first};
+    int taken = 0;   // strips
+    while (w.next(p, items)) {
+        const int kv = w.item / chunks, head0 = kv * group + w.item % chunks * S::kHeads;
+        const int heads = min(S::kHeads, group - w.item % chunks * S::kHeads);
         // ---- Q^T fragments: k = channel, n = head
         uint32_t qf[D / 16][NT][2];
         {
             const uint32_t *q = reinterpret_cast<const uint32_t *>(p.q) +
-                                (static_cast<int64_t>(b) * p.hq + head0) * (D / 2);
+                                (static_cast<int64_t>(w.b) * p.hq + head0) * (D / 2);
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 const int h = t * 8 + r8;
@@ -209,45 +275,6 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
             }
         }
 
-        const int tok_end = min(tile1 * kTile, len);
-        const int tok0 = tile0 * kTile + warp * kStrip;
-        const int strips = tok0 < tok_end ? (tok_end - tok0 + kTile - 1) / kTile : 0;
-        const int32_t *table = p.table + static_cast<int64_t>(b) * p.max_pages;
-
-        // Page of this lane's token (lanes 16..31 repeat 0..15) of a strip; the
-        // table is read one strip ahead of the copies that need it.
-        auto page_of = [&](int s) -> int {
-            const int t = tok0 + s * kTile + (lane & 15);
-            return t < tok_end && s < strips ? __ldg(table + t / p.page_size) : 0;
-        };
-        auto load = [&](int s, int page) {
-            if (s < strips) {
-                const int t = tok0 + s * kTile + (lane & 15);
-                if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) {
-                    if (t < tok_end) atomicOr(p.err, kErrPage);
-                    page = 0;
-                }
-                const int64_t in = (static_cast<int64_t>(t % p.page_size) * p.hkv + kv) * D;
-                const int64_t ka = page * p.k_stride + in, va = page * p.v_stride + in;
-                const uint32_t dst = ring_u + (s % kStages) * S::kStage;
-                constexpr int G16 = D / 8;             // 16-byte granules of a row
-                constexpr int R = 32 / G16;            // rows per instruction
-                const int g = lane % G16;
-#pragma unroll
-                for (int i = 0; i < kStrip / R; ++i) {
-                    const int row = i * R + lane / G16;
-                    const int64_t kr = __shfl_sync(0xffffffffu, ka, row);
-                    const int64_t vr = __shfl_sync(0xffffffffu, va, row);
-                    const uint32_t at = dst + row * S::kRow + ((g ^ (row & 7)) << 4);
-                    // rows past the end are zeros: whatever the page holds there stays unread
-                    const uint32_t n = tok0 + s * kTile + row < tok_end ? 16 : 0;
-                    cp_async16(at, static_cast<const uint16_t *>(p.k) + kr + g * 8, n);
-                    cp_async16(at + kStrip * S::kRow, static_cast<const uint16_t *>(p.v) + vr + g * 8, n);
-                }
-            }
-            cp_async_commit();
-        };
-
         float o[D / 16][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -258,20 +285,13 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][t][e] = 0.f;
         }
-        int page = page_of(0);
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) {
-            const int next = page_of(s + 1);
-            load(s, page);
-            page = next;
-        }
-        for (int s = 0; s < strips; ++s) {
-            const int next = page_of(s + kStages);
+        for (int step = w.tile0; step < w.tile1; ++step, ++taken) {
             cp_async_wait<kStages - 2>();
             __syncwarp();
-            load(s + kStages - 1, page);   // into the slot that the last step freed
-            page = next;
-            const uint32_t ks = ring_u + (s % kStages) * S::kStage, vs = ks + kStrip * S::kRow;
+            load();   // into the slot that the last step freed
+            const int left = w.len - step * kTile - warp * kStrip;   // tokens of this strip, if < 16
+            if (left <= 0) continue;
+            const uint32_t ks = ring_u + taken % kStages * S::kStage, vs = ks + kStrip * S::kRow;
 
             // ---- S^T = K Q^T, two sums per tile to shorten the chain
             float st[NT][2][4];
@@ -287,7 +307,6 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t) mma16816(st[t][k & 1], a, qf[k][t][0], qf[k][t][1]);
             }
-            const int left = tok_end - (tok0 + s * kTile);   // tokens of this strip, if < 16
             uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -340,68 +359,73 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
             }
             __syncwarp();   // the slot is free once every lane has read it
         }
-        cp_async_wait<0>();
-        __syncwarp();
 
-        // ---- join the warps: each leaves its output in its ring
+        // ---- join the warps: 8 heads at a time, each warp's output through the slot of
+        // its ring that the last step freed
+        const bool whole = w.tile0 == 0 && w.tile1 == w.tiles;
+        // of a CTA's partial pieces only its first can belong to an item that
+        // started in front of its share, and only its last to another one
+        float *slot = slots + static_cast<int64_t>(2 * c + (u0 <= w.item_at)) * S::kSlot;
+        const int freed = (taken - 1) % kStages * S::kStage;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[t][j] += __shfl_xor_sync(0xffffffffu, l[t][j], d);
-                const int h = t * 8 + 2 * q4 + j;
+                const int h = 2 * q4 + j;
                 if (r8 == 0) {
                     s_m[warp][h] = m[t][j];
                     s_l[warp][h] = l[t][j];
                 }
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    float *row = reinterpret_cast<float *>(ring) + h * S::kOut + 16 * i + r8;
+                    float *row = reinterpret_cast<float *>(ring + freed) + h * S::kOut + 16 * i + r8;
                     row[0] = o[i][t][j];
                     row[8] = o[i][t][j + 2];
                 }
             }
-        }
-        __syncthreads();
-        const bool whole = tile0 == 0 && tile1 == tiles;
-        // of a CTA's partial pieces only its first can belong to an item that
-        // started in front of its share, and only its last to another one
-        float *slot = slots + static_cast<int64_t>(2 * c + (u0 <= item_at)) * S::kSlot;
-        for (int i = tid; i < heads * D; i += kPagedWarps * 32) {
-            const int h = i / D, d = i % D;
-            float top = -CUDART_INF_F;
+            __syncthreads();
 #pragma unroll
-            for (int w = 0; w < kPagedWarps; ++w) top = fmaxf(top, s_m[w][h]);
-            const float base = top == -CUDART_INF_F ? 0.f : top;
-            float acc = 0.f, sum = 0.f;
+            for (int i = tid; i < 8 * D; i += kPagedWarps * 32) {
+                const int h = i / D, d = i % D;
+                float top = -CUDART_INF_F;
 #pragma unroll
-            for (int w = 0; w < kPagedWarps; ++w) {
-                const float f = ex2(s_m[w][h] - base);
-                acc = fmaf(reinterpret_cast<const float *>(smem + w * S::kWarpBytes)[h * S::kOut + d], f, acc);
-                sum = fmaf(s_l[w][h], f, sum);
-            }
-            if (whole) {
-                const int64_t row = static_cast<int64_t>(b) * p.hq + head0 + h;
-                static_cast<__nv_bfloat16 *>(p.out)[row * D + d] =
-                    __float2bfloat16_rn(sum > 0.f ? acc / sum : sum == 0.f ? 0.f : sum);
-                if (d == 0 && p.lse != nullptr)
-                    p.lse[row] = sum == 0.f ? -CUDART_INF_F : base * 0.69314718055994531f + logf(sum);
-            } else {
-                slot[h * D + d] = acc;
-                if (d == 0) {
-                    slot[S::kHeads * D + h] = top;
-                    slot[S::kHeads * (D + 1) + h] = sum;
+                for (int v = 0; v < kPagedWarps; ++v) top = fmaxf(top, s_m[v][h]);
+                const float base = top == -CUDART_INF_F ? 0.f : top;
+                float acc = 0.f, sum = 0.f;
+#pragma unroll
+                for (int v = 0; v < kPagedWarps; ++v) {
+                    const float f = ex2(s_m[v][h] - base);
+                    acc = fmaf(reinterpret_cast<const float *>(smem + v * S::kWarpBytes + freed)[h * S::kOut + d],
+                               f, acc);
+                    sum = fmaf(s_l[v][h], f, sum);
+                }
+                if (8 * t + h >= heads) continue;
+                if (whole) {
+                    const int64_t row = static_cast<int64_t>(w.b) * p.hq + head0 + 8 * t + h;
+                    static_cast<__nv_bfloat16 *>(p.out)[row * D + d] =
+                        __float2bfloat16_rn(sum > 0.f ? acc / sum : sum == 0.f ? 0.f : sum);
+                    if (d == 0 && p.lse != nullptr)
+                        p.lse[row] = sum == 0.f ? -CUDART_INF_F : base * 0.69314718055994531f + logf(sum);
+                } else {
+                    slot[(8 * t + h) * D + d] = acc;
+                    if (d == 0) {
+                        slot[S::kHeads * D + 8 * t + h] = top;
+                        slot[S::kHeads * (D + 1) + 8 * t + h] = sum;
+                    }
                 }
             }
+            if (t + 1 < NT) __syncthreads();
         }
         if (!whole) {
             // ---- the last CTA of this (sequence, item) to arrive joins the pieces
-            const int c0 = owner(tile_at, U, G), c1 = owner(tile_at + tiles - 1, U, G);
+            const int c0 = owner(w.item_at + kItemCost, U, G),
+                      c1 = owner(w.item_at + kItemCost + w.tiles - 1, U, G);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
-                int *ctr = arrived + static_cast<int64_t>(b) * items + item;
+                int *ctr = arrived + static_cast<int64_t>(w.b) * items + w.item;
                 const int n = atomicAdd(ctr, 1) + 1;
                 s_last = n == c1 - c0 + 1;
                 if (s_last) *ctr = 0;   // for the next call
@@ -410,7 +434,7 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
             __syncthreads();
             if (s_last) {
                 auto piece = [&](int k) {
-                    const int last = k == c0 && k * U / G <= item_at;
+                    const int last = k == c0 && k * U / G <= w.item_at;
                     return slots + static_cast<int64_t>(2 * k + last) * S::kSlot;
                 };
                 for (int h = warp; h < heads; h += kPagedWarps) {
@@ -432,7 +456,7 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
                         for (int e = 0; e < D / 32; ++e)
                             acc[e] = fmaf(__ldcg(src + h * D + e * 32 + lane), f, acc[e]);
                     }
-                    const int64_t row = static_cast<int64_t>(b) * p.hq + head0 + h;
+                    const int64_t row = static_cast<int64_t>(w.b) * p.hq + head0 + h;
 #pragma unroll
                     for (int e = 0; e < D / 32; ++e)
                         static_cast<__nv_bfloat16 *>(p.out)[row * D + e * 32 + lane] =
