@@ -37,7 +37,7 @@ namespace {
 constexpr int kPagedWarps = 4;
 constexpr int kStrip = 16;                      // tokens per warp step
 constexpr int kTile = kPagedWarps * kStrip;     // tokens per tile of the split
-constexpr int kItemCost = 2;                    // start and end of an item, in tiles
+constexpr int kItemCost = 4;                    // start and end of an item, in tiles
 constexpr int kStages = 3;                      // strips in flight per warp
 constexpr int kPagedCtasPerSm = 2;
 constexpr int kPagedSms = 152;
