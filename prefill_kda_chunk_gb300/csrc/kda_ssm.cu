@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p) {
 
 // --------------------------------------------------------------- a prompt
 
+constexpr int UNR_DS = 1, UNR_CS = 1, UNR_CB = 1, UNR_MX = 1;
 constexpr int kL = 128;              // tokens per chunk
 constexpr int kPS = 64;              // channels of P per unit
 constexpr int kSsmSms = 152;
@@ -561,7 +562,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             tc::fence_after();
             const uint32_t B = desc_lo(sb + kOffB) + 2 * kTile * (i & 1);
             const uint32_t W = desc_lo(sb + off_w(kStates, i)), D = tm_ds(kStates, i);
-#pragma unroll
+#pragma unroll UNR_DS
             for (int k = 0; k < 3 * kL / 16; ++k) {   // the smallest term first
                 const int j = k % (kL / 16), t = 2 - k / (kL / 16);
                 mma_ss(D, B + j * kStepMN, W + t * kTile + j * kStepMN,
@@ -575,7 +576,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                     break;
                 tc::fence_after();
                 const uint32_t C = desc_lo(sb + kOffC), S = desc_lo(sb + kOffS);
-#pragma unroll
+#pragma unroll UNR_CS
                 for (int k = 0; k < kN / 8; ++k) {
                     const int j = k % (kN / 16);
                     mma_ss(kTmCS + 64 * (i & 1), C + (j >> 2) * kTile + (j & 3) * kStepK,
@@ -598,7 +599,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 tc::fence_after();
                 const uint32_t B = desc_lo(sb + kOffB) + 2 * kTile * ((i + 1) & 1), C = desc_lo(sb + kOffC);
                 const uint32_t D = kTmCB + 128 * ((i + 1) & 1);
-#pragma unroll
+#pragma unroll UNR_CB
                 for (int k = 0; k < kN / 16; ++k)
                     mma_ss(D, C + (k >> 2) * kTile + (k & 3) * kStepK, B + (k >> 2) * kTile + (k & 3) * kStepK,
                            tc::idesc(128, 128, 1), k);
@@ -609,7 +610,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             if (!all(wait(kXReady + (i & 1), i >> 1) && wait(kMReady + (i & 1), i >> 1))) break;
             tc::fence_after();
             const uint32_t X = desc_lo(sb + kOffX) + kTile * (i & 1), A = kTmCB + 128 * (i & 1);
-#pragma unroll
+#pragma unroll UNR_MX
             for (int k = 0; k < kL / 8; ++k)
                 mma_ts(kTmY, A + 8 * k, X + (k >> 1) * kStepMN, tc::idesc(128, kPS, 1) | kBMajor, k);
             mma_commit(bar(kMX + (i & 1)));
