@@ -121,7 +121,6 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p) {
 
 // --------------------------------------------------------------- a prompt
 
-constexpr int UNR_DS = 1, UNR_CS = 1, UNR_CB = 1, UNR_MX = 1;
 constexpr int kL = 128;              // tokens per chunk
 constexpr int kPS = 64;              // channels of P per unit
 constexpr int kSsmSms = 152;
@@ -129,9 +128,9 @@ constexpr int kSsmSms = 152;
 // MMAs of the state, one for those of y, one for the copies and one for the decays.
 constexpr int kGroup = 8;
 constexpr int kGroupThreads = 32 * kGroup;
-constexpr int kMmaWarpS = 2 * kGroup, kMmaWarpY = kMmaWarpS + 1, kCopyWarp = kMmaWarpS + 2,
-              kScalWarp = kMmaWarpS + 3;
-constexpr int kThreads = 32 * (kScalWarp + 1);
+constexpr int kScalWarp = 2 * kGroup, kMmaWarpS = kScalWarp + 1, kMmaWarpY = kScalWarp + 2,
+              kCopyWarp = kScalWarp + 3;
+constexpr int kThreads = 32 * (kCopyWarp + 1);
 constexpr int kRing = 4;             // chunks of decays computed ahead
 constexpr int kCols = 32;            // columns of the state and of y per compute thread
 
@@ -177,9 +176,10 @@ constexpr int kSmem = kOffMisc + 8;
 
 // Tensor memory columns; the block takes all of them, so they start at 0. C B^T has
 // two buffers of 128; M replaces it there: 16 columns (tokens s) become the 8 columns
-// of its high terms and the 8 of its low terms. C S has two buffers of 64. The launch
-// for the states works on two chunks at a time.
-constexpr uint32_t kTmCB = 0, kTmY = 256, kTmCS = 320, kTmDS = 448, kTmCols = 512;
+// of its high terms and the 8 of its low terms. C moves here for C S: its tile in shared
+// memory is free for the next chunk as soon as C B^T is formed, not only once the state
+// that C meets is there. The launch for the states works on two chunks at a time.
+constexpr uint32_t kTmCB = 0, kTmY = 256, kTmCS = 320, kTmC = 384, kTmDS = 448, kTmCols = 512;
 __device__ __forceinline__ uint32_t tm_ds(bool states, int i) {
     return states ? 64u * (i & 1) : kTmDS;
 }
@@ -200,24 +200,42 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) {
     return ((saddr >> 4) & 0x3FFF) | (static_cast<uint32_t>(kTileBytes >> 4) << 16);
 }
 
-// One MMA: D (+)= A B with both operands in shared memory, or A in tensor memory,
-// and the commit of those before it. The whole warp calls them and the instruction
-// elects a lane: descriptors then stay in uniform registers. (In a branch of one lane
-// an MMA of N = 64 took 77 cycles in a loop and 52 unrolled, this way 48 and 40.)
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+// Four MMAs, D (+)= A B, with both operands in shared memory, or A in tensor memory, and
+// the commit of those before them; the operands of the second to fourth lie A1.. and B1..
+// behind the first's, those in tensor memory 8 columns apart. The whole warp calls them and the instructions
+// elect a lane: descriptors then stay in uniform registers. (In a branch of one lane an
+// MMA of N = 64 took 77 cycles in a loop and 52 unrolled, this way 48 and 40. One elected
+// at a time, they took 120 and more beside the other warps' work: a dozen dependent
+// instructions each; unrolled throughout, as much for fetching them.)
+template <int A1, int A2, int A3, int B1, int B2, int B3>
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
     asm volatile(
-        "{\n .reg .pred p, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-        " mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi)
+        "{\n .reg .pred p, t, e;\n .reg .b32 u, v;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n"
+        " setp.eq.b32 t, 0, 0;\n elect.sync _|e, 0xffffffff;\n mov.b64 x, {%1, %5};\n mov.b64 y, {%2, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n"
+        " add.u32 u, %1, %6;\n add.u32 v, %2, %9;\n mov.b64 x, {u, %5};\n mov.b64 y, {v, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n"
+        " add.u32 u, %1, %7;\n add.u32 v, %2, %10;\n mov.b64 x, {u, %5};\n mov.b64 y, {v, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n"
+        " add.u32 u, %1, %8;\n add.u32 v, %2, %11;\n mov.b64 x, {u, %5};\n mov.b64 y, {v, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(static_cast<uint32_t>(acc)), "r"(kDescHi), "n"(A1), "n"(A2), "n"(A3),
+        "n"(B1), "n"(B2), "n"(B3)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+template <int B1, int B2, int B3>
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
     asm volatile(
-        "{\n .reg .pred p, e;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-        " mov.b64 y, {%2, %5};\n"
-        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi)
+        "{\n .reg .pred p, t, e;\n .reg .b32 u, v;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n"
+        " setp.eq.b32 t, 0, 0;\n elect.sync _|e, 0xffffffff;\n mov.b64 y, {%2, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n"
+        " add.u32 u, %1, 8;\n add.u32 v, %2, %6;\n mov.b64 y, {v, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, t;\n"
+        " add.u32 u, %1, 16;\n add.u32 v, %2, %7;\n mov.b64 y, {v, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, t;\n"
+        " add.u32 u, %1, 24;\n add.u32 v, %2, %8;\n mov.b64 y, {v, %5};\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %3, t;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(static_cast<uint32_t>(acc)), "r"(kDescHi), "n"(B1), "n"(B2), "n"(B3)
         : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
@@ -301,25 +319,21 @@ __device__ __forceinline__ void ld_wait16(uint32_t (&r)[16]) {
                  : "memory");
 }
 
-// A wait of at most 2^31 clocks (about a second) for a phase of an mbarrier, in
-// few instructions: this kernel waits in some twenty places, and with longer
-// waits at each of them its loops did not fit the instruction cache (a chunk
-// then took 3 times as long).
+// A wait for a phase of an mbarrier, of 2^18 polls at most (about
+// a second, as one that finds nothing takes some 7800 clocks), in few instructions: this
+// kernel waits in some twenty places, and with longer waits at each of them its
+// loops did not fit the instruction cache (a chunk then took 3 times as long). No clock
+// is read and no time to suspend given: a handshake of two warps that wait for one
+// another takes 126 cycles this way, 234 with both.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
-    const uint32_t t0 = static_cast<uint32_t>(clock());
-    bool ok;
-#pragma unroll 1
-    do {
-        // (suspended by the hardware for up to a millisecond: warps that poll would
-        // take the issue slots of those that work)
-        uint32_t r;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-            " selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(r) : "r"(bar), "r"(parity), "r"(1000000u) : "memory");
-        ok = r != 0;
-    } while (!ok && static_cast<int>(static_cast<uint32_t>(clock()) - t0) >= 0);
-    return ok;
+    uint32_t n;
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, 0;\n"
+        "again%=: mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra done%=;\n"
+        " add.u32 n, n, 1;\n setp.lt.u32 q, n, 262144;\n @q bra again%=;\n"
+        "done%=: mov.u32 %0, n;\n}\n"
+        : "=r"(n) : "r"(bar), "r"(parity) : "memory");
+    return n < 262144;
 }
 
 struct SsmMaps {
@@ -562,26 +576,24 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             tc::fence_after();
             const uint32_t B = desc_lo(sb + kOffB) + 2 * kTile * (i & 1);
             const uint32_t W = desc_lo(sb + off_w(kStates, i)), D = tm_ds(kStates, i);
-#pragma unroll UNR_DS
-            for (int k = 0; k < 3 * kL / 16; ++k) {   // the smallest term first
-                const int j = k % (kL / 16), t = 2 - k / (kL / 16);
-                mma_ss(D, B + j * kStepMN, W + t * kTile + j * kStepMN,
-                       tc::idesc(128, kPS, 1) | kAMajor | kBMajor, k);
-            }
+#pragma unroll 1
+            for (int k = 0; k < 6; ++k)   // the smallest term first
+                mma4_ss<kStepMN, 2 * kStepMN, 3 * kStepMN, kStepMN, 2 * kStepMN, 3 * kStepMN>(
+                    D, B + (k & 1) * 4 * kStepMN, W + (2 - (k >> 1)) * kTile + (k & 1) * 4 * kStepMN,
+                    tc::idesc(128, kPS, 1) | kAMajor | kBMajor, k > 0);
             mma_commit(bar(kDS + (i & 1)));
             if (!kStates) {
-                // C S, both terms of S, over that of two chunks before
-                if (!all(wait(kSReady, i) && wait(kFullC, i) &&
-                         (i < 2 || wait(kDone + (i & 1), (i >> 1) - 1))))
-                    break;
+                // C S, both terms of S, once that of the chunk before is read out
+                if (!all(wait(kSReady, i) && (i < 1 || wait(kDone + ((i - 1) & 1), (i - 1) >> 1)))) break;
                 tc::fence_after();
-                const uint32_t C = desc_lo(sb + kOffC), S = desc_lo(sb + kOffS);
-#pragma unroll UNR_CS
-                for (int k = 0; k < kN / 8; ++k) {
-                    const int j = k % (kN / 16);
-                    mma_ss(kTmCS + 64 * (i & 1), C + (j >> 2) * kTile + (j & 3) * kStepK,
-                           S + k / (kN / 16) * kTile + j * kStepMN, tc::idesc(128, kPS, 1) | kBMajor, k);
-                }
+                const uint32_t S = desc_lo(sb + kOffS);
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k)
+#pragma unroll 1
+                    for (int j = 0; j < kN / 64; ++j)
+                        mma4_ts<kStepMN, 2 * kStepMN, 3 * kStepMN>(
+                            kTmCS, kTmC + 32 * j, S + k * kTile + j * 4 * kStepMN,
+                            tc::idesc(128, kPS, 1) | kBMajor, k + j > 0);
                 mma_commit(bar(kCS + (i & 1)));
             }
         }
@@ -599,10 +611,10 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 tc::fence_after();
                 const uint32_t B = desc_lo(sb + kOffB) + 2 * kTile * ((i + 1) & 1), C = desc_lo(sb + kOffC);
                 const uint32_t D = kTmCB + 128 * ((i + 1) & 1);
-#pragma unroll UNR_CB
-                for (int k = 0; k < kN / 16; ++k)
-                    mma_ss(D, C + (k >> 2) * kTile + (k & 3) * kStepK, B + (k >> 2) * kTile + (k & 3) * kStepK,
-                           tc::idesc(128, 128, 1), k);
+#pragma unroll 1
+                for (int k = 0; k < kN / 64; ++k)
+                    mma4_ss<kStepK, 2 * kStepK, 3 * kStepK, kStepK, 2 * kStepK, 3 * kStepK>(
+                        D, C + k * kTile, B + k * kTile, tc::idesc(128, 128, 1), k > 0);
                 mma_commit(bar(kCB + ((i + 1) & 1)));
             }
             if (i < 0) continue;
@@ -610,9 +622,10 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             if (!all(wait(kXReady + (i & 1), i >> 1) && wait(kMReady + (i & 1), i >> 1))) break;
             tc::fence_after();
             const uint32_t X = desc_lo(sb + kOffX) + kTile * (i & 1), A = kTmCB + 128 * (i & 1);
-#pragma unroll UNR_MX
-            for (int k = 0; k < kL / 8; ++k)
-                mma_ts(kTmY, A + 8 * k, X + (k >> 1) * kStepMN, tc::idesc(128, kPS, 1) | kBMajor, k);
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k)
+                mma4_ts<0, kStepMN, kStepMN>(kTmY, A + 32 * k, X + 2 * k * kStepMN,
+                                             tc::idesc(128, kPS, 1) | kBMajor, k > 0);
             mma_commit(bar(kMX + (i & 1)));
         }
         drain(kDrain2);
@@ -625,7 +638,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
 #pragma unroll 1
                 for (int k = 0; k < n; ++k) tma_2d(sb + off + k * kTileBytes, &map, col + 64 * k, row, bar(full));
             };
-            int i = 0;
+            int i = 0, sent_c = 0;
 #pragma unroll 1
             for (; i < count; ++i) {
                 // what chunks i - 2 (b, x) and i - 1 (c) have left
@@ -634,12 +647,13 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 const int row = static_cast<int>(v.row), col = v.gcol, xcol = v.xcol, s = i & 1;
                 if (i > 1 && (!wait(kDS + s, (i >> 1) - 1) || (!kStates && !wait(kCB + s, (i >> 1) - 1)))) break;
                 copy(kFullB + s, kOffB + 2 * s * kTileBytes, maps.b, col, row, kN / 64);
+                if (!kStates) {   // (before x: the products of y wait for it)
+                    if (i > 0 && (!wait(kSReady, i - 1) || !wait(kCB + (s ^ 1), (i - 1) >> 1))) break;
+                    copy(kFullC, kOffC, maps.c, col, row, kN / 64);
+                    sent_c = i + 1;
+                }
                 if (!kStates && i > 1 && !wait(kMX + s, (i >> 1) - 1)) break;
                 copy(kFullX + s, kOffX + s * kTileBytes, maps.x, xcol, row, 1);
-                if (!kStates) {
-                    if (i > 0 && (!wait(kCS + (s ^ 1), (i - 1) >> 1) || !wait(kCB + (s ^ 1), (i - 1) >> 1))) break;
-                    copy(kFullC, kOffC, maps.c, col, row, kN / 64);
-                }
             }
             // the last copies land before the block ends (after a wait that gave up
             // nobody else may have waited for them)
@@ -647,7 +661,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 wait_phase(bar(kFullB + (j & 1)), (j >> 1) & 1);
                 wait_phase(bar(kFullX + (j & 1)), (j >> 1) & 1);
             }
-            if (!kStates && i > 0) wait_phase(bar(kFullC), (i - 1) & 1);
+            if (!kStates && sent_c > 0) wait_phase(bar(kFullC), (sent_c - 1) & 1);
             if (i < count) {   // (of the chunk it gave up at)
                 wait_phase(bar(kFullB + (i & 1)), (i >> 1) & 1);
                 wait_phase(bar(kFullX + (i & 1)), (i >> 1) & 1);
@@ -773,7 +787,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             for (int k = 0; k < 4; ++k) {   // 8 columns at a time
                 uint32_t y[8], cs[8];
                 ld8(lanes + kTmY + kCols * hf + 8 * k, y);
-                ld8(lanes + kTmCS + 64 * (i & 1) + kCols * hf + 8 * k, cs);
+                ld8(lanes + kTmCS + kCols * hf + 8 * k, cs);
                 tc::ld_wait();
                 uint32_t os[4];
 #pragma unroll
@@ -810,25 +824,20 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             const uint32_t at = lanes + kTmCB + 128 * (i & 1);
             const float hi_r = -s.hi[r], lo_r = -s.lo[r];
             const float dv = p.d != nullptr ? __ldg(p.d + (s.unit >> pl.shift)) : 0.f;
-            // rows of quarter 3: blocks (0, 1) and (2, 3); of quarter 2 (0, 1) and the
-            // diagonal; of the others one each; the rest, above the diagonal, is zero.
-            // 16 columns at a time, the next ones read before these are worked on.
-            const int step = q >= 2 ? 16 : 48;
+            // 16 columns at a time, the half hf of each 32-token block (so that both warps
+            // of these rows have as much of the diagonal), the next ones read before these
+            // are worked on; blocks above the diagonal are zero.
             uint32_t ahead[16] = {};
-            int next = (q >= 2 ? 64 : 32) * hf;
-            if (next >> 5 <= q) {
-                tc::ld16(at + next, ahead);
-                ld_wait16(ahead);
-            }
+            tc::ld16(at + 16 * hf, ahead);
+            ld_wait16(ahead);
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                const int col = next, b = col >> 5;
-                next = col + ((k & 1) != 0 ? step : 16);
+            for (int b = 0; b < 4; ++b) {
+                const int col = 32 * b + 16 * hf;
                 uint32_t v[16], hi[8], lo[8];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = ahead[j];
-                const bool more = k < 3 && next >> 5 <= q;
-                if (more) tc::ld16(at + next, ahead);
+                const bool more = b < q;
+                if (more) tc::ld16(at + col + 32, ahead);
                 if (b > q) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) hi[j] = lo[j] = 0u;
@@ -935,8 +944,8 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 for (int j = 0; j < kCols; ++j) pl.saved[slot + j * kGroupThreads] = S[j];
             }
         };
-        // S as two bf16 terms for C S
-        auto put_state = [&]() {
+        // S as two bf16 terms, and C, for C S of chunk i
+        auto put_state = [&](int i) -> bool {
             if (has) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -951,7 +960,21 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 }
             }
             fence_async();
+            if (!wait(kFullC, i)) return false;
+            constexpr int kHalf = kN / 16;   // 16-byte granules of half a row
+            const uint8_t *C = smem + kOffC + r * 128 + (kHalf * hf >> 3) * kTileBytes;
+#pragma unroll
+            for (int k = 0; k < kHalf; k += 2) {
+                const int g = (kHalf * hf & 7) + k;
+                const uint4 x = *reinterpret_cast<const uint4 *>(C + ((g ^ (r & 7)) << 4));
+                const uint4 y = *reinterpret_cast<const uint4 *>(C + (((g + 1) ^ (r & 7)) << 4));
+                const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                tc::st8(lanes + kTmC + 4 * (kHalf * hf + k), v);
+            }
+            tc::st_wait();
+            tc::fence_before();
             arrive(kSReady);
+            return true;
         };
 
         float run_decay = 1.f;   // over this part of the sequence
@@ -997,7 +1020,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 put_rows(i + 1, 4 * (warp - kGroup), 4);   // into the rows that this chunk's product has read
                 if (i < 0 || next.pos == 0) start_state(next);
                 if (i >= 0 && !(ok = wait(kCS + (i & 1), i >> 1))) break;   // the terms of S are read
-                put_state();
+                if (!(ok = put_state(i + 1))) break;
             }
         }
         if (kStates && ok) {
