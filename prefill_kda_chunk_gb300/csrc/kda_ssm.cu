@@ -41,6 +41,7 @@
 #include "kda_seqs.cuh"
 #include "kda_tcgen05.cuh"
 
+#include <cstddef>
 #include <type_traits>
 
 namespace kda {
@@ -125,13 +126,12 @@ constexpr int kL = 128;              // tokens per chunk
 constexpr int kPS = 64;              // channels of P per unit
 constexpr int kSsmSms = 152;
 // Warps: 0..7 form M and the outputs, 8..15 keep the state, then one for the
-// MMAs of the state, one for those of y, one for the copies and one for the decays.
+// MMAs of the state, one for those of y and one for the copies.
 constexpr int kGroup = 8;
 constexpr int kGroupThreads = 32 * kGroup;
-constexpr int kScalWarp = 2 * kGroup, kMmaWarpS = kScalWarp + 1, kMmaWarpY = kScalWarp + 2,
-              kCopyWarp = kScalWarp + 3;
+constexpr int kMmaWarpS = 2 * kGroup, kMmaWarpY = kMmaWarpS + 1, kCopyWarp = kMmaWarpS + 2;
 constexpr int kThreads = 32 * (kCopyWarp + 1);
-constexpr int kRing = 4;             // chunks of decays computed ahead
+constexpr int kRing = 4;             // buffers for the decays of a chunk
 constexpr int kCols = 32;            // columns of the state and of y per compute thread
 
 // Shared memory, from a 1024-byte boundary. Tiles of 128-byte rows with the
@@ -143,20 +143,25 @@ constexpr int kOffB = kOffS + 2 * kTileBytes;    // two buffers of [n / 64][128 
 constexpr int kOffX = kOffB + 4 * kTileBytes;    // two buffers of [128 tokens][64]
 constexpr int kOffW = kOffX + 2 * kTileBytes;    // three terms of the weighted rows
 constexpr int kOffSc = kOffW + 3 * kTileBytes;   // kRing buffers of Scalars
-struct alignas(16) Scalars {   // (read in 16-byte pieces)
+// The decays of a chunk of one head, as a launch before leaves them in the workspace.
+struct alignas(16) Decays {
     float hi[kL], lo[kL];   // -G_t as a sum of two floats, in units of log 2
     float dt[kL];           // delta_t; 0 past the sequence's end
     float to_block[kL];     // 2^(G at the end of t's 32-block - G_t) delta_t
-    float to_end[kL];       // 2^(G_last - G_t) delta_t
-    float from[kL];         // 2^G_t
     float end_hi[4], end_lo[4];   // G at the end of each 32-block
-    float decay;            // 2^G_last
+    // what the launch for the states needs starts here
+    float to_end[kL];       // 2^(G_last - G_t) delta_t
+    float decay, pad[3];    // 2^G_last
+};
+constexpr int kDecaysBytes = static_cast<int>(sizeof(Decays));
+constexpr int kDecaysTail = static_cast<int>(offsetof(Decays, to_end));
+struct alignas(16) Scalars : Decays {
     // where the chunk is, so that the compute warps need not walk the list
     int valid;              // its tokens
     int unit, seq, pos;     // head and slice; sequence; chunk of the sequence
     int flags;              // kLast, kCut
-    int64_t row;            // its first token
     int xcol, gcol;         // its first column of x, and of b and c
+    int64_t row;            // its first token
 };
 enum { kLast = 1, kCut = 2 };   // the sequence's last chunk; the run's end cuts the sequence
 constexpr int kOffBar = kOffSc + kRing * static_cast<int>(sizeof(Scalars));
@@ -291,6 +296,19 @@ __device__ __forceinline__ uint32_t split2(float a, float b, uint32_t &lo) {
     return h;
 }
 
+// Of the lanes l and l ^ m, the one without the bit m gives b for the other's a.
+__device__ __forceinline__ void exchange(uint32_t &a, uint32_t &b, int m, int lane) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, (lane & m) != 0 ? a : b, m);
+    if ((lane & m) != 0) a = got;
+    else b = got;
+}
+__device__ __forceinline__ void exchange(uint4 &a, uint4 &b, int m, int lane) {
+    exchange(a.x, b.x, m, lane);
+    exchange(a.y, b.y, m, lane);
+    exchange(a.z, b.z, m, lane);
+    exchange(a.w, b.w, m, lane);
+}
+
 // hi + lo += x, with the rounding error of the sum kept in lo
 struct Sum2 {
     float hi, lo;
@@ -346,6 +364,7 @@ struct SsmPlan {
     int64_t units;             // heads << shift
     const int32_t *chunk_off;  // packed: first chunk of each sequence [N + 1]
     const int *call_flags;     // packed: set by the prologue
+    Decays *decays;            // [chunk of all sequences][heads]
     int64_t gran;              // chunks that stay together; 0: all of a unit's
     float *slots;              // [G][kCols][kGroupThreads] states at the cuts
     float *saved;              // the same: initial states that a cut run starts from (in place)
@@ -441,6 +460,71 @@ __global__ void __launch_bounds__(256) ssm_hand_on_kernel(SsmParams p) {
     const Seqs seqs{p.cu, p.seq_len, p.n_seqs};
     if (!check_cu(seqs, p.tokens, p.err)) return;
     hand_on<kN>(p, threadIdx.x, 256);
+}
+
+// The decays of all chunks, a warp per chunk and head: running sums over each lane's four
+// tokens, then over the lanes. A dependent chain of some 600 instructions: inside the
+// chunk kernel, on a warp of its own, it took 3100 clocks per chunk, as long as that
+// chunk's products, and a sixth of its instruction cache.
+__global__ void __launch_bounds__(256) ssm_decays_kernel(SsmParams p, SsmPlan pl) {
+    if (pl.call_flags != nullptr && (*pl.call_flags & kErrBadCu) != 0) return;
+    const List list(p, pl);
+    const int lane = threadIdx.x & 31;
+    const int64_t all = list.nc * p.heads;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < all; i += gridDim.x * 8) {
+        const int h = static_cast<int>(i % p.heads);
+        Walk w;
+        w.go(p, pl, list.nc, i / p.heads);   // (of the first unit: all have the same chunks)
+        const int valid = w.valid();
+        const float a2 = __ldg(p.a + h) * 1.44269504088896341f;
+        const float bias = p.dt_bias != nullptr ? __ldg(p.dt_bias + h) : 0.f;
+        const float *src = p.dt + (w.row() + 4 * lane) * p.dt_stride + h;
+        float dt[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dt[j] = 4 * lane + j < valid ? __ldg(src + j * p.dt_stride) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dt[j] = 4 * lane + j < valid ? delta_of(dt[j] + bias, p.softplus) : 0.f;
+        Sum2 sum{0.f, 0.f}, g[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            sum.add(a2 * dt[j], 0.f);
+            g[j] = sum;
+        }
+        Sum2 incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float vh = __shfl_up_sync(0xffffffffu, incl.hi, o);
+            const float vl = __shfl_up_sync(0xffffffffu, incl.lo, o);
+            if (lane >= o) incl.add(vh, vl);
+        }
+        float bh = __shfl_up_sync(0xffffffffu, incl.hi, 1), bl = __shfl_up_sync(0xffffffffu, incl.lo, 1);
+        if (lane == 0) bh = bl = 0.f;
+        const float kh = __shfl_sync(0xffffffffu, incl.hi, lane | 7);
+        const float kl = __shfl_sync(0xffffffffu, incl.lo, lane | 7);
+        const float eh = __shfl_sync(0xffffffffu, incl.hi, 31), el = __shfl_sync(0xffffffffu, incl.lo, 31);
+        float v[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            Sum2 G{bh, bl};
+            G.add(g[j].hi, g[j].lo);
+            v[0][j] = -G.hi;
+            v[1][j] = -G.lo;
+            v[2][j] = ex2((kh - G.hi) + (kl - G.lo)) * dt[j];
+            v[3][j] = ex2((eh - G.hi) + (el - G.lo)) * dt[j];
+        }
+        Decays &s = pl.decays[i];
+        *reinterpret_cast<float4 *>(s.hi + 4 * lane) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
+        *reinterpret_cast<float4 *>(s.lo + 4 * lane) = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
+        *reinterpret_cast<float4 *>(s.dt + 4 * lane) = make_float4(dt[0], dt[1], dt[2], dt[3]);
+        *reinterpret_cast<float4 *>(s.to_block + 4 * lane) = make_float4(v[2][0], v[2][1], v[2][2], v[2][3]);
+        *reinterpret_cast<float4 *>(s.to_end + 4 * lane) = make_float4(v[3][0], v[3][1], v[3][2], v[3][3]);
+        if ((lane & 7) == 7) {
+            s.end_hi[lane >> 3] = kh;
+            s.end_lo[lane >> 3] = kl;
+        }
+        // (carried over all the chunks of a sequence: the more exact exponential)
+        if (lane == 31) s.decay = exp2f(eh);
+    }
 }
 
 template <int kN, bool kStates>
@@ -638,11 +722,48 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
 #pragma unroll 1
                 for (int k = 0; k < n; ++k) tma_2d(sb + off + k * kTileBytes, &map, col + 64 * k, row, bar(full));
             };
-            int i = 0, sent_c = 0;
+            // Where chunk j is, and its decays. Its tiles are fetched into L2: their
+            // buffers are free for about half a chunk's time before they are needed,
+            // less than a read from HBM takes.
+            const int per_group = p.heads / p.groups;
+            auto describe = [&](int j) -> bool {
+                if (j >= kRing && !wait(kScFree + (j & (kRing - 1)), (j / kRing) - 1)) return false;
+                if (j > 0) w.next(p, pl, list.nc);
+                Scalars &s = scal[j & (kRing - 1)];
+                const int h = w.u >> pl.shift, full = kScal + (j & (kRing - 1));
+                s.valid = w.valid();
+                s.unit = w.u;
+                s.seq = w.n;
+                s.pos = w.pos;
+                s.flags = (w.last() ? kLast : 0) | (q0 + j + (w.len + kL - 1) / kL - w.pos > q1 ? kCut : 0);
+                s.row = w.row();
+                s.xcol = h * p.p + (w.u & pl.shift) * kPS;
+                s.gcol = h / per_group * kN;
+                constexpr int kFrom = kStates ? kDecaysTail : 0;
+                mbar_arrive_expect_tx(bar(full), kDecaysBytes - kFrom);
+                bulk_g2s(smem_u32(&s) + kFrom,
+                         reinterpret_cast<const uint8_t *>(pl.decays + w.ch * p.heads + h) + kFrom,
+                         kDecaysBytes - kFrom, bar(full));
+                if (j > 0) {
+                    const int row = static_cast<int>(s.row);
+                    prefetch_2d(&maps.x, s.xcol, row);
+#pragma unroll 1
+                    for (int k = 0; k < kN; k += 64) {
+                        prefetch_2d(&maps.b, s.gcol + k, row);
+                        if (!kStates) prefetch_2d(&maps.c, s.gcol + k, row);
+                    }
+                }
+                return true;
+            };
+            int i = 0, sent_c = 0, described = 0;
 #pragma unroll 1
             for (; i < count; ++i) {
+                while (described < count && described < i + 2) {
+                    if (!describe(described)) break;
+                    ++described;
+                }
+                if (described < i + 1 || (described < i + 2 && described < count)) break;
                 // what chunks i - 2 (b, x) and i - 1 (c) have left
-                if (!wait(kScal + (i & (kRing - 1)), i / kRing)) break;
                 const Scalars &v = scal[i & (kRing - 1)];
                 const int row = static_cast<int>(v.row), col = v.gcol, xcol = v.xcol, s = i & 1;
                 if (i > 1 && (!wait(kDS + s, (i >> 1) - 1) || (!kStates && !wait(kCB + s, (i >> 1) - 1)))) break;
@@ -662,128 +783,35 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 wait_phase(bar(kFullX + (j & 1)), (j >> 1) & 1);
             }
             if (!kStates && sent_c > 0) wait_phase(bar(kFullC), (sent_c - 1) & 1);
+            for (int j = described > 2 ? described - 2 : 0; j < described; ++j)
+                wait_phase(bar(kScal + (j & (kRing - 1))), (j / kRing) & 1);
             if (i < count) {   // (of the chunk it gave up at)
                 wait_phase(bar(kFullB + (i & 1)), (i >> 1) & 1);
                 wait_phase(bar(kFullX + (i & 1)), (i >> 1) & 1);
             }
         }
         __syncwarp();
-    } else if (warp == kScalWarp) {
-        // ------------------------------------ scalars: the decays of each chunk
-        // It runs up to kRing chunks ahead of the others, so it also has the tiles
-        // fetched into L2: their buffers are free for about half a chunk's time
-        // before they are needed, less than a read from HBM takes.
-        const int per_group = p.heads / p.groups;
-        float raw[4] = {}, next_a = 0.f, next_bias = 0.f;
-        int xcol = 0, gcol = 0;
-        auto load = [&](bool ahead) {   // the next chunk's dt, ahead of their use
-            const int h = w.u >> pl.shift, valid = w.valid(), row = static_cast<int>(w.row());
-            const float *src = p.dt + (w.row() + 4 * lane) * p.dt_stride + h;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) raw[j] = 4 * lane + j < valid ? __ldg(src + j * p.dt_stride) : 0.f;
-            next_a = __ldg(p.a + h);
-            if (p.dt_bias != nullptr) next_bias = __ldg(p.dt_bias + h);
-            xcol = h * p.p + (w.u & pl.shift) * kPS;
-            gcol = h / per_group * kN;
-            if (ahead && lane < (kStates ? 2 : 3)) {   // lanes 0, 1, 2: x, b, c
-                const CUtensorMap *map = lane == 0 ? &maps.x : lane == 1 ? &maps.b : &maps.c;
-                prefetch_2d(map, lane == 0 ? xcol : gcol, row);
-                if (lane > 0 && kN == 128) prefetch_2d(map, gcol + 64, row);
-            }
-        };
-        Sum2 sum{0.f, 0.f}, g[4] = {};
-        float dt[4] = {};
-#pragma unroll 1
-        for (int i = -1; i < count; ++i) {
-            Scalars &s = scal[i & (kRing - 1)];
-            if (i >= 0) {
-                if (i >= kRing && !wait(kScFree + (i & (kRing - 1)), (i / kRing) - 1)) break;
-                const int valid = w.valid();
-                const float a2 = next_a * 1.44269504088896341f;
-                if (lane == 0) {
-                    s.valid = valid;
-                    s.unit = w.u;
-                    s.seq = w.n;
-                    s.pos = w.pos;
-                    s.flags = (w.last() ? kLast : 0) | (q0 + i + (w.len + kL - 1) / kL - w.pos > q1 ? kCut : 0);
-                    s.row = w.row();
-                    s.xcol = xcol;
-                    s.gcol = gcol;
-                }
-                // running sums over this lane's four tokens, then over the lanes
-                sum = Sum2{0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    dt[j] = 4 * lane + j < valid ? delta_of(raw[j] + next_bias, p.softplus) : 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sum.add(a2 * dt[j], 0.f);
-                    g[j] = sum;
-                }
-            }
-            if (i + 1 < count) {
-                if (i >= 0) w.next(p, pl, list.nc);
-                load(i >= 0);
-            }
-            if (i < 0) continue;
-            Sum2 incl = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float vh = __shfl_up_sync(0xffffffffu, incl.hi, o);
-                const float vl = __shfl_up_sync(0xffffffffu, incl.lo, o);
-                if (lane >= o) incl.add(vh, vl);
-            }
-            float bh = __shfl_up_sync(0xffffffffu, incl.hi, 1), bl = __shfl_up_sync(0xffffffffu, incl.lo, 1);
-            if (lane == 0) bh = bl = 0.f;
-            const float kh = __shfl_sync(0xffffffffu, incl.hi, lane | 7);
-            const float kl = __shfl_sync(0xffffffffu, incl.lo, lane | 7);
-            const float eh = __shfl_sync(0xffffffffu, incl.hi, 31), el = __shfl_sync(0xffffffffu, incl.lo, 31);
-            float v[5][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                Sum2 G{bh, bl};
-                G.add(g[j].hi, g[j].lo);
-                v[0][j] = -G.hi;
-                v[1][j] = -G.lo;
-                v[2][j] = ex2((kh - G.hi) + (kl - G.lo)) * dt[j];
-                v[3][j] = ex2((eh - G.hi) + (el - G.lo)) * dt[j];
-                v[4][j] = ex2(G.hi);
-            }
-            if (!kStates) {
-                *reinterpret_cast<float4 *>(s.hi + 4 * lane) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
-                *reinterpret_cast<float4 *>(s.lo + 4 * lane) = make_float4(v[1][0], v[1][1], v[1][2], v[1][3]);
-                *reinterpret_cast<float4 *>(s.dt + 4 * lane) = make_float4(dt[0], dt[1], dt[2], dt[3]);
-                *reinterpret_cast<float4 *>(s.to_block + 4 * lane) = make_float4(v[2][0], v[2][1], v[2][2], v[2][3]);
-                *reinterpret_cast<float4 *>(s.from + 4 * lane) = make_float4(v[4][0], v[4][1], v[4][2], v[4][3]);
-            }
-            *reinterpret_cast<float4 *>(s.to_end + 4 * lane) = make_float4(v[3][0], v[3][1], v[3][2], v[3][3]);
-            if ((lane & 7) == 7) {
-                s.end_hi[lane >> 3] = kh;
-                s.end_lo[lane >> 3] = kl;
-            }
-            // (carried over all the chunks of a sequence: the more exact exponential)
-            if (lane == 31) s.decay = exp2f(eh);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kScal + (i & (kRing - 1))));
-        }
     } else if (warp < kGroup) {
         // ------------------------------------------------- M and the output, row
         // 32 q + lane (the lanes of tensor memory that a warp reaches); columns of y:
         // the half hf
         const int q = warp & 3, hf = warp >> 2, r = 32 * q + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-        // y = 2^G (C S) + M X of chunk i
-        auto put_out = [&](int i) -> bool {
+        // y = 2^G (C S) + M X of chunk i, ready to be stored
+        uint4 ys[4];
+        __nv_bfloat16 *dst = nullptr;
+        int valid = 0;
+        auto take_out = [&](int i) -> bool {
             const Scalars &s = scal[i & (kRing - 1)];
             const int h = s.unit >> pl.shift;
-            const float from = s.from[r];
-            const bool live = r < s.valid;
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                                   ((s.row + r) * p.heads + h) * p.p +
-                                                   (s.unit & pl.shift) * kPS + kCols * hf);
+            const float from = ex2(-s.hi[r]);
+            valid = s.valid;
+            dst = static_cast<__nv_bfloat16 *>(p.out) +
+                  ((s.row + (r & ~3)) * p.heads + h) * p.p + (s.unit & pl.shift) * kPS + kCols * hf +
+                  8 * (lane & 3);
             if (!wait(kMX + (i & 1), i >> 1) || !wait(kCS + (i & 1), i >> 1)) return false;
             tc::fence_after();
-#pragma unroll 2
+#pragma unroll
             for (int k = 0; k < 4; ++k) {   // 8 columns at a time
                 uint32_t y[8], cs[8];
                 ld8(lanes + kTmY + kCols * hf + 8 * k, y);
@@ -796,7 +824,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                     fma2(a, b, from, from, __uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
                     os[e] = pack_bf16(a, b);
                 }
-                if (live) dst[k] = make_uint4(os[0], os[1], os[2], os[3]);
+                ys[k] = make_uint4(os[0], os[1], os[2], os[3]);
             }
             tc::fence_before();
             __syncwarp();
@@ -888,8 +916,21 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             tc::st_wait();
             tc::fence_before();
             }
-            if (i > 0 && !put_out(i - 1)) break;
+            if (i > 0 && !take_out(i - 1)) break;
             arrive(kMReady + (i & 1));   // M is there and y's columns are free
+            // stored behind the arrivals: an arrival waits for this warp's stores before it
+            if (i > 0) {
+                // four lanes exchange their 16-byte pieces, so that they write the 64
+                // bytes of one row and not each its own
+                exchange(ys[0], ys[1], 1, lane);
+                exchange(ys[2], ys[3], 1, lane);
+                exchange(ys[0], ys[2], 2, lane);
+                exchange(ys[1], ys[3], 2, lane);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if ((r & ~3) + k < valid)
+                        *reinterpret_cast<uint4 *>(dst + k * static_cast<int64_t>(p.heads) * p.p) = ys[k];
+            }
         }
     } else {
         // ---------------------------------------------------------- the state
@@ -1062,11 +1103,17 @@ bool encode(CUtensorMap *m, const void *base, int64_t tokens, int64_t width, int
 
 int64_t align256(int64_t v) { return (v + 255) / 256 * 256; }
 
-// Workspace: [chunk offsets (packed)][decays][states at the cuts][copies of
-// initial states (in place)].
+// Workspace: [chunk offsets (packed)][decays of the runs][states at the cuts][copies of
+// initial states (in place)][decays of the chunks].
 constexpr int64_t kSlotBytes = static_cast<int64_t>(kCols) * kGroupThreads * 4;
 int64_t offsets_bytes(const SsmParams &p) {
     return p.cu != nullptr ? align256((static_cast<int64_t>(p.n_seqs) + 1) * 4) : 0;
+}
+
+// At most this many chunks of a head.
+int64_t most_chunks(const SsmParams &p) {
+    return p.cu != nullptr ? (p.tokens + static_cast<int64_t>(kL - 1) * p.n_seqs) / kL
+                           : (p.seq_len + kL - 1) / kL * p.n_seqs;
 }
 
 }  // namespace
@@ -1082,7 +1129,7 @@ cudaError_t configure_ssm() {
 }
 
 int64_t ssm_workspace(const SsmParams &p) {
-    return offsets_bytes(p) + 1024 + 2 * kSsmSms * kSlotBytes;
+    return offsets_bytes(p) + 1024 + 2 * kSsmSms * kSlotBytes + most_chunks(p) * p.heads * kDecaysBytes;
 }
 
 cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t stream) {
@@ -1107,6 +1154,7 @@ cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t 
     pl.decay = reinterpret_cast<float *>(ws + offsets_bytes(p));
     pl.slots = reinterpret_cast<float *>(ws + offsets_bytes(p) + 1024);
     pl.saved = pl.slots + kSsmSms * kSlotBytes / 4;
+    pl.decays = reinterpret_cast<Decays *>(ws + offsets_bytes(p) + 1024 + 2 * kSsmSms * kSlotBytes);
     pl.in_place = p.s_final != nullptr && p.s_final == p.s0;
     if (p.cu != nullptr) {
         int32_t *off = reinterpret_cast<int32_t *>(ws);
@@ -1119,13 +1167,16 @@ cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t 
     // Whole sequences (or, packed, all of a unit's) stay in one run, and the
     // launch for the states at the cuts is saved, when they are short, or when
     // there are so many that the SMs are even without cuts.
-    const int64_t nc = p.cu != nullptr ? (p.tokens + static_cast<int64_t>(kL - 1) * p.n_seqs) / kL
-                                       : static_cast<int64_t>(pl.cps) * p.n_seqs;
+    const int64_t nc = most_chunks(p);
     const bool whole = p.cu != nullptr ? p.tokens <= 4 * kL
                                        : pl.cps <= 4 || pl.units * p.n_seqs >= 8 * kSsmSms;
     pl.gran = !whole ? 1 : p.cu != nullptr ? 0 : pl.cps;
     const int64_t runs = pl.units * nc / (pl.gran > 0 ? pl.gran : nc);
     const unsigned grid = static_cast<unsigned>(runs < kSsmSms ? runs : kSsmSms);
+    const int64_t blocks = (nc * p.heads + 7) / 8;
+    ssm_decays_kernel<<<static_cast<unsigned>(blocks < 8 * kSsmSms ? blocks : 8 * kSsmSms), 256, 0, stream>>>(p, pl);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     return with_n(p, [&](auto n) {
         constexpr int kN = decltype(n)::value;
         if (!whole) {
