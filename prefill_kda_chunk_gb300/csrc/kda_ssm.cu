@@ -126,11 +126,13 @@ constexpr int kL = 128;              // tokens per chunk
 constexpr int kPS = 64;              // channels of P per unit
 constexpr int kSsmSms = 152;
 // Warps: 0..7 form M and the outputs, 8..15 keep the state, then one for the
-// MMAs of the state, one for those of y and one for the copies.
+// MMAs of the state and C S, one each for C B^T and M X (in one warp, whichever came
+// first held up the other) and one for the copies.
 constexpr int kGroup = 8;
 constexpr int kGroupThreads = 32 * kGroup;
-constexpr int kMmaWarpS = 2 * kGroup, kMmaWarpY = kMmaWarpS + 1, kCopyWarp = kMmaWarpS + 2;
-constexpr int kThreads = 32 * (kCopyWarp + 1);
+constexpr int kCopyWarp = 2 * kGroup, kMmaWarpS = kCopyWarp + 1, kMmaWarpY = kCopyWarp + 2,
+              kMmaWarpC = kCopyWarp + 3;
+constexpr int kThreads = 32 * (kMmaWarpC + 1);
 constexpr int kRing = 4;             // buffers for the decays of a chunk
 constexpr int kCols = 32;            // columns of the state and of y per compute thread
 
@@ -151,7 +153,7 @@ struct alignas(16) Decays {
     float end_hi[4], end_lo[4];   // G at the end of each 32-block
     // what the launch for the states needs starts here
     float to_end[kL];       // 2^(G_last - G_t) delta_t
-    float decay, pad[3];    // 2^G_last
+    float decay, d, pad[2]; // 2^G_last; the head's d
 };
 constexpr int kDecaysBytes = static_cast<int>(sizeof(Decays));
 constexpr int kDecaysTail = static_cast<int>(offsetof(Decays, to_end));
@@ -168,7 +170,7 @@ constexpr int kOffBar = kOffSc + kRing * static_cast<int>(sizeof(Scalars));
 enum {   // barriers, 8 bytes each; pairs and the ring by the chunk's index
     // phases that one thread or a copy completes
     kFullC, kFullB, kFullX = kFullB + 2, kScal = kFullX + 2, kCB = kScal + kRing, kDS = kCB + 2,
-    kCS = kDS + 2, kMX = kCS + 2, kDrain = kMX + 2, kDrain2,
+    kCS = kDS + 2, kMX = kCS + 2, kDrain = kMX + 2, kDrain2, kDrain3,
     // phases that the warps of a group arrive at
     kMReady, kSReady = kMReady + 2, kXReady, kDone = kXReady + 2,
     // ... the state's, and in the launch for the states both
@@ -523,7 +525,10 @@ __global__ void __launch_bounds__(256) ssm_decays_kernel(SsmParams p, SsmPlan pl
             s.end_lo[lane >> 3] = kl;
         }
         // (carried over all the chunks of a sequence: the more exact exponential)
-        if (lane == 31) s.decay = exp2f(eh);
+        if (lane == 31) {
+            s.decay = exp2f(eh);
+            s.d = p.d != nullptr ? __ldg(p.d + h) : 0.f;
+        }
     }
 }
 
@@ -571,12 +576,8 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
     __syncthreads();
     tc::fence_after();
 
-    // A bounded wait; a role whose wait has run out stops.
-    auto wait = [&](int i, int phase) -> bool {
-        const bool ok = wait_phase(bar(i), phase & 1);
-        if (!ok) s_abort = 1;
-        return ok;
-    };
+    // A bounded wait; a role whose wait has run out stops, and says so.
+    auto wait = [&](int i, int phase) -> bool { return wait_phase(bar(i), phase & 1); };
     auto arrive = [&](int i) {   // one arrival per warp
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(i));
@@ -590,10 +591,9 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
     // after a wait that gave up: let the MMAs that this warp issued end
     auto drain = [&](int i) {
         __syncwarp();
-        if (s_abort != 0) {
-            mma_commit(bar(i));
-            wait_phase(bar(i), 0);
-        }
+        s_abort = 1;
+        mma_commit(bar(i));
+        wait_phase(bar(i), 0);
     };
     auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
     // The weighted rows of chunk i as three bf16 terms, in 32 tasks of 32
@@ -651,8 +651,9 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
     };
     if (warp == kMmaWarpS) {
         // ------------------------------------------- MMAs: B^T (W X) and C S
+        int j0 = 0;
 #pragma unroll 1
-        for (int j0 = 0; j0 < count; ++j0) {
+        for (; j0 < count; ++j0) {
             const int i = __shfl_sync(0xffffffffu, j0, 0);   // (uniform, see above)
             // B^T (W X) (for n = 64 the upper 64 rows are formed from whatever lies
             // there and are not read)
@@ -681,28 +682,34 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 mma_commit(bar(kCS + (i & 1)));
             }
         }
-        drain(kDrain);
-    } else if (warp == kMmaWarpY) {
-        // --------------------------------------------- MMAs: C B^T and M X
+        if (j0 < count) drain(kDrain);
+    } else if (warp == kMmaWarpC) {
+        // ------------------------------------------------------ MMAs: C B^T
+        int j0 = kStates ? count : 0;
 #pragma unroll 1
-        for (int j0 = -1; !kStates && j0 < count; ++j0) {
+        for (; j0 < count; ++j0) {
             const int i = __shfl_sync(0xffffffffu, j0, 0);   // (uniform, see above)
-            if (i + 1 < count) {
-                // C B^T of the next chunk, over M of the one before this
-                if (!all(wait(kFullB + ((i + 1) & 1), (i + 1) >> 1) && wait(kFullC, i + 1) &&
-                         (i < 1 || wait(kMX + ((i - 1) & 1), (i - 1) >> 1))))
-                    break;
-                tc::fence_after();
-                const uint32_t B = desc_lo(sb + kOffB) + 2 * kTile * ((i + 1) & 1), C = desc_lo(sb + kOffC);
-                const uint32_t D = kTmCB + 128 * ((i + 1) & 1);
+            // over M of two chunks before
+            if (!all(wait(kFullB + (i & 1), i >> 1) && wait(kFullC, i) &&
+                     (i < 2 || wait(kMX + (i & 1), (i >> 1) - 1))))
+                break;
+            tc::fence_after();
+            const uint32_t B = desc_lo(sb + kOffB) + 2 * kTile * (i & 1), C = desc_lo(sb + kOffC);
+            const uint32_t D = kTmCB + 128 * (i & 1);
 #pragma unroll 1
-                for (int k = 0; k < kN / 64; ++k)
-                    mma4_ss<kStepK, 2 * kStepK, 3 * kStepK, kStepK, 2 * kStepK, 3 * kStepK>(
-                        D, C + k * kTile, B + k * kTile, tc::idesc(128, 128, 1), k > 0);
-                mma_commit(bar(kCB + ((i + 1) & 1)));
-            }
-            if (i < 0) continue;
-            // M X, both terms of M along K, once the chunk before is read out
+            for (int k = 0; k < kN / 64; ++k)
+                mma4_ss<kStepK, 2 * kStepK, 3 * kStepK, kStepK, 2 * kStepK, 3 * kStepK>(
+                    D, C + k * kTile, B + k * kTile, tc::idesc(128, 128, 1), k > 0);
+            mma_commit(bar(kCB + (i & 1)));
+        }
+        if (j0 < count) drain(kDrain2);
+    } else if (warp == kMmaWarpY) {
+        // -------------------------------------------------------- MMAs: M X
+        int j0 = kStates ? count : 0;
+#pragma unroll 1
+        for (; j0 < count; ++j0) {
+            const int i = __shfl_sync(0xffffffffu, j0, 0);   // (uniform, see above)
+            // both terms of M along K, once the chunk before is read out
             if (!all(wait(kXReady + (i & 1), i >> 1) && wait(kMReady + (i & 1), i >> 1))) break;
             tc::fence_after();
             const uint32_t X = desc_lo(sb + kOffX) + kTile * (i & 1), A = kTmCB + 128 * (i & 1);
@@ -712,7 +719,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                                              tc::idesc(128, kPS, 1) | kBMajor, k > 0);
             mma_commit(bar(kMX + (i & 1)));
         }
-        drain(kDrain2);
+        if (j0 < count) drain(kDrain3);
     } else if (warp == kCopyWarp) {
         // ---------------------------------------------------------- copies
         if (lane == 0) {
@@ -755,26 +762,28 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 }
                 return true;
             };
-            int i = 0, sent_c = 0, described = 0;
+            int i = 0, sent_c = 0, described = describe(0) ? 1 : 0;
 #pragma unroll 1
             for (; i < count; ++i) {
-                while (described < count && described < i + 2) {
-                    if (!describe(described)) break;
-                    ++described;
-                }
-                if (described < i + 1 || (described < i + 2 && described < count)) break;
                 // what chunks i - 2 (b, x) and i - 1 (c) have left
                 const Scalars &v = scal[i & (kRing - 1)];
                 const int row = static_cast<int>(v.row), col = v.gcol, xcol = v.xcol, s = i & 1;
                 if (i > 1 && (!wait(kDS + s, (i >> 1) - 1) || (!kStates && !wait(kCB + s, (i >> 1) - 1)))) break;
                 copy(kFullB + s, kOffB + 2 * s * kTileBytes, maps.b, col, row, kN / 64);
-                if (!kStates) {   // (before x: the products of y wait for it)
+                if (!kStates && i > 1 && !wait(kMX + s, (i >> 1) - 1)) break;
+                copy(kFullX + s, kOffX + s * kTileBytes, maps.x, xcol, row, 1);
+                if (!kStates) {
                     if (i > 0 && (!wait(kSReady, i - 1) || !wait(kCB + (s ^ 1), (i - 1) >> 1))) break;
                     copy(kFullC, kOffC, maps.c, col, row, kN / 64);
                     sent_c = i + 1;
                 }
-                if (!kStates && i > 1 && !wait(kMX + s, (i >> 1) - 1)) break;
-                copy(kFullX + s, kOffX + s * kTileBytes, maps.x, xcol, row, 1);
+                if (described < count) {
+                    if (!describe(described)) {
+                        ++i;   // (its copies are under way)
+                        break;
+                    }
+                    ++described;
+                }
             }
             // the last copies land before the block ends (after a wait that gave up
             // nobody else may have waited for them)
@@ -786,6 +795,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             for (int j = described > 2 ? described - 2 : 0; j < described; ++j)
                 wait_phase(bar(kScal + (j & (kRing - 1))), (j / kRing) & 1);
             if (i < count) {   // (of the chunk it gave up at)
+                s_abort = 1;
                 wait_phase(bar(kFullB + (i & 1)), (i >> 1) & 1);
                 wait_phase(bar(kFullX + (i & 1)), (i >> 1) & 1);
             }
@@ -811,17 +821,25 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                   8 * (lane & 3);
             if (!wait(kMX + (i & 1), i >> 1) || !wait(kCS + (i & 1), i >> 1)) return false;
             tc::fence_after();
+            uint32_t y[2][16], cs[2][16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {   // 8 columns at a time
-                uint32_t y[8], cs[8];
-                ld8(lanes + kTmY + kCols * hf + 8 * k, y);
-                ld8(lanes + kTmCS + kCols * hf + 8 * k, cs);
-                tc::ld_wait();
+            for (int k = 0; k < 2; ++k) {
+                tc::ld16(lanes + kTmY + kCols * hf + 16 * k, y[k]);
+                tc::ld16(lanes + kTmCS + kCols * hf + 16 * k, cs[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                ld_wait16(y[k]);
+                ld_wait16(cs[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
                 uint32_t os[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float a = __uint_as_float(cs[2 * e]), b = __uint_as_float(cs[2 * e + 1]);
-                    fma2(a, b, from, from, __uint_as_float(y[2 * e]), __uint_as_float(y[2 * e + 1]));
+                    const int j = 8 * (k & 1) + 2 * e;
+                    float a = __uint_as_float(cs[k >> 1][j]), b = __uint_as_float(cs[k >> 1][j + 1]);
+                    fma2(a, b, from, from, __uint_as_float(y[k >> 1][j]), __uint_as_float(y[k >> 1][j + 1]));
                     os[e] = pack_bf16(a, b);
                 }
                 ys[k] = make_uint4(os[0], os[1], os[2], os[3]);
@@ -837,12 +855,16 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
         if (kStates) {   // half of the weighted rows
 #pragma unroll 1
             for (int i = 0; i < count; ++i) {
-                if (!landed(i) || (i > 1 && !wait(kDS + (i & 1), (i >> 1) - 1))) break;
+                if (!landed(i) || (i > 1 && !wait(kDS + (i & 1), (i >> 1) - 1))) {
+                    s_abort = 1;
+                    break;
+                }
                 put_rows(i, 16 + 2 * warp, 2);
             }
         }
+        int i = kStates ? count + 1 : 0;
 #pragma unroll 1
-        for (int i = 0; !kStates && i <= count; ++i) {
+        for (; i <= count; ++i) {
             // M of chunk i, then the output of the one before, whose products are done
             if (i < count) {
             const Scalars &s = scal[i & (kRing - 1)];
@@ -851,7 +873,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             tc::fence_after();
             const uint32_t at = lanes + kTmCB + 128 * (i & 1);
             const float hi_r = -s.hi[r], lo_r = -s.lo[r];
-            const float dv = p.d != nullptr ? __ldg(p.d + (s.unit >> pl.shift)) : 0.f;
+            const float dv = s.d;
             // 16 columns at a time, the half hf of each 32-token block (so that both warps
             // of these rows have as much of the diagonal), the next ones read before these
             // are worked on; blocks above the diagonal are zero.
@@ -932,6 +954,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                         *reinterpret_cast<uint4 *>(dst + k * static_cast<int64_t>(p.heads) * p.p) = ys[k];
             }
         }
+        if (i <= count) s_abort = 1;
     } else {
         // ---------------------------------------------------------- the state
         // row 32 q + lane of S; columns: the half hf
@@ -1035,16 +1058,15 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 const float dec = s.decay;
                 if (has) {
                     tc::fence_after();
+                    uint32_t v[2][16];
+                    tc::ld16(lanes + tm_ds(kStates, i) + kCols * hf, v[0]);
+                    tc::ld16(lanes + tm_ds(kStates, i) + kCols * hf + 16, v[1]);
+                    ld_wait16(v[0]);
+                    ld_wait16(v[1]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {   // 8 columns at a time
-                        uint32_t v[8];
-                        ld8(lanes + tm_ds(kStates, i) + kCols * hf + 8 * k, v);
-                        tc::ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 8; j += 2)
-                            fma2(S[8 * k + j], S[8 * k + j + 1], dec, dec, __uint_as_float(v[j]),
-                                 __uint_as_float(v[j + 1]));
-                    }
+                    for (int j = 0; j < kCols; j += 2)
+                        fma2(S[j], S[j + 1], dec, dec, __uint_as_float(v[j >> 4][j & 15]),
+                             __uint_as_float(v[j >> 4][(j & 15) + 1]));
                     tc::fence_before();
                 }
                 run_decay *= dec;
@@ -1058,12 +1080,17 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             }
             if (!kStates && more) {
                 if (!(ok = landed(i + 1))) break;
-                put_rows(i + 1, 4 * (warp - kGroup), 4);   // into the rows that this chunk's product has read
+                // Into the rows that this chunk's product has read. M is the more work the
+                // later its rows, and its warps share an issue slot with these: the last
+                // quarter takes none of the tasks, the first two most (T 131072, 32 heads
+                // of 128, with even shares: 1573 us, this way 1552).
+                put_rows(i + 1, 16 * hf + (q < 3 ? 6 * q : 0), q < 2 ? 6 : q == 2 ? 4 : 0);
                 if (i < 0 || next.pos == 0) start_state(next);
                 if (i >= 0 && !(ok = wait(kCS + (i & 1), i >> 1))) break;   // the terms of S are read
                 if (!(ok = put_state(i + 1))) break;
             }
         }
+        if (!ok) s_abort = 1;
         if (kStates && ok) {
 #pragma unroll
             for (int j = 0; j < kCols; ++j) pl.slots[slot + j * kGroupThreads] = has ? S[j] : 0.f;
