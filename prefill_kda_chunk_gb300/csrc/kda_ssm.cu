@@ -14,18 +14,18 @@
 //   S'  = 2^G_last S + sum_s b_s (2^(G_last - G_s) delta_s x_s)^T
 //
 // so a chunk of one head is four products, all on the 5th-generation tensor
-// core with bf16 operands from shared memory (TMA, 128-byte swizzle) and fp32
-// accumulators in tensor memory: C B^T (128 x 128 x n), M X with
-// M = (C B^T) . decay, C S, and B^T (W X). b, c and x are bf16 as given, so
-// what the products round is only what this kernel makes: M and S enter as two
-// bf16 terms (16 bits of mantissa, well below the bf16 output's rounding), and
-// the weighted rows W X as three (24 bits: the state is an fp32 result and
-// keeps fp32's precision over any length).
+// core with bf16 operands (TMA, 128-byte swizzle) and fp32 accumulators in
+// tensor memory: C B^T (128 x 128 x n), M X with M = (C B^T) . decay + d I, C S,
+// and B^T (W X). b, c and x are bf16 as given, so what the products round is only
+// what this kernel makes: M and S enter as two bf16 terms (16 bits of mantissa,
+// well below the bf16 output's rounding), and the weighted rows W X as three (24
+// bits: the state is an fp32 result and keeps fp32's precision over any length).
 //
 // Every exponent is a difference of running sums kept as two floats, so it is
 // as exact next to a token that forgets everything (G falls by thousands) as
 // anywhere; between 32-token blocks it is split at the block's end into two
-// factors <= 1, so only the diagonal blocks take an exponential per pair.
+// factors <= 1, so only the diagonal blocks take an exponential per pair. These sums
+// and factors come from a launch of their own (ssm_decays_kernel).
 //
 // Work split. The (head, 64 of P) units and chunks form one list, and CTA c
 // of G (one per SM) takes an equal run of it, a run of chunks of one sequence
@@ -33,6 +33,13 @@
 // state comes from a launch before (kStates): there each CTA whose run ends in
 // the middle of a sequence forms the state that its part of that sequence
 // leaves (the state product only), and the CTAs behind add up what they need.
+//
+// Bound. Bytes do not bind (25 us at T 8192, 64 heads of 64, n 128): a chunk takes the
+// tensor core 2700 clocks, most of it reading operands from shared memory at 128
+// bytes a clock, and the warps 3000 issue slots of each quarter of the SM, most of
+// them for M and for the terms of W X; with the waits between the roles it takes 5800.
+// Measured at those sizes: decays 4 us, states 38, chunks 83, together 125 (200 MB/ms,
+// 20 % of copy bandwidth); 131072 tokens, 32 heads of 128: 1552 us.
 
 #include <cuda.h>
 
@@ -83,7 +90,9 @@ __device__ __forceinline__ float delta_of(float v, bool plus) { return plus ? so
 
 // ------------------------------------------------------------- one token
 
-// One block per (sequence, head): thread (q, j) keeps S[j * kN / kParts ..][q].
+// One block per (sequence, head): thread (q, j) keeps S[j * kN / kParts ..][q]. Bound by
+// reading and writing the state (256 sequences, 64 heads of 64, n 128: 160 us, 6.75
+// TB/s, 99 % of copy bandwidth).
 template <int kN, int kP>
 __global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p) {
     constexpr int kParts = 256 / kP, kRows = kN / kParts;
@@ -173,10 +182,11 @@ enum {   // barriers, 8 bytes each; pairs and the ring by the chunk's index
     kCS = kDS + 2, kMX = kCS + 2, kDrain = kMX + 2, kDrain2, kDrain3,
     // phases that the warps of a group arrive at
     kMReady, kSReady = kMReady + 2, kXReady, kDone = kXReady + 2,
-    // ... the state's, and in the launch for the states both
+    // ... the state's, and in the launch for the states both (there one group can be a chunk
+    // ahead of the other, hence two)
     kWReady = kDone + 2,
     // ... both (the launch for the states: the state's)
-    kScFree, kBars = kScFree + kRing
+    kScFree = kWReady + 2, kBars = kScFree + kRing
 };
 constexpr int kOffMisc = kOffBar + 8 * kBars;    // tensor memory base, abort flag
 constexpr int kSmem = kOffMisc + 8;
@@ -208,12 +218,13 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) {
 }
 
 // Four MMAs, D (+)= A B, with both operands in shared memory, or A in tensor memory, and
-// the commit of those before them; the operands of the second to fourth lie A1.. and B1..
-// behind the first's, those in tensor memory 8 columns apart. The whole warp calls them and the instructions
-// elect a lane: descriptors then stay in uniform registers. (In a branch of one lane an
-// MMA of N = 64 took 77 cycles in a loop and 52 unrolled, this way 48 and 40. One elected
-// at a time, they took 120 and more beside the other warps' work: a dozen dependent
-// instructions each; unrolled throughout, as much for fetching them.)
+// the commit of those before them. The operands of the second to fourth lie A1.. and
+// B1.. behind the first's (those in tensor memory 8 columns apart). The whole warp
+// calls them and the instructions elect a lane: descriptors then stay in uniform
+// registers. (In a branch of one lane an MMA of N = 64 took 77 cycles in a loop and
+// 52 unrolled, this way 48 and 40. One elected at a time, they took 120 and more
+// beside the other warps' work: a dozen dependent instructions each; unrolled
+// throughout, as much for fetching them.)
 template <int A1, int A2, int A3, int B1, int B2, int B3>
 __device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, bool acc) {
     asm volatile(
@@ -339,12 +350,12 @@ __device__ __forceinline__ void ld_wait16(uint32_t (&r)[16]) {
                  : "memory");
 }
 
-// A wait for a phase of an mbarrier, of 2^18 polls at most (about
-// a second, as one that finds nothing takes some 7800 clocks), in few instructions: this
-// kernel waits in some twenty places, and with longer waits at each of them its
-// loops did not fit the instruction cache (a chunk then took 3 times as long). No clock
-// is read and no time to suspend given: a handshake of two warps that wait for one
-// another takes 126 cycles this way, 234 with both.
+// A wait for a phase of an mbarrier, of 2^18 polls at most (about a second: one that
+// finds nothing takes some 7800 clocks), in few instructions: this kernel waits in
+// some twenty places, and with longer waits at each of them its loops did not fit
+// the instruction cache (a chunk then took twice as long). No clock is read and no
+// time to suspend given: a handshake of two warps that wait for one another takes
+// 126 cycles this way, 234 with both.
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity) {
     uint32_t n;
     asm volatile(
@@ -564,7 +575,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
         s_abort = (sb & 1023) != 0;   // (the tiles' swizzle counts on it)
         for (int i = 0; i < kBars; ++i) 
             mbar_init(bar(i), i < kMReady ? 1
-                              : i == kWReady ? (kStates ? 2 * kGroup : kGroup)
+                              : i >= kWReady && i < kScFree ? (kStates ? 2 * kGroup : kGroup)
                               : i >= kScFree ? (kStates ? kGroup : 2 * kGroup) : kGroup);
         mbar_fence_init();
     }
@@ -642,7 +653,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
         fence_async();
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(bar(kWReady));
+            mbar_arrive(bar(kWReady + (i & 1)));
             mbar_arrive(bar(kXReady + (i & 1)));
         }
     };
@@ -657,7 +668,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
             const int i = __shfl_sync(0xffffffffu, j0, 0);   // (uniform, see above)
             // B^T (W X) (for n = 64 the upper 64 rows are formed from whatever lies
             // there and are not read)
-            if (!all(wait(kFullB + (i & 1), i >> 1) && wait(kWReady, i))) break;
+            if (!all(wait(kFullB + (i & 1), i >> 1) && wait(kWReady + (i & 1), i >> 1))) break;
             tc::fence_after();
             const uint32_t B = desc_lo(sb + kOffB) + 2 * kTile * (i & 1);
             const uint32_t W = desc_lo(sb + off_w(kStates, i)), D = tm_ds(kStates, i);
@@ -807,7 +818,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
         // the half hf
         const int q = warp & 3, hf = warp >> 2, r = 32 * q + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
-        // y = 2^G (C S) + M X of chunk i, ready to be stored
+        // y = 2^G (C S) + M X of chunk i, ready to be stored, rounded to bf16 as out is
         uint4 ys[4];
         __nv_bfloat16 *dst = nullptr;
         int valid = 0;

@@ -306,6 +306,32 @@ def test_ssm_long_sequence_and_its_parts():
     assert float((f2.double() - f.double()).norm() / f.double().norm()) < 2.0 ** -18
 
 
+@pytest.mark.parametrize("lens,H,P,G", [([384, 363, 783, 1, 6660], 64, 64, 1), ([20000], 16, 128, 2)])
+def test_ssm_same_bits_from_cold_caches(lens, H, P, G):
+    """Many heads whose sequences are cut, with initial states that come from HBM: some
+    warps then wait long and others do not, which must not show."""
+    x, dt, a, b, c, d, bias, s0 = ssm_case(lens, H, P, G, 128, True)
+    cu = cu_of(lens)
+    cold = torch.empty(320 << 20, dtype=torch.uint8, device="cuda")
+    first = None
+    for i in range(6):
+        cold.fill_(i)
+        o, f = K.ssm_prefill(x, dt, a, b, c, d, bias, initial_state=s0, cu_seqlens=cu.cuda(),
+                             dt_softplus=True)
+        if first is None:
+            first = o, f
+        assert torch.equal(o, first[0]) and torch.equal(f, first[1])
+    K.check_device_error()
+    n, hs = (len(lens), [5, H - 2]) if P == 64 else (1, [1])
+    t = sum(lens) if P == 64 else 4000
+    g = [h // (H // G) for h in hs]
+    ro, rf, so, sf = ops.ssm(x[:t, hs], dt[:t, hs], a[hs], b[:t, g], c[:t, g], d[hs], bias[hs], s0[:, hs],
+                             cu=cu if P == 64 else [0, t], n=n, softplus=True)
+    close(o[:t, hs], ro, so, "out")
+    if P == 64:
+        close(f[:, hs], rf, sf, "state")
+
+
 def test_ssm_bad_cu_seqlens_is_reported_and_skips():
     x, dt, a, b, c, d, bias, _ = ssm_case([30], 2, 64, 1, 128, False)
     out = torch.zeros(30, 2, 64, dtype=BF16, device="cuda")
