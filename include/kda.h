@@ -326,7 +326,7 @@ KDA_API kda_status kda_short_conv_step(const void *x, const float *weight, const
  *   d_initial_state fp32 [N, W-1, D] or NULL (not written)
  * The sums over tokens are taken in fp32 in a fixed order (the same call gives
  * the same bits). Workspace (the stream's, as for the prefill): (W + 1) * D
- * floats for every 256 tokens (every fewer when the call is small).
+ * floats for every 512 to 1024 tokens (for fewer, when the call is small).
  */
 KDA_API kda_status kda_short_conv_backward(const void *x, const float *weight, const float *bias,
                                            const void *initial_state, const int32_t *cu_seqlens,
@@ -348,7 +348,7 @@ KDA_API kda_status kda_short_conv_backward(const void *x, const float *weight, c
  *   dt           device, fp32 [B*T, H], tokens dt_stride elements apart
  *   a            device, fp32 [H]; a * delta is the log decay of a token and is
  *                expected to be <= 0 (a positive one is computed too, as long as
- *                the growth over any 64 tokens stays within fp32)
+ *                the growth over any 128 tokens stays within fp32)
  *   b, c         device, bf16 [B*T, G, n], tokens b_stride / c_stride elements
  *                apart; head h uses group h / (H / G), H a multiple of G
  *   d            device, fp32 [H] or NULL (0)
@@ -362,9 +362,10 @@ KDA_API kda_status kda_short_conv_backward(const void *x, const float *weight, c
  *
  * Alignment: x, b, c, out and the states 16 bytes, and x_stride, b_stride,
  * c_stride multiples of 8 elements; fp32 vectors and cu_seqlens 4 bytes.
- * States, decays and sums are held in fp32. Workspace: the
- * chunk offsets of a packed batch and the states at the cuts of a split
- * sequence.
+ * States, decays and sums are held in fp32; the outputs and states of a call are the
+ * same bits every time. Workspace (the stream's): 2,608 B of decays for every
+ * 128 tokens of a sequence and head, 10 MB for the states where a sequence is
+ * cut, and the chunk offsets of a packed batch.
  */
 enum { KDA_SSM_DT_SOFTPLUS = 1 };
 

@@ -400,7 +400,8 @@ const char *kda_build_info(void) {
     return "prefill_kda_chunk_gb300 0.4 (sm_103a; 16-token chunks: intra-chunk mma.sync with an "
            "exact form for strong decay, recurrent warp-MMA chain with bulk-async staged records "
            "and a segment-parallel scan for long sequences; 64-token chunks on tcgen05 opt-in; decode step; in-kernel q/k "
-           "normalisation and gate logits; token-serial gradients)";
+           "normalisation and gate logits; token-serial and chunked gradients; short convolution, "
+           "state space scan and paged decode attention)";
 }
 
 int64_t kda_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t N, int has_cu_seqlens) {

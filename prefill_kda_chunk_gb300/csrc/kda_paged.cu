@@ -17,13 +17,20 @@
 //
 // Inside a CTA each of 4 warps works for itself on strips of 16 tokens with a
 // ring of kStages strips in shared memory, so nothing waits on a block barrier
-// but the join at the end of a piece. The products are formed transposed,
+// but the join at the end of a piece. Its copies run ahead across the ends of pieces:
+// while one is joined, the next one's keys are on their way (64 sequences of 1 to 16384
+// tokens: 80 to 102 us, and 94 to 117 with a start from nothing at each piece).
+// The products are formed transposed,
 // S^T = K Q^T (16 tokens x 8 heads per MMA) and O^T = V^T P^T: a group of 8 or
 // fewer query heads then fills the N = 8 side of one MMA instead of half of
 // an M = 16 side. P goes from accumulators to operand with an 8 x 8 register
 // transpose. It enters the product as two bf16 terms (16 bits of mantissa
 // together): the tensor pipe is far from busy here, and one term alone would
 // add an error as large as the output's own rounding.
+//
+// Measured: 2 sequences of 131072 tokens, 32 heads over 8 of 128: 163 us (6.6 TB/s,
+// 97 % of copy bandwidth); 64 sequences of 1 to 16384 tokens, 64 heads over 8: 76 to 97 us
+// (78 to 83 %, by the lengths drawn); one of 700 tokens: 12 us, a chain of latencies.
 
 #include <math_constants.h>
 
@@ -37,7 +44,9 @@ namespace {
 constexpr int kPagedWarps = 4;
 constexpr int kStrip = 16;                      // tokens per warp step
 constexpr int kTile = kPagedWarps * kStrip;     // tokens per tile of the split
-constexpr int kItemCost = 4;                    // start and end of an item, in tiles
+// Start and end of an item, in tiles: the join, and steps that wait for the first keys
+// (those 64 sequences: 101 to 134 us with 1, 80 to 102 with 2, 76 to 97 with 3, 4 or 6).
+constexpr int kItemCost = 4;
 constexpr int kStages = 3;                      // strips in flight per warp
 constexpr int kPagedCtasPerSm = 2;
 constexpr int kPagedSms = 152;
