@@ -472,10 +472,18 @@ def _row_stride(t, rows_dims, name):
     """Elements between the rows of a [T, ...] or [B, T, ...] tensor: rows are
     contiguous inside, evenly spaced, and batches follow one another."""
     shape = t.shape
-    expect = math.prod(shape[-rows_dims:])
+    if rows_dims == 1:
+        expect = shape[-1]
+    elif rows_dims == 2:
+        expect = shape[-1] * shape[-2]
+    else:
+        expect = math.prod(shape[-rows_dims:])
     if t.is_contiguous():
         return expect
     strides = t.stride()
+    if len(shape) == 3 and rows_dims == 2 and strides[2] == 1 and strides[1] == shape[2]:
+        if strides[0] >= expect:
+            return strides[0]   # (the usual slice of a projection)
     inner = 1
     for i in range(1, rows_dims + 1):
         if strides[-i] != inner and shape[-i] > 1:
@@ -561,7 +569,7 @@ def short_conv(x, weight, bias=None, initial_state=None, cu_seqlens=None, activa
         _need("final_state", final_state, torch.bfloat16, (N, W - 1, D))
     elif output_final_state:
         final_state = torch.empty((N, W - 1, D), dtype=torch.bfloat16, device=x.device)
-    rc = kda_short_conv(_ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens),
+    rc = lib().kda_short_conv(_ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens),
                         B, T, D, W, N, _row_stride(x, 1, "x"), flags, _ptr(out),
                         _row_stride(out, 1, "out"), _ptr(final_state), _current_stream(x, stream))
     if rc != 0:
@@ -598,7 +606,7 @@ def short_conv_step(x, weight, state=None, bias=None, activation="silu", out=Non
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     else:
         _need("out", out, torch.bfloat16, x.shape, contiguous=False)
-    rc = kda_short_conv_step(_ptr(x), _ptr(weight), _ptr(bias), _ptr(state), N, D, W,
+    rc = lib().kda_short_conv_step(_ptr(x), _ptr(weight), _ptr(bias), _ptr(state), N, D, W,
                              _row_stride(x, 1, "x"), flags, _ptr(out), _row_stride(out, 1, "out"),
                              _ptr(state_out), _current_stream(x, stream))
     if rc != 0:
@@ -639,7 +647,7 @@ def short_conv_backward(x, weight, d_out, bias=None, initial_state=None, cu_seql
     dweight = torch.empty((D, W), **f32)
     dbias = torch.empty((D,), **f32) if bias is not None else None
     dh = torch.empty((N, W - 1, D), **f32) if d_initial_state else None
-    rc = kda_short_conv_backward(
+    rc = lib().kda_short_conv_backward(
         _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_state), _ptr(cu_seqlens), B, T, D, W, N,
         _row_stride(x, 1, "x"), flags, _ptr(d_out), _row_stride(d_out, 1, "d_out"),
         _ptr(d_final_state), _ptr(dx), _row_stride(dx, 1, "dx"), _ptr(dweight), _ptr(dbias),
@@ -696,7 +704,7 @@ def ssm_prefill(x, dt, a, b, c, d=None, dt_bias=None, initial_state=None, cu_seq
         _need("final_state", final_state, torch.float32, (N, H, n, P))
     elif output_final_state:
         final_state = torch.empty((N, H, n, P), dtype=torch.float32, device=x.device)
-    rc = kda_ssm_prefill(
+    rc = lib().kda_ssm_prefill(
         _ptr(x), _ptr(dt), _ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(dt_bias),
         _ptr(initial_state), _ptr(cu_seqlens), B, T, H, P, G, n, N, _row_stride(x, 2, "x"),
         _row_stride(dt, 1, "dt"), _row_stride(b, 2, "b"), _row_stride(c, 2, "c"),
@@ -735,7 +743,7 @@ def ssm_step(x, dt, a, b, c, state=None, d=None, dt_bias=None, dt_softplus=False
         out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     else:
         _need("out", out, torch.bfloat16, x.shape)
-    rc = kda_ssm_step(_ptr(x), _ptr(dt), _ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(dt_bias),
+    rc = lib().kda_ssm_step(_ptr(x), _ptr(dt), _ptr(a), _ptr(b), _ptr(c), _ptr(d), _ptr(dt_bias),
                       _ptr(state), N, H, P, G, n, _row_stride(x, 2, "x"),
                       _row_stride(dt, 1, "dt"), _row_stride(b, 2, "b"), _row_stride(c, 2, "c"),
                       SSM_DT_SOFTPLUS if dt_softplus else 0, _ptr(out), _ptr(state_out),
@@ -771,14 +779,14 @@ def paged_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, out=None
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty_like(q)
     else:
         _need("out", out, torch.bfloat16, q.shape)
     if lse is None:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     else:
         _need("lse", lse, torch.float32, (B, Hq))
-    rc = kda_paged_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
+    rc = lib().kda_paged_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
                           B, Hq, Hkv, D, pages, page_size, page_table.shape[1],
                           _row_stride(k_cache, 3, "k_cache"), _row_stride(v_cache, 3, "v_cache"),
                           float(scale), _ptr(out), _ptr(lse), _current_stream(q, stream))
