@@ -12,8 +12,8 @@
 // ring in shared memory, 12 of each warp on their way at a time. Sequence ends only
 // move the window, so a packed batch runs like one long sequence. All sums are fp32.
 //
-// Measured at T = D = 8192, W = 4: forward 53 us (5.0 TB/s, 74 % of copy bandwidth),
-// gradient with fp32 d_out 99 us (5.4 TB/s, 80 %); one token for each of 256 sequences,
+// Measured at T = D = 8192, W = 4: forward 51 us (5.2 TB/s, 77 % of copy bandwidth),
+// gradient with fp32 d_out 97 us (5.5 TB/s, 81 %); one token for each of 256 sequences,
 // D = 24576: 19 us (5.4 TB/s, 79 %).
 
 #include "kda_device.cuh"
@@ -99,13 +99,15 @@ __device__ __forceinline__ void store_f32(float *dst, const float (&f)[VEC]) {
 // product stays finite and no channel can reach the other: below z = -43.7 the
 // result is 2^-63 instead of something smaller.
 __device__ __forceinline__ void sigmoid2(float z0, float z1, float &s0, float &s1) {
-    float e0, e1, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fminf(z0 * -1.44269504f, 63.f)));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fminf(z1 * -1.44269504f, 63.f)));
-    const float a = 1.f + e0, b = 1.f + e1;
+    mul2(z0, z1, -1.44269504f, -1.44269504f);
+    float a, b, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(fminf(z0, 63.f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(fminf(z1, 63.f)));
+    add2(a, b, 1.f, 1.f);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
-    s0 = r * b;
-    s1 = r * a;
+    s0 = b;
+    s1 = a;
+    mul2(s0, s1, r, r);
 }
 template <int VEC>
 __device__ __forceinline__ void sigmoids(const float (&z)[VEC], float (&s)[VEC]) {
@@ -117,12 +119,45 @@ __device__ __forceinline__ void sigmoids(const float (&z)[VEC], float (&s)[VEC])
         for (int i = 0; i < VEC; i += 2) sigmoid2(z[i], z[i + 1], s[i], s[i + 1]);
     }
 }
+// The arithmetic on a thread's channels goes two by two, in packed instructions: with
+// single ones the forward issued in 74 % of all slots (53 us, this way 51).
+template <int VEC>
+__device__ __forceinline__ void times(float (&a)[VEC], const float (&x)[VEC]) {
+    if constexpr (VEC == 1) {
+        a[0] *= x[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) mul2(a[i], a[i + 1], x[i], x[i + 1]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void plus(float (&a)[VEC], const float (&x)[VEC]) {
+    if constexpr (VEC == 1) {
+        a[0] += x[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) add2(a[i], a[i + 1], x[i], x[i + 1]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void plus(float (&a)[VEC], const float (&x)[VEC], const float (&y)[VEC]) {
+    if constexpr (VEC == 1) {
+        a[0] = fmaf(x[0], y[0], a[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) muladd2(a[i], a[i + 1], x[i], x[i + 1], y[i], y[i + 1]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ void copy(float (&a)[VEC], const float (&x)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) a[i] = x[i];
+}
 template <int VEC>
 __device__ __forceinline__ void silu(float (&z)[VEC]) {
     float s[VEC];
     sigmoids<VEC>(z, s);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) z[i] *= s[i];
+    times<VEC>(z, s);
 }
 
 // The filters of a block's 32 VEC channels, read once and kept tap by tap in shared
@@ -191,23 +226,20 @@ __device__ __forceinline__ void load_window(const ConvParams &p, int n, int64_t 
 template <int W, int VEC>
 __device__ __forceinline__ void step_window(const Filter<W, VEC> &f, float (&win)[W - 1][VEC],
                                             const float (&row)[VEC], float (&z)[VEC]) {
+    copy<VEC>(z, f.b);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        float s = f.b[i];
+    for (int j = 0; j < W - 1; ++j) plus<VEC>(z, f.w[j], win[j]);
+    plus<VEC>(z, f.w[W - 1], row);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) s = fmaf(f.w[j][i], win[j][i], s);
-        z[i] = fmaf(f.w[W - 1][i], row[i], s);
-#pragma unroll
-        for (int j = 0; j + 1 < W - 1; ++j) win[j][i] = win[j + 1][i];
-        win[W - 2][i] = row[i];
-    }
+    for (int j = 0; j + 1 < W - 1; ++j) copy<VEC>(win[j], win[j + 1]);
+    copy<VEC>(win[W - 2], row);
 }
 
 // Rows per warp: at most `most`, and such that the blocks fill whole waves of two per
 // SM. The W - 1 rows read twice are 5 % at 64 (out of L2), and the gradient's W - 1
 // tokens worked on twice are as many, so that it takes longer runs (T = D = 8192:
-// runs of 64, 96 and 128 rows at most take 110, 103 and 99 us, the forward's 53, 53 and
-// 55).
+// runs of 64, 96 and 128 rows at most took 110, 103 and 99 us, the forward's 53, 53 and
+// 55, before the arithmetic went two by two).
 constexpr int kRun = 64, kBackRun = 128, kMinRun = 4, kSlots = 2 * 152;
 int64_t run_for(int64_t tokens, int64_t cols, int64_t most) {
     int64_t run = most;
@@ -338,14 +370,12 @@ __global__ void __launch_bounds__(kWarps * 32) conv_step_kernel(ConvParams p, in
         const int64_t n = n0 + u * kWarps;
         if (n >= p.tokens) break;
         float z[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) z[i] = f.b[i];
+        copy<VEC>(z, f.b);
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             float row[VEC];
             widen<VEC>(raw[u][j], row);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) z[i] = fmaf(f.w[j][i], row[i], z[i]);
+            plus<VEC>(z, f.w[j], row);
         }
         if (SILU) silu<VEC>(z);
         *reinterpret_cast<R *>(static_cast<uint16_t *>(p.out) + n * p.out_stride + d) = narrow<VEC>(z);
@@ -429,34 +459,44 @@ conv_backward_kernel(ConvParams p, int run, int64_t col_blocks) {
             int64_t at = lo * p.dout_stride + d;
             // token t: dz completes row t - (W - 1), which goes to `done`
             auto token = [&](const R &raw, const float (&g)[VEC], bool own, float (&done)[VEC]) {
-                float row[VEC], z[VEC], sg[VEC];
+                float row[VEC], z[VEC], dz[VEC];
                 widen<VEC>(raw, row);
+                copy<VEC>(z, f.b);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    z[i] = f.b[i];
+                for (int j = 0; j < W - 1; ++j) plus<VEC>(z, f.w[j], win[j]);
+                plus<VEC>(z, f.w[W - 1], row);
+                copy<VEC>(dz, g);
+                if (SILU) {   // s (1 + z (1 - s))
+                    float sg[VEC], ones[VEC], t[VEC], m[VEC];
+                    sigmoids<VEC>(z, sg);
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) z[i] = fmaf(f.w[j][i], win[j][i], z[i]);
-                    z[i] = fmaf(f.w[W - 1][i], row[i], z[i]);
-                }
-                if (SILU) sigmoids<VEC>(z, sg);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    float dz = g[i];
-                    if (SILU) dz *= sg[i] * (1.f + z[i] * (1.f - sg[i]));
-                    done[i] = fmaf(f.w[0][i], dz, open[0][i]);
-#pragma unroll
-                    for (int j = 0; j + 1 < W - 1; ++j) open[j][i] = fmaf(f.w[j + 1][i], dz, open[j + 1][i]);
-                    open[W - 2][i] = f.w[W - 1][i] * dz;
-                    if (own) {
-                        db[i] += dz;
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) dw[j][i] = fmaf(dz, win[j][i], dw[j][i]);
-                        dw[W - 1][i] = fmaf(dz, row[i], dw[W - 1][i]);
+                    for (int i = 0; i < VEC; ++i) {
+                        t[i] = ones[i] = 1.f;
+                        m[i] = -1.f;
                     }
-#pragma unroll
-                    for (int j = 0; j + 1 < W - 1; ++j) win[j][i] = win[j + 1][i];
-                    win[W - 2][i] = row[i];
+                    plus<VEC>(t, sg, m);
+                    plus<VEC>(ones, z, t);
+                    times<VEC>(sg, ones);
+                    times<VEC>(dz, sg);
                 }
+                copy<VEC>(done, open[0]);
+                plus<VEC>(done, f.w[0], dz);
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j) {
+                    copy<VEC>(open[j], open[j + 1]);
+                    plus<VEC>(open[j], f.w[j + 1], dz);
+                }
+                copy<VEC>(open[W - 2], dz);
+                times<VEC>(open[W - 2], f.w[W - 1]);
+                if (own) {
+                    plus<VEC>(db, dz);
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) plus<VEC>(dw[j], dz, win[j]);
+                    plus<VEC>(dw[W - 1], dz, row);
+                }
+#pragma unroll
+                for (int j = 0; j + 1 < W - 1; ++j) copy<VEC>(win[j], win[j + 1]);
+                copy<VEC>(win[W - 2], row);
             };
             const int rows = static_cast<int>(end - lo), own = static_cast<int>(hi - lo);
             auto gradient = [&](const G &got, float (&g)[VEC]) {

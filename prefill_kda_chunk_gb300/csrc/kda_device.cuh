@@ -110,6 +110,17 @@ __device__ __forceinline__ void mul2(float &a, float &b, float x, float y) {
         " mul.rn.f32x2 t, t, u;\n mov.b64 {%0, %1}, t;\n}\n"
         : "+f"(a), "+f"(b) : "f"(x), "f"(y));
 }
+// packed likewise: (a, b) += (x, y), and (a, b) += (x, y) * (u, v) with one rounding
+__device__ __forceinline__ void add2(float &a, float &b, float x, float y) {
+    asm("{\n .reg .b64 t, u;\n mov.b64 t, {%0, %1};\n mov.b64 u, {%2, %3};\n"
+        " add.rn.f32x2 t, t, u;\n mov.b64 {%0, %1}, t;\n}\n"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void muladd2(float &a, float &b, float x, float y, float u, float v) {
+    asm("{\n .reg .b64 t, s, w;\n mov.b64 t, {%0, %1};\n mov.b64 s, {%2, %3};\n mov.b64 w, {%4, %5};\n"
+        " fma.rn.f32x2 t, s, w, t;\n mov.b64 {%0, %1}, t;\n}\n"
+        : "+f"(a), "+f"(b) : "f"(x), "f"(y), "f"(u), "f"(v));
+}
 // Non-blocking look at an mbarrier phase (acquire on success).
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     uint32_t ok;

@@ -282,12 +282,7 @@ __device__ __forceinline__ void fence_async() {
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
 }
 
-// packed fp32 pairs: (a, b) += (x, y), (a, b) = (a, b) * (x, y) + (u, v)
-__device__ __forceinline__ void add2(float &a, float &b, float x, float y) {
-    asm("{\n .reg .b64 t, u;\n mov.b64 t, {%0, %1};\n mov.b64 u, {%2, %3};\n"
-        " add.rn.f32x2 t, t, u;\n mov.b64 {%0, %1}, t;\n}\n"
-        : "+f"(a), "+f"(b) : "f"(x), "f"(y));
-}
+// packed fp32 pairs: (a, b) = (a, b) * (x, y) + (u, v)
 __device__ __forceinline__ void fma2(float &a, float &b, float x, float y, float u, float v) {
     asm("{\n .reg .b64 t, s, w;\n mov.b64 t, {%0, %1};\n mov.b64 s, {%2, %3};\n mov.b64 w, {%4, %5};\n"
         " fma.rn.f32x2 t, t, s, w;\n mov.b64 {%0, %1}, t;\n}\n"
@@ -332,12 +327,6 @@ struct Sum2 {
         lo = e - (hi - s);
     }
 };
-
-__device__ __forceinline__ void ld8(uint32_t taddr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-}
 
 // Waits for this thread's tensor memory loads and hands on the registers of one of
 // them, so that no use (or copy) of them moves in front of the wait.
