@@ -6,7 +6,7 @@
 // operator is bound by reading the cache: 4 D B per (token, key-value head).
 //
 // Split. The cache is cut into tiles of 64 tokens of one work item (sequence,
-// key-value head, up to 32 of its query heads). An item costs its tiles and
+// key-value head, up to 16 of its query heads). An item costs its tiles and
 // kItemCost more for its start and end; these units are numbered sequence by
 // sequence, and CTA c of G takes the units [c U / G, (c + 1) U / G): all CTAs
 // have the same work, be the lengths ragged, few or one. A CTA's tiles of one
@@ -52,14 +52,17 @@ constexpr int kPagedCtasPerSm = 2;
 constexpr int kPagedSms = 152;
 constexpr int kMaxCtas = kPagedSms * kPagedCtasPerSm;
 
-// Heads of one work item: 8 NT query heads of one key-value head.
+// Heads of one work item: 8 NT query heads of one key-value head. Two sets of 8 share
+// one reading of the keys and values; larger groups read them again, out of L2, as
+// four sets would not fit in registers (8 sequences of 32768 tokens, 2 key-value heads of
+// 128, groups of 16 and 32: with one set 91 and 160 us, two 71 and 102, up to four 73 and 133).
 struct Plan {
-    int nt;       // 1, 2 or 4
+    int nt;       // 1 or 2
     int chunks;   // items per key-value head
 };
 
 __host__ __device__ inline Plan plan_heads(int group) {
-    const int nt = group <= 8 ? 1 : group <= 16 ? 2 : 4;
+    const int nt = group <= 8 ? 1 : 2;
     return {nt, (group + 8 * nt - 1) / (8 * nt)};
 }
 
@@ -484,18 +487,16 @@ auto with_shape(const PagedParams &p, F &&go) {
     const int nt = plan_heads(p.hq / p.hkv).nt;
     if (p.dim == 64)
         return nt == 1 ? go(Shape<64, 1>(), paged_kernel<64, 1>)
-             : nt == 2 ? go(Shape<64, 2>(), paged_kernel<64, 2>)
-                       : go(Shape<64, 4>(), paged_kernel<64, 4>);
+                       : go(Shape<64, 2>(), paged_kernel<64, 2>);
     return nt == 1 ? go(Shape<128, 1>(), paged_kernel<128, 1>)
-         : nt == 2 ? go(Shape<128, 2>(), paged_kernel<128, 2>)
-                   : go(Shape<128, 4>(), paged_kernel<128, 4>);
+                   : go(Shape<128, 2>(), paged_kernel<128, 2>);
 }
 
 }  // namespace
 
 cudaError_t configure_paged() {
     for (int dim : {64, 128})
-        for (int group : {1, 16, 32}) {
+        for (int group : {1, 16}) {
             PagedParams p{};
             p.dim = dim;
             p.hq = group;
