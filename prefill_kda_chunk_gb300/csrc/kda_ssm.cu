@@ -464,11 +464,18 @@ __global__ void __launch_bounds__(256) ssm_hand_on_kernel(SsmParams p) {
     hand_on<kN>(p, threadIdx.x, 256);
 }
 
+// The launches of one call overlap: a launch may begin while the one in front of it still
+// runs, sets itself up, and waits here until that one's writes are visible. Every
+// CTA waits before it leaves, so that a launch is over only after all before it.
+__device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
 // The decays of all chunks, a warp per chunk and head: running sums over each lane's four
 // tokens, then over the lanes. A dependent chain of some 600 instructions: inside the
 // chunk kernel, on a warp of its own, it took 3100 clocks per chunk, as long as that
 // chunk's products, and a sixth of its instruction cache.
 __global__ void __launch_bounds__(256) ssm_decays_kernel(SsmParams p, SsmPlan pl) {
+    let_next_launch();
     if (pl.call_flags != nullptr && (*pl.call_flags & kErrBadCu) != 0) return;
     const List list(p, pl);
     const int lane = threadIdx.x & 31;
@@ -537,24 +544,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) {
     extern __shared__ __align__(1024) uint8_t smem[];
     volatile int &s_abort = *reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
-    if (pl.call_flags != nullptr && (*pl.call_flags & kErrBadCu) != 0) return;
+    if (pl.call_flags != nullptr && (*pl.call_flags & kErrBadCu) != 0) {
+        wait_for_launch();
+        return;
+    }
     // (the shuffle tells the compiler that a warp's index is uniform: without it, it
     // guards every MMA's registers against lanes that differ, 32 instructions each)
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     if (!kStates && tid < kGroupThreads) hand_on<kN>(p, tid, kGroupThreads);
     const List list(p, pl);
     const int c = blockIdx.x;
-    if (c >= list.G) return;
-    int64_t q0 = list.begin(c);
-    const int64_t q1 = list.begin(c + 1);
+    int64_t q0 = c < list.G ? list.begin(c) : 0;
+    const int64_t q1 = c < list.G ? list.begin(c + 1) : 0;
     if (kStates) {   // only the part of the sequence that the end of the run cuts
-        if (q1 >= list.W) return;
         Walk w;
-        w.go(p, pl, list.nc, q1);
-        if (w.pos == 0) return;
+        w.pos = 0;
+        if (q1 < list.W && q1 > q0) w.go(p, pl, list.nc, q1);
         if (q1 - w.pos > q0) q0 = q1 - w.pos;
     }
     const int count = static_cast<int>(q1 - q0);
+    if (count <= 0) {
+        wait_for_launch();
+        return;
+    }
 
     const uint32_t sb = smem_u32(smem);
     const auto bar = [&](int i) { return sb + kOffBar + 8 * i; };
@@ -575,6 +587,9 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+
+    if (kStates) let_next_launch();
+    wait_for_launch();
 
     // A bounded wait; a role whose wait has run out stops, and says so.
     auto wait = [&](int i, int phase) -> bool { return wait_phase(bar(i), phase & 1); };
@@ -1201,6 +1216,17 @@ cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t 
     pl.gran = !whole ? 1 : p.cu != nullptr ? 0 : pl.cps;
     const int64_t runs = pl.units * nc / (pl.gran > 0 ? pl.gran : nc);
     const unsigned grid = static_cast<unsigned>(runs < kSsmSms ? runs : kSsmSms);
+    // a launch that may begin before the one in front of it is over
+    cudaLaunchAttribute overlap;
+    overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    overlap.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t next{};
+    next.gridDim = dim3(grid);
+    next.blockDim = dim3(kThreads);
+    next.dynamicSmemBytes = kSmem;
+    next.stream = stream;
+    next.attrs = &overlap;
+    next.numAttrs = 1;
     const int64_t blocks = (nc * p.heads + 7) / 8;
     ssm_decays_kernel<<<static_cast<unsigned>(blocks < 8 * kSsmSms ? blocks : 8 * kSsmSms), 256, 0, stream>>>(p, pl);
     const cudaError_t e = cudaGetLastError();
@@ -1208,12 +1234,10 @@ cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t 
     return with_n(p, [&](auto n) {
         constexpr int kN = decltype(n)::value;
         if (!whole) {
-            ssm_chunk_kernel<kN, true><<<grid, kThreads, kSmem, stream>>>(maps, p, pl);
-            const cudaError_t e = cudaGetLastError();
+            const cudaError_t e = cudaLaunchKernelEx(&next, ssm_chunk_kernel<kN, true>, maps, p, pl);
             if (e != cudaSuccess) return e;
         }
-        ssm_chunk_kernel<kN, false><<<grid, kThreads, kSmem, stream>>>(maps, p, pl);
-        return cudaGetLastError();
+        return cudaLaunchKernelEx(&next, ssm_chunk_kernel<kN, false>, maps, p, pl);
     });
 }
 
