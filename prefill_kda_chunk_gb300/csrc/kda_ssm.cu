@@ -662,7 +662,9 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
         }
     };
     auto landed = [&](int i) {
-        return wait(kScal + (i & (kRing - 1)), i / kRing) && wait(kFullB + (i & 1), i >> 1) && wait(kFullX + (i & 1), i >> 1);
+        // (b only where put_rows writes to it)
+        return wait(kScal + (i & (kRing - 1)), i / kRing) && wait(kFullX + (i & 1), i >> 1) &&
+               (scal[i & (kRing - 1)].valid == kL || wait(kFullB + (i & 1), i >> 1));
     };
     if (warp == kMmaWarpS) {
         // ------------------------------------------- MMAs: B^T (W X) and C S
@@ -783,11 +785,15 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 // what chunks i - 2 (b, x) and i - 1 (c) have left
                 const Scalars &v = scal[i & (kRing - 1)];
                 const int row = static_cast<int>(v.row), col = v.gcol, xcol = v.xcol, s = i & 1;
+                if (kStates) {   // x is free as soon as its weighted rows are there
+                    if (i > 1 && !wait(kWReady + s, (i >> 1) - 1)) break;
+                    copy(kFullX + s, kOffX + s * kTileBytes, maps.x, xcol, row, 1);
+                }
                 if (i > 1 && (!wait(kDS + s, (i >> 1) - 1) || (!kStates && !wait(kCB + s, (i >> 1) - 1)))) break;
                 copy(kFullB + s, kOffB + 2 * s * kTileBytes, maps.b, col, row, kN / 64);
-                if (!kStates && i > 1 && !wait(kMX + s, (i >> 1) - 1)) break;
-                copy(kFullX + s, kOffX + s * kTileBytes, maps.x, xcol, row, 1);
                 if (!kStates) {
+                    if (i > 1 && !wait(kMX + s, (i >> 1) - 1)) break;
+                    copy(kFullX + s, kOffX + s * kTileBytes, maps.x, xcol, row, 1);
                     if (i > 0 && (!wait(kSReady, i - 1) || !wait(kCB + (s ^ 1), (i - 1) >> 1))) break;
                     copy(kFullC, kOffC, maps.c, col, row, kN / 64);
                     sent_c = i + 1;
