@@ -37,9 +37,9 @@
 // Bound. Bytes do not bind (25 us at T 8192, 64 heads of 64, n 128): a chunk takes the
 // tensor core 2700 clocks, most of it reading operands from shared memory at 128
 // bytes a clock, and the warps 3000 issue slots of each quarter of the SM, most of
-// them for M and for the terms of W X; with the waits between the roles it takes 5800.
-// Measured at those sizes: decays 4 us, states 38, chunks 83, together 125 (200 MB/ms,
-// 20 % of copy bandwidth); 131072 tokens, 32 heads of 128: 1552 us.
+// them for M and for the terms of W X; with the waits between the roles it takes 5600.
+// Measured at those sizes: decays 4 us, states 34, chunks 80, together 118 (1.5 TB/s,
+// 21 % of copy bandwidth); 131072 tokens, 32 heads of 128: 1540 us.
 
 #include <cuda.h>
 
