@@ -574,7 +574,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
 
     if (tid == 0) {
         s_abort = (sb & 1023) != 0;   // (the tiles' swizzle counts on it)
-        for (int i = 0; i < kBars; ++i) 
+        for (int i = 0; i < kBars; ++i)
             mbar_init(bar(i), i < kMReady ? 1
                               : i >= kWReady && i < kScFree ? (kStates ? 2 * kGroup : kGroup)
                               : i >= kScFree ? (kStates ? kGroup : 2 * kGroup) : kGroup);
@@ -888,76 +888,76 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
         for (; i <= count; ++i) {
             // M of chunk i, then the output of the one before, whose products are done
             if (i < count) {
-            const Scalars &s = scal[i & (kRing - 1)];
-            // ---- M = (C B^T) . decay + d I, two bf16 terms: two 32-token blocks
-            if (!wait(kScal + (i & (kRing - 1)), i / kRing) || !wait(kCB + (i & 1), i >> 1)) break;
-            tc::fence_after();
-            const uint32_t at = lanes + kTmCB + 128 * (i & 1);
-            const float hi_r = -s.hi[r], lo_r = -s.lo[r];
-            const float dv = s.d;
-            // 16 columns at a time, the half hf of each 32-token block (so that both warps
-            // of these rows have as much of the diagonal), the next ones read before these
-            // are worked on; blocks above the diagonal are zero.
-            uint32_t ahead[16] = {};
-            tc::ld16(at + 16 * hf, ahead);
-            ld_wait16(ahead);
+                const Scalars &s = scal[i & (kRing - 1)];
+                // ---- M = (C B^T) . decay + d I, two bf16 terms
+                if (!wait(kScal + (i & (kRing - 1)), i / kRing) || !wait(kCB + (i & 1), i >> 1)) break;
+                tc::fence_after();
+                const uint32_t at = lanes + kTmCB + 128 * (i & 1);
+                const float hi_r = -s.hi[r], lo_r = -s.lo[r];
+                const float dv = s.d;
+                // 16 columns at a time, the half hf of each 32-token block (so that both warps
+                // of these rows have as much of the diagonal), the next ones read before these
+                // are worked on; blocks above the diagonal are zero.
+                uint32_t ahead[16] = {};
+                tc::ld16(at + 16 * hf, ahead);
+                ld_wait16(ahead);
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                const int col = 32 * b + 16 * hf;
-                uint32_t v[16], hi[8], lo[8];
+                for (int b = 0; b < 4; ++b) {
+                    const int col = 32 * b + 16 * hf;
+                    uint32_t v[16], hi[8], lo[8];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = ahead[j];
-                const bool more = b < q;
-                if (more) tc::ld16(at + col + 32, ahead);
-                if (b > q) {
+                    for (int j = 0; j < 16; ++j) v[j] = ahead[j];
+                    const bool more = b < q;
+                    if (more) tc::ld16(at + col + 32, ahead);
+                    if (b > q) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) hi[j] = lo[j] = 0u;
-                } else {
-                    const float f = ex2((hi_r - s.end_hi[b]) + (lo_r - s.end_lo[b]));
-                    if (b < q) {
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 e = *reinterpret_cast<const float4 *>(s.to_block + col + j);
-                            float x[4] = {__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
-                                          __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])};
-                            mul2(x[0], x[1], f, f);
-                            mul2(x[2], x[3], f, f);
-                            mul2(x[0], x[1], e.x, e.y);
-                            mul2(x[2], x[3], e.z, e.w);
-                            hi[j / 2] = split2(x[0], x[1], lo[j / 2]);
-                            hi[j / 2 + 1] = split2(x[2], x[3], lo[j / 2 + 1]);
-                        }
+                        for (int j = 0; j < 8; ++j) hi[j] = lo[j] = 0u;
                     } else {
+                        const float f = ex2((hi_r - s.end_hi[b]) + (lo_r - s.end_lo[b]));
+                        if (b < q) {
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            float4 a = *reinterpret_cast<const float4 *>(s.hi + col + j);
-                            float4 g = *reinterpret_cast<const float4 *>(s.lo + col + j);
-                            const float4 d = *reinterpret_cast<const float4 *>(s.dt + col + j);
-                            add2(a.x, a.y, hi_r, hi_r);
-                            add2(a.z, a.w, hi_r, hi_r);
-                            add2(g.x, g.y, lo_r, lo_r);
-                            add2(g.z, g.w, lo_r, lo_r);
-                            add2(a.x, a.y, g.x, g.y);
-                            add2(a.z, a.w, g.z, g.w);
-                            float x[4] = {ex2(a.x), ex2(a.y), ex2(a.z), ex2(a.w)};
-                            mul2(x[0], x[1], d.x, d.y);
-                            mul2(x[2], x[3], d.z, d.w);
-                            mul2(x[0], x[1], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-                            mul2(x[2], x[3], __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 e = *reinterpret_cast<const float4 *>(s.to_block + col + j);
+                                float x[4] = {__uint_as_float(v[j]), __uint_as_float(v[j + 1]),
+                                              __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])};
+                                mul2(x[0], x[1], f, f);
+                                mul2(x[2], x[3], f, f);
+                                mul2(x[0], x[1], e.x, e.y);
+                                mul2(x[2], x[3], e.z, e.w);
+                                hi[j / 2] = split2(x[0], x[1], lo[j / 2]);
+                                hi[j / 2 + 1] = split2(x[2], x[3], lo[j / 2 + 1]);
+                            }
+                        } else {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                x[e] = col + j + e > r ? 0.f : col + j + e == r ? x[e] + dv : x[e];
-                            hi[j / 2] = split2(x[0], x[1], lo[j / 2]);
-                            hi[j / 2 + 1] = split2(x[2], x[3], lo[j / 2 + 1]);
+                            for (int j = 0; j < 16; j += 4) {
+                                float4 a = *reinterpret_cast<const float4 *>(s.hi + col + j);
+                                float4 g = *reinterpret_cast<const float4 *>(s.lo + col + j);
+                                const float4 d = *reinterpret_cast<const float4 *>(s.dt + col + j);
+                                add2(a.x, a.y, hi_r, hi_r);
+                                add2(a.z, a.w, hi_r, hi_r);
+                                add2(g.x, g.y, lo_r, lo_r);
+                                add2(g.z, g.w, lo_r, lo_r);
+                                add2(a.x, a.y, g.x, g.y);
+                                add2(a.z, a.w, g.z, g.w);
+                                float x[4] = {ex2(a.x), ex2(a.y), ex2(a.z), ex2(a.w)};
+                                mul2(x[0], x[1], d.x, d.y);
+                                mul2(x[2], x[3], d.z, d.w);
+                                mul2(x[0], x[1], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+                                mul2(x[2], x[3], __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    x[e] = col + j + e > r ? 0.f : col + j + e == r ? x[e] + dv : x[e];
+                                hi[j / 2] = split2(x[0], x[1], lo[j / 2]);
+                                hi[j / 2 + 1] = split2(x[2], x[3], lo[j / 2 + 1]);
+                            }
                         }
                     }
+                    tc::st8(at + col, hi);
+                    tc::st8(at + col + 8, lo);
+                    if (more) ld_wait16(ahead);
                 }
-                tc::st8(at + col, hi);
-                tc::st8(at + col + 8, lo);
-                if (more) ld_wait16(ahead);
-            }
-            tc::st_wait();
-            tc::fence_before();
+                tc::st_wait();
+                tc::fence_before();
             }
             if (i > 0 && !take_out(i - 1)) break;
             arrive(kMReady + (i & 1));   // M is there and y's columns are free
