@@ -29,8 +29,8 @@
 // add an error as large as the output's own rounding.
 //
 // Measured: 2 sequences of 131072 tokens, 32 heads over 8 of 128: 163 us (6.6 TB/s,
-// 97 % of copy bandwidth); 64 sequences of 1 to 16384 tokens, 64 heads over 8: 76 to 97 us
-// (78 to 83 %, by the lengths drawn); one of 700 tokens: 12 us, a chain of latencies.
+// 97 % of copy bandwidth); 64 sequences of 1 to 16384 tokens, 64 heads over 8: 73 to 94 us
+// (81 to 86 %, by the lengths drawn); one of 700 tokens: 12 us, a chain of latencies.
 
 #include <math_constants.h>
 
@@ -45,7 +45,7 @@ constexpr int kPagedWarps = 4;
 constexpr int kStrip = 16;                      // tokens per warp step
 constexpr int kTile = kPagedWarps * kStrip;     // tokens per tile of the split
 // Start and end of an item, in tiles: the join, and steps that wait for the first keys
-// (those 64 sequences: 101 to 134 us with 1, 80 to 102 with 2, 76 to 97 with 3, 4 or 6).
+// (those 64 sequences: 100 to 129 us with 1, 78 to 99 with 2, 73 to 94 with 3 or 4).
 constexpr int kItemCost = 4;
 constexpr int kStages = 3;                      // strips in flight per warp
 constexpr int kPagedCtasPerSm = 2;
@@ -55,7 +55,7 @@ constexpr int kMaxCtas = kPagedSms * kPagedCtasPerSm;
 // Heads of one work item: 8 NT query heads of one key-value head. Two sets of 8 share
 // one reading of the keys and values; larger groups read them again, out of L2, as
 // four sets would not fit in registers (8 sequences of 32768 tokens, 2 key-value heads of
-// 128, groups of 16 and 32: with one set 91 and 160 us, two 71 and 102, up to four 73 and 133).
+// 128, groups of 16 and 32: with one set 88 and 160 us, with two 59 and 92).
 struct Plan {
     int nt;       // 1 or 2
     int chunks;   // items per key-value head
@@ -113,6 +113,14 @@ __host__ __device__ __forceinline__ int64_t units_of(int64_t len) {
 // Owner of unit u when G CTAs split U units evenly.
 __device__ __forceinline__ int owner(int64_t u, int64_t U, int64_t G) {
     return static_cast<int>(((u + 1) * G - 1) / U);
+}
+
+// Adds to a counter, after this block's writes before the barrier in front of it and before
+// its reads behind the next one.
+__device__ __forceinline__ int add_acq_rel(int *p, int v) {
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;\n" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
 }
 
 // A CTA's way through its share [u, u1) of the units, piece by piece.
@@ -434,46 +442,70 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
             // ---- the last CTA of this (sequence, item) to arrive joins the pieces
             const int c0 = owner(w.item_at + kItemCost, U, G),
                       c1 = owner(w.item_at + kItemCost + w.tiles - 1, U, G);
-            __threadfence();
-            __syncthreads();
+            __syncthreads();   // (the slot is written)
             if (tid == 0) {
                 int *ctr = arrived + static_cast<int64_t>(w.b) * items + w.item;
-                const int n = atomicAdd(ctr, 1) + 1;
+                const int n = add_acq_rel(ctr, 1) + 1;
                 s_last = n == c1 - c0 + 1;
                 if (s_last) *ctr = 0;   // for the next call
-                __threadfence();
             }
             __syncthreads();
             if (s_last) {
+                // A group of threads per head: each takes every so many-th piece's maximum
+                // and sum, then VD channels of all pieces, several on their way at a time.
+                // (A warp per head, piece after piece: 64 ragged sequences 76 to 97 us, this way
+                // 73 to 94; 8 x 32768 tokens with groups of 16: 71 and 59.)
+                constexpr int H = S::kHeads, kPer = kPagedWarps * 32 / H, VD = D / kPer;
+                const int last = c0 * U / G <= w.item_at;
+                const float *first = slots + static_cast<int64_t>(2 * c0 + last) * S::kSlot;
                 auto piece = [&](int k) {
-                    const int last = k == c0 && k * U / G <= w.item_at;
-                    return slots + static_cast<int64_t>(2 * k + last) * S::kSlot;
+                    return k == c0 ? first : slots + static_cast<int64_t>(2 * k) * S::kSlot;
                 };
-                for (int h = warp; h < heads; h += kPagedWarps) {
-                    float top = -CUDART_INF_F;
-                    for (int k = c0 + lane; k <= c1; k += 32)
-                        top = fmaxf(top, __ldcg(piece(k) + S::kHeads * D + h));
+                const int h = tid / kPer, j = tid % kPer;
+                float top = -CUDART_INF_F, sum = 0.f;
+                #pragma unroll 1
+                for (int k = c0 + j; k <= c1 && h < heads; k += kPer) {
+                    const float mk = __ldcg(piece(k) + H * D + h), lk = __ldcg(piece(k) + H * (D + 1) + h);
+                    const float t = fmaxf(top, mk), base = t == -CUDART_INF_F ? 0.f : t;
+                    sum = fmaf(sum, ex2(top - base), lk * ex2(mk - base));
+                    top = t;
+                }
+                const float own = top;
 #pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    const float base = top == -CUDART_INF_F ? 0.f : top;
-                    float acc[D / 32], sum = 0.f;
+                for (int d = 1; d < kPer; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const float base = top == -CUDART_INF_F ? 0.f : top;
+                sum *= ex2(own - base);
 #pragma unroll
-                    for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+                for (int d = 1; d < kPer; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                float acc[VD];
+#pragma unroll
+                for (int e = 0; e < VD; ++e) acc[e] = 0.f;
 #pragma unroll 4
-                    for (int k = c0; k <= c1; ++k) {
-                        const float *src = piece(k);
-                        const float f = ex2(__ldcg(src + S::kHeads * D + h) - base);
-                        sum = fmaf(__ldcg(src + S::kHeads * (D + 1) + h), f, sum);
+                for (int k = c0; k <= c1 && h < heads; ++k) {
+                    const float *src = piece(k);
+                    const float f = ex2(__ldcg(src + H * D + h) - base);
 #pragma unroll
-                        for (int e = 0; e < D / 32; ++e)
-                            acc[e] = fmaf(__ldcg(src + h * D + e * 32 + lane), f, acc[e]);
+                    for (int e = 0; e < VD; e += 4) {
+                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(src + h * D + j * VD + e));
+                        acc[e] = fmaf(x.x, f, acc[e]);
+                        acc[e + 1] = fmaf(x.y, f, acc[e + 1]);
+                        acc[e + 2] = fmaf(x.z, f, acc[e + 2]);
+                        acc[e + 3] = fmaf(x.w, f, acc[e + 3]);
                     }
+                }
+                if (h < heads) {
                     const int64_t row = static_cast<int64_t>(w.b) * p.hq + head0 + h;
+                    uint32_t *out = static_cast<uint32_t *>(p.out) + (row * D + j * VD) / 2;
 #pragma unroll
-                    for (int e = 0; e < D / 32; ++e)
-                        static_cast<__nv_bfloat16 *>(p.out)[row * D + e * 32 + lane] =
-                            __float2bfloat16_rn(sum > 0.f ? acc[e] / sum : sum == 0.f ? 0.f : sum);
-                    if (lane == 0 && p.lse != nullptr)
+                    for (int e = 0; e < VD; e += 4) {
+                        float y[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            y[i] = sum > 0.f ? acc[e + i] / sum : sum == 0.f ? 0.f : sum;
+                        *reinterpret_cast<uint2 *>(out + e / 2) =
+                            make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+                    }
+                    if (j == 0 && p.lse != nullptr)
                         p.lse[row] = sum == 0.f ? -CUDART_INF_F : base * 0.69314718055994531f + logf(sum);
                 }
             }
