@@ -510,6 +510,18 @@ KDA_API kda_status kda_set_backward_impl(int impl);
 KDA_API kda_status kda_test_stall_recurrent(int chunk, int64_t wait_ns);
 
 /*
+ * Test hook: how kda_short_conv_backward would launch its kernel for arguments
+ * of these sizes, strides and alignments (nothing is read from the pointers and no
+ * GPU is needed). plan receives the bytes of scratch that the call asks for, the
+ * channels of a block, the blocks along the channels, the tokens of a warp's run
+ * and the tiles of eight runs; every tile writes (W + 1) * D floats of the scratch.
+ */
+KDA_API kda_status kda_test_conv_backward_plan(const void *x, const void *d_out, const void *dx,
+                                               int64_t tokens, int64_t D, int64_t W,
+                                               int64_t x_stride, int64_t dout_stride,
+                                               int64_t dx_stride, int flags, int64_t plan[5]);
+
+/*
  * Segments of the segment-parallel scan for later fixed-length calls on the
  * 16-token path (process-wide, host only): 0 (default) = chosen from the SM
  * count as described for kda_chunk_prefill, 1 = off (one chain per

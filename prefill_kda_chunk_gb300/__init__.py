@@ -34,6 +34,7 @@ from ._binding import (  # noqa: F401
     kda_short_conv_step,
     kda_ssm_prefill,
     kda_ssm_step,
+    kda_test_conv_backward_plan,
     kda_test_stall_recurrent,
     kda_stage_timing_begin,
     kda_stage_timing_end,

@@ -75,6 +75,9 @@ def lib() -> ctypes.CDLL:
             L.kda_short_conv_backward.restype = ctypes.c_int
             L.kda_short_conv_backward.argtypes = ([vp] * 5 + [i64] * 6 + [ctypes.c_int, vp, i64, vp,
                                                   vp, i64] + [vp] * 4)
+            L.kda_test_conv_backward_plan.restype = ctypes.c_int
+            L.kda_test_conv_backward_plan.argtypes = ([vp] * 3 + [i64] * 6
+                                                      + [ctypes.c_int, ctypes.POINTER(i64)])
             L.kda_ssm_prefill.restype = ctypes.c_int
             L.kda_ssm_prefill.argtypes = [vp] * 9 + [i64] * 11 + [ctypes.c_int, vp, vp, vp]
             L.kda_ssm_step.restype = ctypes.c_int
@@ -249,6 +252,16 @@ def kda_test_stall_recurrent(chunk: int, wait_ns: int = 0) -> int:
     """Test hook: the recurrent kernel's record producer stops before `chunk`
     and its waits give up after `wait_ns` (-1: off)."""
     return lib().kda_test_stall_recurrent(int(chunk), int(wait_ns))
+
+
+def kda_test_conv_backward_plan(x, d_out, dx, tokens, D, W, x_stride, dout_stride, dx_stride,
+                                flags):
+    """Test hook: (status, (scratch bytes, channels of a block, blocks along the
+    channels, tokens of a run, tiles)) of the convolution's gradient."""
+    plan = (ctypes.c_int64 * 5)()
+    rc = lib().kda_test_conv_backward_plan(x, d_out, dx, tokens, D, W, x_stride, dout_stride,
+                                           dx_stride, flags, plan)
+    return rc, tuple(plan)
 
 
 def kda_build_info() -> str:

@@ -253,7 +253,7 @@ int64_t run_for(int64_t tokens, int64_t cols, int64_t most) {
 }
 
 constexpr int kGroup = 4, kDepth = 4;   // rows of a group, groups of the ring
-constexpr int kForwardVec = 8;
+constexpr int kForwardVec = 8, kBackwardVec = 4;   // channels per thread at most
 template <int VEC>
 constexpr int ring_bytes() {
     return VEC > 1 ? kDepth * kGroup * kWarps * 32 * 2 * VEC : 0;
@@ -678,7 +678,7 @@ cudaError_t configure_conv() {
                     return raise(conv_kernel<W, VEC, decltype(s)::value>, ring_bytes<VEC>());
                 });
                 if (e != cudaSuccess) return e;
-                e = with_shape<4>(p, [&](auto w, auto v, auto s) {
+                e = with_shape<kBackwardVec>(p, [&](auto w, auto v, auto s) {
                     constexpr int W = decltype(w)::value, VEC = decltype(v)::value;
                     constexpr bool S = decltype(s)::value;
                     const cudaError_t r =
@@ -714,31 +714,37 @@ cudaError_t launch_conv_step(const ConvParams &p, cudaStream_t stream) {
     });
 }
 
-// Partial sums of the weights' gradients; with 4 channels per thread the runs are the
-// shortest.
-int64_t conv_backward_tiles(int64_t tokens, int64_t dim) {
-    return tiles_of(tokens, run_for(tokens, (dim + 127) / 128, kBackRun));
+// How the gradient is launched. The scratch is sized from the same plan: the channels per
+// block follow from the alignment, and with fewer of them a run can be longer or
+// shorter (whole waves), so the tiles of one form say nothing about another's.
+ConvBackwardPlan plan_conv_backward(const ConvParams &p) {
+    ConvBackwardPlan pl;
+    pl.channels = 32 * conv_vec(p, kBackwardVec);
+    pl.cols = (p.dim + pl.channels - 1) / pl.channels;
+    pl.run = run_for(p.tokens, pl.cols, kBackRun);
+    pl.tiles = tiles_of(p.tokens, pl.run);
+    pl.scratch_bytes = pl.tiles * (p.width + 1) * p.dim * 4;
+    return pl;
 }
 
-cudaError_t launch_conv_backward(const ConvParams &p, cudaStream_t stream) {
-    int64_t tiles = 0;
-    const cudaError_t e = with_shape<4>(p, [&](auto w, auto v, auto s) {
+cudaError_t launch_conv_backward(const ConvParams &p, const ConvBackwardPlan &pl, cudaStream_t stream) {
+    const cudaError_t e = with_shape<kBackwardVec>(p, [&](auto w, auto v, auto s) {
         constexpr int W = decltype(w)::value, VEC = decltype(v)::value;
         constexpr bool S = decltype(s)::value;
-        const int64_t cols = (p.dim + 32 * VEC - 1) / (32 * VEC), run = run_for(p.tokens, cols, kBackRun);
-        tiles = tiles_of(p.tokens, run);
-        const unsigned grid = static_cast<unsigned>(tiles * cols);
+        if (pl.channels != 32 * VEC) return cudaErrorInvalidValue;   // (another call's plan)
+        const unsigned grid = static_cast<unsigned>(pl.tiles * pl.cols);
+        const int run = static_cast<int>(pl.run);
         if (p.dout32)
             conv_backward_kernel<W, VEC, S, true>
-                <<<grid, kWarps * 32, back_bytes<W, VEC, true>(), stream>>>(p, static_cast<int>(run), cols);
+                <<<grid, kWarps * 32, back_bytes<W, VEC, true>(), stream>>>(p, run, pl.cols);
         else
             conv_backward_kernel<W, VEC, S, false>
-                <<<grid, kWarps * 32, back_bytes<W, VEC, false>(), stream>>>(p, static_cast<int>(run), cols);
+                <<<grid, kWarps * 32, back_bytes<W, VEC, false>(), stream>>>(p, run, pl.cols);
         return cudaGetLastError();
     });
     if (e != cudaSuccess) return e;
     const dim3 grid(static_cast<unsigned>((p.dim + 31) / 32), p.width + (p.dbias != nullptr));
-    conv_reduce_kernel<<<grid, 256, 0, stream>>>(p, tiles);
+    conv_reduce_kernel<<<grid, 256, 0, stream>>>(p, pl.tiles);
     return cudaGetLastError();
 }
 

@@ -252,10 +252,15 @@ struct ConvParams {
     int *err;
 };
 cudaError_t configure_conv();
-int64_t conv_backward_tiles(int64_t tokens, int64_t dim);
+// The gradient's grid: `cols` blocks of `channels` channels by `tiles` tiles of eight
+// runs; a partial sum of the weights' gradients per tile in the scratch.
+struct ConvBackwardPlan {
+    int64_t channels, cols, run, tiles, scratch_bytes;
+};
+ConvBackwardPlan plan_conv_backward(const ConvParams &p);
 cudaError_t launch_conv(const ConvParams &p, cudaStream_t stream);
 cudaError_t launch_conv_step(const ConvParams &p, cudaStream_t stream);
-cudaError_t launch_conv_backward(const ConvParams &p, cudaStream_t stream);
+cudaError_t launch_conv_backward(const ConvParams &p, const ConvBackwardPlan &pl, cudaStream_t stream);
 
 // Selective state space scan (kda_ssm.cu).
 struct SsmParams {

@@ -182,10 +182,6 @@ kda_status kda_short_conv_backward(const void *x, const float *weight, const flo
 
     const void *ptrs[] = {x, weight, bias, initial_state, cu_seqlens, d_out, d_final_state, dx,
                           dweight, dbias, d_initial_state};
-    kda::CallContext ctx;
-    const int64_t ws = kda::conv_backward_tiles(tokens, D) * (W + 1) * D * 4;
-    rc = static_cast<kda_status>(kda::begin_call(ptrs, 11, stream, ws, 0, &ctx));
-    if (rc != KDA_OK) return rc;
     kda::ConvParams p{};
     p.x = x; p.weight = weight; p.bias = bias; p.hist_in = initial_state; p.cu = cu_seqlens;
     p.tokens = tokens; p.seq_len = T; p.dim = D;
@@ -194,10 +190,34 @@ kda_status kda_short_conv_backward(const void *x, const float *weight, const flo
     p.silu = (flags & KDA_CONV_SILU) != 0;
     p.dout32 = dsize == 4;
     p.out = dx; p.dout = d_out; p.dhist_out = d_final_state; p.dhist_in = d_initial_state;
+    p.dweight = dweight; p.dbias = dbias;
+    const kda::ConvBackwardPlan plan = kda::plan_conv_backward(p);
+    kda::CallContext ctx;
+    rc = static_cast<kda_status>(kda::begin_call(ptrs, 11, stream, plan.scratch_bytes, 0, &ctx));
+    if (rc != KDA_OK) return rc;
     p.partial = reinterpret_cast<float *>(ctx.ws);
-    p.dweight = dweight; p.dbias = dbias; p.err = ctx.err;
-    return kda::launch_conv_backward(p, static_cast<cudaStream_t>(stream)) == cudaSuccess
+    p.err = ctx.err;
+    return kda::launch_conv_backward(p, plan, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_test_conv_backward_plan(const void *x, const void *d_out, const void *dx,
+                                       int64_t tokens, int64_t D, int64_t W, int64_t x_stride,
+                                       int64_t dout_stride, int64_t dx_stride, int flags,
+                                       int64_t plan[5]) {
+    if ((flags & ~(KDA_CONV_SILU | KDA_CONV_DOUT_FP32)) != 0) return KDA_ERR_BAD_FLAGS;
+    if (W < 2 || W > 4) return KDA_ERR_UNSUPPORTED_DIM;
+    if (tokens < 0 || D < 1) return KDA_ERR_BAD_SHAPE;
+    if (!plan) return KDA_ERR_NULL_ARG;
+    kda::ConvParams p{};
+    p.x = x; p.dout = d_out; p.out = const_cast<void *>(dx);
+    p.tokens = tokens; p.dim = D; p.width = static_cast<int32_t>(W);
+    p.x_stride = x_stride; p.out_stride = dx_stride; p.dout_stride = dout_stride;
+    p.dout32 = (flags & KDA_CONV_DOUT_FP32) != 0;
+    const kda::ConvBackwardPlan pl = kda::plan_conv_backward(p);
+    plan[0] = pl.scratch_bytes; plan[1] = pl.channels; plan[2] = pl.cols;
+    plan[3] = pl.run; plan[4] = pl.tiles;
+    return KDA_OK;
 }
 
 // The checks that the two scan entry points share; `rows` tokens, `seqs` states.

@@ -206,6 +206,33 @@ def test_conv_gradient_without_tokens():
     assert not dw.any() and not db.any() and torch.equal(dh, df)
 
 
+@pytest.mark.parametrize("T,D,off,d32", [(14400, 2050, 0, True), (7180, 3841, 0, False),
+                                         (13766, 2112, 1, False), (9001, 385, 0, True)])
+def test_conv_gradient_one_channel_per_thread_over_waves(T, D, off, d32):
+    """Widths and offsets that leave one channel per thread, at sizes of several waves
+    of blocks, on a stream whose scratch is no larger than this call asks for."""
+    r = make(T + D)
+    x = r(T, D + off)[:, off:]
+    w, b = r(D, 4, dtype=F32, scale=0.5), r(D, dtype=F32)
+    dy = r(T, D + off, dtype=F32 if d32 else BF16)[:, off:]
+    cu = cu_of([T - 5, 0, 5])
+    K.check_device_error()
+    assert K.kda_workspace_release() == 0
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = K.short_conv_backward(x, w, dy, bias=b, cu_seqlens=cu.cuda())
+        again = K.short_conv_backward(x, w, dy, bias=b, cu_seqlens=cu.cuda())
+        K.check_device_error()
+    side.synchronize()
+    ch = [0, 1, 31, 32, D // 2, D - 2, D - 1]
+    ref = ops.short_conv_backward(x[:, ch], w[ch], dy[:, ch], b[ch], cu=cu, n=3)
+    for g, g2, name in zip(got, again, ("dx", "dweight", "dbias", "dstate")):
+        g, g2 = (g[ch], g2[ch]) if name in ("dweight", "dbias") else (g[..., ch], g2[..., ch])
+        close(g, *ref[name], name)
+        assert torch.equal(g, g2), "not the same bits again"
+
+
 # ---------------------------------------------------------------- the scan
 
 def ssm_case(lens, H, P, G, N, state, seed=0, fused=True, dt_scale=0.5, step=(1e-3, 0.1)):

@@ -210,3 +210,29 @@ def test_python_front_refuses():
                        torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16),
                        torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16),
                        torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("d32", [False, True])
+@pytest.mark.parametrize("off", [0, 4, 1])
+def test_conv_gradient_scratch_holds_every_tile(off, d32):
+    """Each form of the gradient (its channels per block follow from the width and the
+    alignment) asks for the scratch that its own tiles write."""
+    g = torch.Generator().manual_seed(10 * off + d32)
+    cases = [(7180, 3841), (13766, 2112), (14400, 2050), (27712, 1026), (71708, 385),
+             (87297, 800), (131072, 130), (126474, 150), (0, 5), (1, 1)]
+    for _ in range(1000):
+        u, v = torch.rand(2, generator=g, dtype=torch.float64).tolist()
+        cases.append((int(2 ** (18 * u)), int(2 ** (14 * v))))
+    forms = set()
+    for T, D in cases:
+        at, stride = A + 2 * off, -(-(D + off) // 8) * 8
+        rc, (scratch, channels, cols, run, tiles) = K.kda_test_conv_backward_plan(
+            at, A + (4 if d32 else 2) * off, at, T, D, 4, stride, stride, stride,
+            K.CONV_DOUT_FP32 * d32)
+        assert rc == 0
+        forms.add(channels)
+        assert channels == (32 if off == 1 or D % 4 else 128)
+        assert (cols - 1) * channels < D <= cols * channels
+        assert (tiles - 1) * 8 * run < max(T, 1) <= tiles * 8 * run   # every token, no empty tile
+        assert scratch >= tiles * 5 * D * 4, (T, D, channels)
+    assert forms == ({32} if off == 1 else {32, 128})
