@@ -67,11 +67,13 @@ __device__ __forceinline__ float ex2(float x) {
 
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v| <= 1, to a few units of the
 // last place at every v (the state is linear in it). e^-|v|: the rounding error
-// of |v| log2(e) is put back to first order. log(1 + e) = 2 atanh z with
+// of |v| log2(e) is put back to first order. |v| is held at 128, where e is below
+// fp32's range, so that the product stays finite up to the largest |v| and infinity
+// (a token masked with the lowest value has delta = 0); a NaN passes. log(1 + e) = 2 atanh z with
 // z = e / (2 + e) <= 1/3, whose series z (1 + z^2/3 + ... + z^16/17) ends at
 // 3^-18/19 = 1.4e-10 and keeps the relative precision of small e.
 __device__ __forceinline__ float softplus(float v) {
-    const float x = -fabsf(v), t = x * 1.44269504f;
+    const float x = fabsf(v) > 128.f ? -128.f : -fabsf(v), t = x * 1.44269504f;
     const float r = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;   // log2(e) - 1.44269504f
     const float e2 = ex2(t), e = fmaf(e2 * 0.69314718f, r, e2);
     const float z = __fdividef(e, 2.f + e), q = z * z;

@@ -394,6 +394,46 @@ def test_ssm_step(S, H, P, G, N, state):
         assert torch.equal(o2, o) and torch.equal(s1, f)
 
 
+@pytest.mark.parametrize("lens,H,P,G,N", [([300, 7], 3, 64, 1, 128), ([1100], 2, 128, 2, 64)])
+def test_ssm_softplus_far_from_zero(lens, H, P, G, N):
+    """Tokens masked with the lowest value of the type or -infinity (delta = 0: the state
+    stays as it is), and steps far on either side of zero."""
+    x, dt, a, b, c, d, bias, s0 = ssm_case(lens, H, P, G, N, True)
+    T = sum(lens)
+    low = [torch.finfo(F32).min, -math.inf, -2.5e38, -1e30, -130.0, -88.0, -40.0, 20.0, 100.0]
+    for i, v in enumerate(low):
+        dt[i::11] = v
+    dt[T // 2:T // 2 + 40] = torch.finfo(F32).min
+    cu = cu_of(lens)
+    o, f = K.ssm_prefill(x, dt, a, b, c, d, bias, initial_state=s0, cu_seqlens=cu.cuda(),
+                         dt_softplus=True)
+    K.check_device_error()
+    ro, rf, so, sf = ops.ssm(x, dt, a, b, c, d, bias, s0, cu=cu, n=len(lens), softplus=True)
+    close(o, ro, so, "out")
+    close(f, rf, sf, "state")
+    # one token each, from the same values (and the largest, where x is 0)
+    S = 12
+    s0 = make(5)(S, H, N, P, dtype=F32)
+    dt[11], x[11] = torch.finfo(F32).max, 0
+    args = [t[:S] for t in (x, dt, b, c)]
+    o, f = K.ssm_step(args[0], args[1], a, args[2], args[3], s0, d, bias, dt_softplus=True)
+    ro, rf, so, sf = ops.ssm(args[0], args[1], a, args[2], args[3], d, bias, s0, cu=range(S + 1),
+                             n=S, softplus=True)
+    close(o, ro, so, "step out")
+    close(f, rf, sf, "step state")
+
+
+def test_ssm_nan_steps_stay_nan():
+    x, dt, a, b, c, d, bias, _ = ssm_case([200], 2, 64, 1, 128, False)
+    dt[150, 1] = math.nan
+    o, f = K.ssm_prefill(x, dt, a, b, c, d, bias, dt_softplus=True)
+    assert torch.isfinite(o[:, 0].float()).all() and torch.isfinite(f[0, 0]).all()
+    assert torch.isfinite(o[:150].float()).all()
+    assert o[150:, 1].float().isnan().all() and f[0, 1].isnan().all()
+    o, f = K.ssm_step(x[149:151], dt[149:151], a, b[149:151], c[149:151], None, d, bias, dt_softplus=True)
+    assert torch.isfinite(o[0].float()).all() and f[1, 1].isnan().all()
+
+
 # --------------------------------------------------------- paged attention
 
 def cache_case(lens, Hq, Hkv, D, page, seed=0, poison=True, spare=3, one=True):
