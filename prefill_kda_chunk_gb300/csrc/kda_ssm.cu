@@ -21,9 +21,9 @@
 // well below the bf16 output's rounding), and the weighted rows W X as three (24
 // bits: the state is an fp32 result and keeps fp32's precision over any length).
 //
-// Every exponent is a difference of running sums kept as two floats, so it is
-// as exact next to a token that forgets everything (G falls by thousands) as
-// anywhere; between 32-token blocks it is split at the block's end into two
+// Every exponent is a difference of running sums kept as two floats, a token's share of
+// which is at least -1024 (its decay is then 0), so it is as exact next to a token
+// that forgets everything as anywhere; between 32-token blocks it is split at the block's end into two
 // factors <= 1, so only the diagonal blocks take an exponential per pair. These sums
 // and factors come from a launch of their own (ssm_decays_kernel).
 //
@@ -89,6 +89,13 @@ __device__ __forceinline__ float softplus(float v) {
     return v > 0.f ? v + l : l;
 }
 __device__ __forceinline__ float delta_of(float v, bool plus) { return plus ? softplus(v) : v; }
+// A token's log decay, a delta log2(e), held at -1024: 2^-1024 is 0 in fp32, whatever
+// growth within fp32's range stands beside it, and the running sums of a chunk stay so
+// small (2^17) that two floats resolve the tokens behind the one that forgets all.
+__device__ __forceinline__ float log_decay(float a2, float delta) {
+    const float g = a2 * delta;
+    return g < -1024.f ? -1024.f : g;
+}
 
 // ------------------------------------------------------------- one token
 
@@ -498,7 +505,7 @@ __global__ void __launch_bounds__(256) ssm_decays_kernel(SsmParams p, SsmPlan pl
         Sum2 sum{0.f, 0.f}, g[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            sum.add(a2 * dt[j], 0.f);
+            sum.add(log_decay(a2, dt[j]), 0.f);
             g[j] = sum;
         }
         Sum2 incl = sum;

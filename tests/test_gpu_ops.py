@@ -434,6 +434,20 @@ def test_ssm_nan_steps_stay_nan():
     assert torch.isfinite(o[0].float()).all() and f[1, 1].isnan().all()
 
 
+@pytest.mark.parametrize("huge", [1e9, 1e15, 1e30])
+def test_ssm_steps_that_forget_everything_keep_later_decays_exact(huge):
+    """A huge delta on a token with x = 0 empties the state; the sums of the tokens behind
+    it in the same chunk must not drown in it."""
+    x, dt, a, b, c, d, _, s0 = ssm_case([700], 3, 64, 1, 128, True, fused=False)
+    dt = dt.abs()
+    at = [0, 5, 60, 127, 128, 300, 301, 511, 650]
+    dt[at], x[at] = huge, 0
+    y, f = K.ssm_prefill(x, dt, a, b, c, d, initial_state=s0)
+    ro, rf, so, sf = ops.ssm(x, dt, a, b, c, d, state=s0)
+    close(y, ro, so, "out")
+    close(f, rf, sf, "state")
+
+
 # --------------------------------------------------------- paged attention
 
 def cache_case(lens, Hq, Hkv, D, page, seed=0, poison=True, spare=3, one=True):
