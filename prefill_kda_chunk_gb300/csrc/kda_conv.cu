@@ -98,11 +98,13 @@ __device__ __forceinline__ void store_f32(float *dst, const float (&f)[VEC]) {
 // of each per pair would keep as busy as HBM. e^-z is held at 2^63, so that the
 // product stays finite and no channel can reach the other: below z = -43.7 the
 // result is 2^-63 instead of something smaller.
-__device__ __forceinline__ void sigmoid2(float z0, float z1, float &s0, float &s1) {
+// e0 and e1 are e^-z: the gradient takes 1 - s as e^-z s, since s is 1 but for its
+// rounding at large z and z would multiply that.
+__device__ __forceinline__ void sigmoid2(float z0, float z1, float &s0, float &s1, float &e0, float &e1) {
     mul2(z0, z1, -1.44269504f, -1.44269504f);
-    float a, b, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(fminf(z0, 63.f)));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(fminf(z1, 63.f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fminf(z0, 63.f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fminf(z1, 63.f)));
+    float a = e0, b = e1, r;
     add2(a, b, 1.f, 1.f);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
     s0 = b;
@@ -110,13 +112,13 @@ __device__ __forceinline__ void sigmoid2(float z0, float z1, float &s0, float &s
     mul2(s0, s1, r, r);
 }
 template <int VEC>
-__device__ __forceinline__ void sigmoids(const float (&z)[VEC], float (&s)[VEC]) {
+__device__ __forceinline__ void sigmoids(const float (&z)[VEC], float (&s)[VEC], float (&e)[VEC]) {
     if constexpr (VEC == 1) {
-        float other;
-        sigmoid2(z[0], 0.f, s[0], other);
+        float s1, e1;
+        sigmoid2(z[0], 0.f, s[0], s1, e[0], e1);
     } else {
 #pragma unroll
-        for (int i = 0; i < VEC; i += 2) sigmoid2(z[i], z[i + 1], s[i], s[i + 1]);
+        for (int i = 0; i < VEC; i += 2) sigmoid2(z[i], z[i + 1], s[i], s[i + 1], e[i], e[i + 1]);
     }
 }
 // The arithmetic on a thread's channels goes two by two, in packed instructions: with
@@ -155,8 +157,8 @@ __device__ __forceinline__ void copy(float (&a)[VEC], const float (&x)[VEC]) {
 }
 template <int VEC>
 __device__ __forceinline__ void silu(float (&z)[VEC]) {
-    float s[VEC];
-    sigmoids<VEC>(z, s);
+    float s[VEC], e[VEC];
+    sigmoids<VEC>(z, s, e);
     times<VEC>(z, s);
 }
 
@@ -467,15 +469,12 @@ conv_backward_kernel(ConvParams p, int run, int64_t col_blocks) {
                 plus<VEC>(z, f.w[W - 1], row);
                 copy<VEC>(dz, g);
                 if (SILU) {   // s (1 + z (1 - s))
-                    float sg[VEC], ones[VEC], t[VEC], m[VEC];
-                    sigmoids<VEC>(z, sg);
+                    float sg[VEC], rest[VEC], ones[VEC];
+                    sigmoids<VEC>(z, sg, rest);
+                    times<VEC>(rest, sg);   // 1 - s
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        t[i] = ones[i] = 1.f;
-                        m[i] = -1.f;
-                    }
-                    plus<VEC>(t, sg, m);
-                    plus<VEC>(ones, z, t);
+                    for (int i = 0; i < VEC; ++i) ones[i] = 1.f;
+                    plus<VEC>(ones, z, rest);
                     times<VEC>(sg, ones);
                     times<VEC>(dz, sg);
                 }

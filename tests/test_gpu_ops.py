@@ -233,6 +233,26 @@ def test_conv_gradient_one_channel_per_thread_over_waves(T, D, off, d32):
         assert torch.equal(g, g2), "not the same bits again"
 
 
+@pytest.mark.parametrize("D", [32, 7])
+def test_conv_gradient_of_silu_at_large_z(D):
+    """s (1 + z (1 - s)) tends to 1: an error of s itself must not be multiplied by z. The
+    filter is one tap of 1, so z = x; a bf16 dx may be off by 2^-8 of it, the fp32 sums by
+    2^-17 of their terms."""
+    large = [15.0, 30.0, 1000.0, 1e5, 1e7, 1e10, 1e20, 1e30]
+    x = make(D)(2 * len(large), D)
+    x[:, ::3] = torch.tensor(large * 2, device="cuda").to(BF16)[:, None]
+    w = torch.zeros(D, 2, device="cuda")
+    w[:, 1] = 1
+    z = x.cpu().double()
+    s = torch.sigmoid(z)
+    dz = s * (1 + z * torch.sigmoid(-z))
+    for dtype in (F32, BF16):
+        dx, dw, db, _ = K.short_conv_backward(x, w, torch.ones_like(x, dtype=dtype), torch.zeros(D, device="cuda"))
+        close(dx, dz, s * (1 + z.abs() * torch.sigmoid(-z)), "dx")
+        close(dw[:, 1], (dz * z).sum(0), (dz * z).abs().sum(0), "dweight")
+        close(db, dz.sum(0), dz.abs().sum(0) + 1, "dbias")
+
+
 # ---------------------------------------------------------------- the scan
 
 def ssm_case(lens, H, P, G, N, state, seed=0, fused=True, dt_scale=0.5, step=(1e-3, 0.1)):
