@@ -93,34 +93,6 @@ __device__ __forceinline__ void store_f32(float *dst, const float (&f)[VEC]) {
     }
 }
 
-// 1 / (1 + e^-z) of two values with one reciprocal: r = 1 / (a b), 1 / a = r b. The
-// exponential and the reciprocal share one unit of 16 results a clock and SM, which two
-// of each per pair would keep as busy as HBM. e^-z is held at 2^63, so that the
-// product stays finite and no channel can reach the other: below z = -43.7 the
-// result is 2^-63 instead of something smaller.
-// e0 and e1 are e^-z: the gradient takes 1 - s as e^-z s, since s is 1 but for its
-// rounding at large z and z would multiply that.
-__device__ __forceinline__ void sigmoid2(float z0, float z1, float &s0, float &s1, float &e0, float &e1) {
-    mul2(z0, z1, -1.44269504f, -1.44269504f);
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fminf(z0, 63.f)));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fminf(z1, 63.f)));
-    float a = e0, b = e1, r;
-    add2(a, b, 1.f, 1.f);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * b));
-    s0 = b;
-    s1 = a;
-    mul2(s0, s1, r, r);
-}
-template <int VEC>
-__device__ __forceinline__ void sigmoids(const float (&z)[VEC], float (&s)[VEC], float (&e)[VEC]) {
-    if constexpr (VEC == 1) {
-        float s1, e1;
-        sigmoid2(z[0], 0.f, s[0], s1, e[0], e1);
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; i += 2) sigmoid2(z[i], z[i + 1], s[i], s[i + 1], e[i], e[i + 1]);
-    }
-}
 // The arithmetic on a thread's channels goes two by two, in packed instructions: with
 // single ones the forward issued in 74 % of all slots (53 us, this way 51).
 template <int VEC>
@@ -130,6 +102,61 @@ __device__ __forceinline__ void times(float (&a)[VEC], const float (&x)[VEC]) {
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; i += 2) mul2(a[i], a[i + 1], x[i], x[i + 1]);
+    }
+}
+
+// 1 / (1 + e^-z) of two values with one reciprocal: r = 1 / (a b), 1 / a = r b. The
+// exponential and the reciprocal share one unit of 16 results a clock and SM, which two
+// of each per pair would keep as busy as HBM. e^-z is held at 2^63, so that the
+// product stays finite and no channel can reach the other: right down to z = kFar.
+// e0 and e1 are e^-z: the gradient takes 1 - s as e^-z s, since s is 1 but for its
+// rounding at large z and z would multiply that. Returns a b.
+__device__ __forceinline__ float sigmoid2(float z0, float z1, float &s0, float &s1, float &e0, float &e1) {
+    mul2(z0, z1, -1.44269504f, -1.44269504f);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(fminf(z0, 63.f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(fminf(z1, 63.f)));
+    float a = e0, b = e1, r;
+    add2(a, b, 1.f, 1.f);
+    const float ab = a * b;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ab));
+    s0 = b;
+    s1 = a;
+    mul2(s0, s1, r, r);
+    return ab;
+}
+// s and 1 - s (`rest`) of a thread's channels, right down to kFar; the products a b, none
+// of them below 1, are added to `products`. Where they add up to kFarSum or more, a
+// channel may be below kFar.
+constexpr float kFar = -43.66f, kFarSum = 4.6e18f;   // (2^62)
+template <int VEC>
+__device__ __forceinline__ void sigmoids_near(const float (&z)[VEC], float (&s)[VEC], float (&rest)[VEC],
+                                              float (&products)[2]) {
+    if constexpr (VEC == 1) {
+        float s1, e1;
+        products[0] += sigmoid2(z[0], 0.f, s[0], s1, rest[0], e1);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 4) {
+            const float u = sigmoid2(z[i], z[i + 1], s[i], s[i + 1], rest[i], rest[i + 1]);
+            const float v = sigmoid2(z[i + 2], z[i + 3], s[i + 2], s[i + 3], rest[i + 2], rest[i + 3]);
+            add2(products[0], products[1], u, v);
+        }
+    }
+    times<VEC>(rest, s);
+}
+// ... at any z: below kFar the sigmoid is e^z to fp32's precision (down to its
+// subnormals), which only a thread with such a channel computes.
+template <int VEC>
+__device__ __forceinline__ void sigmoids(const float (&z)[VEC], float (&s)[VEC], float (&rest)[VEC]) {
+    float products[2] = {0.f, 0.f};
+    sigmoids_near<VEC>(z, s, rest, products);
+    if (products[0] + products[1] >= kFarSum) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            float t;
+            asm("ex2.approx.f32 %0, %1;" : "=f"(t) : "f"(z[i] * 1.44269504f));
+            if (z[i] < kFar) s[i] = t;
+        }
     }
 }
 template <int VEC>
@@ -157,8 +184,8 @@ __device__ __forceinline__ void copy(float (&a)[VEC], const float (&x)[VEC]) {
 }
 template <int VEC>
 __device__ __forceinline__ void silu(float (&z)[VEC]) {
-    float s[VEC], e[VEC];
-    sigmoids<VEC>(z, s, e);
+    float s[VEC], rest[VEC];
+    sigmoids<VEC>(z, s, rest);
     times<VEC>(z, s);
 }
 
@@ -288,11 +315,16 @@ conv_kernel(ConvParams p, int run, int64_t col_blocks) {
         load_window<W, VEC>(p, n, a, lo, d, win);
         const uint16_t *src = static_cast<const uint16_t *>(p.x) + lo * p.x_stride + d;
         uint16_t *dst = static_cast<uint16_t *>(p.out) + lo * p.out_stride + d;
-        auto row_out = [&](const R &raw, uint16_t *to) {
+        auto row_out = [&](const R &raw, uint16_t *to, float (&products)[2]) {
             float row[VEC], z[VEC];
             widen<VEC>(raw, row);
             step_window<W, VEC>(f, win, row, z);
-            if (SILU) silu<VEC>(z);
+            if (SILU) {
+                float s[VEC], rest[VEC];
+                if constexpr (VEC > 1) sigmoids_near<VEC>(z, s, rest, products);
+                else sigmoids<VEC>(z, s, rest);
+                times<VEC>(z, s);
+            }
             *reinterpret_cast<R *>(to) = narrow<VEC>(z);
         };
         const int rows = static_cast<int>(hi - lo);
@@ -315,16 +347,33 @@ conv_kernel(ConvParams p, int run, int64_t col_blocks) {
                 fetch(r0 + (kDepth - 1) * kGroup);
                 copies_but<kDepth - 1>();
                 const R *from = ring + r0 / kGroup % kDepth * kGroup * kWarps * 32;
+                float products[2] = {0.f, 0.f};
 #pragma unroll
                 for (int u = 0; u < kGroup; ++u) {
-                    if (r0 + u < rows) row_out(from[u * kWarps * 32], dst);
+                    if (r0 + u < rows) row_out(from[u * kWarps * 32], dst, products);
                     dst += p.out_stride;
+                }
+                // a group with a channel below kFar is formed again, row by row out of L2
+                // (a branch per group: with one per row the forward takes 53.4 us, this way 52.2)
+                if (SILU && products[0] + products[1] >= kFarSum) {
+#pragma unroll 1
+                    for (int u = 0; u < kGroup && r0 + u < rows; ++u) {
+                        float past[W - 1][VEC], row[VEC], z[VEC];
+                        const int64_t t = lo + r0 + u;
+                        load_window<W, VEC>(p, n, a, t, d, past);
+                        widen<VEC>(load_row<VEC>(p.x, t * p.x_stride + d), row);
+                        step_window<W, VEC>(f, past, row, z);
+                        silu<VEC>(z);
+                        *reinterpret_cast<R *>(static_cast<uint16_t *>(p.out) + t * p.out_stride + d) =
+                            narrow<VEC>(z);
+                    }
                 }
             }
         } else {
 #pragma unroll 4
             for (int r = 0; r < rows; ++r) {
-                row_out(*reinterpret_cast<const R *>(src), dst);
+                float products[2];
+                row_out(*reinterpret_cast<const R *>(src), dst, products);
                 src += p.x_stride;
                 dst += p.out_stride;
             }
@@ -471,7 +520,6 @@ conv_backward_kernel(ConvParams p, int run, int64_t col_blocks) {
                 if (SILU) {   // s (1 + z (1 - s))
                     float sg[VEC], rest[VEC], ones[VEC];
                     sigmoids<VEC>(z, sg, rest);
-                    times<VEC>(rest, sg);   // 1 - s
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) ones[i] = 1.f;
                     plus<VEC>(ones, z, rest);

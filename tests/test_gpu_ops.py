@@ -253,6 +253,38 @@ def test_conv_gradient_of_silu_at_large_z(D):
         close(db, dz.sum(0), dz.abs().sum(0) + 1, "dbias")
 
 
+FAR = [-43.0, -44.0, -50.0, -60.0, -87.0, -95.0, -130.0, -1e10, -1e30, 30.0, 1e30]
+
+
+@pytest.mark.parametrize("D", [32, 7])
+def test_conv_silu_far_from_zero(D):
+    """z / (1 + e^-z) and its gradient to the ends of the range, ordinary channels beside.
+    The filter is one tap of 1, so z = x. A bf16 result may be off by its rounding (2^-8 of
+    it is allowed, and fp32's smallest normal number), an fp32 sum by 2^-17 of its terms."""
+    T = 2 * len(FAR)
+    x = make(D)(T, D)
+    x[:, ::3] = torch.tensor(FAR * 2, device="cuda").to(BF16)[:, None]
+    w = torch.zeros(D, 2, device="cuda")
+    w[:, 1] = 1
+    z = x.cpu().double()
+    s = torch.sigmoid(z)
+
+    def near(got, ref, tag, rel=2.0 ** -8):
+        got = got.cpu().double()
+        assert torch.isfinite(got).all(), tag
+        assert ((got - ref).abs() <= rel * ref.abs() + 2.0 ** -126).all(), tag
+
+    near(K.short_conv(x, w)[0], z * s, "prompt")
+    near(K.short_conv_step(x, w)[0], z * s, "step")
+    for dtype in (F32, BF16):
+        dy = torch.ones(T, D, device="cuda", dtype=dtype)
+        dx, dw, _, _ = K.short_conv_backward(x, w, dy)
+        dz = s * (1 + z * (1 - s))
+        near(dx, dz, "dx")
+        size = (dz * z).abs().sum(0) + (dz.abs() * (1 + z.abs()) * z.abs() * 2.0 ** -24).sum(0)
+        assert ((dw[:, 1].cpu().double() - (dz * z).sum(0)).abs() <= 2.0 ** -17 * size).all(), "dweight"
+
+
 # ---------------------------------------------------------------- the scan
 
 def ssm_case(lens, H, P, G, N, state, seed=0, fused=True, dt_scale=0.5, step=(1e-3, 0.1)):
