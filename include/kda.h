@@ -360,6 +360,10 @@ KDA_API kda_status kda_short_conv_backward(const void *x, const float *weight, c
  *                initial_state
  *   P = 64 or 128, n = 64 or 128 (others: KDA_ERR_UNSUPPORTED_DIM).
  *
+ * An infinity or NaN in x makes that channel of out NaN from its token to the
+ * sequence's end, and that column of the state not finite; earlier tokens and
+ * other channels are not touched.
+ *
  * Alignment: x, b, c, out and the states 16 bytes, and x_stride, b_stride,
  * c_stride multiples of 8 elements; fp32 vectors and cu_seqlens 4 bytes.
  * States, decays and sums are held in fp32; the outputs and states of a call are the

@@ -182,6 +182,10 @@ struct alignas(16) Scalars : Decays {
     int flags;              // kLast, kCut
     int xcol, gcol;         // its first column of x, and of b and c
     int64_t row;            // its first token
+    // Infinities and NaN in x: the 32-row by 8-channel pieces that hold any (bit 8 * block
+    // + granule), and in those the first row of each channel that does (kL: none).
+    unsigned odd;
+    uint8_t odd_from[4][kPS];
 };
 enum { kLast = 1, kCut = 2 };   // the sequence's last chunk; the run's end cuts the sequence
 constexpr int kOffBar = kOffSc + kRing * static_cast<int>(sizeof(Scalars));
@@ -199,6 +203,7 @@ enum {   // barriers, 8 bytes each; pairs and the ring by the chunk's index
 };
 constexpr int kOffMisc = kOffBar + 8 * kBars;    // tensor memory base, abort flag
 constexpr int kSmem = kOffMisc + 8;
+static_assert(kSmem <= 232448, "what a block can have");
 
 // Tensor memory columns; the block takes all of them, so they start at 0. C B^T has
 // two buffers of 128; M replaces it there: 16 columns (tokens s) become the 8 columns
@@ -296,6 +301,11 @@ __device__ __forceinline__ void fma2(float &a, float &b, float x, float y, float
     asm("{\n .reg .b64 t, s, w;\n mov.b64 t, {%0, %1};\n mov.b64 s, {%2, %3};\n mov.b64 w, {%4, %5};\n"
         " fma.rn.f32x2 t, t, s, w;\n mov.b64 {%0, %1}, t;\n}\n"
         : "+f"(a), "+f"(b) : "f"(x), "f"(y), "f"(u), "f"(v));
+}
+
+// Two bf16 values: acc stays +-0 as long as every x was finite, and becomes NaN otherwise.
+__device__ __forceinline__ void look_for_odd(uint32_t &acc, uint32_t x) {
+    asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
 }
 
 // (a, b) as two bf16 terms: hi + lo; (a, b) keeps what hi leaves
@@ -621,13 +631,19 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
     };
     auto all = [&](bool ok) { return __all_sync(0xffffffffu, ok) != 0; };
     // The weighted rows of chunk i as three bf16 terms, in 32 tasks of 32
-    // rows x 8 channels, Rows past the end of the sequence belong to
+    // rows x 8 channels. Rows past the end of the sequence belong to
     // another one: they are zeroed here, as no weight of 0 makes an infinity or NaN
     // vanish. (With two groups each takes 16 of the tasks.)
+    // Nor does one of M's zeros: an infinity or NaN of x would reach the tokens in front
+    // of its own through M X. Such values become 0 in the tile that M X reads, while W X,
+    // and with it the state, keep them, and take_out makes their channel NaN from their
+    // token on. (Looking for them, an instruction per two values: T 8192, 64 heads 118.2
+    // -> 119.5 us.)
     auto put_rows = [&](int i, int task0, int tasks) {
         uint8_t *X = smem + kOffX + (i & 1) * kTileBytes, *W = smem + off_w(kStates, i);
-        const Scalars &s = scal[i & (kRing - 1)];
+        Scalars &s = scal[i & (kRing - 1)];
         const int valid = s.valid;
+        uint32_t odd = 0;
 #pragma unroll 1
         for (int k0 = task0; k0 < task0 + tasks; k0 += 2) {
             uint4 xv[2];
@@ -653,6 +669,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 uint32_t t0[4], t1[4], t2[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
+                    if (!kStates) look_for_odd(odd, xs[e]);
                     float a = __uint_as_float(xs[e] << 16), b = __uint_as_float(xs[e] & 0xffff0000u);
                     mul2(a, b, wts[m], wts[m]);
                     t0[e] = take2(a, b);
@@ -661,6 +678,23 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 *reinterpret_cast<uint4 *>(W + ats[m]) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
                 *reinterpret_cast<uint4 *>(W + kTileBytes + ats[m]) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
                 *reinterpret_cast<uint4 *>(W + 2 * kTileBytes + ats[m]) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+            }
+        }
+        if (!kStates && __any_sync(0xffffffffu, (odd & 0x7fff7fffu) != 0)) {
+#pragma unroll 1
+            for (int k = task0; k < task0 + tasks; ++k) {
+                const int row = (k >> 3) * 32 + lane;
+                uint16_t *x = reinterpret_cast<uint16_t *>(X + row * 128 + (((k ^ row) & 7) << 4));
+                bool any = false;
+#pragma unroll 1
+                for (int e = 0; e < 8; ++e) {
+                    const bool is = (x[e] & 0x7f80) == 0x7f80;
+                    const unsigned rows = __ballot_sync(0xffffffffu, is);
+                    if (is) x[e] = 0;
+                    if (lane == 0) s.odd_from[k >> 3][(k & 7) * 8 + e] = rows != 0 ? (k & ~7) * 4 + __ffs(rows) - 1 : kL;
+                    any |= rows != 0;
+                }
+                if (lane == 0 && any) atomicOr(&s.odd, 1u << k);
             }
         }
         fence_async();
@@ -770,6 +804,7 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 s.pos = w.pos;
                 s.flags = (w.last() ? kLast : 0) | (q0 + j + (w.len + kL - 1) / kL - w.pos > q1 ? kCut : 0);
                 s.row = w.row();
+                s.odd = 0;
                 s.xcol = h * p.p + (w.u & pl.shift) * kPS;
                 s.gcol = h / per_group * kN;
                 constexpr int kFrom = kStates ? kDecaysTail : 0;
@@ -873,6 +908,25 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                     os[e] = pack_bf16(a, b);
                 }
                 ys[k] = make_uint4(os[0], os[1], os[2], os[3]);
+            }
+            // (written before the arrival that let M X start)
+            const unsigned odd = *const_cast<const volatile unsigned *>(&s.odd);
+            if (odd != 0) {
+                uint32_t nan = 0;   // of this row's channels
+#pragma unroll 1
+                for (int ch = 0; ch < kCols; ++ch)
+#pragma unroll 1
+                    for (int b = 0; b < 4; ++b)
+                        if ((odd >> (8 * b + ((kCols * hf + ch) >> 3)) & 1) != 0 &&
+                            r >= s.odd_from[b][kCols * hf + ch])
+                            nan |= 1u << ch;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        reinterpret_cast<uint32_t *>(&ys[k])[e] |=
+                            (nan >> (8 * k + 2 * e) & 1 ? 0x7fffu : 0u) |
+                            (nan >> (8 * k + 2 * e + 1) & 1 ? 0x7fff0000u : 0u);
             }
             tc::fence_before();
             __syncwarp();

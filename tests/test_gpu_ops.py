@@ -500,6 +500,31 @@ def test_ssm_steps_that_forget_everything_keep_later_decays_exact(huge):
     close(f, rf, sf, "state")
 
 
+@pytest.mark.parametrize("lens,H,P,G,N", [([200], 2, 64, 1, 128), ([1500, 40, 0, 300], 3, 64, 1, 64),
+                                          ([900, 128], 2, 128, 2, 128), ([20000], 2, 64, 1, 128)])
+def test_ssm_non_finite_x_stays_in_its_channel_and_behind_its_token(lens, H, P, G, N):
+    """An infinity or NaN in x at token s: y is not finite from s to the sequence's end, nor
+    is that column of the state, and every other value has the bits it has without it."""
+    x, dt, a, b, c, d, bias, s0 = ssm_case(lens, H, P, G, N, True)
+    cu, T = cu_of(lens), sum(lens)
+    kw = dict(initial_state=s0, cu_seqlens=cu.cuda(), dt_softplus=True)
+    o, f = K.ssm_prefill(x, dt, a, b, c, d, bias, **kw)
+    x2, want, state = x.clone(), torch.ones(T, H, P, dtype=torch.bool), torch.ones(f.shape, dtype=torch.bool)
+    spots = [(0, 0, 0, math.inf), (31, 0, 1, math.nan), (32, 1, P - 1, -math.inf), (100, 1, 17, math.nan),
+             (127, 1, 40, math.inf), (150, 0, 1, math.nan), (170, 1, 40, math.nan), (T - 1, 0, 33, math.nan),
+             (T - 20, 0, 34, math.inf), (T - 129, 1, 35, math.nan)]
+    for t, h, p, v in spots:
+        x2[t, h, p] = v
+        seq = int(torch.searchsorted(cu.long()[1:], t, right=True))
+        want[t:int(cu[seq + 1]), h, p] = False
+        state[seq, h, :, p] = False
+    o2, f2 = K.ssm_prefill(x2, dt, a, b, c, d, bias, **kw)
+    K.check_device_error()
+    assert torch.equal(torch.isfinite(o2.float()).cpu(), want)
+    assert torch.equal(torch.isfinite(f2).cpu(), state)
+    assert torch.equal(o2.cpu()[want], o.cpu()[want]) and torch.equal(f2.cpu()[state], f.cpu()[state])
+
+
 # --------------------------------------------------------- paged attention
 
 def cache_case(lens, Hq, Hkv, D, page, seed=0, poison=True, spare=3, one=True):
