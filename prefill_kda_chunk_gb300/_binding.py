@@ -683,7 +683,7 @@ def _ssm_inputs(x, dt, a, b, c, d, dt_bias, rows):
     for name, t in (("a", a), ("d", d), ("dt_bias", dt_bias)):
         if t is not None or name == "a":
             _need(name, t, torch.float32, (H,))
-    if H % G:
+    if G == 0 or H % G:
         raise ValueError("the heads must be a multiple of the groups of b and c")
     return H, P, G, n
 
@@ -790,7 +790,7 @@ def paged_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, out=None
     _need("page_table", page_table, torch.int32, (B, page_table.shape[1]))
     _need("seq_lens", seq_lens, torch.int32, (B,))
     if scale is None:
-        scale = 1.0 / math.sqrt(D)
+        scale = 1.0 / math.sqrt(max(D, 1))   # (D = 0 is refused below)
     if out is None:
         out = torch.empty_like(q)
     else:

@@ -645,6 +645,17 @@ def test_paged_offsets_past_32_bits():
     attention_close(o, l, q, k, v, table, [230])
 
 
+def test_sizes_of_zero_are_refused():
+    x, dt, a, b, c, d, bias, _ = ssm_case([4], 2, 64, 1, 128, False, fused=False)
+    with pytest.raises(ValueError):
+        K.ssm_prefill(x, dt, a, b[:, :0], c[:, :0])
+    with pytest.raises(ValueError):
+        K.ssm_step(x, dt, a, b[:, :0], c[:, :0])
+    q, k, v, table, n = cache_case([5], 4, 2, 64, 16)
+    with pytest.raises(K.KdaError, match="UNSUPPORTED_DIM"):
+        K.paged_decode(q[..., :0].contiguous(), k[..., :0].contiguous(), v[..., :0].contiguous(), table, n)
+
+
 # ------------------------------------------------- streams, graphs, threads
 
 def test_side_stream_and_graph():
