@@ -31,7 +31,6 @@ struct StreamWorkspace {
 
 struct DeviceState {
     bool ready = false;
-    int sm_count = 0;
     int *err = nullptr;  // sticky error word (device memory, 256 B)
     std::map<cudaStream_t, StreamWorkspace> ws;
 };
@@ -220,8 +219,6 @@ kda_status init_device(int dev, DeviceState &st) {
     if (kda::configure_conv() != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::configure_ssm() != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::configure_paged() != cudaSuccess) return KDA_ERR_CUDA;
-    if (cudaDeviceGetAttribute(&st.sm_count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return KDA_ERR_CUDA;
     st.ready = true;
     return KDA_OK;
 }
@@ -289,7 +286,6 @@ int kda::begin_call(const void *const *ptrs, int n, void *stream_, int64_t ws_by
         if (rc != KDA_OK) return rc;
     }
     ctx->err = st.err;
-    ctx->sm_count = st.sm_count;
     if (ws_bytes > 0 || sync_bytes > 0) {
         StreamWorkspace &ws = st.ws[stream];
         if (ws_bytes > 0) {

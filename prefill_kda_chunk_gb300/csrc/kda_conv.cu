@@ -269,7 +269,7 @@ __device__ __forceinline__ void step_window(const Filter<W, VEC> &f, float (&win
 // tokens worked on twice are as many, so that it takes longer runs (T = D = 8192:
 // runs of 64, 96 and 128 rows at most took 110, 103 and 99 us, the forward's 53, 53 and
 // 55, before the arithmetic went two by two).
-constexpr int kRun = 64, kBackRun = 128, kMinRun = 4, kSlots = 2 * 152;
+constexpr int kRun = 64, kBackRun = 128, kMinRun = 4, kSlots = 2 * kPlannedSms;
 int64_t run_for(int64_t tokens, int64_t cols, int64_t most) {
     int64_t run = most;
     for (int64_t waves = 1;; ++waves) {

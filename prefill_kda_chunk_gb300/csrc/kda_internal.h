@@ -214,6 +214,10 @@ cudaError_t launch_c64_fused(const C64Args &a, int grid, cudaStream_t stream);
 // kda_status the entry point returns (not device memory / wrong device).
 int pointer_device_status(const void *p, int dev);
 
+// SMs of a GB300, for which the operators below plan their grids and scratch. Where fewer
+// are to be had (a partition), results are the same and only the balance is off.
+constexpr int kPlannedSms = 152;
+
 // What an entry point works with once its arguments are checked: the device's
 // error word, the stream's workspace (ws_bytes of it; call_flags is the
 // per-call flag word in front) and its zeroed arrival counters. The lock is
@@ -224,7 +228,6 @@ struct CallContext {
     int *call_flags = nullptr;
     uint8_t *ws = nullptr;
     int *sync = nullptr;
-    int sm_count = 0;
 };
 // The device checks of an entry point (first use, stream, pointers; NULLs are
 // skipped) and its workspace. Returns a kda_status.

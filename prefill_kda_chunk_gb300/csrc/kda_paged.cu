@@ -49,8 +49,7 @@ constexpr int kTile = kPagedWarps * kStrip;     // tokens per tile of the split
 constexpr int kItemCost = 4;
 constexpr int kStages = 3;                      // strips in flight per warp
 constexpr int kPagedCtasPerSm = 2;
-constexpr int kPagedSms = 152;
-constexpr int kMaxCtas = kPagedSms * kPagedCtasPerSm;
+constexpr int kMaxCtas = kPlannedSms * kPagedCtasPerSm;
 
 // Heads of one work item: 8 NT query heads of one key-value head. Two sets of 8 share
 // one reading of the keys and values; larger groups read them again, out of L2, as

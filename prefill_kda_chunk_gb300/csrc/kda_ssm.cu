@@ -142,7 +142,6 @@ __global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p) {
 
 constexpr int kL = 128;              // tokens per chunk
 constexpr int kPS = 64;              // channels of P per unit
-constexpr int kSsmSms = 152;
 // Warps: 0..7 form M and the outputs, 8..15 keep the state, then one for the
 // MMAs of the state and C S, one each for C B^T and M X (in one warp, whichever came
 // first held up the other) and one for the copies.
@@ -1240,7 +1239,7 @@ cudaError_t configure_ssm() {
 }
 
 int64_t ssm_workspace(const SsmParams &p) {
-    return offsets_bytes(p) + 1024 + 2 * kSsmSms * kSlotBytes + most_chunks(p) * p.heads * kDecaysBytes;
+    return offsets_bytes(p) + 1024 + 2 * kPlannedSms * kSlotBytes + most_chunks(p) * p.heads * kDecaysBytes;
 }
 
 cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t stream) {
@@ -1264,8 +1263,8 @@ cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t 
     pl.cps = static_cast<int>((p.seq_len + kL - 1) / kL);
     pl.decay = reinterpret_cast<float *>(ws + offsets_bytes(p));
     pl.slots = reinterpret_cast<float *>(ws + offsets_bytes(p) + 1024);
-    pl.saved = pl.slots + kSsmSms * kSlotBytes / 4;
-    pl.decays = reinterpret_cast<Decays *>(ws + offsets_bytes(p) + 1024 + 2 * kSsmSms * kSlotBytes);
+    pl.saved = pl.slots + kPlannedSms * kSlotBytes / 4;
+    pl.decays = reinterpret_cast<Decays *>(ws + offsets_bytes(p) + 1024 + 2 * kPlannedSms * kSlotBytes);
     pl.in_place = p.s_final != nullptr && p.s_final == p.s0;
     if (p.cu != nullptr) {
         int32_t *off = reinterpret_cast<int32_t *>(ws);
@@ -1281,10 +1280,10 @@ cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t 
     // 22 us whole and 25 cut, 20 x 1024 tokens 205 and 211; 8 heads: 1024 tokens 31 and 23).
     const int64_t nc = most_chunks(p);
     const bool whole = p.cu != nullptr ? p.tokens <= 4 * kL
-                                       : pl.cps <= 4 || pl.units * p.n_seqs >= 8 * kSsmSms;
+                                       : pl.cps <= 4 || pl.units * p.n_seqs >= 8 * kPlannedSms;
     pl.gran = !whole ? 1 : p.cu != nullptr ? 0 : pl.cps;
     const int64_t runs = pl.units * nc / (pl.gran > 0 ? pl.gran : nc);
-    const unsigned grid = static_cast<unsigned>(runs < kSsmSms ? runs : kSsmSms);
+    const unsigned grid = static_cast<unsigned>(runs < kPlannedSms ? runs : kPlannedSms);
     // a launch that may begin before the one in front of it is over
     cudaLaunchAttribute overlap;
     overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1297,7 +1296,7 @@ cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t 
     next.attrs = &overlap;
     next.numAttrs = 1;
     const int64_t blocks = (nc * p.heads + 7) / 8;
-    ssm_decays_kernel<<<static_cast<unsigned>(blocks < 8 * kSsmSms ? blocks : 8 * kSsmSms), 256, 0, stream>>>(p, pl);
+    ssm_decays_kernel<<<static_cast<unsigned>(blocks < 8 * kPlannedSms ? blocks : 8 * kPlannedSms), 256, 0, stream>>>(p, pl);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return with_n(p, [&](auto n) {
