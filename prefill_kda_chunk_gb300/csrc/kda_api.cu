@@ -31,6 +31,7 @@ struct StreamWorkspace {
 
 struct DeviceState {
     bool ready = false;
+    bool configured[3] = {};   // the operators around KDA, by kda::Operator
     int *err = nullptr;  // sticky error word (device memory, 256 B)
     std::map<cudaStream_t, StreamWorkspace> ws;
 };
@@ -216,9 +217,6 @@ kda_status init_device(int dev, DeviceState &st) {
     if (kda::configure_recurrent() != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::configure_c64() != cudaSuccess) return KDA_ERR_CUDA;
     if (kda::configure_backward_chunk() != cudaSuccess) return KDA_ERR_CUDA;
-    if (kda::configure_conv() != cudaSuccess) return KDA_ERR_CUDA;
-    if (kda::configure_ssm() != cudaSuccess) return KDA_ERR_CUDA;
-    if (kda::configure_paged() != cudaSuccess) return KDA_ERR_CUDA;
     st.ready = true;
     return KDA_OK;
 }
@@ -261,7 +259,7 @@ static kda_status grow(void **ptr, size_t *bytes, int64_t need, int64_t zero, bo
     return KDA_OK;
 }
 
-int kda::begin_call(const void *const *ptrs, int n, void *stream_, int64_t ws_bytes,
+int kda::begin_call(Operator op, const void *const *ptrs, int n, void *stream_, int64_t ws_bytes,
                     int64_t sync_bytes, CallContext *ctx) {
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     int dev = -1;
@@ -284,6 +282,14 @@ int kda::begin_call(const void *const *ptrs, int n, void *stream_, int64_t ws_by
     for (int i = 0; i < n && !capturing; ++i) {   // pointer queries are not stream work
         const kda_status rc = check_pointer_device(ptrs[i], dev);
         if (rc != KDA_OK) return rc;
+    }
+    // On the operator's own first call: setting a kernel's attributes loads it, which took
+    // 2 ms of every program's first KDA call when all of them were set there. (No stream
+    // work: also while capturing.)
+    if (!st.configured[op]) {
+        if ((op == kConv ? configure_conv() : op == kSsm ? configure_ssm() : configure_paged()) != cudaSuccess)
+            return KDA_ERR_CUDA;
+        st.configured[op] = true;
     }
     ctx->err = st.err;
     if (ws_bytes > 0 || sync_bytes > 0) {

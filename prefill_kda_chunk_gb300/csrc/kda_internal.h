@@ -229,9 +229,10 @@ struct CallContext {
     uint8_t *ws = nullptr;
     int *sync = nullptr;
 };
+enum Operator { kConv, kSsm, kPaged };
 // The device checks of an entry point (first use, stream, pointers; NULLs are
 // skipped) and its workspace. Returns a kda_status.
-int begin_call(const void *const *ptrs, int n, void *stream, int64_t ws_bytes, int64_t sync_bytes,
+int begin_call(Operator op, const void *const *ptrs, int n, void *stream, int64_t ws_bytes, int64_t sync_bytes,
                CallContext *ctx);
 
 // Short causal convolution (kda_conv.cu). Rows of x, out, d_out and dx are

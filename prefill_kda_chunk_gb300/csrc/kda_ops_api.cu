@@ -99,7 +99,7 @@ kda_status kda_short_conv(const void *x, const float *weight, const float *bias,
 
     const void *ptrs[] = {x, weight, bias, initial_state, cu_seqlens, out, final_state};
     kda::CallContext ctx;
-    rc = static_cast<kda_status>(kda::begin_call(ptrs, 7, stream, 0, 0, &ctx));
+    rc = static_cast<kda_status>(kda::begin_call(kda::kConv, ptrs, 7, stream, 0, 0, &ctx));
     if (rc != KDA_OK) return rc;
     kda::ConvParams p{};
     p.x = x; p.weight = weight; p.bias = bias; p.hist_in = initial_state; p.cu = cu_seqlens;
@@ -134,7 +134,7 @@ kda_status kda_short_conv_step(const void *x, const float *weight, const float *
 
     const void *ptrs[] = {x, weight, bias, state_in, out, state_out};
     kda::CallContext ctx;
-    const kda_status rc = static_cast<kda_status>(kda::begin_call(ptrs, 6, stream, 0, 0, &ctx));
+    const kda_status rc = static_cast<kda_status>(kda::begin_call(kda::kConv, ptrs, 6, stream, 0, 0, &ctx));
     if (rc != KDA_OK) return rc;
     kda::ConvParams p{};
     p.x = x; p.weight = weight; p.bias = bias; p.hist_in = state_in;
@@ -193,7 +193,7 @@ kda_status kda_short_conv_backward(const void *x, const float *weight, const flo
     p.dweight = dweight; p.dbias = dbias;
     const kda::ConvBackwardPlan plan = kda::plan_conv_backward(p);
     kda::CallContext ctx;
-    rc = static_cast<kda_status>(kda::begin_call(ptrs, 11, stream, plan.scratch_bytes, 0, &ctx));
+    rc = static_cast<kda_status>(kda::begin_call(kda::kConv, ptrs, 11, stream, plan.scratch_bytes, 0, &ctx));
     if (rc != KDA_OK) return rc;
     p.partial = reinterpret_cast<float *>(ctx.ws);
     p.err = ctx.err;
@@ -285,7 +285,7 @@ kda_status kda_ssm_prefill(const void *x, const float *dt, const float *a, const
                                   out, final_state);
     const void *ptrs[] = {x, dt, a, b, c, d, dt_bias, initial_state, cu_seqlens, out, final_state};
     kda::CallContext ctx;
-    rc = static_cast<kda_status>(kda::begin_call(ptrs, 11, stream, kda::ssm_workspace(p), 0, &ctx));
+    rc = static_cast<kda_status>(kda::begin_call(kda::kSsm, ptrs, 11, stream, kda::ssm_workspace(p), 0, &ctx));
     if (rc != KDA_OK) return rc;
     p.err = ctx.err;
     return kda::launch_ssm(p, ctx, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK
@@ -308,7 +308,7 @@ kda_status kda_ssm_step(const void *x, const float *dt, const float *a, const vo
                                   state_out);
     const void *ptrs[] = {x, dt, a, b, c, d, dt_bias, state_in, out, state_out};
     kda::CallContext ctx;
-    rc = static_cast<kda_status>(kda::begin_call(ptrs, 10, stream, 0, 0, &ctx));
+    rc = static_cast<kda_status>(kda::begin_call(kda::kSsm, ptrs, 10, stream, 0, 0, &ctx));
     if (rc != KDA_OK) return rc;
     p.err = ctx.err;
     return kda::launch_ssm_step(p, static_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -355,7 +355,7 @@ kda_status kda_paged_decode(const void *q, const void *k_cache, const void *v_ca
     const void *ptrs[] = {q, k_cache, v_cache, page_table, seq_lens, out, lse};
     kda::CallContext ctx;
     const kda_status rc = static_cast<kda_status>(
-        kda::begin_call(ptrs, 7, stream, kda::paged_workspace(p), kda::paged_sync(p), &ctx));
+        kda::begin_call(kda::kPaged, ptrs, 7, stream, kda::paged_workspace(p), kda::paged_sync(p), &ctx));
     if (rc != KDA_OK) return rc;
     p.err = ctx.err;
     return kda::launch_paged(p, ctx, static_cast<cudaStream_t>(stream)) == cudaSuccess

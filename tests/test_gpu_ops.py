@@ -695,3 +695,39 @@ def test_side_stream_and_graph():
     torch.cuda.synchronize()
     for r, t in zip(ref, held):
         assert torch.equal(r, t)
+
+
+def test_first_use_inside_a_capture():
+    """An operator that needs no workspace may be captured as its first call of all: its
+    kernels are set up on first use, which no KDA call does for it."""
+    code = """
+import torch
+import prefill_kda_chunk_gb300 as K
+g = torch.Generator(device="cuda").manual_seed(0)
+def r(*s, dtype=torch.bfloat16):
+    return torch.randn(*s, generator=g, device="cuda").to(dtype)
+q, k, v = r(64, 2, 128), r(64, 2, 128), r(64, 2, 128)
+K.chunk_prefill(q, k, v, -r(64, 2, 128, dtype=torch.float32).abs(), r(64, 2, dtype=torch.float32).sigmoid())
+x, w, h = r(40, 256), r(256, 4, dtype=torch.float32), r(40, 3, 256)
+a, dt = -r(4, dtype=torch.float32).abs(), r(40, 4, dtype=torch.float32)
+b, c, s = r(40, 1, 128), r(40, 1, 128), r(40, 4, 128, 64, dtype=torch.float32)
+def go():
+    y, f = K.short_conv(x, w)
+    z, e = K.short_conv_step(x, w, h)
+    o, t = K.ssm_step(z.view(40, 4, 64), dt, a, b, c, s, dt_softplus=True)
+    return [y, f, z, e, o, t]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    held = go()
+graph.replay()
+torch.cuda.synchronize()
+K.check_device_error()
+assert all(torch.equal(p, q) for p, q in zip(held, go()))
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
