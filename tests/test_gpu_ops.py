@@ -731,3 +731,49 @@ assert all(torch.equal(p, q) for p, q in zip(held, go()))
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert p.returncode == 0, p.stderr[-2000:]
+
+
+def test_two_threads_on_streams_of_their_own():
+    """Calls from two threads, each on its own stream, at work at the same time: every
+    call gives the bits that it gives alone."""
+    import threading
+
+    x, dt, a, b, c, d, bias, s0 = ssm_case([2500, 60], 4, 64, 2, 128, True)
+    cu = cu_of([2500, 60]).cuda()
+    w = make(1)(256, 4, dtype=F32)
+    q, k, v, table, n = cache_case([30000, 7, 900], 8, 2, 128, 16)
+    flat = [x.reshape(2560, 256).contiguous(), x.reshape(2560, 256) * 0.5]
+    dy = torch.randn(2560, 256, device="cuda")
+
+    def go(i):
+        y, h = K.short_conv(flat[i], w, cu_seqlens=cu)
+        s, f = K.ssm_prefill(y.view(2560, 4, 64), dt, a, b, c, d, bias, initial_state=s0,
+                             cu_seqlens=cu, dt_softplus=True)
+        o, l = K.paged_decode(q[i:i + 2].contiguous(), k, v, table[i:i + 2].contiguous(),
+                              n[i:i + 2].contiguous())
+        g = K.short_conv_backward(flat[i], w, dy, cu_seqlens=cu, d_initial_state=False)
+        return [y, h, s, f, o, l, g[0], g[1]]
+
+    ref = [go(i) for i in (0, 1)]
+    K.check_device_error()
+    failed, start = [], threading.Barrier(2)
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()) as _:
+                start.wait()
+                for _ in range(20):
+                    got = go(i)
+                torch.cuda.current_stream().synchronize()
+                if not all(torch.equal(r, t) for r, t in zip(ref[i], got)):
+                    failed.append(i)
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    K.check_device_error()
+    assert not failed
