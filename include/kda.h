@@ -514,6 +514,16 @@ KDA_API kda_status kda_set_backward_impl(int impl);
 KDA_API kda_status kda_test_stall_recurrent(int chunk, int64_t wait_ns);
 
 /*
+ * Test hook for kda_ssm_prefill (process-wide, host only): in later calls every
+ * thread block copies the tiles of its first `chunk` chunks only, so that the waits
+ * for the next one run out (after about a second each). The call then records
+ * KDA_ERR_DEVICE_TIMEOUT and leaves, outputs and states unspecified; copies and
+ * products under way are waited for. chunk = -1 turns the hook off (the default);
+ * chunk < -1: KDA_ERR_BAD_SHAPE.
+ */
+KDA_API kda_status kda_test_stall_scan(int chunk);
+
+/*
  * Test hook: how kda_short_conv_backward would launch its kernel for arguments
  * of these sizes, strides and alignments (nothing is read from the pointers and no
  * GPU is needed). plan receives the bytes of scratch that the call asks for, the

@@ -36,6 +36,7 @@ from ._binding import (  # noqa: F401
     kda_ssm_step,
     kda_test_conv_backward_plan,
     kda_test_stall_recurrent,
+    kda_test_stall_scan,
     kda_stage_timing_begin,
     kda_stage_timing_end,
     kda_status_string,

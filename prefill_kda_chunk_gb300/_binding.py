@@ -106,6 +106,8 @@ def lib() -> ctypes.CDLL:
             L.kda_set_backward_impl.argtypes = [ctypes.c_int]
             L.kda_test_stall_recurrent.restype = ctypes.c_int
             L.kda_test_stall_recurrent.argtypes = [ctypes.c_int, i64]
+            L.kda_test_stall_scan.restype = ctypes.c_int
+            L.kda_test_stall_scan.argtypes = [ctypes.c_int]
             L.kda_build_info.restype = ctypes.c_char_p
             L.kda_build_info.argtypes = []
             _lib = L
@@ -252,6 +254,12 @@ def kda_test_stall_recurrent(chunk: int, wait_ns: int = 0) -> int:
     """Test hook: the recurrent kernel's record producer stops before `chunk`
     and its waits give up after `wait_ns` (-1: off)."""
     return lib().kda_test_stall_recurrent(int(chunk), int(wait_ns))
+
+
+def kda_test_stall_scan(chunk: int) -> int:
+    """Test hook: the state space scan's blocks copy the tiles of their first `chunk`
+    chunks only, and their waits run out (-1: off)."""
+    return lib().kda_test_stall_scan(int(chunk))
 
 
 def kda_test_conv_backward_plan(x, d_out, dx, tokens, D, W, x_stride, dout_stride, dx_stride,

@@ -281,6 +281,7 @@ struct SsmParams {
     void *out;                 // bf16 [tokens, H, P]
     float *s_final;            // [n_seqs, H, n, P] or nullptr
     int *err;
+    int stall;                 // test hook: chunks of every run whose tiles are copied
 };
 cudaError_t configure_ssm();
 int64_t ssm_workspace(const SsmParams &p);

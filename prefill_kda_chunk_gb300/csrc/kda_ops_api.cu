@@ -5,6 +5,9 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <climits>
+
 #include "kda.h"
 #include "kda_device.cuh"
 #include "kda_internal.h"
@@ -12,6 +15,8 @@
 namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
+
+std::atomic<int> g_stall_scan{INT_MAX};   // kda_test_stall_scan
 
 // A block of rows: `row` bytes each, `step` bytes apart.
 struct Rows {
@@ -264,6 +269,7 @@ static kda::SsmParams ssm_params(const void *x, const float *dt, const float *a,
     p.n = static_cast<int32_t>(n);
     p.softplus = (flags & KDA_SSM_DT_SOFTPLUS) != 0;
     p.out = out; p.s_final = s_out;
+    p.stall = g_stall_scan.load();
     return p;
 }
 
@@ -290,6 +296,12 @@ kda_status kda_ssm_prefill(const void *x, const float *dt, const float *a, const
     p.err = ctx.err;
     return kda::launch_ssm(p, ctx, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KDA_OK
                                                                                      : KDA_ERR_CUDA;
+}
+
+kda_status kda_test_stall_scan(int chunk) {
+    if (chunk < -1) return KDA_ERR_BAD_SHAPE;
+    g_stall_scan.store(chunk < 0 ? INT_MAX : chunk);
+    return KDA_OK;
 }
 
 kda_status kda_ssm_step(const void *x, const float *dt, const float *a, const void *b,

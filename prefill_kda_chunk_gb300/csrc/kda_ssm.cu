@@ -390,6 +390,7 @@ struct SsmPlan {
     float *saved;              // the same: initial states that a cut run starts from (in place)
     float *decay;              // [G]
     bool in_place;
+    int stall;                 // test hook: chunks of a run whose tiles are copied
 };
 
 // The list of (unit, chunk) and the run of it that a CTA takes.
@@ -822,9 +823,10 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 }
                 return true;
             };
+            const int copied = min(count, pl.stall);
             int i = 0, sent_c = 0, described = describe(0) ? 1 : 0;
 #pragma unroll 1
-            for (; i < count; ++i) {
+            for (; i < copied; ++i) {
                 // what chunks i - 2 (b, x) and i - 1 (c) have left
                 const Scalars &v = scal[i & (kRing - 1)];
                 const int row = static_cast<int>(v.row), col = v.gcol, xcol = v.xcol, s = i & 1;
@@ -856,9 +858,9 @@ ssm_chunk_kernel(const __grid_constant__ SsmMaps maps, SsmParams p, SsmPlan pl) 
                 wait_phase(bar(kFullX + (j & 1)), (j >> 1) & 1);
             }
             if (!kStates && sent_c > 0) wait_phase(bar(kFullC), (sent_c - 1) & 1);
-            for (int j = described > 2 ? described - 2 : 0; j < described; ++j)
+            for (int j = described > kRing ? described - kRing : 0; j < described; ++j)
                 wait_phase(bar(kScal + (j & (kRing - 1))), (j / kRing) & 1);
-            if (i < count) {   // (of the chunk it gave up at)
+            if (i < count) {   // (of the chunk it gave up at, where it got so far)
                 s_abort = 1;
                 wait_phase(bar(kFullB + (i & 1)), (i >> 1) & 1);
                 wait_phase(bar(kFullX + (i & 1)), (i >> 1) & 1);
@@ -1266,6 +1268,7 @@ cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t 
     pl.saved = pl.slots + kPlannedSms * kSlotBytes / 4;
     pl.decays = reinterpret_cast<Decays *>(ws + offsets_bytes(p) + 1024 + 2 * kPlannedSms * kSlotBytes);
     pl.in_place = p.s_final != nullptr && p.s_final == p.s0;
+    pl.stall = p.stall;
     if (p.cu != nullptr) {
         int32_t *off = reinterpret_cast<int32_t *>(ws);
         const cudaError_t e = launch_varlen_prologue(p.cu, p.n_seqs, p.tokens, off, ctx.call_flags, p.err,

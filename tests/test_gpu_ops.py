@@ -525,6 +525,30 @@ def test_ssm_non_finite_x_stays_in_its_channel_and_behind_its_token(lens, H, P, 
     assert torch.equal(o2.cpu()[want], o.cpu()[want]) and torch.equal(f2.cpu()[state], f.cpu()[state])
 
 
+@pytest.mark.parametrize("lens,chunk", [([300], 0), ([5000, 40], 2), ([5000, 40], 3)])
+def test_ssm_wait_runs_out_then_clean_call(lens, chunk):
+    """Tiles that never come (a test hook): the waits run out, the call says so and ends
+    by itself, and the next one is right. Whole sequences, and ones that are cut (then
+    the launch for the states gives up as well)."""
+    x, dt, a, b, c, d, bias, s0 = ssm_case(lens, 20, 64, 1, 128, True)
+    cu = cu_of(lens).cuda()
+    kw = dict(initial_state=s0, cu_seqlens=cu, dt_softplus=True)
+    ref = K.ssm_prefill(x, dt, a, b, c, d, bias, **kw)
+    K.check_device_error()
+    assert K.kda_test_stall_scan(-2) != 0
+    assert K.kda_test_stall_scan(chunk) == 0
+    try:
+        K.ssm_prefill(x, dt, a, b, c, d, bias, **kw)
+        with pytest.raises(K.KdaError, match="TIMEOUT"):
+            K.check_device_error()
+    finally:
+        assert K.kda_test_stall_scan(-1) == 0
+    K.check_device_error()
+    got = K.ssm_prefill(x, dt, a, b, c, d, bias, **kw)
+    K.check_device_error()
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
 # --------------------------------------------------------- paged attention
 
 def cache_case(lens, Hq, Hkv, D, page, seed=0, poison=True, spare=3, one=True):
