@@ -278,7 +278,8 @@ KDA_API kda_status kda_chunk_prefill_backward(const void *q, const void *k, cons
  *   out          device, bf16 [B*T, D], rows out_stride elements apart
  *   final_state  device, bf16 [N, W-1, D] or NULL: the last W-1 rows of
  *                (history, sequence); not initial_state itself
- *   D >= 1; x_stride, out_stride >= D; B*T*max(strides) < 2^40.
+ *   1 <= D <= 2^24; x_stride, out_stride >= D; B*T < 2^31 and
+ *   B*T*max(strides) < 2^40.
  *
  * Any D, strides and alignment to the element are taken; rows that start on
  * 16-byte boundaries (8-byte ones next) with D a multiple of 8 (4) run
@@ -358,16 +359,23 @@ KDA_API kda_status kda_short_conv_backward(const void *x, const float *weight, c
  *   out          device, bf16 [B*T, H, P] (contiguous)
  *   final_state  device, fp32 [N, H, n, P] or NULL (not written); may equal
  *                initial_state
- *   P = 64 or 128, n = 64 or 128 (others: KDA_ERR_UNSUPPORTED_DIM).
+ *   P = 64 or 128, n = 64 or 128 (others: KDA_ERR_UNSUPPORTED_DIM); H <= 65535,
+ *   N*H < 2^30, B*T < 2^31.
  *
+ * A log decay below -1024 log 2 counts as that (its exponential is 0 either way).
  * An infinity or NaN in x makes that channel of out NaN from its token to the
  * sequence's end, and that column of the state not finite; earlier tokens and
  * other channels are not touched.
  *
  * Alignment: x, b, c, out and the states 16 bytes, and x_stride, b_stride,
  * c_stride multiples of 8 elements; fp32 vectors and cu_seqlens 4 bytes.
- * States, decays and sums are held in fp32; the outputs and states of a call are the
- * same bits every time. Workspace (the stream's): 2,608 B of decays for every
+ * States, decays and sums are held in fp32. The tensor core's operands are bf16: x, b
+ * and c as they are, the state in S^T c and the decayed c . b in front of x as two
+ * bf16 terms (16 bits of mantissa, below out's own rounding), and what enters the
+ * state as three (24 bits). The outputs and states of a call are the
+ * same bits every time. A packed batch of at most 512 tokens is not cut over the
+ * SMs, so many short sequences in it take their turns, a chunk each (24 sequences
+ * of 20 tokens: 115 us; of 22 tokens, which are cut: 25). Workspace (the stream's): 2,608 B of decays for every
  * 128 tokens of a sequence and head, 10 MB for the states where a sequence is
  * cut, and the chunk offsets of a packed batch.
  */
@@ -417,7 +425,8 @@ KDA_API kda_status kda_ssm_step(const void *x, const float *dt, const float *a, 
  *   out          device, bf16 [B, Hq, D]
  *   lse          device, fp32 [B, Hq] or NULL (natural logarithm)
  *   D = 64 or 128 (others: KDA_ERR_UNSUPPORTED_DIM); Hq a multiple of Hkv;
- *   page_size >= 1; B <= 65536; max_pages * page_size < 2^31.
+ *   page_size >= 1; B <= 65536; Hq <= 65535; pages < 2^31;
+ *   max_pages * page_size < 2^31.
  *
  * A length that is negative or beyond max_pages * page_size, or a page index
  * outside [0, pages), is reported by kda_last_device_error() as
@@ -426,8 +435,10 @@ KDA_API kda_status kda_ssm_step(const void *x, const float *dt, const float *a, 
  * meaningless and those of the others are right.
  *
  * Alignment: q, k_cache, v_cache, out 16 bytes, page strides multiples of 8
- * elements; int32 and fp32 arrays 4 bytes. Scores, softmax and sums in fp32;
- * the sum over the cache is split over the SMs and joined in a fixed order (the
+ * elements; int32 and fp32 arrays 4 bytes. Scores, softmax and sums in fp32; the
+ * weights enter their product with v as two bf16 terms (16 bits of mantissa, below
+ * out's own rounding; an infinity in v can therefore give NaN where the formula
+ * gives an infinity). The sum over the cache is split over the SMs and joined in a fixed order (the
  * same call gives the same bits). Workspace: partial sums of the split.
  */
 KDA_API kda_status kda_paged_decode(const void *q, const void *k_cache, const void *v_cache,

@@ -12,8 +12,8 @@
 // ring in shared memory, 12 of each warp on their way at a time. Sequence ends only
 // move the window, so a packed batch runs like one long sequence. All sums are fp32.
 //
-// Measured at T = D = 8192, W = 4: forward 51 us (5.2 TB/s, 77 % of copy bandwidth),
-// gradient with fp32 d_out 97 us (5.5 TB/s, 81 %); one token for each of 256 sequences,
+// Measured at T = D = 8192, W = 4: forward 52 us (5.2 TB/s, 76 % of copy bandwidth),
+// gradient with fp32 d_out 98 us (5.5 TB/s, 80 %); one token for each of 256 sequences,
 // D = 24576: 19 us (5.4 TB/s, 79 %).
 
 #include "kda_device.cuh"
@@ -94,7 +94,8 @@ __device__ __forceinline__ void store_f32(float *dst, const float (&f)[VEC]) {
 }
 
 // The arithmetic on a thread's channels goes two by two, in packed instructions: with
-// single ones the forward issued in 74 % of all slots (53 us, this way 51).
+// single ones the forward issued in 74 % of all slots, this way in 63 % (53 us against 51,
+// before the branch for z below kFar).
 template <int VEC>
 __device__ __forceinline__ void times(float (&a)[VEC], const float (&x)[VEC]) {
     if constexpr (VEC == 1) {

@@ -38,8 +38,8 @@
 // tensor core 2700 clocks, most of it reading operands from shared memory at 128
 // bytes a clock, and the warps 3000 issue slots of each quarter of the SM, most of
 // them for M and for the terms of W X; with the waits between the roles it takes 5600.
-// Measured at those sizes: decays 4 us, states 34, chunks 80, together 118 (1.5 TB/s,
-// 21 % of copy bandwidth); 131072 tokens, 32 heads of 128: 1540 us.
+// Measured at those sizes: decays 4 us, states 34, chunks 81, together 119.5 (1.4 TB/s,
+// 21 % of copy bandwidth); 131072 tokens, 32 heads of 128: 1550 us.
 
 #include <cuda.h>
 
@@ -100,8 +100,8 @@ __device__ __forceinline__ float log_decay(float a2, float delta) {
 // ------------------------------------------------------------- one token
 
 // One block per (sequence, head): thread (q, j) keeps S[j * kN / kParts ..][q]. Bound by
-// reading and writing the state (256 sequences, 64 heads of 64, n 128: 160 us, 6.75
-// TB/s, 99 % of copy bandwidth).
+// reading and writing the state (256 sequences, 64 heads of 64, n 128: 156 us, 6.9
+// TB/s, copy bandwidth).
 template <int kN, int kP>
 __global__ void __launch_bounds__(256) ssm_step_kernel(SsmParams p) {
     constexpr int kParts = 256 / kP, kRows = kN / kParts;
@@ -1281,6 +1281,10 @@ cudaError_t launch_ssm(const SsmParams &p, const CallContext &ctx, cudaStream_t 
     // launch for the states at the cuts is saved, when they are short, or when
     // there are so many that the SMs are even without cuts (64 heads of 64: 512 tokens
     // 22 us whole and 25 cut, 20 x 1024 tokens 205 and 211; 8 heads: 1024 tokens 31 and 23).
+    // These are fixed lengths. Of a packed batch the rule looks at the tokens only, which is
+    // right for a few sequences and far off for many short ones: each is a chunk, and one
+    // block per unit walks them all (8 heads: 4 x 128 tokens 29 us, 24 x 20 whole 115 and
+    // 24 x 22 cut 25, 256 x 2 whole 1147 and 257 x 2 cut 85).
     const int64_t nc = most_chunks(p);
     const bool whole = p.cu != nullptr ? p.tokens <= 4 * kL
                                        : pl.cps <= 4 || pl.units * p.n_seqs >= 8 * kPlannedSms;
