@@ -28,6 +28,10 @@
  *     kda_last_device_error() blocks the host.
  *   - Errors found from the arguments alone are returned before anything
  *     is enqueued and leave every output untouched.
+ *   - Workspaces belong to the (device, stream) of the call. A graph keeps the
+ *     ones that its calls were captured with, also when a later call on that
+ *     stream needs larger ones; graphs captured on one stream share them, so
+ *     that they are replayed one after another, not side by side.
  */
 #ifndef KDA_GB300_H
 #define KDA_GB300_H
@@ -63,7 +67,8 @@ typedef enum {
     KDA_ERR_SCRATCH_LIMIT = -14,    /* kda_chunk_prefill_noalloc: the call needs more scratch
                                        than its fixed 64 MiB array holds */
     KDA_ERR_BAD_FLAGS = -15,        /* a flag bit the entry point does not know */
-    KDA_ERR_BAD_PAGE_TABLE = -16    /* (device) a sequence length or page index out of range */
+    KDA_ERR_BAD_PAGE_TABLE = -16,   /* (device) a sequence length or page index out of range */
+    KDA_ERR_OUT_OF_PAGES = -17      /* (device) kda_page_plan: too few free pages */
 } kda_status;
 
 /*
@@ -447,6 +452,173 @@ KDA_API kda_status kda_paged_decode(const void *q, const void *k_cache, const vo
                                     int64_t page_size, int64_t max_pages, int64_t k_page_stride,
                                     int64_t v_page_stride, float scale, void *out, float *lse,
                                     void *stream);
+
+/*
+ * kda_page_plan -- page tables, positions and slots of a batch's next tokens, from
+ * request lengths, on the GPU (what kda_paged_decode and the entry points below
+ * read). Slot i of the batch holds seq_lens[i] tokens in the pages
+ * page_table[i, 0 .. ceil(seq_lens[i] / page_size) - 1], and new_lens[i] tokens join
+ * it; free_pages[0 .. free_count) is a stack of the pages that nobody holds.
+ *
+ *   1. Every slot with release[i] != 0 gives its pages back: they are pushed on the
+ *      stack in the order of i, then of the page's place; the slot is then empty.
+ *   2. Pages that the new tokens need are taken from the top of the stack, in the
+ *      order of i, then of the page's place, and entered into the table.
+ *   3. cu_seqlens[i] = new_lens[0] + .. + new_lens[i - 1]. Row r of slot i, in
+ *      [cu_seqlens[i], cu_seqlens[i + 1]), is at position p = (tokens held) + r -
+ *      cu_seqlens[i], in slot page_table[i, p / page_size] * page_size + p % page_size
+ *      of the cache. Rows behind the last new token get position 0 and slot -1.
+ *
+ *   page_table   device, int32 [B, max_pages]
+ *   seq_lens, new_lens device, int32 [B]
+ *   release      device, uint8 [B] or NULL (none)
+ *   free_pages   device, int32 [pool]; free_count device, int32 [1]
+ *   page_table_out, seq_lens_out (tokens held after the call), free_pages_out,
+ *   free_count_out: like their inputs; each may be its input itself (updated in
+ *                place: only what changes is written), but may not overlap it otherwise
+ *   cu_seqlens   device, int32 [B + 1]; positions device, int32 [T]; slots device,
+ *                int64 [T]: T rows, at least as many as there are new tokens
+ *   0 <= B <= 65536; page_size >= 1; max_pages * page_size < 2^31; T, pool < 2^31.
+ *
+ * Entries of the table and of the stack are moved, not looked at. A length that is
+ * negative or past max_pages * page_size, more new tokens than T, or a free_count
+ * outside [0, pool] (after the pages given back) is reported by kda_last_device_error()
+ * as KDA_ERR_BAD_PAGE_TABLE, too few free pages as KDA_ERR_OUT_OF_PAGES; nothing is
+ * planned then: tables, lengths and stack stay as they are, cu_seqlens is 0
+ * throughout, and every row has position 0 and slot -1. Workspace: 24 B per slot.
+ */
+KDA_API kda_status kda_page_plan(const int32_t *page_table, const int32_t *seq_lens,
+                                 const int32_t *new_lens, const uint8_t *release,
+                                 const int32_t *free_pages, const int32_t *free_count, int64_t B,
+                                 int64_t max_pages, int64_t pool, int64_t page_size, int64_t T,
+                                 int32_t *page_table_out, int32_t *seq_lens_out,
+                                 int32_t *free_pages_out, int32_t *free_count_out,
+                                 int32_t *cu_seqlens, int32_t *positions, int64_t *slots,
+                                 void *stream);
+
+/*
+ * kda_qk_norm_rope -- root-mean-square norm of every query and key head and the
+ * rotation by its position, in one pass. For a head x of D channels
+ *
+ *     u = x / sqrt(mean(x^2) + eps) * weight
+ *     (y_a, y_b) = (u_a cos t - u_b sin t, u_b cos t + u_a sin t),  t = position * inv_freq[i]
+ *
+ * over the pairs (a, b) = (i, i + R / 2), or (2 i, 2 i + 1) under KDA_ROPE_INTERLEAVED,
+ * i < R / 2; channels from R on are u. Angles are reduced from the exact product of
+ * the position and the fp32 frequency, so that far positions keep their precision
+ * (to 2^-20 of a turn up to position 2^24).
+ *
+ *   q, k         device, bf16 [T, Hq, D], [T, Hk, D], tokens q_stride / k_stride elements
+ *                apart (slices of a fused projection); Hk = 0: no keys (k, k_out NULL)
+ *   q_weight, k_weight device, fp32 [D] or NULL (ones)
+ *   inv_freq     device, fp32 [R / 2]; positions device, int32 [T] (any value); with
+ *                R = 0 nothing is rotated and both may be NULL
+ *   q_out, k_out device, bf16 like q and k, tokens q_out_stride / k_out_stride apart; each
+ *                may be its input itself with the same stride (in place)
+ *   D = 64, 128 or 256, R a multiple of 16 up to D (others: KDA_ERR_UNSUPPORTED_DIM);
+ *   Hq >= 1; Hq + Hk <= 65535; eps >= 0; T < 2^31.
+ *
+ * Alignment: 16 bytes for q, k and the outputs, and strides multiples of 8 elements;
+ * 4 bytes for the others. Norms, angles and products in fp32, results rounded once.
+ */
+enum { KDA_ROPE_INTERLEAVED = 1, KDA_ROPE_DOUT_FP32 = 2 };
+
+KDA_API kda_status kda_qk_norm_rope(const void *q, const void *k, const float *q_weight,
+                                    const float *k_weight, const float *inv_freq,
+                                    const int32_t *positions, int64_t T, int64_t Hq, int64_t Hk,
+                                    int64_t D, int64_t R, int64_t q_stride, int64_t k_stride,
+                                    float eps, int flags, void *q_out, int64_t q_out_stride,
+                                    void *k_out, int64_t k_out_stride, void *stream);
+
+/*
+ * kda_qk_norm_rope_backward -- gradients of kda_qk_norm_rope. With g = dL/dy turned
+ * back by the angles and r = 1 / sqrt(mean(x^2) + eps):
+ *
+ *     dweight = sum over tokens and heads of g x r
+ *     dx      = r (g weight - x r mean(g weight x r))
+ *
+ *   q, k, q_weight, k_weight, inv_freq, positions, sizes, eps: as given to the forward call
+ *   dq_out, dk_out device [T, H, D], tokens dq_out_stride / dk_out_stride elements apart:
+ *                bf16, or both fp32 with KDA_ROPE_DOUT_FP32
+ *   dq, dk       device, bf16 like q and k, tokens dq_stride / dk_stride apart; not an input
+ *   dq_weight, dk_weight device, fp32 [D] or NULL (not wanted)
+ *
+ * The weights' sums are taken in fp32 in a fixed order (the same call gives the same
+ * bits). Workspace: 2 D floats for each of at most 608 blocks.
+ */
+KDA_API kda_status kda_qk_norm_rope_backward(
+    const void *q, const void *k, const float *q_weight, const float *k_weight,
+    const float *inv_freq, const int32_t *positions, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+    int64_t R, int64_t q_stride, int64_t k_stride, float eps, int flags, const void *dq_out,
+    int64_t dq_out_stride, const void *dk_out, int64_t dk_out_stride, void *dq, int64_t dq_stride,
+    void *dk, int64_t dk_stride, float *dq_weight, float *dk_weight, void *stream);
+
+/*
+ * kda_paged_append_fp8 -- new keys and values into a paged cache of 8-bit numbers
+ * (e4m3), with one scale for each page and head: a cached number stands for itself
+ * times its scale. Slot i's new tokens are rows [cu_seqlens[i], cu_seqlens[i + 1]) of k
+ * and v, its last ones: they go to positions seq_lens[i] - (their number) .. seq_lens[i] - 1.
+ *
+ * The scale of a page and head, for keys and for values, is a power of two and only
+ * grows: the least one (from 2^-126 on) that brings the largest new value to 448 or
+ * below, or the one that the page has, if that is larger. A page whose row 0 is among
+ * the new rows starts anew. When the scale grows, the rows in front of the new ones are
+ * scaled down to it, which is exact but for what leaves e4m3's range below. New
+ * values are x / scale, rounded once to the nearest, ties to even; infinities and NaN
+ * become NaN and do not count for the scale. (A scale that a caller has put into a page,
+ * any positive number, is kept and used as its reciprocal.)
+ *
+ *   k, v         device, bf16 [T, Hkv, D], tokens k_stride / v_stride elements apart
+ *   k_cache, v_cache device, e4m3 [pages, page_size, Hkv, D], channels contiguous; pages,
+ *                tokens and heads the given strides (elements) apart, in any order, as
+ *                long as no two rows overlap; both may lie in one buffer
+ *   k_scale, v_scale device, fp32 [pages, Hkv], pages k_scale_stride / v_scale_stride apart;
+ *                not inside the caches' buffers
+ *   page_table, seq_lens, max_pages, pages as for kda_paged_decode, the new tokens included
+ *                in seq_lens (as kda_page_plan leaves it)
+ *   cu_seqlens   device, int32 [B + 1], rising from 0 to at most T, or NULL: T = B, a token
+ *                for each slot (none where seq_lens is 0)
+ *   D = 64 or 128 (others: KDA_ERR_UNSUPPORTED_DIM); B <= 65536; T < 2^31; (T + 2 B) * Hkv < 2^30.
+ *
+ * Pages of different slots that get new tokens must differ. Rows of k and v behind the last
+ * slot are not read. A slot with a wrong cu_seqlens (KDA_ERR_BAD_CU_SEQLENS), length or page
+ * index (KDA_ERR_BAD_PAGE_TABLE) is reported by kda_last_device_error(); its tokens, or those
+ * of the bad page, are not written. Alignment: 16 bytes for k, v and the caches, k_stride and
+ * v_stride multiples of 8 elements, the caches' strides of 16. No workspace.
+ */
+KDA_API kda_status kda_paged_append_fp8(
+    const void *k, const void *v, void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+    const int32_t *page_table, const int32_t *seq_lens, const int32_t *cu_seqlens, int64_t T,
+    int64_t B, int64_t Hkv, int64_t D, int64_t pages, int64_t page_size, int64_t max_pages,
+    int64_t k_stride, int64_t v_stride, int64_t k_page_stride, int64_t k_token_stride,
+    int64_t k_head_stride, int64_t v_page_stride, int64_t v_token_stride, int64_t v_head_stride,
+    int64_t k_scale_stride, int64_t v_scale_stride, void *stream);
+
+/*
+ * kda_paged_decode_fp8 -- kda_paged_decode over the cache of kda_paged_append_fp8:
+ *
+ *     s_j = scale k_scale[page of j] (q . k_j)
+ *     out = sum_j softmax_j(s) v_scale[page of j] v_j,   lse = log sum_j exp(s_j)
+ *
+ *   k_cache, v_cache, their strides, k_scale, v_scale: as for kda_paged_append_fp8. Scales
+ *                are any positive numbers (k_scale: any)
+ *   q, page_table, seq_lens, out, lse, limits and errors as for kda_paged_decode; D, B,
+ *   Hq, pages, max_pages, page_size likewise.
+ *
+ * Alignment: q, k_cache, v_cache, out 16 bytes, the caches' strides multiples of 16
+ * elements; int32 and fp32 arrays 4 bytes. Scores, softmax and sums in fp32. The tensor
+ * core takes the cache's numbers as they are; a query enters as two e4m3 terms (exact to
+ * 2^-19 of its largest channel) and the weights, times the values' scales, as four (16
+ * bits, below out's own rounding). The sum over the cache is split over the SMs and
+ * joined in a fixed order (the same call gives the same bits). Workspace: partial sums.
+ */
+KDA_API kda_status kda_paged_decode_fp8(
+    const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+    const float *v_scale, const int32_t *page_table, const int32_t *seq_lens, int64_t B,
+    int64_t Hq, int64_t Hkv, int64_t D, int64_t pages, int64_t page_size, int64_t max_pages,
+    int64_t k_page_stride, int64_t k_token_stride, int64_t k_head_stride, int64_t v_page_stride,
+    int64_t v_token_stride, int64_t v_head_stride, int64_t k_scale_stride, int64_t v_scale_stride,
+    float scale, void *out, float *lse, void *stream);
 
 /* Static text for a status code (never NULL). */
 KDA_API const char *kda_status_string(kda_status status);

@@ -21,7 +21,7 @@ STATUS = {
     -7: "KDA_ERR_DEVICE_TIMEOUT", -8: "KDA_ERR_NO_DEVICE_SUPPORT", -9: "KDA_ERR_ALIAS",
     -10: "KDA_ERR_GATE_RANGE", -11: "KDA_ERR_CAPTURE", -12: "KDA_ERR_WRONG_DEVICE",
     -13: "KDA_ERR_NOT_DEVICE_MEMORY", -14: "KDA_ERR_SCRATCH_LIMIT", -15: "KDA_ERR_BAD_FLAGS",
-    -16: "KDA_ERR_BAD_PAGE_TABLE",
+    -16: "KDA_ERR_BAD_PAGE_TABLE", -17: "KDA_ERR_OUT_OF_PAGES",
 }
 # input preprocessing flags (include/kda.h)
 PRE_NORM_QK = 1
@@ -30,6 +30,9 @@ PRE_GATE_LOGITS = 2
 CONV_SILU = 1
 CONV_DOUT_FP32 = 2
 SSM_DT_SOFTPLUS = 1
+# flags of the norms with the rotation
+ROPE_INTERLEAVED = 1
+ROPE_DOUT_FP32 = 2
 STATUS_CODE = {v: k for k, v in STATUS.items()}
 
 _lib = None
@@ -84,6 +87,18 @@ def lib() -> ctypes.CDLL:
             L.kda_ssm_step.argtypes = [vp] * 8 + [i64] * 9 + [ctypes.c_int, vp, vp, vp]
             L.kda_paged_decode.restype = ctypes.c_int
             L.kda_paged_decode.argtypes = [vp] * 5 + [i64] * 9 + [f32, vp, vp, vp]
+            L.kda_page_plan.restype = ctypes.c_int
+            L.kda_page_plan.argtypes = [vp] * 6 + [i64] * 5 + [vp] * 8
+            L.kda_qk_norm_rope.restype = ctypes.c_int
+            L.kda_qk_norm_rope.argtypes = ([vp] * 6 + [i64] * 7 + [f32, ctypes.c_int, vp, i64, vp, i64,
+                                           vp])
+            L.kda_qk_norm_rope_backward.restype = ctypes.c_int
+            L.kda_qk_norm_rope_backward.argtypes = ([vp] * 6 + [i64] * 7 + [f32, ctypes.c_int]
+                                                    + [vp, i64] * 4 + [vp] * 3)
+            L.kda_paged_append_fp8.restype = ctypes.c_int
+            L.kda_paged_append_fp8.argtypes = [vp] * 9 + [i64] * 17 + [vp]
+            L.kda_paged_decode_fp8.restype = ctypes.c_int
+            L.kda_paged_decode_fp8.argtypes = [vp] * 7 + [i64] * 15 + [f32, vp, vp, vp]
             L.kda_status_string.restype = ctypes.c_char_p
             L.kda_status_string.argtypes = [ctypes.c_int]
             L.kda_last_device_error.restype = ctypes.c_int
@@ -204,6 +219,56 @@ def kda_paged_decode(q, k_cache, v_cache, page_table, seq_lens, B, Hq, Hkv, D, p
     return lib().kda_paged_decode(q, k_cache, v_cache, page_table, seq_lens, B, Hq, Hkv, D, pages,
                                   page_size, max_pages, k_page_stride, v_page_stride, scale, out,
                                   lse, stream)
+
+
+def kda_page_plan(page_table, seq_lens, new_lens, release, free_pages, free_count, B, max_pages, pool,
+                  page_size, T, page_table_out, seq_lens_out, free_pages_out, free_count_out,
+                  cu_seqlens, positions, slots, stream) -> int:
+    """The page plan C entry point, pointers as ints (0 = NULL)."""
+    return lib().kda_page_plan(page_table, seq_lens, new_lens, release, free_pages, free_count, B,
+                               max_pages, pool, page_size, T, page_table_out, seq_lens_out,
+                               free_pages_out, free_count_out, cu_seqlens, positions, slots, stream)
+
+
+def kda_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, T, Hq, Hk, D, R, q_stride, k_stride,
+                     eps, flags, q_out, q_out_stride, k_out, k_out_stride, stream) -> int:
+    """The C entry point of the norms with the rotation, pointers as ints (0 = NULL)."""
+    return lib().kda_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, T, Hq, Hk, D, R,
+                                  q_stride, k_stride, eps, flags, q_out, q_out_stride, k_out,
+                                  k_out_stride, stream)
+
+
+def kda_qk_norm_rope_backward(q, k, q_weight, k_weight, inv_freq, positions, T, Hq, Hk, D, R, q_stride,
+                              k_stride, eps, flags, dq_out, dq_out_stride, dk_out, dk_out_stride, dq,
+                              dq_stride, dk, dk_stride, dq_weight, dk_weight, stream) -> int:
+    """The C entry point of their gradients, pointers as ints (0 = NULL)."""
+    return lib().kda_qk_norm_rope_backward(q, k, q_weight, k_weight, inv_freq, positions, T, Hq, Hk, D,
+                                           R, q_stride, k_stride, eps, flags, dq_out, dq_out_stride,
+                                           dk_out, dk_out_stride, dq, dq_stride, dk, dk_stride,
+                                           dq_weight, dk_weight, stream)
+
+
+def kda_paged_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_seqlens, T,
+                         B, Hkv, D, pages, page_size, max_pages, k_stride, v_stride, k_page_stride,
+                         k_token_stride, k_head_stride, v_page_stride, v_token_stride, v_head_stride,
+                         k_scale_stride, v_scale_stride, stream) -> int:
+    """The C entry point that fills an 8-bit cache, pointers as ints (0 = NULL)."""
+    return lib().kda_paged_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens,
+                                      cu_seqlens, T, B, Hkv, D, pages, page_size, max_pages, k_stride,
+                                      v_stride, k_page_stride, k_token_stride, k_head_stride,
+                                      v_page_stride, v_token_stride, v_head_stride, k_scale_stride,
+                                      v_scale_stride, stream)
+
+
+def kda_paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, B, Hq, Hkv, D,
+                         pages, page_size, max_pages, k_page_stride, k_token_stride, k_head_stride,
+                         v_page_stride, v_token_stride, v_head_stride, k_scale_stride, v_scale_stride,
+                         scale, out, lse, stream) -> int:
+    """The C entry point of the attention over an 8-bit cache, pointers as ints (0 = NULL)."""
+    return lib().kda_paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, B, Hq,
+                                      Hkv, D, pages, page_size, max_pages, k_page_stride, k_token_stride,
+                                      k_head_stride, v_page_stride, v_token_stride, v_head_stride,
+                                      k_scale_stride, v_scale_stride, scale, out, lse, stream)
 
 
 def kda_status_string(code: int) -> str:
@@ -813,6 +878,252 @@ def paged_decode(q, k_cache, v_cache, page_table, seq_lens, scale=None, out=None
                           float(scale), _ptr(out), _ptr(lse), _current_stream(q, stream))
     if rc != 0:
         raise KdaError(rc, "kda_paged_decode")
+    return out, lse
+
+
+def page_plan(page_table, seq_lens, new_lens, free_pages, free_count, page_size, tokens, release=None,
+              in_place=False, stream=None):
+    """Page tables, positions and slots of a batch's next tokens, on the current CUDA device.
+
+    page_table: int32 [B, max_pages]; seq_lens: int32 [B], the tokens each slot holds;
+    new_lens: int32 [B], those that join; free_pages: int32 [pool], a stack of the
+    pages that nobody holds, the first free_count (int32 [1]) of them; release: bool
+    or uint8 [B] or None, slots whose pages are given back first; tokens: rows of the
+    positions and slots, at least the new tokens. Returns (page_table, seq_lens,
+    free_pages, free_count, cu_seqlens, positions, slots): the first four after the
+    call (with in_place=True the tensors given, updated), int32 [B + 1], int32
+    [tokens] and int64 [tokens]. Rows behind the last new token have position 0 and
+    slot -1. Too few pages and bad lengths are reported by check_device_error(), and
+    nothing is planned then.
+    """
+    import torch
+
+    if page_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("page_table must be [B, max_pages] and free_pages [pool]")
+    B, width = page_table.shape
+    given = (page_table, seq_lens, free_pages, free_count)
+    _need("page_table", page_table, torch.int32, (B, width))
+    _need("seq_lens", seq_lens, torch.int32, (B,))
+    _need("new_lens", new_lens, torch.int32, (B,))
+    _need("free_pages", free_pages, torch.int32, free_pages.shape)
+    _need("free_count", free_count, torch.int32, (1,))
+    if release is not None:
+        if release.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("release must be bool or uint8")
+        _need("release", release, release.dtype, (B,))
+    tokens, device = int(tokens), page_table.device
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    after = given if in_place else tuple(torch.empty_like(t) for t in given)
+    cu = torch.empty((B + 1,), dtype=torch.int32, device=device)
+    positions = torch.empty((tokens,), dtype=torch.int32, device=device)
+    slots = torch.empty((tokens,), dtype=torch.int64, device=device)
+    rc = lib().kda_page_plan(_ptr(page_table), _ptr(seq_lens), _ptr(new_lens), _ptr(release),
+                             _ptr(free_pages), _ptr(free_count), B, width, free_pages.shape[0],
+                             page_size, tokens, _ptr(after[0]), _ptr(after[1]), _ptr(after[2]),
+                             _ptr(after[3]), _ptr(cu), _ptr(positions), _ptr(slots),
+                             _current_stream(page_table, stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_page_plan")
+    return (*after, cu, positions, slots)
+
+
+def _heads_inputs(q, k, q_weight, k_weight, inv_freq, positions):
+    """Checks of the norms' inputs; returns (leading dims, T, Hq, Hk, D, R)."""
+    import torch
+
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [T, Hq, D] or [B, T, Hq, D]")
+    lead = q.shape[:-2]
+    Hq, D = q.shape[-2:]
+    _need("q", q, torch.bfloat16, (*lead, Hq, D), contiguous=False)
+    Hk = 0
+    if k is not None:
+        Hk = k.shape[-2] if k.dim() == q.dim() else -1
+        _need("k", k, torch.bfloat16, (*lead, Hk, D), contiguous=False)
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None:
+            _need(name, t, torch.float32, (D,))
+    R = 0
+    if inv_freq is not None:
+        R = 2 * inv_freq.numel()
+        _need("inv_freq", inv_freq, torch.float32, (R // 2,))
+        if positions is None:
+            raise ValueError("inv_freq needs positions")
+        _need("positions", positions, torch.int32, lead)
+    return lead, math.prod(lead), Hq, Hk, D, R
+
+
+def _like(name, t, x, dtypes):
+    """An output or gradient shaped like x, strided as it likes: given, or made."""
+    import torch
+
+    if t is None:
+        return torch.empty(x.shape, dtype=dtypes[0], device=x.device)
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}")
+    _need(name, t, t.dtype, x.shape, contiguous=False)
+    return t
+
+
+def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=None, eps=1e-6,
+                 interleaved=False, q_out=None, k_out=None, stream=None):
+    """Norm of every query and key head and the rotation by its position, current CUDA device.
+
+    x / sqrt(mean(x^2) + eps) * weight over the channels of a head, then the first R
+    channels turned by positions * inv_freq, in pairs (i, i + R/2) or, interleaved,
+    (2i, 2i + 1). q, k: bf16 [T, H, D] or [B, T, H, D], D = 64, 128 or 256, tokens any
+    even stride apart (slices of a fused projection), k may be None; weights: fp32 [D]
+    or None; inv_freq: fp32 [R/2] (R a multiple of 16) with positions int32 [T] or
+    [B, T], or None (no rotation). q_out and k_out may be q and k (in place). Returns
+    (q_out, k_out), bf16 (None without k).
+    """
+    import torch
+
+    _, T, Hq, Hk, D, R = _heads_inputs(q, k, q_weight, k_weight, inv_freq, positions)
+    q_out = _like("q_out", q_out, q, (torch.bfloat16,))
+    k_out = _like("k_out", k_out, k, (torch.bfloat16,)) if k is not None else None
+    rc = lib().kda_qk_norm_rope(
+        _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), T, Hq, Hk, D,
+        R, _row_stride(q, 2, "q"), _row_stride(k, 2, "k") if Hk else 0, float(eps),
+        ROPE_INTERLEAVED if interleaved else 0, _ptr(q_out), _row_stride(q_out, 2, "q_out"), _ptr(k_out),
+        _row_stride(k_out, 2, "k_out") if Hk else 0, _current_stream(q, stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, inv_freq=None,
+                          positions=None, eps=1e-6, interleaved=False, dq=None, dk=None, stream=None):
+    """Gradients of ``qk_norm_rope`` on the current CUDA device.
+
+    Inputs as there (q and k as given to it), plus dq_out and dk_out, bf16 or both fp32,
+    shaped like q and k. Returns (dq, dk, dq_weight, dk_weight): bf16 like q and k
+    (written to `dq` and `dk` if given, which may be strided), fp32 [D] (None for
+    weights that are None; dk and dk_weight None without k).
+    """
+    import torch
+
+    _, T, Hq, Hk, D, R = _heads_inputs(q, k, q_weight, k_weight, inv_freq, positions)
+    flags = ROPE_INTERLEAVED if interleaved else 0
+    if dq_out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("dq_out must be bfloat16 or float32")
+    _need("dq_out", dq_out, dq_out.dtype, q.shape, contiguous=False)
+    if dq_out.dtype == torch.float32:
+        flags |= ROPE_DOUT_FP32
+    if k is not None:
+        if dk_out is None:
+            raise ValueError("dk_out is missing")
+        _need("dk_out", dk_out, dq_out.dtype, k.shape, contiguous=False)
+    elif dk_out is not None:
+        raise ValueError("dk_out needs k")
+    dq = _like("dq", dq, q, (torch.bfloat16,))
+    dk = _like("dk", dk, k, (torch.bfloat16,)) if k is not None else None
+    dqw = torch.empty_like(q_weight) if q_weight is not None else None
+    dkw = torch.empty_like(k_weight) if k_weight is not None and k is not None else None
+    rc = lib().kda_qk_norm_rope_backward(
+        _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), T, Hq, Hk, D,
+        R, _row_stride(q, 2, "q"), _row_stride(k, 2, "k") if Hk else 0, float(eps), flags, _ptr(dq_out),
+        _row_stride(dq_out, 2, "dq_out"), _ptr(dk_out), _row_stride(dk_out, 2, "dk_out") if Hk else 0,
+        _ptr(dq), _row_stride(dq, 2, "dq"), _ptr(dk), _row_stride(dk, 2, "dk") if Hk else 0, _ptr(dqw),
+        _ptr(dkw), _current_stream(q, stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_qk_norm_rope_backward")
+    return dq, dk, dqw, dkw
+
+
+def _fp8_cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, B):
+    """Checks of an 8-bit cache; returns (pages, page_size, Hkv, D, max_pages, strides)."""
+    import torch
+
+    if k_cache.dim() != 4:
+        raise ValueError("the caches must be [pages, page_size, Hkv, D]")
+    f8, shape = torch.float8_e4m3fn, k_cache.shape
+    pages, page_size, Hkv, D = shape
+    strides = []
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _need(name, t, f8, shape, contiguous=False)
+        page, token, head, channel = t.stride()
+        if channel != 1 and D > 1:
+            raise ValueError(f"{name} must be contiguous within a head")
+        strides += (page, token, head)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _need(name, t, torch.float32, (pages, Hkv), contiguous=False)
+        strides.append(_row_stride(t, 1, name))
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    _need("page_table", page_table, torch.int32, (B, page_table.shape[1]))
+    _need("seq_lens", seq_lens, torch.int32, (B,))
+    return pages, page_size, Hkv, D, page_table.shape[1], strides
+
+
+def paged_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_seqlens=None,
+                     stream=None):
+    """New keys and values into a paged 8-bit cache, on the current CUDA device.
+
+    k, v: bf16 [T, Hkv, D], D = 64 or 128, tokens any even stride apart; k_cache, v_cache:
+    float8_e4m3fn [pages, page_size, Hkv, D] with channels contiguous and any other strides;
+    k_scale, v_scale: fp32 [pages, Hkv], powers of two that this call settles (a page's scale
+    only grows while it is filled); page_table: int32 [B, max_pages]; seq_lens: int32 [B], the
+    new tokens included; cu_seqlens: int32 [B + 1], the rows of each slot, which go to its last
+    positions, or None (T = B, one token each). Writes the caches and scales in place.
+    """
+    import torch
+
+    if k.dim() != 3:
+        raise ValueError("k must be [T, Hkv, D]")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    T, B = k.shape[0], page_table.shape[0]
+    pages, page_size, Hkv, D, width, strides = _fp8_cache(k_cache, v_cache, k_scale, v_scale, page_table,
+                                                          seq_lens, B)
+    _need("k", k, torch.bfloat16, (T, Hkv, D), contiguous=False)
+    _need("v", v, torch.bfloat16, (T, Hkv, D), contiguous=False)
+    if cu_seqlens is None:
+        if T != B:
+            raise ValueError("without cu_seqlens there is one row per slot")
+    else:
+        _need("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
+    rc = lib().kda_paged_append_fp8(
+        _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
+        _ptr(seq_lens), _ptr(cu_seqlens), T, B, Hkv, D, pages, page_size, width, _row_stride(k, 2, "k"),
+        _row_stride(v, 2, "v"), *strides, _current_stream(k, stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_paged_append_fp8")
+
+
+def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, scale=None, out=None,
+                     lse=None, stream=None):
+    """Attention of one new token per sequence over a paged 8-bit cache, current CUDA device.
+
+    q: bf16 [B, Hq, D], D = 64 or 128; the cache, its scales, page_table and seq_lens (the new
+    token included; 0: out = 0, lse = -inf) as for paged_append_fp8; scale: 1/sqrt(D) by
+    default. Returns (out, lse): bf16 like q and fp32 [B, Hq] (natural logarithm).
+    """
+    import torch
+
+    if q.dim() != 3:
+        raise ValueError("q must be [B, Hq, D]")
+    B, Hq, D = q.shape
+    pages, page_size, Hkv, dim, width, strides = _fp8_cache(k_cache, v_cache, k_scale, v_scale,
+                                                            page_table, seq_lens, B)
+    _need("q", q, torch.bfloat16, (B, Hq, dim))
+    if scale is None:
+        scale = 1.0 / math.sqrt(max(D, 1))   # (D = 0 is refused below)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need("out", out, torch.bfloat16, q.shape)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    else:
+        _need("lse", lse, torch.float32, (B, Hq))
+    rc = lib().kda_paged_decode_fp8(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
+        _ptr(seq_lens), B, Hq, Hkv, D, pages, page_size, width, *strides, float(scale), _ptr(out),
+        _ptr(lse), _current_stream(q, stream))
+    if rc != 0:
+        raise KdaError(rc, "kda_paged_decode_fp8")
     return out, lse
 
 

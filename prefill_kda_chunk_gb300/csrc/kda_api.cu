@@ -27,11 +27,22 @@ struct StreamWorkspace {
     // zero by every launch that uses them
     void *sync = nullptr;
     size_t sync_bytes = 0;
+    // A captured call has used the buffers: a graph may hold their addresses, so that
+    // growing leaves them (kda_workspace_release frees them).
+    bool captured = false;
+    std::vector<void *> left;
+    // Before a buffer is replaced by a larger one.
+    cudaError_t give_up(void *p, cudaStream_t stream) {
+        if (p == nullptr) return cudaSuccess;
+        if (!captured) return cudaFreeAsync(p, stream);
+        left.push_back(p);
+        return cudaSuccess;
+    }
 };
 
 struct DeviceState {
     bool ready = false;
-    bool configured[3] = {};   // the operators around KDA, by kda::Operator
+    bool configured[kda::kOperators] = {};   // the operators around KDA
     int *err = nullptr;  // sticky error word (device memory, 256 B)
     std::map<cudaStream_t, StreamWorkspace> ws;
 };
@@ -242,11 +253,11 @@ int kda::pointer_device_status(const void *p, int dev) {
 
 // Replaces *ptr by at least `need` bytes in stream order, the first `zero` of
 // them zeroed.
-static kda_status grow(void **ptr, size_t *bytes, int64_t need, int64_t zero, bool capturing,
-                       cudaStream_t stream) {
+static kda_status grow(StreamWorkspace &ws, void **ptr, size_t *bytes, int64_t need, int64_t zero,
+                       bool capturing, cudaStream_t stream) {
     if (*bytes >= static_cast<size_t>(need)) return KDA_OK;
     if (capturing) return KDA_ERR_CAPTURE;
-    if (*ptr != nullptr && cudaFreeAsync(*ptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    if (ws.give_up(*ptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
     *ptr = nullptr;
     *bytes = 0;
     if (cudaMallocAsync(ptr, need, stream) != cudaSuccess) {
@@ -287,17 +298,19 @@ int kda::begin_call(Operator op, const void *const *ptrs, int n, void *stream_, 
     // 2 ms of every program's first KDA call when all of them were set there. (No stream
     // work: also while capturing.)
     if (!st.configured[op]) {
-        if ((op == kConv ? configure_conv() : op == kSsm ? configure_ssm() : configure_paged()) != cudaSuccess)
-            return KDA_ERR_CUDA;
+        cudaError_t (*const configure[kOperators])() = {configure_conv, configure_ssm, configure_paged,
+                                                        configure_heads, configure_cache, configure_paged8};
+        if (configure[op]() != cudaSuccess) return KDA_ERR_CUDA;
         st.configured[op] = true;
     }
     ctx->err = st.err;
     if (ws_bytes > 0 || sync_bytes > 0) {
         StreamWorkspace &ws = st.ws[stream];
+        ws.captured |= capturing;
         if (ws_bytes > 0) {
             // the flag block at the start (its zeros included) belongs to the
             // prefill's and the gradients' calls on this buffer
-            const kda_status rc = grow(&ws.ptr, &ws.bytes, 256 + ws_bytes, 256, capturing, stream);
+            const kda_status rc = grow(ws, &ws.ptr, &ws.bytes, 256 + ws_bytes, 256, capturing, stream);
             if (rc != KDA_OK) return rc;
             ws.ring_clean = 0;
             ctx->ws = static_cast<uint8_t *>(ws.ptr) + 256;
@@ -305,7 +318,7 @@ int kda::begin_call(Operator op, const void *const *ptrs, int n, void *stream_, 
         }
         if (sync_bytes > 0) {
             const kda_status rc =
-                grow(&ws.sync, &ws.sync_bytes, sync_bytes, sync_bytes, capturing, stream);
+                grow(ws, &ws.sync, &ws.sync_bytes, sync_bytes, sync_bytes, capturing, stream);
             if (rc != KDA_OK) return rc;
             ctx->sync = static_cast<int *>(ws.sync);
         }
@@ -336,6 +349,7 @@ const char *kda_status_string(kda_status s) {
                    "kda_chunk_prefill_noalloc";
         case KDA_ERR_BAD_FLAGS: return "an unknown flag bit is set";
         case KDA_ERR_BAD_PAGE_TABLE: return "a sequence length or page index is out of range";
+        case KDA_ERR_OUT_OF_PAGES: return "fewer free pages than the new tokens need";
     }
     return "unknown status";
 }
@@ -483,9 +497,10 @@ kda_status kda_chunk_prefill_ex(const void *q, const void *k, const void *v, con
     }
 
     StreamWorkspace &ws = st.ws[stream];
+    ws.captured |= capturing;
     if (ws.bytes < static_cast<size_t>(pl.ws_bytes)) {
         if (capturing) return KDA_ERR_CAPTURE;
-        if (ws.ptr != nullptr && cudaFreeAsync(ws.ptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
+        if (ws.give_up(ws.ptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
         ws.ptr = nullptr;
         ws.bytes = 0;
         if (cudaMallocAsync(&ws.ptr, pl.ws_bytes, stream) != cudaSuccess) {
@@ -719,9 +734,10 @@ kda_status kda_chunk_prefill_backward(const void *q, const void *k, const void *
     const int64_t ckpt_bytes = backward_ckpt_bytes(B, T, H, N, cu_seqlens != nullptr, pl);
     const int64_t need = backward_ws_bytes(B, T, H, N, cu_seqlens != nullptr, pl);
     StreamWorkspace &ws = st.ws[stream];
+    ws.captured |= capturing;
     if (ws.bytes < static_cast<size_t>(need)) {
         if (capturing) return KDA_ERR_CAPTURE;
-        if (ws.ptr != nullptr && cudaFreeAsync(ws.ptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
+        if (ws.give_up(ws.ptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
         ws.ptr = nullptr;
         ws.bytes = 0;
         if (cudaMallocAsync(&ws.ptr, need, stream) != cudaSuccess) {
@@ -893,6 +909,7 @@ kda_status kda_last_device_error(void *stream_) {
     if (word & kda::kErrTimeout) return KDA_ERR_DEVICE_TIMEOUT;
     if (word & kda::kErrGate) return KDA_ERR_GATE_RANGE;
     if (word & kda::kErrPage) return KDA_ERR_BAD_PAGE_TABLE;
+    if (word & kda::kErrPool) return KDA_ERR_OUT_OF_PAGES;
     return KDA_OK;
 }
 
@@ -909,6 +926,9 @@ kda_status kda_workspace_release(void) {
         w.ptr = nullptr;
         if (w.sync != nullptr && cudaFree(w.sync) != cudaSuccess) return KDA_ERR_CUDA;
         w.sync = nullptr;
+        for (void *p : w.left)
+            if (cudaFree(p) != cudaSuccess) return KDA_ERR_CUDA;
+        w.left.clear();
     }
     it->second.ws.clear();
     return KDA_OK;

@@ -229,7 +229,7 @@ struct CallContext {
     uint8_t *ws = nullptr;
     int *sync = nullptr;
 };
-enum Operator { kConv, kSsm, kPaged };
+enum Operator { kConv, kSsm, kPaged, kHeads, kCache, kPaged8, kOperators };
 // The device checks of an entry point (first use, stream, pointers; NULLs are
 // skipped) and its workspace. Returns a kda_status.
 int begin_call(Operator op, const void *const *ptrs, int n, void *stream, int64_t ws_bytes, int64_t sync_bytes,
@@ -304,6 +304,75 @@ cudaError_t configure_paged();
 int64_t paged_workspace(const PagedParams &p);
 int64_t paged_sync(const PagedParams &p);
 cudaError_t launch_paged(const PagedParams &p, const CallContext &ctx, cudaStream_t stream);
+
+// Norms of queries and keys with the position rotation (kda_heads.cu). Rows of a token
+// are contiguous, [H, D]; tokens are their own stride apart.
+struct HeadsParams {
+    const void *q, *k;         // bf16 [T, Hq, D], [T, Hk, D]
+    const float *qw, *kw;      // [D] or nullptr (ones)
+    const float *freq;         // [rot / 2]
+    const int32_t *pos;        // [T]
+    int64_t tokens, q_stride, k_stride, qo_stride, ko_stride, dq_stride, dk_stride;
+    int32_t hq, hk, dim, rot;
+    float eps;
+    bool pairs, dout32;
+    void *q_out, *k_out;       // bf16: the results; gradient: dq, dk
+    const void *dq, *dk;       // gradient: bf16 or fp32 [T, H, D]
+    float *dqw, *dkw;          // gradient: [D] or nullptr
+    float *partial;            // gradient: [blocks][2][D]
+};
+cudaError_t configure_heads();
+cudaError_t launch_heads(const HeadsParams &p, cudaStream_t stream);
+int64_t heads_workspace(const HeadsParams &p);
+cudaError_t launch_heads_backward(const HeadsParams &p, cudaStream_t stream);
+
+// Page tables, positions and slots from request lengths (kda_cache.cu).
+struct PlanParams {
+    const int32_t *table, *lens, *news, *free, *count;   // [B, width], [B], [B], [pool], [1]
+    const uint8_t *release;    // [B] or nullptr
+    int64_t width, pool, page_size, tokens;
+    int32_t batch;
+    int32_t *table_out, *lens_out, *free_out, *count_out, *cu, *pos;
+    int64_t *slots;            // [tokens]
+    int64_t *meta;             // scratch: what the first launch hands to the second
+    int *err;
+};
+int64_t plan_workspace(const PlanParams &p);
+cudaError_t launch_plan(const PlanParams &p, cudaStream_t stream);
+
+// A paged cache of e4m3 numbers with a scale per page and head. Strides in bytes:
+// pages, tokens, heads; scales in floats: pages.
+struct Cache8 {
+    uint8_t *k, *v;
+    float *ks, *vs;
+    int64_t k_page, k_token, k_head, v_page, v_token, v_head, ks_page, vs_page;
+    int64_t pages, max_pages;
+    const int32_t *table, *lens;   // [B, max_pages], [B]
+    int32_t batch, hkv, dim, page_size;
+    int *err;
+};
+struct AppendParams {
+    Cache8 c;
+    const void *k, *v;         // bf16 [T, Hkv, D]
+    const int32_t *cu;         // [B + 1] or nullptr (a token each)
+    int64_t tokens, k_stride, v_stride;
+};
+cudaError_t configure_cache();
+cudaError_t launch_append(const AppendParams &p, cudaStream_t stream);
+
+// Decode attention over that cache (kda_paged8.cu).
+struct Paged8Params {
+    Cache8 c;
+    const void *q;             // bf16 [B, Hq, D]
+    int32_t hq;
+    float scale;
+    void *out;                 // bf16 [B, Hq, D]
+    float *lse;                // [B, Hq] or nullptr
+};
+cudaError_t configure_paged8();
+int64_t paged8_workspace(const Paged8Params &p);
+int64_t paged8_sync(const Paged8Params &p);
+cudaError_t launch_paged8(const Paged8Params &p, const CallContext &ctx, cudaStream_t stream);
 
 // The error word of the allocation-free entry point's fixed scratch array on
 // device `dev` (kda_noalloc.cu): read and cleared with a synchronous copy,
