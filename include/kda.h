@@ -608,8 +608,8 @@ KDA_API kda_status kda_paged_append_fp8(
  * Alignment: q, k_cache, v_cache, out 16 bytes, the caches' strides multiples of 16
  * elements; int32 and fp32 arrays 4 bytes. Scores, softmax and sums in fp32. The tensor
  * core takes the cache's numbers as they are; a query enters as two e4m3 terms (exact to
- * 2^-19 of its largest channel) and the weights, times the values' scales, as four (16
- * bits, below out's own rounding). The sum over the cache is split over the SMs and
+ * 2^-22 of its largest channel) and the weights, times the values' scales, as four (16
+ * bits, below out's own rounding, to 2^-33 of the largest among 128 tokens). The sum over the cache is split over the SMs and
  * joined in a fixed order (the same call gives the same bits). Workspace: partial sums.
  */
 KDA_API kda_status kda_paged_decode_fp8(
@@ -705,6 +705,15 @@ KDA_API kda_status kda_test_stall_recurrent(int chunk, int64_t wait_ns);
  * chunk < -1: KDA_ERR_BAD_SHAPE.
  */
 KDA_API kda_status kda_test_stall_scan(int chunk);
+
+/*
+ * Test hook for kda_paged_decode_fp8, likewise (process-wide, host only): in later calls
+ * every thread block copies the first `tile` tiles of its share only, and the waits for
+ * the next one run out (after about two seconds). The call then records
+ * KDA_ERR_DEVICE_TIMEOUT and leaves, outputs unspecified. tile = -1 turns the hook off
+ * (the default); tile < -1: KDA_ERR_BAD_SHAPE.
+ */
+KDA_API kda_status kda_test_stall_paged_fp8(int tile);
 
 /*
  * Test hook: how kda_short_conv_backward would launch its kernel for arguments

@@ -137,7 +137,24 @@ def append(x, cache, scale, table, lens, cu=None):
 
 
 def paged_attention(q, k_cache, v_cache, k_scale, v_scale, table, lens, scale=None):
-    """As ops.paged_attention, over the numbers that the cache stands for."""
-    k, v = (c.detach().cpu().to(F64) * s.detach().cpu().to(F64)[:, None, :, None]
-            for c, s in ((k_cache, k_scale), (v_cache, v_scale)))
-    return ops.paged_attention(q, k, v, table, lens, scale)
+    """-> (out, lse, sum of p |v|, largest sum of |q||k| scale of a row, floor), as
+    ops.paged_attention over the numbers that the cache stands for. floor: the largest weight
+    times its value's scale, times the sum of the cached |v|: the terms that a weight is split
+    into end at a fraction of the largest one."""
+    numbers = [(c.detach().cpu().to(F64), s.detach().cpu().to(F64))
+               for c, s in ((k_cache, k_scale), (v_cache, v_scale))]
+    k, v = (c * s[:, None, :, None] for c, s in numbers)
+    out, lse, size, reach = ops.paged_attention(q, k, v, table, lens, scale)
+    q, table = q.detach().cpu().to(F64), table.cpu()
+    page, H, D = k.shape[1:]
+    scale = 1 / math.sqrt(D) if scale is None else scale
+    floor = torch.zeros_like(out)
+    for i, n in enumerate(int(x) for x in lens):
+        ids = table[i, :-(-n // page)].long()
+        kk, codes = k[ids].reshape(-1, H, D)[:n], numbers[1][0][ids].reshape(-1, H, D)[:n].abs().sum(0)
+        vs = numbers[1][1][ids].repeat_interleave(page, 0)[:n]
+        for h in range(q.shape[1] if n else 0):
+            g = h // (q.shape[1] // H)
+            p = torch.softmax(scale * (kk[:, g] @ q[i, h]), 0)
+            floor[i, h] = (p * vs[:, g]).max() * codes[g]
+    return out, lse, size, reach, floor

@@ -123,6 +123,8 @@ def lib() -> ctypes.CDLL:
             L.kda_test_stall_recurrent.argtypes = [ctypes.c_int, i64]
             L.kda_test_stall_scan.restype = ctypes.c_int
             L.kda_test_stall_scan.argtypes = [ctypes.c_int]
+            L.kda_test_stall_paged_fp8.restype = ctypes.c_int
+            L.kda_test_stall_paged_fp8.argtypes = [ctypes.c_int]
             L.kda_build_info.restype = ctypes.c_char_p
             L.kda_build_info.argtypes = []
             _lib = L
@@ -325,6 +327,12 @@ def kda_test_stall_scan(chunk: int) -> int:
     """Test hook: the state space scan's blocks copy the tiles of their first `chunk`
     chunks only, and their waits run out (-1: off)."""
     return lib().kda_test_stall_scan(int(chunk))
+
+
+def kda_test_stall_paged_fp8(tile: int) -> int:
+    """Test hook: the blocks of the attention over an 8-bit cache copy their first `tile` tiles
+    only, and their waits run out (-1: off)."""
+    return lib().kda_test_stall_paged_fp8(int(tile))
 
 
 def kda_test_conv_backward_plan(x, d_out, dx, tokens, D, W, x_stride, dout_stride, dx_stride,

@@ -5,6 +5,9 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <climits>
+
 #include "kda.h"
 #include "kda_checks.h"
 #include "kda_device.cuh"
@@ -20,6 +23,8 @@ using kda::Rows;
 using kda::rows_fit;
 
 constexpr int64_t k31 = int64_t(1) << 31;
+
+std::atomic<int> g_stall_paged8{INT_MAX};   // kda_test_stall_paged_fp8
 
 kda_status status(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
@@ -353,6 +358,12 @@ kda_status kda_paged_append_fp8(
     return status(kda::launch_append(p, static_cast<cudaStream_t>(stream)));
 }
 
+kda_status kda_test_stall_paged_fp8(int tile) {
+    if (tile < -1) return KDA_ERR_BAD_SHAPE;
+    g_stall_paged8.store(tile < 0 ? INT_MAX : tile);
+    return KDA_OK;
+}
+
 kda_status kda_paged_decode_fp8(
     const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
     const float *v_scale, const int32_t *page_table, const int32_t *seq_lens, int64_t B,
@@ -385,6 +396,7 @@ kda_status kda_paged_decode_fp8(
     p.c = cache_of(kc, vc, k_scale, v_scale, page_table, seq_lens, B, max_pages, k_scale_stride,
                    v_scale_stride);
     p.q = q; p.hq = static_cast<int32_t>(Hq); p.scale = scale; p.out = out; p.lse = lse;
+    p.stall = g_stall_paged8.load();
     const void *ptrs[] = {q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, out, lse};
     kda::CallContext ctx;
     const kda_status rc = begin(kda::kPaged8, ptrs, 9, stream, kda::paged8_workspace(p),

@@ -368,6 +368,7 @@ struct Paged8Params {
     float scale;
     void *out;                 // bf16 [B, Hq, D]
     float *lse;                // [B, Hq] or nullptr
+    int stall;                 // test hook: tiles of a block that are copied
 };
 cudaError_t configure_paged8();
 int64_t paged8_workspace(const Paged8Params &p);

@@ -5,12 +5,9 @@
 // Every key and value is used once per query head that shares it, so the
 // operator is bound by reading the cache: 4 D B per (token, key-value head).
 //
-// Split. The cache is cut into tiles of 64 tokens of one work item (sequence,
-// key-value head, up to 16 of its query heads). An item costs its tiles and
-// kItemCost more for its start and end; these units are numbered sequence by
-// sequence, and CTA c of G takes the units [c U / G, (c + 1) U / G): all CTAs
-// have the same work, be the lengths ragged, few or one. A CTA's tiles of one
-// item are a piece. A piece that is the whole item writes the result; the
+// Split (kda_pieces.cuh). Tiles of 64 tokens of one work item (sequence, key-value
+// head, up to 16 of its query heads), kItemCost more for its start and end, shared
+// out evenly over the CTAs. A piece that is the whole item writes the result; the
 // others leave their maximum, sum and unnormalised output in the workspace,
 // and the last CTA to arrive joins them in CTA order (which one that is does
 // not change the result).
@@ -36,6 +33,7 @@
 
 #include "kda_device.cuh"
 #include "kda_internal.h"
+#include "kda_pieces.cuh"
 
 namespace kda {
 
@@ -94,105 +92,31 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 
-// Tokens of sequence b, or 0 where the length cannot be right.
-__device__ __forceinline__ int length_of(const PagedParams &p, int b, bool *bad) {
-    const int len = __ldg(p.lens + b);
-    if (len < 0 || len > p.max_pages * p.page_size || (len > 0 && p.pages == 0)) {
-        *bad = true;
-        return 0;
-    }
-    return len;
+using PagedSplit = Split<kTile, kItemCost>;
+
+__host__ __device__ __forceinline__ Lengths lengths_of(const PagedParams &p) {
+    return {p.lens, p.max_pages * p.page_size, p.batch, p.pages > 0};
 }
-
-// Units of an item of a sequence of this length.
-__host__ __device__ __forceinline__ int64_t units_of(int64_t len) {
-    return len > 0 ? (len + kTile - 1) / kTile + kItemCost : 0;
-}
-
-// Owner of unit u when G CTAs split U units evenly.
-__device__ __forceinline__ int owner(int64_t u, int64_t U, int64_t G) {
-    return static_cast<int>(((u + 1) * G - 1) / U);
-}
-
-// Adds to a counter, after this block's writes before the barrier in front of it and before
-// its reads behind the next one.
-__device__ __forceinline__ int add_acq_rel(int *p, int v) {
-    int old;
-    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;\n" : "=r"(old) : "l"(p), "r"(v) : "memory");
-    return old;
-}
-
-// A CTA's way through its share [u, u1) of the units, piece by piece.
-struct Pieces {
-    int64_t u, u1, seq_at;   // next unit; end of the share; first unit of sequence b
-    int b;
-    // the piece: its item, and the tiles of it
-    int len, tiles, item, tile0, tile1;
-    int64_t item_at;
-
-    __device__ __forceinline__ bool next(const PagedParams &p, int items) {
-        while (u < u1) {
-            bool ignore = false;
-            len = length_of(p, b, &ignore);
-            const int64_t units = units_of(len);
-            if (u >= seq_at + units * items) {
-                seq_at += units * items;
-                ++b;
-                continue;
-            }
-            tiles = static_cast<int>(units) - kItemCost;
-            item = static_cast<int>((u - seq_at) / units);
-            item_at = seq_at + item * units;
-            const int64_t tile_at = item_at + kItemCost;
-            // the tiles among the units [u, min(u1, end of the item))
-            tile0 = static_cast<int>(u > tile_at ? u - tile_at : 0);
-            tile1 = static_cast<int>(u1 - tile_at < tiles ? u1 - tile_at : tiles);
-            u = item_at + units;
-            if (tile0 < tile1) return true;
-        }
-        return false;
-    }
-};
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kPagedWarps * 32, kPagedCtasPerSm)
 paged_kernel(PagedParams p, float *slots, int *arrived) {
     using S = Shape<D, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_sum[kPagedWarps], s_off;
-    __shared__ int s_first, s_last;
+    __shared__ int s_last;
     __shared__ float s_m[kPagedWarps][8], s_l[kPagedWarps][8];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = p.hq / p.hkv, chunks = (group + S::kHeads - 1) / S::kHeads;
     const int items = p.hkv * chunks;   // work items of a sequence
 
-    // ---- the split: units before each thread's run of sequences, by a block scan
-    const int per = (p.batch + kPagedWarps * 32 - 1) / (kPagedWarps * 32);
-    bool bad = false;
-    int64_t mine = 0;
-    for (int i = 0, b = tid * per; i < per && b < p.batch; ++i, ++b)
-        mine += units_of(length_of(p, b, &bad)) * items;
-    if (bad && blockIdx.x == 0) atomicOr(p.err, kErrPage);
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) s_sum[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - mine, U = 0;
-#pragma unroll
-    for (int w = 0; w < kPagedWarps; ++w) {
-        if (w < warp) before += s_sum[w];
-        U += s_sum[w];
-    }
-    const int64_t G = U < gridDim.x ? U : gridDim.x;
+    const Lengths lens = lengths_of(p);
+    const PagedSplit::Share sh = PagedSplit::share<kPagedWarps * 32>(lens, items, p.err);
+    const int64_t U = sh.U, G = sh.G, u0 = sh.u0;
 
     // sequences without tokens
     for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
         bool ignore = false;
-        if (length_of(p, b, &ignore) != 0) continue;
+        if (lens.of(b, &ignore) != 0) continue;
         for (int i = tid; i < p.hq * D / 8; i += kPagedWarps * 32)
             reinterpret_cast<uint4 *>(p.out)[static_cast<int64_t>(b) * (p.hq * D / 8) + i] =
                 make_uint4(0, 0, 0, 0);
@@ -202,20 +126,6 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
     }
     const int c = blockIdx.x;
     if (c >= G) return;
-    const int64_t u0 = c * U / G, u1 = (c + 1) * U / G;
-    if (u0 >= before && u0 < before + mine) {   // one thread of the block
-        int64_t at = before;
-        int b = tid * per;
-        for (;; ++b) {
-            bool ignore = false;
-            const int64_t n = units_of(length_of(p, b, &ignore)) * items;
-            if (u0 < at + n) break;
-            at += n;
-        }
-        s_first = b;
-        s_off = at;
-    }
-    __syncthreads();
 
     uint8_t *ring = smem + warp * S::kWarpBytes;
     const uint32_t ring_u = smem_u32(ring);
@@ -224,8 +134,8 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
 
     // ---- copies: they run kStages - 1 strips ahead, across the ends of pieces. The
     // page of this lane's token (lanes 16..31 repeat 0..15) is read a strip earlier.
-    Pieces ahead{u0, u1, s_off, s_first};
-    bool more = ahead.next(p, items);
+    PagedSplit::Pieces ahead = sh.pieces();
+    bool more = ahead.next(lens, items);
     int tile = ahead.tile0, page = 0;
     auto page_of = [&] {
         const int t = tile * kTile + warp * kStrip + (lane & 15);
@@ -240,7 +150,7 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
             const int kv = ahead.item / chunks;
             int pg = page;
             if (++tile == ahead.tile1) {
-                more = ahead.next(p, items);
+                more = ahead.next(lens, items);
                 tile = ahead.tile0;
             }
             page_of();
@@ -273,9 +183,9 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
 #pragma unroll 1
     for (int s = 0; s < kStages - 1; ++s) load();
 
-    Pieces w{u0, u1, s_off, s_first};
+    PagedSplit::Pieces w = sh.pieces();
     int taken = 0;   // strips
-    while (w.next(p, items)) {
+    while (w.next(lens, items)) {
         const int kv = w.item / chunks, head0 = kv * group + w.item % chunks * S::kHeads;
         const int heads = min(S::kHeads, group - w.item % chunks * S::kHeads);
         // ---- Q^T fragments: k = channel, n = head
@@ -439,8 +349,8 @@ paged_kernel(PagedParams p, float *slots, int *arrived) {
         }
         if (!whole) {
             // ---- the last CTA of this (sequence, item) to arrive joins the pieces
-            const int c0 = owner(w.item_at + kItemCost, U, G),
-                      c1 = owner(w.item_at + kItemCost + w.tiles - 1, U, G);
+            const int c0 = PagedSplit::owner(w.item_at + kItemCost, U, G),
+                      c1 = PagedSplit::owner(w.item_at + kItemCost + w.tiles - 1, U, G);
             __syncthreads();   // (the slot is written)
             if (tid == 0) {
                 int *ctr = arrived + static_cast<int64_t>(w.b) * items + w.item;
@@ -557,7 +467,7 @@ cudaError_t launch_paged(const PagedParams &p, const CallContext &ctx, cudaStrea
     // units the lengths may come to; empty sequences need a CTA as well
     const int64_t most = p.max_pages * p.page_size;
     const int64_t units = static_cast<int64_t>(p.batch) * p.hkv *
-                          plan_heads(p.hq / p.hkv).chunks * units_of(most);
+                          plan_heads(p.hq / p.hkv).chunks * PagedSplit::units_of(most);
     const unsigned grid =
         static_cast<unsigned>(units < 1 ? 1 : units < kMaxCtas ? units : kMaxCtas);
     return with_shape(p, [&](auto s, auto kernel) {

@@ -96,7 +96,8 @@ def test_attention_of_equal_keys_is_the_mean():
     v = torch.randn(3, 4, 1, 64, generator=g).to(torch.float8_e4m3fn)
     k = torch.ones(3, 4, 1, 64).to(torch.float8_e4m3fn)
     vs = torch.tensor([[0.5], [2.0], [1.0]])
-    out, lse, _, _ = C.paged_attention(torch.ones(1, 2, 64), k, v, torch.ones(3, 1), vs,
+    out, lse, _, _, floor = C.paged_attention(torch.ones(1, 2, 64), k, v, torch.ones(3, 1), vs,
                                        torch.tensor([[2, 1]]), [6])
     rows = torch.cat([v[2].to(F64), 2 * v[1, :2].to(F64)])[:, 0]
     assert torch.allclose(out[0, 0], rows.mean(0)) and math.isclose(float(lse[0, 0]), 8 + math.log(6))
+    assert torch.allclose(floor[0, 0], 2 / 6 * torch.cat([v[2], v[1, :2]]).to(F64)[:, 0].abs().sum(0))

@@ -517,9 +517,12 @@ def cache_case(lens, Hq, Hkv, D, page, layout="page", seed=0, spread=3):
 
 
 def attention_close(out, lse, q, kc, vc, ks, vs, table, lens, scale=None):
-    ro, rl, size, reach = C.paged_attention(q, kc, vc, ks, vs, table, lens, scale)
-    # weights p carry the error of their score, at most 2^-18 of sum |q||k|
-    close(out, ro, size * (1 + 2.0 ** -6 * reach[..., None]), "out")
+    ro, rl, size, reach, floor = C.paged_attention(q, kc, vc, ks, vs, table, lens, scale)
+    # weights p carry the error of their score, at most 2^-18 of sum |q||k|; below 2^-16 of the
+    # largest (times the values' scales) they keep less than 16 bits: the last of four terms of
+    # e4m3, 32 times finer each and starting from 2^8, steps by 2^-9 / 32^3 / 2^8 = 2^-32, and half
+    # of that is lost (`close` allows 2^-12 of what it is given)
+    close(out, ro, size * (1 + 2.0 ** -6 * reach[..., None]) + 2.0 ** (12 - 33) * floor, "out")
     lse = lse.cpu().double()
     empty = torch.isinf(rl)
     assert torch.equal(torch.isinf(lse) & (lse < 0), empty)
