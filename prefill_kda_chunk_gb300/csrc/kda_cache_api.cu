@@ -397,6 +397,7 @@ kda_status kda_paged_decode_fp8(
                    v_scale_stride);
     p.q = q; p.hq = static_cast<int32_t>(Hq); p.scale = scale; p.out = out; p.lse = lse;
     p.stall = g_stall_paged8.load();
+    p.divide_by(static_cast<uint32_t>(page_size));
     const void *ptrs[] = {q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, out, lse};
     kda::CallContext ctx;
     const kda_status rc = begin(kda::kPaged8, ptrs, 9, stream, kda::paged8_workspace(p),

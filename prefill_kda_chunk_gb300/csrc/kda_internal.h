@@ -369,6 +369,18 @@ struct Paged8Params {
     void *out;                 // bf16 [B, Hq, D]
     float *lse;                // [B, Hq] or nullptr
     int stall;                 // test hook: tiles of a block that are copied
+    // t / page_size for 0 <= t < 2^31 as (t * mul) >> (31 + shift), 2^shift >= page_size
+    uint32_t mul, shift;
+    void divide_by(uint32_t size) {
+        for (shift = 0; (uint64_t(1) << shift) < size; ++shift) {
+        }
+        mul = static_cast<uint32_t>(((uint64_t(1) << (31 + shift)) + size - 1) / size);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ uint32_t page_of(uint32_t t) const {
+        return static_cast<uint32_t>((static_cast<uint64_t>(t) * mul) >> (31 + shift));
+    }
+#endif
 };
 cudaError_t configure_paged8();
 int64_t paged8_workspace(const Paged8Params &p);

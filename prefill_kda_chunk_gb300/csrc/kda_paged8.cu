@@ -31,6 +31,7 @@
 // that is not a whole item leaves its sums in the workspace, and the last block to
 // arrive joins them in the order of the blocks.
 
+#include <cuda.h>
 #include <cuda_fp8.h>
 #include <math_constants.h>
 
@@ -47,89 +48,97 @@ constexpr int kTile = 128;           // tokens
 constexpr int kItemCost = 2;         // start and end of an item, in tiles
 constexpr int kQTerms = 2, kPTerms = 4;
 constexpr float kFiner = 32.f;       // from one term to the next
-// Warps: two groups for the weights, one for the outputs (each of four: a warp reaches the
-// 32 lanes of tensor memory of its number modulo 4), then the copies, MMAs and queries.
-constexpr int kOutWarp = 8, kCopyWarp = 12, kMmaWarp = 16, kQueryWarp = 17;
-constexpr int kThreads = 18 * 32;
-constexpr int kCopyWarps = 4;
+constexpr unsigned long long kLandNs = 100000000;   // within which copies and products end
+// Warps: groups of four for the weights, then one for the outputs (a warp reaches the 32 lanes
+// of tensor memory of its number modulo 4), then one for each of the two products, one for
+// the queries, and those for the copies (with 16 heads fewer: a thread has more registers).
+constexpr int groups_of(int) { return 2; }
+constexpr int copy_warps(int heads, bool tma) { return tma && heads > 8 ? 2 : 4; }
+constexpr int threads_of(int heads, bool tma) { return 32 * (4 * groups_of(heads) + 7 + copy_warps(heads, tma)); }
 using Paged8Split = Split<kTile, kItemCost>;
 
 // H = 8 or 16 query heads of one key-value head are an item.
 template <int D, int H>
 struct Shape {
+    static constexpr int kHeads = H, kGroups = groups_of(H);
+    static constexpr int kOutWarp = 4 * kGroups, kMmaWarpS = kOutWarp + 4, kMmaWarpO = kMmaWarpS + 1,
+                         kQueryWarp = kMmaWarpO + 1, kCopyWarp = kQueryWarp + 1;
     static constexpr int kTileBytes = kTile * D;
-    static constexpr int kStages = D == 128 ? 6 : 10;
-    // Tiles on their way behind the one that is announced. A tile is announced when the one
-    // kAhead behind it has been asked for, and that one's place is free once the tile
-    // kStages in front of it is done, for which the next one has to be there as well:
-    // kAhead <= kStages - 2.
-    static constexpr int kAhead = kStages - 3;
+    // Places for tiles of K and of V: a tile's keys are done with when S is formed, its values
+    // only with O.
+    // (Even numbers where two warps take turns: a place is then one warp's.)
+    static constexpr int kKeys = D == 128 ? (H == 8 ? 6 : 5) : 10, kValues = D == 128 ? 6 : 12;
+    // Buffers of S, of P and O.
+    static constexpr int kSBufs = 4, kPBufs = H == 8 ? 4 : 3;
     static constexpr int kQRows = kQTerms * H, kPRows = kPTerms * H;
     // shared memory, from a 1024-byte boundary
-    static constexpr int kOffV = kTileBytes;                        // V behind K in a stage
-    static constexpr int kStage = 2 * kTileBytes;
-    static constexpr int kOffQ = kStages * kStage;                  // two buffers
-    static constexpr int kOffP = kOffQ + 2 * kQRows * D;            // two buffers
-    static constexpr int kOffSc = kOffP + 2 * kPRows * kTile;       // ks and vs of a stage's tokens
-    static constexpr int kOffMax = kOffSc + kStages * 2 * kTile * 4;    // [group][2][warp][2 H]
-    static constexpr int kOffStat = kOffMax + 2 * 2 * 4 * 2 * H * 4;    // [2][H]: the tile's maximum
-    static constexpr int kOffMul = kOffStat + 2 * H * 4;            // [2][H]: what a score is multiplied by
-    static constexpr int kOffSum = kOffMul + 2 * H * 4;             // [2][8 warps][H]
-    static constexpr int kOffTop = kOffSum + 2 * 8 * H * 4;         // [2][group][H]
-    static constexpr int kOffJoin = kOffTop + 2 * 2 * H * 4;        // [2][H]
-    static constexpr int kOffBar = kOffJoin + 2 * H * 4;
-    // tensor memory columns: S, then O, two buffers each
-    static constexpr int kTmO = 2 * kQRows;
-    static constexpr int kTmCols = 2 * (kQRows + kPRows) <= 128 ? 128 : 256;
+    static constexpr int kOffV = kKeys * kTileBytes;
+    static constexpr int kOffQ = kOffV + kValues * kTileBytes;      // two buffers
+    static constexpr int kOffP = kOffQ + 2 * kQRows * D;
+    static constexpr int kOffSc = kOffP + kPBufs * kPRows * kTile;  // ks and vs of a tile's tokens, by V's place
+    static constexpr int kOffMax = kOffSc + kValues * 2 * kTile * 4;    // [group][2][warp][2 H]
+    static constexpr int kOffStat = kOffMax + kGroups * 2 * 4 * 2 * H * 4;    // [kPBufs][H]: the tile's maximum
+    static constexpr int kOffMul = kOffStat + kPBufs * H * 4;       // [2][H]: what a score is multiplied by
+    static constexpr int kOffSum = kOffMul + 2 * H * 4;             // [2][weights' warps][H]
+    static constexpr int kOffTop = kOffSum + 2 * 4 * kGroups * H * 4;         // [2][group][H]
+    static constexpr int kOffJoin = kOffTop + 2 * kGroups * H * 4;        // [2][H]
+    static constexpr int kOffCast = kOffJoin + 2 * H * 4;           // [weights' warps][3][H]
+    static constexpr int kOffBar = kOffCast + 4 * kGroups * 3 * H * 4;
+    // tensor memory columns: S, then O
+    static constexpr int kTmO = kSBufs * kQRows;
+    static constexpr int kTmCols = kTmO + kPBufs * kPRows <= 256 ? 256 : 512;
     static constexpr int kSlot = H * (D + 3);                       // floats of one partial result
 };
 
-// Barriers, 8 bytes each.
-template <int kStages>
+// Barriers, 8 bytes each, and the arrivals that complete a phase of each.
+template <typename S, bool kTma>
 struct Bars {
+    static constexpr int kCopyWarps = copy_warps(S::kHeads, kTma);
     enum {
-        kFull, kEmpty = kFull + kStages, kQFull = kEmpty + kStages, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2,
-        kPFull = kSFull + 2, kOFull = kPFull + 2, kOEmpty = kOFull + 2, kMax = kOEmpty + 2, kLFull = kMax + 2,
-        kLEmpty = kLFull + 2, kJoin = kLEmpty + 2, kDrain, kCount
+        kKFull, kVFull = kKFull + S::kKeys, kKEmpty = kVFull + S::kValues, kVEmpty = kKEmpty + S::kKeys,
+        kQFull = kVEmpty + S::kValues, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2,
+        kSEmpty = kSFull + S::kSBufs, kPFull = kSEmpty + S::kSBufs, kOFull = kPFull + S::kPBufs, kOEmpty = kOFull + S::kPBufs,
+        kLFull = kOEmpty + S::kPBufs, kLEmpty = kLFull + 2, kDrain = kLEmpty + 2, kCount = kDrain + 2
     };
     static __device__ __forceinline__ int arrivals(int i) {
-        if (i < kEmpty) return kCopyWarps;
-        if (i < kQFull) return 1;
-        if (i < kQEmpty) return 1;
-        if (i < kSFull) return 9;       // the products of a piece, and the 8 warps that read kOffMul
-        if (i < kPFull) return 1;
-        if (i < kOFull) return 4;
+        if (i < kVFull) return kTma ? 1 : 32 * kCopyWarps;
+        if (i < kKEmpty) return kTma ? 1 : 33 * kCopyWarps;
+        if (i < kQEmpty) return 1;      // kKEmpty, kVEmpty, kQFull
+        if (i < kSFull) return 1 + 4 * S::kGroups;   // the products of a piece, and the warps that read kOffMul
+        if (i < kSEmpty) return 1;
+        if (i < kOFull) return 4;       // kSEmpty, kPFull
         if (i < kOEmpty) return 1;
-        if (i < kLFull) return 4;       // kOEmpty, kMax
-        if (i < kLEmpty) return 8;
-        return i < kDrain ? 4 : 1;      // kLEmpty, kJoin
+        if (i < kLFull) return 4;
+        if (i < kLEmpty) return 4 * S::kGroups;
+        return i < kDrain ? 4 : 1;
     }
 };
 
 template <int D, int H>
 constexpr int smem_bytes() {
-    return Shape<D, H>::kOffBar + 8 * Bars<Shape<D, H>::kStages>::kCount;
+    return Shape<D, H>::kOffBar + 8 * Bars<Shape<D, H>, true>::kCount;
 }
 
-// ---- descriptors: rows of D (K, V, Q) or 128 (P) bytes, 16-byte granules XOR-ed by the
-// row within 1024 (512, for 64-byte rows) bytes. Contiguous along K (K, Q, P) the stride
-// field is the step between groups of 8 rows; contiguous along M (V) the step between
-// groups of 8 tokens: the same number.
+// ---- descriptors: rows of 128, 64 or 32 bytes (K, V, Q: D; P: its terms and heads, a token
+// after the other), 16-byte granules XOR-ed by the row within each 8 rows. Contiguous
+// along K (K, Q) the stride field is the step between groups of 8 rows; contiguous along M
+// or N (V, P) the step between groups of 8 tokens: the same number.
 template <int kRow>
 __device__ __forceinline__ uint64_t desc(uint32_t saddr) {
-    constexpr uint32_t hi = ((8u * kRow) >> 4) | (1u << 14) | ((kRow == 128 ? 2u : 4u) << 29);
+    constexpr uint32_t hi = ((8u * kRow) >> 4) | (1u << 14) | ((kRow == 128 ? 2u : kRow == 64 ? 4u : 6u) << 29);
     return (static_cast<uint64_t>(hi) << 32) | ((saddr >> 4) & 0x3FFF) | (1u << 16);
 }
 template <int kRow>
 __device__ __forceinline__ int swizzled(int row, int granule) {
-    return row * kRow + ((kRow == 128 ? granule ^ (row & 7) : granule ^ ((row >> 1) & 3)) << 4);
+    const int x = kRow == 128 ? row & 7 : kRow == 64 ? (row >> 1) & 3 : (row >> 2) & 1;
+    return row * kRow + ((granule ^ x) << 4);
 }
 
 // e4m3 operands, fp32 accumulators.
 __host__ __device__ constexpr uint32_t idesc8(int M, int N) {
     return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-constexpr uint32_t kAMajor = 1u << 15;   // A contiguous along M
+constexpr uint32_t kAMajor = 1u << 15, kBMajor = 1u << 16;   // contiguous along M / N
 
 // The whole warp calls these, an elected lane issues.
 __device__ __forceinline__ void mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool acc) {
@@ -161,32 +170,85 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 __device__ __forceinline__ float finite_base(float m) { return m == -CUDART_INF_F ? 0.f : m; }
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t n) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int token, int head, int page,
+                                       uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(token), "r"(head), "r"(page), "r"(bar)
+        : "memory");
 }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+// An arrival once this thread's copies so far have landed.
+__device__ __forceinline__ void arrive_landed(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 
-// Two numbers of at most 256 as e4m3, the first in the low byte; what is left of them
-// (at most 8, half a step) times kFiner.
+// Sums over a warp's lanes of H values each: lanes 32 / H h .. get that of value h. Of two
+// lanes each keeps half of the values and hands over the other half.
+template <int H>
+__device__ __forceinline__ float lane_sums(float (&v)[H], int lane) {
+    int m = 16;
+#pragma unroll
+    for (int n = H / 2; n > 0; n >>= 1, m >>= 1) {
+        const bool upper = (lane & m) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float got = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + n], m);
+            v[i] = (upper ? v[i + n] : v[i]) + got;
+        }
+    }
+    for (; m > 0; m >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
+    return v[0];
+}
+
+// The four warps of a role.
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;\n" ::"r"(id) : "memory"); }
+
+// Two numbers of at most 256 as e4m3, the first in the low byte. Half a step, 8 at most, is
+// left of them.
+__device__ __forceinline__ uint32_t to_e4m3(float a, float b) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ __half2 from_e4m3(uint32_t t) {
+    return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(t), __NV_E4M3));
+}
+// ... and what the first term leaves, times kFiner.
 __device__ __forceinline__ uint32_t take8(float &a, float &b) {
-    const __nv_fp8x2_storage_t t = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(t, __NV_E4M3)));
-    a = (a - f.x) * kFiner;
-    b = (b - f.y) * kFiner;
+    const uint32_t t = to_e4m3(a, b);
+    const float2 f = __half22float2(from_e4m3(t));
+    add2(a, b, -f.x, -f.y);
+    mul2(a, b, kFiner, kFiner);
     return t;
+}
+// Four terms: behind the first, half precision's 11 bits hold what is left, and the three
+// others' 12 all of that.
+__device__ __forceinline__ void split4(float a, float b, uint32_t (&t)[kPTerms]) {
+    static_assert(kPTerms == 4, "");
+    t[0] = take8(a, b);
+    __half2 r = __floats2half2_rn(a, b);
+    const __half2 finer = __float2half2_rn(kFiner);
+#pragma unroll
+    for (int k = 1; k < kPTerms; ++k) {
+        t[k] = __nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);
+        if (k + 1 < kPTerms) r = __hmul2(__hsub2(r, from_e4m3(t[k])), finer);
+    }
 }
 
 __host__ __device__ __forceinline__ Lengths lengths_of(const Cache8 &c) {
     return {c.lens, c.max_pages * c.page_size, c.batch, c.pages > 0};
 }
 
-template <int D, int H>
-__global__ void __launch_bounds__(kThreads, 1) paged8_kernel(Paged8Params p, float *slots, int *arrived) {
+struct Paged8Maps {
+    CUtensorMap k, v;   // (channel, token, head, page), boxes of 2^shift tokens
+    int shift;
+};
+
+template <int D, int H, bool kTma>
+__global__ void __launch_bounds__(threads_of(H, kTma), 1)
+paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *slots, int *arrived) {
     using S = Shape<D, H>;
-    using B = Bars<S::kStages>;
+    using B = Bars<S, kTma>;
+    constexpr int kThreads = threads_of(H, kTma);
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last;
@@ -225,126 +287,186 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_kernel(Paged8Params p, flo
     tc::fence_after();
     const uint32_t tm = s_tmem;
 
-    // A bounded wait, the same for a whole warp. Once one has run out, all stop.
-    auto wait = [&](int i, int phase) -> bool {
-        bool ok = mbar_try_wait(bar(i), phase & 1);
-        if (!ok) {
+    // A bounded wait. Once one has run out none waits any more: all roles go through their
+    // tiles to the end, whatever they find there, so that every barrier and counter is
+    // arrived at as often as otherwise.
+    auto wait = [&](int i, int phase) {
+        if (!mbar_try_wait(bar(i), phase & 1)) {
             const unsigned long long t0 = globaltimer();
-            for (;;) {
+            while (*static_cast<volatile int *>(&s_abort) == 0) {
+                bool ok = false;
                 for (int k = 0; k < 32 && !ok; ++k) ok = mbar_try_wait(bar(i), phase & 1);
-                if (ok || *static_cast<volatile int *>(&s_abort) != 0) break;
+                if (ok) break;
                 if (globaltimer() - t0 > kWaitLimitNs) {
                     *static_cast<volatile int *>(&s_abort) = 1;
                     atomicOr(c.err, kErrTimeout);
-                    break;
                 }
             }
         }
-        return __all_sync(0xffffffffu, ok) != 0;
+        __syncwarp();
     };
     auto arrive = [&](int i) {   // one arrival per warp
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(i));
     };
 
+    // Nothing that a warp has issued is under way when tensor memory is given back.
+    auto drain = [&](int i) {
+        mma_commit(bar(B::kDrain + i));
+        mbar_wait(bar(B::kDrain + i), 0, kLandNs);
+    };
+
     Paged8Split::Pieces w = sh.pieces();
-    if (warp >= kCopyWarp && warp < kMmaWarp) {
-        // ------------------------------------------------------------- copies: 32 tokens each
-        constexpr int G16 = D / 16, R = 32 / G16;   // granules of a row, rows per instruction
-        const int first = 32 * (warp - kCopyWarp);
+    if (warp >= S::kCopyWarp) {
+        // ----------------------------------------------------------------------------- copies
+        // What a lane copies of a tile: 32 tokens of a warp, one each; or (kTma) boxes of tokens
+        // of one page, K's in one warp and V's in the next, the tiles in turns where there are
+        // two such pairs (a box takes a warp 80 clocks). Pages are read two tiles of the warp's
+        // ahead, their scales one.
+        const int cw = warp - S::kCopyWarp, turns = kTma ? B::kCopyWarps / 2 : 1, turn = kTma ? cw / 2 : 0;
+        const bool of_v = cw & 1;
+        const int offset = kTma ? (lane & 15) << maps.shift : 32 * cw + lane;
+        struct Place {
+            int tok0, len, kv, page, in;   // len: 0 behind the last tile
+            float ks, vs;
+        };
         bool more = w.next(lens, items);
-        int tile = w.tile0, page = 0, n = 0, said = 0;
-        auto page_of = [&] {   // (read a tile earlier)
-            const int t = tile * kTile + first + lane;
-            page = more && t < w.len ? __ldg(c.table + static_cast<int64_t>(w.b) * c.max_pages + t / c.page_size) : 0;
+        int tile = w.tile0;
+        auto step = [&](int by) {
+            for (int i = 0; i < by && more; ++i)
+                if (++tile == w.tile1) {
+                    more = w.next(lens, items);
+                    tile = w.tile0;
+                }
         };
-        page_of();
-        for (; more && n < p.stall; ++n) {
-            const int s = n % S::kStages;
-            if (n >= S::kStages && !wait(B::kEmpty + s, n / S::kStages - 1)) break;
-            const int tok0 = tile * kTile + first, t = tok0 + lane, len = w.len, kv = w.item / chunks;
-            int pg = page;
-            if (++tile == w.tile1) {
-                more = w.next(lens, items);
-                tile = w.tile0;
+        step(turn);
+        auto look = [&]() -> Place {
+            Place a{0, 0, 0, 0, 0, 0.f, 0.f};
+            if (!more) return a;
+            a.tok0 = tile * kTile;
+            a.len = w.len;
+            a.kv = w.item / chunks;
+            const int t = a.tok0 + offset, at = static_cast<int>(p.page_of(t));
+            a.in = t - at * c.page_size;
+            if (t < w.len && offset < kTile) a.page = __ldg(c.table + static_cast<int64_t>(w.b) * c.max_pages + at);
+            step(turns);
+            return a;
+        };
+        auto scales = [&](Place &a) {
+            if (a.tok0 + offset >= a.len || offset >= kTile) return;
+            if (static_cast<unsigned>(a.page) >= static_cast<unsigned>(c.pages)) {
+                atomicOr(c.err, kErrPage);
+                a.page = 0;
             }
-            page_of();
-            if (static_cast<unsigned>(pg) >= static_cast<unsigned>(c.pages)) {
-                if (t < len) atomicOr(c.err, kErrPage);
-                pg = 0;
-            }
-            const int64_t in = t % c.page_size;
-            const uint8_t *ka = c.k + pg * c.k_page + in * c.k_token + kv * c.k_head;
-            const uint8_t *va = c.v + pg * c.v_page + in * c.v_token + kv * c.v_head;
-            const uint32_t at = sb + s * S::kStage, sc = sb + S::kOffSc + (s * 2 * kTile + first + lane) * 4;
-            const int g = lane % G16;
-#pragma unroll
-            for (int i = 0; i < 32 / R; ++i) {
-                const int row = i * R + lane / G16;
-                const uint64_t kr = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(ka), row);
-                const uint64_t vr = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(va), row);
-                const uint32_t dst = at + swizzled<D>(first + row, g);
+            if (!kTma || (of_v && lane >= 16)) a.ks = __ldg(c.ks + a.page * c.ks_page + a.kv);
+            if (!kTma || (of_v && lane < 16)) a.vs = __ldg(c.vs + a.page * c.vs_page + a.kv);
+        };
+        Place now = look(), next = look();
+        scales(now);
+        int n = turn;
+        for (; now.len > 0 && n < p.stall; n += turns) {
+            const Place far = look();
+            scales(next);
+            const int ks = n % S::kKeys, vs = n % S::kValues;
+            if ((!kTma || !of_v) && n >= S::kKeys) wait(B::kKEmpty + ks, n / S::kKeys - 1);
+            if ((!kTma || of_v) && n >= S::kValues) wait(B::kVEmpty + vs, n / S::kValues - 1);
+            const uint32_t to_k = sb + ks * S::kTileBytes, to_v = sb + S::kOffV + vs * S::kTileBytes;
+            float *sc = reinterpret_cast<float *>(smem + S::kOffSc) + vs * 2 * kTile;
+            const int left = now.len - now.tok0;
+            if (kTma) {
+                const uint32_t full = bar(of_v ? B::kVFull + vs : B::kKFull + ks);
+                if (of_v && offset < kTile) sc[(lane < 16 ? kTile : 0) + (lane & 15)] = lane < 16 ? now.vs : now.ks;
+                __syncwarp();
+                if (lane == 0) {
+                    const int rows = 1 << maps.shift, most = left < kTile ? left : kTile;
+                    mbar_arrive_expect_tx(full, static_cast<uint32_t>(((most + rows - 1) >> maps.shift << maps.shift) * D));
+                }
+                __syncwarp();
+                // rows past the end come with the box: those of V are zeroed with the weights
+                if (lane < 16 && offset < left && offset < kTile)
+                    tma_4d((of_v ? to_v : to_k) + offset * D, of_v ? &maps.v : &maps.k, now.in, now.kv, now.page, full);
+                __syncwarp();
+            } else {
+                constexpr int G16 = D / 16, R = 32 / G16;   // granules of a row, rows per instruction
+                const int g = lane % G16, first = offset - lane;
                 // rows past the end are zeros: whatever the page holds there stays unread
-                const uint32_t bytes = tok0 + row < len ? 16 : 0;
-                cp_async16(dst, reinterpret_cast<const uint8_t *>(kr) + 16 * g, bytes);
-                cp_async16(dst + S::kOffV, reinterpret_cast<const uint8_t *>(vr) + 16 * g, bytes);
-            }
-            const uint32_t four = t < len ? 4 : 0;
-            cp_async4(sc, c.ks + pg * c.ks_page + kv, four);
-            cp_async4(sc + 4 * kTile, c.vs + pg * c.vs_page + kv, four);
-            cp_async_commit();
-            if (n >= S::kAhead) {
-                cp_async_wait<S::kAhead>();
-                fence_async();
-                arrive(B::kFull + said++ % S::kStages);
-            }
-        }
-        cp_async_wait<0>();
-        fence_async();
-        for (; said < n; ++said) arrive(B::kFull + said % S::kStages);
-    } else if (warp == kMmaWarp) {
-        // ----------------------------------------------------------------------- the products
-        constexpr uint32_t kIdS = idesc8(kTile, S::kQRows), kIdO = idesc8(D, S::kPRows) | kAMajor;
-        int n = 0, pc = 0;
-        bool ok = true;
-        auto out = [&](int m) {   // O^T of tile m
-            if (!wait(B::kPFull + (m & 1), m >> 1)) return false;
-            tc::fence_after();
-            const uint64_t v = desc<D>(sb + m % S::kStages * S::kStage + S::kOffV);
-            const uint64_t q = desc<128>(sb + S::kOffP + (m & 1) * S::kPRows * kTile);
+                auto copy = [&](const uint8_t *from, uint32_t to) {
 #pragma unroll
-            for (int k = 0; k < kTile / 32; ++k)   // 32 tokens
-                mma8(tm + S::kTmO + (m & 1) * S::kPRows, v + k * (32 * D >> 4), q + k * (32 >> 4), kIdO, k > 0);
-            mma_commit(bar(B::kOFull + (m & 1)));
-            mma_commit(bar(B::kEmpty + m % S::kStages));
-            return true;
-        };
-        for (; ok && w.next(lens, items); ++pc) {
-            ok = wait(B::kQFull + (pc & 1), pc >> 1);
-            for (int tile = w.tile0; ok && tile < w.tile1; ++tile, ++n) {
-                // (S's buffer is free: the weights of tile n - 2 are there, see `out`)
-                if (!(ok = wait(B::kFull + n % S::kStages, n / S::kStages))) break;
+                    for (int i = 0; i < 32 / R; ++i) {
+                        const int row = i * R + lane / G16;
+                        const uint64_t src = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(from), row);
+                        cp_async16(to + swizzled<D>(first + row, g), reinterpret_cast<const uint8_t *>(src) + 16 * g,
+                                   first + row < left ? 16 : 0);
+                    }
+                };
+                copy(c.k + now.page * c.k_page + now.in * c.k_token + now.kv * c.k_head, to_k);
+                arrive_landed(bar(B::kKFull + ks));
+                copy(c.v + now.page * c.v_page + now.in * c.v_token + now.kv * c.v_head, to_v);
+                arrive_landed(bar(B::kVFull + vs));
+                sc[offset] = now.ks;
+                sc[kTile + offset] = now.vs;
+                arrive(B::kVFull + vs);
+            }
+            now = next;
+            next = far;
+        }
+        // the last copies land before the block ends, whatever the others do
+        cp_async_wait_all();
+        if (kTma) {
+            const int places = of_v ? S::kValues : S::kKeys, first = of_v ? B::kVFull : B::kKFull;
+            for (int j = turn; j < n; j += turns)
+                if (j + places >= n) mbar_wait(bar(first + j % places), j / places & 1, kLandNs);
+        }
+    } else if (warp == S::kMmaWarpS) {
+        // ------------------------------------------------------------------------- S^T = K Q^T
+        constexpr uint32_t kId = idesc8(kTile, S::kQRows);
+        int n = 0;
+        for (int pc = 0; w.next(lens, items); ++pc) {
+            wait(B::kQFull + (pc & 1), pc >> 1);
+            const uint64_t q = desc<D>(sb + S::kOffQ + (pc & 1) * S::kQRows * D);
+            for (int tile = w.tile0; tile < w.tile1; ++tile, ++n) {
+                const int b = n % S::kSBufs;
+                if (n >= S::kSBufs) wait(B::kSEmpty + b, n / S::kSBufs - 1);
+                wait(B::kKFull + n % S::kKeys, n / S::kKeys);
+                fence_async();   // (the threads' copies were ordinary writes)
                 tc::fence_after();
-                const uint64_t k8 = desc<D>(sb + n % S::kStages * S::kStage);
-                const uint64_t q = desc<D>(sb + S::kOffQ + (pc & 1) * S::kQRows * D);
+                const uint64_t k8 = desc<D>(sb + n % S::kKeys * S::kTileBytes);
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k)   // 32 channels
-                    mma8(tm + (n & 1) * S::kQRows, k8 + k * (32 >> 4), q + k * (32 >> 4), kIdS, k > 0);
-                mma_commit(bar(B::kSFull + (n & 1)));
+                    mma8(tm + b * S::kQRows, k8 + k * (32 >> 4), q + k * (32 >> 4), kId, k > 0);
+                mma_commit(bar(B::kSFull + b));
+                mma_commit(bar(B::kKEmpty + n % S::kKeys));
                 if (tile + 1 == w.tile1) mma_commit(bar(B::kQEmpty + (pc & 1)));
-                if (n > 0) ok = out(n - 1);
             }
         }
-        if (ok && n > 0) out(n - 1);
-        // nothing is under way when tensor memory is given back
-        mma_commit(bar(B::kDrain));
-        for (int k = 0; k < 1000000 && !mbar_try_wait(bar(B::kDrain), 0); ++k) {
+        drain(0);
+    } else if (warp == S::kMmaWarpO) {
+        // ------------------------------------------------------------------------ O^T = V^T P^T
+        constexpr uint32_t kId = idesc8(D, S::kPRows) | kAMajor | kBMajor;
+        int n = 0;
+        while (w.next(lens, items)) {
+            for (int tile = w.tile0; tile < w.tile1; ++tile, ++n) {
+                const int b = n % S::kPBufs, vs = n % S::kValues;
+                // (the weights are there: so are the values, and O's buffer is free)
+                wait(B::kVFull + vs, n / S::kValues);
+                wait(B::kPFull + b, n / S::kPBufs);
+                fence_async();
+                tc::fence_after();
+                const uint64_t v = desc<D>(sb + S::kOffV + vs * S::kTileBytes);
+                const uint64_t q = desc<S::kPRows>(sb + S::kOffP + b * S::kPRows * kTile);
+#pragma unroll
+                for (int k = 0; k < kTile / 32; ++k)   // 32 tokens
+                    mma8(tm + S::kTmO + b * S::kPRows, v + k * (32 * D >> 4), q + k * (32 * S::kPRows >> 4), kId, k > 0);
+                mma_commit(bar(B::kOFull + b));
+                mma_commit(bar(B::kVEmpty + vs));
+            }
         }
-    } else if (warp == kQueryWarp) {
+        drain(1);
+    } else if (warp == S::kQueryWarp) {
         // ------------------------------------------------------------------------ the queries
         constexpr int kPer = D / 32;   // channels of a lane
         for (int pc = 0; w.next(lens, items); ++pc) {
-            if (pc >= 2 && !wait(B::kQEmpty + (pc & 1), (pc >> 1) - 1)) break;
+            if (pc >= 2) wait(B::kQEmpty + (pc & 1), (pc >> 1) - 1);
             const int kv = w.item / chunks, head0 = kv * group + w.item % chunks * H;
             const int heads = min(H, group - w.item % chunks * H);
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
@@ -384,15 +506,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_kernel(Paged8Params p, flo
             fence_async();
             arrive(B::kQFull + (pc & 1));
         }
-    } else if (warp < kOutWarp) {
+    } else if (warp < S::kOutWarp) {
         // --------------------------------------------------- the weights; a thread has a token
         const int g = warp >> 2, q = warp & 3, t = 32 * q + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
         float *maxima = reinterpret_cast<float *>(smem + S::kOffMax) + g * 2 * 4 * 2 * H;
-        int n = 0, taken = 0;
-        bool ok = true;
-        for (int pc = 0; ok && w.next(lens, items); ++pc) {
-            if (!(ok = wait(B::kQFull + (pc & 1), pc >> 1))) break;
+        float *cast = reinterpret_cast<float *>(smem + S::kOffCast) + warp * 3 * H;
+        int n = 0;
+        for (int pc = 0; w.next(lens, items); ++pc) {
+            wait(B::kQFull + (pc & 1), pc >> 1);
             float mul[H], l[H], top = -CUDART_INF_F;   // top: lane h has head h's
 #pragma unroll
             for (int h = 0; h < H; ++h) {
@@ -401,17 +523,27 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_kernel(Paged8Params p, flo
             }
             arrive(B::kQEmpty + (pc & 1));
             for (int tile = w.tile0; tile < w.tile1; ++tile, ++n) {
-                if ((n & 1) != g) continue;
-                const int s = n % S::kStages, b = n & 1;
-                if (!(ok = wait(B::kFull + s, n / S::kStages)) || !(ok = wait(B::kSFull + b, n >> 1))) break;
+                if (n % S::kGroups != g) continue;
+                const int vs = n % S::kValues, b = n % S::kPBufs, sbuf = n % S::kSBufs;
+                wait(B::kVFull + vs, n / S::kValues);
+                wait(B::kSFull + sbuf, n / S::kSBufs);
                 tc::fence_after();
-                const float *sc = reinterpret_cast<const float *>(smem + S::kOffSc) + s * 2 * kTile + t;
-                const float ks = sc[0], lv = __log2f(sc[kTile]);
+                const float *sc = reinterpret_cast<const float *>(smem + S::kOffSc) + vs * 2 * kTile + (kTma ? t >> maps.shift : t);
+                const float ks = sc[0];
                 uint32_t raw[S::kQRows / 16][16];
 #pragma unroll
-                for (int i = 0; i < S::kQRows / 16; ++i) tc::ld16(tm + lanes + b * S::kQRows + 16 * i, raw[i]);
+                for (int i = 0; i < S::kQRows / 16; ++i) tc::ld16(tm + lanes + sbuf * S::kQRows + 16 * i, raw[i]);
                 tc::ld_wait();
+                tc::fence_before();
+                arrive(B::kSEmpty + sbuf);
                 const bool live = tile * kTile + t < w.len;
+                const float lv = live ? __log2f(sc[kTile]) : 0.f;
+                if (kTma && !live) {   // no weight of 0 makes an infinity or NaN vanish
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+                        *reinterpret_cast<uint4 *>(smem + S::kOffV + vs * S::kTileBytes + t * D + 16 * i) =
+                            make_uint4(0, 0, 0, 0);
+                }
                 float x[H];
 #pragma unroll
                 for (int h = 0; h < H; ++h) {
@@ -427,63 +559,59 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_kernel(Paged8Params p, flo
                     if (lane == h) mine = a;
                     if (lane == H + h) mine = v;
                 }
-                float *m = maxima + (taken & 1) * 4 * 2 * H;
+                float *m = maxima + (n / S::kGroups & 1) * 4 * 2 * H;
                 if (lane < 2 * H) m[q * 2 * H + lane] = mine;
-                arrive(B::kMax + g);
-                if (!(ok = wait(B::kMax + g, taken))) break;
-                ++taken;
-                if (n >= 2 && !(ok = wait(B::kOEmpty + b, (n >> 1) - 1))) break;
-                float base = 0.f, f = 0.f;
+                group_sync(1 + g);
+                if (n >= S::kPBufs) wait(B::kOEmpty + b, n / S::kPBufs - 1);
                 if (lane < 2 * H) {
                     const float all = fmaxf(fmaxf(m[lane], m[2 * H + lane]), fmaxf(m[4 * H + lane], m[6 * H + lane]));
                     if (lane < H) {
-                        const float now = fmaxf(top, all);
-                        base = finite_base(now);
-                        f = ex2(top - base);
+                        const float now = fmaxf(top, all), base = finite_base(now);
+                        cast[lane] = base;
+                        cast[H + lane] = ex2(top - base);
                         top = now;
                     } else {
-                        base = finite_base(all);
+                        cast[H + lane] = finite_base(all);
                         if (q == 0) reinterpret_cast<float *>(smem + S::kOffStat)[b * H + lane - H] = all;
                     }
                 }
+                __syncwarp();
+                uint32_t terms[kPTerms][H / 4];   // the token's row of P
+#pragma unroll
+                for (int h = 0; h < H; h += 4) {
+                    const float4 xb = *reinterpret_cast<const float4 *>(cast + h);
+                    const float4 fb = *reinterpret_cast<const float4 *>(cast + H + h);
+                    const float4 yb = *reinterpret_cast<const float4 *>(cast + 2 * H + h);
+                    const float xs[4] = {xb.x, xb.y, xb.z, xb.w}, fs[4] = {fb.x, fb.y, fb.z, fb.w},
+                                ys[4] = {yb.x, yb.y, yb.z, yb.w};
+                    float wt[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        l[h + j] = fmaf(l[h + j], fs[j], ex2(x[h + j] - xs[j]));
+                        wt[j] = ex2(x[h + j] + lv - ys[j]) * 256.f;   // e4m3 reaches 448
+                    }
+                    uint32_t lo[kPTerms], hi[kPTerms];
+                    split4(wt[0], wt[1], lo);
+                    split4(wt[2], wt[3], hi);
+#pragma unroll
+                    for (int k = 0; k < kPTerms; ++k) terms[k][h / 4] = lo[k] | (hi[k] << 16);
+                }
                 uint8_t *dst = smem + S::kOffP + b * S::kPRows * kTile;
 #pragma unroll
-                for (int h = 0; h < H; h += 2) {
-                    float wt[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float xb = __shfl_sync(0xffffffffu, base, h + j);
-                        const float fb = __shfl_sync(0xffffffffu, f, h + j);
-                        const float yb = __shfl_sync(0xffffffffu, base, H + h + j);
-                        l[h + j] = fmaf(l[h + j], fb, ex2(x[h + j] - xb));
-                        wt[j] = ex2(x[h + j] + lv - yb) * 256.f;   // e4m3 reaches 448
-                    }
-#pragma unroll
-                    for (int k = 0; k < kPTerms; ++k) {
-                        const uint32_t two = take8(wt[0], wt[1]);
-                        dst[swizzled<128>(k * H + h, t >> 4) + (t & 15)] = static_cast<uint8_t>(two);
-                        dst[swizzled<128>(k * H + h + 1, t >> 4) + (t & 15)] = static_cast<uint8_t>(two >> 8);
-                    }
+                for (int i = 0; i < S::kPRows / 16; ++i) {
+                    const uint32_t *from = &terms[0][0] + 4 * i;
+                    *reinterpret_cast<uint4 *>(dst + swizzled<S::kPRows>(t, i)) = make_uint4(from[0], from[1], from[2], from[3]);
                 }
                 fence_async();
-                tc::fence_before();
                 arrive(B::kPFull + b);
             }
-            if (!ok) break;
             // the piece's sums
-            if (pc >= 2 && !(ok = wait(B::kLEmpty + (pc & 1), (pc >> 1) - 1))) break;
-            float mine = 0.f;
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                float v = l[h];
-#pragma unroll
-                for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-                if (lane == h) mine = v;
-            }
-            if (lane < H) {
-                reinterpret_cast<float *>(smem + S::kOffSum)[((pc & 1) * 8 + warp) * H + lane] = mine;
-                if (q == 0) reinterpret_cast<float *>(smem + S::kOffTop)[((pc & 1) * 2 + g) * H + lane] = top;
-            }
+            if (pc >= 2) wait(B::kLEmpty + (pc & 1), (pc >> 1) - 1);
+            const float sum = lane_sums(l, lane);
+            const int h = lane * H / 32;
+            if (lane * H % 32 == 0)
+                reinterpret_cast<float *>(smem + S::kOffSum)[((pc & 1) * 4 * S::kGroups + warp) * H + h] = sum;
+            if (lane < H && q == 0) reinterpret_cast<float *>(smem + S::kOffTop)[((pc & 1) * S::kGroups + g) * H + lane] = top;
             arrive(B::kLFull + (pc & 1));
         }
     } else {
@@ -493,24 +621,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_kernel(Paged8Params p, flo
         const int d = D == 128 ? t : 16 * q + lane;
         const bool has = D == 128 || lane < 16;
         const uint32_t lanes = static_cast<uint32_t>(32 * q) << 16;
+        constexpr int kOutSync = 1 + S::kGroups;
         const int64_t U = sh.U, G = sh.G;
         const int me = blockIdx.x;
         float *join = reinterpret_cast<float *>(smem + S::kOffJoin);
-        int n = 0, joined = 0;
-        bool ok = true;
-        auto together = [&]() -> bool {   // the four warps
-            arrive(B::kJoin);
-            return wait(B::kJoin, joined++);
-        };
+        int n = 0;
         for (int pc = 0; w.next(lens, items); ++pc) {
             const int kv = w.item / chunks, head0 = kv * group + w.item % chunks * H;
             const int heads = min(H, group - w.item % chunks * H);
             float acc[H], top = -CUDART_INF_F;   // top: lane h has head h's
 #pragma unroll
             for (int h = 0; h < H; ++h) acc[h] = 0.f;
-            for (int tile = w.tile0; ok && tile < w.tile1; ++tile, ++n) {
-                const int b = n & 1;
-                if (!(ok = wait(B::kOFull + b, n >> 1))) break;
+            for (int tile = w.tile0; tile < w.tile1; ++tile, ++n) {
+                const int b = n % S::kPBufs;
+                wait(B::kOFull + b, n / S::kPBufs);
                 tc::fence_after();
                 uint32_t raw[S::kPRows / 16][16];
 #pragma unroll
@@ -541,16 +665,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_kernel(Paged8Params p, flo
             // of a block's partial pieces only its first can belong to an item that
             // started in front of its share, and only its last to another one
             float *slot = slots + static_cast<int64_t>(2 * me + (sh.u0 <= w.item_at)) * S::kSlot;
-            if (ok) ok = wait(B::kLFull + (pc & 1), pc >> 1);
-            if (ok) {
+            wait(B::kLFull + (pc & 1), pc >> 1);
+            {
                 float sum = 0.f, most = -CUDART_INF_F;
                 if (lane < H) {
-                    const float *ls = reinterpret_cast<const float *>(smem + S::kOffSum) + (pc & 1) * 8 * H + lane;
-                    const float *ms = reinterpret_cast<const float *>(smem + S::kOffTop) + (pc & 1) * 2 * H + lane;
-                    most = fmaxf(ms[0], ms[H]);
+                    const float *ls = reinterpret_cast<const float *>(smem + S::kOffSum) + (pc & 1) * 4 * S::kGroups * H + lane;
+                    const float *ms = reinterpret_cast<const float *>(smem + S::kOffTop) + (pc & 1) * S::kGroups * H + lane;
+#pragma unroll
+                    for (int g = 0; g < S::kGroups; ++g) most = fmaxf(most, ms[g * H]);
                     const float base = finite_base(most);
-                    sum = (ls[0] + ls[H] + ls[2 * H] + ls[3 * H]) * ex2(ms[0] - base) +
-                          (ls[4 * H] + ls[5 * H] + ls[6 * H] + ls[7 * H]) * ex2(ms[H] - base);
+#pragma unroll
+                    for (int g = 0; g < S::kGroups; ++g)
+                        sum = fmaf((ls[4 * g * H] + ls[(4 * g + 1) * H]) + (ls[(4 * g + 2) * H] + ls[(4 * g + 3) * H]),
+                                   ex2(ms[g * H] - base), sum);
                 }
                 arrive(B::kLEmpty + (pc & 1));
                 const int64_t row = static_cast<int64_t>(w.b) * p.hq + head0;
@@ -578,19 +705,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_kernel(Paged8Params p, flo
                 }
             }
             if (whole) continue;
-            // ---- the last block of this item to arrive joins the pieces. (The arrival is made
-            // even if a wait has run out: the counters stay right.)
+            // ---- the last block of this item to arrive joins the pieces
             const int c0 = Paged8Split::owner(w.item_at + kItemCost, U, G),
                       c1 = Paged8Split::owner(w.item_at + kItemCost + w.tiles - 1, U, G);
-            if (ok) ok = together();   // (the slot is written)
+            group_sync(kOutSync);   // (the slot is written)
             if (q == 0 && lane == 0) {
                 int *ctr = arrived + static_cast<int64_t>(w.b) * items + w.item;
                 const int before = add_acq_rel(ctr, 1);
                 s_last = before == c1 - c0;
                 if (s_last) *ctr = 0;   // for the next call
             }
-            if (ok) ok = together();
-            if (!ok || !*static_cast<volatile int *>(&s_last)) continue;
+            group_sync(kOutSync);
+            if (!*static_cast<volatile int *>(&s_last)) continue;
             const int last = c0 * U / G <= w.item_at;
             auto piece = [&](int k) { return slots + static_cast<int64_t>(2 * k + (k == c0 ? last : 0)) * S::kSlot; };
             for (int h = q; h < H; h += 4) {   // a warp per head: its maximum and sum
@@ -616,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_kernel(Paged8Params p, flo
                             sum == 0.f ? -CUDART_INF_F : base * 0.69314718055994531f + logf(sum);
                 }
             }
-            if (!(ok = together())) continue;
+            group_sync(kOutSync);
 #pragma unroll
             for (int h = 0; h < H; ++h) acc[h] = 0.f;
             for (int k = c0; k <= c1; ++k) {
@@ -643,14 +769,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged8_kernel(Paged8Params p, flo
 
 constexpr int heads_of(int group) { return group <= 8 ? 8 : 16; }
 
+// Pages of a multiple of 8 tokens are copied by the tensor memory accelerator, in boxes of
+// the largest power of two that divides them; others by threads, 16 bytes a time (131072 x 2
+// tokens, pages of 32: FIGURES).
+int box_rows(const Cache8 &c) {
+    const int two = c.page_size & -c.page_size;
+    return two < 8 ? 0 : two < kTile ? two : kTile;
+}
+
 template <typename F>
 auto with_shape(const Paged8Params &p, F &&go) {
-    const bool few = heads_of(p.hq / p.c.hkv) == 8;
+    const bool few = heads_of(p.hq / p.c.hkv) == 8, tma = box_rows(p.c) > 0;
+    auto pick = [&](auto s, auto bytes, auto with, auto without) { return go(s, tma ? with : without, bytes, threads_of(decltype(s)::kHeads, tma)); };
     if (p.c.dim == 64)
-        return few ? go(Shape<64, 8>(), paged8_kernel<64, 8>, smem_bytes<64, 8>())
-                   : go(Shape<64, 16>(), paged8_kernel<64, 16>, smem_bytes<64, 16>());
-    return few ? go(Shape<128, 8>(), paged8_kernel<128, 8>, smem_bytes<128, 8>())
-               : go(Shape<128, 16>(), paged8_kernel<128, 16>, smem_bytes<128, 16>());
+        return few ? pick(Shape<64, 8>(), smem_bytes<64, 8>(), paged8_kernel<64, 8, true>, paged8_kernel<64, 8, false>)
+                   : pick(Shape<64, 16>(), smem_bytes<64, 16>(), paged8_kernel<64, 16, true>, paged8_kernel<64, 16, false>);
+    return few ? pick(Shape<128, 8>(), smem_bytes<128, 8>(), paged8_kernel<128, 8, true>, paged8_kernel<128, 8, false>)
+               : pick(Shape<128, 16>(), smem_bytes<128, 16>(), paged8_kernel<128, 16, true>, paged8_kernel<128, 16, false>);
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool encode(CUtensorMap *m, const Cache8 &c, const uint8_t *base, int64_t page, int64_t token, int64_t head) {
+    const EncodeFn enc = reinterpret_cast<EncodeFn>(tensor_map_encoder());
+    if (enc == nullptr) return false;
+    // an axis of one row has no step of its own
+    const int64_t row = c.dim;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.page_size),
+                                static_cast<cuuint64_t>(c.hkv), static_cast<cuuint64_t>(c.pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.page_size > 1 ? token : row),
+                                   static_cast<cuuint64_t>(c.hkv > 1 ? head : row),
+                                   static_cast<cuuint64_t>(c.pages > 1 ? page : row)};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(c.dim), static_cast<cuuint32_t>(box_rows(c)), 1, 1},
+                     estr[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int64_t chunks_of(const Paged8Params &p) {
@@ -664,22 +820,24 @@ static_assert(smem_bytes<128, 16>() <= 232448 - 1024, "what a block can have");
 
 cudaError_t configure_paged8() {
     for (int dim : {64, 128})
-        for (int group : {1, 16}) {
-            Paged8Params p{};
-            p.c.dim = dim;
-            p.c.hkv = 1;
-            p.hq = group;
-            const cudaError_t e = with_shape(p, [](auto, auto kernel, int bytes) {
-                return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-            });
-            if (e != cudaSuccess) return e;
-        }
+        for (int group : {1, 16})
+            for (int page : {1, 16}) {
+                Paged8Params p{};
+                p.c.dim = dim;
+                p.c.page_size = page;
+                p.c.hkv = 1;
+                p.hq = group;
+                const cudaError_t e = with_shape(p, [](auto, auto kernel, int bytes, int) {
+                    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                });
+                if (e != cudaSuccess) return e;
+            }
     return cudaSuccess;
 }
 
 // Two partial results per block.
 int64_t paged8_workspace(const Paged8Params &p) {
-    return with_shape(p, [](auto s, auto, int) {
+    return with_shape(p, [](auto s, auto, int, int) {
         return static_cast<int64_t>(kPlannedSms) * 2 * decltype(s)::kSlot * 4;
     });
 }
@@ -694,8 +852,14 @@ cudaError_t launch_paged8(const Paged8Params &p, const CallContext &ctx, cudaStr
     const int64_t units = static_cast<int64_t>(p.c.batch) * p.c.hkv * chunks_of(p) *
                           Paged8Split::units_of(p.c.max_pages * p.c.page_size);
     const unsigned grid = static_cast<unsigned>(units < 1 ? 1 : units < kPlannedSms ? units : kPlannedSms);
-    return with_shape(p, [&](auto, auto kernel, int bytes) {
-        kernel<<<grid, kThreads, bytes, stream>>>(p, reinterpret_cast<float *>(ctx.ws), ctx.sync);
+    Paged8Maps maps{};
+    while (2 << maps.shift <= box_rows(p.c)) ++maps.shift;
+    if (box_rows(p.c) > 0 && p.c.pages > 0 &&
+        (!encode(&maps.k, p.c, p.c.k, p.c.k_page, p.c.k_token, p.c.k_head) ||
+         !encode(&maps.v, p.c, p.c.v, p.c.v_page, p.c.v_token, p.c.v_head)))
+        return cudaErrorInvalidValue;
+    return with_shape(p, [&](auto, auto kernel, int bytes, int threads) {
+        kernel<<<grid, threads, bytes, stream>>>(maps, p, reinterpret_cast<float *>(ctx.ws), ctx.sync);
         return cudaGetLastError();
     });
 }

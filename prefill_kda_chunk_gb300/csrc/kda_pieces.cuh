@@ -49,30 +49,32 @@ struct Split {
 
     // A block's way through its share [u, u1) of the units, piece by piece.
     struct Pieces {
-        int64_t u, u1, seq_at;   // next unit; end of the share; first unit of sequence b
-        int b;
+        int64_t u, u1;      // next unit; end of the share
+        int64_t at;         // first unit of item `coming` of sequence `seq`
+        int seq, coming, length;
         // the piece: its item, and the tiles of it
-        int len, tiles, item, tile0, tile1;
+        int b, item, len, tiles, tile0, tile1;
         int64_t item_at;
 
         __device__ __forceinline__ bool next(const Lengths &s, int items) {
             while (u < u1) {
-                bool ignore = false;
-                len = s.of(b, &ignore);
-                const int64_t units = units_of(len);
-                if (u >= seq_at + units * items) {
-                    seq_at += units * items;
-                    ++b;
+                const int64_t units = units_of(length);
+                if (units == 0 || coming == items) {
+                    bool ignore = false;
+                    length = s.of(++seq, &ignore);
+                    coming = 0;
                     continue;
                 }
+                b = seq;
+                item = coming++;
+                len = length;
                 tiles = static_cast<int>(units) - kCost;
-                item = static_cast<int>((u - seq_at) / units);
-                item_at = seq_at + item * units;
+                item_at = at;
                 const int64_t tile_at = item_at + kCost;
                 // the tiles among the units [u, min(u1, end of the item))
                 tile0 = static_cast<int>(u > tile_at ? u - tile_at : 0);
                 tile1 = static_cast<int>(u1 - tile_at < tiles ? u1 - tile_at : tiles);
-                u = item_at + units;
+                u = at = item_at + units;
                 if (tile0 < tile1) return true;
             }
             return false;
@@ -82,9 +84,9 @@ struct Split {
     // The batch's units and this block's share of them. All kThreads threads call it;
     // a wrong length is recorded by block 0. Blocks from G on have no share.
     struct Share {
-        int64_t U, G, u0, u1, seq_at;   // seq_at, b: where the share starts
-        int b;
-        __device__ __forceinline__ Pieces pieces() const { return {u0, u1, seq_at, b}; }
+        int64_t U, G, u0, u1, at;   // at, b, item: the item that the share starts in
+        int b, item, len;
+        __device__ __forceinline__ Pieces pieces() const { return {u0, u1, at, b, item, len}; }
     };
     template <int kThreads>
     static __device__ __forceinline__ Share share(const Lengths &s, int items, int *err) {
@@ -117,8 +119,8 @@ struct Split {
         r.U = U;
         r.G = U < gridDim.x ? U : gridDim.x;
         const int c = blockIdx.x;
-        r.u0 = r.u1 = r.seq_at = 0;
-        r.b = 0;
+        r.u0 = r.u1 = r.at = 0;
+        r.b = r.item = r.len = 0;
         if (c >= r.G) return r;   // (the whole block)
         r.u0 = c * U / r.G;
         r.u1 = (c + 1) * U / r.G;
@@ -135,8 +137,12 @@ struct Split {
             s_off = at;
         }
         __syncthreads();
+        bool ignore = false;
         r.b = s_first;
-        r.seq_at = s_off;
+        r.len = s.of(r.b, &ignore);
+        const int64_t units = units_of(r.len);
+        r.item = static_cast<int>((r.u0 - s_off) / units);
+        r.at = s_off + r.item * units;
         return r;
     }
 };
