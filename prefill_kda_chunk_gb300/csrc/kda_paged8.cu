@@ -51,10 +51,11 @@ constexpr float kFiner = 32.f;       // from one term to the next
 constexpr unsigned long long kLandNs = 100000000;   // within which copies and products end
 // Warps: groups of four for the weights, then one for the outputs (a warp reaches the 32 lanes
 // of tensor memory of its number modulo 4), then one for each of the two products, one for
-// the queries, and those for the copies (with 16 heads fewer: a thread has more registers).
+// the queries, and those for the copies. With 16 heads the second product's warp does the
+// queries too: no more than 16 warps, and a thread can have 128 registers.
 constexpr int groups_of(int) { return 2; }
 constexpr int copy_warps(int heads, bool tma) { return tma && heads > 8 ? 2 : 4; }
-constexpr int threads_of(int heads, bool tma) { return 32 * (4 * groups_of(heads) + 7 + copy_warps(heads, tma)); }
+constexpr int threads_of(int heads, bool tma) { return 32 * (4 * groups_of(heads) + (heads > 8 ? 6 : 7) + copy_warps(heads, tma)); }
 using Paged8Split = Split<kTile, kItemCost>;
 
 // H = 8 or 16 query heads of one key-value head are an item.
@@ -62,7 +63,7 @@ template <int D, int H>
 struct Shape {
     static constexpr int kHeads = H, kGroups = groups_of(H);
     static constexpr int kOutWarp = 4 * kGroups, kMmaWarpS = kOutWarp + 4, kMmaWarpO = kMmaWarpS + 1,
-                         kQueryWarp = kMmaWarpO + 1, kCopyWarp = kQueryWarp + 1;
+                         kQueryWarp = H > 8 ? kMmaWarpO : kMmaWarpO + 1, kCopyWarp = kQueryWarp + 1;
     static constexpr int kTileBytes = kTile * D;
     // Places for tiles of K and of V: a tile's keys are done with when S is formed, its values
     // only with O.
@@ -317,6 +318,49 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
     };
 
     Paged8Split::Pieces w = sh.pieces();
+    // The queries of piece pc, which is where w is, as two terms each.
+    auto queries = [&](int pc) {
+        constexpr int kPer = D / 32;   // channels of a lane
+        if (pc >= 2) wait(B::kQEmpty + (pc & 1), (pc >> 1) - 1);
+        const int kv = w.item / chunks, head0 = kv * group + w.item % chunks * H;
+        const int heads = min(H, group - w.item % chunks * H);
+        const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
+                                 (static_cast<int64_t>(w.b) * p.hq + head0) * D + kPer * lane;
+        uint32_t x[H][kPer / 2];
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int e = 0; e < kPer / 2; ++e)
+                x[h][e] = h < heads ? __ldg(reinterpret_cast<const uint32_t *>(q + h * D) + e) : 0u;
+        uint8_t *dst = smem + S::kOffQ + (pc & 1) * S::kQRows * D;
+        float mul = 0.f;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < kPer / 2; ++e) top = max(top, max(x[h][e] & 0x7fffu, (x[h][e] >> 16) & 0x7fffu));
+            top = __reduce_max_sync(0xffffffffu, top);
+            // 2^-k brings the row's largest channel below 2^8; an infinity or NaN makes its
+            // scores NaN
+            const int k = max(static_cast<int>(top >> 7) - 127 - 7, -126);
+            const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+            const float up = top >= 0x7f80u ? CUDART_NAN_F : __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+            if (lane == h) mul = p.scale * 1.44269504088896341f * up;
+#pragma unroll
+            for (int e = 0; e < kPer / 2; ++e) {
+                float a = __uint_as_float(x[h][e] << 16) * down, b = __uint_as_float(x[h][e] & 0xffff0000u) * down;
+#pragma unroll
+                for (int t = 0; t < kQTerms; ++t) {
+                    const int row = t * H + h, byte = kPer * lane + 2 * e;
+                    *reinterpret_cast<uint16_t *>(dst + swizzled<D>(row, byte >> 4) + (byte & 15)) =
+                        static_cast<uint16_t>(take8(a, b));
+                }
+            }
+        }
+        if (lane < H) reinterpret_cast<float *>(smem + S::kOffMul)[(pc & 1) * H + lane] = mul;
+        fence_async();
+        arrive(B::kQFull + (pc & 1));
+    };
     if (warp >= S::kCopyWarp) {
         // ----------------------------------------------------------------------------- copies
         // What a lane copies of a tile: 32 tokens of a warp, one each; or (kTma) boxes of tokens
@@ -443,9 +487,13 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
     } else if (warp == S::kMmaWarpO) {
         // ------------------------------------------------------------------------ O^T = V^T P^T
         constexpr uint32_t kId = idesc8(D, S::kPRows) | kAMajor | kBMajor;
+        constexpr bool kQueries = S::kQueryWarp == S::kMmaWarpO;
+        Paged8Split::Pieces now = w;
         int n = 0;
-        while (w.next(lens, items)) {
-            for (int tile = w.tile0; tile < w.tile1; ++tile, ++n) {
+        if (kQueries && w.next(lens, items)) queries(0);
+        for (int pc = 1; now.next(lens, items); ++pc) {
+            if (kQueries && w.next(lens, items)) queries(pc);   // (a piece ahead)
+            for (int tile = now.tile0; tile < now.tile1; ++tile, ++n) {
                 const int b = n % S::kPBufs, vs = n % S::kValues;
                 // (the weights are there: so are the values, and O's buffer is free)
                 wait(B::kVFull + vs, n / S::kValues);
@@ -463,49 +511,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         }
         drain(1);
     } else if (warp == S::kQueryWarp) {
-        // ------------------------------------------------------------------------ the queries
-        constexpr int kPer = D / 32;   // channels of a lane
-        for (int pc = 0; w.next(lens, items); ++pc) {
-            if (pc >= 2) wait(B::kQEmpty + (pc & 1), (pc >> 1) - 1);
-            const int kv = w.item / chunks, head0 = kv * group + w.item % chunks * H;
-            const int heads = min(H, group - w.item % chunks * H);
-            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
-                                     (static_cast<int64_t>(w.b) * p.hq + head0) * D + kPer * lane;
-            uint32_t x[H][kPer / 2];
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-#pragma unroll
-                for (int e = 0; e < kPer / 2; ++e)
-                    x[h][e] = h < heads ? __ldg(reinterpret_cast<const uint32_t *>(q + h * D) + e) : 0u;
-            uint8_t *dst = smem + S::kOffQ + (pc & 1) * S::kQRows * D;
-            float mul = 0.f;
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                uint32_t top = 0;
-#pragma unroll
-                for (int e = 0; e < kPer / 2; ++e) top = max(top, max(x[h][e] & 0x7fffu, (x[h][e] >> 16) & 0x7fffu));
-                top = __reduce_max_sync(0xffffffffu, top);
-                // 2^-k brings the row's largest channel below 2^8; an infinity or NaN makes its
-                // scores NaN
-                const int k = max(static_cast<int>(top >> 7) - 127 - 7, -126);
-                const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-                const float up = top >= 0x7f80u ? CUDART_NAN_F : __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-                if (lane == h) mul = p.scale * 1.44269504088896341f * up;
-#pragma unroll
-                for (int e = 0; e < kPer / 2; ++e) {
-                    float a = __uint_as_float(x[h][e] << 16) * down, b = __uint_as_float(x[h][e] & 0xffff0000u) * down;
-#pragma unroll
-                    for (int t = 0; t < kQTerms; ++t) {
-                        const int row = t * H + h, byte = kPer * lane + 2 * e;
-                        *reinterpret_cast<uint16_t *>(dst + swizzled<D>(row, byte >> 4) + (byte & 15)) =
-                            static_cast<uint16_t>(take8(a, b));
-                    }
-                }
-            }
-            if (lane < H) reinterpret_cast<float *>(smem + S::kOffMul)[(pc & 1) * H + lane] = mul;
-            fence_async();
-            arrive(B::kQFull + (pc & 1));
-        }
+        for (int pc = 0; w.next(lens, items); ++pc) queries(pc);
     } else if (warp < S::kOutWarp) {
         // --------------------------------------------------- the weights; a thread has a token
         const int g = warp >> 2, q = warp & 3, t = 32 * q + lane;
@@ -719,9 +725,14 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             if (!*static_cast<volatile int *>(&s_last)) continue;
             const int last = c0 * U / G <= w.item_at;
             auto piece = [&](int k) { return slots + static_cast<int64_t>(2 * k + (k == c0 ? last : 0)) * S::kSlot; };
-            for (int h = q; h < H; h += 4) {   // a warp per head: its maximum and sum
+            // The pieces' maxima and sums: a warp takes a quarter of the heads, so many pieces at
+            // a time as it has lanes for.
+            {
+                constexpr int kHs = H / 4, kPieces = 32 / kHs;
+                const int h = q * kHs + lane % kHs;
                 float most = -CUDART_INF_F, sum = 0.f;
-                for (int k = c0 + lane; k <= c1; k += 32) {
+#pragma unroll 2
+                for (int k = c0 + lane / kHs; k <= c1; k += kPieces) {
                     const float mk = __ldcg(piece(k) + H * (D + 1) + h), lk = __ldcg(piece(k) + H * (D + 2) + h);
                     const float now = fmaxf(most, mk), base = finite_base(now);
                     sum = fmaf(sum, ex2(most - base), lk * ex2(mk - base));
@@ -729,12 +740,12 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 }
                 float all = most;
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+                for (int o = 16; o >= kHs; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
                 const float base = finite_base(all);
                 sum *= ex2(most - base);
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (lane == 0) {
+                for (int o = 16; o >= kHs; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (lane < kHs) {
                     join[h] = base;
                     join[H + h] = sum;
                     if (h < heads && p.lse != nullptr)
@@ -745,12 +756,24 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             group_sync(kOutSync);
 #pragma unroll
             for (int h = 0; h < H; ++h) acc[h] = 0.f;
-            for (int k = c0; k <= c1; ++k) {
-                const float *src = piece(k);
-                const float by = lane < H ? ex2(finite_base(__ldcg(src + H * D + lane)) - join[lane]) : 0.f;
+            // 32 numbers on their way at a time
+            constexpr int kBatch = 32 / H;
+            for (int k0 = c0; k0 <= c1; k0 += kBatch) {
+                float by[kBatch], v[kBatch][H];
 #pragma unroll
-                for (int h = 0; h < H; ++h)
-                    acc[h] = fmaf(has ? __ldcg(src + h * D + d) : 0.f, __shfl_sync(0xffffffffu, by, h), acc[h]);
+                for (int i = 0; i < kBatch; ++i) {
+                    const bool is = k0 + i <= c1;
+                    const float *src = piece(is ? k0 + i : c0);
+                    by[i] = is && lane < H ? __ldcg(src + H * D + lane) : -CUDART_INF_F;
+#pragma unroll
+                    for (int h = 0; h < H; ++h) v[i][h] = is && has ? __ldcg(src + h * D + d) : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    by[i] = lane < H ? ex2(by[i] - join[lane]) : 0.f;
+#pragma unroll
+                    for (int h = 0; h < H; ++h) acc[h] = fmaf(v[i][h], __shfl_sync(0xffffffffu, by[i], h), acc[h]);
+                }
             }
 #pragma unroll
             for (int h = 0; h < H; ++h) {
