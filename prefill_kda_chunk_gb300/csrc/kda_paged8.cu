@@ -58,6 +58,15 @@ constexpr int copy_warps(int heads, bool tma) { return tma && heads > 8 ? 2 : 4;
 constexpr int threads_of(int heads, bool tma) { return 32 * (4 * groups_of(heads) + (heads > 8 ? 6 : 7) + copy_warps(heads, tma)); }
 using Paged8Split = Split<kTile, kItemCost>;
 
+// A piece of the block's share, as the queries' warp hands it to the other roles beside the
+// queries themselves (each going through the share by itself: 256 sequences of 1000 tokens
+// 119 us; this way FIGURE).
+struct alignas(16) Piece {
+    int tile0, tile1, len, tiles;   // tile1 = 0 behind the last one
+    int64_t row, item_at;           // of out; first unit
+    int b, item, heads, pad;
+};
+
 // H = 8 or 16 query heads of one key-value head are an item.
 template <int D, int H>
 struct Shape {
@@ -69,18 +78,19 @@ struct Shape {
     // only with O.
     // (Even numbers where two warps take turns: a place is then one warp's.)
     static constexpr int kKeys = D == 128 ? (H == 8 ? 6 : 5) : 10, kValues = D == 128 ? 6 : 12;
-    // Buffers of S, of P and O.
-    static constexpr int kSBufs = 4, kPBufs = H == 8 ? 4 : 3;
+    // Buffers of S, of P and O, of queries and pieces.
+    static constexpr int kSBufs = 4, kPBufs = H == 8 ? 4 : 3, kQBufs = H == 8 ? 4 : 3;
     static constexpr int kQRows = kQTerms * H, kPRows = kPTerms * H;
     // shared memory, from a 1024-byte boundary
     static constexpr int kOffV = kKeys * kTileBytes;
-    static constexpr int kOffQ = kOffV + kValues * kTileBytes;      // two buffers
-    static constexpr int kOffP = kOffQ + 2 * kQRows * D;
+    static constexpr int kOffQ = kOffV + kValues * kTileBytes;
+    static constexpr int kOffP = kOffQ + kQBufs * kQRows * D;
     static constexpr int kOffSc = kOffP + kPBufs * kPRows * kTile;  // ks and vs of a tile's tokens, by V's place
     static constexpr int kOffMax = kOffSc + kValues * 2 * kTile * 4;    // [group][2][warp][2 H]
     static constexpr int kOffStat = kOffMax + kGroups * 2 * 4 * 2 * H * 4;    // [kPBufs][H]: the tile's maximum
-    static constexpr int kOffMul = kOffStat + kPBufs * H * 4;       // [2][H]: what a score is multiplied by
-    static constexpr int kOffSum = kOffMul + 2 * H * 4;             // [2][weights' warps][H]
+    static constexpr int kOffMul = kOffStat + kPBufs * H * 4;       // [kQBufs][H]: what a score is multiplied by
+    static constexpr int kOffPiece = kOffMul + kQBufs * H * 4;      // [kQBufs]
+    static constexpr int kOffSum = kOffPiece + kQBufs * static_cast<int>(sizeof(Piece));   // [2][weights' warps][H]
     static constexpr int kOffTop = kOffSum + 2 * 4 * kGroups * H * 4;         // [2][group][H]
     static constexpr int kOffJoin = kOffTop + 2 * kGroups * H * 4;        // [2][H]
     static constexpr int kOffCast = kOffJoin + 2 * H * 4;           // [weights' warps][3][H]
@@ -97,7 +107,7 @@ struct Bars {
     static constexpr int kCopyWarps = copy_warps(S::kHeads, kTma);
     enum {
         kKFull, kVFull = kKFull + S::kKeys, kKEmpty = kVFull + S::kValues, kVEmpty = kKEmpty + S::kKeys,
-        kQFull = kVEmpty + S::kValues, kQEmpty = kQFull + 2, kSFull = kQEmpty + 2,
+        kQFull = kVEmpty + S::kValues, kQEmpty = kQFull + S::kQBufs, kSFull = kQEmpty + S::kQBufs,
         kSEmpty = kSFull + S::kSBufs, kPFull = kSEmpty + S::kSBufs, kOFull = kPFull + S::kPBufs, kOEmpty = kOFull + S::kPBufs,
         kLFull = kOEmpty + S::kPBufs, kLEmpty = kLFull + 2, kDrain = kLEmpty + 2, kCount = kDrain + 2
     };
@@ -105,7 +115,8 @@ struct Bars {
         if (i < kVFull) return kTma ? 1 : 32 * kCopyWarps;
         if (i < kKEmpty) return kTma ? 1 : 33 * kCopyWarps;
         if (i < kQEmpty) return 1;      // kKEmpty, kVEmpty, kQFull
-        if (i < kSFull) return 1 + 4 * S::kGroups;   // the products of a piece, and the warps that read kOffMul
+        // kQEmpty: the products of a piece, and the warps that have read what it is
+        if (i < kSFull) return 1 + 4 * S::kGroups + 4 + (S::kQueryWarp != S::kMmaWarpO);
         if (i < kSEmpty) return 1;
         if (i < kOFull) return 4;       // kSEmpty, kPFull
         if (i < kOEmpty) return 1;
@@ -204,6 +215,13 @@ __device__ __forceinline__ float lane_sums(float (&v)[H], int lane) {
 
 // The four warps of a role.
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;\n" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool group_any(int id, bool x) {
+    int any;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.s32 p, %2, 0;\n bar.red.or.pred q, %1, 128, p;\n selp.s32 %0, 1, 0, q;\n}\n"
+        : "=r"(any) : "r"(id), "r"(static_cast<int>(x)) : "memory");
+    return any != 0;
+}
 
 // Two numbers of at most 256 as e4m3, the first in the low byte. Half a step, 8 at most, is
 // left of them.
@@ -318,12 +336,25 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
     };
 
     Paged8Split::Pieces w = sh.pieces();
-    // The queries of piece pc, which is where w is, as two terms each.
-    auto queries = [&](int pc) {
+    auto stopped = [&] { return *static_cast<volatile int *>(&s_abort) != 0; };
+    // What piece pc is, where w is (or, if there are no more, the end), and its queries as two
+    // terms each.
+    auto queries = [&](int pc, bool more) {
         constexpr int kPer = D / 32;   // channels of a lane
-        if (pc >= 2) wait(B::kQEmpty + (pc & 1), (pc >> 1) - 1);
+        const int buf = pc % S::kQBufs;
+        if (pc >= S::kQBufs) wait(B::kQEmpty + buf, pc / S::kQBufs - 1);
+        if (stopped()) return;   // (others may still be reading)
+        Piece *piece = reinterpret_cast<Piece *>(smem + S::kOffPiece) + buf;
+        if (!more) {
+            if (lane == 0) piece->tile1 = 0;
+            arrive(B::kQFull + buf);
+            return;
+        }
         const int kv = w.item / chunks, head0 = kv * group + w.item % chunks * H;
         const int heads = min(H, group - w.item % chunks * H);
+        if (lane == 0)
+            *piece = {w.tile0, w.tile1, w.len, w.tiles, static_cast<int64_t>(w.b) * p.hq + head0, w.item_at,
+                      w.b, w.item, heads, 0};
         const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
                                  (static_cast<int64_t>(w.b) * p.hq + head0) * D + kPer * lane;
         uint32_t x[H][kPer / 2];
@@ -332,7 +363,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
 #pragma unroll
             for (int e = 0; e < kPer / 2; ++e)
                 x[h][e] = h < heads ? __ldg(reinterpret_cast<const uint32_t *>(q + h * D) + e) : 0u;
-        uint8_t *dst = smem + S::kOffQ + (pc & 1) * S::kQRows * D;
+        uint8_t *dst = smem + S::kOffQ + buf * S::kQRows * D;
         float mul = 0.f;
 #pragma unroll
         for (int h = 0; h < H; ++h) {
@@ -357,9 +388,14 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 }
             }
         }
-        if (lane < H) reinterpret_cast<float *>(smem + S::kOffMul)[(pc & 1) * H + lane] = mul;
+        if (lane < H) reinterpret_cast<float *>(smem + S::kOffMul)[buf * H + lane] = mul;
         fence_async();
-        arrive(B::kQFull + (pc & 1));
+        arrive(B::kQFull + buf);
+    };
+    // The piece pc; none, too, once a wait has run out.
+    auto piece_at = [&](int pc) -> const Piece & {
+        wait(B::kQFull + pc % S::kQBufs, pc / S::kQBufs);
+        return reinterpret_cast<const Piece *>(smem + S::kOffPiece)[pc % S::kQBufs];
     };
     if (warp >= S::kCopyWarp) {
         // ----------------------------------------------------------------------------- copies
@@ -465,10 +501,12 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         // ------------------------------------------------------------------------- S^T = K Q^T
         constexpr uint32_t kId = idesc8(kTile, S::kQRows);
         int n = 0;
-        for (int pc = 0; w.next(lens, items); ++pc) {
-            wait(B::kQFull + (pc & 1), pc >> 1);
-            const uint64_t q = desc<D>(sb + S::kOffQ + (pc & 1) * S::kQRows * D);
-            for (int tile = w.tile0; tile < w.tile1; ++tile, ++n) {
+        for (int pc = 0;; ++pc) {
+            const Piece &piece = piece_at(pc);
+            const int tile0 = piece.tile0, tile1 = piece.tile1;
+            if (tile1 == 0 || stopped()) break;
+            const uint64_t q = desc<D>(sb + S::kOffQ + pc % S::kQBufs * S::kQRows * D);
+            for (int tile = tile0; tile < tile1; ++tile, ++n) {
                 const int b = n % S::kSBufs;
                 if (n >= S::kSBufs) wait(B::kSEmpty + b, n / S::kSBufs - 1);
                 wait(B::kKFull + n % S::kKeys, n / S::kKeys);
@@ -480,7 +518,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                     mma8(tm + b * S::kQRows, k8 + k * (32 >> 4), q + k * (32 >> 4), kId, k > 0);
                 mma_commit(bar(B::kSFull + b));
                 mma_commit(bar(B::kKEmpty + n % S::kKeys));
-                if (tile + 1 == w.tile1) mma_commit(bar(B::kQEmpty + (pc & 1)));
+                if (tile + 1 == tile1) mma_commit(bar(B::kQEmpty + pc % S::kQBufs));
             }
         }
         drain(0);
@@ -488,12 +526,15 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         // ------------------------------------------------------------------------ O^T = V^T P^T
         constexpr uint32_t kId = idesc8(D, S::kPRows) | kAMajor | kBMajor;
         constexpr bool kQueries = S::kQueryWarp == S::kMmaWarpO;
-        Paged8Split::Pieces now = w;
+        if (kQueries) queries(0, w.next(lens, items));
         int n = 0;
-        if (kQueries && w.next(lens, items)) queries(0);
-        for (int pc = 1; now.next(lens, items); ++pc) {
-            if (kQueries && w.next(lens, items)) queries(pc);   // (a piece ahead)
-            for (int tile = now.tile0; tile < now.tile1; ++tile, ++n) {
+        for (int pc = 0;; ++pc) {
+            const Piece &piece = piece_at(pc);
+            const int count = piece.tile1 == 0 ? 0 : piece.tile1 - piece.tile0;
+            if (count == 0 || stopped()) break;
+            if (kQueries) queries(pc + 1, w.next(lens, items));   // (a piece ahead)
+            else arrive(B::kQEmpty + pc % S::kQBufs);
+            for (int i = 0; i < count; ++i, ++n) {
                 const int b = n % S::kPBufs, vs = n % S::kValues;
                 // (the weights are there: so are the values, and O's buffer is free)
                 wait(B::kVFull + vs, n / S::kValues);
@@ -511,7 +552,11 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         }
         drain(1);
     } else if (warp == S::kQueryWarp) {
-        for (int pc = 0; w.next(lens, items); ++pc) queries(pc);
+        bool more = true;
+        for (int pc = 0; more; ++pc) {
+            more = w.next(lens, items);
+            queries(pc, more);
+        }
     } else if (warp < S::kOutWarp) {
         // --------------------------------------------------- the weights; a thread has a token
         const int g = warp >> 2, q = warp & 3, t = 32 * q + lane;
@@ -519,16 +564,18 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         float *maxima = reinterpret_cast<float *>(smem + S::kOffMax) + g * 2 * 4 * 2 * H;
         float *cast = reinterpret_cast<float *>(smem + S::kOffCast) + warp * 3 * H;
         int n = 0;
-        for (int pc = 0; w.next(lens, items); ++pc) {
-            wait(B::kQFull + (pc & 1), pc >> 1);
+        for (int pc = 0;; ++pc) {
+            const Piece &piece = piece_at(pc);
+            const int tile0 = piece.tile0, tile1 = piece.tile1, len = piece.len;
+            if (group_any(1 + g, tile1 == 0 || stopped())) break;
             float mul[H], l[H], top = -CUDART_INF_F;   // top: lane h has head h's
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                mul[h] = reinterpret_cast<const float *>(smem + S::kOffMul)[(pc & 1) * H + h];
+                mul[h] = reinterpret_cast<const float *>(smem + S::kOffMul)[pc % S::kQBufs * H + h];
                 l[h] = 0.f;
             }
-            arrive(B::kQEmpty + (pc & 1));
-            for (int tile = w.tile0; tile < w.tile1; ++tile, ++n) {
+            arrive(B::kQEmpty + pc % S::kQBufs);
+            for (int tile = tile0; tile < tile1; ++tile, ++n) {
                 if (n % S::kGroups != g) continue;
                 const int vs = n % S::kValues, b = n % S::kPBufs, sbuf = n % S::kSBufs;
                 wait(B::kVFull + vs, n / S::kValues);
@@ -542,7 +589,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 tc::ld_wait();
                 tc::fence_before();
                 arrive(B::kSEmpty + sbuf);
-                const bool live = tile * kTile + t < w.len;
+                const bool live = tile * kTile + t < len;
                 const float lv = live ? __log2f(sc[kTile]) : 0.f;
                 if (kTma && !live) {   // no weight of 0 makes an infinity or NaN vanish
 #pragma unroll
@@ -632,13 +679,28 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         const int me = blockIdx.x;
         float *join = reinterpret_cast<float *>(smem + S::kOffJoin);
         int n = 0;
-        for (int pc = 0; w.next(lens, items); ++pc) {
-            const int kv = w.item / chunks, head0 = kv * group + w.item % chunks * H;
-            const int heads = min(H, group - w.item % chunks * H);
+        // One arrival at an item's counter for each of its pieces; the last finds it complete,
+        // and sets it back for the next call.
+        auto last_piece = [&](const Piece &piece, int c0, int c1) -> bool {
+            int *ctr = arrived + static_cast<int64_t>(piece.b) * items + piece.item;
+            const bool last = add_acq_rel(ctr, 1) == c1 - c0;
+            if (last) *ctr = 0;
+            return last;
+        };
+        auto owners = [&](const Piece &piece, int &c0, int &c1) {
+            c0 = Paged8Split::owner(piece.item_at + kItemCost, U, G);
+            c1 = Paged8Split::owner(piece.item_at + kItemCost + piece.tiles - 1, U, G);
+        };
+        int pc = 0;
+        for (;; ++pc) {
+            const Piece piece = piece_at(pc);
+            if (group_any(kOutSync, piece.tile1 == 0 || stopped())) break;
+            arrive(B::kQEmpty + pc % S::kQBufs);
+            const int heads = piece.heads;
             float acc[H], top = -CUDART_INF_F;   // top: lane h has head h's
 #pragma unroll
             for (int h = 0; h < H; ++h) acc[h] = 0.f;
-            for (int tile = w.tile0; tile < w.tile1; ++tile, ++n) {
+            for (int tile = piece.tile0; tile < piece.tile1; ++tile, ++n) {
                 const int b = n % S::kPBufs;
                 wait(B::kOFull + b, n / S::kPBufs);
                 tc::fence_after();
@@ -667,10 +729,10 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 }
             }
             // ---- the piece's end: lane h has the sum and maximum of head h
-            const bool whole = w.tile0 == 0 && w.tile1 == w.tiles;
+            const bool whole = piece.tile0 == 0 && piece.tile1 == piece.tiles;
             // of a block's partial pieces only its first can belong to an item that
             // started in front of its share, and only its last to another one
-            float *slot = slots + static_cast<int64_t>(2 * me + (sh.u0 <= w.item_at)) * S::kSlot;
+            float *slot = slots + static_cast<int64_t>(2 * me + (sh.u0 <= piece.item_at)) * S::kSlot;
             wait(B::kLFull + (pc & 1), pc >> 1);
             {
                 float sum = 0.f, most = -CUDART_INF_F;
@@ -686,7 +748,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                                    ex2(ms[g * H] - base), sum);
                 }
                 arrive(B::kLEmpty + (pc & 1));
-                const int64_t row = static_cast<int64_t>(w.b) * p.hq + head0;
+                const int64_t row = piece.row;
                 if (whole) {
                     const float mine = sum > 0.f ? ex2(finite_base(top) - finite_base(most)) / sum : sum == 0.f ? 0.f : sum;
 #pragma unroll
@@ -712,19 +774,14 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             }
             if (whole) continue;
             // ---- the last block of this item to arrive joins the pieces
-            const int c0 = Paged8Split::owner(w.item_at + kItemCost, U, G),
-                      c1 = Paged8Split::owner(w.item_at + kItemCost + w.tiles - 1, U, G);
+            int c0, c1;
+            owners(piece, c0, c1);
             group_sync(kOutSync);   // (the slot is written)
-            if (q == 0 && lane == 0) {
-                int *ctr = arrived + static_cast<int64_t>(w.b) * items + w.item;
-                const int before = add_acq_rel(ctr, 1);
-                s_last = before == c1 - c0;
-                if (s_last) *ctr = 0;   // for the next call
-            }
+            if (q == 0 && lane == 0) s_last = last_piece(piece, c0, c1);
             group_sync(kOutSync);
             if (!*static_cast<volatile int *>(&s_last)) continue;
-            const int last = c0 * U / G <= w.item_at;
-            auto piece = [&](int k) { return slots + static_cast<int64_t>(2 * k + (k == c0 ? last : 0)) * S::kSlot; };
+            const int last = c0 * U / G <= piece.item_at;
+            auto part = [&](int k) { return slots + static_cast<int64_t>(2 * k + (k == c0 ? last : 0)) * S::kSlot; };
             // The pieces' maxima and sums: a warp takes a quarter of the heads, so many pieces at
             // a time as it has lanes for.
             {
@@ -733,7 +790,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 float most = -CUDART_INF_F, sum = 0.f;
 #pragma unroll 2
                 for (int k = c0 + lane / kHs; k <= c1; k += kPieces) {
-                    const float mk = __ldcg(piece(k) + H * (D + 1) + h), lk = __ldcg(piece(k) + H * (D + 2) + h);
+                    const float mk = __ldcg(part(k) + H * (D + 1) + h), lk = __ldcg(part(k) + H * (D + 2) + h);
                     const float now = fmaxf(most, mk), base = finite_base(now);
                     sum = fmaf(sum, ex2(most - base), lk * ex2(mk - base));
                     most = now;
@@ -749,7 +806,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                     join[h] = base;
                     join[H + h] = sum;
                     if (h < heads && p.lse != nullptr)
-                        p.lse[static_cast<int64_t>(w.b) * p.hq + head0 + h] =
+                        p.lse[piece.row + h] =
                             sum == 0.f ? -CUDART_INF_F : base * 0.69314718055994531f + logf(sum);
                 }
             }
@@ -763,7 +820,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     const bool is = k0 + i <= c1;
-                    const float *src = piece(is ? k0 + i : c0);
+                    const float *src = part(is ? k0 + i : c0);
                     by[i] = is && lane < H ? __ldcg(src + H * D + lane) : -CUDART_INF_F;
 #pragma unroll
                     for (int h = 0; h < H; ++h) v[i][h] = is && has ? __ldcg(src + h * D + d) : 0.f;
@@ -779,11 +836,25 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             for (int h = 0; h < H; ++h) {
                 const float sum = join[H + h];
                 if (h < heads && has)
-                    static_cast<__nv_bfloat16 *>(p.out)[(static_cast<int64_t>(w.b) * p.hq + head0 + h) * D + d] =
+                    static_cast<__nv_bfloat16 *>(p.out)[(piece.row + h) * D + d] =
                         __float2bfloat16_rn(sum > 0.f ? acc[h] / sum : sum == 0.f ? 0.f : sum);
             }
             // (the next piece's join comes after barriers of its own: `join` is read by then)
         }
+        // Where a wait has run out, the arrivals for the pieces that are left, so that the counters
+        // are right for the next call.
+        if (q == 0 && lane == 0 && stopped())
+            for (int i = 0; w.next(lens, items); ++i) {
+                if (i < pc || (w.tile0 == 0 && w.tile1 == w.tiles)) continue;
+                Piece piece{};
+                piece.item_at = w.item_at;
+                piece.tiles = w.tiles;
+                piece.b = w.b;
+                piece.item = w.item;
+                int c0, c1;
+                owners(piece, c0, c1);
+                last_piece(piece, c0, c1);
+            }
     }
     tc::fence_before();
     __syncthreads();
