@@ -263,6 +263,7 @@ kda_status kda_qk_norm_rope(const void *q, const void *k, const float *q_weight,
     kda::CallContext ctx;
     const kda_status rc = begin(kda::kHeads, ptrs, 8, stream, 0, 0, &ctx);
     if (rc != KDA_OK) return rc;
+    p.err = ctx.err;
     return status(kda::launch_heads(p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -310,6 +311,7 @@ kda_status kda_qk_norm_rope_backward(
     const kda_status rc = begin(kda::kHeads, ptrs, 12, stream, kda::heads_workspace(p), 0, &ctx);
     if (rc != KDA_OK) return rc;
     p.partial = reinterpret_cast<float *>(ctx.ws);
+    p.err = ctx.err;
     return status(kda::launch_heads_backward(p, static_cast<cudaStream_t>(stream)));
 }
 

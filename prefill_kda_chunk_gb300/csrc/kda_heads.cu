@@ -5,10 +5,13 @@
 //   r = 1 / sqrt(mean(x^2) + eps),  y = R (x r w)
 //   g = R^T dy,  dw = sum g x r,  dx = r (g w - x r mean(g w x r))
 //
-// A head is a row; D / 8 lanes share it, 16 bytes of it each, so that a row is one
-// load, one store and a few shuffles. The angles are the same for all heads of a
-// token: a block takes rows of a few tokens and forms their sines and cosines once,
-// in shared memory.
+// D / 8 lanes share a head, 16 bytes of it each, and keep the same channels from head to
+// head: a warp takes some heads of one token with what a channel and its partner in the
+// rotation are multiplied by (weight times cosine and sine) in registers. The sines and
+// cosines of a token are formed once for them. Bound by reading and writing the heads.
+// These come through a ring of bulk copies of each warp's own, a batch of heads (contiguous in
+// a token) each, so that what is on its way takes no registers (batches in registers: the
+// 8192 tokens below 64 us, gradient 94).
 
 #include <type_traits>
 
@@ -19,14 +22,16 @@ namespace kda {
 
 namespace {
 
-constexpr int kHeadsThreads = 256;
-constexpr int kHeadsTokens = 8;      // tokens of a block's angles
-// rows of a lane group whose loads are on their way together
-constexpr int kAhead = 4;
+constexpr int kHeadsThreads = 256, kHeadsWarps = 8;
+constexpr int kRing = 3;                      // batches of a warp
+constexpr int kAhead = 4, kAheadGrad = 2;     // heads of a lane group in a batch
+constexpr int kHeadsBlocks = 2, kGradBlocksPerSm = 2;   // of an SM
 
 // cos and sin of position * f, where f turns by f / 2 pi a position. The turns are
 // formed as two floats (f / 2 pi to 2^-48, the position in two parts that fp32 holds
-// exactly, each product with its rounding error) and whole turns are dropped on the way.
+// exactly, each product with its rounding error) and whole turns are dropped on the way;
+// what is left, half a turn at most, is exact to some 2^-22 of a turn, and the hardware's sine
+// and cosine of it to 2^-20.
 __device__ __forceinline__ void angle(int pos, float f, float &c, float &s) {
     const float inv = 0.15915494f, inv_lo = 6.42063833e-9f;   // 1 / 2 pi
     const float hi = f * inv, lo = fmaf(f, inv, -hi) + f * inv_lo;
@@ -34,8 +39,9 @@ __device__ __forceinline__ void angle(int pos, float f, float &c, float &s) {
     const float a = p0 * hi, b = p1 * hi;
     float t = (a - rintf(a)) + (b - rintf(b));
     t += fmaf(p0, hi, -a) + fmaf(p1, hi, -b) + (p0 + p1) * lo;
-    t -= rintf(t);
-    sincospif(2.f * t, &s, &c);
+    t = (t - rintf(t)) * 6.2831853f;
+    c = __cosf(t);
+    s = __sinf(t);
 }
 
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
@@ -51,6 +57,16 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                       pack_bf16(x[6], x[7]));
 }
 
+// kN floats (4 or 8) from a 16-byte boundary
+template <int kN>
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < kN; i += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(p + i);
+        x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+    }
+}
+
 template <int kLanes>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
@@ -58,216 +74,362 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// Eight channels of a row turned by the token's angles, or back (sign = -1).
-// cs: the token's cosines, then its sines, rot / 2 each.
-template <bool kPairs>
-__device__ __forceinline__ void turn(float (&x)[8], const float *cs, int rot, int at, int lane, float sign) {
-    const int half = rot / 2;
-    if (kPairs) {
-        if (8 * at >= rot) return;
-        const float4 c = *reinterpret_cast<const float4 *>(cs + 4 * at);
-        const float4 s = *reinterpret_cast<const float4 *>(cs + half + 4 * at);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1], t = sign * ss[i];
-            x[2 * i] = fmaf(a, cc[i], -b * t);
-            x[2 * i + 1] = fmaf(b, cc[i], a * t);
-        }
-    } else {
-        const bool in = 8 * at < rot, low = 8 * at < half;
-        const int from = !in ? lane : low ? lane + rot / 16 : lane - rot / 16;
-        float other[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) other[i] = __shfl_sync(0xffffffffu, x[i], from);
-        if (!in) return;
-        const int f = low ? 8 * at : 8 * at - half;
-        const float sg = low ? -sign : sign;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float4 c = *reinterpret_cast<const float4 *>(cs + f + 4 * j);
-            const float4 s = *reinterpret_cast<const float4 *>(cs + half + f + 4 * j);
-            const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[4 * j + i] = fmaf(x[4 * j + i], cc[i], other[4 * j + i] * (sg * ss[i]));
-        }
-    }
-}
-
-// The sines and cosines of tokens [t0, t0 + n).
-__device__ __forceinline__ void fill_angles(const HeadsParams &p, float *cs, int64_t t0, int n) {
+// A token's cosines, then its sines, by the warp that needs them.
+__device__ __forceinline__ void fill_angles(const HeadsParams &p, float *cs, int pos) {
     const int half = p.rot / 2;
-    for (int i = threadIdx.x; i < n * half; i += kHeadsThreads) {
-        const int t = i / half, f = i % half;
+    __syncwarp();
+    for (int f = threadIdx.x & 31; f < half; f += 32) {
         float c, s;
-        angle(__ldg(p.pos + t0 + t), __ldg(p.freq + f), c, s);
-        cs[t * p.rot + f] = c;
-        cs[t * p.rot + half + f] = s;
+        angle(pos, __ldg(p.freq + f), c, s);
+        cs[f] = c;
+        cs[half + f] = s;
+    }
+    __syncwarp();
+}
+
+// Where the lane's channels stand in the rotation: (i, i + n) together, or (2i, 2i + 1).
+template <bool kPairs>
+struct Turn {
+    bool in, low;   // rotated at all; the first of the pair
+    int from;       // the lane that has the partners
+    int partner;    // their first channel
+    int f;          // first frequency
+    __device__ __forceinline__ Turn(int rot, int at, int lane) {
+        const int half = rot / 2;
+        in = 8 * at < rot;
+        low = 8 * at < half;
+        from = kPairs || !in ? lane : low ? lane + rot / 16 : lane - rot / 16;
+        partner = kPairs || !in ? 8 * at : low ? 8 * at + half : 8 * at - half;
+        f = kPairs ? 4 * at : low ? 8 * at : 8 * at - half;
+    }
+    // Cosines, and sines with the sign that the partner enters with, of the lane's channels.
+    __device__ __forceinline__ void angles(const float *cs, int rot, float (&c)[8], float (&s)[8]) const {
+        constexpr int kN = kPairs ? 4 : 8;
+        float cc[8], ss[8];
+        const int i = in ? f : 0;
+        load8<kN>(cs + i, cc);
+        load8<kN>(cs + rot / 2 + i, ss);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int j = kPairs ? e / 2 : e;
+            const bool first = kPairs ? e % 2 == 0 : low;
+            c[e] = in ? cc[j] : 1.f;
+            s[e] = in ? (first ? -ss[j] : ss[j]) : 0.f;
+        }
+    }
+    // The partners of eight packed channels.
+    __device__ __forceinline__ uint4 partners(const uint4 &u) const {
+        if (kPairs)
+            return make_uint4(__byte_perm(u.x, 0, 0x1032), __byte_perm(u.y, 0, 0x1032), __byte_perm(u.z, 0, 0x1032),
+                              __byte_perm(u.w, 0, 0x1032));
+        return make_uint4(__shfl_sync(0xffffffffu, u.x, from), __shfl_sync(0xffffffffu, u.y, from),
+                          __shfl_sync(0xffffffffu, u.z, from), __shfl_sync(0xffffffffu, u.w, from));
+    }
+    __device__ __forceinline__ void partners(const float (&x)[8], float (&o)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = kPairs ? x[e ^ 1] : __shfl_sync(0xffffffffu, x[e], from);
+    }
+};
+
+// The weights of queries and keys in shared memory (ones where there are none).
+template <int D>
+__device__ __forceinline__ void fill_weights(const HeadsParams &p, float *w) {
+    for (int i = threadIdx.x; i < D; i += kHeadsThreads) {
+        w[i] = p.qw != nullptr ? __ldg(p.qw + i) : 1.f;
+        w[D + i] = p.kw != nullptr ? __ldg(p.kw + i) : 1.f;
     }
 }
 
-__device__ __forceinline__ void weights8(const float *w, int at, float (&x)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = w != nullptr ? __ldg(w + 8 * at + i) : 1.f;
+// A warp's work: the heads [q0, q1) of the queries and [k0, k1) of the keys of every token it
+// comes to, in batches. Warp w of a block that takes 8 / parts tokens together has token
+// w / parts of them, and one part of its heads.
+struct Share {
+    int q0, q1, k0, k1;
+    int64_t token, step;   // (the first, and to the next)
+    __device__ __forceinline__ Share(const HeadsParams &p, int parts) {
+        const int w = threadIdx.x >> 5, part = w % parts, H = p.hq + p.hk, tokens = kHeadsWarps / parts;
+        const int a = part * H / parts, b = (part + 1) * H / parts;
+        q0 = min(a, p.hq);
+        q1 = min(b, p.hq);
+        k0 = max(a - p.hq, 0);
+        k1 = max(b - p.hq, 0);
+        token = static_cast<int64_t>(blockIdx.x) * tokens + w / parts;
+        step = static_cast<int64_t>(gridDim.x) * tokens;
+    }
+};
+
+// `step` heads, or what is left, from head h of the queries or keys of a token on.
+struct Batch {
+    int64_t token;
+    bool keys;
+    int h;
+    __device__ __forceinline__ explicit Batch(const Share &mine)
+        : token(mine.token), keys(mine.q0 >= mine.q1), h(keys ? mine.k0 : mine.q0) {}
+    __device__ __forceinline__ int end(const Share &mine) const { return keys ? mine.k1 : mine.q1; }
+    __device__ __forceinline__ void advance(const Share &mine, int step) {
+        h += step;
+        if (h < end(mine)) return;
+        if (!keys && mine.k0 < mine.k1) {
+            keys = true;
+            h = mine.k0;
+            return;
+        }
+        token += mine.step;
+        keys = mine.q0 >= mine.q1;
+        h = keys ? mine.k0 : mine.q0;
+    }
+};
+
+// A warp's ring: kRing places of kBytes, a barrier each.
+template <int kBytes>
+struct WarpRing {
+    uint32_t base, bars;
+    int n = 0;   // batches taken
+    __device__ __forceinline__ WarpRing(uint8_t *places, uint64_t *barriers) {
+        const int w = threadIdx.x >> 5;
+        base = smem_u32(places) + w * kRing * kBytes;
+        bars = smem_u32(barriers + w * kRing);
+        if ((threadIdx.x & 31) == 0)
+            for (int i = 0; i < kRing; ++i) mbar_init(bars + 8 * i, 1);
+        mbar_fence_init();
+        __syncwarp();
+    }
+    __device__ __forceinline__ uint32_t place(int i) const { return base + i % kRing * kBytes; }
+    __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * (i % kRing); }
+    __device__ __forceinline__ void wait(int *err) const {
+        if (!mbar_wait(bar(n), n / kRing & 1)) atomicOr(err, kErrTimeout);
+        __syncwarp();
+    }
+};
+
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
 }
 
-// Block b takes the rows (token, head) [b * rows, (b + 1) * rows), which lie in at most
-// kHeadsTokens + 1 tokens.
 template <int D, bool kPairs>
-__global__ void __launch_bounds__(kHeadsThreads) heads_kernel(HeadsParams p, int rows) {
-    constexpr int kLanes = D / 8, kGroups = kHeadsThreads / kLanes;
-    extern __shared__ __align__(16) float cs[];
-    const int lane = threadIdx.x & 31, at = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-    const int H = p.hq + p.hk;
-    const int64_t total = p.tokens * H, row0 = static_cast<int64_t>(blockIdx.x) * rows;
-    const int count = static_cast<int>(total - row0 < rows ? total - row0 : rows);
-    const int64_t t0 = row0 / H;
-    const int h0 = static_cast<int>(row0 - t0 * H);
-    if (p.rot > 0) {
-        fill_angles(p, cs, t0, (h0 + count - 1) / H + 1);
-        __syncthreads();
+__global__ void __launch_bounds__(kHeadsThreads, kHeadsBlocks) heads_kernel(HeadsParams p, int parts) {
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kStep = kRows * kAhead;
+    extern __shared__ __align__(128) uint8_t places[];   // the warps' rings, then the angles
+    __shared__ __align__(16) float weights[2 * D];
+    __shared__ uint64_t barriers[kHeadsWarps * kRing];
+    constexpr int kBytes = kStep * D * 2;
+    float *table = reinterpret_cast<float *>(places + kHeadsWarps * kRing * kBytes) + (threadIdx.x >> 5) * p.rot;
+    const int lane = threadIdx.x & 31, at = lane % kLanes, sub = lane / kLanes;
+    const Turn<kPairs> turn(p.rot, at, lane);
+    const Share mine(p, parts);
+    WarpRing<kBytes> ring(places, barriers);
+    auto ask = [&](const Batch &b, int i) {
+        if (b.token >= p.tokens || lane != 0) return;
+        const int rows = min(kStep, b.end(mine) - b.h);
+        const uint16_t *src = (b.keys ? static_cast<const uint16_t *>(p.k) + b.token * p.k_stride
+                                      : static_cast<const uint16_t *>(p.q) + b.token * p.q_stride) + b.h * D;
+        mbar_arrive_expect_tx(ring.bar(i), rows * D * 2);
+        bulk_g2s(ring.place(i), src, rows * D * 2, ring.bar(i));
+    };
+    Batch now(mine), ahead(mine);
+    for (int i = 0; i < kRing; ++i) {
+        ask(ahead, i);
+        ahead.advance(mine, kStep);
     }
-    float qw[8], kw[8];
-    weights8(p.qw, at, qw);
-    weights8(p.kw, at, kw);
-    for (int base = 0; base < count; base += kGroups * kAhead) {
-        uint4 in[kAhead];
-        int tok[kAhead], head[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int r = base + i * kGroups + group, near = r < count ? r : count - 1;
-            tok[i] = (h0 + near) / H;   // (lane groups past the end join in the shuffles)
-            head[i] = r < count ? h0 + r - tok[i] * H : -1;
-            in[i] = make_uint4(0, 0, 0, 0);
-            if (head[i] >= 0) {
-                const int64_t t = t0 + tok[i];
-                const uint16_t *src = head[i] < p.hq
-                    ? static_cast<const uint16_t *>(p.q) + t * p.q_stride + head[i] * D
-                    : static_cast<const uint16_t *>(p.k) + t * p.k_stride + (head[i] - p.hq) * D;
-                in[i] = *reinterpret_cast<const uint4 *>(src + 8 * at);
-            }
+    fill_weights<D>(p, weights);
+    __syncthreads();
+    int pos = p.rot > 0 && mine.token < p.tokens ? __ldg(p.pos + mine.token) : 0;
+    for (int64_t token = mine.token; token < p.tokens; token += mine.step) {
+        float c[8], s[8];
+        if (p.rot > 0) {
+            fill_angles(p, table, pos);
+            turn.angles(table, p.rot, c, s);
+            if (token + mine.step < p.tokens) pos = __ldg(p.pos + token + mine.step);
         }
+#pragma unroll 1
+        for (int keys = 0; keys < 2; ++keys) {
+            const int end = keys ? mine.k1 : mine.q1;
+            if ((keys ? mine.k0 : mine.q0) >= end) continue;
+            // y = (x a + partner b) r
+            float a[8], b[8];
+            load8<8>(weights + keys * D + 8 * at, a);
+            if (p.rot > 0) {
+                float w[8];
+                load8<8>(weights + keys * D + turn.partner, w);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (base + i * kGroups >= count) break;   // (the same for the whole block)
-            float x[8];
-            unpack8(in[i], x);
-            float sum = 0.f;
+                for (int e = 0; e < 8; ++e) b[e] = w[kPairs ? e ^ 1 : e];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
-            const float r = rsqrtf(row_sum<kLanes>(sum) * (1.f / D) + p.eps);
-            const bool is_q = head[i] < p.hq;
+                for (int e = 0; e < 8; e += 2) {
+                    mul2(a[e], a[e + 1], c[e], c[e + 1]);
+                    mul2(b[e], b[e + 1], s[e], s[e + 1]);
+                }
+            }
+            uint16_t *out = (keys ? static_cast<uint16_t *>(p.k_out) + token * p.ko_stride
+                                  : static_cast<uint16_t *>(p.q_out) + token * p.qo_stride) + sub * D + 8 * at;
+            while (now.token == token && now.keys == (keys != 0)) {
+                ring.wait(p.err);
+                const uint32_t from = ring.place(ring.n) + lane * 16;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= r * (is_q ? qw[e] : kw[e]);
-            if (p.rot > 0) turn<kPairs>(x, cs + tok[i] * p.rot, p.rot, at, lane, 1.f);
-            if (head[i] >= 0) {
-                const int64_t t = t0 + tok[i];
-                uint16_t *dst = is_q
-                    ? static_cast<uint16_t *>(p.q_out) + t * p.qo_stride + head[i] * D
-                    : static_cast<uint16_t *>(p.k_out) + t * p.ko_stride + (head[i] - p.hq) * D;
-                *reinterpret_cast<uint4 *>(dst + 8 * at) = pack8(x);
+                for (int i = 0; i < kAhead; ++i) {
+                    if (now.h + i * kRows >= end) break;   // (the whole warp)
+                    const uint4 in = lds16(from + i * 512);
+                    float x[8], sq[2] = {0.f, 0.f};
+                    unpack8(in, x);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) muladd2(sq[0], sq[1], x[e], x[e + 1], x[e], x[e + 1]);
+                    const float r = rsqrtf(row_sum<kLanes>(sq[0] + sq[1]) * (1.f / D) + p.eps);
+                    float o[8];
+                    if (p.rot > 0) unpack8(turn.partners(in), o);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        mul2(x[e], x[e + 1], a[e], a[e + 1]);
+                        if (p.rot > 0) muladd2(x[e], x[e + 1], o[e], o[e + 1], b[e], b[e + 1]);
+                        mul2(x[e], x[e + 1], r, r);
+                    }
+                    const int head = now.h + i * kRows;
+                    if (head + sub < end) *reinterpret_cast<uint4 *>(out + head * D) = pack8(x);
+                }
+                __syncwarp();
+                ask(ahead, ring.n);   // (the place just read)
+                ++ring.n;
+                now.advance(mine, kStep);
+                ahead.advance(mine, kStep);
             }
         }
     }
 }
 
-// Blocks of the gradient: each walks a run of rows, kHeadsTokens tokens' angles at a time,
-// and leaves its part of the weights' gradients.
-constexpr int kGradBlocks = 4 * kPlannedSms;
-
-__device__ __forceinline__ void load8(const void *p, int64_t i, bool f32, float (&x)[8]) {
-    if (f32) {
-        const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-        const float4 a = s[0], b = s[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
-        unpack8(*reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i), x);
-    }
-}
+// The gradient. With g = R^T dy, A = sum x^2, B = sum g w x over the channels:
+//   dw += r g x,  dx = r w g - (r^3 B / D) x
+// Blocks keep their parts of the weights' gradients in registers to the end.
+constexpr int kGradBlocks = kGradBlocksPerSm * kPlannedSms;
 
 template <int D, bool kPairs, bool kF32>
-__global__ void __launch_bounds__(kHeadsThreads) heads_backward_kernel(HeadsParams p) {
-    constexpr int kLanes = D / 8, kGroups = kHeadsThreads / kLanes;
-    extern __shared__ __align__(16) float cs[];
-    const int lane = threadIdx.x & 31, at = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-    const int H = p.hq + p.hk;
-    const int64_t total = p.tokens * H;
-    const int64_t row0 = total * blockIdx.x / gridDim.x, row1 = total * (blockIdx.x + 1) / gridDim.x;
-    float qw[8], kw[8], dqw[8], dkw[8];
-    weights8(p.qw, at, qw);
-    weights8(p.kw, at, kw);
+__global__ void __launch_bounds__(kHeadsThreads, kGradBlocksPerSm) heads_backward_kernel(HeadsParams p, int parts) {
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kStep = kRows * kAheadGrad, kSize = kF32 ? 4 : 2;
+    extern __shared__ __align__(128) uint8_t places[];   // the warps' rings, then the angles
+    __shared__ __align__(16) float weights[2 * D];
+    __shared__ uint64_t barriers[kHeadsWarps * kRing];
+    constexpr int kBytes = kStep * D * (2 + kSize), kOffY = kStep * D * 2;   // x, then dy
+    float *table = reinterpret_cast<float *>(places + kHeadsWarps * kRing * kBytes) + (threadIdx.x >> 5) * p.rot;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = lane % kLanes, sub = lane / kLanes;
+    const Turn<kPairs> turn(p.rot, at, lane);
+    const Share mine(p, parts);
+    WarpRing<kBytes> ring(places, barriers);
+    auto ask = [&](const Batch &b, int i) {
+        if (b.token >= p.tokens || lane != 0) return;
+        const int rows = min(kStep, b.end(mine) - b.h);
+        const uint16_t *x = (b.keys ? static_cast<const uint16_t *>(p.k) + b.token * p.k_stride
+                                    : static_cast<const uint16_t *>(p.q) + b.token * p.q_stride) + b.h * D;
+        const uint8_t *y = static_cast<const uint8_t *>(b.keys ? p.dk : p.dq) +
+                           (b.token * (b.keys ? p.dk_stride : p.dq_stride) + b.h * D) * kSize;
+        mbar_arrive_expect_tx(ring.bar(i), rows * D * (2 + kSize));
+        bulk_g2s(ring.place(i), x, rows * D * 2, ring.bar(i));
+        bulk_g2s(ring.place(i) + kOffY, y, rows * D * kSize, ring.bar(i));
+    };
+    Batch now(mine), ahead(mine);
+    for (int i = 0; i < kRing; ++i) {
+        ask(ahead, i);
+        ahead.advance(mine, kStep);
+    }
+    fill_weights<D>(p, weights);
+    __syncthreads();
+    float dqw[8], dkw[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) dqw[e] = dkw[e] = 0.f;
-    for (int64_t start = row0; start < row1;) {
-        const int64_t t0 = start / H;
-        const int h0 = static_cast<int>(start - t0 * H);
-        int64_t end = (t0 + kHeadsTokens) * H;
-        if (end > row1) end = row1;
-        const int count = static_cast<int>(end - start);
+    int pos = p.rot > 0 && mine.token < p.tokens ? __ldg(p.pos + mine.token) : 0;
+    for (int64_t token = mine.token; token < p.tokens; token += mine.step) {
+        float c[8], s[8];
         if (p.rot > 0) {
-            __syncthreads();
-            fill_angles(p, cs, t0, (h0 + count - 1) / H + 1);
-            __syncthreads();
+            fill_angles(p, table, pos);
+            turn.angles(table, p.rot, c, s);
+            if (token + mine.step < p.tokens) pos = __ldg(p.pos + token + mine.step);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = -s[e];   // (back)
         }
-        for (int base = 0; base < count; base += kGroups) {
-            const int r = base + group, near = r < count ? r : count - 1;
-            const int tok = (h0 + near) / H, head = r < count ? h0 + r - tok * H : -1;
-            const bool is_q = head < p.hq;
-            const int64_t t = t0 + tok;
-            float x[8], g[8];
-            if (head >= 0) {
-                load8(is_q ? p.q : p.k,
-                      (is_q ? t * p.q_stride + head * D : t * p.k_stride + (head - p.hq) * D) + 8 * at,
-                      false, x);
-                load8(is_q ? p.dq : p.dk,
-                      (is_q ? t * p.dq_stride + head * D : t * p.dk_stride + (head - p.hq) * D) + 8 * at,
-                      kF32, g);
-            } else {
+        auto run = [&](bool keys, int end, uint16_t *out, float (&dw)[8]) {
+            if (now.token != token || now.keys != keys) return;
+            float w[8];
+            load8<8>(weights + keys * D + 8 * at, w);
+            out += sub * D + 8 * at;
+            while (now.token == token && now.keys == keys) {
+                ring.wait(p.err);
+                const uint32_t from = ring.place(ring.n);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = g[e] = 0.f;
+                for (int i = 0; i < kAheadGrad; ++i) {
+                    if (now.h + i * kRows >= end) break;   // (the whole warp)
+                    const bool row = now.h + i * kRows + sub < end;
+                    float x[8], g[8], o[8];
+                    // (what lies behind the last head is an earlier batch's)
+                    uint4 u = lds16(from + i * 512 + lane * 16);
+                    if (!row) u = make_uint4(0, 0, 0, 0);
+                    unpack8(u, x);
+                    if (kF32) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint4 v = lds16(from + kOffY + i * 1024 + lane * 32 + 16 * j);
+                            g[4 * j] = __uint_as_float(v.x);
+                            g[4 * j + 1] = __uint_as_float(v.y);
+                            g[4 * j + 2] = __uint_as_float(v.z);
+                            g[4 * j + 3] = __uint_as_float(v.w);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) g[e] = row ? g[e] : 0.f;
+                        if (p.rot > 0) turn.partners(g, o);
+                    } else {
+                        u = lds16(from + kOffY + i * 512 + lane * 16);
+                        if (!row) u = make_uint4(0, 0, 0, 0);
+                        unpack8(u, g);
+                        if (p.rot > 0) unpack8(turn.partners(u), o);
+                    }
+                    float A[2] = {0.f, 0.f}, B[2] = {0.f, 0.f}, t[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        if (p.rot > 0) {
+                            mul2(g[e], g[e + 1], c[e], c[e + 1]);
+                            muladd2(g[e], g[e + 1], o[e], o[e + 1], s[e], s[e + 1]);
+                        }
+                        t[e] = g[e];
+                        t[e + 1] = g[e + 1];
+                        mul2(t[e], t[e + 1], x[e], x[e + 1]);
+                        muladd2(A[0], A[1], x[e], x[e + 1], x[e], x[e + 1]);
+                        muladd2(B[0], B[1], t[e], t[e + 1], w[e], w[e + 1]);
+                    }
+                    float a = A[0] + A[1], b = B[0] + B[1];
+#pragma unroll
+                    for (int m = kLanes / 2; m > 0; m >>= 1)
+                        add2(a, b, __shfl_xor_sync(0xffffffffu, a, m), __shfl_xor_sync(0xffffffffu, b, m));
+                    const float r = row ? rsqrtf(a * (1.f / D) + p.eps) : 0.f;
+                    const float k = -r * r * (r * b) * (1.f / D);
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        muladd2(dw[e], dw[e + 1], t[e], t[e + 1], r, r);
+                        mul2(g[e], g[e + 1], w[e], w[e + 1]);
+                        mul2(g[e], g[e + 1], r, r);
+                        muladd2(g[e], g[e + 1], x[e], x[e + 1], k, k);
+                    }
+                    if (row) *reinterpret_cast<uint4 *>(out + (now.h + i * kRows) * D) = pack8(g);
+                }
+                __syncwarp();
+                ask(ahead, ring.n);   // (the place just read)
+                ++ring.n;
+                now.advance(mine, kStep);
+                ahead.advance(mine, kStep);
             }
-            float sum = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
-            const float rr = rsqrtf(row_sum<kLanes>(sum) * (1.f / D) + p.eps);
-            if (p.rot > 0) turn<kPairs>(g, cs + tok * p.rot, p.rot, at, lane, -1.f);
-            float dot = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[e] *= rr;
-                const float part = head >= 0 ? g[e] * x[e] : 0.f;
-                if (is_q) dqw[e] += part;
-                else dkw[e] += part;
-                g[e] *= is_q ? qw[e] : kw[e];
-                dot = fmaf(g[e], x[e], dot);
-            }
-            dot = row_sum<kLanes>(dot) * (1.f / D);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = rr * fmaf(-x[e], dot, g[e]);
-            if (head >= 0) {
-                uint16_t *dst = is_q
-                    ? static_cast<uint16_t *>(p.q_out) + t * p.qo_stride + head * D
-                    : static_cast<uint16_t *>(p.k_out) + t * p.ko_stride + (head - p.hq) * D;
-                *reinterpret_cast<uint4 *>(dst + 8 * at) = pack8(x);
-            }
-        }
-        start = end;
+        };
+        run(false, mine.q1, static_cast<uint16_t *>(p.q_out) + token * p.qo_stride, dqw);
+        run(true, mine.k1, static_cast<uint16_t *>(p.k_out) + token * p.ko_stride, dkw);
     }
     if (p.dqw == nullptr && p.dkw == nullptr) return;
-    // the groups of a block, in order
-    __shared__ float part[2][kGroups][D];
+    // the lane groups of a block, in order
+    __shared__ float part[2][kHeadsWarps * kRows][D];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        part[0][group][8 * at + e] = dqw[e];
-        part[1][group][8 * at + e] = dkw[e];
+        part[0][warp * kRows + sub][8 * at + e] = dqw[e];
+        part[1][warp * kRows + sub][8 * at + e] = dkw[e];
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * D; i += kHeadsThreads) {
-        float s = 0.f;
-        for (int j = 0; j < kGroups; ++j) s += part[i / D][j][i % D];
-        p.partial[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = s;
+        float sum = 0.f;
+        for (int j = 0; j < kHeadsWarps * kRows; ++j) sum += part[i / D][j][i % D];
+        p.partial[static_cast<int64_t>(blockIdx.x) * 2 * D + i] = sum;
     }
 }
 
@@ -277,6 +439,7 @@ __global__ void __launch_bounds__(256) heads_weights_kernel(HeadsParams p, int b
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + lane;
     float s = 0.f;
+#pragma unroll 8
     for (int b = warp; b < blocks; b += 8) s += p.partial[static_cast<int64_t>(b) * 2 * p.dim + i];
     part[warp][lane] = s;
     __syncthreads();
@@ -293,21 +456,64 @@ cudaError_t with_dim(const HeadsParams &p, F &&go) {
     return go(std::integral_constant<int, 256>());
 }
 
-int angles_bytes(const HeadsParams &p) { return (kHeadsTokens + 1) * p.rot * 4; }
+// Parts that a token's heads are cut into, 1, 2, 4 or 8: up to one round of the warps as long
+// as there are heads for all, up to four rounds as long as a part has four times its lane
+// groups' heads (what a warp does for a token alone then weighs little).
+int parts_of(const HeadsParams &p, int blocks) {
+    const int64_t warps = static_cast<int64_t>(blocks) * kPlannedSms * kHeadsWarps;
+    const int H = p.hq + p.hk, rows = 256 / p.dim;
+    int parts = 1;
+    while (parts < kHeadsWarps && ((p.tokens * parts < warps && H >= 2 * parts * rows) ||
+                                   (p.tokens * parts < 4 * warps && H >= 8 * parts * rows)))
+        parts *= 2;
+    return parts;
+}
+
+// The rings of a block, `bytes` for each channel of a batch, and its warps' angles.
+int heads_smem(const HeadsParams &p, int ahead, int bytes) {
+    return kHeadsWarps * (kRing * 256 * ahead * bytes + p.rot * 4);
+}
+
+unsigned grid_of(const HeadsParams &p, int parts, int64_t most) {
+    const int64_t blocks = (p.tokens * parts + kHeadsWarps - 1) / kHeadsWarps;
+    return static_cast<unsigned>(blocks < 1 ? 1 : blocks < most ? blocks : most);
+}
 
 }  // namespace
 
-cudaError_t configure_heads() { return cudaSuccess; }
+namespace {
+
+template <int D>
+cudaError_t configure_heads_dim() {
+    const auto more = [](auto kernel, int bytes) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    };
+    HeadsParams p{};
+    p.rot = D;   // (the most that a block takes)
+    const int forward = heads_smem(p, kAhead, 2), back = heads_smem(p, kAheadGrad, 6);
+    cudaError_t e = more(heads_kernel<D, true>, forward);
+    if (e == cudaSuccess) e = more(heads_kernel<D, false>, forward);
+    if (e == cudaSuccess) e = more(heads_backward_kernel<D, true, true>, back);
+    if (e == cudaSuccess) e = more(heads_backward_kernel<D, true, false>, back);
+    if (e == cudaSuccess) e = more(heads_backward_kernel<D, false, true>, back);
+    if (e == cudaSuccess) e = more(heads_backward_kernel<D, false, false>, back);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t configure_heads() {
+    cudaError_t e = configure_heads_dim<64>();
+    if (e == cudaSuccess) e = configure_heads_dim<128>();
+    return e == cudaSuccess ? configure_heads_dim<256>() : e;
+}
 
 cudaError_t launch_heads(const HeadsParams &p, cudaStream_t stream) {
-    const int64_t H = p.hq + p.hk, total = p.tokens * H;
     return with_dim(p, [&](auto d) {
-        constexpr int D = decltype(d)::value, kGroups = kHeadsThreads * 8 / D;
-        int64_t rows = kGroups * 8;
-        if (rows > H * kHeadsTokens) rows = H * kHeadsTokens;
-        const unsigned grid = static_cast<unsigned>((total + rows - 1) / rows);
+        constexpr int D = decltype(d)::value;
+        const int parts = parts_of(p, kHeadsBlocks);
         auto kernel = p.pairs ? heads_kernel<D, true> : heads_kernel<D, false>;
-        kernel<<<grid, kHeadsThreads, angles_bytes(p), stream>>>(p, static_cast<int>(rows));
+        kernel<<<grid_of(p, parts, kHeadsBlocks * kPlannedSms), kHeadsThreads, heads_smem(p, kAhead, 2), stream>>>(p, parts);
         return cudaGetLastError();
     });
 }
@@ -317,17 +523,16 @@ int64_t heads_workspace(const HeadsParams &p) {
 }
 
 cudaError_t launch_heads_backward(const HeadsParams &p, cudaStream_t stream) {
-    const int64_t total = p.tokens * (p.hq + p.hk);
     return with_dim(p, [&](auto d) {
-        constexpr int D = decltype(d)::value, kGroups = kHeadsThreads * 8 / D;
-        const int64_t want = (total + kGroups - 1) / kGroups;
-        const int grid = static_cast<int>(want < 1 ? 1 : want < kGradBlocks ? want : kGradBlocks);
+        constexpr int D = decltype(d)::value;
+        const int parts = parts_of(p, kGradBlocksPerSm);
+        const unsigned grid = grid_of(p, parts, kGradBlocks);
         auto kernel = p.pairs ? (p.dout32 ? heads_backward_kernel<D, true, true> : heads_backward_kernel<D, true, false>)
                               : (p.dout32 ? heads_backward_kernel<D, false, true> : heads_backward_kernel<D, false, false>);
-        kernel<<<grid, kHeadsThreads, angles_bytes(p), stream>>>(p);
+        kernel<<<grid, kHeadsThreads, heads_smem(p, kAheadGrad, p.dout32 ? 6 : 4), stream>>>(p, parts);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess || (p.dqw == nullptr && p.dkw == nullptr)) return e;
-        heads_weights_kernel<<<2 * D / 32, 256, 0, stream>>>(p, grid);
+        heads_weights_kernel<<<2 * D / 32, 256, 0, stream>>>(p, static_cast<int>(grid));
         return cudaGetLastError();
     });
 }

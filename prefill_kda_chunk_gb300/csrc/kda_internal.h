@@ -320,6 +320,7 @@ struct HeadsParams {
     const void *dq, *dk;       // gradient: bf16 or fp32 [T, H, D]
     float *dqw, *dkw;          // gradient: [D] or nullptr
     float *partial;            // gradient: [blocks][2][D]
+    int *err;
 };
 cudaError_t configure_heads();
 cudaError_t launch_heads(const HeadsParams &p, cudaStream_t stream);
