@@ -271,6 +271,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last;
+    __shared__ unsigned long long s_start;
     const Cache8 &c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = p.hq / c.hkv, chunks = (group + H - 1) / H;
@@ -294,6 +295,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
     const auto bar = [&](int i) { return sb + S::kOffBar + 8 * i; };
     if (tid == 0) {
         s_abort = 0;
+        s_start = globaltimer();
         for (int i = 0; i < B::kCount; ++i) mbar_init(bar(i), B::arrivals(i));
         mbar_fence_init();
     }
@@ -306,20 +308,16 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
     tc::fence_after();
     const uint32_t tm = s_tmem;
 
-    // A bounded wait. Once one has run out none waits any more: all roles go through their
-    // tiles to the end, whatever they find there, so that every barrier and counter is
-    // arrived at as often as otherwise.
+    // A bounded wait (the clock from the block's start on: short code, as the roles' loops
+    // together are more than the instruction caches hold). Once one has run out none waits
+    // any more: all roles go through the piece they are at to its end, whatever they find there.
     auto wait = [&](int i, int phase) {
-        if (!mbar_try_wait(bar(i), phase & 1)) {
-            const unsigned long long t0 = globaltimer();
-            while (*static_cast<volatile int *>(&s_abort) == 0) {
-                bool ok = false;
-                for (int k = 0; k < 32 && !ok; ++k) ok = mbar_try_wait(bar(i), phase & 1);
-                if (ok) break;
-                if (globaltimer() - t0 > kWaitLimitNs) {
-                    *static_cast<volatile int *>(&s_abort) = 1;
-                    atomicOr(c.err, kErrTimeout);
-                }
+        for (unsigned spins = 1; !mbar_try_wait(bar(i), phase & 1); ++spins) {
+            if (spins % 256 != 0) continue;
+            if (*static_cast<volatile int *>(&s_abort) != 0) break;
+            if (globaltimer() - s_start > kWaitLimitNs) {
+                *static_cast<volatile int *>(&s_abort) = 1;
+                atomicOr(c.err, kErrTimeout);
             }
         }
         __syncwarp();
