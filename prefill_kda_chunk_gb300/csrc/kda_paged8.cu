@@ -93,8 +93,8 @@ struct Shape {
     static constexpr int kOffSum = kOffPiece + kQBufs * static_cast<int>(sizeof(Piece));   // [2][weights' warps][H]
     static constexpr int kOffTop = kOffSum + 2 * 4 * kGroups * H * 4;         // [2][group][H]
     static constexpr int kOffJoin = kOffTop + 2 * kGroups * H * 4;        // [2][H]
-    static constexpr int kOffCast = kOffJoin + 2 * H * 4;           // [weights' warps][3][H]
-    static constexpr int kOffBar = kOffCast + 4 * kGroups * 3 * H * 4;
+    static constexpr int kOffCast = kOffJoin + 2 * H * 4;           // [weights' and outputs' warps][3][H]
+    static constexpr int kOffBar = kOffCast + (4 * kGroups + 4) * 3 * H * 4;
     // tensor memory columns: S, then O
     static constexpr int kTmO = kSBufs * kQRows;
     static constexpr int kTmCols = kTmO + kPBufs * kPRows <= 256 ? 256 : 512;
@@ -257,6 +257,18 @@ __host__ __device__ __forceinline__ Lengths lengths_of(const Cache8 &c) {
     return {c.lens, c.max_pages * c.page_size, c.batch, c.pages > 0};
 }
 
+// Where a role is in a ring of N places: which one, and which time around.
+template <int N>
+struct Place {
+    int at = 0, turn = 0;
+    __device__ __forceinline__ void step() {
+        if (++at == N) {
+            at = 0;
+            ++turn;
+        }
+    }
+};
+
 struct Paged8Maps {
     CUtensorMap k, v;   // (channel, token, head, page), boxes of 2^shift tokens
     int shift;
@@ -404,7 +416,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         const int cw = warp - S::kCopyWarp, turns = kTma ? B::kCopyWarps / 2 : 1, turn = kTma ? cw / 2 : 0;
         const bool of_v = cw & 1;
         const int offset = kTma ? (lane & 15) << maps.shift : 32 * cw + lane;
-        struct Place {
+        struct Spot {
             int tok0, len, kv, page, in;   // len: 0 behind the last tile
             float ks, vs;
         };
@@ -418,8 +430,8 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 }
         };
         step(turn);
-        auto look = [&]() -> Place {
-            Place a{0, 0, 0, 0, 0, 0.f, 0.f};
+        auto look = [&]() -> Spot {
+            Spot a{0, 0, 0, 0, 0, 0.f, 0.f};
             if (!more) return a;
             a.tok0 = tile * kTile;
             a.len = w.len;
@@ -430,7 +442,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             step(turns);
             return a;
         };
-        auto scales = [&](Place &a) {
+        auto scales = [&](Spot &a) {
             if (a.tok0 + offset >= a.len || offset >= kTile) return;
             if (static_cast<unsigned>(a.page) >= static_cast<unsigned>(c.pages)) {
                 atomicOr(c.err, kErrPage);
@@ -439,15 +451,24 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             if (!kTma || (of_v && lane >= 16)) a.ks = __ldg(c.ks + a.page * c.ks_page + a.kv);
             if (!kTma || (of_v && lane < 16)) a.vs = __ldg(c.vs + a.page * c.vs_page + a.kv);
         };
-        Place now = look(), next = look();
+        Spot now = look(), next = look();
         scales(now);
+        Place<S::kKeys> kp;
+        Place<S::kValues> vp;
+        auto place_on = [&](int by) {
+            for (int i = 0; i < by; ++i) {
+                kp.step();
+                vp.step();
+            }
+        };
+        place_on(turn);
         int n = turn;
-        for (; now.len > 0 && n < p.stall; n += turns) {
-            const Place far = look();
+        for (; now.len > 0 && n < p.stall; n += turns, place_on(turns)) {
+            const Spot far = look();
             scales(next);
-            const int ks = n % S::kKeys, vs = n % S::kValues;
-            if ((!kTma || !of_v) && n >= S::kKeys) wait(B::kKEmpty + ks, n / S::kKeys - 1);
-            if ((!kTma || of_v) && n >= S::kValues) wait(B::kVEmpty + vs, n / S::kValues - 1);
+            const int ks = kp.at, vs = vp.at;
+            if ((!kTma || !of_v) && kp.turn > 0) wait(B::kKEmpty + ks, kp.turn - 1);
+            if ((!kTma || of_v) && vp.turn > 0) wait(B::kVEmpty + vs, vp.turn - 1);
             const uint32_t to_k = sb + ks * S::kTileBytes, to_v = sb + S::kOffV + vs * S::kTileBytes;
             float *sc = reinterpret_cast<float *>(smem + S::kOffSc) + vs * 2 * kTile;
             const int left = now.len - now.tok0;
@@ -498,24 +519,24 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
     } else if (warp == S::kMmaWarpS) {
         // ------------------------------------------------------------------------- S^T = K Q^T
         constexpr uint32_t kId = idesc8(kTile, S::kQRows);
-        int n = 0;
+        Place<S::kSBufs> sp;
+        Place<S::kKeys> kp;
         for (int pc = 0;; ++pc) {
             const Piece &piece = piece_at(pc);
             const int tile0 = piece.tile0, tile1 = piece.tile1;
             if (tile1 == 0 || stopped()) break;
             const uint64_t q = desc<D>(sb + S::kOffQ + pc % S::kQBufs * S::kQRows * D);
-            for (int tile = tile0; tile < tile1; ++tile, ++n) {
-                const int b = n % S::kSBufs;
-                if (n >= S::kSBufs) wait(B::kSEmpty + b, n / S::kSBufs - 1);
-                wait(B::kKFull + n % S::kKeys, n / S::kKeys);
+            for (int tile = tile0; tile < tile1; ++tile, sp.step(), kp.step()) {
+                if (sp.turn > 0) wait(B::kSEmpty + sp.at, sp.turn - 1);
+                wait(B::kKFull + kp.at, kp.turn);
                 fence_async();   // (the threads' copies were ordinary writes)
                 tc::fence_after();
-                const uint64_t k8 = desc<D>(sb + n % S::kKeys * S::kTileBytes);
+                const uint64_t k8 = desc<D>(sb + kp.at * S::kTileBytes);
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k)   // 32 channels
-                    mma8(tm + b * S::kQRows, k8 + k * (32 >> 4), q + k * (32 >> 4), kId, k > 0);
-                mma_commit(bar(B::kSFull + b));
-                mma_commit(bar(B::kKEmpty + n % S::kKeys));
+                    mma8(tm + sp.at * S::kQRows, k8 + k * (32 >> 4), q + k * (32 >> 4), kId, k > 0);
+                mma_commit(bar(B::kSFull + sp.at));
+                mma_commit(bar(B::kKEmpty + kp.at));
                 if (tile + 1 == tile1) mma_commit(bar(B::kQEmpty + pc % S::kQBufs));
             }
         }
@@ -525,27 +546,28 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         constexpr uint32_t kId = idesc8(D, S::kPRows) | kAMajor | kBMajor;
         constexpr bool kQueries = S::kQueryWarp == S::kMmaWarpO;
         if (kQueries) queries(0, w.next(lens, items));
-        int n = 0;
+        Place<S::kPBufs> pp;
+        Place<S::kValues> vp;
         for (int pc = 0;; ++pc) {
             const Piece &piece = piece_at(pc);
             const int count = piece.tile1 == 0 ? 0 : piece.tile1 - piece.tile0;
             if (count == 0 || stopped()) break;
             if (kQueries) queries(pc + 1, w.next(lens, items));   // (a piece ahead)
             else arrive(B::kQEmpty + pc % S::kQBufs);
-            for (int i = 0; i < count; ++i, ++n) {
-                const int b = n % S::kPBufs, vs = n % S::kValues;
-                // (the weights are there: so are the values, and O's buffer is free)
-                wait(B::kVFull + vs, n / S::kValues);
-                wait(B::kPFull + b, n / S::kPBufs);
+            for (int i = 0; i < count; ++i, pp.step(), vp.step()) {
+                const int b = pp.at;
+                // (the weights are there: O's buffer is free)
+                wait(B::kVFull + vp.at, vp.turn);
+                wait(B::kPFull + b, pp.turn);
                 fence_async();
                 tc::fence_after();
-                const uint64_t v = desc<D>(sb + S::kOffV + vs * S::kTileBytes);
+                const uint64_t v = desc<D>(sb + S::kOffV + vp.at * S::kTileBytes);
                 const uint64_t q = desc<S::kPRows>(sb + S::kOffP + b * S::kPRows * kTile);
 #pragma unroll
                 for (int k = 0; k < kTile / 32; ++k)   // 32 tokens
                     mma8(tm + S::kTmO + b * S::kPRows, v + k * (32 * D >> 4), q + k * (32 * S::kPRows >> 4), kId, k > 0);
                 mma_commit(bar(B::kOFull + b));
-                mma_commit(bar(B::kVEmpty + vs));
+                mma_commit(bar(B::kVEmpty + vp.at));
             }
         }
         drain(1);
@@ -562,6 +584,8 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         float *maxima = reinterpret_cast<float *>(smem + S::kOffMax) + g * 2 * 4 * 2 * H;
         float *cast = reinterpret_cast<float *>(smem + S::kOffCast) + warp * 3 * H;
         int n = 0;
+        Place<S::kValues> vp;
+        Place<S::kPBufs> pp;
         for (int pc = 0;; ++pc) {
             const Piece &piece = piece_at(pc);
             const int tile0 = piece.tile0, tile1 = piece.tile1, len = piece.len;
@@ -573,10 +597,10 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 l[h] = 0.f;
             }
             arrive(B::kQEmpty + pc % S::kQBufs);
-            for (int tile = tile0; tile < tile1; ++tile, ++n) {
+            for (int tile = tile0; tile < tile1; ++tile, ++n, vp.step(), pp.step()) {
                 if (n % S::kGroups != g) continue;
-                const int vs = n % S::kValues, b = n % S::kPBufs, sbuf = n % S::kSBufs;
-                wait(B::kVFull + vs, n / S::kValues);
+                const int vs = vp.at, b = pp.at, sbuf = n % S::kSBufs;
+                wait(B::kVFull + vs, vp.turn);
                 wait(B::kSFull + sbuf, n / S::kSBufs);
                 tc::fence_after();
                 const float *sc = reinterpret_cast<const float *>(smem + S::kOffSc) + vs * 2 * kTile + (kTma ? t >> maps.shift : t);
@@ -613,7 +637,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 float *m = maxima + (n / S::kGroups & 1) * 4 * 2 * H;
                 if (lane < 2 * H) m[q * 2 * H + lane] = mine;
                 group_sync(1 + g);
-                if (n >= S::kPBufs) wait(B::kOEmpty + b, n / S::kPBufs - 1);
+                if (pp.turn > 0) wait(B::kOEmpty + b, pp.turn - 1);
                 if (lane < 2 * H) {
                     const float all = fmaxf(fmaxf(m[lane], m[2 * H + lane]), fmaxf(m[4 * H + lane], m[6 * H + lane]));
                     if (lane < H) {
@@ -622,7 +646,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                         cast[H + lane] = ex2(top - base);
                         top = now;
                     } else {
-                        cast[H + lane] = finite_base(all);
+                        cast[H + lane] = finite_base(all) - 8.f;   // weights up to 2^8: e4m3 reaches 448
                         if (q == 0) reinterpret_cast<float *>(smem + S::kOffStat)[b * H + lane - H] = all;
                     }
                 }
@@ -639,7 +663,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         l[h + j] = fmaf(l[h + j], fs[j], ex2(x[h + j] - xs[j]));
-                        wt[j] = ex2(x[h + j] + lv - ys[j]) * 256.f;   // e4m3 reaches 448
+                        wt[j] = ex2(x[h + j] + lv - ys[j]);
                     }
                     uint32_t lo[kPTerms], hi[kPTerms];
                     split4(wt[0], wt[1], lo);
@@ -676,7 +700,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         const int64_t U = sh.U, G = sh.G;
         const int me = blockIdx.x;
         float *join = reinterpret_cast<float *>(smem + S::kOffJoin);
-        int n = 0;
+        Place<S::kPBufs> pp;
         // One arrival at an item's counter for each of its pieces; the last finds it complete,
         // and sets it back for the next call.
         auto last_piece = [&](const Piece &piece, int c0, int c1) -> bool {
@@ -690,6 +714,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             c1 = Paged8Split::owner(piece.item_at + kItemCost + piece.tiles - 1, U, G);
         };
         int pc = 0;
+        float *cast = reinterpret_cast<float *>(smem + S::kOffCast) + warp * 3 * H;
         for (;; ++pc) {
             const Piece piece = piece_at(pc);
             if (group_any(kOutSync, piece.tile1 == 0 || stopped())) break;
@@ -698,33 +723,40 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             float acc[H], top = -CUDART_INF_F;   // top: lane h has head h's
 #pragma unroll
             for (int h = 0; h < H; ++h) acc[h] = 0.f;
-            for (int tile = piece.tile0; tile < piece.tile1; ++tile, ++n) {
-                const int b = n % S::kPBufs;
-                wait(B::kOFull + b, n / S::kPBufs);
+            for (int tile = piece.tile0; tile < piece.tile1; ++tile, pp.step()) {
+                const int b = pp.at;
+                wait(B::kOFull + b, pp.turn);
                 tc::fence_after();
                 uint32_t raw[S::kPRows / 16][16];
 #pragma unroll
                 for (int i = 0; i < S::kPRows / 16; ++i)
                     tc::ld16(tm + lanes + S::kTmO + b * S::kPRows + 16 * i, raw[i]);
-                float f = 0.f, gain = 0.f;
                 if (lane < H) {
                     const float all = reinterpret_cast<const float *>(smem + S::kOffStat)[b * H + lane];
                     const float now = fmaxf(top, all), base = finite_base(now);
-                    f = ex2(top - base);
-                    gain = ex2(all - base) * (1.f / 256);
+                    cast[lane] = ex2(top - base);
+                    cast[H + lane] = ex2(all - base) * (1.f / 256);
                     top = now;
                 }
                 tc::ld_wait();
                 tc::fence_before();
                 arrive(B::kOEmpty + b);
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    float o = __uint_as_float(raw[(3 * H + h) / 16][(3 * H + h) % 16]);
+                for (int h = 0; h < H; h += 4) {
+                    const float4 fb = *reinterpret_cast<const float4 *>(cast + h);
+                    const float4 gb = *reinterpret_cast<const float4 *>(cast + H + h);
+                    const float fs[4] = {fb.x, fb.y, fb.z, fb.w}, gains[4] = {gb.x, gb.y, gb.z, gb.w};
 #pragma unroll
-                    for (int k = kPTerms - 2; k >= 0; --k)
-                        o = fmaf(o, 1.f / kFiner, __uint_as_float(raw[(k * H + h) / 16][(k * H + h) % 16]));
-                    acc[h] = fmaf(acc[h], __shfl_sync(0xffffffffu, f, h), o * __shfl_sync(0xffffffffu, gain, h));
+                    for (int j = 0; j < 4; ++j) {
+                        const int i = h + j;
+                        float o = __uint_as_float(raw[(3 * H + i) / 16][(3 * H + i) % 16]);
+#pragma unroll
+                        for (int k = kPTerms - 2; k >= 0; --k)
+                            o = fmaf(o, 1.f / kFiner, __uint_as_float(raw[(k * H + i) / 16][(k * H + i) % 16]));
+                        acc[i] = fmaf(acc[i], fs[j], o * gains[j]);
+                    }
                 }
+                __syncwarp();   // (`cast` is read)
             }
             // ---- the piece's end: lane h has the sum and maximum of head h
             const bool whole = piece.tile0 == 0 && piece.tile1 == piece.tiles;
