@@ -45,7 +45,7 @@ namespace kda {
 namespace {
 
 constexpr int kTile = 128;           // tokens
-constexpr int kItemCost = 2;         // start and end of an item, in tiles
+constexpr int kItemCost = 3;         // start and end of an item, in tiles (64 ragged sequences: 64 us with 1, 54 with 2, 50 with 3 or 4)
 constexpr int kQTerms = 2, kPTerms = 4;
 constexpr float kFiner = 32.f;       // from one term to the next
 constexpr unsigned long long kLandNs = 100000000;   // within which copies and products end
