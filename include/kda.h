@@ -562,8 +562,8 @@ KDA_API kda_status kda_qk_norm_rope_backward(
  * The scale of a page and head, for keys and for values, is a power of two and only
  * grows: the least one (from 2^-126 on) that brings the largest new value to 448 or
  * below, or the one that the page has, if that is larger. A page whose row 0 is among
- * the new rows starts anew. When the scale grows, the rows in front of the new ones are
- * scaled down to it, which is exact but for what leaves e4m3's range below. New
+ * the new rows starts anew. When the scale grows, the other rows of the page are scaled
+ * down to it, which is exact but for what leaves e4m3's range below. New
  * values are x / scale, rounded once to the nearest, ties to even; infinities and NaN
  * become NaN and do not count for the scale. (A scale that a caller has put into a page,
  * any positive number, is kept and used as its reciprocal.)

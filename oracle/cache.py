@@ -130,7 +130,7 @@ def append(x, cache, scale, table, lens, cu=None):
                 if row > 0:
                     want = max(want, float(scale[p, h]))
                     if want > scale[p, h]:
-                        cache[p, :row, h] = e4m3(cache[p, :row, h] * (scale[p, h] / want))
+                        cache[p, :, h] = e4m3(cache[p, :, h] * (scale[p, h] / want))
                 cache[p, row:row + m, h] = e4m3(new / want)
                 scale[p, h] = want
             at, pos = at + m, pos + m

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(256) plan_fill_kernel(PlanParams p) {
 // ----------------------------------------------------------- into the cache
 //
 // A work item is the new rows of one page and some heads, keys or values. A group of warps
-// takes it head by head: the largest value, the scale, the rows (and the page's older rows
+// takes it head by head: the largest value, the scale, the rows (and the page's other rows
 // where the scale grew), with the next head's rows on their way into registers meanwhile.
 // What leads to a page (cu_seqlens, length, table: a chain of loads) is then paid once for
 // several heads. Slot i can touch n_i / page_size + 2 pages, so candidates are numbered with
@@ -415,10 +415,11 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p, int64_t ite
         for (int r = sub + kKeep * kStep; r < rows; r += kStep)
             *reinterpret_cast<uint2 *>(dst + (row + r) * step) =
                 quantise(*reinterpret_cast<const uint4 *>(rest + r * stride), inv, odd);
-        if (grew) {
+        if (grew) {   // the page's other rows, what they stand for as before
             const float f = old / scale;
 #pragma unroll 4
-            for (int r = sub; r < row; r += kStep) {
+            for (int r = sub; r < c.page_size; r += kStep) {
+                if (r >= row && r < row + rows) continue;
                 uint2 *q = reinterpret_cast<uint2 *>(dst + r * step);
                 const uint2 u = *q;
                 *q = make_uint2(rescale4(u.x, f), rescale4(u.y, f));
