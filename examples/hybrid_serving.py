@@ -4,7 +4,9 @@ Three layers, each with a norm before it and a residual around it:
 
   KDA          short convolution over q, k and v, then the gated delta rule
   state space  short convolution over x, b and c, then the scan
-  attention    keys and values in a paged cache, read by paged_decode
+  attention    keys and values in a paged cache, read by paged_decode; or, with --fp8, norms
+               and a rotation of queries and keys, and the cache in 8 bits, its pages dealt
+               out on the GPU
 
 A batch of ragged prompts goes through packed; every layer then holds what it
 needs to go on (a history, a state, a cache), and tokens follow one per
@@ -13,6 +15,7 @@ check is one of the library against itself: the outputs of prompt + steps
 equal those of one prompt that holds all the tokens, to bf16 rounding.
 
     python examples/hybrid_serving.py --prompts 300,37,1 --steps 16
+    python examples/hybrid_serving.py --fp8            # the attention layer's 8-bit form
     python examples/hybrid_serving.py --train          # gradients of the KDA layer too
 """
 import argparse
@@ -149,10 +152,50 @@ class Attention(Layer):
         return o
 
 
+class Attention8(Layer):
+    """Norms and rotation in front, keys and values in e4m3 with a scale per page and head."""
+    HEADS, KV_HEADS, DIM = 16, 2, 64
+
+    def __init__(self, gen, longest, sequences):
+        super().__init__(gen)
+        self.sizes = [self.HEADS * self.DIM] + 2 * [self.KV_HEADS * self.DIM]
+        self.qkv, self.out = self.weight(sum(self.sizes)), self.weight(WIDTH, self.HEADS * self.DIM)
+        self.norms = [1 + 0.1 * torch.randn(self.DIM, generator=gen).to("cuda") for _ in "qk"]
+        self.freq = (10000.0 ** (-torch.arange(0, self.DIM, 2) / self.DIM)).float().to("cuda")
+        per = (longest + PAGE - 1) // PAGE
+        pages = sequences * per
+        both = torch.zeros(pages, 2, PAGE, self.KV_HEADS, self.DIM, dtype=torch.uint8, device="cuda")
+        both, scales = both.view(torch.float8_e4m3fn), torch.zeros(pages, 2, self.KV_HEADS, device="cuda")
+        self.cache = both[:, 0], both[:, 1], scales[:, 0], scales[:, 1]
+        # nobody holds a page yet: table, lengths, the stack of free pages, how many
+        self.pool = [torch.zeros(sequences, per, dtype=torch.int32, device="cuda"),
+                     torch.zeros(sequences, dtype=torch.int32, device="cuda"),
+                     torch.randperm(pages, generator=gen).to("cuda", torch.int32),
+                     torch.full((1,), pages, dtype=torch.int32, device="cuda")]
+
+    def attend(self, x, new):
+        """`new` tokens of each sequence join it; each sees its sequence up to itself."""
+        table, lens, free, count = self.pool
+        _, _, _, _, cu, pos, _ = K.page_plan(table, lens, new, free, count, PAGE, len(x), in_place=True)
+        q, k, v = (t.unflatten(-1, (-1, self.DIM)) for t in (x @ self.qkv.T).split(self.sizes, dim=-1))
+        q, k = K.qk_norm_rope(q, k, *self.norms, self.freq, pos)
+        K.paged_append_fp8(k, v, *self.cache, table, lens, cu)
+        seq = torch.repeat_interleave(torch.arange(len(new), device="cuda"), new.long(), output_size=len(x))
+        o, _ = K.paged_decode_fp8(q, *self.cache, table[seq], pos + 1)
+        return o.reshape(-1, self.HEADS * self.DIM) @ self.out.T
+
+    def prompt(self, x, cu):
+        return self.attend(x, cu[1:] - cu[:-1])
+
+    def step(self, x):
+        return self.attend(x, torch.ones(len(x), dtype=torch.int32, device="cuda"))
+
+
 class Model:
-    def __init__(self, seed, longest, sequences):
+    def __init__(self, seed, longest, sequences, fp8=False):
         gen = torch.Generator().manual_seed(seed)
-        self.layers = [Kda(gen), StateSpace(gen), Attention(gen, longest, sequences)]
+        attention = Attention8 if fp8 else Attention
+        self.layers = [Kda(gen), StateSpace(gen), attention(gen, longest, sequences)]
 
     def prompt(self, x, cu):
         for layer in self.layers:
@@ -165,7 +208,7 @@ class Model:
         return x
 
 
-def serve(prompts, steps, seed=1):
+def serve(prompts, steps, seed=1, fp8=False):
     """The largest difference of prompt + steps from one prompt, over the largest value."""
     gen = torch.Generator().manual_seed(seed)
     tokens = [torch.randn(n + steps, WIDTH, generator=gen).to("cuda", BF16) for n in prompts]
@@ -173,7 +216,7 @@ def serve(prompts, steps, seed=1):
     def cu(lens):
         return torch.tensor([0] + lens, device="cuda").cumsum(0).to(torch.int32)
 
-    model = Model(seed, max(prompts) + steps, len(prompts))
+    model = Model(seed, max(prompts) + steps, len(prompts), fp8)
     got = [[row] for row in model.prompt(torch.cat([t[:n] for t, n in zip(tokens, prompts)]),
                                          cu(prompts)).split(prompts)]
     for i in range(steps):
@@ -182,7 +225,7 @@ def serve(prompts, steps, seed=1):
             rows.append(row[None])
     K.check_device_error()
 
-    whole = Model(seed, max(prompts) + steps, len(prompts))
+    whole = Model(seed, max(prompts) + steps, len(prompts), fp8)
     lens = [n + steps for n in prompts]
     ref = whole.prompt(torch.cat(tokens), cu(lens))
     K.check_device_error()
@@ -224,9 +267,10 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--prompts", default="300,37,1", help="tokens of each prompt")
     ap.add_argument("--steps", type=int, default=16, help="tokens after the prompts")
+    ap.add_argument("--fp8", action="store_true", help="the attention layer's cache in 8 bits")
     ap.add_argument("--train", action="store_true", help="take gradient steps as well")
     a = ap.parse_args()
-    worst = serve([int(n) for n in a.prompts.split(",")], a.steps)
+    worst = serve([int(n) for n in a.prompts.split(",")], a.steps, fp8=a.fp8)
     print(f"prompt + {a.steps} steps against one prompt: largest difference {worst:.2e} of the largest value")
     if a.train:
         print("filters in front of KDA, relative loss: %.3e -> %.3e" % train())

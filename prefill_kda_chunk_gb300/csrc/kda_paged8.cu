@@ -24,12 +24,19 @@
 // into the exponent (s_j + log2 vs_j): the weights of a tile then reach 1 whatever the
 // scales are.
 //
-// Roles, one block per SM: 4 warps copy (cp.async, 16 bytes of a row each, so that any
-// page size, stride and order of the pages will do), one warp issues the products, two
-// groups of 4 warps take turns with the tiles' weights, 4 warps add up the outputs, one
-// prepares the queries. Shares, pieces and the join of pieces: kda_pieces.cuh; a piece
-// that is not a whole item leaves its sums in the workspace, and the last block to
-// arrive joins them in the order of the blocks.
+// Roles, one block per SM: two or four warps copy (by the tensor memory accelerator, or, where
+// the pages do not allow it, 16 bytes a time with cp.async: any page size, stride and order of
+// the pages will do), one warp issues each product, two groups of four warps take turns with
+// the tiles' weights, four warps add up the outputs, one prepares the queries and says what
+// the block's next piece is. Shares, pieces and their join: kda_pieces.cuh; a piece that is not
+// a whole item leaves its sums in the workspace, and the last block to arrive joins them in
+// the order of the blocks.
+//
+// Measured (copy bandwidth: 1340 clocks for a tile of D = 128): 2 sequences of 131072 tokens, 32
+// heads over 8 of 128: 92 us (5.8 TB/s, 86 % of copy bandwidth); 64 sequences of 1 to 16384
+// tokens, 64 heads over 8: 50 us (67 %); one of 700: 11 us, a chain of latencies. What a tile
+// takes the weights' warps, some 1250 clocks with 8 heads, bounds D = 64 (8 x 32768 tokens: 72
+// us, 55 %), and 1600 with 16 heads those (8 x 65536, 2 key-value heads: 64 us, 62 %).
 
 #include <cuda.h>
 #include <cuda_fp8.h>
@@ -59,8 +66,8 @@ constexpr int threads_of(int heads, bool tma) { return 32 * (4 * groups_of(heads
 using Paged8Split = Split<kTile, kItemCost>;
 
 // A piece of the block's share, as the queries' warp hands it to the other roles beside the
-// queries themselves (each going through the share by itself: 256 sequences of 1000 tokens
-// 119 us; this way FIGURE).
+// queries themselves (with each going through the share by itself 256 sequences of 1000
+// tokens took 119 us, this way 112).
 struct alignas(16) Piece {
     int tile0, tile1, len, tiles;   // tile1 = 0 behind the last one
     int64_t row, item_at;           // of out; first unit
@@ -436,14 +443,14 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             a.tok0 = tile * kTile;
             a.len = w.len;
             a.kv = w.item / chunks;
-            const int t = a.tok0 + offset, at = static_cast<int>(p.page_of(t));
-            a.in = t - at * c.page_size;
-            if (t < w.len && offset < kTile) a.page = __ldg(c.table + static_cast<int64_t>(w.b) * c.max_pages + at);
+            const uint32_t t = static_cast<uint32_t>(a.tok0) + offset, at = p.page_of(t);
+            a.in = static_cast<int>(t - at * c.page_size);
+            if (offset < a.len - a.tok0 && offset < kTile) a.page = __ldg(c.table + static_cast<int64_t>(w.b) * c.max_pages + at);
             step(turns);
             return a;
         };
         auto scales = [&](Spot &a) {
-            if (a.tok0 + offset >= a.len || offset >= kTile) return;
+            if (offset >= a.len - a.tok0 || offset >= kTile) return;
             if (static_cast<unsigned>(a.page) >= static_cast<unsigned>(c.pages)) {
                 atomicOr(c.err, kErrPage);
                 a.page = 0;
@@ -469,6 +476,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             const int ks = kp.at, vs = vp.at;
             if ((!kTma || !of_v) && kp.turn > 0) wait(B::kKEmpty + ks, kp.turn - 1);
             if ((!kTma || of_v) && vp.turn > 0) wait(B::kVEmpty + vs, vp.turn - 1);
+            if (stopped()) break;   // (its places may be in use)
             const uint32_t to_k = sb + ks * S::kTileBytes, to_v = sb + S::kOffV + vs * S::kTileBytes;
             float *sc = reinterpret_cast<float *>(smem + S::kOffSc) + vs * 2 * kTile;
             const int left = now.len - now.tok0;
@@ -611,7 +619,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 tc::ld_wait();
                 tc::fence_before();
                 arrive(B::kSEmpty + sbuf);
-                const bool live = tile * kTile + t < len;
+                const bool live = t < len - tile * kTile;
                 const float lv = live ? __log2f(sc[kTile]) : 0.f;
                 if (kTma && !live) {   // no weight of 0 makes an infinity or NaN vanish
 #pragma unroll
@@ -894,8 +902,8 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
 constexpr int heads_of(int group) { return group <= 8 ? 8 : 16; }
 
 // Pages of a multiple of 8 tokens are copied by the tensor memory accelerator, in boxes of
-// the largest power of two that divides them; others by threads, 16 bytes a time (131072 x 2
-// tokens, pages of 32: FIGURES).
+// the largest power of two that divides them; others by threads, 16 bytes a time (2 x 131072
+// tokens, pages of 32: 92 us and 150; 64 ragged sequences, pages of 64: 50 and 75).
 int box_rows(const Cache8 &c) {
     const int two = c.page_size & -c.page_size;
     return two < 8 ? 0 : two < kTile ? two : kTile;

@@ -634,6 +634,74 @@ def test_decode_non_finite_numbers_keep_to_their_rows():
     assert torch.isfinite(l3[0]).all()
 
 
+@pytest.mark.parametrize("page", [16, 17])
+def test_decode_strides_of_no_pattern(page):
+    """Rows, heads and pages a multiple of 16 bytes apart, but of nothing else."""
+    lens, pages, Hkv, D = [200, 75], 20, 3, 64
+    q, kc, vc, ks, vs, table, n = cache_case(lens, 6, Hkv, D, page)
+    ref = K.paged_decode_fp8(q, kc, vc, ks, vs, table, n)
+    pages = kc.shape[0]
+    steps = (Hkv * (page * 80 + 48) + 16, 80, page * 80 + 48)   # page, token, head
+    apart = []
+    for c in (kc, vc):
+        t = torch.empty(pages * steps[0], dtype=torch.uint8, device="cuda").fill_(127)
+        t = t.as_strided(c.shape, (*steps, 1))
+        t.copy_(c.view(torch.uint8))
+        apart.append(t.view(F8))
+    wide = [torch.full((pages, 2 * Hkv + 1), float("nan"), device="cuda")[:, :Hkv] for _ in "kv"]
+    for w, s in zip(wide, (ks, vs)):
+        w.copy_(s)
+    got = K.paged_decode_fp8(q, *apart, *wide, table, n)
+    K.check_device_error()
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+def test_decode_longest_cache():
+    """2^31 - 4096 tokens, one page again and again: the attention over that page. A thread adds
+    up 2^31 / 152 / 256 = 55000 weights of about the same size in fp32, so each sum is within
+    55000 * 2^-24 = 2^-8.2 of itself, and the output within twice that."""
+    q, kc, vc, ks, vs, table, n = cache_case([4096], 4, 1, 64, 4096, seed=3)
+    ref, l = K.paged_decode_fp8(q, kc, vc, ks, vs, table, n)
+    reps = (1 << 31) // 4096 - 1
+    o, m = K.paged_decode_fp8(q, kc, vc, ks, vs, table[:, :1].expand(1, reps).contiguous(), i32([reps * 4096]))
+    K.check_device_error()
+    assert ((m - l - math.log(reps)).abs() <= 2.0 ** -8).all()
+    at = int(table[0, 0])
+    assert ((o.float() - ref.float()).abs() <= 2.0 ** -7 * vc[at].float().abs().max() * vs[at].max()).all()
+
+
+@pytest.mark.parametrize("page", [16, 17])
+@pytest.mark.parametrize("lens,tile", [([300], 0), ([40000, 9, 3000], 2), ([40000, 9, 3000], 3)])
+def test_decode_wait_runs_out_then_clean_call(lens, tile, page):
+    """(A share of the second batch is four or five tiles of 128 tokens.)"""
+    case = cache_case(lens, 16, 2, 128, page)
+    ref = K.paged_decode_fp8(*case)
+    K.check_device_error()
+    assert K.kda_test_stall_paged_fp8(tile) == 0
+    try:
+        K.paged_decode_fp8(*case)
+        with pytest.raises(K.KdaError, match="TIMEOUT"):
+            K.check_device_error()
+    finally:
+        assert K.kda_test_stall_paged_fp8(-1) == 0
+    K.check_device_error()
+    for _ in range(2):   # the counters of the joins are right again
+        got = K.paged_decode_fp8(*case)
+        K.check_device_error()
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+def test_decode_same_bits_from_cold_caches():
+    """Many calls, each with the caches of the GPU emptied first."""
+    case = cache_case([7000, 350, 2, 12000], 16, 2, 128, 64, layout="heads first")
+    big = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    ref = K.paged_decode_fp8(*case)
+    for i in range(40):
+        big.fill_(i)
+        got = K.paged_decode_fp8(*case)
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1]), i
+
+
 def test_decode_bad_tables_are_reported():
     lens = [50, 20, 40]
     q, kc, vc, ks, vs, table, n = cache_case(lens, 8, 2, 128, 16)
