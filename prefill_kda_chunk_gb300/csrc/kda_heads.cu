@@ -237,10 +237,8 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsBlocks) heads_kernel(Head
     __syncthreads();
     int pos = p.rot > 0 && mine.token < p.tokens ? __ldg(p.pos + mine.token) : 0;
     for (int64_t token = mine.token; token < p.tokens; token += mine.step) {
-        float c[8], s[8];
         if (p.rot > 0) {
             fill_angles(p, table, pos);
-            turn.angles(table, p.rot, c, s);
             if (token + mine.step < p.tokens) pos = __ldg(p.pos + token + mine.step);
         }
 #pragma unroll 1
@@ -251,7 +249,8 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsBlocks) heads_kernel(Head
             float a[8], b[8];
             load8<8>(weights + keys * D + 8 * at, a);
             if (p.rot > 0) {
-                float w[8];
+                float w[8], c[8], s[8];
+                turn.angles(table, p.rot, c, s);
                 load8<8>(weights + keys * D + turn.partner, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) b[e] = w[kPairs ? e ^ 1 : e];
@@ -267,24 +266,37 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsBlocks) heads_kernel(Head
                 ring.wait(p.err);
                 const uint32_t from = ring.place(ring.n) + lane * 16;
 #pragma unroll
-                for (int i = 0; i < kAhead; ++i) {
+                for (int i = 0; i < kAhead; i += 2) {   // two heads of a lane group side by side
                     if (now.h + i * kRows >= end) break;   // (the whole warp)
-                    const uint4 in = lds16(from + i * 512);
-                    float x[8], sq[2] = {0.f, 0.f};
-                    unpack8(in, x);
+                    uint4 in[2];
+                    float x[2][8], o[2][8], r[2];
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2) muladd2(sq[0], sq[1], x[e], x[e + 1], x[e], x[e + 1]);
-                    const float r = rsqrtf(row_sum<kLanes>(sq[0] + sq[1]) * (1.f / D) + p.eps);
-                    float o[8];
-                    if (p.rot > 0) unpack8(turn.partners(in), o);
+                    for (int j = 0; j < 2; ++j) in[j] = lds16(from + (i + j) * 512);
 #pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        mul2(x[e], x[e + 1], a[e], a[e + 1]);
-                        if (p.rot > 0) muladd2(x[e], x[e + 1], o[e], o[e + 1], b[e], b[e + 1]);
-                        mul2(x[e], x[e + 1], r, r);
+                    for (int j = 0; j < 2; ++j) {
+                        float sq[2] = {0.f, 0.f};
+                        unpack8(in[j], x[j]);
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) muladd2(sq[0], sq[1], x[j][e], x[j][e + 1], x[j][e], x[j][e + 1]);
+                        r[j] = sq[0] + sq[1];
                     }
-                    const int head = now.h + i * kRows;
-                    if (head + sub < end) *reinterpret_cast<uint4 *>(out + head * D) = pack8(x);
+#pragma unroll
+                    for (int m = kLanes / 2; m > 0; m >>= 1)
+                        add2(r[0], r[1], __shfl_xor_sync(0xffffffffu, r[0], m), __shfl_xor_sync(0xffffffffu, r[1], m));
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        r[j] = rsqrtf(r[j] * (1.f / D) + p.eps);
+                        if (p.rot > 0) unpack8(turn.partners(in[j]), o[j]);
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            mul2(x[j][e], x[j][e + 1], a[e], a[e + 1]);
+                            if (p.rot > 0) muladd2(x[j][e], x[j][e + 1], o[j][e], o[j][e + 1], b[e], b[e + 1]);
+                            mul2(x[j][e], x[j][e + 1], r[j], r[j]);
+                        }
+                        // (what lies behind the last head is an earlier batch's)
+                        const int head = now.h + (i + j) * kRows;
+                        if (head + sub < end) *reinterpret_cast<uint4 *>(out + head * D) = pack8(x[j]);
+                    }
                 }
                 __syncwarp();
                 ask(ahead, ring.n);   // (the place just read)
