@@ -67,13 +67,6 @@ __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
     }
 }
 
-template <int kLanes>
-__device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-    for (int m = kLanes / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-    return v;
-}
-
 // A token's cosines, then its sines, by the warp that needs them.
 __device__ __forceinline__ void fill_angles(const HeadsParams &p, float *cs, int pos) {
     const int half = p.rot / 2;
@@ -468,17 +461,23 @@ cudaError_t with_dim(const HeadsParams &p, F &&go) {
     return go(std::integral_constant<int, 256>());
 }
 
-// Parts that a token's heads are cut into, 1, 2, 4 or 8: up to one round of the warps as long
-// as there are heads for all, up to four rounds as long as a part has four times its lane
-// groups' heads (what a warp does for a token alone then weighs little).
+// Parts that a token's heads are cut into, 1, 2, 4 or 8: those with the least time by this
+// count. Warps take (token, part) after (token, part), as many rounds as that makes; one costs its
+// lane groups' heads and four more for what is done for the token alone. (8192 tokens, 40 heads of
+// 64: 17 us in one part, 21 in two; 72 heads of 128: 56 and 51.)
 int parts_of(const HeadsParams &p, int blocks) {
     const int64_t warps = static_cast<int64_t>(blocks) * kPlannedSms * kHeadsWarps;
     const int H = p.hq + p.hk, rows = 256 / p.dim;
-    int parts = 1;
-    while (parts < kHeadsWarps && ((p.tokens * parts < warps && H >= 2 * parts * rows) ||
-                                   (p.tokens * parts < 4 * warps && H >= 8 * parts * rows)))
-        parts *= 2;
-    return parts;
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int parts = 1; parts <= kHeadsWarps && parts <= H; parts *= 2) {
+        const int64_t cost = ((p.tokens * parts + warps - 1) / warps) * ((H + parts * rows - 1) / (parts * rows) + 4);
+        if (cost < least) {
+            least = cost;
+            best = parts;
+        }
+    }
+    return best;
 }
 
 // The rings of a block, `bytes` for each channel of a batch, and its warps' angles.
