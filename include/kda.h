@@ -544,7 +544,7 @@ KDA_API kda_status kda_qk_norm_rope(const void *q, const void *k, const float *q
  *   dq_weight, dk_weight device, fp32 [D] or NULL (not wanted)
  *
  * The weights' sums are taken in fp32 in a fixed order (the same call gives the same
- * bits). Workspace: 2 D floats for each of at most 608 blocks.
+ * bits). Workspace: 2 D floats for each of at most 304 blocks.
  */
 KDA_API kda_status kda_qk_norm_rope_backward(
     const void *q, const void *k, const float *q_weight, const float *k_weight,
@@ -580,7 +580,7 @@ KDA_API kda_status kda_qk_norm_rope_backward(
  *                for each slot (none where seq_lens is 0)
  *   D = 64 or 128 (others: KDA_ERR_UNSUPPORTED_DIM); B <= 65536; T < 2^31; (T + 2 B) * Hkv < 2^30.
  *
- * Pages of different slots that get new tokens must differ. Rows of k and v behind the last
+ * Pages that get new tokens must differ, those of one slot and those of different slots. Rows of k and v behind the last
  * slot are not read. A slot with a wrong cu_seqlens (KDA_ERR_BAD_CU_SEQLENS), length or page
  * index (KDA_ERR_BAD_PAGE_TABLE) is reported by kda_last_device_error(); its tokens, or those
  * of the bad page, are not written. Alignment: 16 bytes for k, v and the caches, k_stride and

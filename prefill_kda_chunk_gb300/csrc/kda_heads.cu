@@ -10,8 +10,13 @@
 // rotation are multiplied by (weight times cosine and sine) in registers. The sines and
 // cosines of a token are formed once for them. Bound by reading and writing the heads.
 // These come through a ring of bulk copies of each warp's own, a batch of heads (contiguous in
-// a token) each, so that what is on its way takes no registers (batches in registers: the
-// 8192 tokens below 64 us, gradient 94).
+// a token) each, so that what is on its way takes no registers (with batches in registers the
+// 8192 tokens below took 64 us, their gradient 94).
+//
+// Measured: 8192 tokens of 64 + 8 heads of 128: 51 us (5.9 TB/s, 87 % of copy bandwidth), the
+// gradient 81 us (82 %, and 62 % of the issue slots taken); 5003 tokens of 16 + 2 heads, gradient
+// 16.6 us (41 %: start, end and the weights' sums are 6 us of it); one token 4.0 us, a launch and
+// a chain of loads.
 
 #include <type_traits>
 
@@ -133,7 +138,7 @@ __device__ __forceinline__ void fill_weights(const HeadsParams &p, float *w) {
     }
 }
 
-// A warp's work: the heads [q0, q1) of the queries and [k0, k1) of the keys of every token it
+// A warp's work in the forward kernel: the heads [q0, q1) of the queries and [k0, k1) of the keys of every token it
 // comes to, in batches. Warp w of a block that takes 8 / parts tokens together has token
 // w / parts of them, and one part of its heads.
 struct Share {
@@ -301,14 +306,55 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsBlocks) heads_kernel(Head
     }
 }
 
+// A warp's way through its share of the gradient's work: token after token the queries' heads, then the
+// keys', cut into units of kUnit heads. All warps have as many units, one more or less; a
+// token's heads may so be cut anywhere. A batch is up to kMost units of one token, of its
+// queries or its keys. (Parts of tokens in turns, as the forward kernel takes them: 8192 tokens
+// of 72 heads of 128 took 86 us, this way 81; 5003 of 18 heads 17.5 and 16.6. The forward kernel,
+// nearer the memory's rate, gains from all warps reading one stretch of it: 51 us in turns, 57
+// this way.)
+template <int kUnit, int kMost>
+struct Walk {
+    int token, left;   // units left
+    int h, heads;      // the batch: heads from h on
+    bool keys;         // of the keys
+    __device__ __forceinline__ static int units(int heads) { return (heads + kUnit - 1) / kUnit; }
+    __device__ __forceinline__ explicit Walk(const HeadsParams &p) {
+        const int nq = units(p.hq), n = nq + units(p.hk);
+        const int64_t all = p.tokens * n, warps = static_cast<int64_t>(gridDim.x) * kHeadsWarps,
+                      w = static_cast<int64_t>(blockIdx.x) * kHeadsWarps + (threadIdx.x >> 5);
+        const int64_t u0 = w * all / warps, u1 = (w + 1) * all / warps;
+        token = static_cast<int>(u0 / n);
+        const int at = static_cast<int>(u0 - static_cast<int64_t>(token) * n);
+        left = static_cast<int>(u1 - u0);
+        keys = at >= nq;
+        h = (keys ? at - nq : at) * kUnit;
+        batch(p);
+    }
+    __device__ __forceinline__ void batch(const HeadsParams &p) {
+        heads = min(min((keys ? p.hk : p.hq) - h, kMost * kUnit), left * kUnit);
+    }
+    __device__ __forceinline__ void advance(const HeadsParams &p) {
+        left -= units(heads);
+        h += heads;
+        if (h >= (keys ? p.hk : p.hq)) {
+            h = 0;
+            if (keys || p.hk == 0) ++token;
+            keys = !keys && p.hk > 0;
+        }
+        batch(p);
+    }
+};
+
 // The gradient. With g = R^T dy, A = sum x^2, B = sum g w x over the channels:
 //   dw += r g x,  dx = r w g - (r^3 B / D) x
 // Blocks keep their parts of the weights' gradients in registers to the end.
 constexpr int kGradBlocks = kGradBlocksPerSm * kPlannedSms;
 
 template <int D, bool kPairs, bool kF32>
-__global__ void __launch_bounds__(kHeadsThreads, kGradBlocksPerSm) heads_backward_kernel(HeadsParams p, int parts) {
+__global__ void __launch_bounds__(kHeadsThreads, kGradBlocksPerSm) heads_backward_kernel(HeadsParams p) {
     constexpr int kLanes = D / 8, kRows = 32 / kLanes, kStep = kRows * kAheadGrad, kSize = kF32 ? 4 : 2;
+    using Walk = Walk<kRows, kAheadGrad>;
     extern __shared__ __align__(128) uint8_t places[];   // the warps' rings, then the angles
     __shared__ __align__(16) float weights[2 * D];
     __shared__ uint64_t barriers[kHeadsWarps * kRing];
@@ -316,51 +362,56 @@ __global__ void __launch_bounds__(kHeadsThreads, kGradBlocksPerSm) heads_backwar
     float *table = reinterpret_cast<float *>(places + kHeadsWarps * kRing * kBytes) + (threadIdx.x >> 5) * p.rot;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, at = lane % kLanes, sub = lane / kLanes;
     const Turn<kPairs> turn(p.rot, at, lane);
-    const Share mine(p, parts);
     WarpRing<kBytes> ring(places, barriers);
-    auto ask = [&](const Batch &b, int i) {
-        if (b.token >= p.tokens || lane != 0) return;
-        const int rows = min(kStep, b.end(mine) - b.h);
-        const uint16_t *x = (b.keys ? static_cast<const uint16_t *>(p.k) + b.token * p.k_stride
-                                    : static_cast<const uint16_t *>(p.q) + b.token * p.q_stride) + b.h * D;
-        const uint8_t *y = static_cast<const uint8_t *>(b.keys ? p.dk : p.dq) +
-                           (b.token * (b.keys ? p.dk_stride : p.dq_stride) + b.h * D) * kSize;
+    // (the weights' sums are a second launch, which comes up while this one is at work)
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    auto ask = [&](const Walk &b, int i) {
+        if (b.left == 0 || lane != 0) return;
+        const int rows = b.heads;
+        const bool keys = b.keys;
+        const uint16_t *x = (keys ? static_cast<const uint16_t *>(p.k) + b.token * p.k_stride
+                                  : static_cast<const uint16_t *>(p.q) + b.token * p.q_stride) + b.h * D;
+        const uint8_t *y = static_cast<const uint8_t *>(keys ? p.dk : p.dq) +
+                           (b.token * (keys ? p.dk_stride : p.dq_stride) + b.h * D) * kSize;
         mbar_arrive_expect_tx(ring.bar(i), rows * D * (2 + kSize));
         bulk_g2s(ring.place(i), x, rows * D * 2, ring.bar(i));
         bulk_g2s(ring.place(i) + kOffY, y, rows * D * kSize, ring.bar(i));
     };
-    Batch now(mine), ahead(mine);
+    Walk now(p), ahead(now);
     for (int i = 0; i < kRing; ++i) {
         ask(ahead, i);
-        ahead.advance(mine, kStep);
+        ahead.advance(p);
     }
     fill_weights<D>(p, weights);
     __syncthreads();
     float dqw[8], dkw[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) dqw[e] = dkw[e] = 0.f;
-    int pos = p.rot > 0 && mine.token < p.tokens ? __ldg(p.pos + mine.token) : 0;
-    for (int64_t token = mine.token; token < p.tokens; token += mine.step) {
+    int pos = p.rot > 0 && now.left > 0 ? __ldg(p.pos + now.token) : 0;
+    while (now.left > 0) {
+        const int64_t token = now.token;
         float c[8], s[8];
         if (p.rot > 0) {
             fill_angles(p, table, pos);
             turn.angles(table, p.rot, c, s);
-            if (token + mine.step < p.tokens) pos = __ldg(p.pos + token + mine.step);
+            if (token + 1 < p.tokens) pos = __ldg(p.pos + token + 1);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] = -s[e];   // (back)
         }
-        auto run = [&](bool keys, int end, uint16_t *out, float (&dw)[8]) {
-            if (now.token != token || now.keys != keys) return;
+        auto run = [&](bool keys, uint16_t *out, float (&dw)[8]) {
+            const auto here = [&] { return now.left > 0 && now.token == token && now.keys == keys; };
+            if (!here()) return;
             float w[8];
             load8<8>(weights + keys * D + 8 * at, w);
             out += sub * D + 8 * at;
-            while (now.token == token && now.keys == keys) {
+            do {
+                const int first = now.h, heads = now.heads;
                 ring.wait(p.err);
                 const uint32_t from = ring.place(ring.n);
 #pragma unroll
                 for (int i = 0; i < kAheadGrad; ++i) {
-                    if (now.h + i * kRows >= end) break;   // (the whole warp)
-                    const bool row = now.h + i * kRows + sub < end;
+                    if (i * kRows >= heads) break;   // (the whole warp)
+                    const bool row = i * kRows + sub < heads;
                     float x[8], g[8], o[8];
                     // (what lies behind the last head is an earlier batch's)
                     uint4 u = lds16(from + i * 512 + lane * 16);
@@ -410,17 +461,17 @@ __global__ void __launch_bounds__(kHeadsThreads, kGradBlocksPerSm) heads_backwar
                         mul2(g[e], g[e + 1], r, r);
                         muladd2(g[e], g[e + 1], x[e], x[e + 1], k, k);
                     }
-                    if (row) *reinterpret_cast<uint4 *>(out + (now.h + i * kRows) * D) = pack8(g);
+                    if (row) *reinterpret_cast<uint4 *>(out + (first + i * kRows) * D) = pack8(g);
                 }
                 __syncwarp();
                 ask(ahead, ring.n);   // (the place just read)
                 ++ring.n;
-                now.advance(mine, kStep);
-                ahead.advance(mine, kStep);
-            }
+                now.advance(p);
+                ahead.advance(p);
+            } while (here());
         };
-        run(false, mine.q1, static_cast<uint16_t *>(p.q_out) + token * p.qo_stride, dqw);
-        run(true, mine.k1, static_cast<uint16_t *>(p.k_out) + token * p.ko_stride, dkw);
+        run(false, static_cast<uint16_t *>(p.q_out) + token * p.qo_stride, dqw);
+        run(true, static_cast<uint16_t *>(p.k_out) + token * p.ko_stride, dkw);
     }
     if (p.dqw == nullptr && p.dkw == nullptr) return;
     // the lane groups of a block, in order
@@ -444,6 +495,7 @@ __global__ void __launch_bounds__(256) heads_weights_kernel(HeadsParams p, int b
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + lane;
     float s = 0.f;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
 #pragma unroll 8
     for (int b = warp; b < blocks; b += 8) s += p.partial[static_cast<int64_t>(b) * 2 * p.dim + i];
     part[warp][lane] = s;
@@ -465,8 +517,8 @@ cudaError_t with_dim(const HeadsParams &p, F &&go) {
 // count. Warps take (token, part) after (token, part), as many rounds as that makes; one costs its
 // lane groups' heads and four more for what is done for the token alone. (8192 tokens, 40 heads of
 // 64: 17 us in one part, 21 in two; 72 heads of 128: 56 and 51.)
-int parts_of(const HeadsParams &p, int blocks) {
-    const int64_t warps = static_cast<int64_t>(blocks) * kPlannedSms * kHeadsWarps;
+int parts_of(const HeadsParams &p) {
+    const int64_t warps = static_cast<int64_t>(kHeadsBlocks) * kPlannedSms * kHeadsWarps;
     const int H = p.hq + p.hk, rows = 256 / p.dim;
     int best = 1;
     int64_t least = INT64_MAX;
@@ -485,14 +537,16 @@ int heads_smem(const HeadsParams &p, int ahead, int bytes) {
     return kHeadsWarps * (kRing * 256 * ahead * bytes + p.rot * 4);
 }
 
-unsigned grid_of(const HeadsParams &p, int parts, int64_t most) {
-    const int64_t blocks = (p.tokens * parts + kHeadsWarps - 1) / kHeadsWarps;
+unsigned blocks_of(int64_t warps, int64_t most) {
+    const int64_t blocks = (warps + kHeadsWarps - 1) / kHeadsWarps;
     return static_cast<unsigned>(blocks < 1 ? 1 : blocks < most ? blocks : most);
 }
 
-}  // namespace
-
-namespace {
+// A warp for each unit of a lane group's heads, as far as there are so many.
+unsigned grad_grid(const HeadsParams &p) {
+    const int unit = 256 / p.dim;
+    return blocks_of(p.tokens * ((p.hq + unit - 1) / unit + (p.hk + unit - 1) / unit), kGradBlocks);
+}
 
 template <int D>
 cudaError_t configure_heads_dim() {
@@ -522,9 +576,9 @@ cudaError_t configure_heads() {
 cudaError_t launch_heads(const HeadsParams &p, cudaStream_t stream) {
     return with_dim(p, [&](auto d) {
         constexpr int D = decltype(d)::value;
-        const int parts = parts_of(p, kHeadsBlocks);
+        const int parts = parts_of(p);
         auto kernel = p.pairs ? heads_kernel<D, true> : heads_kernel<D, false>;
-        kernel<<<grid_of(p, parts, kHeadsBlocks * kPlannedSms), kHeadsThreads, heads_smem(p, kAhead, 2), stream>>>(p, parts);
+        kernel<<<blocks_of(p.tokens * parts, kHeadsBlocks * kPlannedSms), kHeadsThreads, heads_smem(p, kAhead, 2), stream>>>(p, parts);
         return cudaGetLastError();
     });
 }
@@ -536,15 +590,22 @@ int64_t heads_workspace(const HeadsParams &p) {
 cudaError_t launch_heads_backward(const HeadsParams &p, cudaStream_t stream) {
     return with_dim(p, [&](auto d) {
         constexpr int D = decltype(d)::value;
-        const int parts = parts_of(p, kGradBlocksPerSm);
-        const unsigned grid = grid_of(p, parts, kGradBlocks);
+        const unsigned grid = grad_grid(p);
         auto kernel = p.pairs ? (p.dout32 ? heads_backward_kernel<D, true, true> : heads_backward_kernel<D, true, false>)
                               : (p.dout32 ? heads_backward_kernel<D, false, true> : heads_backward_kernel<D, false, false>);
-        kernel<<<grid, kHeadsThreads, heads_smem(p, kAheadGrad, p.dout32 ? 6 : 4), stream>>>(p, parts);
+        kernel<<<grid, kHeadsThreads, heads_smem(p, kAheadGrad, p.dout32 ? 6 : 4), stream>>>(p);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess || (p.dqw == nullptr && p.dkw == nullptr)) return e;
-        heads_weights_kernel<<<2 * D / 32, 256, 0, stream>>>(p, static_cast<int>(grid));
-        return cudaGetLastError();
+        cudaLaunchAttribute overlap;
+        overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        overlap.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t sums{};
+        sums.gridDim = dim3(2 * D / 32);
+        sums.blockDim = dim3(256);
+        sums.stream = stream;
+        sums.attrs = &overlap;
+        sums.numAttrs = 1;
+        return cudaLaunchKernelEx(&sums, heads_weights_kernel, p, static_cast<int>(grid));
     });
 }
 
