@@ -485,7 +485,7 @@ KDA_API kda_status kda_paged_decode(const void *q, const void *k_cache, const vo
  * outside [0, pool] (after the pages given back) is reported by kda_last_device_error()
  * as KDA_ERR_BAD_PAGE_TABLE, too few free pages as KDA_ERR_OUT_OF_PAGES; nothing is
  * planned then: tables, lengths and stack stay as they are, cu_seqlens is 0
- * throughout, and every row has position 0 and slot -1. Workspace: 24 B per slot.
+ * throughout, and every row has position 0 and slot -1. Workspace: up to 12 B per slot.
  */
 KDA_API kda_status kda_page_plan(const int32_t *page_table, const int32_t *seq_lens,
                                  const int32_t *new_lens, const uint8_t *release,

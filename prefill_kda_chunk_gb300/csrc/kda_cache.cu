@@ -14,30 +14,36 @@ namespace {
 //
 // Three prefix sums over the batch: pages given back, pages needed, new tokens. With them
 // every entry is known by itself: the k-th needed page is the k-th from the top of the
-// stack. One block forms the sums and pushes the pages given back; the entries, positions
-// and slots follow in the same block where they are few, and from a grid where they are
-// many. (A page given back may lie in a row of the table that the same call fills again:
-// no entry is written before all are pushed.) Bound by two launches and their chains of
-// loads; 131072 entries copied out of place move in about a microsecond.
+// stack. Up to 1024 slots are summed by a block in shared memory. Where no output is its
+// input, a grid does all in one launch, each block with sums of its own; a call in place
+// (a page given back may lie in a row of the table that the same call fills again, so that no
+// entry is written before all are pushed) takes one block if there are few entries, else, like
+// larger batches, a launch that sums and pushes and one that fills. Bound by launches and
+// chains of loads: 256 slots with a token each, 256 pages wide, 6.7 us (in two launches 10.1); 64
+// prompts of 65536 tokens together 7.7 us (11.0).
 
 constexpr int kPlanThreads = 1024;
-// Rows, and entries copied out of place, that the one block writes itself.
+// Rows, and entries copied out of place, that one block writes.
 constexpr int64_t kPlanAlone = 8192;
-// Slots whose offsets a block holds in shared memory.
+// Slots whose sums a block holds in shared memory.
 constexpr int kPlanHeld = 1024;
 
-// What the sums hand on: the top of the stack with what was given back, the pages that were
-// there before, whether anything is planned, and the rows; then per slot the tokens held after
-// the release, the number of the first page it needs, and that of the first it gives back.
-struct PlanMeta {
+// The sums: the top of the stack with what was given back, the pages that were there before, the
+// rows, and whether anything is planned; then per slot its first row, the tokens held after the
+// release, the number of the first page it needs, and that of the first it gives back.
+struct PlanTotals {
+    int64_t top, before, rows, ok;
+};
+struct PlanHeld {   // in shared memory
+    PlanTotals all;
+    int32_t first[kPlanHeld], held[kPlanHeld], need[kPlanHeld], back[kPlanHeld];
+};
+struct PlanMeta {   // in the workspace, from one launch to the next
     int64_t *m;
-    __device__ __forceinline__ int64_t &top() const { return m[0]; }
-    __device__ __forceinline__ int64_t &before() const { return m[1]; }
-    __device__ __forceinline__ int64_t &ok() const { return m[2]; }
-    __device__ __forceinline__ int64_t &rows() const { return m[3]; }
-    __device__ __forceinline__ int64_t &held(int i) const { return m[4 + 3 * i]; }
-    __device__ __forceinline__ int64_t &base(int i) const { return m[5 + 3 * i]; }
-    __device__ __forceinline__ int64_t &back(int i) const { return m[6 + 3 * i]; }
+    __device__ __forceinline__ PlanTotals &all() const { return *reinterpret_cast<PlanTotals *>(m); }
+    __device__ __forceinline__ int32_t &held(int i) const { return reinterpret_cast<int32_t *>(m + 4)[3 * i]; }
+    __device__ __forceinline__ int32_t &need(int i) const { return reinterpret_cast<int32_t *>(m + 4)[3 * i + 1]; }
+    __device__ __forceinline__ int32_t &back(int i) const { return reinterpret_cast<int32_t *>(m + 4)[3 * i + 2]; }
 };
 
 // (of tokens that a row of the table can hold, less than 2^31)
@@ -89,25 +95,44 @@ __device__ __forceinline__ int last_from(int n, int64_t x, F &&first) {
     return lo;
 }
 
-__device__ __forceinline__ int32_t stacked(const PlanParams &p, int64_t before, int64_t k) {
-    return k < before ? p.free[k] : p.free_out[k];   // (pushed ones are in the result only)
+// The sums as plan_fill reads them, of one block's shared memory or of the workspace.
+struct NearSums {
+    const PlanHeld &h;
+    __device__ __forceinline__ int32_t first(int i) const { return h.first[i]; }
+    __device__ __forceinline__ int32_t held(int i) const { return h.held[i]; }
+    __device__ __forceinline__ int32_t need(int i) const { return h.need[i]; }
+    __device__ __forceinline__ int32_t back(int i) const { return h.back[i]; }
+};
+struct FarSums {
+    PlanMeta m;
+    const int32_t *cu;
+    __device__ __forceinline__ int32_t first(int i) const { return cu[i]; }
+    __device__ __forceinline__ int32_t held(int i) const { return m.held(i); }
+    __device__ __forceinline__ int32_t need(int i) const { return m.need(i); }
+    __device__ __forceinline__ int32_t back(int i) const { return m.back(i); }
+};
+
+// The r-th page that is given back.
+template <typename S>
+__device__ __forceinline__ int32_t given_back(const PlanParams &p, const S &s, int64_t r) {
+    const int i = last_from(p.batch, r, [&](int k) { return s.back(k); });
+    return p.table[i * p.width + (r - s.back(i))];
 }
 
-// Thread `at` of `n` that write the entries, positions and slots. held: kPlanHeld numbers of
-// the block's.
-__device__ void plan_fill(const PlanParams &p, int64_t at, int64_t n, int32_t *held) {
-    const PlanMeta m{p.meta};
-    const bool ok = m.ok() != 0, near = p.batch <= kPlanHeld;
-    const int64_t top = m.top(), before = m.before(), rows = m.rows();
-    if (near)
-        for (int i = threadIdx.x; i < p.batch; i += blockDim.x) held[i] = p.cu[i];
-    __syncthreads();
+// Thread `at` of `n` that write the entries, positions and slots; kPushed: the pages given back
+// are in free_out already.
+template <bool kPushed, typename S>
+__device__ __forceinline__ void plan_fill(const PlanParams &p, const PlanTotals &all, const S &s, int64_t at, int64_t n) {
+    const bool ok = all.ok != 0;
+    const int64_t top = all.top, before = all.before;
+    auto stacked = [&](int64_t k) {
+        return k < before ? p.free[k] : kPushed ? p.free_out[k] : given_back(p, s, k - before);
+    };
     if (p.free_out != p.free)
         for (int64_t k = at; k < p.pool; k += n)
             if (!ok || k < before || k >= top) p.free_out[k] = p.free[k];
-    auto entry = [&](int i, int64_t j, int64_t have) {
-        return stacked(p, before, top - 1 - (m.base(i) + j - have));
-    };
+            else if (!kPushed) p.free_out[k] = given_back(p, s, k - before);
+    auto entry = [&](int i, int64_t j, int64_t have) { return stacked(top - 1 - (s.need(i) + j - have)); };
     // a warp per slot: all of its row, or the new pages only
     const int lane = static_cast<int>(at & 31);
     const bool copy = p.table_out != p.table;
@@ -115,8 +140,8 @@ __device__ void plan_fill(const PlanParams &p, int64_t at, int64_t n, int32_t *h
         const uint32_t parts = copy ? static_cast<uint32_t>((p.width + 127) / 128) : 1;
         for (int64_t w = at >> 5; w < static_cast<int64_t>(p.batch) * parts; w += n >> 5) {
             const int i = static_cast<int>(static_cast<uint32_t>(w) / parts), part = static_cast<int>(static_cast<uint32_t>(w) % parts);
-            const int64_t have = pages_of(m.held(i), p.page_size),
-                          end = ok ? pages_of(m.held(i) + p.news[i], p.page_size) : have;
+            const int64_t have = pages_of(s.held(i), p.page_size),
+                          end = ok ? pages_of(static_cast<int64_t>(s.held(i)) + p.news[i], p.page_size) : have;
             const int64_t row = i * p.width, j0 = copy ? part * 128 : have,
                           j1 = copy ? (j0 + 128 < p.width ? j0 + 128 : p.width) : end;
 #pragma unroll 4
@@ -127,11 +152,10 @@ __device__ void plan_fill(const PlanParams &p, int64_t at, int64_t n, int32_t *h
     for (int64_t r = at; r < p.tokens; r += n) {
         int32_t pos = 0;
         int64_t slot = -1;
-        if (r < rows) {
-            const int i = near ? last_from(p.batch, r, [&](int k) { return held[k]; })
-                               : last_from(p.batch, r, [&](int k) { return p.cu[k]; });
-            const int64_t had = m.held(i), have = pages_of(had, p.page_size);
-            pos = static_cast<int32_t>(had + r - p.cu[i]);
+        if (r < all.rows) {
+            const int i = last_from(p.batch, r, [&](int k) { return s.first(k); });
+            const int64_t had = s.held(i), have = pages_of(had, p.page_size);
+            pos = static_cast<int32_t>(had + r - s.first(i));
             const uint32_t j = static_cast<uint32_t>(pos) / static_cast<uint32_t>(p.page_size);
             const int32_t page = j >= have ? entry(i, j, have) : p.table[i * p.width + j];
             slot = static_cast<int64_t>(page) * p.page_size + (pos - static_cast<int64_t>(j) * p.page_size);
@@ -141,14 +165,19 @@ __device__ void plan_fill(const PlanParams &p, int64_t at, int64_t n, int32_t *h
     }
 }
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p, bool alone) {
+// How a call's launches share the work: all of it in one launch, of one block or (nothing in
+// place) of a grid, or sums and pushes in a launch of one block in front of plan_fill_kernel.
+enum class PlanHow { kAlone, kGrid, kTwo };
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p, PlanHow how) {
     __shared__ Sums s_warps[kPlanThreads / 32];
-    __shared__ int32_t s_held[kPlanHeld];
+    __shared__ PlanHeld s_held;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const PlanMeta m{p.meta};
     const int tid = threadIdx.x, per = (p.batch + kPlanThreads - 1) / kPlanThreads;
     const int i0 = tid * per < p.batch ? tid * per : p.batch, i1 = i0 + per < p.batch ? i0 + per : p.batch;
     const int64_t most = p.width * p.page_size, count = *p.count;
+    const bool near = p.batch <= kPlanHeld, writes = blockIdx.x == 0;
     auto gone = [&](int i) { return p.release != nullptr && p.release[i] != 0; };
     Sums mine{0, 0, 0}, all;
     int bad = count < 0 || count > p.pool;
@@ -166,50 +195,75 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p, bool a
     Sums at = scan(mine, s_warps, all);
     const int64_t top = count + all.back;
     if (all.rows > p.tokens || top > p.pool) bad = 1;
-    const bool ok = !bad && all.need <= top, near = p.batch <= kPlanHeld;
-    if (!ok && tid == 0) atomicOr(p.err, bad ? kErrPage : kErrPool);
-    for (int i = i0; i < i1; ++i) {
+    const bool ok = !bad && all.need <= top;
+    if (!ok && writes && tid == 0) atomicOr(p.err, bad ? kErrPage : kErrPool);
+    for (int i = i0; i < i1; ++i) {   // (sums that fit 32 bits, if anything is planned)
         const int64_t len = p.lens[i], held = gone(i) ? 0 : len, add = ok ? p.news[i] : 0;
-        m.held(i) = ok ? held : len;
-        m.base(i) = at.need;
-        m.back(i) = at.back;
-        if (near) s_held[i] = static_cast<int32_t>(ok ? at.back : 0);
-        p.cu[i] = static_cast<int32_t>(ok ? at.rows : 0);
+        const int32_t first = static_cast<int32_t>(ok ? at.rows : 0), had = static_cast<int32_t>(ok ? held : len),
+                      need = static_cast<int32_t>(ok ? at.need : 0), back = static_cast<int32_t>(ok ? at.back : 0);
+        if (near) {
+            s_held.first[i] = first;
+            s_held.held[i] = had;
+            s_held.need[i] = need;
+            s_held.back[i] = back;
+        }
+        if (how == PlanHow::kTwo) {
+            m.held(i) = had;
+            m.need(i) = need;
+            m.back(i) = back;
+        }
+        if (writes) p.cu[i] = first;
         if (!ok) {
-            if (p.lens_out != p.lens) p.lens_out[i] = p.lens[i];
+            if (writes && p.lens_out != p.lens) p.lens_out[i] = static_cast<int32_t>(len);
             continue;
         }
-        p.lens_out[i] = static_cast<int32_t>(held + add);
+        if (writes) p.lens_out[i] = static_cast<int32_t>(held + add);
         at.rows += add;
         at.need += pages_of(held + add, p.page_size) - pages_of(held, p.page_size);
         if (gone(i)) at.back += pages_of(len, p.page_size);
     }
     if (tid == 0) {
-        p.cu[p.batch] = static_cast<int32_t>(ok ? all.rows : 0);
-        m.top() = ok ? top : count;
-        m.before() = count;
-        m.ok() = ok;
-        m.rows() = ok ? all.rows : 0;
-        *p.count_out = static_cast<int32_t>(ok ? top - all.need : count);
+        const PlanTotals totals{ok ? top : count, count, ok ? all.rows : 0, ok};
+        s_held.all = totals;
+        if (how == PlanHow::kTwo) m.all() = totals;
+        if (writes) {
+            p.cu[p.batch] = static_cast<int32_t>(totals.rows);
+            *p.count_out = static_cast<int32_t>(ok ? top - all.need : count);
+        }
     }
     __syncthreads();
+    if (how == PlanHow::kGrid) {
+        plan_fill<false>(p, s_held.all, NearSums{s_held}, static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid,
+                         static_cast<int64_t>(gridDim.x) * kPlanThreads);
+        return;
+    }
     if (ok)   // the pages given back (a slot's place in the order is below its row's width)
 #pragma unroll 4
-        for (int64_t r = tid; r < all.back; r += kPlanThreads) {
-            const int i = near ? last_from(p.batch, r, [&](int k) { return s_held[k]; })
-                               : last_from(p.batch, r, [&](int k) { return m.back(k); });
-            p.free_out[count + r] = p.table[i * p.width + (r - (near ? s_held[i] : m.back(i)))];
-        }
-    if (alone) {
+        for (int64_t r = tid; r < all.back; r += kPlanThreads)
+            p.free_out[count + r] = near ? given_back(p, NearSums{s_held}, r) : given_back(p, FarSums{m, p.cu}, r);
+    if (how == PlanHow::kAlone) {
         __syncthreads();
-        plan_fill(p, tid, kPlanThreads, s_held);
+        plan_fill<true>(p, s_held.all, NearSums{s_held}, tid, kPlanThreads);
     }
 }
 
 __global__ void __launch_bounds__(256) plan_fill_kernel(PlanParams p) {
-    __shared__ int32_t s_held[kPlanHeld];
+    __shared__ PlanHeld s_held;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    plan_fill(p, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, static_cast<int64_t>(gridDim.x) * 256, s_held);
+    const FarSums far{PlanMeta{p.meta}, p.cu};
+    const PlanTotals all = far.m.all();
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, n = static_cast<int64_t>(gridDim.x) * 256;
+    if (p.batch > kPlanHeld) {
+        plan_fill<true>(p, all, far, at, n);
+        return;
+    }
+    for (int i = threadIdx.x; i < p.batch; i += 256) {
+        s_held.first[i] = far.first(i);
+        s_held.held[i] = far.held(i);
+        s_held.need[i] = far.need(i);
+    }
+    __syncthreads();
+    plan_fill<true>(p, all, NearSums{s_held}, at, n);
 }
 
 // ----------------------------------------------------------- into the cache
@@ -452,25 +506,41 @@ cudaError_t launch_append_dim(const AppendParams &p, cudaStream_t stream) {
 
 }  // namespace
 
-int64_t plan_workspace(const PlanParams &p) { return 32 + 24 * static_cast<int64_t>(p.batch); }
+namespace {
+
+int64_t plan_cells(const PlanParams &p) {
+    return p.tokens + (p.table_out != p.table ? p.batch * p.width : 0) + (p.free_out != p.free ? p.pool : 0);
+}
+
+PlanHow plan_how(const PlanParams &p) {
+    if (p.batch > kPlanHeld) return PlanHow::kTwo;
+    if (plan_cells(p) <= kPlanAlone) return PlanHow::kAlone;
+    const bool in_place = p.table_out == p.table || p.free_out == p.free || p.lens_out == p.lens || p.count_out == p.count;
+    return in_place ? PlanHow::kTwo : PlanHow::kGrid;
+}
+
+}  // namespace
+
+int64_t plan_workspace(const PlanParams &p) {
+    return plan_how(p) == PlanHow::kTwo ? 32 + 12 * static_cast<int64_t>(p.batch) : 0;
+}
 
 cudaError_t configure_cache() { return cudaSuccess; }
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t stream) {
-    int64_t cells = p.tokens;
-    if (p.table_out != p.table) cells += p.batch * p.width;
-    if (p.free_out != p.free) cells += p.pool;
-    const bool alone = cells <= kPlanAlone;
-    plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, alone);
+    const PlanHow how = plan_how(p);
+    const int64_t cells = plan_cells(p), grid = (cells + kPlanThreads - 1) / kPlanThreads;
+    plan_kernel<<<how == PlanHow::kGrid ? static_cast<unsigned>(grid < kPlannedSms ? grid : kPlannedSms) : 1, kPlanThreads, 0,
+                  stream>>>(p, how);
     const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || alone) return e;
+    if (e != cudaSuccess || how != PlanHow::kTwo) return e;
     const int64_t blocks = (cells + 255) / 256, most = 8 * kPlannedSms;
     // (the second launch's blocks come up while the first one is at work)
     cudaLaunchAttribute overlap;
     overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     overlap.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t next{};
-    next.gridDim = dim3(static_cast<unsigned>(blocks < most ? blocks : most));
+    next.gridDim = dim3(static_cast<unsigned>(blocks < 1 ? 1 : blocks < most ? blocks : most));
     next.blockDim = dim3(256);
     next.stream = stream;
     next.attrs = &overlap;

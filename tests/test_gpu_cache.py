@@ -158,6 +158,28 @@ def test_plan_refuses_as_a_whole(fault, error, in_place):
     assert not got[4].any() and not got[5].any() and (got[6] == -1).all()
 
 
+@pytest.mark.parametrize("B", [70, 1100])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("fault", ["rows", "pool", "held"])
+def test_large_plan_refuses_as_a_whole(fault, in_place, B):
+    """Likewise where several blocks fill the tables."""
+    table, lens, news, free, count, gone = plan_case(B, 16, 200, 300, 4)
+    lens[B - 1], news[B - 1], gone[B - 1] = 5, 12, False
+    tokens = int(news.sum()) - (fault == "rows")
+    if fault == "pool":
+        count[0] = 0
+        gone[:] = False
+    elif fault == "held":
+        lens[B - 1] = 16 * 200 + 1
+    dev = [t.to("cuda", I32) for t in (table, lens, news, free, count)]
+    got = K.page_plan(*dev, 16, tokens, release=gone.cuda(), in_place=in_place)
+    with pytest.raises(K.KdaError, match="OUT_OF_PAGES" if fault == "pool" else "PAGE_TABLE"):
+        K.check_device_error()
+    for g, r in zip(got, (table, lens, free, count)):
+        assert torch.equal(g.cpu().long(), r)
+    assert not got[4].any() and not got[5].any() and (got[6] == -1).all()
+
+
 def test_plan_without_slots_or_tokens():
     got = K.page_plan(i32([]).view(0, 4), i32([]), i32([]), i32([3, 1]), i32([2]), 16, 3)
     assert got[4].tolist() == [0] and got[6].tolist() == [-1] * 3 and got[2].tolist() == [3, 1]
