@@ -606,6 +606,17 @@ def _need(name, t, dtype, shape, contiguous=True):
     raise ValueError(f"{name} must be a {'contiguous ' if contiguous else ''}CUDA tensor")
 
 
+def _need_rows(name, t, dtype, shape, dims=2):
+    """_need for rows of `dims` dimensions that may be strided; returns their stride."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_cuda):
+        _need(name, t, dtype, shape, contiguous=False)
+    if dims == 2 and len(shape) == 3:
+        row, head, channel = t.stride()
+        if channel == 1 and head == shape[2] and row >= shape[1] * head and shape[0] > 1:
+            return row
+    return _row_stride(t, dims, name)
+
+
 def _conv_flags(activation):
     if activation not in (None, "silu"):
         raise ValueError("activation must be None or 'silu'")
@@ -937,41 +948,43 @@ def page_plan(page_table, seq_lens, new_lens, free_pages, free_count, page_size,
 
 
 def _heads_inputs(q, k, q_weight, k_weight, inv_freq, positions):
-    """Checks of the norms' inputs; returns (leading dims, T, Hq, Hk, D, R)."""
+    """Checks of the norms' inputs; returns (T, Hq, Hk, D, R, q's and k's stride)."""
     import torch
 
-    if q.dim() not in (3, 4):
+    shape, bf16 = q.shape, torch.bfloat16
+    if len(shape) == 3:
+        T, Hq, D = shape
+    elif len(shape) == 4:
+        T, Hq, D = shape[0] * shape[1], shape[2], shape[3]
+    else:
         raise ValueError("q must be [T, Hq, D] or [B, T, Hq, D]")
-    lead = q.shape[:-2]
-    Hq, D = q.shape[-2:]
-    _need("q", q, torch.bfloat16, (*lead, Hq, D), contiguous=False)
-    Hk = 0
+    q_stride = _need_rows("q", q, bf16, shape)
+    Hk = k_stride = R = 0
     if k is not None:
-        Hk = k.shape[-2] if k.dim() == q.dim() else -1
-        _need("k", k, torch.bfloat16, (*lead, Hk, D), contiguous=False)
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None:
-            _need(name, t, torch.float32, (D,))
-    R = 0
+        like = k.shape
+        Hk = like[-2] if len(like) == len(shape) else -1
+        k_stride = _need_rows("k", k, bf16, (*shape[:-2], Hk, D))
+    if q_weight is not None:
+        _need("q_weight", q_weight, torch.float32, (D,))
+    if k_weight is not None:
+        _need("k_weight", k_weight, torch.float32, (D,))
     if inv_freq is not None:
         R = 2 * inv_freq.numel()
         _need("inv_freq", inv_freq, torch.float32, (R // 2,))
         if positions is None:
             raise ValueError("inv_freq needs positions")
-        _need("positions", positions, torch.int32, lead)
-    return lead, math.prod(lead), Hq, Hk, D, R
+        _need("positions", positions, torch.int32, shape[:-2])
+    return T, Hq, Hk, D, R, q_stride, k_stride
 
 
-def _like(name, t, x, dtypes):
-    """An output or gradient shaped like x, strided as it likes: given, or made."""
+def _like(name, t, x):
+    """An output shaped like x, strided as it likes: given, or made; and its stride."""
     import torch
 
-    if t is None:
-        return torch.empty(x.shape, dtype=dtypes[0], device=x.device)
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}")
-    _need(name, t, t.dtype, x.shape, contiguous=False)
-    return t
+    if t is not None:
+        return t, _need_rows(name, t, torch.bfloat16, x.shape)
+    t = torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return t, t.shape[-1] * t.shape[-2]
 
 
 def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positions=None, eps=1e-6,
@@ -988,14 +1001,13 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, inv_freq=None, positio
     """
     import torch
 
-    _, T, Hq, Hk, D, R = _heads_inputs(q, k, q_weight, k_weight, inv_freq, positions)
-    q_out = _like("q_out", q_out, q, (torch.bfloat16,))
-    k_out = _like("k_out", k_out, k, (torch.bfloat16,)) if k is not None else None
+    T, Hq, Hk, D, R, q_stride, k_stride = _heads_inputs(q, k, q_weight, k_weight, inv_freq, positions)
+    q_out, qo_stride = _like("q_out", q_out, q)
+    k_out, ko_stride = _like("k_out", k_out, k) if k is not None else (None, 0)
     rc = lib().kda_qk_norm_rope(
-        _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), T, Hq, Hk, D,
-        R, _row_stride(q, 2, "q"), _row_stride(k, 2, "k") if Hk else 0, float(eps),
-        ROPE_INTERLEAVED if interleaved else 0, _ptr(q_out), _row_stride(q_out, 2, "q_out"), _ptr(k_out),
-        _row_stride(k_out, 2, "k_out") if Hk else 0, _current_stream(q, stream))
+        q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), T, Hq, Hk,
+        D, R, q_stride, k_stride, eps, ROPE_INTERLEAVED if interleaved else 0, q_out.data_ptr(), qo_stride,
+        _ptr(k_out), ko_stride, _current_stream(q, stream))
     if rc != 0:
         raise KdaError(rc, "kda_qk_norm_rope")
     return q_out, k_out
@@ -1012,29 +1024,30 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, q_weight=None, k_weight=None, in
     """
     import torch
 
-    _, T, Hq, Hk, D, R = _heads_inputs(q, k, q_weight, k_weight, inv_freq, positions)
-    flags = ROPE_INTERLEAVED if interleaved else 0
-    if dq_out.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("dq_out must be bfloat16 or float32")
-    _need("dq_out", dq_out, dq_out.dtype, q.shape, contiguous=False)
-    if dq_out.dtype == torch.float32:
+    T, Hq, Hk, D, R, q_stride, k_stride = _heads_inputs(q, k, q_weight, k_weight, inv_freq, positions)
+    flags, dtype = ROPE_INTERLEAVED if interleaved else 0, dq_out.dtype
+    if dtype is torch.float32:
         flags |= ROPE_DOUT_FP32
+    elif dtype is not torch.bfloat16:
+        raise ValueError("dq_out must be bfloat16 or float32")
+    dqo_stride = _need_rows("dq_out", dq_out, dtype, q.shape)
+    dko_stride = dk_stride = 0
     if k is not None:
         if dk_out is None:
             raise ValueError("dk_out is missing")
-        _need("dk_out", dk_out, dq_out.dtype, k.shape, contiguous=False)
+        dko_stride = _need_rows("dk_out", dk_out, dtype, k.shape)
+        dk, dk_stride = _like("dk", dk, k)
     elif dk_out is not None:
         raise ValueError("dk_out needs k")
-    dq = _like("dq", dq, q, (torch.bfloat16,))
-    dk = _like("dk", dk, k, (torch.bfloat16,)) if k is not None else None
+    else:
+        dk = None
+    dq, dq_stride = _like("dq", dq, q)
     dqw = torch.empty_like(q_weight) if q_weight is not None else None
     dkw = torch.empty_like(k_weight) if k_weight is not None and k is not None else None
     rc = lib().kda_qk_norm_rope_backward(
-        _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), T, Hq, Hk, D,
-        R, _row_stride(q, 2, "q"), _row_stride(k, 2, "k") if Hk else 0, float(eps), flags, _ptr(dq_out),
-        _row_stride(dq_out, 2, "dq_out"), _ptr(dk_out), _row_stride(dk_out, 2, "dk_out") if Hk else 0,
-        _ptr(dq), _row_stride(dq, 2, "dq"), _ptr(dk), _row_stride(dk, 2, "dk") if Hk else 0, _ptr(dqw),
-        _ptr(dkw), _current_stream(q, stream))
+        q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions), T, Hq, Hk,
+        D, R, q_stride, k_stride, eps, flags, dq_out.data_ptr(), dqo_stride, _ptr(dk_out), dko_stride,
+        dq.data_ptr(), dq_stride, _ptr(dk), dk_stride, _ptr(dqw), _ptr(dkw), _current_stream(q, stream))
     if rc != 0:
         raise KdaError(rc, "kda_qk_norm_rope_backward")
     return dq, dk, dqw, dkw
@@ -1044,25 +1057,24 @@ def _fp8_cache(k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, B):
     """Checks of an 8-bit cache; returns (pages, page_size, Hkv, D, max_pages, strides)."""
     import torch
 
-    if k_cache.dim() != 4:
+    shape, table = k_cache.shape, page_table.shape
+    if len(shape) != 4:
         raise ValueError("the caches must be [pages, page_size, Hkv, D]")
-    f8, shape = torch.float8_e4m3fn, k_cache.shape
-    pages, page_size, Hkv, D = shape
-    strides = []
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _need(name, t, f8, shape, contiguous=False)
-        page, token, head, channel = t.stride()
-        if channel != 1 and D > 1:
-            raise ValueError(f"{name} must be contiguous within a head")
-        strides += (page, token, head)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _need(name, t, torch.float32, (pages, Hkv), contiguous=False)
-        strides.append(_row_stride(t, 1, name))
-    if page_table.dim() != 2:
+    if len(table) != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    _need("page_table", page_table, torch.int32, (B, page_table.shape[1]))
+    f8, width = torch.float8_e4m3fn, table[1]
+    pages, page_size, Hkv, D = shape
+    _need("k_cache", k_cache, f8, shape, contiguous=False)
+    _need("v_cache", v_cache, f8, shape, contiguous=False)
+    *k_strides, k_channel = k_cache.stride()
+    *v_strides, v_channel = v_cache.stride()
+    if (k_channel != 1 or v_channel != 1) and D > 1:
+        raise ValueError(f"{'v' if k_channel == 1 else 'k'}_cache must be contiguous within a head")
+    strides = (*k_strides, *v_strides, _need_rows("k_scale", k_scale, torch.float32, (pages, Hkv), 1),
+               _need_rows("v_scale", v_scale, torch.float32, (pages, Hkv), 1))
+    _need("page_table", page_table, torch.int32, (B, width))
     _need("seq_lens", seq_lens, torch.int32, (B,))
-    return pages, page_size, Hkv, D, page_table.shape[1], strides
+    return pages, page_size, Hkv, D, width, strides
 
 
 def paged_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, cu_seqlens=None,
@@ -1085,17 +1097,18 @@ def paged_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, seq_l
     T, B = k.shape[0], page_table.shape[0]
     pages, page_size, Hkv, D, width, strides = _fp8_cache(k_cache, v_cache, k_scale, v_scale, page_table,
                                                           seq_lens, B)
-    _need("k", k, torch.bfloat16, (T, Hkv, D), contiguous=False)
-    _need("v", v, torch.bfloat16, (T, Hkv, D), contiguous=False)
+    rows = (T, Hkv, D)
+    k_stride = _need_rows("k", k, torch.bfloat16, rows)
+    v_stride = _need_rows("v", v, torch.bfloat16, rows)
     if cu_seqlens is None:
         if T != B:
             raise ValueError("without cu_seqlens there is one row per slot")
     else:
         _need("cu_seqlens", cu_seqlens, torch.int32, (B + 1,))
     rc = lib().kda_paged_append_fp8(
-        _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
-        _ptr(seq_lens), _ptr(cu_seqlens), T, B, Hkv, D, pages, page_size, width, _row_stride(k, 2, "k"),
-        _row_stride(v, 2, "v"), *strides, _current_stream(k, stream))
+        k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_seqlens), T, B, Hkv, D,
+        pages, page_size, width, k_stride, v_stride, *strides, _current_stream(k, stream))
     if rc != 0:
         raise KdaError(rc, "kda_paged_append_fp8")
 
@@ -1110,9 +1123,10 @@ def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens
     """
     import torch
 
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be [B, Hq, D]")
-    B, Hq, D = q.shape
+    B, Hq, D = shape
     pages, page_size, Hkv, dim, width, strides = _fp8_cache(k_cache, v_cache, k_scale, v_scale,
                                                             page_table, seq_lens, B)
     _need("q", q, torch.bfloat16, (B, Hq, dim))
@@ -1121,15 +1135,15 @@ def paged_decode_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens
     if out is None:
         out = torch.empty_like(q)
     else:
-        _need("out", out, torch.bfloat16, q.shape)
+        _need("out", out, torch.bfloat16, shape)
     if lse is None:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
     else:
         _need("lse", lse, torch.float32, (B, Hq))
     rc = lib().kda_paged_decode_fp8(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
-        _ptr(seq_lens), B, Hq, Hkv, D, pages, page_size, width, *strides, float(scale), _ptr(out),
-        _ptr(lse), _current_stream(q, stream))
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        page_table.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, D, pages, page_size, width, *strides,
+        scale, out.data_ptr(), lse.data_ptr(), _current_stream(q, stream))
     if rc != 0:
         raise KdaError(rc, "kda_paged_decode_fp8")
     return out, lse
