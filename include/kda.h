@@ -580,11 +580,12 @@ KDA_API kda_status kda_qk_norm_rope_backward(
  *                for each slot (none where seq_lens is 0)
  *   D = 64 or 128 (others: KDA_ERR_UNSUPPORTED_DIM); B <= 65536; T < 2^31; (T + 2 B) * Hkv < 2^30.
  *
- * Pages that get new tokens must differ, those of one slot and those of different slots. Rows of k and v behind the last
- * slot are not read. A slot with a wrong cu_seqlens (KDA_ERR_BAD_CU_SEQLENS), length or page
- * index (KDA_ERR_BAD_PAGE_TABLE) is reported by kda_last_device_error(); its tokens, or those
- * of the bad page, are not written. Alignment: 16 bytes for k, v and the caches, k_stride and
- * v_stride multiples of 8 elements, the caches' strides of 16. No workspace.
+ * Pages that get new tokens must differ, those of one slot and those of different slots.
+ * Rows of k and v behind the last slot are not read. A slot with a wrong cu_seqlens
+ * (KDA_ERR_BAD_CU_SEQLENS), length or page index (KDA_ERR_BAD_PAGE_TABLE) is reported by
+ * kda_last_device_error(); its tokens, or those of the bad page, are not written. Alignment:
+ * 16 bytes for k, v and the caches, k_stride and v_stride multiples of 8 elements, the
+ * caches' strides of 16. No workspace.
  */
 KDA_API kda_status kda_paged_append_fp8(
     const void *k, const void *v, void *k_cache, void *v_cache, float *k_scale, float *v_scale,
@@ -609,8 +610,9 @@ KDA_API kda_status kda_paged_append_fp8(
  * elements; int32 and fp32 arrays 4 bytes. Scores, softmax and sums in fp32. The tensor
  * core takes the cache's numbers as they are; a query enters as two e4m3 terms (exact to
  * 2^-22 of its largest channel) and the weights, times the values' scales, as four (16
- * bits, below out's own rounding, to 2^-33 of the largest among 128 tokens). The sum over the cache is split over the SMs and
- * joined in a fixed order (the same call gives the same bits). Workspace: partial sums.
+ * bits, below out's own rounding, to 2^-33 of the largest among 128 tokens). The sum over
+ * the cache is split over the SMs and joined in a fixed order (the same call gives the
+ * same bits). Workspace: partial sums.
  */
 KDA_API kda_status kda_paged_decode_fp8(
     const void *q, const void *k_cache, const void *v_cache, const float *k_scale,

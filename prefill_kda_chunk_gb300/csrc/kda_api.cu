@@ -417,7 +417,8 @@ const char *kda_build_info(void) {
            "exact form for strong decay, recurrent warp-MMA chain with bulk-async staged records "
            "and a segment-parallel scan for long sequences; 64-token chunks on tcgen05 opt-in; decode step; in-kernel q/k "
            "normalisation and gate logits; token-serial and chunked gradients; short convolution, "
-           "state space scan and paged decode attention)";
+           "state space scan and paged decode attention; page plans, query and key norms with rotation, "
+           "8-bit paged cache and attention over it)";
 }
 
 int64_t kda_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t N, int has_cu_seqlens) {

@@ -17,22 +17,23 @@ namespace {
 // stack. Up to 1024 slots are summed by a block in shared memory. Where no output is its
 // input, a grid does all in one launch, each block with sums of its own; a call in place
 // (a page given back may lie in a row of the table that the same call fills again, so that no
-// entry is written before all are pushed) takes one block if there are few entries, else, like
+// entry is written before all are pushed) takes one block if there are few rows, else, like
 // larger batches, a launch that sums and pushes and one that fills. Bound by launches and
 // chains of loads: 256 slots with a token each, 256 pages wide, 6.7 us (in two launches 10.1); 64
 // prompts of 65536 tokens together 7.7 us (11.0).
 
 constexpr int kPlanThreads = 1024;
-// Rows, and entries copied out of place, that one block writes.
-constexpr int64_t kPlanAlone = 8192;
+// Rows that one block writes in place (16 slots of 64 tokens: 5.0 us, in two launches about 5.5; of
+// 256: 7.4 and 5.5).
+constexpr int64_t kPlanAlone = 2048;
 // Slots whose sums a block holds in shared memory.
 constexpr int kPlanHeld = 1024;
 
 // The sums: the top of the stack with what was given back, the pages that were there before, the
-// rows, and whether anything is planned; then per slot its first row, the tokens held after the
+// rows, and the pages needed (-1: nothing is planned); then per slot its first row, the tokens held after the
 // release, the number of the first page it needs, and that of the first it gives back.
 struct PlanTotals {
-    int64_t top, before, rows, ok;
+    int64_t top, before, rows, need;
 };
 struct PlanHeld {   // in shared memory
     PlanTotals all;
@@ -123,7 +124,7 @@ __device__ __forceinline__ int32_t given_back(const PlanParams &p, const S &s, i
 // are in free_out already.
 template <bool kPushed, typename S>
 __device__ __forceinline__ void plan_fill(const PlanParams &p, const PlanTotals &all, const S &s, int64_t at, int64_t n) {
-    const bool ok = all.ok != 0;
+    const bool ok = all.need >= 0;
     const int64_t top = all.top, before = all.before;
     auto stacked = [&](int64_t k) {
         return k < before ? p.free[k] : kPushed ? p.free_out[k] : given_back(p, s, k - before);
@@ -133,20 +134,23 @@ __device__ __forceinline__ void plan_fill(const PlanParams &p, const PlanTotals 
             if (!ok || k < before || k >= top) p.free_out[k] = p.free[k];
             else if (!kPushed) p.free_out[k] = given_back(p, s, k - before);
     auto entry = [&](int i, int64_t j, int64_t have) { return stacked(top - 1 - (s.need(i) + j - have)); };
-    // a warp per slot: all of its row, or the new pages only
-    const int lane = static_cast<int>(at & 31);
-    const bool copy = p.table_out != p.table;
-    if (ok || copy) {
-        const uint32_t parts = copy ? static_cast<uint32_t>((p.width + 127) / 128) : 1;
+    if (p.table_out != p.table) {   // 128 entries of a slot's row by a warp
+        const int lane = static_cast<int>(at & 31);
+        const uint32_t parts = static_cast<uint32_t>((p.width + 127) / 128);
         for (int64_t w = at >> 5; w < static_cast<int64_t>(p.batch) * parts; w += n >> 5) {
             const int i = static_cast<int>(static_cast<uint32_t>(w) / parts), part = static_cast<int>(static_cast<uint32_t>(w) % parts);
             const int64_t have = pages_of(s.held(i), p.page_size),
                           end = ok ? pages_of(static_cast<int64_t>(s.held(i)) + p.news[i], p.page_size) : have;
-            const int64_t row = i * p.width, j0 = copy ? part * 128 : have,
-                          j1 = copy ? (j0 + 128 < p.width ? j0 + 128 : p.width) : end;
+            const int64_t row = i * p.width, j0 = part * 128, j1 = j0 + 128 < p.width ? j0 + 128 : p.width;
 #pragma unroll 4
             for (int64_t j = j0 + lane; j < j1; j += 32)
                 p.table_out[row + j] = j >= have && j < end ? entry(i, j, have) : p.table[row + j];
+        }
+    } else {   // the new ones (a warp per slot: 1000 slots with a page each 31 us,
+        // this way 7)
+        for (int64_t k = at; k < all.need; k += n) {
+            const int i = last_from(p.batch, k, [&](int o) { return s.need(o); });
+            p.table_out[i * p.width + pages_of(s.held(i), p.page_size) + (k - s.need(i))] = stacked(top - 1 - k);
         }
     }
     for (int64_t r = at; r < p.tokens; r += n) {
@@ -223,7 +227,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p, PlanHo
         if (gone(i)) at.back += pages_of(len, p.page_size);
     }
     if (tid == 0) {
-        const PlanTotals totals{ok ? top : count, count, ok ? all.rows : 0, ok};
+        const PlanTotals totals{ok ? top : count, count, ok ? all.rows : 0, ok ? all.need : -1};
         s_held.all = totals;
         if (how == PlanHow::kTwo) m.all() = totals;
         if (writes) {
@@ -275,6 +279,11 @@ __global__ void __launch_bounds__(256) plan_fill_kernel(PlanParams p) {
 // several heads. Slot i can touch n_i / page_size + 2 pages, so candidates are numbered with
 // cu_seqlens[i] / page_size + 2 i in front of slot i, which a warp inverts with a 32-way
 // search; no launch before this one is needed. Bound by reading k and v and writing the rows.
+//
+// Measured, 8 heads of 128: one prompt of 65536 tokens, pages of 32: 77 us (5.2 TB/s, 77 % of
+// copy bandwidth; a page and head at a time 137 us, 61 % of the issue slots are taken); 16 ragged
+// prompts of 8191 tokens: 14 us (52 %: launch, table and first rows are 6 us of it); a token for
+// each of 256 slots: 4.7 us, a launch and a chain of loads.
 
 __device__ __forceinline__ int64_t items_before(const AppendParams &p, int32_t cu, int i) {
     return cu / p.c.page_size + 2 * static_cast<int64_t>(i);
@@ -489,13 +498,17 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p, int64_t ite
 template <int D>
 cudaError_t launch_append_dim(const AppendParams &p, cudaStream_t stream) {
     const int64_t cand = p.cu == nullptr ? p.tokens : p.tokens / p.c.page_size + 2 * static_cast<int64_t>(p.c.batch);
-    // Warps of an item: as many as keep a page's rows in registers, four or eight a lane.
+    // Warps of an item: as many as keep a page's rows in registers, four or eight a lane. (One
+    // warp, rows behind the first four read twice: pages of 32 tokens 108 us for 77, of 128 103
+    // for 37; with eight warps and four rows 45.)
     const int rows = p.cu == nullptr ? 1 : p.c.page_size, group = 256 / D;
     int w = 1;
     while (w < 8 && rows > 4 * group * w) w *= 2;
-    // Heads of an item: up to eight, as long as there are 32 warps for every SM.
+    // Heads of an item: up to eight, as long as there are 24 warps for every SM. (One and eight
+    // throughout: 65536 tokens 122 us and 77, 8191 tokens of 16 prompts 18 and 19, by the rule 14;
+    // a token of 256 slots 4.8 and 6.0.)
     int per = 8;
-    while (per > 1 && (per > p.c.hkv || cand * 2 * ((p.c.hkv + per - 1) / per) * w < 32 * kPlannedSms)) per /= 2;
+    while (per > 1 && (per > p.c.hkv || cand * 2 * ((p.c.hkv + per - 1) / per) * w < 24 * kPlannedSms)) per /= 2;
     const int64_t items = cand * 2 * ((p.c.hkv + per - 1) / per);
     const unsigned grid = static_cast<unsigned>((items * w + 7) / 8);
     auto kernel = w == 1 ? append_kernel<D, 1, 4> : w == 2 ? append_kernel<D, 2, 4> : w == 4 ? append_kernel<D, 4, 4>
@@ -513,10 +526,9 @@ int64_t plan_cells(const PlanParams &p) {
 }
 
 PlanHow plan_how(const PlanParams &p) {
-    if (p.batch > kPlanHeld) return PlanHow::kTwo;
-    if (plan_cells(p) <= kPlanAlone) return PlanHow::kAlone;
     const bool in_place = p.table_out == p.table || p.free_out == p.free || p.lens_out == p.lens || p.count_out == p.count;
-    return in_place ? PlanHow::kTwo : PlanHow::kGrid;
+    if (p.batch > kPlanHeld) return PlanHow::kTwo;
+    return !in_place ? PlanHow::kGrid : plan_cells(p) <= kPlanAlone ? PlanHow::kAlone : PlanHow::kTwo;
 }
 
 }  // namespace
@@ -529,18 +541,17 @@ cudaError_t configure_cache() { return cudaSuccess; }
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t stream) {
     const PlanHow how = plan_how(p);
-    const int64_t cells = plan_cells(p), grid = (cells + kPlanThreads - 1) / kPlanThreads;
-    plan_kernel<<<how == PlanHow::kGrid ? static_cast<unsigned>(grid < kPlannedSms ? grid : kPlannedSms) : 1, kPlanThreads, 0,
-                  stream>>>(p, how);
+    const int64_t blocks = (plan_cells(p) + 255) / 256;
+    auto grid = [&](int64_t most) { return static_cast<unsigned>(blocks < 1 ? 1 : blocks < most ? blocks : most); };
+    plan_kernel<<<how == PlanHow::kGrid ? grid(kPlannedSms) : 1, kPlanThreads, 0, stream>>>(p, how);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || how != PlanHow::kTwo) return e;
-    const int64_t blocks = (cells + 255) / 256, most = 8 * kPlannedSms;
     // (the second launch's blocks come up while the first one is at work)
     cudaLaunchAttribute overlap;
     overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     overlap.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t next{};
-    next.gridDim = dim3(static_cast<unsigned>(blocks < 1 ? 1 : blocks < most ? blocks : most));
+    next.gridDim = dim3(grid(8 * kPlannedSms));
     next.blockDim = dim3(256);
     next.stream = stream;
     next.attrs = &overlap;
