@@ -418,8 +418,9 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         // ----------------------------------------------------------------------------- copies
         // What a lane copies of a tile: 32 tokens of a warp, one each; or (kTma) boxes of tokens
         // of one page, K's in one warp and V's in the next, the tiles in turns where there are
-        // two such pairs (a box takes a warp 80 clocks). Pages are read two tiles of the warp's
-        // ahead, their scales one.
+        // two such pairs (a box takes a warp 80 clocks). Pages are read kDeep tiles of the warp's
+        // ahead, their scales kScale: farther where a warp has every tile (2 x 131072 tokens, pages
+        // of 17: 116 us, with 2 and 1 145, with 6 and 3 127; pages of one, 65536: 70, 105 and 98).
         const int cw = warp - S::kCopyWarp, turns = kTma ? B::kCopyWarps / 2 : 1, turn = kTma ? cw / 2 : 0;
         const bool of_v = cw & 1;
         const int offset = kTma ? (lane & 15) << maps.shift : 32 * cw + lane;
@@ -458,8 +459,12 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             if (!kTma || (of_v && lane >= 16)) a.ks = __ldg(c.ks + a.page * c.ks_page + a.kv);
             if (!kTma || (of_v && lane < 16)) a.vs = __ldg(c.vs + a.page * c.vs_page + a.kv);
         };
-        Spot now = look(), next = look();
-        scales(now);
+        constexpr int kDeep = kTma ? 2 : 4, kScale = kTma ? 1 : 2;
+        Spot spots[kDeep];
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) spots[i] = look();
+#pragma unroll
+        for (int i = 0; i < kScale; ++i) scales(spots[i]);
         Place<S::kKeys> kp;
         Place<S::kValues> vp;
         auto place_on = [&](int by) {
@@ -470,9 +475,10 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         };
         place_on(turn);
         int n = turn;
-        for (; now.len > 0 && n < p.stall; n += turns, place_on(turns)) {
+        for (; spots[0].len > 0 && n < p.stall; n += turns, place_on(turns)) {
             const Spot far = look();
-            scales(next);
+            scales(spots[kScale]);
+            const Spot &now = spots[0];
             const int ks = kp.at, vs = vp.at;
             if ((!kTma || !of_v) && kp.turn > 0) wait(B::kKEmpty + ks, kp.turn - 1);
             if ((!kTma || of_v) && vp.turn > 0) wait(B::kVEmpty + vs, vp.turn - 1);
@@ -514,8 +520,9 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 sc[kTile + offset] = now.vs;
                 arrive(B::kVFull + vs);
             }
-            now = next;
-            next = far;
+#pragma unroll
+            for (int i = 0; i + 1 < kDeep; ++i) spots[i] = spots[i + 1];
+            spots[kDeep - 1] = far;
         }
         // the last copies land before the block ends, whatever the others do
         cp_async_wait_all();
@@ -903,7 +910,7 @@ constexpr int heads_of(int group) { return group <= 8 ? 8 : 16; }
 
 // Pages of a multiple of 8 tokens are copied by the tensor memory accelerator, in boxes of
 // the largest power of two that divides them; others by threads, 16 bytes a time (2 x 131072
-// tokens, pages of 32: 92 us and 150; 64 ragged sequences, pages of 64: 50 and 75).
+// tokens, pages of 32: 92 us and 115; 64 ragged sequences, pages of 64: 50 and 68).
 int box_rows(const Cache8 &c) {
     const int two = c.page_size & -c.page_size;
     return two < 8 ? 0 : two < kTile ? two : kTile;
