@@ -14,7 +14,7 @@ namespace {
 //
 // Three prefix sums over the batch: pages given back, pages needed, new tokens. With them
 // every entry is known by itself: the k-th needed page is the k-th from the top of the
-// stack. Up to 1024 slots are summed by a block in shared memory. Where no output is its
+// stack. The sums of up to 4096 slots are in a block's shared memory. Where no output is its
 // input, a grid does all in one launch, each block with sums of its own; a call in place
 // (a page given back may lie in a row of the table that the same call fills again, so that no
 // entry is written before all are pushed) takes one block if there are few rows, else, like
@@ -26,18 +26,15 @@ constexpr int kPlanThreads = 1024;
 // Rows that one block writes in place (16 slots of 64 tokens: 5.0 us, in two launches about 5.5; of
 // 256: 7.4 and 5.5).
 constexpr int64_t kPlanAlone = 2048;
-// Slots whose sums a block holds in shared memory.
-constexpr int kPlanHeld = 1024;
+// Slots whose sums a block of plan_kernel holds in shared memory, and one of plan_fill_kernel,
+// which has to load them first.
+constexpr int kPlanHeld = 4096, kFillHeld = 1024;
 
 // The sums: the top of the stack with what was given back, the pages that were there before, the
 // rows, and the pages needed (-1: nothing is planned); then per slot its first row, the tokens held after the
 // release, the number of the first page it needs, and that of the first it gives back.
 struct PlanTotals {
     int64_t top, before, rows, need;
-};
-struct PlanHeld {   // in shared memory
-    PlanTotals all;
-    int32_t first[kPlanHeld], held[kPlanHeld], need[kPlanHeld], back[kPlanHeld];
 };
 struct PlanMeta {   // in the workspace, from one launch to the next
     int64_t *m;
@@ -98,11 +95,12 @@ __device__ __forceinline__ int last_from(int n, int64_t x, F &&first) {
 
 // The sums as plan_fill reads them, of one block's shared memory or of the workspace.
 struct NearSums {
-    const PlanHeld &h;
-    __device__ __forceinline__ int32_t first(int i) const { return h.first[i]; }
-    __device__ __forceinline__ int32_t held(int i) const { return h.held[i]; }
-    __device__ __forceinline__ int32_t need(int i) const { return h.need[i]; }
-    __device__ __forceinline__ int32_t back(int i) const { return h.back[i]; }
+    int32_t *f;   // [4][n]
+    int n;
+    __device__ __forceinline__ int32_t &first(int i) const { return f[i]; }
+    __device__ __forceinline__ int32_t &held(int i) const { return f[n + i]; }
+    __device__ __forceinline__ int32_t &need(int i) const { return f[2 * n + i]; }
+    __device__ __forceinline__ int32_t &back(int i) const { return f[3 * n + i]; }
 };
 struct FarSums {
     PlanMeta m;
@@ -175,9 +173,11 @@ enum class PlanHow { kAlone, kGrid, kTwo };
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p, PlanHow how) {
     __shared__ Sums s_warps[kPlanThreads / 32];
-    __shared__ PlanHeld s_held;
+    __shared__ PlanTotals s_all;
+    extern __shared__ int32_t s_sums[];   // up to kPlanHeld slots
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const PlanMeta m{p.meta};
+    const NearSums held_here{s_sums, p.batch};
     const int tid = threadIdx.x, per = (p.batch + kPlanThreads - 1) / kPlanThreads;
     const int i0 = tid * per < p.batch ? tid * per : p.batch, i1 = i0 + per < p.batch ? i0 + per : p.batch;
     const int64_t most = p.width * p.page_size, count = *p.count;
@@ -206,10 +206,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p, PlanHo
         const int32_t first = static_cast<int32_t>(ok ? at.rows : 0), had = static_cast<int32_t>(ok ? held : len),
                       need = static_cast<int32_t>(ok ? at.need : 0), back = static_cast<int32_t>(ok ? at.back : 0);
         if (near) {
-            s_held.first[i] = first;
-            s_held.held[i] = had;
-            s_held.need[i] = need;
-            s_held.back[i] = back;
+            held_here.first(i) = first;
+            held_here.held(i) = had;
+            held_here.need(i) = need;
+            held_here.back(i) = back;
         }
         if (how == PlanHow::kTwo) {
             m.held(i) = had;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p, PlanHo
     }
     if (tid == 0) {
         const PlanTotals totals{ok ? top : count, count, ok ? all.rows : 0, ok ? all.need : -1};
-        s_held.all = totals;
+        s_all = totals;
         if (how == PlanHow::kTwo) m.all() = totals;
         if (writes) {
             p.cu[p.batch] = static_cast<int32_t>(totals.rows);
@@ -237,37 +237,38 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(PlanParams p, PlanHo
     }
     __syncthreads();
     if (how == PlanHow::kGrid) {
-        plan_fill<false>(p, s_held.all, NearSums{s_held}, static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid,
+        plan_fill<false>(p, s_all, held_here, static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid,
                          static_cast<int64_t>(gridDim.x) * kPlanThreads);
         return;
     }
     if (ok)   // the pages given back (a slot's place in the order is below its row's width)
 #pragma unroll 4
         for (int64_t r = tid; r < all.back; r += kPlanThreads)
-            p.free_out[count + r] = near ? given_back(p, NearSums{s_held}, r) : given_back(p, FarSums{m, p.cu}, r);
+            p.free_out[count + r] = near ? given_back(p, held_here, r) : given_back(p, FarSums{m, p.cu}, r);
     if (how == PlanHow::kAlone) {
         __syncthreads();
-        plan_fill<true>(p, s_held.all, NearSums{s_held}, tid, kPlanThreads);
+        plan_fill<true>(p, s_all, held_here, tid, kPlanThreads);
     }
 }
 
 __global__ void __launch_bounds__(256) plan_fill_kernel(PlanParams p) {
-    __shared__ PlanHeld s_held;
+    __shared__ int32_t s_sums[3 * kFillHeld];
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const FarSums far{PlanMeta{p.meta}, p.cu};
     const PlanTotals all = far.m.all();
     const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, n = static_cast<int64_t>(gridDim.x) * 256;
-    if (p.batch > kPlanHeld) {
+    if (p.batch > kFillHeld) {
         plan_fill<true>(p, all, far, at, n);
         return;
     }
+    const NearSums near{s_sums, p.batch};   // (but for `back`)
     for (int i = threadIdx.x; i < p.batch; i += 256) {
-        s_held.first[i] = far.first(i);
-        s_held.held[i] = far.held(i);
-        s_held.need[i] = far.need(i);
+        near.first(i) = far.first(i);
+        near.held(i) = far.held(i);
+        near.need(i) = far.need(i);
     }
     __syncthreads();
-    plan_fill<true>(p, all, NearSums{s_held}, at, n);
+    plan_fill<true>(p, all, near, at, n);
 }
 
 // ----------------------------------------------------------- into the cache
@@ -537,13 +538,16 @@ int64_t plan_workspace(const PlanParams &p) {
     return plan_how(p) == PlanHow::kTwo ? 32 + 12 * static_cast<int64_t>(p.batch) : 0;
 }
 
-cudaError_t configure_cache() { return cudaSuccess; }
+cudaError_t configure_cache() {
+    return cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * kPlanHeld);
+}
 
 cudaError_t launch_plan(const PlanParams &p, cudaStream_t stream) {
     const PlanHow how = plan_how(p);
     const int64_t blocks = (plan_cells(p) + 255) / 256;
     auto grid = [&](int64_t most) { return static_cast<unsigned>(blocks < 1 ? 1 : blocks < most ? blocks : most); };
-    plan_kernel<<<how == PlanHow::kGrid ? grid(kPlannedSms) : 1, kPlanThreads, 0, stream>>>(p, how);
+    const int held = p.batch <= kPlanHeld ? 16 * p.batch : 0;
+    plan_kernel<<<how == PlanHow::kGrid ? grid(kPlannedSms) : 1, kPlanThreads, held, stream>>>(p, how);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || how != PlanHow::kTwo) return e;
     // (the second launch's blocks come up while the first one is at work)

@@ -105,6 +105,12 @@ def test_plan(B, page, width, new, extra):
     assert all(a.data_ptr() == b.data_ptr() for a, b in zip(got, state))
 
 
+@pytest.mark.parametrize("B,page,width,new", [(4096, 16, 3, 2), (4097, 16, 3, 2), (9000, 8, 2, 16)])
+def test_plan_of_many_slots(B, page, width, new):
+    """At and past the slots whose sums a block holds."""
+    test_plan(B, page, width, new, 2)
+
+
 def test_plan_steps_follow_one_another():
     """A batch served for a while, in place, with slots given back and filled again."""
     g = torch.Generator().manual_seed(7)
