@@ -34,7 +34,8 @@
 //
 // Measured (copy bandwidth: 1340 clocks for a tile of D = 128): 2 sequences of 131072 tokens, 32
 // heads over 8 of 128: 92 us (5.8 TB/s, 86 % of copy bandwidth); 64 sequences of 1 to 16384
-// tokens, 64 heads over 8: 50 us (67 %); one of 700: 11 us, a chain of latencies. What a tile
+// tokens, 64 heads over 8: 50 us (67 %); 256 of 1000, 32 heads over 8: 95 us (81 %); one of 700:
+// 11 us, a chain of latencies. What a tile
 // takes the weights' warps, some 1250 clocks with 8 heads, bounds D = 64 (8 x 32768 tokens: 72
 // us, 55 %), and 1600 with 16 heads those (8 x 65536, 2 key-value heads: 64 us, 62 %).
 
@@ -357,7 +358,8 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
     // What piece pc is, where w is (or, if there are no more, the end), and its queries as two
     // terms each.
     auto queries = [&](int pc, bool more) {
-        constexpr int kPer = D / 32;   // channels of a lane
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+        const int at = lane % kLanes, sub = lane / kLanes;
         const int buf = pc % S::kQBufs;
         if (pc >= S::kQBufs) wait(B::kQEmpty + buf, pc / S::kQBufs - 1);
         if (stopped()) return;   // (others may still be reading)
@@ -372,40 +374,42 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         if (lane == 0)
             *piece = {w.tile0, w.tile1, w.len, w.tiles, static_cast<int64_t>(w.b) * p.hq + head0, w.item_at,
                       w.b, w.item, heads, 0};
+        // D / 8 lanes take a head, 16 bytes each (a warp taking head after head, unrolled: 256
+        // sequences of 1000 tokens 101 us for 95, 200 of 11 tokens 34 for 29)
         const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) +
-                                 (static_cast<int64_t>(w.b) * p.hq + head0) * D + kPer * lane;
-        uint32_t x[H][kPer / 2];
+                                 (static_cast<int64_t>(w.b) * p.hq + head0 + sub) * D + 8 * at;
+        uint4 x[H / kRows];
 #pragma unroll
-        for (int h = 0; h < H; ++h)
+        for (int i = 0; i < H / kRows; ++i)
+            x[i] = i * kRows + sub < heads ? __ldg(reinterpret_cast<const uint4 *>(q + i * kRows * D)) : make_uint4(0, 0, 0, 0);
+        uint8_t *dst = smem + S::kOffQ + buf * S::kQRows * D + 8 * (at & 1);
+#pragma unroll 1
+        for (int row = sub; row < H; row += kRows) {   // (rolled: shorter code)
+            uint32_t u[4] = {x[0].x, x[0].y, x[0].z, x[0].w}, top = 0;
 #pragma unroll
-            for (int e = 0; e < kPer / 2; ++e)
-                x[h][e] = h < heads ? __ldg(reinterpret_cast<const uint32_t *>(q + h * D) + e) : 0u;
-        uint8_t *dst = smem + S::kOffQ + buf * S::kQRows * D;
-        float mul = 0.f;
+            for (int i = 0; i + 1 < H / kRows; ++i) x[i] = x[i + 1];
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-            uint32_t top = 0;
+            for (int e = 0; e < 4; ++e) top = __vmaxu2(top, u[e] & 0x7fff7fffu);
 #pragma unroll
-            for (int e = 0; e < kPer / 2; ++e) top = max(top, max(x[h][e] & 0x7fffu, (x[h][e] >> 16) & 0x7fffu));
-            top = __reduce_max_sync(0xffffffffu, top);
+            for (int m = kLanes / 2; m > 0; m >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, m));
+            top = max(top & 0xffffu, top >> 16);
             // 2^-k brings the row's largest channel below 2^8; an infinity or NaN makes its
             // scores NaN
             const int k = max(static_cast<int>(top >> 7) - 127 - 7, -126);
             const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
             const float up = top >= 0x7f80u ? CUDART_NAN_F : __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-            if (lane == h) mul = p.scale * 1.44269504088896341f * up;
+            if (at == 0) reinterpret_cast<float *>(smem + S::kOffMul)[buf * H + row] = p.scale * 1.44269504088896341f * up;
+            uint32_t terms[kQTerms][2] = {};
 #pragma unroll
-            for (int e = 0; e < kPer / 2; ++e) {
-                float a = __uint_as_float(x[h][e] << 16) * down, b = __uint_as_float(x[h][e] & 0xffff0000u) * down;
+            for (int e = 0; e < 4; ++e) {
+                float a = __uint_as_float(u[e] << 16) * down, b = __uint_as_float(u[e] & 0xffff0000u) * down;
 #pragma unroll
-                for (int t = 0; t < kQTerms; ++t) {
-                    const int row = t * H + h, byte = kPer * lane + 2 * e;
-                    *reinterpret_cast<uint16_t *>(dst + swizzled<D>(row, byte >> 4) + (byte & 15)) =
-                        static_cast<uint16_t>(take8(a, b));
-                }
+                for (int t = 0; t < kQTerms; ++t) terms[t][e / 2] |= take8(a, b) << (e % 2 * 16);
             }
+#pragma unroll
+            for (int t = 0; t < kQTerms; ++t)
+                *reinterpret_cast<uint2 *>(dst + swizzled<D>(t * H + row, at >> 1)) = make_uint2(terms[t][0], terms[t][1]);
         }
-        if (lane < H) reinterpret_cast<float *>(smem + S::kOffMul)[buf * H + lane] = mul;
         fence_async();
         arrive(B::kQFull + buf);
     };
@@ -586,7 +590,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             }
         }
         drain(1);
-    } else if (warp == S::kQueryWarp) {
+    } else if (S::kQueryWarp != S::kMmaWarpO && warp == S::kQueryWarp) {
         bool more = true;
         for (int pc = 0; more; ++pc) {
             more = w.next(lens, items);
@@ -833,7 +837,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 constexpr int kHs = H / 4, kPieces = 32 / kHs;
                 const int h = q * kHs + lane % kHs;
                 float most = -CUDART_INF_F, sum = 0.f;
-#pragma unroll 2
+#pragma unroll 1
                 for (int k = c0 + lane / kHs; k <= c1; k += kPieces) {
                     const float mk = __ldcg(part(k) + H * (D + 1) + h), lk = __ldcg(part(k) + H * (D + 2) + h);
                     const float now = fmaxf(most, mk), base = finite_base(now);
@@ -860,6 +864,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             for (int h = 0; h < H; ++h) acc[h] = 0.f;
             // 32 numbers on their way at a time
             constexpr int kBatch = 32 / H;
+#pragma unroll 1
             for (int k0 = c0; k0 <= c1; k0 += kBatch) {
                 float by[kBatch], v[kBatch][H];
 #pragma unroll
