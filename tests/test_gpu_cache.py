@@ -702,7 +702,15 @@ def test_decode_longest_cache():
 @pytest.mark.parametrize("lens,tile", [([300], 0), ([40000, 9, 3000], 2), ([40000, 9, 3000], 3)])
 def test_decode_wait_runs_out_then_clean_call(lens, tile, page):
     """(A share of the second batch is four or five tiles of 128 tokens.)"""
-    case = cache_case(lens, 16, 2, 128, page)
+    runs_out_then_clean(cache_case(lens, 16, 2, 128, page), tile)
+
+
+@pytest.mark.parametrize("Hq,D,page", [(32, 128, 16), (32, 128, 17), (16, 64, 16), (32, 64, 17)])
+def test_decode_wait_runs_out_in_other_shapes(Hq, D, page):
+    runs_out_then_clean(cache_case([40000, 9, 3000], Hq, 2, D, page), 2)
+
+
+def runs_out_then_clean(case, tile):
     ref = K.paged_decode_fp8(*case)
     K.check_device_error()
     assert K.kda_test_stall_paged_fp8(tile) == 0
