@@ -353,6 +353,17 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t u, float f) {
     return o[0] | (o[1] << 16);
 }
 
+// cu_seqlens as a whole, by the first block of 256 threads.
+__device__ __forceinline__ void check_cu(const AppendParams &p) {
+    if (blockIdx.x != 0 || p.cu == nullptr) return;
+    bool bad = false;
+    for (int i = threadIdx.x; i <= p.c.batch; i += 256) {
+        const int32_t a = i > 0 ? __ldg(p.cu + i - 1) : 0, b = __ldg(p.cu + i);
+        bad |= b < a || b > p.tokens || (i == 0 && b != 0);
+    }
+    if (bad) atomicOr(p.c.err, kErrBadCu);
+}
+
 // W warps for each item of `per` heads; kKeep rows of a lane group in registers.
 template <int D, int W, int kKeep>
 __global__ void __launch_bounds__(256) append_kernel(AppendParams p, int64_t items, int per) {
@@ -360,14 +371,7 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p, int64_t ite
     __shared__ uint32_t s_top[3][8];
     const Cache8 &c = p.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W;
-    if (blockIdx.x == 0 && p.cu != nullptr) {   // the table as a whole, once
-        bool bad = false;
-        for (int i = threadIdx.x; i <= c.batch; i += 256) {
-            const int32_t a = i > 0 ? __ldg(p.cu + i - 1) : 0, b = __ldg(p.cu + i);
-            bad |= b < a || b > p.tokens || (i == 0 && b != 0);
-        }
-        if (bad) atomicOr(c.err, kErrBadCu);
-    }
+    check_cu(p);
     // ---- which rows (the warps of an item agree on everything)
     const int64_t item = (static_cast<int64_t>(blockIdx.x) * 8 + warp) / W;
     if (item >= items) return;
@@ -496,8 +500,84 @@ __global__ void __launch_bounds__(256) append_kernel(AppendParams p, int64_t ite
     }
 }
 
+// Pages of one token: every page starts anew, so that a row and head is all there is to a scale. A
+// warp takes a token's keys and values, D / 8 lanes a head, four sets of heads on their way at a
+// time. (As items of a page, one row in a warp: 32854 tokens, 8 heads of
+// 64 167 us, this way 27.)
+template <int D>
+__global__ void __launch_bounds__(256) append_rows_kernel(AppendParams p) {
+    constexpr int kLanes = D / 8, kRows = 32 / kLanes, kSets = 4;
+    const Cache8 &c = p.c;
+    const int lane = threadIdx.x & 31, at = lane % kLanes, sub = lane / kLanes;
+    check_cu(p);
+    const int64_t tok = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (tok >= p.tokens) return;
+    int64_t i = tok, a = tok, b = tok + 1;
+    if (p.cu != nullptr) {
+        int lo = 0, hi = c.batch;   // the last slot that starts at tok or in front of it, in [lo, hi)
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, k = lo + lane * step;
+            const int m = __popc(__ballot_sync(0xffffffffu, k < hi && __ldg(p.cu + k) <= tok));
+            lo += (m > 0 ? m - 1 : 0) * step;
+            hi = lo + step < hi ? lo + step : hi;
+        }
+        i = lo;
+        a = __ldg(p.cu + i);
+        b = __ldg(p.cu + i + 1);
+        if (a < 0 || a > tok || b <= tok || b > p.tokens) return;
+    }
+    const int64_t len = __ldg(c.lens + i), j = len - b + tok;   // (a page of the slot's)
+    if (p.cu == nullptr && len == 0) return;
+    if (len < b - a || len > c.max_pages) {
+        if (lane == 0) atomicOr(c.err, kErrPage);
+        return;
+    }
+    const int page = __ldg(c.table + i * c.max_pages + j);
+    if (page < 0 || page >= c.pages) {
+        if (lane == 0) atomicOr(c.err, kErrPage);
+        return;
+    }
+    for (int h0 = 0; h0 < 2 * c.hkv; h0 += kSets * kRows) {   // heads of the keys, then of the values
+        uint4 x[kSets];
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) {
+            const int h = h0 + s * kRows + sub;
+            const bool is_v = h >= c.hkv;
+            const uint16_t *src = is_v ? static_cast<const uint16_t *>(p.v) + tok * p.v_stride + (h - c.hkv) * D
+                                       : static_cast<const uint16_t *>(p.k) + tok * p.k_stride + h * D;
+            x[s] = h < 2 * c.hkv ? *reinterpret_cast<const uint4 *>(src + 8 * at) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) {
+            const int h = h0 + s * kRows + sub;
+            auto most = [&](uint32_t top) {
+#pragma unroll
+                for (int m = kLanes / 2; m > 0; m >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, m));
+                return max(top & 0xffffu, top >> 16);
+            };
+            uint32_t top = most(largest<false>(0, x[s]));
+            const bool odd = top >= kOdd;
+            if (__any_sync(0xffffffffu, odd)) {   // infinities and NaN do not count
+                const uint32_t fine = most(largest<true>(0, x[s]));
+                if (odd) top = fine;
+            }
+            const float scale = __uint_as_float(static_cast<uint32_t>(scale_exponent(top) + 127) << 23);
+            if (h >= 2 * c.hkv) continue;
+            const bool is_v = h >= c.hkv;
+            const int head = is_v ? h - c.hkv : h;
+            uint8_t *dst = is_v ? c.v + page * c.v_page + head * c.v_head : c.k + page * c.k_page + head * c.k_head;
+            *reinterpret_cast<uint2 *>(dst + 8 * at) = quantise(x[s], 1.f / scale, odd);
+            if (at == 0) (is_v ? c.vs + page * c.vs_page : c.ks + page * c.ks_page)[head] = scale;
+        }
+    }
+}
+
 template <int D>
 cudaError_t launch_append_dim(const AppendParams &p, cudaStream_t stream) {
+    if (p.c.page_size == 1) {
+        append_rows_kernel<D><<<static_cast<unsigned>((p.tokens + 7) / 8), 256, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
     const int64_t cand = p.cu == nullptr ? p.tokens : p.tokens / p.c.page_size + 2 * static_cast<int64_t>(p.c.batch);
     // Warps of an item: as many as keep a page's rows in registers, four or eight a lane. (One
     // warp, rows behind the first four read twice: pages of 32 tokens 108 us for 77, of 128 103

@@ -423,6 +423,43 @@ def test_append(rounds, H, D, page, layout):
         same_cache(dev, ref)
 
 
+@pytest.mark.parametrize("H,D,layout", [(8, 64, "page"), (1, 64, "heads first"), (3, 128, "heads first"),
+                                        (17, 128, "page")])
+def test_append_pages_of_one(H, D, layout):
+    """Slots more than a warp's lanes, some without new tokens; infinities and NaN; a bad page."""
+    B = 75
+    g = torch.Generator().manual_seed(H)
+    old = torch.randint(0, 4, (B,), generator=g).tolist()
+    new = torch.randint(0, 6, (B,), generator=g).tolist()
+    new[-1] = 0
+    lens = [a + b for a, b in zip(old, new)]
+    table, pages = deal(lens, 1, 2, H)
+    dev = empty_cache(pages, 1, H, D, layout)
+    ref = [(c.cpu().double(), s.cpu().double()) for c, s in ((dev[0], dev[2]), (dev[1], dev[3]))]
+    T = sum(new)
+    x = make(H + D)(T + 9, 2, H, D)
+    x[5, 0, 0, 3], x[6, 1, H - 1, 0], x[7] = math.inf, math.nan, -math.inf
+    x[T:] = float("nan")
+    k, v, cu = x[:, 0], x[:, 1], cu_of(new)
+    K.paged_append_fp8(k, v, *dev, table.cuda(), i32(lens), cu.cuda())
+    K.check_device_error()
+    for y, (codes, scale) in zip((k, v), ref):
+        C.append(y, codes, scale, table, lens, cu)
+    same_cache(dev, ref)
+    bad, at = table.clone(), max(i for i in range(B) if new[i])
+    bad[at, lens[at] - 1] = pages
+    again = empty_cache(pages, 1, H, D, layout)
+    K.paged_append_fp8(k, v, *again, bad.cuda(), i32(lens), cu.cuda())
+    with pytest.raises(K.KdaError, match="PAGE_TABLE"):
+        K.check_device_error()
+    page = int(table[at, lens[at] - 1])
+    for a, b in zip(again, dev):
+        a, b = (t.view(torch.uint8) if t.dtype == F8 else t.view(I32) for t in (a, b))
+        keep = torch.arange(pages, device="cuda") != page
+        assert torch.equal(a[keep], b[keep])
+    assert torch.isnan(again[2][page]).all()
+
+
 def test_append_ends_of_the_range():
     """Zeros, the smallest and the largest bf16 numbers, infinities and NaN, values at the
     borders of two scales, and scales that a caller has set."""
