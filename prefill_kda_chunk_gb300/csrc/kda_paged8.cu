@@ -30,14 +30,14 @@
 // the tiles' weights, four warps add up the outputs, one prepares the queries and says what
 // the block's next piece is. Shares, pieces and their join: kda_pieces.cuh; a piece that is not
 // a whole item leaves its sums in the workspace, and the last block to arrive joins them in
-// the order of the blocks.
+// the order of the blocks (where they are many, groups of them first).
 //
 // Measured (copy bandwidth: 1340 clocks for a tile of D = 128): 2 sequences of 131072 tokens, 32
 // heads over 8 of 128: 92 us (5.8 TB/s, 86 % of copy bandwidth); 64 sequences of 1 to 16384
 // tokens, 64 heads over 8: 50 us (67 %); 256 of 1000, 32 heads over 8: 95 us (81 %); one of 700:
 // 11 us, a chain of latencies. What a tile
 // takes the weights' warps, some 1250 clocks with 8 heads, bounds D = 64 (8 x 32768 tokens: 72
-// us, 55 %), and 1600 with 16 heads those (8 x 65536, 2 key-value heads: 64 us, 62 %).
+// us, 55 %), and 1600 with 16 heads those (8 x 65536, 2 key-value heads: 68 us, 58 %).
 
 #include <cuda.h>
 #include <cuda_fp8.h>
@@ -65,6 +65,7 @@ constexpr int groups_of(int) { return 2; }
 constexpr int copy_warps(int heads, bool tma) { return tma && heads > 8 ? 2 : 4; }
 constexpr int threads_of(int heads, bool tma) { return 32 * (4 * groups_of(heads) + (heads > 8 ? 6 : 7) + copy_warps(heads, tma)); }
 using Paged8Split = Split<kTile, kItemCost>;
+constexpr int kJoined = 8, kFlat = 16;   // pieces of a group; pieces that are joined without groups
 
 // A piece of the block's share, as the queries' warp hands it to the other roles beside the
 // queries themselves (with each going through the share by itself 256 sequences of 1000
@@ -100,8 +101,8 @@ struct Shape {
     static constexpr int kOffPiece = kOffMul + kQBufs * H * 4;      // [kQBufs]
     static constexpr int kOffSum = kOffPiece + kQBufs * static_cast<int>(sizeof(Piece));   // [2][weights' warps][H]
     static constexpr int kOffTop = kOffSum + 2 * 4 * kGroups * H * 4;         // [2][group][H]
-    static constexpr int kOffJoin = kOffTop + 2 * kGroups * H * 4;        // [2][H]
-    static constexpr int kOffCast = kOffJoin + 2 * H * 4;           // [weights' and outputs' warps][3][H]
+    static constexpr int kOffJoin = kOffTop + 2 * kGroups * H * 4;        // [3][H]
+    static constexpr int kOffCast = kOffJoin + 3 * H * 4;           // [weights' and outputs' warps][3][H]
     static constexpr int kOffBar = kOffCast + (4 * kGroups + 4) * 3 * H * 4;
     // tensor memory columns: S, then O
     static constexpr int kTmO = kSBufs * kQRows;
@@ -281,6 +282,122 @@ struct Paged8Maps {
     CUtensorMap k, v;   // (channel, token, head, page), boxes of 2^shift tokens
     int shift;
 };
+
+// An arrival at a counter of n: the last one finds it complete, and sets it back for the next call.
+__device__ __forceinline__ bool last_of(int *counter, int n) {
+    const bool last = add_acq_rel(counter, 1) == n - 1;
+    if (last) *counter = 0;
+    return last;
+}
+
+// An item's pieces, in the blocks c0 .. c1, are joined by the last of them to arrive; more than kFlat
+// in groups of kJoined first, and then the groups (8 ragged sequences up to 43116 tokens, one
+// key-value head: 24 us, all at once 48). By the outputs' warps, at a piece's end, and not inlined:
+// the roles' loops run slower with more code between them (256 sequences of 1000 tokens:
+// inlined 110 us, this way 95; 16 heads, 8 x 65536, 72 and 68).
+template <int D, int H>
+__device__ __noinline__ void join_pieces(float *slots, int *arrived, int *item_counter, int c0, int c1, int slot0,
+                                         __nv_bfloat16 *out, float *lse, int heads, float *join, int *s_last) {
+    using S = Shape<D, H>;
+    constexpr int kOutSync = 1 + S::kGroups;
+    const int lane = threadIdx.x & 31, q = threadIdx.x >> 5 & 3, t = 32 * q + lane;
+    const int d = D == 128 ? t : 16 * q + lane;
+    const bool has = D == 128 || lane < 16;
+    auto slot_at = [&](int k) { return k == c0 ? slot0 : 2 * k; };
+    float acc[H];
+    int lo = c0, step = 1, n = c1 - c0 + 1;
+    bool whole_item = n <= kFlat;
+    if (!whole_item) {
+        lo = c0 + (static_cast<int>(blockIdx.x) - c0) / kJoined * kJoined;
+        n = min(kJoined, c1 + 1 - lo);
+    }
+#pragma unroll 1
+    for (;;) {
+        group_sync(kOutSync);   // (the slot is written)
+        if (q == 0 && lane == 0)
+            *s_last = last_of(whole_item ? item_counter : arrived + slot_at(lo), n);
+        group_sync(kOutSync);
+        if (!*static_cast<volatile int *>(s_last)) return;
+        auto part = [&](int m) { return slots + static_cast<int64_t>(slot_at(lo + m * step)) * S::kSlot; };
+        // The pieces' maxima and sums: a warp takes a quarter of the heads, so many pieces at
+        // a time as it has lanes for.
+        {
+            constexpr int kHs = H / 4, kPieces = 32 / kHs;
+            const int h = q * kHs + lane % kHs;
+            float most = -CUDART_INF_F, sum = 0.f;
+#pragma unroll 1
+            for (int k = lane / kHs; k < n; k += kPieces) {
+                const float mk = __ldcg(part(k) + H * (D + 1) + h), lk = __ldcg(part(k) + H * (D + 2) + h);
+                const float now = fmaxf(most, mk), base = finite_base(now);
+                sum = fmaf(sum, ex2(most - base), lk * ex2(mk - base));
+                most = now;
+            }
+            float all = most;
+#pragma unroll
+            for (int o = 16; o >= kHs; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
+            const float base = finite_base(all);
+            sum *= ex2(most - base);
+#pragma unroll
+            for (int o = 16; o >= kHs; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane < kHs) {
+                join[h] = base;
+                join[H + h] = sum;
+                join[2 * H + h] = all;
+                if (whole_item && h < heads && lse != nullptr)
+                    lse[h] =
+                        sum == 0.f ? -CUDART_INF_F : base * 0.69314718055994531f + logf(sum);
+            }
+        }
+        group_sync(kOutSync);
+#pragma unroll
+        for (int h = 0; h < H; ++h) acc[h] = 0.f;
+        // 32 numbers on their way at a time
+        constexpr int kBatch = 32 / H;
+#pragma unroll 1
+        for (int k0 = 0; k0 < n; k0 += kBatch) {
+            float by[kBatch], v[kBatch][H];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const bool is = k0 + i < n;
+                const float *src = part(is ? k0 + i : 0);
+                by[i] = is && lane < H ? __ldcg(src + H * D + lane) : -CUDART_INF_F;
+#pragma unroll
+                for (int h = 0; h < H; ++h) v[i][h] = is && has ? __ldcg(src + h * D + d) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                by[i] = lane < H ? ex2(by[i] - join[lane]) : 0.f;
+#pragma unroll
+                for (int h = 0; h < H; ++h) acc[h] = fmaf(v[i][h], __shfl_sync(0xffffffffu, by[i], h), acc[h]);
+            }
+        }
+        if (whole_item) {
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const float sum = join[H + h];
+                if (h < heads && has)
+                    out[h * D + d] =
+                        __float2bfloat16_rn(sum > 0.f ? acc[h] / sum : sum == 0.f ? 0.f : sum);
+            }
+            break;
+        }
+        // the group, in the place of its first piece
+        group_sync(kOutSync);   // (which is read)
+        float *to = slots + static_cast<int64_t>(slot_at(lo)) * S::kSlot;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+            if (has) to[h * D + d] = acc[h];
+        if (q == 0 && lane < H) {
+            to[H * D + lane] = join[2 * H + lane];
+            to[H * (D + 1) + lane] = join[2 * H + lane];
+            to[H * (D + 2) + lane] = join[H + lane];
+        }
+        lo = c0;
+        step = kJoined;
+        n = (c1 - c0) / kJoined + 1;
+        whole_item = true;
+    }
+}
 
 template <int D, int H, bool kTma>
 __global__ void __launch_bounds__(threads_of(H, kTma), 1)
@@ -720,18 +837,13 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         const int me = blockIdx.x;
         float *join = reinterpret_cast<float *>(smem + S::kOffJoin);
         Place<S::kPBufs> pp;
-        // One arrival at an item's counter for each of its pieces; the last finds it complete,
-        // and sets it back for the next call.
-        auto last_piece = [&](const Piece &piece, int c0, int c1) -> bool {
-            int *ctr = arrived + static_cast<int64_t>(piece.b) * items + piece.item;
-            const bool last = add_acq_rel(ctr, 1) == c1 - c0;
-            if (last) *ctr = 0;
-            return last;
-        };
+        auto item_counter = [&](const Piece &piece) { return arrived + 2 * kPlannedSms + static_cast<int64_t>(piece.b) * items + piece.item; };
         auto owners = [&](const Piece &piece, int &c0, int &c1) {
             c0 = Paged8Split::owner(piece.item_at + kItemCost, U, G);
             c1 = Paged8Split::owner(piece.item_at + kItemCost + piece.tiles - 1, U, G);
         };
+        // Which of the slots (and group counters) of block k, two of each, an item's piece has.
+        auto slot_of = [&](const Piece &piece, int k, int c0) { return 2 * k + (k == c0 && c0 * U / G <= piece.item_at); };
         int pc = 0;
         float *cast = reinterpret_cast<float *>(smem + S::kOffCast) + warp * 3 * H;
         for (;; ++pc) {
@@ -822,73 +934,10 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 }
             }
             if (whole) continue;
-            // ---- the last block of this item to arrive joins the pieces
             int c0, c1;
             owners(piece, c0, c1);
-            group_sync(kOutSync);   // (the slot is written)
-            if (q == 0 && lane == 0) s_last = last_piece(piece, c0, c1);
-            group_sync(kOutSync);
-            if (!*static_cast<volatile int *>(&s_last)) continue;
-            const int last = c0 * U / G <= piece.item_at;
-            auto part = [&](int k) { return slots + static_cast<int64_t>(2 * k + (k == c0 ? last : 0)) * S::kSlot; };
-            // The pieces' maxima and sums: a warp takes a quarter of the heads, so many pieces at
-            // a time as it has lanes for.
-            {
-                constexpr int kHs = H / 4, kPieces = 32 / kHs;
-                const int h = q * kHs + lane % kHs;
-                float most = -CUDART_INF_F, sum = 0.f;
-#pragma unroll 1
-                for (int k = c0 + lane / kHs; k <= c1; k += kPieces) {
-                    const float mk = __ldcg(part(k) + H * (D + 1) + h), lk = __ldcg(part(k) + H * (D + 2) + h);
-                    const float now = fmaxf(most, mk), base = finite_base(now);
-                    sum = fmaf(sum, ex2(most - base), lk * ex2(mk - base));
-                    most = now;
-                }
-                float all = most;
-#pragma unroll
-                for (int o = 16; o >= kHs; o >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, o));
-                const float base = finite_base(all);
-                sum *= ex2(most - base);
-#pragma unroll
-                for (int o = 16; o >= kHs; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (lane < kHs) {
-                    join[h] = base;
-                    join[H + h] = sum;
-                    if (h < heads && p.lse != nullptr)
-                        p.lse[piece.row + h] =
-                            sum == 0.f ? -CUDART_INF_F : base * 0.69314718055994531f + logf(sum);
-                }
-            }
-            group_sync(kOutSync);
-#pragma unroll
-            for (int h = 0; h < H; ++h) acc[h] = 0.f;
-            // 32 numbers on their way at a time
-            constexpr int kBatch = 32 / H;
-#pragma unroll 1
-            for (int k0 = c0; k0 <= c1; k0 += kBatch) {
-                float by[kBatch], v[kBatch][H];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const bool is = k0 + i <= c1;
-                    const float *src = part(is ? k0 + i : c0);
-                    by[i] = is && lane < H ? __ldcg(src + H * D + lane) : -CUDART_INF_F;
-#pragma unroll
-                    for (int h = 0; h < H; ++h) v[i][h] = is && has ? __ldcg(src + h * D + d) : 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    by[i] = lane < H ? ex2(by[i] - join[lane]) : 0.f;
-#pragma unroll
-                    for (int h = 0; h < H; ++h) acc[h] = fmaf(v[i][h], __shfl_sync(0xffffffffu, by[i], h), acc[h]);
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                const float sum = join[H + h];
-                if (h < heads && has)
-                    static_cast<__nv_bfloat16 *>(p.out)[(piece.row + h) * D + d] =
-                        __float2bfloat16_rn(sum > 0.f ? acc[h] / sum : sum == 0.f ? 0.f : sum);
-            }
+            join_pieces<D, H>(slots, arrived, item_counter(piece), c0, c1, slot_of(piece, c0, c0), static_cast<__nv_bfloat16 *>(p.out) + piece.row * D,
+                              p.lse != nullptr ? p.lse + piece.row : nullptr, heads, join, &s_last);
             // (the next piece's join comes after barriers of its own: `join` is read by then)
         }
         // Where a wait has run out, the arrivals for the pieces that are left, so that the counters
@@ -903,7 +952,10 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
                 piece.item = w.item;
                 int c0, c1;
                 owners(piece, c0, c1);
-                last_piece(piece, c0, c1);
+                const int n = c1 - c0 + 1, lo = c0 + (me - c0) / kJoined * kJoined;
+                if (n <= kFlat) last_of(item_counter(piece), n);
+                else if (last_of(arrived + slot_of(piece, lo, c0), min(kJoined, c1 + 1 - lo)))
+                    last_of(item_counter(piece), (n - 1) / kJoined + 1);
             }
     }
     tc::fence_before();
@@ -986,20 +1038,26 @@ int64_t paged8_workspace(const Paged8Params &p) {
     });
 }
 
-// One arrival counter per (sequence, work item).
+// Arrival counters: two per block for groups of pieces, then one per (sequence, work item).
 int64_t paged8_sync(const Paged8Params &p) {
-    return static_cast<int64_t>(p.c.batch) * p.c.hkv * chunks_of(p) * 4;
+    return (2 * kPlannedSms + static_cast<int64_t>(p.c.batch) * p.c.hkv * chunks_of(p)) * 4;
 }
 
 cudaError_t launch_paged8(const Paged8Params &p, const CallContext &ctx, cudaStream_t stream) {
     // Units the lengths may come to; empty sequences need a block as well. An item of n units is not
-    // cut into more than some 2 sqrt(n) pieces: a unit takes a block four times as long as a piece
-    // takes the join. (Two sequences of up to 12893 tokens, one key-value head: 16.5 us, cut as
-    // finely as it goes 24; one of 131072: 28 and 36; 8192 tokens, 8 heads: 14.5 and 16.)
+    // cut into more than some 2 sqrt(n) pieces, as a unit takes a block four times as long as a
+    // piece takes the join, or, where that makes groups of pieces, into 4 sqrt(n). (Cut as finely
+    // as it goes, joined at once: two sequences of up to 12893 tokens, one key-value head, 24 us
+    // for 16; one of 131072 36 for 21; 8192 tokens, 8 heads, 16 for 15.)
     const int64_t items = static_cast<int64_t>(p.c.batch) * p.c.hkv * chunks_of(p),
                   units = Paged8Split::units_of(p.c.max_pages * p.c.page_size);
-    int64_t pieces = 1;
-    while (pieces < kPlannedSms && (pieces + 1) * (pieces + 1) <= 4 * units) ++pieces;
+    auto root = [](int64_t x) {
+        int64_t r = 1;
+        while (r < kPlannedSms && (r + 1) * (r + 1) <= x) ++r;
+        return r;
+    };
+    int64_t pieces = root(4 * units);
+    if (pieces > kFlat) pieces = root(16 * units);
     if (pieces > units) pieces = units;
     const unsigned grid = static_cast<unsigned>(items * pieces < 1 ? 1 : items * pieces < kPlannedSms ? items * pieces : kPlannedSms);
     Paged8Maps maps{};

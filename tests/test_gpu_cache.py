@@ -632,6 +632,21 @@ def test_decode_long_and_ragged():
     attention_close(o, l, *case[:6], lens)
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page,scale", [
+    ([20000], 7, 1, 128, 17, None), ([20000], 16, 1, 64, 32, None), ([30, 0, 31000, 500], 12, 1, 128, 64, None),
+    ([17000, 9], 2, 2, 64, 100, 4.0), ([25000], 24, 1, 128, 8, 40.0), ([19000], 8, 1, 128, 16, -1000.0)])
+def test_decode_joins_in_groups(lens, Hq, Hkv, D, page, scale):
+    """Few sequences, cut into so many pieces that they are joined in two steps; with a large
+    scale most pieces' weights vanish."""
+    case = cache_case(lens, Hq, Hkv, D, page, "heads first", seed=6, spread=1)
+    o, l = K.paged_decode_fp8(*case, scale=scale)
+    K.check_device_error()
+    attention_close(o, l, *case[:6], lens, *([] if scale is None else [scale]))
+    for _ in range(3):
+        o2, l2 = K.paged_decode_fp8(*case, scale=scale)
+        assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("scale", [1.0, 4.0, -0.5, 0.0])
 def test_decode_scores_far_apart(scale, D):
