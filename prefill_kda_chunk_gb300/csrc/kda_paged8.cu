@@ -37,7 +37,7 @@
 // tokens, 64 heads over 8: 50 us (67 %); 256 of 1000, 32 heads over 8: 95 us (81 %); one of 700:
 // 11 us, a chain of latencies. What a tile
 // takes the weights' warps, some 1250 clocks with 8 heads, bounds D = 64 (8 x 32768 tokens: 72
-// us, 55 %), and 1600 with 16 heads those (8 x 65536, 2 key-value heads: 68 us, 58 %).
+// us, 55 %), and 1600 with 16 heads those (8 x 65536, 2 key-value heads: 64 us, 61 %).
 
 #include <cuda.h>
 #include <cuda_fp8.h>
@@ -500,8 +500,11 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         for (int i = 0; i < H / kRows; ++i)
             x[i] = i * kRows + sub < heads ? __ldg(reinterpret_cast<const uint4 *>(q + i * kRows * D)) : make_uint4(0, 0, 0, 0);
         uint8_t *dst = smem + S::kOffQ + buf * S::kQRows * D + 8 * (at & 1);
-#pragma unroll 1
-        for (int row = sub; row < H; row += kRows) {   // (rolled: shorter code)
+        // (rolled: shorter code. 16 heads, 8 x 65536: by two 64 us, by one 68; 8 heads, 256 x 1000: 101
+        // and 95)
+        constexpr int kUnroll = H > 8 ? 2 : 1;
+#pragma unroll kUnroll
+        for (int row = sub; row < H; row += kRows) {
             uint32_t u[4] = {x[0].x, x[0].y, x[0].z, x[0].w}, top = 0;
 #pragma unroll
             for (int i = 0; i + 1 < H / kRows; ++i) x[i] = x[i + 1];
@@ -541,7 +544,8 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         // of one page, K's in one warp and V's in the next, the tiles in turns where there are
         // two such pairs (a box takes a warp 80 clocks). Pages are read kDeep tiles of the warp's
         // ahead, their scales kScale: farther where a warp has every tile (2 x 131072 tokens, pages
-        // of 17: 116 us, with 2 and 1 145, with 6 and 3 127; pages of one, 65536: 70, 105 and 98).
+        // of 17: 116 us, with 2 and 1 145, with 6 and 3 127; pages of one, 65536: 70, 105 and 98; by
+        // tensor copies, pages of 32: 91.6 with 3 and 1, 93.4 with 2 and 1).
         const int cw = warp - S::kCopyWarp, turns = kTma ? B::kCopyWarps / 2 : 1, turn = kTma ? cw / 2 : 0;
         const bool of_v = cw & 1;
         const int offset = kTma ? (lane & 15) << maps.shift : 32 * cw + lane;
@@ -580,7 +584,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             if (!kTma || (of_v && lane >= 16)) a.ks = __ldg(c.ks + a.page * c.ks_page + a.kv);
             if (!kTma || (of_v && lane < 16)) a.vs = __ldg(c.vs + a.page * c.vs_page + a.kv);
         };
-        constexpr int kDeep = kTma ? 2 : 4, kScale = kTma ? 1 : 2;
+        constexpr int kDeep = kTma ? 3 : 4, kScale = kTma ? 1 : 2;
         Spot spots[kDeep];
 #pragma unroll
         for (int i = 0; i < kDeep; ++i) spots[i] = look();
