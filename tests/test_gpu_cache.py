@@ -133,6 +133,35 @@ def test_plan_steps_follow_one_another():
     assert sorted(used + state[2][:state[3]]) == list(range(pool))   # no page lost or held twice
 
 
+@pytest.mark.parametrize("B,page,width,new", [(16, 16, 8, 30), (64, 16, 20, 200), (1100, 8, 3, 5)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_plan_captured_into_a_graph(B, page, width, new, in_place):
+    """Every form's launches, replayed: in place each replay goes on from the one before, with
+    all slots given back and filled anew."""
+    table, lens, news, free, count, gone = plan_case(B, page, width, new, 11)
+    gone[:] = True
+    tokens = int(news.sum()) + 7
+    dev = [t.to("cuda", I32) for t in (table, lens, news, free, count)]
+    rel = gone.cuda()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        K.page_plan(*dev, page, tokens, release=rel)   # (its workspace)
+        K.page_plan(*(t.clone() for t in dev), page, tokens, release=rel, in_place=True)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            got = K.page_plan(*dev, page, tokens, release=rel, in_place=in_place)
+        state = table, lens, free, int(count)
+        for _ in range(3):
+            graph.replay()
+            ref = C.page_plan(state[0], state[1], news, state[2], state[3], page, tokens, gone)
+            if in_place:
+                state = ref[:4]
+            stream.synchronize()
+            plan_check(got, ref)
+    K.check_device_error()
+
+
 @pytest.mark.parametrize("fault,error", [
     ("long", "PAGE_TABLE"), ("negative", "PAGE_TABLE"), ("held", "PAGE_TABLE"), ("rows", "PAGE_TABLE"),
     ("count", "PAGE_TABLE"), ("pool", "OUT_OF_PAGES")])
