@@ -14,7 +14,7 @@
 // 8192 tokens below took 64 us, their gradient 94).
 //
 // Measured: 8192 tokens of 64 + 8 heads of 128: 51 us (5.9 TB/s, 87 % of copy bandwidth), the
-// gradient 81 us (82 %, and 62 % of the issue slots taken); 5003 tokens of 16 + 2 heads, gradient
+// gradient 81 us (82 %, and 62 % of the issue slots taken); 5003 tokens of 16 + 2 heads of 64, gradient
 // 16.6 us (41 %: start, end and the weights' sums are 6 us of it); one token 4.0 us, a launch and
 // a chain of loads.
 
