@@ -609,10 +609,10 @@ KDA_API kda_status kda_paged_append_fp8(
  * Alignment: q, k_cache, v_cache, out 16 bytes, the caches' strides multiples of 16
  * elements; int32 and fp32 arrays 4 bytes. Scores, softmax and sums in fp32. The tensor
  * core takes the cache's numbers as they are; a query enters as two e4m3 terms (exact to
- * 2^-22 of its largest channel) and the weights, times the values' scales, as four (16
- * bits, below out's own rounding, to 2^-33 of the largest among 128 tokens). The sum over
- * the cache is split over the SMs and joined in a fixed order (the same call gives the
- * same bits). Workspace: partial sums.
+ * 2^-22 of its largest channel) and the weights, times the values' scales, as four (to
+ * 2^-18.7 of each at most, 2^-21 in the mean; to 2^-33 of the largest among 128 tokens). The
+ * sum over the cache is split over the SMs and joined in a fixed order (the same call gives
+ * the same bits). Workspace: partial sums.
  */
 KDA_API kda_status kda_paged_decode_fp8(
     const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
