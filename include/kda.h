@@ -30,8 +30,9 @@
  *     is enqueued and leave every output untouched.
  *   - Workspaces belong to the (device, stream) of the call. A graph keeps the
  *     ones that its calls were captured with, also when a later call on that
- *     stream needs larger ones; graphs captured on one stream share them, so
- *     that they are replayed one after another, not side by side.
+ *     stream needs larger ones; graphs captured on one stream share them with one
+ *     another and with its later calls, so that replays and calls may follow one
+ *     another in any order, but not run side by side.
  */
 #ifndef KDA_GB300_H
 #define KDA_GB300_H

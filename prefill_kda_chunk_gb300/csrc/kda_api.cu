@@ -19,12 +19,10 @@ namespace {
 struct StreamWorkspace {
     void *ptr = nullptr;
     size_t bytes = 0;
-    // bytes at offset 256 known to hold zeros for the fused launch's ring
-    // counters (a fused launch leaves its own counters zero and writes past
-    // them; any other use of the buffer may overwrite them)
-    int64_t ring_clean = 0;
-    // arrival counters of the joined kernels: zeroed when allocated, and left
-    // zero by every launch that uses them
+    // arrival counters of the joined kernels and the fused 64-token launch's ring
+    // counters: zeroed when allocated, and left zero by every launch that uses them.
+    // (Not in the buffer above: what a graph writes there when it is replayed is
+    // not seen here.)
     void *sync = nullptr;
     size_t sync_bytes = 0;
     // A captured call has used the buffers: a graph may hold their addresses, so that
@@ -126,7 +124,7 @@ int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
 struct Plan {
     int impl = 1;            // recurrent kernel / path actually used (see g_recur_impl)
     int64_t c64_chunks = 0;  // 64-token paths: chunks of the call (upper bound when packed)
-    int64_t c64_sync = 0;    // fused 64-token path: bytes of the ring counters after the flag block
+    int64_t c64_sync = 0;    // fused 64-token path: bytes of the ring counters
     int64_t tokens = 0;      // total tokens
     int64_t max_chunks = 0;  // chunk records of one launch (upper bound when packed)
     int64_t off_bytes = 0;   // chunk offset table
@@ -197,8 +195,8 @@ kda_status plan_sizes(int64_t B, int64_t T, int64_t H, int64_t N, bool packed, i
     pl->impl = impl;
     if (impl >= kImplC64Split) {
         // 64-token chunks: flag block, 64-token chunk offsets (packed), then the
-        // records of every chunk-head (split) or a ring of kC64Ring per head and
-        // its counters (fused). TMA coordinates are 32-bit.
+        // records of every chunk-head (split) or a ring of kC64Ring per head
+        // (fused; its counters lie in the counter buffer). TMA coordinates are 32-bit.
         if (pl->tokens >= (int64_t(1) << 31)) return KDA_ERR_BAD_SHAPE;
         pl->c64_chunks = packed ? (T + 63 * N) / 64 : B * ((T + 63) / 64);
         if (impl == kImplC64Fused && H + kC64MinBuilders > sm_count) pl->impl = kImplC64Split;
@@ -208,9 +206,8 @@ kda_status plan_sizes(int64_t B, int64_t T, int64_t H, int64_t N, bool packed, i
         if (pl->impl == kImplC64Split) {
             pl->ws_bytes = 256 + pl->off_bytes + pl->c64_chunks * H * kda::kC64RecBytes;
         } else {
-            // the ring counters sit right after the flag block, whatever H is
             pl->c64_sync = align256((kC64Ring * H + H) * 8 + 64);
-            pl->ws_bytes = 256 + pl->c64_sync + pl->off_bytes + kC64Ring * H * kda::kC64RecBytes;
+            pl->ws_bytes = 256 + pl->off_bytes + kC64Ring * H * kda::kC64RecBytes;
         }
     }
     return KDA_OK;
@@ -312,7 +309,6 @@ int kda::begin_call(Operator op, const void *const *ptrs, int n, void *stream_, 
             // prefill's and the gradients' calls on this buffer
             const kda_status rc = grow(ws, &ws.ptr, &ws.bytes, 256 + ws_bytes, 256, capturing, stream);
             if (rc != KDA_OK) return rc;
-            ws.ring_clean = 0;
             ctx->ws = static_cast<uint8_t *>(ws.ptr) + 256;
             ctx->call_flags = static_cast<int *>(ws.ptr);
         }
@@ -509,11 +505,15 @@ kda_status kda_chunk_prefill_ex(const void *q, const void *k, const void *v, con
             return KDA_ERR_CUDA;
         }
         ws.bytes = pl.ws_bytes;
-        ws.ring_clean = 0;
         // the flag block starts zeroed (the exact-form list counters above all)
         if (cudaMemsetAsync(ws.ptr, 0, 256, stream) != cudaSuccess) return KDA_ERR_CUDA;
     }
     uint8_t *wsb = static_cast<uint8_t *>(ws.ptr);
+    const bool fused = pl.impl == kImplC64Fused && pl.tokens > 0;
+    if (fused) {
+        rc = grow(ws, &ws.sync, &ws.sync_bytes, pl.c64_sync, pl.c64_sync, capturing, stream);
+        if (rc != KDA_OK) return rc;
+    }
 
     const bool timed = t_timing.calls < t_timing.max_calls;
     if (timed) ++t_timing.calls;
@@ -532,10 +532,8 @@ kda_status kda_chunk_prefill_ex(const void *q, const void *k, const void *v, con
 
     if (pl.impl >= kImplC64Split) {
         // ---- 64-token chunks on tcgen05
-        const bool fused = pl.impl == kImplC64Fused;
-        if (!fused) ws.ring_clean = 0;
-        // fused: [flags | ring counters | chunk offsets | ring]; split: [flags | offsets | records]
-        const int64_t off_at = 256 + (fused ? pl.c64_sync : 0);
+        // [flags | chunk offsets | ring (fused) or records]
+        const int64_t off_at = 256;
         if (cu_seqlens != nullptr &&
             kda::launch_varlen_prologue(cu_seqlens, static_cast<int32_t>(N), pl.tokens,
                                         reinterpret_cast<int32_t *>(wsb + off_at),
@@ -558,20 +556,14 @@ kda_status kda_chunk_prefill_ex(const void *q, const void *k, const void *v, con
         a.scale = scale;
         a.pre = flags;
         a.rec = wsb + off_at + pl.off_bytes;
-        if (!fused) {
+        if (pl.impl == kImplC64Split) {
             rc = timed_launch(true, stream, [&] { return kda::launch_c64_intra(a, sm_count, stream); });
             if (rc != KDA_OK) return rc;
             return timed_launch(false, stream, [&] { return kda::launch_c64_chain(a, stream); });
         }
-        if (pl.tokens == 0)   // nothing for the builders: the chains alone carry the states
+        if (!fused)   // nothing for the builders: the chains alone carry the states
             return timed_launch(false, stream, [&] { return kda::launch_c64_chain(a, stream); });
-        long long *sync = reinterpret_cast<long long *>(wsb + 256);
-        if (ws.ring_clean < pl.c64_sync &&
-            cudaMemsetAsync(sync, 0, pl.c64_sync, stream) != cudaSuccess)
-            return KDA_ERR_CUDA;
-        // the launch leaves its own counters zero again; what lies past them
-        // (chunk offsets, ring) is not, whatever a larger layout needs there
-        ws.ring_clean = pl.c64_sync;
+        long long *sync = static_cast<long long *>(ws.sync);
         a.ring_depth = static_cast<int>(kC64Ring);
         a.n_chain = static_cast<int>(H);
         a.ready = sync;
@@ -579,7 +571,6 @@ kda_status kda_chunk_prefill_ex(const void *q, const void *k, const void *v, con
         a.exit_ctr = reinterpret_cast<int *>(sync + kC64Ring * H + H);
         return timed_launch(false, stream, [&] { return kda::launch_c64_fused(a, sm_count, stream); });
     }
-    ws.ring_clean = 0;
 
     kda::ChunkGeometry geo{};
     geo.cu = cu_seqlens;
@@ -749,7 +740,6 @@ kda_status kda_chunk_prefill_backward(const void *q, const void *k, const void *
         if (cudaMemsetAsync(ws.ptr, 0, 256, stream) != cudaSuccess) return KDA_ERR_CUDA;
     }
     uint8_t *wsb = static_cast<uint8_t *>(ws.ptr);
-    ws.ring_clean = 0;   // this call overwrites the area of the 64-token ring counters
 
     kda::ChunkGeometry geo{};
     geo.cu = cu_seqlens;
