@@ -408,7 +408,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last;
-    __shared__ unsigned long long s_start;
+    __shared__ unsigned long long s_moved;   // when the block last got on
     const Cache8 &c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = p.hq / c.hkv, chunks = (group + H - 1) / H;
@@ -432,7 +432,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
     const auto bar = [&](int i) { return sb + S::kOffBar + 8 * i; };
     if (tid == 0) {
         s_abort = 0;
-        s_start = globaltimer();
+        s_moved = globaltimer();
         for (int i = 0; i < B::kCount; ++i) mbar_init(bar(i), B::arrivals(i));
         mbar_fence_init();
     }
@@ -445,14 +445,17 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
     tc::fence_after();
     const uint32_t tm = s_tmem;
 
-    // A bounded wait (the clock from the block's start on: short code, as the roles' loops
-    // together are more than the instruction caches hold). Once one has run out none waits
-    // any more: all roles go through the piece they are at to its end, whatever they find there.
+    // A bounded wait: it runs out when the first product has taken no tile for kWaitLimitNs (a
+    // piece may take longer than that, and the queries of a later one wait for its end; one clock
+    // for all waits: short code, as the roles' loops together are more than the instruction
+    // caches hold. With a clock and a count of tiles in each wait 256 sequences of 1000 tokens
+    // took 112 us for 95). Once one has run out none waits any more: all roles go through the piece
+    // they are at to its end, whatever they find there.
     auto wait = [&](int i, int phase) {
         for (unsigned spins = 1; !mbar_try_wait(bar(i), phase & 1); ++spins) {
             if (spins % 256 != 0) continue;
             if (*static_cast<volatile int *>(&s_abort) != 0) break;
-            if (globaltimer() - s_start > kWaitLimitNs) {
+            if (globaltimer() - *static_cast<volatile unsigned long long *>(&s_moved) > kWaitLimitNs) {
                 *static_cast<volatile int *>(&s_abort) = 1;
                 atomicOr(c.err, kErrTimeout);
             }
@@ -669,6 +672,7 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
             for (int tile = tile0; tile < tile1; ++tile, sp.step(), kp.step()) {
                 if (sp.turn > 0) wait(B::kSEmpty + sp.at, sp.turn - 1);
                 wait(B::kKFull + kp.at, kp.turn);
+                if (kp.at == 0) *static_cast<volatile unsigned long long *>(&s_moved) = globaltimer();
                 fence_async();   // (the threads' copies were ordinary writes)
                 tc::fence_after();
                 const uint64_t k8 = desc<D>(sb + kp.at * S::kTileBytes);

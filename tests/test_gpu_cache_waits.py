@@ -1,0 +1,43 @@
+"""Bounded waits of the operators around the 8-bit cache: calls that take long are not cut off."""
+import math
+
+import pytest
+import torch
+
+import prefill_kda_chunk_gb300 as K
+from test_gpu_cache import BF16, F8, I32, attention_close, built, i32, make  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def test_attention_for_seconds():
+    """A call that works for three seconds or more, where the queries of later pieces wait for the end of
+    one that takes nearly as long: 2^31 - 4096 tokens for each of 48 heads, one page again and again,
+    and six short sequences behind them.
+
+    Scores are zero and values whole numbers whose sum over 128 tokens is -1, 0 or 1, so that every sum of
+    a piece's values and weights is a whole number below 2^24, exact in fp32. The pieces' values add up to
+    less than 2^24 as well; their weights, to 2^31, are off by 2^-24 for each of the 20 additions at
+    most. out = (-1, 0, 1) / 128, which bf16 holds, is less than half a step away."""
+    page, H, D, pages, short = 4096, 48, 64, 7, [5, 1, 130, 7, 4096, 33]
+    reps = (1 << 31) // page - 1
+    r = make(4)
+    k, v = (r(pages, page, H, D).to(F8) for _ in "kv")
+    k.view(torch.uint8)[0] = 0
+    c = torch.randint(-1, 2, (H, D), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).float()
+    t = torch.arange(page, device="cuda") % 128
+    sign = torch.where(t < 64, 1.0, -1.0)[:, None, None].expand(page, H, D)
+    v[0] = torch.where((t == 127)[:, None, None], c - 1, sign).to(F8)
+    one = torch.ones(pages, H, device="cuda")
+    table = torch.zeros(1 + len(short), reps, dtype=I32, device="cuda")
+    table[1:, 0] = torch.arange(1, 1 + len(short), dtype=I32, device="cuda")
+    q = r(1 + len(short), H, D)
+    began, ended = torch.cuda.Event(True), torch.cuda.Event(True)
+    began.record()
+    o, l = K.paged_decode_fp8(q, k, v, one, one, table, i32([reps * page] + short))
+    ended.record()
+    K.check_device_error()
+    assert began.elapsed_time(ended) > 2200, "the call does not take long enough for what this test is for"
+    assert torch.equal(o[0].float(), c / 128)
+    assert ((l[0] - math.log(reps * page)).abs() <= 1e-5).all()
+    attention_close(o[1:], l[1:], q[1:], k, v, one, one, table[1:, :1], short)
