@@ -710,6 +710,15 @@ KDA_API kda_status kda_test_stall_recurrent(int chunk, int64_t wait_ns);
 KDA_API kda_status kda_test_stall_scan(int chunk);
 
 /*
+ * Test hook for kda_qk_norm_rope and its gradients, likewise (process-wide, host only): in
+ * later calls a warp that has taken `batch` batches of heads asks for no more than the three
+ * that are under way. Its wait for the next one runs out after two seconds and it stops there.
+ * The call then records KDA_ERR_DEVICE_TIMEOUT, outputs unspecified. batch = -1 turns the hook
+ * off (the default); batch < -1: KDA_ERR_BAD_SHAPE.
+ */
+KDA_API kda_status kda_test_stall_qk_norm_rope(int batch);
+
+/*
  * Test hook for kda_paged_decode_fp8, likewise (process-wide, host only): in later calls
  * every thread block copies the first `tile` tiles of its share only, and the waits for
  * the next one run out (after about two seconds). The call then records

@@ -123,6 +123,8 @@ def lib() -> ctypes.CDLL:
             L.kda_test_stall_recurrent.argtypes = [ctypes.c_int, i64]
             L.kda_test_stall_scan.restype = ctypes.c_int
             L.kda_test_stall_scan.argtypes = [ctypes.c_int]
+            L.kda_test_stall_qk_norm_rope.restype = ctypes.c_int
+            L.kda_test_stall_qk_norm_rope.argtypes = [ctypes.c_int]
             L.kda_test_stall_paged_fp8.restype = ctypes.c_int
             L.kda_test_stall_paged_fp8.argtypes = [ctypes.c_int]
             L.kda_build_info.restype = ctypes.c_char_p
@@ -327,6 +329,12 @@ def kda_test_stall_scan(chunk: int) -> int:
     """Test hook: the state space scan's blocks copy the tiles of their first `chunk`
     chunks only, and their waits run out (-1: off)."""
     return lib().kda_test_stall_scan(int(chunk))
+
+
+def kda_test_stall_qk_norm_rope(batch: int) -> int:
+    """Test hook: the warps of the norms with the rotation and of their gradients ask for no more
+    heads once they have taken `batch` batches, and their waits run out (-1: off)."""
+    return lib().kda_test_stall_qk_norm_rope(int(batch))
 
 
 def kda_test_stall_paged_fp8(tile: int) -> int:

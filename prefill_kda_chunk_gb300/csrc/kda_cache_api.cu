@@ -25,6 +25,7 @@ using kda::rows_fit;
 constexpr int64_t k31 = int64_t(1) << 31;
 
 std::atomic<int> g_stall_paged8{INT_MAX};   // kda_test_stall_paged_fp8
+std::atomic<int> g_stall_heads{INT_MAX};    // kda_test_stall_qk_norm_rope
 
 kda_status status(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
@@ -169,6 +170,7 @@ kda::HeadsParams heads_params(const void *q, const void *k, const float *qw, con
     p.eps = eps;
     p.pairs = (flags & KDA_ROPE_INTERLEAVED) != 0;
     p.dout32 = (flags & KDA_ROPE_DOUT_FP32) != 0;
+    p.stall = g_stall_heads.load();
     return p;
 }
 
@@ -358,6 +360,12 @@ kda_status kda_paged_append_fp8(
     if (rc != KDA_OK) return rc;
     p.c.err = ctx.err;
     return status(kda::launch_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+kda_status kda_test_stall_qk_norm_rope(int batch) {
+    if (batch < -1) return KDA_ERR_BAD_SHAPE;
+    g_stall_heads.store(batch < 0 ? INT_MAX : batch);
+    return KDA_OK;
 }
 
 kda_status kda_test_stall_paged_fp8(int tile) {

@@ -14,8 +14,8 @@
 // 8192 tokens below took 64 us, their gradient 94).
 //
 // Measured: 8192 tokens of 64 + 8 heads of 128: 51 us (5.9 TB/s, 87 % of copy bandwidth), the
-// gradient 81 us (82 %, and 62 % of the issue slots taken); 5003 tokens of 16 + 2 heads of 64, gradient
-// 16.6 us (41 %: start, end and the weights' sums are 6 us of it); one token 4.0 us, a launch and
+// gradient 82.5 us (81 %, and 62 % of the issue slots taken); 5003 tokens of 16 + 2 heads of 64, gradient
+// 16.7 us (41 %: start, end and the weights' sums are 6 us of it); one token 4.0 us, a launch and
 // a chain of loads.
 
 #include <type_traits>
@@ -31,6 +31,7 @@ constexpr int kHeadsThreads = 256, kHeadsWarps = 8;
 constexpr int kRing = 3;                      // batches of a warp
 constexpr int kAhead = 4, kAheadGrad = 2;     // heads of a lane group in a batch
 constexpr int kHeadsBlocks = 2, kGradBlocksPerSm = 2;   // of an SM
+constexpr unsigned long long kLandNs = 100000000;       // within which a copy under way ends
 
 // cos and sin of position * f, where f turns by f / 2 pi a position. The turns are
 // formed as two floats (f / 2 pi to 2^-48, the position in two parts that fp32 holds
@@ -178,6 +179,13 @@ struct Batch {
     }
 };
 
+// A wait for batch n has run out: what has been asked for from there on lands, within a limit.
+// (Not inlined: in the loops it costs the gradient another 0.5 us.)
+__device__ __noinline__ void gave_up(uint32_t bars, int n, int *err) {
+    atomicOr(err, kErrTimeout);
+    for (int i = n; i < n + kRing; ++i) mbar_wait(bars + 8 * (i % kRing), i / kRing & 1, kLandNs);
+}
+
 // A warp's ring: kRing places of kBytes, a barrier each.
 template <int kBytes>
 struct WarpRing {
@@ -194,9 +202,11 @@ struct WarpRing {
     }
     __device__ __forceinline__ uint32_t place(int i) const { return base + i % kRing * kBytes; }
     __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * (i % kRing); }
-    __device__ __forceinline__ void wait(int *err) const {
-        if (!mbar_wait(bar(n), n / kRing & 1)) atomicOr(err, kErrTimeout);
-        __syncwarp();
+    // For the next batch; false where it has not come: the warp stops then, with its copies landed.
+    __device__ __forceinline__ bool wait(int *err) const {
+        if (__all_sync(0xffffffffu, mbar_wait(bar(n), n / kRing & 1))) return true;
+        gave_up(bars, n, err);
+        return false;
     }
 };
 
@@ -261,7 +271,7 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsBlocks) heads_kernel(Head
             uint16_t *out = (keys ? static_cast<uint16_t *>(p.k_out) + token * p.ko_stride
                                   : static_cast<uint16_t *>(p.q_out) + token * p.qo_stride) + sub * D + 8 * at;
             while (now.token == token && now.keys == (keys != 0)) {
-                ring.wait(p.err);
+                if (!ring.wait(p.err)) return;
                 const uint32_t from = ring.place(ring.n) + lane * 16;
 #pragma unroll
                 for (int i = 0; i < kAhead; i += 2) {   // two heads of a lane group side by side
@@ -297,7 +307,7 @@ __global__ void __launch_bounds__(kHeadsThreads, kHeadsBlocks) heads_kernel(Head
                     }
                 }
                 __syncwarp();
-                ask(ahead, ring.n);   // (the place just read)
+                if (ring.n < p.stall) ask(ahead, ring.n);   // (the place just read)
                 ++ring.n;
                 now.advance(mine, kStep);
                 ahead.advance(mine, kStep);
@@ -406,7 +416,10 @@ __global__ void __launch_bounds__(kHeadsThreads, kGradBlocksPerSm) heads_backwar
             out += sub * D + 8 * at;
             do {
                 const int first = now.h, heads = now.heads;
-                ring.wait(p.err);
+                if (!ring.wait(p.err)) {
+                    now.left = 0;
+                    break;
+                }
                 const uint32_t from = ring.place(ring.n);
 #pragma unroll
                 for (int i = 0; i < kAheadGrad; ++i) {
@@ -464,7 +477,7 @@ __global__ void __launch_bounds__(kHeadsThreads, kGradBlocksPerSm) heads_backwar
                     if (row) *reinterpret_cast<uint4 *>(out + (first + i * kRows) * D) = pack8(g);
                 }
                 __syncwarp();
-                ask(ahead, ring.n);   // (the place just read)
+                if (ring.n < p.stall) ask(ahead, ring.n);   // (the place just read)
                 ++ring.n;
                 now.advance(p);
                 ahead.advance(p);

@@ -320,6 +320,7 @@ struct HeadsParams {
     const void *dq, *dk;       // gradient: bf16 or fp32 [T, H, D]
     float *dqw, *dkw;          // gradient: [D] or nullptr
     float *partial;            // gradient: [blocks][2][D]
+    int stall;                 // test hook: batches that a warp takes before it asks for no more
     int *err;
 };
 cudaError_t configure_heads();

@@ -41,3 +41,44 @@ def test_attention_for_seconds():
     assert torch.equal(o[0].float(), c / 128)
     assert ((l[0] - math.log(reps * page)).abs() <= 1e-5).all()
     attention_close(o[1:], l[1:], q[1:], k, v, one, one, table[1:, :1], short)
+
+
+def stalled(batch, call):
+    """Milliseconds that the call takes on the GPU when no warp gets more than so many batches and three."""
+    began, ended = torch.cuda.Event(True), torch.cuda.Event(True)
+    assert K.kda_test_stall_qk_norm_rope(batch) == 0
+    try:
+        began.record()
+        call()
+        ended.record()
+        with pytest.raises(K.KdaError, match="TIMEOUT"):
+            K.check_device_error()
+    finally:
+        assert K.kda_test_stall_qk_norm_rope(-1) == 0
+    return began.elapsed_time(ended)
+
+
+@pytest.mark.parametrize("batch", [0, 1, 4])
+@pytest.mark.parametrize("weights", [True, False])
+def test_norms_wait_once_and_no_more(weights, batch):
+    """Warps with a dozen batches or more to come: the first wait that runs out, two seconds, is the last one (and a
+    tenth for each of three places of the ring). The next call is right."""
+    T, H, D = 12000, 40, 64
+    r = make(3)
+    q, k, dq, dk = r(T, H, D), r(T, 8, D), r(T, H, D), r(T, 8, D)
+    w = [1 + 0.1 * r(D, dtype=torch.float32) if weights else None for _ in "qk"]
+    pos = torch.arange(T, dtype=I32, device="cuda")
+    freq = torch.rand(D // 2, device="cuda")
+    for call in (lambda: K.qk_norm_rope(q, k, *w, freq, pos),
+                 lambda: K.qk_norm_rope_backward(q, k, dq, dk, *w, freq, pos)):
+        ref = call()
+        K.check_device_error()
+        assert stalled(batch, call) < 3500
+        got = call()
+        K.check_device_error()
+        assert all(a is None and b is None or torch.equal(a, b) for a, b in zip(got, ref))
+
+
+def test_stall_hook_arguments():
+    assert K.kda_test_stall_qk_norm_rope(-2) != 0
+    assert K.kda_test_stall_qk_norm_rope(-1) == 0
