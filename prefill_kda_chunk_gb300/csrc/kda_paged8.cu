@@ -455,7 +455,9 @@ paged8_kernel(const __grid_constant__ Paged8Maps maps, Paged8Params p, float *sl
         for (unsigned spins = 1; !mbar_try_wait(bar(i), phase & 1); ++spins) {
             if (spins % 256 != 0) continue;
             if (*static_cast<volatile int *>(&s_abort) != 0) break;
-            if (globaltimer() - *static_cast<volatile unsigned long long *>(&s_moved) > kWaitLimitNs) {
+            // (signed: s_moved may be set between the two readings)
+            if (static_cast<long long>(globaltimer() - *static_cast<volatile unsigned long long *>(&s_moved)) >
+                static_cast<long long>(kWaitLimitNs)) {
                 *static_cast<volatile int *>(&s_abort) = 1;
                 atomicOr(c.err, kErrTimeout);
             }

@@ -82,3 +82,20 @@ def test_norms_wait_once_and_no_more(weights, batch):
 def test_stall_hook_arguments():
     assert K.kda_test_stall_qk_norm_rope(-2) != 0
     assert K.kda_test_stall_qk_norm_rope(-1) == 0
+
+
+def test_no_wait_runs_out_at_work():
+    """Hundreds of calls whose roles wait for one another all the time: the clock that they share may be set
+    between a wait's two readings of the time."""
+    r, H, D, page = make(6), 8, 64, 64
+    lens = [32768] * 8
+    k, v = (r(4096, page, H, D).to(F8) for _ in "kv")
+    one = torch.ones(4096, H, device="cuda")
+    table = torch.arange(4096, dtype=I32, device="cuda").view(8, 512)
+    q, n = r(8, 64, D), i32(lens)
+    ref = K.paged_decode_fp8(q, k, v, one, one, table, n)
+    for i in range(400):
+        got = K.paged_decode_fp8(q, k, v, one, one, table, n)
+        if i % 50 == 0:
+            assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    K.check_device_error()
