@@ -99,3 +99,29 @@ def test_no_wait_runs_out_at_work():
         if i % 50 == 0:
             assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
     K.check_device_error()
+
+
+@pytest.mark.parametrize("page", [4096, 17])
+def test_attention_leaves_a_long_piece(page):
+    """A wait that runs out early in pieces of 110000 tiles: the roles come to their end in a second or two."""
+    r, H, D = make(5), 1, 64
+    reps = (1 << 31) // page - 1
+    k, v = (r(2, page, H, D).to(F8) for _ in "kv")
+    one = torch.ones(2, H, device="cuda")
+    q, table, lens = r(1, 8, D), torch.zeros(1, reps, dtype=I32, device="cuda"), i32([reps * page])
+    small = (q, k, v, one, one, table[:, :1].contiguous(), i32([page]))
+    ref = K.paged_decode_fp8(*small)
+    began, ended = torch.cuda.Event(True), torch.cuda.Event(True)
+    assert K.kda_test_stall_paged_fp8(3) == 0
+    try:
+        began.record()
+        K.paged_decode_fp8(q, k, v, one, one, table, lens)
+        ended.record()
+        with pytest.raises(K.KdaError, match="TIMEOUT"):
+            K.check_device_error()
+    finally:
+        assert K.kda_test_stall_paged_fp8(-1) == 0
+    assert began.elapsed_time(ended) < 6000
+    got = K.paged_decode_fp8(*small)
+    K.check_device_error()
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
