@@ -638,7 +638,8 @@ KDA_API kda_status kda_last_device_error(void *stream);
 /*
  * Frees every cached workspace buffer of the current device after
  * synchronising the device. Safe to call at any time no call of this
- * library is in flight on the device.
+ * library is in flight on the device; graphs that hold calls with a workspace
+ * cannot be replayed after it.
  */
 KDA_API kda_status kda_workspace_release(void);
 

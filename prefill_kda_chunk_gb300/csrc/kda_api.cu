@@ -16,26 +16,22 @@
 namespace {
 
 // Per caller stream: the scratch buffer.
-struct StreamWorkspace {
+// A buffer that calls on one stream share.
+struct Buffer {
     void *ptr = nullptr;
     size_t bytes = 0;
+    bool captured = false;   // a captured call has been given it: a graph may hold its address
+};
+
+struct StreamWorkspace {
+    Buffer work;
     // arrival counters of the joined kernels and the fused 64-token launch's ring
     // counters: zeroed when allocated, and left zero by every launch that uses them.
     // (Not in the buffer above: what a graph writes there when it is replayed is
     // not seen here.)
-    void *sync = nullptr;
-    size_t sync_bytes = 0;
-    // A captured call has used the buffers: a graph may hold their addresses, so that
-    // growing leaves them (kda_workspace_release frees them).
-    bool captured = false;
+    Buffer counters;
+    // buffers that graphs hold, replaced by larger ones (kda_workspace_release frees them)
     std::vector<void *> left;
-    // Before a buffer is replaced by a larger one.
-    cudaError_t give_up(void *p, cudaStream_t stream) {
-        if (p == nullptr) return cudaSuccess;
-        if (!captured) return cudaFreeAsync(p, stream);
-        left.push_back(p);
-        return cudaSuccess;
-    }
 };
 
 struct DeviceState {
@@ -248,22 +244,26 @@ int kda::pointer_device_status(const void *p, int dev) {
     return KDA_OK;
 }
 
-// Replaces *ptr by at least `need` bytes in stream order, the first `zero` of
-// them zeroed.
-static kda_status grow(StreamWorkspace &ws, void **ptr, size_t *bytes, int64_t need, int64_t zero,
-                       bool capturing, cudaStream_t stream) {
-    if (*bytes >= static_cast<size_t>(need)) return KDA_OK;
-    if (capturing) return KDA_ERR_CAPTURE;
-    if (ws.give_up(*ptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
-    *ptr = nullptr;
-    *bytes = 0;
-    if (cudaMallocAsync(ptr, need, stream) != cudaSuccess) {
-        cudaGetLastError();
-        *ptr = nullptr;
-        return KDA_ERR_CUDA;
+// Makes a buffer of `ws` at least `need` bytes, in stream order, the first `zero` bytes of a new
+// one zeroed. One that a graph may hold is kept beside it, others are freed.
+static kda_status grow(StreamWorkspace &ws, Buffer &b, int64_t need, int64_t zero, bool capturing,
+                       cudaStream_t stream) {
+    if (b.bytes < static_cast<size_t>(need)) {
+        if (capturing) return KDA_ERR_CAPTURE;
+        if (b.ptr != nullptr) {
+            if (b.captured) ws.left.push_back(b.ptr);
+            else if (cudaFreeAsync(b.ptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
+        }
+        b = Buffer{};
+        if (cudaMallocAsync(&b.ptr, need, stream) != cudaSuccess) {
+            cudaGetLastError();
+            b.ptr = nullptr;
+            return KDA_ERR_CUDA;
+        }
+        if (zero > 0 && cudaMemsetAsync(b.ptr, 0, zero, stream) != cudaSuccess) return KDA_ERR_CUDA;
+        b.bytes = need;
     }
-    *bytes = need;
-    if (zero > 0 && cudaMemsetAsync(*ptr, 0, zero, stream) != cudaSuccess) return KDA_ERR_CUDA;
+    b.captured |= capturing;
     return KDA_OK;
 }
 
@@ -303,20 +303,18 @@ int kda::begin_call(Operator op, const void *const *ptrs, int n, void *stream_, 
     ctx->err = st.err;
     if (ws_bytes > 0 || sync_bytes > 0) {
         StreamWorkspace &ws = st.ws[stream];
-        ws.captured |= capturing;
         if (ws_bytes > 0) {
             // the flag block at the start (its zeros included) belongs to the
             // prefill's and the gradients' calls on this buffer
-            const kda_status rc = grow(ws, &ws.ptr, &ws.bytes, 256 + ws_bytes, 256, capturing, stream);
+            const kda_status rc = grow(ws, ws.work, 256 + ws_bytes, 256, capturing, stream);
             if (rc != KDA_OK) return rc;
-            ctx->ws = static_cast<uint8_t *>(ws.ptr) + 256;
-            ctx->call_flags = static_cast<int *>(ws.ptr);
+            ctx->ws = static_cast<uint8_t *>(ws.work.ptr) + 256;
+            ctx->call_flags = static_cast<int *>(ws.work.ptr);
         }
         if (sync_bytes > 0) {
-            const kda_status rc =
-                grow(ws, &ws.sync, &ws.sync_bytes, sync_bytes, sync_bytes, capturing, stream);
+            const kda_status rc = grow(ws, ws.counters, sync_bytes, sync_bytes, capturing, stream);
             if (rc != KDA_OK) return rc;
-            ctx->sync = static_cast<int *>(ws.sync);
+            ctx->sync = static_cast<int *>(ws.counters.ptr);
         }
     }
     return KDA_OK;
@@ -494,24 +492,13 @@ kda_status kda_chunk_prefill_ex(const void *q, const void *k, const void *v, con
     }
 
     StreamWorkspace &ws = st.ws[stream];
-    ws.captured |= capturing;
-    if (ws.bytes < static_cast<size_t>(pl.ws_bytes)) {
-        if (capturing) return KDA_ERR_CAPTURE;
-        if (ws.give_up(ws.ptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
-        ws.ptr = nullptr;
-        ws.bytes = 0;
-        if (cudaMallocAsync(&ws.ptr, pl.ws_bytes, stream) != cudaSuccess) {
-            ws.ptr = nullptr;
-            return KDA_ERR_CUDA;
-        }
-        ws.bytes = pl.ws_bytes;
-        // the flag block starts zeroed (the exact-form list counters above all)
-        if (cudaMemsetAsync(ws.ptr, 0, 256, stream) != cudaSuccess) return KDA_ERR_CUDA;
-    }
-    uint8_t *wsb = static_cast<uint8_t *>(ws.ptr);
+    // the flag block starts zeroed (the exact-form list counters above all)
+    rc = grow(ws, ws.work, pl.ws_bytes, 256, capturing, stream);
+    if (rc != KDA_OK) return rc;
+    uint8_t *wsb = static_cast<uint8_t *>(ws.work.ptr);
     const bool fused = pl.impl == kImplC64Fused && pl.tokens > 0;
     if (fused) {
-        rc = grow(ws, &ws.sync, &ws.sync_bytes, pl.c64_sync, pl.c64_sync, capturing, stream);
+        rc = grow(ws, ws.counters, pl.c64_sync, pl.c64_sync, capturing, stream);
         if (rc != KDA_OK) return rc;
     }
 
@@ -563,7 +550,7 @@ kda_status kda_chunk_prefill_ex(const void *q, const void *k, const void *v, con
         }
         if (!fused)   // nothing for the builders: the chains alone carry the states
             return timed_launch(false, stream, [&] { return kda::launch_c64_chain(a, stream); });
-        long long *sync = static_cast<long long *>(ws.sync);
+        long long *sync = static_cast<long long *>(ws.counters.ptr);
         a.ring_depth = static_cast<int>(kC64Ring);
         a.n_chain = static_cast<int>(H);
         a.ready = sync;
@@ -726,20 +713,9 @@ kda_status kda_chunk_prefill_backward(const void *q, const void *k, const void *
     const int64_t ckpt_bytes = backward_ckpt_bytes(B, T, H, N, cu_seqlens != nullptr, pl);
     const int64_t need = backward_ws_bytes(B, T, H, N, cu_seqlens != nullptr, pl);
     StreamWorkspace &ws = st.ws[stream];
-    ws.captured |= capturing;
-    if (ws.bytes < static_cast<size_t>(need)) {
-        if (capturing) return KDA_ERR_CAPTURE;
-        if (ws.give_up(ws.ptr, stream) != cudaSuccess) return KDA_ERR_CUDA;
-        ws.ptr = nullptr;
-        ws.bytes = 0;
-        if (cudaMallocAsync(&ws.ptr, need, stream) != cudaSuccess) {
-            ws.ptr = nullptr;
-            return KDA_ERR_CUDA;
-        }
-        ws.bytes = need;
-        if (cudaMemsetAsync(ws.ptr, 0, 256, stream) != cudaSuccess) return KDA_ERR_CUDA;
-    }
-    uint8_t *wsb = static_cast<uint8_t *>(ws.ptr);
+    rc = grow(ws, ws.work, need, 256, capturing, stream);
+    if (rc != KDA_OK) return rc;
+    uint8_t *wsb = static_cast<uint8_t *>(ws.work.ptr);
 
     kda::ChunkGeometry geo{};
     geo.cu = cu_seqlens;
@@ -913,13 +889,12 @@ kda_status kda_workspace_release(void) {
     if (it == g_devices.end()) return KDA_OK;
     for (auto &kv : it->second.ws) {
         StreamWorkspace &w = kv.second;
-        if (w.ptr != nullptr && cudaFree(w.ptr) != cudaSuccess) return KDA_ERR_CUDA;
-        w.ptr = nullptr;
-        if (w.sync != nullptr && cudaFree(w.sync) != cudaSuccess) return KDA_ERR_CUDA;
-        w.sync = nullptr;
-        for (void *p : w.left)
-            if (cudaFree(p) != cudaSuccess) return KDA_ERR_CUDA;
-        w.left.clear();
+        for (Buffer *b : {&w.work, &w.counters}) {
+            if (b->ptr != nullptr && cudaFree(b->ptr) != cudaSuccess) return KDA_ERR_CUDA;
+            *b = Buffer{};
+        }
+        for (; !w.left.empty(); w.left.pop_back())
+            if (cudaFree(w.left.back()) != cudaSuccess) return KDA_ERR_CUDA;
     }
     it->second.ws.clear();
     return KDA_OK;

@@ -133,3 +133,45 @@ def test_counters_are_shared_in_turns():
         assert all(same(f(), r) for f, r in zip((many, few, call), (ref[2], ref[0], ref[1])))
     K.check_device_error()
     many.check(ref[2])
+
+
+def used():
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    free, total = torch.cuda.mem_get_info()
+    return total - free
+
+
+def test_growing_keeps_what_graphs_hold_and_no_more():
+    """A call is captured, then ever larger ones follow on its stream: of their workspaces (86 to 345 MB) the
+    last one stays, and the graph's own (11 MB), with which a replay is still right."""
+    H, r = 32, make(7)
+
+    def gradient(T):
+        x = [r(T, H, 128) for _ in range(4)]
+        g, beta = -r(T, H, 128, dtype=F32).abs(), r(T, H, dtype=F32).sigmoid()
+        return lambda: K.chunk_prefill_backward(x[0], x[1], x[2], g, beta, x[3])
+
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        assert K.kda_workspace_release() == 0
+        first = gradient(64)
+        ref = first()
+        graph, held = captured(first, stream)
+        before, sizes = used(), (512, 1024, 1536, 2048)
+        for T in sizes:
+            gradient(T)()
+        stream.synchronize()
+        grown = used() - before
+        for t in held:
+            if t is not None:
+                t.zero_()
+        graph.replay()
+        stream.synchronize()
+        assert all(a is None and b is None or torch.equal(a, b) for a, b in zip(held, ref))
+    K.check_device_error(stream.cuda_stream)
+    last = K.kda_backward_workspace_bytes(1, sizes[-1], H, 1, False)
+    assert last > 300 << 20 and grown < last + (64 << 20), f"{grown >> 20} MB more for {last >> 20}"
+    del graph, held
+    assert K.kda_workspace_release() == 0
+    assert used() <= before + (64 << 20)
