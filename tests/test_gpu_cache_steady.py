@@ -60,3 +60,76 @@ def test_gradients_of_many_tokens(T, Hq, Hk, D, R, pairs, fused, far, d32):
         rx, rw = C.norm_rope_backward(x, dyo, wi, freq, pos, interleaved=pairs)
         close(d, *rx, "d" + name)
         close(dw, *rw, f"d{name}_weight")
+
+
+# ----------------------------------------------------------- into the cache
+
+# D, page, key-value heads: warps of an item (kept rows a lane), heads of an item and its sets of them.
+HEADS_TOGETHER = [
+    (128, 8, 9),      # 1 (4), 8 + 1
+    (64, 16, 5),      # 1 (4), 4 + 1
+    (128, 8, 3),      # 1 (4), 2 + 1
+    (128, 16, 5),     # 2 (4), 4 + 1
+    (64, 32, 9),      # 2 (4), 8 + 1
+    (128, 32, 9),     # 4 (4), 8 + 1
+    (64, 64, 3),      # 4 (4), 2 + 1
+    (128, 64, 9),     # 8 (4), 8 + 1
+    (128, 50, 6),     # 8 (4), 4 + 2
+    (64, 128, 5),     # 8 (4), 4 + 1
+    (128, 128, 9),    # 8 (8), 8 + 1
+    (128, 200, 4),    # 8 (8), 2 + 2; rows behind those in registers
+]
+
+
+@pytest.mark.parametrize("D,page,H,layout", [(*c, ("page", "heads first")[i % 2]) for i, c in enumerate(HEADS_TOGETHER)])
+def test_append_of_several_heads_an_item(D, page, H, layout):
+    """Prompts, then more tokens for the same slots: pages that go on, whose scales grow in some of an
+    item's heads and not in the next; infinities and NaN in some heads only, the first and
+    the last among them."""
+    g = torch.Generator().manual_seed(D + page + H)
+    # (24 warps for every SM with all sets of heads: what the items' number goes by)
+    w = next(w for w in (1, 2, 4, 8) if page <= 4 * (256 // D) * w or w == 8)
+    B, want = 40, -(-24 * 152 // (2 * 2 * w)) * page
+    rounds = [torch.randint(1, 3 * page, (B,), generator=g).tolist(),
+              [want // B + int(x) for x in torch.randint(0, page, (B,), generator=g)]]
+    ends = [sum(r[i] for r in rounds) for i in range(B)]
+    table, pages = deal(ends, page, 2, B + page)
+    dev = empty_cache(pages, page, H, D, layout)
+    ref = [(c.cpu().double(), s.cpu().double()) for c, s in ((dev[0], dev[2]), (dev[1], dev[3]))]
+    r, lens = make(D + page + H), [0] * B
+    for n, new in enumerate(rounds):
+        lens = [a + b for a, b in zip(lens, new)]
+        T = sum(new)
+        x = r(T, 2, H, D)
+        x *= torch.exp2(torch.randint(-3, 3, (T, 1, 1, 1), device="cuda").float())
+        # the heads' sizes go up, stay, or go down from one round to the next
+        x *= torch.exp2((n * (torch.arange(H, device="cuda") % 3 - 1) * 5.0))[None, None, :, None]
+        for i in range(24):
+            at, h = int(torch.randint(0, T, (1,), generator=g)), (0, H - 1, int(torch.randint(0, H, (1,), generator=g)))[i % 3]
+            x[at, i % 2, h, i] = (math.inf, -math.inf, math.nan)[i % 3 - (i > 11)]
+        cu = cu_of(new)
+        K.paged_append_fp8(x[:, 0], x[:, 1], *dev, table.cuda(), i32(lens), cu.cuda())
+        K.check_device_error()
+        for y, (codes, scale) in zip((x[:, 0], x[:, 1]), ref):
+            C.append(y, codes, scale, table, lens, cu)
+        same_cache(dev, ref)
+
+
+def test_append_of_several_heads_a_token_each():
+    """Enough slots that a token each is taken by items of several heads."""
+    B, H, D, page = 700, 11, 64, 4
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 9, (B,), generator=g).tolist()
+    table, pages = deal([n + 1 for n in lens], page, 1, 1)
+    dev = empty_cache(pages, page, H, D, "page")
+    for c, s in ((dev[0], dev[2]), (dev[1], dev[3])):
+        c.view(torch.uint8).copy_(torch.randint(0, 120, c.shape, generator=g, dtype=torch.uint8))
+        s.copy_(torch.exp2(torch.randint(-9, -4, s.shape, generator=g).float()))
+    ref = [(c.cpu().double(), s.cpu().double()) for c, s in ((dev[0], dev[2]), (dev[1], dev[3]))]
+    new = [n + 1 if i % 7 else 0 for i, n in enumerate(lens)]   # (some without)
+    x = make(8)(B, 2, H, D)
+    K.paged_append_fp8(x[:, 0], x[:, 1], *dev, table.cuda(), i32(new))
+    K.check_device_error()
+    for y, (codes, scale) in zip((x[:, 0], x[:, 1]), ref):
+        C.append(y, codes, scale, table, new)
+    same_cache(dev, ref)
