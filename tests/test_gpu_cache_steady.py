@@ -133,3 +133,36 @@ def test_append_of_several_heads_a_token_each():
     for y, (codes, scale) in zip((x[:, 0], x[:, 1]), ref):
         C.append(y, codes, scale, table, new)
     same_cache(dev, ref)
+
+
+# -------------------------------------------------------------- the attention
+
+# Tiles of 128 tokens that each of 152 blocks takes (more than twice the places for keys, of which there
+# are 5, 6 or, with 64 channels, 10): 16 to 17, or 27 to 28.
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page,layout", [
+    ([69000, 9000, 0, 2500], 64, 4, 128, 64, "page"),            # 16 heads
+    ([69000, 9000, 0, 2500], 64, 4, 128, 17, "heads first"),     # copies by threads
+    ([70000, 11, 8500], 32, 4, 128, 17, "token"),                # 8 heads
+    ([110000, 21000, 3], 64, 4, 64, 32, "heads first"),
+    ([110000, 21000, 3], 64, 4, 64, 17, "page"),
+    ([7, 130000, 2500], 20, 4, 64, 8, "page"),
+    ([130000, 2500], 32, 4, 64, 17, "apart"),
+])
+def test_decode_of_many_tiles_a_block(lens, Hq, Hkv, D, page, layout):
+    case = cache_case(lens, Hq, Hkv, D, page, layout, seed=11, spread=1)
+    o, l = K.paged_decode_fp8(*case)
+    K.check_device_error()
+    attention_close(o, l, *case[:6], lens)
+
+
+# A block's pieces, whole items and parts of them: 10 to 11, of 3 or 4 places for queries.
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(32, 8, 128, 16), (128, 8, 128, 64), (64, 8, 64, 17), (96, 8, 64, 32),
+                                           (128, 8, 128, 17)])
+def test_decode_of_many_pieces_a_block(Hq, Hkv, D, page):
+    g = torch.Generator().manual_seed(Hq + D + page)
+    lens = torch.randint(1, 301, (200,), generator=g).tolist()
+    lens[3] = lens[199] = 0
+    case = cache_case(lens, Hq, Hkv, D, page, seed=12, spread=1)
+    o, l = K.paged_decode_fp8(*case)
+    K.check_device_error()
+    attention_close(o, l, *case[:6], lens)
