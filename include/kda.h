@@ -507,7 +507,7 @@ KDA_API kda_status kda_page_plan(const int32_t *page_table, const int32_t *seq_l
  * over the pairs (a, b) = (i, i + R / 2), or (2 i, 2 i + 1) under KDA_ROPE_INTERLEAVED,
  * i < R / 2; channels from R on are u. Angles are reduced from the exact product of
  * the position and the fp32 frequency, so that far positions keep their precision
- * (to 2^-20 of a turn up to position 2^24).
+ * (to 2^-23 of a turn up to position 2^24).
  *
  *   q, k         device, bf16 [T, Hq, D], [T, Hk, D], tokens q_stride / k_stride elements
  *                apart (slices of a fused projection); Hk = 0: no keys (k, k_out NULL)

@@ -13,9 +13,9 @@
 // a token) each, so that what is on its way takes no registers (with batches in registers the
 // 8192 tokens below took 64 us, their gradient 94).
 //
-// Measured: 8192 tokens of 64 + 8 heads of 128: 51 us (5.9 TB/s, 87 % of copy bandwidth), the
-// gradient 82.5 us (81 %, and 62 % of the issue slots taken); 5003 tokens of 16 + 2 heads of 64, gradient
-// 16.7 us (41 %: start, end and the weights' sums are 6 us of it); one token 4.0 us, a launch and
+// Measured: 8192 tokens of 64 + 8 heads of 128: 52 us (5.8 TB/s, 86 % of copy bandwidth), the
+// gradient 83 us (80 %, and 62 % of the issue slots taken); 5003 tokens of 16 + 2 heads of 64, gradient
+// 17.0 us (40 %: start, end and the weights' sums are 6 us of it); one token 4.2 us, a launch and
 // a chain of loads.
 
 #include <type_traits>
@@ -36,8 +36,9 @@ constexpr unsigned long long kLandNs = 100000000;       // within which a copy u
 // cos and sin of position * f, where f turns by f / 2 pi a position. The turns are
 // formed as two floats (f / 2 pi to 2^-48, the position in two parts that fp32 holds
 // exactly, each product with its rounding error) and whole turns are dropped on the way;
-// what is left, half a turn at most, is exact to some 2^-22 of a turn, and the hardware's sine
-// and cosine of it to 2^-20.
+// what is left, half a turn at most, is exact to 2^-23 of a turn. (With the hardware's sine and
+// cosine, off by 2^-21, one token took 4.0 us for 4.2, 8192 of 72 heads 51.5 for 51.9; a
+// result rounded otherwise than the 64-bit one three times as often.)
 __device__ __forceinline__ void angle(int pos, float f, float &c, float &s) {
     const float inv = 0.15915494f, inv_lo = 6.42063833e-9f;   // 1 / 2 pi
     const float hi = f * inv, lo = fmaf(f, inv, -hi) + f * inv_lo;
@@ -45,9 +46,7 @@ __device__ __forceinline__ void angle(int pos, float f, float &c, float &s) {
     const float a = p0 * hi, b = p1 * hi;
     float t = (a - rintf(a)) + (b - rintf(b));
     t += fmaf(p0, hi, -a) + fmaf(p1, hi, -b) + (p0 + p1) * lo;
-    t = (t - rintf(t)) * 6.2831853f;
-    c = __cosf(t);
-    s = __sinf(t);
+    sincospif(2.f * (t - rintf(t)), &s, &c);
 }
 
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
