@@ -61,7 +61,9 @@ constexpr unsigned long long kLandNs = 100000000;   // within which copies and p
 // Warps: groups of four for the weights, then one for the outputs (a warp reaches the 32 lanes
 // of tensor memory of its number modulo 4), then one for each of the two products, one for
 // the queries, and those for the copies. With 16 heads the second product's warp does the
-// queries too: no more than 16 warps, and a thread can have 128 registers.
+// queries too: by tensor copies these are 16 warps, and a thread can have 128 registers. Where
+// threads copy they are 18, of 96 registers, which the weights' loop overflows by some 100 bytes
+// (64 channels, 16 heads, 3 x 78520 tokens, pages of 17: 73 us, a quarter of copy bandwidth).
 constexpr int groups_of(int) { return 2; }
 constexpr int copy_warps(int heads, bool tma) { return tma && heads > 8 ? 2 : 4; }
 constexpr int threads_of(int heads, bool tma) { return 32 * (4 * groups_of(heads) + (heads > 8 ? 6 : 7) + copy_warps(heads, tma)); }
