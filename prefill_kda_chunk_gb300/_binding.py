@@ -4,6 +4,11 @@ Argument marshalling only: every step of the prefill runs in the library's
 CUDA kernels. PyTorch supplies device memory and the current stream. There
 is no fallback: if the library is missing or the device is not sm_103, calls
 raise.
+
+`stream` of a call is a raw handle, for programs that order their streams
+themselves: the tensors that the call makes belong to PyTorch's current stream, and
+their memory may still be in use there. Give such a call its outputs, or make its
+stream the current one.
 """
 from __future__ import annotations
 

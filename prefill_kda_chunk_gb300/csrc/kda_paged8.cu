@@ -34,11 +34,11 @@
 // the order of the blocks (where they are many, groups of them first).
 //
 // Measured (copy bandwidth: 1340 clocks for a tile of D = 128): 2 sequences of 131072 tokens, 32
-// heads over 8 of 128: 92 us (5.8 TB/s, 86 % of copy bandwidth); 64 sequences of 1 to 16384
-// tokens, 64 heads over 8: 50 us (67 %); 256 of 1000, 32 heads over 8: 95 us (81 %); one of 700:
-// 11 us, a chain of latencies. What a tile
-// takes the weights' warps, some 1250 clocks with 8 heads, bounds D = 64 (8 x 32768 tokens: 72
-// us, 55 %), and 1600 with 16 heads those (8 x 65536, 2 key-value heads: 64 us, 61 %).
+// heads over 8 of 128: 92 to 94 us (5.8 TB/s, 84 to 86 % of copy bandwidth); 64 sequences of 1 to
+// 16384 tokens, 64 heads over 8: 51 us (66 %); 256 of 1000, 32 heads over 8: 97 us (80 %); one of
+// 700: 11 us, a chain of latencies. What a tile
+// takes the weights' warps, some 1250 clocks with 8 heads, bounds D = 64 (8 x 32768 tokens: 74
+// us, 54 %), and 1600 with 16 heads those (8 x 65536, 2 key-value heads: 66 us, 60 %).
 
 #include <cuda.h>
 #include <cuda_fp8.h>
