@@ -643,7 +643,8 @@ KDA_API kda_status kda_last_device_error(void *stream);
  */
 KDA_API kda_status kda_workspace_release(void);
 
-/* Workspace bytes a call with these sizes needs (0 on bad sizes). Host only. */
+/* Workspace bytes a call with these sizes needs (0 on bad sizes); the counters that some kernels
+ * keep between calls, 40 H + 64 B for the launch in one, lie beside it. Host only. */
 KDA_API int64_t kda_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t N, int has_cu_seqlens);
 
 /* The same for kda_chunk_prefill_backward with the gradient form set by
